@@ -1,0 +1,190 @@
+"""ctypes binding of the operators around the attention passes (include/fa.h,
+ABI 1.4): rotary positions.
+
+As in ``_lib``: argument checks, output and workspace allocation with torch,
+raw pointers and the stream; the computation runs in ``libfa_gb300.so``.
+A call runs on the device of its tensors, on ``stream`` or that device's
+current stream.  With ``stream`` given, outputs and workspace are allocated
+on that stream, and small conversions of index arguments run on it too.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+
+from ._lib import DTYPE_CODE, FA_OK, FAError, load
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class fa_rope_params(ctypes.Structure):
+    _fields_ = ([(n, _i32) for n in ("B", "H", "H_kv", "N", "d", "rot", "dtype", "interleaved", "backward",
+                                     "positions_i64")] +
+                [("%s_stride_%s" % (t, x), _i64) for t in ("q", "k", "q_out", "k_out") for x in "bhn"] +
+                [("positions", _vp), ("pos_stride_b", _i64), ("pos_stride_n", _i64), ("start", _i64),
+                 ("inv_freq", _vp), ("mscale", _f32)])
+
+
+_typed = {}
+
+
+def _fn(name, *argtypes, restype=ctypes.c_int):
+    """The library's function `name` with its argument types set (once)."""
+    f = _typed.get(name)
+    if f is None:
+        f = getattr(load(), name)
+        f.argtypes, f.restype = list(argtypes), restype
+        _typed[name] = f
+    return f
+
+
+@contextlib.contextmanager
+def _entered(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+class _Plain:
+    """_entered for the usual case (the tensors' device is current, no stream given), without its cost."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _on(device, stream):
+    """Context that makes the tensors' device (and the given stream) current; yields the raw stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+        return _entered(device, stream)
+    if torch.cuda.current_device() != device.index:
+        return _entered(device, None)
+    return _Plain(device)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _check4(t, name, device=None, dtype=None):
+    if t.dim() != 4:
+        raise ValueError("%s must have 4 dimensions, got shape %s" % (name, tuple(t.shape)))
+    _check_place(t, name, device, dtype)
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("%s: the last dimension must be contiguous (stride 1), got strides %s" % (name, t.stride()))
+
+
+def _check_place(t, name, device=None, dtype=None):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if dtype is None:
+        if t.dtype not in DTYPE_CODE:
+            raise ValueError("unsupported dtype %s of %s" % (t.dtype, name))
+    elif t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+def _check_out(t, like, name):
+    if t.shape != like.shape:
+        raise ValueError("out %s must have shape %s, got %s" % (name, tuple(like.shape), tuple(t.shape)))
+    _check4(t, "out " + name, like.device, like.dtype)
+
+
+def rope_frequencies(rot, *, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0,
+                     device="cuda"):
+    """(inv_freq, mscale) of a rotation of ``rot`` columns, for :func:`rope`.
+
+    inv_freq is a float64 tensor [rot/2] on ``device``; mscale the factor on
+    cos and sin.  ``scaling``: "none", "linear" (positions interpolated by
+    ``factor``), "ntk" (base stretched so that the slowest pair is slowed by
+    ``factor``) or "yarn" (per pair, by how often it turns within
+    ``original_len`` positions)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError("scaling must be one of %s, got %r" % (sorted(ROPE_SCALING), scaling))
+    rot = int(rot)
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2, got %d" % rot)
+    buf = (ctypes.c_double * (rot // 2))()
+    m = _f32()
+    dbl = ctypes.c_double
+    f = _fn("fa_rope_frequencies", _i32, dbl, _i32, dbl, _i64, dbl, dbl, _vp, _vp)
+    st = f(rot, float(base), ROPE_SCALING[scaling], float(factor), int(original_len), float(beta_fast), float(beta_slow),
+           ctypes.addressof(buf), ctypes.addressof(m))
+    if st != FA_OK:
+        raise FAError(st, "fa_rope_frequencies")
+    return torch.tensor(list(buf), dtype=torch.float64).to(device), float(m.value)
+
+
+def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleaved=False, backward=False, out=None,
+         stream=None):
+    """q and k rotated by their positions (fa_rope), as (q_out, k_out); q_out alone without k.
+
+    q [B,H,N,d], k [B,H_kv,N,d].  ``inv_freq`` (float64 [rot/2], see
+    :func:`rope_frequencies`) sets how many leading columns turn; the others
+    are copied.  ``positions``: int32 / int64 tensor [N], [1,N] or [B,N];
+    None means start + n.  ``backward`` applies the transposed rotation: give
+    it dQ and dK to get the gradients of the unrotated q and k.  ``out`` =
+    (q_out, k_out), or q_out without k, may be the inputs themselves."""
+    _check4(q, "q")
+    B, H, N, d = q.shape
+    if k is not None:
+        _check4(k, "k", q.device, q.dtype)
+        if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+            raise ValueError("k must be [B, H_kv, N, d] with the B, N, d of q")
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or inv_freq.device != q.device or \
+            not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 tensor [rot/2] on q's device")
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device:
+            raise ValueError("positions must be an int32 or int64 tensor on q's device")
+        if positions.dim() == 1:
+            positions = positions[None]
+        if positions.dim() != 2 or positions.shape[1] != N or positions.shape[0] not in (1, B):
+            raise ValueError("positions must have shape [N], [1, N] or [B, N]")
+    p = fa_rope_params()
+    p.B, p.H, p.N, p.d, p.rot = B, H, N, d, 2 * inv_freq.shape[0]
+    p.H_kv = 0 if k is None else k.shape[1]
+    p.dtype = DTYPE_CODE[q.dtype]
+    p.interleaved, p.backward = bool(interleaved), bool(backward)
+    p.mscale, p.start = float(mscale), int(start)
+    p.inv_freq = inv_freq.data_ptr()
+    if positions is not None:
+        p.positions, p.positions_i64 = positions.data_ptr(), positions.dtype == torch.int64
+        p.pos_stride_b = positions.stride(0) if positions.shape[0] > 1 else 0
+        p.pos_stride_n = positions.stride(1)
+    with _on(q.device, stream) as raw:
+        if out is None:
+            qo = torch.empty_like(q)
+            ko = None if k is None else torch.empty_like(k)
+        else:
+            qo, ko = (out, None) if k is None else out
+            _check_out(qo, q, "q")
+            if k is not None:
+                _check_out(ko, k, "k")
+        p.q_stride_b, p.q_stride_h, p.q_stride_n = q.stride()[:3]
+        p.q_out_stride_b, p.q_out_stride_h, p.q_out_stride_n = qo.stride()[:3]
+        if k is not None:
+            p.k_stride_b, p.k_stride_h, p.k_stride_n = k.stride()[:3]
+            p.k_out_stride_b, p.k_out_stride_h, p.k_out_stride_n = ko.stride()[:3]
+        f = _fn("fa_rope", _vp, _vp, _vp, _vp, _vp, _vp)
+        st = f(ctypes.addressof(p), _ptr(q), _ptr(k), _ptr(qo), _ptr(ko), raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_rope")
+    return qo if k is None else (qo, ko)

@@ -519,6 +519,6 @@ const char* fa_status_string(fa_status s) {
   return "FA_ERR_UNKNOWN";
 }
 
-int32_t fa_version(void) { return 103; }
+int32_t fa_version(void) { return 104; }
 
 }  // extern "C"

@@ -315,12 +315,78 @@ fa_status fa_fp8_quantize(const fa_params *p, const fa_fp8_params *f, const void
 fa_status fa_fwd_fp8(const fa_params *p, const fa_fp8_params *f, const void *buf, size_t buf_bytes,
                      void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions (ABI 1.4).
+ * fa_rope turns the first `rot` columns of every row of q and k by the row's
+ * position, one pair of columns at a time:
+ *     (x0, x1) -> m (x0 cos a - x1 sin a, x1 cos a + x0 sin a),  a = p f_i,
+ * with p the token's position, f_i = inv_freq[i] the pair's inverse frequency
+ * (radians per position) and m = mscale.  Pair i is columns (i, i + rot/2), or
+ * (2i, 2i + 1) when `interleaved` is set; columns from rot on are copied.
+ * `backward` flips the sign of sin, which makes the map the transpose of the
+ * forward one: applied to dQ and dK after the attention's backward pass it
+ * gives the gradients of the unrotated q and k.
+ *   - q, q_out are [B,H,N,d] and k, k_out [B,H_kv,N,d] tensors of one dtype
+ *     (float32, float16, bfloat16), each with its own element strides; the
+ *     last dimension is contiguous.  H_kv = 0: no k.  Inputs may be broadcast
+ *     (stride 0).  An output may be its own input (same base, same strides);
+ *     any other overlap of an output with an input is an error of the caller.
+ *   - d is a multiple of 8 up to 256, rot even, 2 <= rot <= d.
+ *   - Bases and strides follow the 16-byte rule (a dimension of one element
+ *     may have any stride).
+ *   - positions: device int32 (or int64 with positions_i64) array, the
+ *     position of token n of sequence b at b*pos_stride_b + n*pos_stride_n
+ *     (pos_stride_b = 0: the same for every sequence); NULL: start + n.
+ *     Positions may be negative.  The angle is reduced to a fraction of a
+ *     turn exactly, in 64-bit integers, so it does not lose accuracy with
+ *     the position (float64's own 2^-53 of p f remains).
+ *   - inv_freq: device float64 [rot/2], read on the stream.
+ *   - Products and sums are float32, rounded once to the dtype.
+ *   - No workspace, one launch.  B*N*d < 2^32 - 4096.
+ * ------------------------------------------------------------------------- */
+typedef enum { FA_ROPE_NONE = 0, FA_ROPE_LINEAR = 1, FA_ROPE_NTK = 2, FA_ROPE_YARN = 3 } fa_rope_scaling;
+
+typedef struct {
+  int32_t B, H, H_kv, N, d;
+  int32_t rot;               /* rotated leading columns, even                   */
+  int32_t dtype;             /* fa_dtype                                        */
+  int32_t interleaved;       /* 0: pairs (i, i + rot/2); else (2i, 2i + 1)      */
+  int32_t backward;          /* nonzero: the transposed rotation                */
+  int32_t positions_i64;     /* positions are int64                             */
+  int64_t q_stride_b, q_stride_h, q_stride_n;
+  int64_t k_stride_b, k_stride_h, k_stride_n;
+  int64_t q_out_stride_b, q_out_stride_h, q_out_stride_n;
+  int64_t k_out_stride_b, k_out_stride_h, k_out_stride_n;
+  const void *positions;     /* device, or NULL                                 */
+  int64_t pos_stride_b, pos_stride_n;
+  int64_t start;             /* position of token 0 when positions is NULL      */
+  const double *inv_freq;    /* device float64 [rot/2]                          */
+  float mscale;              /* factor on cos and sin (1 for plain rotations)   */
+} fa_rope_params;
+
+fa_status fa_rope(const fa_rope_params *p, const void *q, const void *k, void *q_out, void *k_out, void *stream);
+
+/* fa_rope_frequencies -- inverse frequencies and mscale of a rotation of rot
+ * columns, written to HOST memory (a pure host function):
+ *   FA_ROPE_NONE    base^(-2i/rot)
+ *   FA_ROPE_LINEAR  the same divided by factor (positions interpolated)
+ *   FA_ROPE_NTK     base replaced by base * factor^(rot/(rot-2)): the slowest
+ *                   pair is slowed by factor, the fastest not at all
+ *   FA_ROPE_YARN    pairs that turn more than beta_fast times within
+ *                   original_len positions are kept, those that turn less
+ *                   than beta_slow times are divided by factor, a linear ramp
+ *                   over the pair index between; mscale = 0.1 ln(factor) + 1
+ * factor >= 1; original_len, beta_fast > beta_slow > 0 matter to YARN only. */
+fa_status fa_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, int64_t original_len,
+                              double beta_fast, double beta_slow, double *inv_freq, float *mscale);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fa_status_string(fa_status s);
 
 /* Library ABI version (major * 100 + minor): 101 adds H_kv, kv_stride_*
  * and window to fa_params; 102 adds the FP8 forward; 103 adds fwd_kernel,
- * fa_noalloc_check_status and fa_noalloc_scratch. */
+ * fa_noalloc_check_status and fa_noalloc_scratch; 104 adds fa_rope,
+ * fa_diff_* and fa_prefix_*. */
 int32_t fa_version(void);
 
 #ifdef __cplusplus
