@@ -23,7 +23,8 @@ DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 EXPORTED = ["fa_fwd_workspace_size", "fa_bwd_workspace_size", "fa_fwd", "fa_bwd", "fa_bwd_noalloc",
             "fa_noalloc_check_status", "fa_noalloc_scratch",
             "fa_check_status", "fa_dropout_mask", "fa_selftest_wait_timeout", "fa_status_string", "fa_version",
-            "fa_fp8_buffer_layout", "fa_fp8_quantize", "fa_fwd_fp8", "fa_rope", "fa_rope_frequencies"]
+            "fa_fp8_buffer_layout", "fa_fp8_quantize", "fa_fwd_fp8", "fa_rope", "fa_rope_frequencies",
+            "fa_diff_fwd_workspace_size", "fa_diff_bwd_workspace_size", "fa_diff_fwd", "fa_diff_bwd"]
 
 
 class fa_params(ctypes.Structure):

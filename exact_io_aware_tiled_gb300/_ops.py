@@ -188,3 +188,153 @@ def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleave
     if st != FA_OK:
         raise FAError(st, "fa_rope")
     return qo if k is None else (qo, ko)
+
+
+class fa_diff_params(ctypes.Structure):
+    _fields_ = ([(n, _i32) for n in ("B", "H", "H_kv", "N", "d", "dtype", "causal", "window")] +
+                [("scale", _f32), ("seqlens_k", _vp), ("lam", _vp)] +
+                [("%s_stride_%s" % (t, x), _i64) for t in ("q", "k", "v", "o", "do") for x in "bhn"])
+
+
+def _set_strides(p, name, t):
+    s = t.stride()
+    setattr(p, name + "_stride_b", s[0])
+    setattr(p, name + "_stride_h", s[1])
+    setattr(p, name + "_stride_n", s[2])
+
+
+def _lens(seqlens, B, device, name="seqlens_k"):
+    """int32 [B] lengths on `device` (converted on the current stream where they are something else)."""
+    if seqlens is None:
+        return None
+    if tuple(seqlens.shape) != (B,):
+        raise ValueError("%s must have shape [B] = [%d]" % (name, B))
+    if seqlens.dtype.is_floating_point or seqlens.dtype == torch.bool:
+        raise ValueError("%s must hold whole numbers" % name)
+    return seqlens.to(device=device, dtype=torch.int32).contiguous()
+
+
+def _need_workspace(workspace, size, device):
+    if workspace is None:
+        return torch.empty(size, device=device, dtype=torch.uint8)
+    if workspace.dtype != torch.uint8 or workspace.numel() < size or workspace.device != device or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor of >= %d bytes on %s" % (size, device))
+    return workspace
+
+
+def _diff_params(q, k, v, lam, causal, window, scale):
+    _check4(q, "q")
+    if q.shape[3] != 64 or q.shape[1] % 2:
+        raise ValueError("q must be [B, 2H, N, 64] (the two maps of head pair h in heads 2h, 2h + 1)")
+    _check4(k, "k", q.device, q.dtype)
+    _check4(v, "v", q.device, q.dtype)
+    B, H2, N, d = q.shape
+    H, Hkv = H2 // 2, v.shape[1]
+    if tuple(k.shape) != (B, 2 * Hkv, N, d) or tuple(v.shape) != (B, Hkv, N, 2 * d):
+        raise ValueError("k must be [B, 2 H_kv, N, 64] and v [B, H_kv, N, 128] with the B, N of q")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("the number of query head pairs must be a multiple of the number of K/V pairs")
+    if tuple(lam.shape) != (H,) or lam.dtype != torch.float32 or lam.device != q.device or not lam.is_contiguous():
+        raise ValueError("lam must be a contiguous float32 tensor [H] on q's device")
+    p = fa_diff_params()
+    p.B, p.H, p.H_kv, p.N, p.d, p.dtype = B, H, Hkv, N, d, DTYPE_CODE[q.dtype]
+    p.causal, p.window = bool(causal), int(window)
+    p.scale = 0.0 if scale is None else float(scale)
+    p.lam = lam.data_ptr()
+    for n, t in (("q", q), ("k", k), ("v", v)):
+        _set_strides(p, n, t)
+    return p
+
+
+def diff_fwd(q, k, v, lam, *, causal=False, seqlens_k=None, window=0, scale=None, need_o2=True, out=None,
+             workspace=None, stream=None):
+    """Differential attention (fa_diff_fwd): (o, lse, o2).
+
+    q [B,2H,N,64] and k [B,2H_kv,N,64] hold the two maps of head pair h in
+    heads 2h and 2h + 1, v [B,H_kv,N,128]; lam float32 [H].
+    o = (softmax(tau q1 k1^T) - lam softmax(tau q2 k2^T)) v, [B,H,N,128];
+    lse float32 [B,2H,N].  o2, the second map's own output, is what
+    :func:`diff_bwd` needs besides; ``need_o2=False`` leaves it out (None).
+    ``out`` = (o, lse, o2), o2 None where it is not needed; o and o2 share
+    their strides."""
+    p = _diff_params(q, k, v, lam, causal, window, scale)
+    B, H, N, dv = p.B, p.H, p.N, 2 * p.d
+    with _on(q.device, stream) as raw:
+        lens = _lens(seqlens_k, B, q.device)
+        p.seqlens_k = _ptr(lens)
+        if out is None:
+            o = torch.empty((B, H, N, dv), device=q.device, dtype=q.dtype)
+            o2 = torch.empty_like(o) if need_o2 else None
+            lse = torch.empty((B, 2 * H, N), device=q.device, dtype=torch.float32)
+        else:
+            o, lse, o2 = out
+            for t, n in ((o, "o"), (o2, "o2")):
+                if t is None and n == "o2" and not need_o2:
+                    continue
+                if t is None or tuple(t.shape) != (B, H, N, dv):
+                    raise ValueError("out %s must have shape %s" % (n, (B, H, N, dv)))
+                _check4(t, "out " + n, q.device, q.dtype)
+            if o2 is not None and o2.stride() != o.stride():
+                raise ValueError("out o and o2 must share their strides")
+            _check_place(lse, "out lse", q.device, torch.float32)
+            if tuple(lse.shape) != (B, 2 * H, N) or not lse.is_contiguous():
+                raise ValueError("out lse must be contiguous with shape %s" % ((B, 2 * H, N),))
+        _set_strides(p, "o", o)
+        a = ctypes.addressof(p)
+        size = _fn("fa_diff_fwd_workspace_size", _vp, restype=ctypes.c_size_t)(a)
+        ws = _need_workspace(workspace, size, q.device)
+        f = _fn("fa_diff_fwd", *([_vp] * 8), ctypes.c_size_t, _vp)
+        st = f(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(o2), lse.data_ptr(), ws.data_ptr(),
+               ws.numel(), raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_diff_fwd")
+    diff_fwd.last_workspace = ws
+    return o, lse, o2
+
+
+def diff_bwd(q, k, v, lam, o, o2, do, lse, *, causal=False, seqlens_k=None, window=0, scale=None, out=None,
+             workspace=None, stream=None):
+    """(dq, dk, dv, dlam) of :func:`diff_fwd` (fa_diff_bwd) for the upstream
+    gradient ``do`` [B,H,N,128]; o, o2, lse and the masks are the forward
+    call's.  dq, dk, dv have the shapes and strides of q, k, v; dlam is
+    float32 [H].  ``out`` = (dq, dk, dv, dlam)."""
+    p = _diff_params(q, k, v, lam, causal, window, scale)
+    B, H, N, dv_ = p.B, p.H, p.N, 2 * p.d
+    for t, n in ((o, "o"), (o2, "o2"), (do, "do")):
+        _check4(t, n, q.device, q.dtype)
+        if tuple(t.shape) != (B, H, N, dv_):
+            raise ValueError("%s must have shape %s" % (n, (B, H, N, dv_)))
+    if o.stride() != o2.stride():
+        raise ValueError("o and o2 must share their strides")
+    _check_place(lse, "lse", q.device, torch.float32)
+    if tuple(lse.shape) != (B, 2 * H, N) or not lse.is_contiguous():
+        raise ValueError("lse must be the contiguous [B, 2H, N] float32 tensor diff_fwd returns")
+    _set_strides(p, "o", o)
+    _set_strides(p, "do", do)
+    with _on(q.device, stream) as raw:
+        lens = _lens(seqlens_k, B, q.device)
+        p.seqlens_k = _ptr(lens)
+        likes = (q, k, v)
+        if out is None:
+            dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), device=t.device, dtype=t.dtype) for t in likes)
+            dlam = torch.empty((H,), device=q.device, dtype=torch.float32)
+        else:
+            dq, dk, dv, dlam = out
+            _check_place(dlam, "out dlam", q.device, torch.float32)
+            if tuple(dlam.shape) != (H,) or not dlam.is_contiguous():
+                raise ValueError("out dlam must be contiguous with shape [H]")
+        for t, like, n in zip((dq, dk, dv), likes, ("dq", "dk", "dv")):
+            _check_out(t, like, n)
+            if t.stride() != like.stride():
+                raise ValueError("out %s must have the strides %s" % (n, like.stride()))
+        a = ctypes.addressof(p)
+        size = _fn("fa_diff_bwd_workspace_size", _vp, restype=ctypes.c_size_t)(a)
+        ws = _need_workspace(workspace, size, q.device)
+        f = _fn("fa_diff_bwd", *([_vp] * 13), ctypes.c_size_t, _vp)
+        st = f(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), o2.data_ptr(), do.data_ptr(), lse.data_ptr(),
+               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlam.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_diff_bwd")
+    diff_bwd.last_workspace = ws
+    return dq, dk, dv, dlam

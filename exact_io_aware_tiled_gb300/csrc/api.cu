@@ -260,6 +260,85 @@ fa_status map_u8(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[4], 
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+// ---- differential attention ---------------------------------------------------
+struct DiffLayout {
+  size_t status = 0, rows = 0, dqacc = 0, part = 0, sched = 0, total = 0;
+  int nq = 0, npad = 0;
+};
+
+int diff_hkv(const fa_diff_params* p) { return p->H_kv == 0 ? p->H : p->H_kv; }
+
+DiffLayout diff_layout(const fa_diff_params* p, bool bwd) {
+  DiffLayout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += align256(bytes);
+    return o;
+  };
+  L.nq = (p->N + kTile - 1) / kTile;
+  L.npad = L.nq * kTile;
+  L.status = take(256);
+  if (bwd) {
+    L.rows = take((size_t)p->B * p->H * L.npad * 4 * sizeof(float));
+    L.dqacc = take((size_t)p->B * p->H * 2 * p->N * p->d * sizeof(float));
+    L.part = take((size_t)p->B * p->H * L.nq * 16 * sizeof(float));
+    L.sched = take(sizeof(int));
+  }
+  L.total = off;
+  return L;
+}
+
+// One [B,heads,N,cols] tensor's strides: the dimensions of one element are
+// normalised, the others follow the 16-byte rule.
+fa_status diff_strides(Strides& s, const fa_diff_params* p, int heads, int cols) {
+  if (p->N == 1) s.n = cols;
+  if (heads == 1) s.h = (int64_t)p->N * s.n;
+  if (p->B == 1) s.b = (int64_t)heads * s.h;
+  if (s.n < cols || s.h < 1 || s.b < 1) return FA_ERR_INVALID_ARG;
+  if (s.n % 8 || s.h % 8 || s.b % 8) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+struct DiffStrides { Strides q, k, v, o, dout; };
+
+fa_status check_diff(const fa_diff_params* p, DiffStrides& s, bool bwd) {
+  if (p == nullptr) return FA_ERR_INVALID_ARG;
+  if (p->B < 1 || p->H < 1 || p->N < 1 || p->d < 1 || p->H_kv < 0) return FA_ERR_INVALID_ARG;
+  if (p->dtype != FA_DT_F32 && p->dtype != FA_DT_F16 && p->dtype != FA_DT_BF16) return FA_ERR_INVALID_ARG;
+  if (p->d != 64 || p->dtype == FA_DT_F32) return FA_ERR_UNSUPPORTED;
+  const int hkv = diff_hkv(p);
+  if (p->H % hkv != 0) return FA_ERR_INVALID_ARG;
+  if (p->window < 0) return FA_ERR_INVALID_ARG;
+  if (p->window > 0 && !p->causal) return FA_ERR_UNSUPPORTED;
+  if (2ll * p->B * p->H * p->N >= (1ll << 32)) return FA_ERR_UNSUPPORTED;
+  if (p->lam == nullptr) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(p->lam) | reinterpret_cast<uintptr_t>(p->seqlens_k)) & 3u) return FA_ERR_MISALIGNED;
+  s.q = {p->q_stride_b, p->q_stride_h, p->q_stride_n};
+  s.k = {p->k_stride_b, p->k_stride_h, p->k_stride_n};
+  s.v = {p->v_stride_b, p->v_stride_h, p->v_stride_n};
+  s.o = {p->o_stride_b, p->o_stride_h, p->o_stride_n};
+  s.dout = {p->do_stride_b, p->do_stride_h, p->do_stride_n};
+  fa_status e;
+  if ((e = diff_strides(s.q, p, 2 * p->H, 64)) != FA_OK || (e = diff_strides(s.k, p, 2 * hkv, 64)) != FA_OK ||
+      (e = diff_strides(s.v, p, hkv, 128)) != FA_OK || (e = diff_strides(s.o, p, p->H, 128)) != FA_OK)
+    return e;
+  return bwd ? diff_strides(s.dout, p, p->H, 128) : FA_OK;
+}
+
+float diff_scale(const fa_diff_params* p) {
+  return (p->scale > 0.f && std::isfinite(p->scale)) ? p->scale : 1.f / std::sqrt((float)p->d);
+}
+
+// A 16-bit [B,heads,N,cols] map with boxes of 64 columns and `rows` rows.
+fa_status diff_map(CUtensorMap* m, const void* base, const fa_diff_params* p, int heads, int cols, Strides s, int rows) {
+  fa_params q{};
+  q.B = p->B;
+  q.N = p->N;
+  return make_map(m, base, p->dtype == FA_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  2, cols, 64, &q, heads, s, rows);
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -504,6 +583,109 @@ fa_status fa_fwd_fp8(const fa_params* p, const fa_fp8_params* f, const void* buf
   if ((s = prepare_common(p, L, w, st)) != FA_OK) return s;
   ProfScope prof(p, st);
   return cuda_status(launch_fwd_fp8(p->d, mq, mk, mv, mo, a, st));
+}
+
+size_t fa_diff_fwd_workspace_size(const fa_diff_params* p) {
+  if (p == nullptr || p->N < 1) return 256;
+  return diff_layout(p, false).total;
+}
+
+size_t fa_diff_bwd_workspace_size(const fa_diff_params* p) {
+  if (p == nullptr || p->N < 1 || p->B < 1 || p->H < 1 || p->d < 1) return 256;
+  return diff_layout(p, true).total;
+}
+
+fa_status fa_diff_fwd(const fa_diff_params* p, const void* q, const void* k, const void* v, void* o, void* o2,
+                      float* lse, void* ws, size_t ws_bytes, void* stream) {
+  DiffStrides sd;
+  fa_status s = check_diff(p, sd, false);
+  if (s != FA_OK) return s;
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(o2) || !aligned16(lse))
+    return FA_ERR_MISALIGNED;
+  const DiffLayout L = diff_layout(p, false);
+  if (ws == nullptr || ws_bytes < L.total || !aligned16(ws)) return FA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const int hkv = diff_hkv(p);
+  DiffFwdArgs a{};
+  a.B = p->B; a.H = p->H; a.N = p->N;
+  a.group = p->H / hkv;
+  a.nq = L.nq;
+  a.causal = p->causal ? 1 : 0;
+  a.window = p->window;
+  a.scale_log2 = diff_scale(p) * 1.4426950408889634f;
+  a.seqlens_k = p->seqlens_k;
+  a.lam = p->lam;
+  a.lse = lse;
+  a.has_o2 = o2 != nullptr ? 1 : 0;
+  a.status = reinterpret_cast<int*>(w + L.status);
+  CUtensorMap mq, mk, mv, mo, mo2;
+  if ((s = diff_map(&mq, q, p, 2 * p->H, 64, sd.q, kTile)) != FA_OK ||
+      (s = diff_map(&mk, k, p, 2 * hkv, 64, sd.k, kTile)) != FA_OK ||
+      (s = diff_map(&mv, v, p, hkv, 128, sd.v, kTile)) != FA_OK ||
+      (s = diff_map(&mo, o, p, p->H, 128, sd.o, kTile)) != FA_OK ||
+      (s = diff_map(&mo2, o2 != nullptr ? o2 : o, p, p->H, 128, sd.o, kTile)) != FA_OK)
+    return s;
+  if (cudaMemsetAsync(w + L.status, 0, sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
+  return cuda_status(launch_diff_fwd(p->dtype, mq, mk, mv, mo, mo2, a, st));
+}
+
+fa_status fa_diff_bwd(const fa_diff_params* p, const void* q, const void* k, const void* v, const void* o,
+                      const void* o2, const void* dout, const float* lse, void* dq, void* dk, void* dv, float* dlam,
+                      void* ws, size_t ws_bytes, void* stream) {
+  DiffStrides sd;
+  fa_status s = check_diff(p, sd, true);
+  if (s != FA_OK) return s;
+  if (!q || !k || !v || !o || !o2 || !dout || !lse || !dq || !dk || !dv || !dlam) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(o2) || !aligned16(dout) ||
+      !aligned16(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      (reinterpret_cast<uintptr_t>(dlam) & 3u))
+    return FA_ERR_MISALIGNED;
+  const DiffLayout L = diff_layout(p, true);
+  if (ws == nullptr || ws_bytes < L.total || !aligned16(ws)) return FA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const int hkv = diff_hkv(p);
+  DiffBwdArgs a{};
+  a.B = p->B; a.H = p->H; a.H_kv = hkv; a.N = p->N;
+  a.group = p->H / hkv;
+  a.nq = L.nq; a.npad = L.npad;
+  a.causal = p->causal ? 1 : 0;
+  a.window = p->window;
+  a.scale = diff_scale(p);
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.seqlens_k = p->seqlens_k;
+  a.lam = p->lam;
+  a.rows = reinterpret_cast<const float*>(w + L.rows);
+  a.dlam_part = reinterpret_cast<float*>(w + L.part);
+  a.sched = reinterpret_cast<int*>(w + L.sched);
+  a.status = reinterpret_cast<int*>(w + L.status);
+  a.dk = dk; a.dv = dv;
+  a.kst = sd.k; a.vst = sd.v;
+  a.dkv_v8 = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 &&
+             (sd.k.n | sd.k.h | sd.k.b | sd.v.n | sd.v.h | sd.v.b) % 16 == 0;
+  float* dqacc = reinterpret_cast<float*>(w + L.dqacc);
+  const Strides acc{(int64_t)2 * p->H * p->N * 64, (int64_t)p->N * 64, 64};
+  fa_params bn{};
+  bn.B = p->B;
+  bn.N = p->N;
+  CUtensorMap mq, mk, mv, mdo, macc;
+  if ((s = diff_map(&mq, q, p, 2 * p->H, 64, sd.q, 64)) != FA_OK ||
+      (s = diff_map(&mk, k, p, 2 * hkv, 64, sd.k, kTile)) != FA_OK ||
+      (s = diff_map(&mv, v, p, hkv, 128, sd.v, kTile)) != FA_OK ||
+      (s = diff_map(&mdo, dout, p, p->H, 128, sd.dout, 64)) != FA_OK ||
+      (s = make_map(&macc, dqacc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, 64, 32, &bn, 2 * p->H, acc, 64)) != FA_OK)
+    return s;
+  if (cudaMemsetAsync(w + L.status, 0, sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
+  // bf16 kernels fold tau into dS; see diff_bwd.cu
+  const float c1 = p->dtype == FA_DT_BF16 ? a.scale : 1.f;
+  cudaError_t e = launch_diff_prep(p->dtype, o, o2, sd.o, dout, sd.dout, lse, p->lam, p->B, p->H, p->N, L.npad, c1,
+                                   reinterpret_cast<float*>(w + L.rows), dqacc, a.sched, st);
+  if (e == cudaSuccess) e = launch_diff_bwd(p->dtype, mq, mk, mv, mdo, macc, a, st);
+  if (e == cudaSuccess) e = launch_dq_convert(p->dtype, dqacc, dq, sd.q, p->B, 2 * p->H, p->N, 64, st);
+  if (e == cudaSuccess) e = launch_diff_dlam(a.dlam_part, dlam, p->B, p->H, a.group, L.nq, st);
+  return cuda_status(e);
 }
 
 const char* fa_status_string(fa_status s) {

@@ -1,0 +1,798 @@
+// diff_bwd.cu -- differential attention, backward, 16-bit inputs, sm_103a.
+//
+// Mathematics (O = (P_1 - lambda P_2) V, P_m rebuilt from Q_m, K_m and the saved
+// logsumexps).  Both maps meet the same dP, because they share V and dO:
+//     dP   = dO V^T,   D_m = rowsum(P_m o dP) = dO . O_m
+//     dS_1 = P_1 o (dP - D_1),   dS_2 = -lambda P_2 o (dP - D_2)
+//     dV   = (P_1 - lambda P_2)^T dO     one product for both maps
+//     dQ_m = tau dS_m K_m,   dK_m = tau dS_m^T Q_m,   dlambda = -sum P_2 o dP
+// Per visible pair: 2 x 128 flops of scores, 256 each of dP, dV, dQ and dK
+// (1280 in all) and two exponentials.  Two separate backward passes at d = 128
+// (Q, K padded) would do 2560.  dlambda is summed from the float32 P_2 and dP,
+// not from rounded outputs: it is a long sum of both signs.
+//
+// Tiles: 128 keys x 64 query rows a step, keys on the tensor-memory lanes, as in
+// the d = 128 backward (bwd_tc128.cu), whose roles and barriers this kernel
+// keeps.  Tensor memory (512 columns):
+//   S_1^T 0-63 | S_2^T 64-127 | dP^T 128-191 | dQ^T 192-255 | dK_1, dK_2 256-383 | dV 384-511
+// W^T = (P_1 - lambda P_2)^T, the 16-bit operand of dV, lies over S_1^T (the 16
+// queries of warpgroup w in the first 8 of its own 16 columns), so S_1 of the
+// next step waits for dV; S_2 is issued before it and covers the wait.
+//
+// dQ^T has 64 rows (head dims) per map, half of what the tensor core's M = 128
+// takes.  Both maps share one accumulator: lanes 0-63 hold dQ_1^T, 64-127
+// dQ_2^T.  The A operand of map 1 is (K_1 | Z) and of map 2 (Z | K_2), Z a tile
+// of zeros that lies between K_1 and K_2 in shared memory, so each product adds
+// zeros to the other map's half.  That doubles this product's multiplies (+20 %
+// of the total) and keeps everything within 512 columns and one drain.
+//
+// What bounds it: the chain S -> P -> dS -> dQ of a step and the compute warps'
+// instructions (two exponentials and two dS per pair), not the tensor core.
+//
+// Keys behind seqlens_k[b] may hold anything: their P and dP are replaced, and
+// their K rows are zeroed in shared memory before dQ reads them.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 640;
+constexpr int kCompute = 512;   // threads of warps 0-15
+constexpr int kQS = 64;         // query rows per step
+constexpr int NQ = 2;           // Q / dO stages
+constexpr int kLag = 3;         // dQ reduce-adds trail the loads by this many steps
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct DSmem {
+  static constexpr int kK = 0;                      // K_1 | zeros | K_2, 16 KB each
+  static constexpr int kV = 49152;                  // 32 KB: V [2 boxes][128 keys][64]
+  static constexpr int kQ = 81920;                  // NQ x (Q_1, Q_2: 8 KB each)
+  static constexpr int kDO = kQ + NQ * 16384;       // NQ x 16 KB: dO [2 boxes][64 q][64]
+  static constexpr int kDS = kDO + NQ * 16384;      // dS_1^T, dS_2^T [128 keys][64 q], 16 KB each
+  static constexpr int kDQ = kDS + 32768;           // 32 KB: float32 dQ staging [4 boxes][64 q][32]
+  static constexpr int kLD = kDQ + 32768;           // NQ x 4 x 64 floats: LSE_1, LSE_2, e_1, e_2
+  static constexpr int kInfo = kLD + NQ * 1024;     // (first query row, head pair, batch) of the last kLag+1 steps
+  static constexpr int kItem = kInfo + 64;          // the two published work items
+  static constexpr int kBar = kItem + 64;
+  static constexpr int kBytes = kBar + 320;
+  static constexpr int kDyn = kBytes + 1024;
+};
+static_assert(DSmem::kDyn <= 232448, "shared memory over the per-block limit");
+
+struct DBars {
+  uint64_t item_full[2], item_empty[2];
+  uint64_t kv_full, kv_empty;
+  uint64_t q_full[NQ], q_empty[NQ];
+  uint64_t s_full, p_full, dp_full, ds_full, dq_full, dq_free, dkv_full, pt_free;
+  uint64_t dsm_free;
+  uint64_t done[3];
+  uint64_t stg_full, stg_free;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(DBars) <= 320, "barrier block overflows its shared-memory slot");
+
+constexpr uint32_t kColS1 = 0, kColS2 = 64, kColDP = 128, kColDQ = 192, kColDK = 256, kColDV = 384;
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+  const bool ok = mbar_wait(bar, parity, ctl);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// One work item: key tile jt of K/V pair hk of batch b, and its steps: the two
+// 64-row halves of every query tile that sees the key tile, for each of the
+// group's query head pairs.
+struct DItem {
+  int b, hk, jt, Lk;
+  int n;                  // query tiles per query head pair
+  int i0;                 // first query tile
+  int h0;                 // first query head pair of the group
+  int steps;              // 64-row steps
+};
+
+__device__ __forceinline__ DItem make_item(const DiffBwdArgs& a, int u) {
+  DItem it;
+  const int bk = u / a.nq;
+  it.jt = u - bk * a.nq;
+  it.b = bk / a.H_kv;
+  it.hk = bk - it.b * a.H_kv;
+  it.Lk = a.N;
+  if (a.seqlens_k != nullptr) it.Lk = max(0, min(a.N, a.seqlens_k[it.b]));
+  it.i0 = a.causal ? it.jt : 0;
+  it.h0 = it.hk * a.group;
+  int qlast = a.nq - 1;
+  // under a window of w keys, key j is seen by queries j .. j + w - 1 (the sum in 64 bits: w may be any int)
+  if (a.window > 0) qlast = (int)min((long long)qlast, ((long long)it.jt * kTile + kTile - 1 + a.window - 1) / kTile);
+  it.n = it.jt * kTile < it.Lk ? max(0, qlast - it.i0 + 1) : 0;
+  it.steps = 2 * it.n * a.group;
+  return it;
+}
+
+struct StepPos {
+  int qu = 0, hq = 0, hf = 0;
+  __device__ __forceinline__ void next(const DItem& it) {
+    if (++hf == 2) {
+      hf = 0;
+      if (++qu == it.n) { qu = 0; ++hq; }
+    }
+  }
+};
+
+template <typename T, bool kWin>
+__global__ void __launch_bounds__(kThreads, 1)
+diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                const __grid_constant__ CUtensorMap tmDQ, const DiffBwdArgs a) {
+  using L = DSmem;
+  // bf16: tau is folded into dS, so dQ and dK leave the tensor core scaled; not
+  // for fp16, whose smaller range would push small dS values into subnormals.
+  constexpr bool kFold = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DBars* bars = reinterpret_cast<DBars*>(smem + L::kBar);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int total = a.nq * a.B * a.H_kv;
+  WaitCtl ctl{a.status, &bars->abort};
+
+  // the zero tile between K_1 and K_2
+  for (int o = threadIdx.x * 16; o < 16384; o += kThreads * 16)
+    *reinterpret_cast<uint4*>(smem + L::kK + 16384 + o) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], 3 + kCompute);   // warps 17-19 and the compute threads
+    }
+    mbar_init(&bars->kv_full, 1);
+    mbar_init(&bars->kv_empty, 2);      // S^T / dP^T warp and dQ warp read K, V
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 1);
+    }
+    mbar_init(&bars->s_full, 1);
+    mbar_init(&bars->p_full, kCompute);
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->ds_full, kCompute);
+    mbar_init(&bars->dq_full, 1);
+    mbar_init(&bars->dq_free, kCompute);
+    mbar_init(&bars->dkv_full, 1);
+    mbar_init(&bars->pt_free, 1);
+    mbar_init(&bars->dsm_free, 2);     // dK and dQ^T both read the shared dS^T tiles
+    for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
+    mbar_init(&bars->stg_full, kCompute);
+    mbar_init(&bars->stg_free, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 17) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp >= 16) {
+    constexpr int ab = Cvt<T>::kAB;
+    constexpr uint32_t idST = idesc_f16(128, 64, ab, 0, 0);    // S^T, dP^T (both operands K-major)
+    constexpr uint32_t idV = idesc_f16(128, 128, ab, 0, 1);    // dV (A in tensor memory, B MN-major)
+    constexpr uint32_t idK = idesc_f16(128, 64, ab, 0, 1);     // dK_m (A K-major, B MN-major)
+    constexpr uint32_t idQ = idesc_f16(128, 64, ab, 1, 1);     // dQ^T (A = (K_1 | Z)^T or (Z | K_2)^T, B = dS^T, MN-major)
+    const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+    const uint32_t sQ = smem_u32(smem + L::kQ), sDO = smem_u32(smem + L::kDO);
+    const uint32_t sDS = smem_u32(smem + L::kDS);
+    volatile int* item_u = reinterpret_cast<volatile int*>(smem + L::kItem);
+    int kc = 0;
+    auto fetch = [&]() -> int {
+      const int slot = kc & 1;
+      if (!mbar_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl)) return -1;
+      const int v = item_u[slot];
+      mbar_arrive(&bars->item_empty[slot]);
+      ++kc;
+      return v;
+    };
+    if (warp == 16) {
+      // ===================== TMA producer + dQ reduce =====================
+      if (lane == 0) {
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmDO);
+        prefetch_tmap(&tmDQ);
+        int4* info = reinterpret_cast<int4*>(smem + L::kInfo);
+        int g = 0, nkv = 0;
+        bool ok = true;
+        // the staged dQ of step r: 32-column boxes of both maps; a half tile
+        // that starts at or past N has nothing to add
+        auto reduce = [&](int r) -> bool {
+          if (!mbar_wait(&bars->stg_full, (uint32_t)r & 1u, ctl)) return false;
+          const uint8_t* sb = smem + L::kDQ;
+          const int4 inf = info[r & 3];
+          if (inf.x < a.N) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tma_reduce_add_4d(&tmDQ, sb + c * 8192, (c & 1) * 32, inf.x, 2 * inf.y + (c >> 1), inf.z);
+            bulk_commit();
+            bulk_wait_read0();
+          }
+          mbar_arrive(&bars->stg_free);
+          return true;
+        };
+        int kf = 0;
+        auto publish = [&]() -> int {
+          const int slot = kf & 1;
+          if (!mbar_wait(&bars->item_empty[slot], ((uint32_t)(kf >> 1) & 1u) ^ 1u, ctl)) return -2;
+          int v = atomicAdd(a.sched, 1);
+          if (v >= total) v = -1;
+          item_u[slot] = v;
+          mbar_arrive(&bars->item_full[slot]);
+          ++kf;
+          return v;
+        };
+        int rd = 0;
+        auto reduce_to = [&](int last) -> bool {
+          for (; rd <= last; ++rd)
+            if (!reduce(rd)) return false;
+          return true;
+        };
+        int u;
+        while (ok) {
+          if (!(ok = reduce_to(g - kLag))) break;
+          u = publish();
+          if (u < 0) {
+            ok = u == -1;
+            break;
+          }
+          const DItem it = make_item(a, u);
+          if (it.steps == 0) continue;
+          // K, V: one buffer each, free once the previous item's S^T, dP^T and dQ^T products are done
+          if (!(ok = mbar_wait(&bars->kv_empty, ((uint32_t)nkv & 1u) ^ 1u, ctl))) break;
+          mbar_expect_tx(&bars->kv_full, 65536);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tma_load_4d(smem + L::kK + c * 32768, &tmK, &bars->kv_full, 0, it.jt * kTile, 2 * it.hk + c, it.b);
+            tma_load_4d(smem + L::kV + c * 16384, &tmV, &bars->kv_full, c * 64, it.jt * kTile, it.hk, it.b);
+          }
+          ++nkv;
+          StepPos sp;
+          sp.hq = it.h0;
+          for (int t = 0; t < it.steps && ok; ++t, ++g, sp.next(it)) {
+            const int st = g % NQ;
+            if (!(ok = mbar_wait(&bars->q_empty[st], ((uint32_t)(g / NQ) & 1u) ^ 1u, ctl))) break;
+            const int q0 = (it.i0 + sp.qu) * kTile + sp.hf * kQS;
+            const size_t ld_row = (((size_t)it.b * a.H + sp.hq) * a.npad + (size_t)q0) * 4;
+            mbar_expect_tx(&bars->q_full[st], 32768 + 1024);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tma_load_4d(smem + L::kQ + st * 16384 + c * 8192, &tmQ, &bars->q_full[st], 0, q0, 2 * sp.hq + c, it.b);
+              tma_load_4d(smem + L::kDO + st * 16384 + c * 8192, &tmDO, &bars->q_full[st], c * 64, q0, sp.hq, it.b);
+            }
+            bulk_load(smem + L::kLD + st * 1024, a.rows + ld_row, 1024, &bars->q_full[st]);
+            info[g & 3] = make_int4(q0, sp.hq, it.b, 0);
+            if (!(ok = reduce_to(g - kLag))) {
+              ++g;                       // this step's loads are in flight
+              break;
+            }
+          }
+        }
+        if (ok) ok = reduce_to(g - 1);
+        for (int t = max(0, g - NQ); t < g; ++t) mbar_wait(&bars->q_full[t % NQ], (uint32_t)(t / NQ) & 1u, ctl);
+        if (nkv > 0) mbar_wait(&bars->kv_full, (uint32_t)(nkv - 1) & 1u, ctl);
+        bulk_wait_read0();
+      }
+    } else if (warp == 17) {
+      // ===================== S^T / dP^T issuer =====================
+      if (lane == 0) {
+        int g = 0, nkv = 0;
+        bool ok = true;
+        int u;
+        while (ok && (u = fetch()) >= 0) {
+          const DItem it = make_item(a, u);
+          if (it.steps == 0) continue;
+          if (!(ok = mbar_wait(&bars->kv_full, (uint32_t)nkv & 1u, ctl))) break;
+          ++nkv;
+          for (int t = 0; t < it.steps && ok; ++t, ++g) {
+            const int st = g % NQ;
+            // S_2^T(g) once part 1 of step g-1 has read S_2^T(g-1); S_1^T(g) also
+            // once dV(g-1) has read W^T(g-1), which lies over S_1^T(g-1)
+            if (g > 0 && !(ok = mbar_wait(&bars->p_full, (uint32_t)(g - 1) & 1u, ctl))) break;
+            if (!(ok = mbar_wait(&bars->q_full[st], (uint32_t)(g / NQ) & 1u, ctl))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss(tmem + kColS2, sdesc_sw128(sK + 32768 + k * 32, 16, 1024),
+                     sdesc_sw128(sQ + st * 16384 + 8192 + k * 32, 16, 1024), idST, k > 0 ? 1u : 0u);
+            if (g > 0 && !(ok = mbar_wait(&bars->pt_free, (uint32_t)(g - 1) & 1u, ctl))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss(tmem + kColS1, sdesc_sw128(sK + k * 32, 16, 1024), sdesc_sw128(sQ + st * 16384 + k * 32, 16, 1024),
+                     idST, k > 0 ? 1u : 0u);
+            mma_commit(&bars->s_full);
+            // dP^T(g) = V dO_g^T once part 2 of step g-1 has read dP^T(g-1)
+            if (g > 0 && !(ok = mbar_wait(&bars->ds_full, (uint32_t)(g - 1) & 1u, ctl))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ss(tmem + kColDP, sdesc_sw128(sV + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                     sdesc_sw128(sDO + st * 16384 + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), idST, k > 0 ? 1u : 0u);
+            mma_commit(&bars->dp_full);
+          }
+          mma_commit(&bars->kv_empty);    // this item's S^T and dP^T are done with K, V
+        }
+        mma_commit(&bars->done[0]);
+        mbar_wait(&bars->done[0], 0, ctl);
+      }
+    } else if (warp == 18) {
+      // ===================== dV / dK issuer =====================
+      if (lane == 0) {
+        int g = 0;
+        bool ok = true;
+        int u;
+        while (ok && (u = fetch()) >= 0) {
+          const DItem it = make_item(a, u);
+          if (it.steps == 0) continue;
+          for (int t = 0; t < it.steps && ok; ++t, ++g) {
+            const int st = g % NQ;
+            const uint32_t qb = sQ + st * 16384, db = sDO + st * 16384;
+            // dV += W^T dO_g: A = W^T (16 queries per 16 columns of S_1's place), B = dO MN-major
+            if (!(ok = mbar_wait(&bars->p_full, (uint32_t)g & 1u, ctl) &&
+                       mbar_wait(&bars->q_full[st], (uint32_t)(g / NQ) & 1u, ctl))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColDV, tmem + kColS1 + k * 16, sdesc_sw128(db + k * 2048, 8192, 1024), idV,
+                     (t > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&bars->pt_free);
+            // dK_m += dS_m^T Q_m: A = dS^T K-major (32 bytes per 16 queries), B = Q MN-major
+            if (!(ok = mbar_wait(&bars->ds_full, (uint32_t)g & 1u, ctl))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ss(tmem + kColDK + m * 64, sdesc_sw128(sDS + m * 16384 + k * 32, 16, 1024),
+                       sdesc_sw128(qb + m * 8192 + k * 2048, 8192, 1024), idK, (t > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&bars->dsm_free);
+            mma_commit(&bars->q_empty[st]);
+          }
+          mma_commit(&bars->dkv_full);
+        }
+        mma_commit(&bars->done[1]);
+        mbar_wait(&bars->done[1], 0, ctl);
+      }
+    } else {
+      // ===================== dQ^T issuer (warp 19, all lanes) =====================
+      int g = 0, nkv = 0;
+      bool ok = true;
+      while (ok) {
+        const int slot = kc & 1;
+        if (!(ok = warp_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl))) break;
+        const int u = item_u[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
+        ++kc;
+        if (u < 0) break;
+        const DItem it = make_item(a, u);
+        if (it.steps == 0) continue;
+        const int live = it.Lk - it.jt * kTile;       // K rows of this tile that count
+        if (live < kTile) {
+          if (!(ok = warp_wait(&bars->kv_full, (uint32_t)nkv & 1u, ctl))) break;
+          for (int o = live * 128 + lane * 16; o < 16384; o += 512) {
+            *reinterpret_cast<uint4*>(smem + L::kK + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + L::kK + 32768 + o) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ++nkv;
+        for (int t = 0; t < it.steps && ok; ++t, ++g) {
+          if (!(ok = warp_wait(&bars->ds_full, (uint32_t)g & 1u, ctl))) break;
+          if (g > 0 && !(ok = warp_wait(&bars->dq_free, (uint32_t)(g - 1) & 1u, ctl))) break;
+          if (lane == 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_ss(tmem + kColDQ, sdesc_sw128(sK + m * 16384 + k * 2048, 16384, 1024),
+                       sdesc_sw128(sDS + m * 16384 + k * 2048, 8192, 1024), idQ, (m > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&bars->dq_full);
+            mma_commit(&bars->dsm_free);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mma_commit(&bars->kv_empty);   // this item's dQ^T products are done with K
+        __syncwarp();
+      }
+      if (lane == 0) {
+        mma_commit(&bars->done[2]);
+        mbar_wait(&bars->done[2], 0, ctl);
+      }
+    }
+  } else {
+    // ===================== softmax-gradient warpgroups =====================
+    const int wg = warp >> 2;                 // query columns 16 wg .. 16 wg + 15 of the step
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;        // key row, or (dQ^T) map r / 64 and head dim r % 64 = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tl = tmem + lane_off;
+    const float sl2 = a.scale_log2;
+    const float c1 = kFold ? a.scale : 1.f;
+    const int c0 = wg * 16;                   // first query column of this warpgroup
+    bool ok = true;
+
+    // dQ_t: row r of the stacked dQ^T, this warpgroup's 16 queries -> x tau
+    // (fp16) -> float32 staging box r / 32 (128-byte rows of queries, 128-byte swizzle)
+    auto drain_dq = [&](int t) -> bool {
+      if (!warp_wait(&bars->dq_full, (uint32_t)t & 1u, ctl)) return false;
+      tc_fence_after();
+      uint32_t g[16];
+      tmem_ld16(tl + kColDQ + c0, g);
+      tmem_wait_ld();
+      reg_fence16(g);
+      tc_fence_before();
+      mbar_arrive(&bars->dq_free);
+      if (t >= 1 && !warp_wait(&bars->stg_free, (uint32_t)(t - 1) & 1u, ctl)) return false;
+      uint8_t* sb = smem + L::kDQ + quarter * 8192;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const int q = c0 + c;
+        const uint32_t off = q * 128 + ((((lane >> 2) ^ q) & 7) << 4) + (lane & 3) * 4;
+        const float v = kFold ? __uint_as_float(g[c]) : __uint_as_float(g[c]) * a.scale;
+        asm volatile("st.shared.f32 [%0], %1;" :: "r"(smem_u32(sb + off)), "f"(v) : "memory");
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->stg_full);
+      return true;
+    };
+
+    // dK (x tau for fp16) and dV of an item: columns 32 wg .. 32 wg + 31 of the
+    // stacked (dK_1 | dK_2) row and of the dV row, in two halves of 16
+    auto store_dkv = [&](const DItem& it, int half, const uint32_t (&kraw)[16], const uint32_t (&vraw)[16],
+                         bool have) {
+      const int j = it.jt * kTile + r;
+      if (j >= a.N) return;
+      const size_t koff = (size_t)it.b * a.kst.b + (size_t)(2 * it.hk + (wg >> 1)) * a.kst.h + (size_t)j * a.kst.n +
+                          (wg & 1) * 32 + half * 16;
+      const size_t voff =
+          (size_t)it.b * a.vst.b + (size_t)it.hk * a.vst.h + (size_t)j * a.vst.n + wg * 32 + half * 16;
+      uint32_t wk[8], wv[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float ks = kFold ? 1.f : a.scale;   // bf16: dK is already scaled
+        wk[c] = Cvt<T>::pack(have ? __uint_as_float(kraw[2 * c]) * ks : 0.f,
+                             have ? __uint_as_float(kraw[2 * c + 1]) * ks : 0.f);
+        wv[c] = Cvt<T>::pack(have ? __uint_as_float(vraw[2 * c]) : 0.f, have ? __uint_as_float(vraw[2 * c + 1]) : 0.f);
+      }
+      if (a.dkv_v8) {
+        // one 32-byte store per tensor: whole sectors in one instruction
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     :: "l"(static_cast<T*>(a.dk) + koff), "r"(wk[0]), "r"(wk[1]), "r"(wk[2]), "r"(wk[3]),
+                        "r"(wk[4]), "r"(wk[5]), "r"(wk[6]), "r"(wk[7]) : "memory");
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     :: "l"(static_cast<T*>(a.dv) + voff), "r"(wv[0]), "r"(wv[1]), "r"(wv[2]), "r"(wv[3]),
+                        "r"(wv[4]), "r"(wv[5]), "r"(wv[6]), "r"(wv[7]) : "memory");
+        return;
+      }
+      uint4* dk = reinterpret_cast<uint4*>(static_cast<T*>(a.dk) + koff);
+      uint4* dv = reinterpret_cast<uint4*>(static_cast<T*>(a.dv) + voff);
+      dk[0] = make_uint4(wk[0], wk[1], wk[2], wk[3]);
+      dk[1] = make_uint4(wk[4], wk[5], wk[6], wk[7]);
+      dv[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+      dv[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+    };
+
+    volatile int* item_u = reinterpret_cast<volatile int*>(smem + L::kItem);
+    int kc = 0;
+    auto fetch = [&]() -> int {
+      const int slot = kc & 1;
+      if (!warp_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl)) return -1;
+      const int v = item_u[slot];
+      mbar_arrive(&bars->item_empty[slot]);
+      ++kc;
+      return v;
+    };
+    int t = 0;        // global step
+    int nit = 0;      // items with steps (dkv_full phases)
+    int u;
+    while (ok && (u = fetch()) >= 0) {
+      const DItem it = make_item(a, u);
+      float* part = a.dlam_part + (size_t)u * a.group * 16 + warp;
+      if (it.steps == 0) {            // no query tile sees this key tile: dK = dV = 0, nothing for dlambda
+        const uint32_t zero[16] = {};
+        store_dkv(it, 0, zero, zero, false);
+        store_dkv(it, 1, zero, zero, false);
+        for (int g = lane; g < a.group; g += 32) part[g * 16] = 0.f;
+        continue;
+      }
+      const int j = it.jt * kTile + r;          // global key
+      const bool key_ok = j < it.Lk;
+      StepPos sp;
+      sp.hq = it.h0;
+      float lam = a.lam[it.h0];
+      float dl0 = 0.f, dl1 = 0.f;               // sum of P_2 o dP of this thread, current head pair
+      for (int tt = 0; tt < it.steps && ok; ++tt, ++t, sp.next(it)) {
+        const int st = t % NQ;
+        const int q0 = (it.i0 + sp.qu) * kTile + sp.hf * kQS;   // first query row of the step
+        const uint32_t s_ld = smem_u32(smem + L::kLD + st * 1024) + c0 * 4;
+        // query column c of the step is hidden from this key under causal iff
+        // c < qlo, and outside its sliding window iff c >= qhe
+        const int qlo = a.causal ? (j - q0) : -1;
+        const int qhe = kWin ? (int)min((long long)j + a.window - q0, (long long)kQS) : kQS;
+        const bool any_mask = !key_ok || qlo > c0 || (kWin && qhe < c0 + 16);
+
+        // ---- part 1: P_1, P_2 (float32, kept) and W = P_1 - lambda P_2
+        if (!(ok = warp_wait(&bars->s_full, (uint32_t)t & 1u, ctl) &&
+                   warp_wait(&bars->q_full[st], (uint32_t)(t / NQ) & 1u, ctl))) break;
+        tc_fence_after();
+        uint32_t s1[16], s2[16];
+        tmem_ld16(tl + kColS1 + c0, s1);
+        tmem_ld16(tl + kColS2 + c0, s2);
+        tmem_wait_ld();
+        reg_fence16(s1);
+        reg_fence16(s2);
+        float p1[16], p2[16];
+        uint32_t w[8];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          const int cc = q4 * 4;
+          const float4 l1 = lds128(s_ld + cc * 4), l2 = lds128(s_ld + 256 + cc * 4);
+          fma2(p1[cc], p1[cc + 1], __uint_as_float(s1[cc]), __uint_as_float(s1[cc + 1]), sl2, sl2, -l1.x, -l1.y);
+          fma2(p1[cc + 2], p1[cc + 3], __uint_as_float(s1[cc + 2]), __uint_as_float(s1[cc + 3]), sl2, sl2, -l1.z, -l1.w);
+          fma2(p2[cc], p2[cc + 1], __uint_as_float(s2[cc]), __uint_as_float(s2[cc + 1]), sl2, sl2, -l2.x, -l2.y);
+          fma2(p2[cc + 2], p2[cc + 3], __uint_as_float(s2[cc + 2]), __uint_as_float(s2[cc + 3]), sl2, sl2, -l2.z, -l2.w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p1[cc + e] = ex2(p1[cc + e]);
+            p2[cc + e] = ex2(p2[cc + e]);
+          }
+          if (any_mask) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!key_ok || c0 + cc + e < qlo || (kWin && c0 + cc + e >= qhe)) p1[cc + e] = p2[cc + e] = 0.f;
+          }
+          float w0, w1, w2, w3;
+          fma2(w0, w1, p2[cc], p2[cc + 1], -lam, -lam, p1[cc], p1[cc + 1]);
+          fma2(w2, w3, p2[cc + 2], p2[cc + 3], -lam, -lam, p1[cc + 2], p1[cc + 3]);
+          w[q4 * 2] = Cvt<T>::pack(w0, w1);
+          w[q4 * 2 + 1] = Cvt<T>::pack(w2, w3);
+        }
+        // over this warpgroup's own columns of S_1^T, which are in registers
+        tmem_st8(tl + kColS1 + c0, w);
+        if (!(ok = warp_wait(&bars->dp_full, (uint32_t)t & 1u, ctl))) break;
+        tc_fence_after();
+        uint32_t dp[16];
+        tmem_ld16(tl + kColDP + c0, dp);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full);
+
+        // ---- part 2: dS_1, dS_2 from dP^T into the shared tiles once dK and
+        //      dQ^T of the previous step have read them
+        if (t >= 1 && !(ok = warp_wait(&bars->dsm_free, (uint32_t)(t - 1) & 1u, ctl))) break;
+        tmem_wait_ld();
+        reg_fence16(dp);
+        if (!key_ok) {          // V behind the sequence may hold NaN
+#pragma unroll
+          for (int c = 0; c < 16; ++c) dp[c] = 0u;
+        }
+        const float c2 = -lam * c1;
+        uint32_t d1w[8], d2w[8];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          const int cc = q4 * 4;
+          // e_1 = -c_1 D_1, e_2 = -c_2 D_2
+          const float4 e1 = lds128(s_ld + 512 + cc * 4), e2 = lds128(s_ld + 768 + cc * 4);
+          const float g0 = __uint_as_float(dp[cc]), g1 = __uint_as_float(dp[cc + 1]);
+          const float g2 = __uint_as_float(dp[cc + 2]), g3 = __uint_as_float(dp[cc + 3]);
+          fma2(dl0, dl1, p2[cc], p2[cc + 1], g0, g1, dl0, dl1);
+          fma2(dl0, dl1, p2[cc + 2], p2[cc + 3], g2, g3, dl0, dl1);
+          float y0, y1, y2, y3;
+          fma2(y0, y1, g0, g1, c1, c1, e1.x, e1.y);
+          fma2(y2, y3, g2, g3, c1, c1, e1.z, e1.w);
+          mul2(y0, y1, y0, y1, p1[cc], p1[cc + 1]);
+          mul2(y2, y3, y2, y3, p1[cc + 2], p1[cc + 3]);
+          d1w[q4 * 2] = Cvt<T>::pack(y0, y1);
+          d1w[q4 * 2 + 1] = Cvt<T>::pack(y2, y3);
+          fma2(y0, y1, g0, g1, c2, c2, e2.x, e2.y);
+          fma2(y2, y3, g2, g3, c2, c2, e2.z, e2.w);
+          mul2(y0, y1, y0, y1, p2[cc], p2[cc + 1]);
+          mul2(y2, y3, y2, y3, p2[cc + 2], p2[cc + 3]);
+          d2w[q4 * 2] = Cvt<T>::pack(y0, y1);
+          d2w[q4 * 2 + 1] = Cvt<T>::pack(y2, y3);
+        }
+        // this warpgroup's 16 queries are the 16-byte pieces 2 wg, 2 wg + 1 of the key's 128-byte rows
+        const uint32_t dsb = smem_u32(smem + L::kDS + r * 128);
+#pragma unroll
+        for (int pc2 = 0; pc2 < 2; ++pc2) {
+          const uint32_t off = ((((2 * wg + pc2) ^ r) & 7) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(dsb + off), "r"(d1w[pc2 * 4]), "r"(d1w[pc2 * 4 + 1]), "r"(d1w[pc2 * 4 + 2]),
+                          "r"(d1w[pc2 * 4 + 3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(dsb + 16384 + off), "r"(d2w[pc2 * 4]), "r"(d2w[pc2 * 4 + 1]), "r"(d2w[pc2 * 4 + 2]),
+                          "r"(d2w[pc2 * 4 + 3]) : "memory");
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bars->ds_full);
+
+        // ---- the head pair's last step of this item: its part of dlambda
+        if (sp.hf == 1 && sp.qu == it.n - 1) {
+          float s = dl0 + dl1;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane == 0) part[(sp.hq - it.h0) * 16] = s;
+          dl0 = dl1 = 0.f;
+          if (tt + 1 < it.steps) lam = a.lam[sp.hq + 1];
+        }
+        // ---- drain dQ of the previous step
+        if (t > 0 && !(ok = drain_dq(t - 1))) break;
+      }
+      if (!ok) break;
+      // ---- item end: dK, dV out of tensor memory (the next item's first dV /
+      //      dK follow this thread's next p_full / ds_full arrivals)
+      if (!(ok = warp_wait(&bars->dkv_full, (uint32_t)nit & 1u, ctl))) break;
+      ++nit;
+      tc_fence_after();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t kraw[16], vraw[16];
+        tmem_ld16(tl + kColDK + wg * 32 + half * 16, kraw);
+        tmem_ld16(tl + kColDV + wg * 32 + half * 16, vraw);
+        tmem_wait_ld();
+        reg_fence16(kraw);
+        reg_fence16(vraw);
+        store_dkv(it, half, kraw, vraw, true);
+      }
+      tc_fence_before();
+    }
+    if (ok && t > 0) ok = drain_dq(t - 1);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// D_1 and D_2 of every query row from dO . O and dO . O_2 (D_1 = dO . O +
+// lambda D_2), the logsumexps in log2 units, all in the 64-row groups that a
+// step loads in one piece; the dQ accumulator is cleared on the way.  Eight
+// threads a row, 16 columns each.  Bound by HBM: three 256-byte rows read, two
+// 256-byte accumulator rows written.
+template <typename T>
+__global__ void diff_prep_kernel(const T* __restrict__ o, const T* __restrict__ o2, Strides ost,
+                                 const T* __restrict__ dout, Strides dst, const float* __restrict__ lse,
+                                 const float* __restrict__ lam, int H, int N, int npad, long long total, float c1,
+                                 float* __restrict__ rows, float* __restrict__ dqacc, int* __restrict__ sched) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *sched = 0;   // work counter of the main kernel
+  const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
+  const int part = threadIdx.x & 7;
+  const bool live = row < total;
+  const long long bh = live ? row / npad : 0;
+  const int i = live ? (int)(row - bh * npad) : N;
+  const int b = (int)(bh / H), h = (int)(bh % H);
+  float d = 0.f, d2 = 0.f;
+  if (live && i < N) {
+    const size_t oo = (size_t)b * ost.b + (size_t)h * ost.h + (size_t)i * ost.n;
+    const size_t od = (size_t)b * dst.b + (size_t)h * dst.h + (size_t)i * dst.n;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int c = part * 8 + m * 64;
+      const uint4 uo = *reinterpret_cast<const uint4*>(o + oo + c), u2 = *reinterpret_cast<const uint4*>(o2 + oo + c);
+      const uint4 ud = *reinterpret_cast<const uint4*>(dout + od + c);
+      const uint32_t wo[4] = {uo.x, uo.y, uo.z, uo.w}, w2[4] = {u2.x, u2.y, u2.z, u2.w}, wd[4] = {ud.x, ud.y, ud.z, ud.w};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float g0 = Cvt<T>::lo(wd[t]), g1 = Cvt<T>::hi(wd[t]);
+        d += g0 * Cvt<T>::lo(wo[t]) + g1 * Cvt<T>::hi(wo[t]);
+        d2 += g0 * Cvt<T>::lo(w2[t]) + g1 * Cvt<T>::hi(w2[t]);
+      }
+      // heads 2h, 2h + 1 of the accumulator [B,2H,N,64]: this thread's 8 columns of map m
+      float4* z = reinterpret_cast<float4*>(dqacc + (((size_t)bh * 2 + m) * N + i) * 64 + part * 8);
+      z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) {
+    d += __shfl_xor_sync(0xffffffffu, d, s);
+    d2 += __shfl_xor_sync(0xffffffffu, d2, s);
+  }
+  if (live && part < 4) {
+    // part 0, 1: LSE of map 1, 2 in log2 units; part 2, 3: e_1 = -c_1 D_1, e_2 = lambda c_1 D_2
+    float v;
+    if (part < 2) {
+      v = INFINITY;
+      if (i < N) {
+        const float l = lse[((size_t)bh * 2 + part) * N + i];
+        v = l == -INFINITY ? INFINITY : l * kLog2e;
+      }
+    } else {
+      const float lm = lam[h];
+      v = i >= N ? 0.f : part == 2 ? -c1 * (d + lm * d2) : lm * c1 * d2;
+    }
+    rows[((size_t)row >> 6) * 256 + part * 64 + (row & 63)] = v;
+  }
+}
+
+// dlambda of head pair blockIdx.x: every item's and warp's part, in a fixed order.
+__global__ void diff_dlam_kernel(const float* __restrict__ part, float* __restrict__ dlam, int B, int H, int group,
+                                 int nq) {
+  __shared__ float sh[256];
+  const int h = blockIdx.x, hk = h / group, j = h % group, hkv = H / group;
+  const long long n = (long long)B * nq * 16;
+  float s = 0.f;
+  for (long long e = threadIdx.x; e < n; e += 256) {
+    const long long it = e >> 4;
+    const long long b = it / nq, jt = it - b * nq;
+    s += part[(((b * hkv + hk) * nq + jt) * group + j) * 16 + (e & 15)];
+  }
+  sh[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if (threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) dlam[h] = -sh[0];
+}
+
+template <typename T, bool kWin>
+cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
+                     const CUtensorMap& dqacc, const DiffBwdArgs& a, cudaStream_t s) {
+  auto kern = diff_bwd_kernel<T, kWin>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DSmem::kDyn);
+  if (e != cudaSuccess) return e;
+  const long long total = (long long)a.nq * a.B * a.H_kv;
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<long long>(total, (long long)std::max(sms, 1));
+  kern<<<grid, kThreads, DSmem::kDyn, s>>>(q, k, v, dout, dqacc, a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t prep_t(const void* o, const void* o2, Strides ost, const void* dout, Strides dst, const float* lse,
+                   const float* lam, int B, int H, int N, int npad, float c1, float* rows, float* dqacc, int* sched,
+                   cudaStream_t s) {
+  const long long total = (long long)B * H * npad;
+  const unsigned grid = (unsigned)((total * 8 + 255) / 256);
+  diff_prep_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(o), static_cast<const T*>(o2), ost,
+                                           static_cast<const T*>(dout), dst, lse, lam, H, N, npad, total, c1, rows,
+                                           dqacc, sched);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides ost, const void* dout, Strides dost,
+                             const float* lse, const float* lam, int B, int H, int N, int npad, float c1, float* rows,
+                             float* dqacc, int* sched, cudaStream_t s) {
+  if (dtype == FA_DT_BF16)
+    return prep_t<__nv_bfloat16>(o, o2, ost, dout, dost, lse, lam, B, H, N, npad, c1, rows, dqacc, sched, s);
+  return prep_t<__half>(o, o2, ost, dout, dost, lse, lam, B, H, N, npad, c1, rows, dqacc, sched, s);
+}
+
+cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const CUtensorMap& dout, const CUtensorMap& dqacc, const DiffBwdArgs& a, cudaStream_t s) {
+  if (dtype == FA_DT_BF16)
+    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, dout, dqacc, a, s)
+                        : launch_t<__nv_bfloat16, false>(q, k, v, dout, dqacc, a, s);
+  return a.window > 0 ? launch_t<__half, true>(q, k, v, dout, dqacc, a, s)
+                      : launch_t<__half, false>(q, k, v, dout, dqacc, a, s);
+}
+
+cudaError_t launch_diff_dlam(const float* part, float* dlam, int B, int H, int group, int nq, cudaStream_t s) {
+  diff_dlam_kernel<<<H, 256, 0, s>>>(part, dlam, B, H, group, nq);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

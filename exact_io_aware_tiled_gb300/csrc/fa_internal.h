@@ -95,6 +95,38 @@ struct BwdArgs {
   int* status;
 };
 
+// Differential attention: head pair h of H has score maps 2h and 2h + 1.
+struct DiffFwdArgs {
+  int B, H, N;                // H: head pairs
+  int group;                  // query pairs per K/V pair
+  int nq;                     // ceil(N / 128)
+  int causal, window;
+  float scale_log2;           // tau * log2(e)
+  const int32_t* seqlens_k;   // device [B] or nullptr
+  const float* lam;           // device [H]
+  float* lse;                 // [B,2H,N]
+  int has_o2;                 // also store O_2 (the second map's own output)
+  int* status;
+};
+
+struct DiffBwdArgs {
+  int B, H, H_kv, N;
+  int group;
+  int nq, npad;               // ceil(N / 128), nq * 128
+  int causal, window;
+  float scale, scale_log2;    // tau, tau * log2(e)
+  const int32_t* seqlens_k;
+  const float* lam;
+  const float* rows;          // [B*H][npad/64][4][64]: per 64 query rows the two maps' LSE*log2e, then e_1, e_2
+  float* dlam_part;           // [items * group][16]: per-warp sums of P_2 o dP
+  void* dk;                   // [B,2H_kv,N,64], strides kst
+  void* dv;                   // [B,H_kv,N,128], strides vst
+  Strides kst, vst;
+  int dkv_v8;                 // dk, dv allow 32-byte stores
+  int* sched;
+  int* status;
+};
+
 // ---------------------------------------------------------------------------
 // Launchers (defined in the .cu files; all enqueue on `stream`).
 // ---------------------------------------------------------------------------
@@ -135,6 +167,17 @@ cudaError_t launch_dropout_mask(const DropoutArgs& d, int H, int N, int b, int h
 cudaError_t launch_fp8_quantize(int dtype, const Fp8QuantArgs& a, int per_tensor, cudaStream_t s);
 cudaError_t launch_fwd_fp8(int d, const CUtensorMap& q8, const CUtensorMap& k8, const CUtensorMap& v8t,
                            const CUtensorMap& o, const FwdArgs& a, cudaStream_t s);
+// Differential attention.  Maps: q, k over [B,2H,N,64] / [B,2H_kv,N,64] (box 64 columns), v, o, o2 over
+// [B,H_kv,N,128] / [B,H,N,128] (boxes of 64 columns); the backward's q and dout boxes have 64 rows.
+cudaError_t launch_diff_fwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const CUtensorMap& o, const CUtensorMap& o2, const DiffFwdArgs& a, cudaStream_t s);
+cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides ost, const void* dout, Strides dost,
+                             const float* lse, const float* lam, int B, int H, int N, int npad, float c1, float* rows,
+                             float* dqacc, int* sched, cudaStream_t s);
+cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            const CUtensorMap& dout, const CUtensorMap& dqacc, const DiffBwdArgs& a, cudaStream_t s);
+// dlam[h] = -sum of the partial sums, in a fixed order.
+cudaError_t launch_diff_dlam(const float* part, float* dlam, int B, int H, int group, int nq, cudaStream_t s);
 cudaError_t launch_wait_selftest(int* status, int* out, unsigned long long* out_ns, cudaStream_t s);
 
 }  // namespace fa

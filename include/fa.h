@@ -380,6 +380,62 @@ fa_status fa_rope(const fa_rope_params *p, const void *q, const void *k, void *q
 fa_status fa_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, int64_t original_len,
                               double beta_fast, double beta_slow, double *inv_freq, float *mscale);
 
+/* ---------------------------------------------------------------------------
+ * Differential attention (ABI 1.4).
+ * Head pair h (of H) has two score maps over one set of values:
+ *     P_m = softmax(tau Q_m K_m^T + mask), m = 1, 2;   O = (P_1 - lam[h] P_2) V.
+ *   - q: [B,2H,N,64], the pair's maps in heads 2h and 2h + 1; k: [B,2H_kv,N,64]
+ *     alike; v: [B,H_kv,N,128]; o, o2: [B,H,N,128] (one stride set for both);
+ *     lse: contiguous float32 [B,2H,N], natural log, one row set per map.
+ *     Query pair h reads K/V pair h / (H / H_kv); H_kv = 0 selects H.
+ *   - float16 or bfloat16, d = 64 (128 value columns); others return
+ *     FA_ERR_UNSUPPORTED.  lam: device float32 [H], any finite values.
+ *   - Masks: causal, seqlens_k (keys j >= L_b are masked; K and V rows there
+ *     may hold anything, NaN included), window (causal only).  A query row
+ *     that sees no key has O = 0, O_2 = 0, both logsumexps -inf and no part
+ *     in any gradient.  Every other K and V row should be finite: the tile
+ *     products spread a NaN or infinity over the query rows of its tile.
+ *   - Weights are rounded to the dtype before the product with V, which is
+ *     summed in float32 and normalised by the sum of the rounded weights.
+ *   - 2*B*H*N < 2^32.  16-byte rule for bases and strides (a dimension of one
+ *     element may have any stride).
+ * fa_diff_fwd writes o, lse and, when o2 is not NULL, the second map's own
+ * output O_2 = P_2 V, which the backward pass needs.
+ * fa_diff_bwd takes o, o2 and lse of a forward call with the same p and inputs
+ * and writes, for the upstream gradient dout [B,H,N,128] (do_stride_*):
+ *     dP = dO V^T, D_m = rowsum(P_m o dP), dS_1 = P_1 o (dP - D_1),
+ *     dS_2 = -lam P_2 o (dP - D_2), dV = (P_1 - lam P_2)^T dO,
+ *     dQ_m = tau dS_m K_m, dK_m = tau dS_m^T Q_m, dlam = -sum D_2
+ * with dq, dk, dv in q's, k's and v's strides (no broadcast strides) and dlam
+ * float32 [H].  D_m comes from dO and the rounded O and O_2, so a row whose
+ * exact dS vanishes (one visible key) gets a residue of their rounding.  dQ is
+ * accumulated in float32 in the order in which the key tiles finish: its last
+ * bit may differ from run to run; every other output repeats bit for bit.
+ * Workspace: fa_diff_*_workspace_size bytes, 16-byte aligned; status word at
+ * its start, read by fa_check_status.  Nothing persists in it between calls.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, H, H_kv, N, d;  /* H: head pairs; d = 64 columns per map           */
+  int32_t dtype;
+  int32_t causal, window;    /* as in fa_params                                 */
+  float scale;               /* tau; <= 0 selects 1/sqrt(d)                     */
+  const int32_t *seqlens_k;  /* device [B] or NULL                              */
+  const float *lam;          /* device float32 [H]                              */
+  int64_t q_stride_b, q_stride_h, q_stride_n;
+  int64_t k_stride_b, k_stride_h, k_stride_n;
+  int64_t v_stride_b, v_stride_h, v_stride_n;
+  int64_t o_stride_b, o_stride_h, o_stride_n;
+  int64_t do_stride_b, do_stride_h, do_stride_n;   /* fa_diff_bwd only          */
+} fa_diff_params;
+
+size_t fa_diff_fwd_workspace_size(const fa_diff_params *p);
+size_t fa_diff_bwd_workspace_size(const fa_diff_params *p);
+fa_status fa_diff_fwd(const fa_diff_params *p, const void *q, const void *k, const void *v, void *o, void *o2,
+                      float *lse, void *ws, size_t ws_bytes, void *stream);
+fa_status fa_diff_bwd(const fa_diff_params *p, const void *q, const void *k, const void *v, const void *o,
+                      const void *o2, const void *dout, const float *lse, void *dq, void *dk, void *dv, float *dlam,
+                      void *ws, size_t ws_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fa_status_string(fa_status s);
 

@@ -1,0 +1,312 @@
+"""The differential-attention kernels' barrier protocols, simulated on the CPU.
+
+Forward (csrc/diff_fwd.cu): one query tile, two score maps.  A stage holds the
+K tiles of both maps (released by the S issuer) and one V tile (released by
+both P V issuers); a stage's first use skips the empty waits; S_x(s) waits for
+P V_x(s-1), because P_x lies over S_x.
+
+Backward (csrc/diff_bwd.cu): the roles of the d = 128 backward with a two-stage
+Q / dO ring, and W^T over S_1^T: the S issuer waits for dV(g-1) before S_1(g),
+the compute warps do not wait for it.
+
+tests/protocol_sim.py checks for deadlocks and for parity waits that pass early
+or alias; here also that nothing reads a buffer that is being refilled.
+Planted mistakes must fail.
+"""
+import random
+
+import pytest
+
+from tests.protocol_sim import Bar, Engine, ProtocolError
+
+NS = 3
+
+
+class Forward:
+    def __init__(self, n, rng, plant=None):
+        self.n, self.plant = n, plant
+        self.engine = Engine(rng)
+        self.q_full = Bar("q_full", 1)
+        self.s_full = [Bar("s_full%d" % x, 1) for x in range(2)]
+        self.p_full = [Bar("p_full%d" % x, 1) for x in range(2)]
+        self.pv_done = [Bar("pv_done%d" % x, 1) for x in range(2)]
+        self.k_full = [Bar("k_full%d" % i, 1) for i in range(NS)]
+        self.v_full = [Bar("v_full%d" % i, 1) for i in range(NS)]
+        self.k_empty = [Bar("k_empty%d" % i, 1) for i in range(NS)]
+        self.v_empty = [Bar("v_empty%d" % i, 1 if plant == "v_one_reader" else 2) for i in range(NS)]
+        self.nloads = 0
+
+    def load(self, bar):
+        self.nloads += 1
+        self.engine.later(("tma", self.nloads), bar)
+
+    def producer(self):
+        if self.n == 0:
+            return
+        self.load(self.q_full)
+        for s in range(self.n):
+            st = s % NS
+            if s >= NS:
+                yield ("wait", self.k_empty[st], s // NS - 1)
+            self.load(self.k_full[st])
+            if s >= NS:
+                yield ("wait", self.v_empty[st], s // NS - 1)
+            for x in range(2):
+                if s >= NS and self.pv_done[x].completed < s - NS + 1:
+                    raise ProtocolError("V of step %d refilled before map %d read it" % (s - NS, x))
+            self.load(self.v_full[st])
+        for j in range(max(0, self.n - NS), self.n):
+            yield ("wait", self.k_full[j % NS], j // NS)
+            yield ("wait", self.v_full[j % NS], j // NS)
+        yield ("wait", self.q_full, 0)
+
+    def s_issuer(self):
+        if self.n == 0:
+            return
+        yield ("wait", self.q_full, 0)
+        for s in range(self.n):
+            yield ("wait", self.k_full[s % NS], s // NS)
+            for x in range(2):
+                if s > 0 and self.plant != "s_ungated":
+                    yield ("wait", self.pv_done[x], s - 1)
+                if self.pv_done[x].completed < s:
+                    raise ProtocolError("S_%d(%d) written over P that its product still reads" % (x, s))
+                self.engine.later("S", self.s_full[x])
+            self.engine.later("S", self.k_empty[s % NS])
+
+    def pv_issuer(self, x):
+        for s in range(self.n):
+            yield ("wait", self.v_full[s % NS], s // NS)
+            yield ("wait", self.p_full[x], s)
+            self.engine.later("PV%d" % x, self.pv_done[x])
+            self.engine.later("PV%d" % x, self.v_empty[s % NS])
+
+    def softmax(self, x):
+        for s in range(self.n):
+            yield ("wait", self.s_full[x], s)
+            self.p_full[x].arrive()
+        if self.n > 0:
+            # the last product of the warpgroup's own map; the other's may be
+            # phases behind, so it is learned from the barrier of both groups
+            y = 1 - x if self.plant == "waits_for_other_map" else x
+            yield ("wait", self.pv_done[y], self.n - 1)
+
+    def run(self):
+        self.engine.run({"P": self.producer(), "S": self.s_issuer(), "V0": self.pv_issuer(0), "V1": self.pv_issuer(1),
+                         "X0": self.softmax(0), "X1": self.softmax(1)})
+
+
+def test_forward_protocol():
+    for n in list(range(0, 9)) + [17]:
+        for seed in range(40):
+            Forward(n, random.Random(1000 * n + seed)).run()
+
+
+@pytest.mark.parametrize("plant", ["v_one_reader", "s_ungated", "waits_for_other_map"])
+def test_forward_planted_mistakes_are_caught(plant):
+    for seed in range(300):
+        try:
+            Forward(9, random.Random(seed), plant=plant).run()
+        except ProtocolError:
+            return
+    pytest.fail("not caught")
+
+
+NQ = 2       # Q / dO ring stages
+KLAG = 3     # the dQ reduce of step g - KLAG follows the loads of step g
+
+
+class Backward:
+    def __init__(self, items, rng, plant=None):
+        self.items, self.plant = items, plant
+        B = Bar
+        self.item_full = [B("item_full%d" % i, 1) for i in range(2)]
+        self.item_empty = [B("item_empty%d" % i, 4) for i in range(2)]
+        self.q_full = [B("q_full%d" % i, 1) for i in range(NQ)]
+        self.q_empty = [B("q_empty%d" % i, 1) for i in range(NQ)]
+        self.kv_full, self.kv_empty = B("kv_full", 1), B("kv_empty", 2)
+        for n in ("s_full", "p_full", "dp_full", "ds_full", "dq_full", "dq_free", "dkv_full", "pt_free", "stg_full",
+                  "stg_free"):
+            setattr(self, n, B(n, 1))
+        self.dsm_free = B("dsm_free", 2)
+        self.mailbox, self.info = [None, None], [None] * 4
+        self.engine = Engine(rng)
+        self.nloads = 0
+
+    def commit(self, who, bar):
+        self.engine.later(who, bar)
+
+    def load(self, bar):
+        self.nloads += 1
+        self.engine.later(("tma", self.nloads), bar)
+
+    def producer(self):
+        st = {"g": 0, "rd": 0, "kf": 0, "next": 0, "nkv": 0}
+
+        def reduce_to(last):
+            while st["rd"] <= last:
+                r = st["rd"]
+                yield ("wait", self.stg_full, r)
+                if self.info[r & 3] != r:
+                    raise ProtocolError("step coordinates of %d overwritten before its reduce" % r)
+                self.stg_free.arrive()
+                st["rd"] += 1
+
+        while True:
+            yield from reduce_to(st["g"] - KLAG)
+            slot = st["kf"] & 1
+            yield ("wait", self.item_empty[slot], (st["kf"] >> 1) - 1)
+            u = st["next"] if st["next"] < len(self.items) else -1
+            st["next"] += 1
+            self.mailbox[slot] = u
+            self.item_full[slot].arrive()
+            st["kf"] += 1
+            if u < 0:
+                break
+            if self.items[u] == 0:
+                continue
+            yield ("wait", self.kv_empty, st["nkv"] - 1)
+            self.load(self.kv_full)
+            st["nkv"] += 1
+            for _ in range(self.items[u]):
+                g = st["g"]
+                yield ("wait", self.q_empty[g % NQ], g // NQ - 1)
+                self.load(self.q_full[g % NQ])
+                self.info[g & 3] = g
+                yield from reduce_to(g - (KLAG - 3 if self.plant == "lag_too_short" else KLAG))
+                st["g"] += 1
+        yield from reduce_to(st["g"] - 1)
+
+    def fetch(self, kc):
+        slot = kc & 1
+        yield ("wait", self.item_full[slot], kc >> 1)
+        v = self.mailbox[slot]
+        self.item_empty[slot].arrive()
+        return v
+
+    def s_issuer(self):
+        kc = g = nkv = 0
+        while True:
+            u = yield from self.fetch(kc)
+            kc += 1
+            if u < 0:
+                return
+            if self.items[u] == 0:
+                continue
+            yield ("wait", self.kv_full, nkv)
+            nkv += 1
+            for _ in range(self.items[u]):
+                if g > 0:
+                    yield ("wait", self.p_full, g - 1)
+                yield ("wait", self.q_full[g % NQ], g // NQ)
+                if g > 0 and self.plant != "s1_ungated":
+                    yield ("wait", self.pt_free, g - 1)
+                if self.pt_free.completed < g:
+                    raise ProtocolError("S_1(%d) written over W that dV still reads" % g)
+                self.commit("S", self.s_full)
+                if g > 0:
+                    yield ("wait", self.ds_full, g - 1)
+                self.commit("S", self.dp_full)
+                g += 1
+            self.commit("S", self.kv_empty)
+
+    def dvdk_issuer(self):
+        kc = g = 0
+        while True:
+            u = yield from self.fetch(kc)
+            kc += 1
+            if u < 0:
+                return
+            if self.items[u] == 0:
+                continue
+            for _ in range(self.items[u]):
+                yield ("wait", self.p_full, g)
+                yield ("wait", self.q_full[g % NQ], g // NQ)
+                self.commit("D", self.pt_free)
+                yield ("wait", self.ds_full, g)
+                self.commit("D", self.dsm_free)
+                self.commit("D", self.q_empty[g % NQ])
+                g += 1
+            self.commit("D", self.dkv_full)
+
+    def dq_issuer(self):
+        kc = g = nkv = 0
+        while True:
+            u = yield from self.fetch(kc)
+            kc += 1
+            if u < 0:
+                return
+            if self.items[u] == 0:
+                continue
+            if self.items[u] % 2:                 # some items end inside a tile: K is cleaned first
+                yield ("wait", self.kv_full, nkv)
+            nkv += 1
+            for _ in range(self.items[u]):
+                yield ("wait", self.ds_full, g)
+                if g > 0:
+                    yield ("wait", self.dq_free, g - 1)
+                self.commit("Q", self.dq_full)
+                self.commit("Q", self.dsm_free)
+                g += 1
+            self.commit("Q", self.kv_empty)
+
+    def compute(self):
+        t = nit = kc = 0
+
+        def drain(r):
+            yield ("wait", self.dq_full, r)
+            self.dq_free.arrive()
+            if r >= 1:
+                yield ("wait", self.stg_free, r - 1)
+            self.stg_full.arrive()
+
+        while True:
+            u = yield from self.fetch(kc)
+            kc += 1
+            if u < 0:
+                break
+            if self.items[u] == 0:
+                continue
+            for _ in range(self.items[u]):
+                yield ("wait", self.s_full, t)
+                yield ("wait", self.q_full[t % NQ], t // NQ)
+                yield ("wait", self.dp_full, t)
+                self.p_full.arrive()
+                if t >= 1:
+                    yield ("wait", self.dsm_free, t - 1)
+                self.ds_full.arrive()
+                if t > 0:
+                    yield from drain(t - 1)
+                t += 1
+            yield ("wait", self.dkv_full, nit)
+            nit += 1
+        if t > 0:
+            yield from drain(t - 1)
+
+    def run(self):
+        self.engine.run({"P": self.producer(), "S": self.s_issuer(), "D": self.dvdk_issuer(), "Q": self.dq_issuer(),
+                         "C": self.compute()})
+
+
+def _items(rng):
+    return [rng.choice([0, 1, 2, 2, 3, 4, 5, 8, 16]) for _ in range(rng.randrange(1, 14))]
+
+
+def test_backward_protocol():
+    rng = random.Random(20261)
+    for trial in range(400):
+        Backward(_items(rng), random.Random(rng.random())).run()
+    for items in ([1], [0], [0, 0, 1], [1, 0, 1, 0], [8], [1] * 12, [2] * 9, [0] * 5 + [2]):
+        for seed in range(20):
+            Backward(items, random.Random(seed)).run()
+
+
+@pytest.mark.parametrize("plant", ["s1_ungated", "lag_too_short"])
+def test_backward_planted_mistakes_are_caught(plant):
+    rng = random.Random(8)
+    for trial in range(300):
+        try:
+            Backward(_items(rng), random.Random(rng.random()), plant=plant).run()
+        except ProtocolError:
+            return
+    pytest.fail("not caught")
