@@ -24,7 +24,8 @@ EXPORTED = ["fa_fwd_workspace_size", "fa_bwd_workspace_size", "fa_fwd", "fa_bwd"
             "fa_noalloc_check_status", "fa_noalloc_scratch",
             "fa_check_status", "fa_dropout_mask", "fa_selftest_wait_timeout", "fa_status_string", "fa_version",
             "fa_fp8_buffer_layout", "fa_fp8_quantize", "fa_fwd_fp8", "fa_rope", "fa_rope_frequencies",
-            "fa_diff_fwd_workspace_size", "fa_diff_bwd_workspace_size", "fa_diff_fwd", "fa_diff_bwd"]
+            "fa_diff_fwd_workspace_size", "fa_diff_bwd_workspace_size", "fa_diff_fwd", "fa_diff_bwd",
+            "fa_prefix_workspace_size", "fa_prefix_fwd"]
 
 
 class fa_params(ctypes.Structure):

@@ -1,5 +1,6 @@
 """ctypes binding of the operators around the attention passes (include/fa.h,
-ABI 1.4): rotary positions.
+ABI 1.4): rotary positions, differential attention, attention over a shared
+prefix.
 
 As in ``_lib``: argument checks, output and workspace allocation with torch,
 raw pointers and the stream; the computation runs in ``libfa_gb300.so``.
@@ -338,3 +339,76 @@ def diff_bwd(q, k, v, lam, o, o2, do, lse, *, causal=False, seqlens_k=None, wind
         raise FAError(st, "fa_diff_bwd")
     diff_bwd.last_workspace = ws
     return dq, dk, dv, dlam
+
+
+class fa_prefix_params(ctypes.Structure):
+    _fields_ = ([(n, _i32) for n in ("B", "H", "H_kv", "T", "P", "M", "d", "dtype")] +
+                [("scale", _f32), ("seqlens_k", _vp)] +
+                [("%s_stride_%s" % (t, x), _i64) for t in ("q", "o", "k", "v") for x in "bhn"] +
+                [("%s_stride_%s" % (t, x), _i64) for t in ("kp", "vp") for x in "hn"])
+
+
+def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, out=None, workspace=None, stream=None):
+    """Attention of B sequences that share a prefix (fa_prefix_fwd): (o, lse).
+
+    q [B,H,T,d] holds the T new tokens of each sequence (T = 1: one decoding
+    step), k_prefix and v_prefix [H_kv,P,d] the one shared prefix, k and v
+    [B,H_kv,M,d] the sequences' own caches with ``seqlens_k`` [B] rows
+    filled, the new tokens' included.  Query t sees the whole prefix and the
+    own keys j <= seqlens_k[b] - T + t.  P = 0 is plain cached attention;
+    k_prefix, v_prefix (or k, v) may then be None.  o [B,H,T,d], lse float32
+    [B,H,T].  ``out`` = (o, lse)."""
+    _check4(q, "q")
+    B, H, T, d = q.shape
+    dev = q.device
+    if (k is None) != (v is None) or (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k and v, and k_prefix and v_prefix, come together")
+    if k is None and k_prefix is None:
+        raise ValueError("neither a prefix nor caches given")
+    p = fa_prefix_params()
+    p.B, p.H, p.T, p.d, p.dtype = B, H, T, d, DTYPE_CODE[q.dtype]
+    p.H_kv = k.shape[1] if k is not None else k_prefix.shape[0]
+    p.scale = 0.0 if scale is None else float(scale)
+    if p.H_kv < 1 or H % p.H_kv:
+        raise ValueError("the number of query heads must be a multiple of the number of K/V heads")
+    if k is not None:
+        p.M = k.shape[2]
+        for t, n in ((k, "k"), (v, "v")):
+            _check4(t, n, dev, q.dtype)
+            if tuple(t.shape) != (B, p.H_kv, p.M, d):
+                raise ValueError("k, v must be [B, H_kv, M, d] with the B, d of q")
+            _set_strides(p, n, t)
+    if k_prefix is not None:
+        p.P = k_prefix.shape[1]
+        for t, n in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix")):
+            if t.dim() != 3 or tuple(t.shape) != (p.H_kv, p.P, d):
+                raise ValueError("k_prefix, v_prefix must be [H_kv, P, d]")
+            _check4(t[None], n, dev, q.dtype)
+        p.kp_stride_h, p.kp_stride_n = k_prefix.stride()[:2]
+        p.vp_stride_h, p.vp_stride_n = v_prefix.stride()[:2]
+    _set_strides(p, "q", q)
+    with _on(dev, stream) as raw:
+        lens = _lens(seqlens_k, B, dev)
+        if lens is None:
+            raise ValueError("seqlens_k must be given")
+        p.seqlens_k = lens.data_ptr()
+        if out is None:
+            o = torch.empty((B, H, T, d), device=dev, dtype=q.dtype)
+            lse = torch.empty((B, H, T), device=dev, dtype=torch.float32)
+        else:
+            o, lse = out
+            _check_out(o, q, "o")
+            _check_place(lse, "out lse", dev, torch.float32)
+            if tuple(lse.shape) != (B, H, T) or not lse.is_contiguous():
+                raise ValueError("out lse must be contiguous with shape %s" % ((B, H, T),))
+        _set_strides(p, "o", o)
+        a = ctypes.addressof(p)
+        size = _fn("fa_prefix_workspace_size", _vp, restype=ctypes.c_size_t)(a)
+        ws = _need_workspace(workspace, size, dev)
+        f = _fn("fa_prefix_fwd", *([_vp] * 9), ctypes.c_size_t, _vp)
+        st = f(a, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), o.data_ptr(), lse.data_ptr(),
+               ws.data_ptr(), ws.numel(), raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_prefix_fwd")
+    prefix_fwd.last_workspace = ws
+    return o, lse

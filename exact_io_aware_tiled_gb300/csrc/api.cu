@@ -5,6 +5,7 @@
 // driver-entry-point query so the library needs no -lcuda), and enqueues the
 // kernels on the caller's stream.  It never allocates, frees or synchronises
 // device memory (fa_check_status excepted) and keeps no mutable global state.
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -337,6 +338,47 @@ fa_status diff_map(CUtensorMap* m, const void* base, const fa_diff_params* p, in
   q.N = p->N;
   return make_map(m, base, p->dtype == FA_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   2, cols, 64, &q, heads, s, rows);
+}
+
+// ---- attention over a shared prefix -------------------------------------------
+struct PrefixStrides { Strides q, o, kp, vp, k, v; };
+
+// One tensor of nb x nh x n rows of d columns (see diff_strides).
+fa_status row_strides(Strides& s, int nb, int nh, int n, int d) {
+  if (n <= 1) s.n = d;
+  if (nh <= 1) s.h = (int64_t)std::max(n, 1) * s.n;
+  if (nb <= 1) s.b = (int64_t)std::max(nh, 1) * s.h;
+  if (s.n < d || s.h < 1 || s.b < 1) return FA_ERR_INVALID_ARG;
+  if (s.n % 8 || s.h % 8 || s.b % 8) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+// The problem with H_kv filled in, its strides normalised.
+fa_status check_prefix(const fa_prefix_params* in, fa_prefix_params& p, PrefixStrides& s) {
+  if (in == nullptr) return FA_ERR_INVALID_ARG;
+  p = *in;
+  if (p.B < 1 || p.H < 1 || p.T < 1 || p.d < 1 || p.H_kv < 0 || p.P < 0 || p.M < 0) return FA_ERR_INVALID_ARG;
+  if (p.dtype != FA_DT_F32 && p.dtype != FA_DT_F16 && p.dtype != FA_DT_BF16) return FA_ERR_INVALID_ARG;
+  if ((p.d != 64 && p.d != 128) || p.dtype == FA_DT_F32) return FA_ERR_UNSUPPORTED;
+  if (p.H_kv == 0) p.H_kv = p.H;
+  if (p.H % p.H_kv != 0) return FA_ERR_INVALID_ARG;
+  if ((double)p.B * p.H * p.T >= (double)(1 << 26) || p.P > (1 << 28) || p.M > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  s.q = {p.q_stride_b, p.q_stride_h, p.q_stride_n};
+  s.o = {p.o_stride_b, p.o_stride_h, p.o_stride_n};
+  s.k = {p.k_stride_b, p.k_stride_h, p.k_stride_n};
+  s.v = {p.v_stride_b, p.v_stride_h, p.v_stride_n};
+  s.kp = {0, p.kp_stride_h, p.kp_stride_n};
+  s.vp = {0, p.vp_stride_h, p.vp_stride_n};
+  fa_status e;
+  if ((e = row_strides(s.q, p.B, p.H, p.T, p.d)) != FA_OK || (e = row_strides(s.o, p.B, p.H, p.T, p.d)) != FA_OK)
+    return e;
+  if (p.M > 0 && ((e = row_strides(s.k, p.B, p.H_kv, p.M, p.d)) != FA_OK ||
+                  (e = row_strides(s.v, p.B, p.H_kv, p.M, p.d)) != FA_OK))
+    return e;
+  if (p.P > 0 && ((e = row_strides(s.kp, 1, p.H_kv, p.P, p.d)) != FA_OK ||
+                  (e = row_strides(s.vp, 1, p.H_kv, p.P, p.d)) != FA_OK))
+    return e;
+  return FA_OK;
 }
 
 }  // namespace
@@ -686,6 +728,46 @@ fa_status fa_diff_bwd(const fa_diff_params* p, const void* q, const void* k, con
   if (e == cudaSuccess) e = launch_dq_convert(p->dtype, dqacc, dq, sd.q, p->B, 2 * p->H, p->N, 64, st);
   if (e == cudaSuccess) e = launch_diff_dlam(a.dlam_part, dlam, p->B, p->H, a.group, L.nq, st);
   return cuda_status(e);
+}
+
+size_t fa_prefix_workspace_size(const fa_prefix_params* in) {
+  fa_prefix_params p;
+  PrefixStrides sd;
+  if (check_prefix(in, p, sd) != FA_OK) return 256;
+  return prefix_workspace(&p);
+}
+
+fa_status fa_prefix_fwd(const fa_prefix_params* in, const void* q, const void* k_prefix, const void* v_prefix,
+                        const void* k, const void* v, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  fa_prefix_params p;
+  PrefixStrides sd;
+  fa_status s = check_prefix(in, p, sd);
+  if (s != FA_OK) return s;
+  if (!q || !o || !lse || p.seqlens_k == nullptr) return FA_ERR_INVALID_ARG;
+  if ((p.P > 0 && (!k_prefix || !v_prefix)) || (p.M > 0 && (!k || !v))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(p.seqlens_k) & 3u))
+    return FA_ERR_MISALIGNED;
+  if ((p.P > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix))) || (p.M > 0 && (!aligned16(k) || !aligned16(v))))
+    return FA_ERR_MISALIGNED;
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < prefix_workspace(&p)) return FA_ERR_WORKSPACE;
+  CUtensorMap m[4] = {};
+  const CUtensorMapDataType dt =
+      p.dtype == FA_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  fa_params bn{};
+  bn.B = 1;
+  bn.N = p.P;
+  if (p.P > 0 && ((s = make_map(&m[0], k_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.kp, 64)) != FA_OK ||
+                  (s = make_map(&m[1], v_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.vp, 64)) != FA_OK))
+    return s;
+  bn.B = p.B;
+  bn.N = p.M;
+  if (p.M > 0 && ((s = make_map(&m[2], k, dt, 2, p.d, 64, &bn, p.H_kv, sd.k, 64)) != FA_OK ||
+                  (s = make_map(&m[3], v, dt, 2, p.d, 64, &bn, p.H_kv, sd.v, 64)) != FA_OK))
+    return s;
+  const float scale = (p.scale > 0.f && std::isfinite(p.scale)) ? p.scale : 1.f / std::sqrt((float)p.d);
+  return cuda_status(launch_prefix(&p, m, q, sd.q, o, sd.o, lse, scale * 1.4426950408889634f,
+                                   static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char* fa_status_string(fa_status s) {

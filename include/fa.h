@@ -436,6 +436,48 @@ fa_status fa_diff_bwd(const fa_diff_params *p, const void *q, const void *k, con
                       const void *o2, const void *dout, const float *lse, void *dq, void *dk, void *dv, float *dlam,
                       void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over a shared prefix (ABI 1.4): B sequences that continue one
+ * prefix, T new tokens of each (T = 1: one decoding step).
+ *   - q, o: [B,H,T,d]; k_prefix, v_prefix: [H_kv,P,d], one copy for the batch;
+ *     k, v: [B,H_kv,M,d], each sequence's own cache, of which the first
+ *     L_b = seqlens_k[b] rows are filled, the T new tokens' rows among them
+ *     (L_b is taken into [0, M]).  lse: contiguous float32 [B,H,T], natural log.
+ *   - Query t of sequence b sees every prefix key and its own keys
+ *     j <= L_b - T + t.  A query that sees no key has O = 0 and lse -inf.
+ *     Query head h reads K/V head h / (H / H_kv); H_kv = 0 selects H.
+ *   - P = 0 (plain cached attention) and M = 0 (only the prefix) are allowed;
+ *     the pointers of an empty part may be NULL.
+ *   - Cache rows at or past L_b may hold anything, NaN included, and are
+ *     not written.
+ *   - float16, bfloat16; d = 64 or 128.  Weights are rounded to the dtype
+ *     before the product with V; sums, statistics and joins are float32.
+ *   - Results repeat bit for bit; they do not depend on what else runs.
+ *   - B*H*T < 2^26, P and M <= 2^28.  16-byte rule for bases and strides (a
+ *     dimension of one element may have any stride); offsets are 64-bit.
+ * The prefix is read once per K/V head for up to 64 query rows together
+ * (B * H / H_kv * T of them), not once per sequence.  Workspace:
+ * fa_prefix_workspace_size bytes, 16-byte aligned, nothing persists in it;
+ * status word at its start, read by fa_check_status.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, H, H_kv, T;
+  int32_t P, M;              /* prefix keys; rows of each own cache             */
+  int32_t d, dtype;
+  float scale;               /* tau; <= 0 selects 1/sqrt(d)                     */
+  const int32_t *seqlens_k;  /* device [B]                                      */
+  int64_t q_stride_b, q_stride_h, q_stride_n;
+  int64_t o_stride_b, o_stride_h, o_stride_n;
+  int64_t k_stride_b, k_stride_h, k_stride_n;
+  int64_t v_stride_b, v_stride_h, v_stride_n;
+  int64_t kp_stride_h, kp_stride_n;
+  int64_t vp_stride_h, vp_stride_n;
+} fa_prefix_params;
+
+size_t fa_prefix_workspace_size(const fa_prefix_params *p);
+fa_status fa_prefix_fwd(const fa_prefix_params *p, const void *q, const void *k_prefix, const void *v_prefix,
+                        const void *k, const void *v, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fa_status_string(fa_status s);
 
