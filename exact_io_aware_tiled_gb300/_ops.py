@@ -44,6 +44,20 @@ def _fn(name, *argtypes, restype=ctypes.c_int):
     return f
 
 
+def _ptrs(name, n):
+    """A function of n pointers (the stream among them) that returns a status."""
+    return _typed.get(name) or _fn(name, *([_vp] * n))
+
+
+def _sized(name, n):
+    """A function of n pointers, a workspace's size and the stream that returns a status."""
+    return _typed.get(name) or _fn(name, *([_vp] * n), ctypes.c_size_t, _vp)
+
+
+def _size_of(name):
+    return _typed.get(name) or _fn(name, _vp, restype=ctypes.c_size_t)
+
+
 @contextlib.contextmanager
 def _entered(device, stream):
     with torch.cuda.device(device):
@@ -56,12 +70,13 @@ def _entered(device, stream):
 
 class _Plain:
     """_entered for the usual case (the tensors' device is current, no stream given), without its cost."""
+    __slots__ = ("index",)
 
-    def __init__(self, device):
-        self.device = device
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         return False
@@ -75,18 +90,31 @@ def _on(device, stream):
         return _entered(device, stream)
     if torch.cuda.current_device() != device.index:
         return _entered(device, None)
-    return _Plain(device)
+    return _Plain(device.index)
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
-def _check4(t, name, device=None, dtype=None):
+def _rows(t, name, like, shape):
+    """Strides of a [.,.,.,d] tensor of `shape` on the device and in the dtype of the CUDA tensor `like`."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not like.dtype or t.get_device() != like.get_device() or \
+            (st[-1] != 1 and shape[-1] > 1):
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        _check_place(t, name, like.device, like.dtype)
+        raise ValueError("%s: the last dimension must be contiguous (stride 1), got strides %s" % (name, st))
+    return st
+
+
+def _check4(t, name):
+    """The call's first tensor: 4 dimensions, on a GPU, a dtype of the library, contiguous rows."""
     if t.dim() != 4:
         raise ValueError("%s must have 4 dimensions, got shape %s" % (name, tuple(t.shape)))
-    _check_place(t, name, device, dtype)
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    _check_place(t, name)
+    if t.stride(3) != 1 and t.shape[3] > 1:
         raise ValueError("%s: the last dimension must be contiguous (stride 1), got strides %s" % (name, t.stride()))
 
 
@@ -102,10 +130,9 @@ def _check_place(t, name, device=None, dtype=None):
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
 
-def _check_out(t, like, name):
-    if t.shape != like.shape:
-        raise ValueError("out %s must have shape %s, got %s" % (name, tuple(like.shape), tuple(t.shape)))
-    _check4(t, "out " + name, like.device, like.dtype)
+def _flat_f32(t, name, device, shape):
+    if tuple(t.shape) != shape or t.dtype is not torch.float32 or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of shape %s on %s" % (name, shape, device))
 
 
 def rope_frequencies(rot, *, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0,
@@ -145,47 +172,40 @@ def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleave
     (q_out, k_out), or q_out without k, may be the inputs themselves."""
     _check4(q, "q")
     B, H, N, d = q.shape
+    Hkv, ks = 0, (0, 0, 0)
     if k is not None:
-        _check4(k, "k", q.device, q.dtype)
-        if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
-            raise ValueError("k must be [B, H_kv, N, d] with the B, N, d of q")
-    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or inv_freq.device != q.device or \
+        if k.dim() != 4:
+            raise ValueError("k must be [B, H_kv, N, d]")
+        Hkv = k.shape[1]
+        ks = _rows(k, "k", q, (B, Hkv, N, d))[:3]
+    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or \
             not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor [rot/2] on q's device")
+    pos, wide, pos_b, pos_n = None, 0, 0, 0
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device:
+        wide = positions.dtype is torch.int64
+        if not (wide or positions.dtype is torch.int32) or positions.get_device() != q.get_device():
             raise ValueError("positions must be an int32 or int64 tensor on q's device")
-        if positions.dim() == 1:
-            positions = positions[None]
-        if positions.dim() != 2 or positions.shape[1] != N or positions.shape[0] not in (1, B):
+        ps = positions.shape
+        if not (ps == (N,) or ps == (B, N) or ps == (1, N)):
             raise ValueError("positions must have shape [N], [1, N] or [B, N]")
-    p = fa_rope_params()
-    p.B, p.H, p.N, p.d, p.rot = B, H, N, d, 2 * inv_freq.shape[0]
-    p.H_kv = 0 if k is None else k.shape[1]
-    p.dtype = DTYPE_CODE[q.dtype]
-    p.interleaved, p.backward = bool(interleaved), bool(backward)
-    p.mscale, p.start = float(mscale), int(start)
-    p.inv_freq = inv_freq.data_ptr()
-    if positions is not None:
-        p.positions, p.positions_i64 = positions.data_ptr(), positions.dtype == torch.int64
-        p.pos_stride_b = positions.stride(0) if positions.shape[0] > 1 else 0
-        p.pos_stride_n = positions.stride(1)
+        pos, pos_n = positions.data_ptr(), positions.stride(-1)
+        if len(ps) == 2 and ps[0] > 1:
+            pos_b = positions.stride(0)
     with _on(q.device, stream) as raw:
         if out is None:
             qo = torch.empty_like(q)
             ko = None if k is None else torch.empty_like(k)
+            qos, kos = qo.stride()[:3], ks if k is None else ko.stride()[:3]
         else:
             qo, ko = (out, None) if k is None else out
-            _check_out(qo, q, "q")
-            if k is not None:
-                _check_out(ko, k, "k")
-        p.q_stride_b, p.q_stride_h, p.q_stride_n = q.stride()[:3]
-        p.q_out_stride_b, p.q_out_stride_h, p.q_out_stride_n = qo.stride()[:3]
-        if k is not None:
-            p.k_stride_b, p.k_stride_h, p.k_stride_n = k.stride()[:3]
-            p.k_out_stride_b, p.k_out_stride_h, p.k_out_stride_n = ko.stride()[:3]
-        f = _fn("fa_rope", _vp, _vp, _vp, _vp, _vp, _vp)
-        st = f(ctypes.addressof(p), _ptr(q), _ptr(k), _ptr(qo), _ptr(ko), raw)
+            qos = _rows(qo, "out q", q, q.shape)[:3]
+            kos = ks if k is None else _rows(ko, "out k", q, k.shape)[:3]
+        p = fa_rope_params(B, H, Hkv, N, d, 2 * inv_freq.shape[0], DTYPE_CODE[q.dtype], bool(interleaved),
+                           bool(backward), wide, *q.stride()[:3], *ks, *qos, *kos, pos, pos_b, pos_n, int(start),
+                           inv_freq.data_ptr(), float(mscale))
+        st = _ptrs("fa_rope", 6)(ctypes.addressof(p), q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(),
+                                 None if k is None else ko.data_ptr(), raw)
     if st != FA_OK:
         raise FAError(st, "fa_rope")
     return qo if k is None else (qo, ko)
@@ -197,19 +217,14 @@ class fa_diff_params(ctypes.Structure):
                 [("%s_stride_%s" % (t, x), _i64) for t in ("q", "k", "v", "o", "do") for x in "bhn"])
 
 
-def _set_strides(p, name, t):
-    s = t.stride()
-    setattr(p, name + "_stride_b", s[0])
-    setattr(p, name + "_stride_h", s[1])
-    setattr(p, name + "_stride_n", s[2])
-
-
 def _lens(seqlens, B, device, name="seqlens_k"):
     """int32 [B] lengths on `device` (converted on the current stream where they are something else)."""
     if seqlens is None:
         return None
-    if tuple(seqlens.shape) != (B,):
+    if seqlens.shape != (B,):
         raise ValueError("%s must have shape [B] = [%d]" % (name, B))
+    if seqlens.dtype is torch.int32 and seqlens.device == device and seqlens.is_contiguous():
+        return seqlens
     if seqlens.dtype.is_floating_point or seqlens.dtype == torch.bool:
         raise ValueError("%s must hold whole numbers" % name)
     return seqlens.to(device=device, dtype=torch.int32).contiguous()
@@ -224,28 +239,25 @@ def _need_workspace(workspace, size, device):
     return workspace
 
 
-def _diff_params(q, k, v, lam, causal, window, scale):
+def _diff_args(q, k, v, lam, causal, window, scale, lens, os, dos):
+    """fa_diff_params of checked tensors; os, dos: strides of o (and o2) and of dO."""
+    return fa_diff_params(q.shape[0], q.shape[1] // 2, v.shape[1], q.shape[2], 64, DTYPE_CODE[q.dtype], bool(causal),
+                          int(window), 0.0 if scale is None else float(scale),
+                          None if lens is None else lens.data_ptr(), lam.data_ptr(), *q.stride()[:3], *k.stride()[:3],
+                          *v.stride()[:3], *os[:3], *dos[:3])
+
+
+def _check_diff(q, k, v, lam):
     _check4(q, "q")
-    if q.shape[3] != 64 or q.shape[1] % 2:
-        raise ValueError("q must be [B, 2H, N, 64] (the two maps of head pair h in heads 2h, 2h + 1)")
-    _check4(k, "k", q.device, q.dtype)
-    _check4(v, "v", q.device, q.dtype)
     B, H2, N, d = q.shape
-    H, Hkv = H2 // 2, v.shape[1]
-    if tuple(k.shape) != (B, 2 * Hkv, N, d) or tuple(v.shape) != (B, Hkv, N, 2 * d):
-        raise ValueError("k must be [B, 2 H_kv, N, 64] and v [B, H_kv, N, 128] with the B, N of q")
-    if Hkv < 1 or H % Hkv:
-        raise ValueError("the number of query head pairs must be a multiple of the number of K/V pairs")
-    if tuple(lam.shape) != (H,) or lam.dtype != torch.float32 or lam.device != q.device or not lam.is_contiguous():
-        raise ValueError("lam must be a contiguous float32 tensor [H] on q's device")
-    p = fa_diff_params()
-    p.B, p.H, p.H_kv, p.N, p.d, p.dtype = B, H, Hkv, N, d, DTYPE_CODE[q.dtype]
-    p.causal, p.window = bool(causal), int(window)
-    p.scale = 0.0 if scale is None else float(scale)
-    p.lam = lam.data_ptr()
-    for n, t in (("q", q), ("k", k), ("v", v)):
-        _set_strides(p, n, t)
-    return p
+    if d != 64 or H2 % 2 or v.dim() != 4 or v.shape[1] < 1 or (H2 // 2) % v.shape[1]:
+        raise ValueError("q must be [B, 2H, N, 64] (the two maps of head pair h in heads 2h, 2h + 1), k [B, 2 H_kv, N, "
+                         "64] and v [B, H_kv, N, 128], H a multiple of H_kv; got q %s, v %s" %
+                         (tuple(q.shape), tuple(v.shape)))
+    _rows(k, "k", q, (B, 2 * v.shape[1], N, 64))
+    _rows(v, "v", q, (B, v.shape[1], N, 128))
+    _flat_f32(lam, "lam", q.device, (H2 // 2,))
+    return B, H2 // 2, N
 
 
 def diff_fwd(q, k, v, lam, *, causal=False, seqlens_k=None, window=0, scale=None, need_o2=True, out=None,
@@ -259,35 +271,29 @@ def diff_fwd(q, k, v, lam, *, causal=False, seqlens_k=None, window=0, scale=None
     :func:`diff_bwd` needs besides; ``need_o2=False`` leaves it out (None).
     ``out`` = (o, lse, o2), o2 None where it is not needed; o and o2 share
     their strides."""
-    p = _diff_params(q, k, v, lam, causal, window, scale)
-    B, H, N, dv = p.B, p.H, p.N, 2 * p.d
-    with _on(q.device, stream) as raw:
-        lens = _lens(seqlens_k, B, q.device)
-        p.seqlens_k = _ptr(lens)
+    B, H, N = _check_diff(q, k, v, lam)
+    dev = q.device
+    with _on(dev, stream) as raw:
+        lens = _lens(seqlens_k, B, dev)
         if out is None:
-            o = torch.empty((B, H, N, dv), device=q.device, dtype=q.dtype)
+            o = torch.empty((B, H, N, 128), device=dev, dtype=q.dtype)
             o2 = torch.empty_like(o) if need_o2 else None
-            lse = torch.empty((B, 2 * H, N), device=q.device, dtype=torch.float32)
+            lse = torch.empty((B, 2 * H, N), device=dev, dtype=torch.float32)
+            os = o.stride()
         else:
             o, lse, o2 = out
-            for t, n in ((o, "o"), (o2, "o2")):
-                if t is None and n == "o2" and not need_o2:
-                    continue
-                if t is None or tuple(t.shape) != (B, H, N, dv):
-                    raise ValueError("out %s must have shape %s" % (n, (B, H, N, dv)))
-                _check4(t, "out " + n, q.device, q.dtype)
-            if o2 is not None and o2.stride() != o.stride():
+            os = _rows(o, "out o", q, (B, H, N, 128))
+            if o2 is None and need_o2:
+                raise ValueError("out o2 is missing (need_o2=False leaves it out)")
+            if o2 is not None and _rows(o2, "out o2", q, (B, H, N, 128)) != os:
                 raise ValueError("out o and o2 must share their strides")
-            _check_place(lse, "out lse", q.device, torch.float32)
-            if tuple(lse.shape) != (B, 2 * H, N) or not lse.is_contiguous():
-                raise ValueError("out lse must be contiguous with shape %s" % ((B, 2 * H, N),))
-        _set_strides(p, "o", o)
+            _flat_f32(lse, "out lse", dev, (B, 2 * H, N))
+        p = _diff_args(q, k, v, lam, causal, window, scale, lens, os, (0, 0, 0))
         a = ctypes.addressof(p)
-        size = _fn("fa_diff_fwd_workspace_size", _vp, restype=ctypes.c_size_t)(a)
-        ws = _need_workspace(workspace, size, q.device)
-        f = _fn("fa_diff_fwd", *([_vp] * 8), ctypes.c_size_t, _vp)
-        st = f(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(o2), lse.data_ptr(), ws.data_ptr(),
-               ws.numel(), raw)
+        ws = _need_workspace(workspace, _size_of("fa_diff_fwd_workspace_size")(a), dev)
+        st = _sized("fa_diff_fwd", 8)(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                      None if o2 is None else o2.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                      raw)
     if st != FA_OK:
         raise FAError(st, "fa_diff_fwd")
     diff_fwd.last_workspace = ws
@@ -300,41 +306,30 @@ def diff_bwd(q, k, v, lam, o, o2, do, lse, *, causal=False, seqlens_k=None, wind
     gradient ``do`` [B,H,N,128]; o, o2, lse and the masks are the forward
     call's.  dq, dk, dv have the shapes and strides of q, k, v; dlam is
     float32 [H].  ``out`` = (dq, dk, dv, dlam)."""
-    p = _diff_params(q, k, v, lam, causal, window, scale)
-    B, H, N, dv_ = p.B, p.H, p.N, 2 * p.d
-    for t, n in ((o, "o"), (o2, "o2"), (do, "do")):
-        _check4(t, n, q.device, q.dtype)
-        if tuple(t.shape) != (B, H, N, dv_):
-            raise ValueError("%s must have shape %s" % (n, (B, H, N, dv_)))
-    if o.stride() != o2.stride():
+    B, H, N = _check_diff(q, k, v, lam)
+    dev = q.device
+    os = _rows(o, "o", q, (B, H, N, 128))
+    if _rows(o2, "o2", q, (B, H, N, 128)) != os:
         raise ValueError("o and o2 must share their strides")
-    _check_place(lse, "lse", q.device, torch.float32)
-    if tuple(lse.shape) != (B, 2 * H, N) or not lse.is_contiguous():
-        raise ValueError("lse must be the contiguous [B, 2H, N] float32 tensor diff_fwd returns")
-    _set_strides(p, "o", o)
-    _set_strides(p, "do", do)
-    with _on(q.device, stream) as raw:
-        lens = _lens(seqlens_k, B, q.device)
-        p.seqlens_k = _ptr(lens)
-        likes = (q, k, v)
+    dos = _rows(do, "do", q, (B, H, N, 128))
+    _flat_f32(lse, "lse", dev, (B, 2 * H, N))
+    with _on(dev, stream) as raw:
+        lens = _lens(seqlens_k, B, dev)
         if out is None:
-            dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), device=t.device, dtype=t.dtype) for t in likes)
-            dlam = torch.empty((H,), device=q.device, dtype=torch.float32)
+            dq, dk, dv = (torch.empty_strided(t.shape, t.stride(), device=dev, dtype=t.dtype) for t in (q, k, v))
+            dlam = torch.empty((H,), device=dev, dtype=torch.float32)
         else:
             dq, dk, dv, dlam = out
-            _check_place(dlam, "out dlam", q.device, torch.float32)
-            if tuple(dlam.shape) != (H,) or not dlam.is_contiguous():
-                raise ValueError("out dlam must be contiguous with shape [H]")
-        for t, like, n in zip((dq, dk, dv), likes, ("dq", "dk", "dv")):
-            _check_out(t, like, n)
-            if t.stride() != like.stride():
-                raise ValueError("out %s must have the strides %s" % (n, like.stride()))
+            for t, like, n in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+                if _rows(t, "out " + n, q, like.shape) != like.stride():
+                    raise ValueError("out %s must have the strides %s" % (n, like.stride()))
+            _flat_f32(dlam, "out dlam", dev, (H,))
+        p = _diff_args(q, k, v, lam, causal, window, scale, lens, os, dos)
         a = ctypes.addressof(p)
-        size = _fn("fa_diff_bwd_workspace_size", _vp, restype=ctypes.c_size_t)(a)
-        ws = _need_workspace(workspace, size, q.device)
-        f = _fn("fa_diff_bwd", *([_vp] * 13), ctypes.c_size_t, _vp)
-        st = f(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), o2.data_ptr(), do.data_ptr(), lse.data_ptr(),
-               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlam.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+        ws = _need_workspace(workspace, _size_of("fa_diff_bwd_workspace_size")(a), dev)
+        st = _sized("fa_diff_bwd", 13)(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), o2.data_ptr(),
+                                       do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                       dlam.data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if st != FA_OK:
         raise FAError(st, "fa_diff_bwd")
     diff_bwd.last_workspace = ws
@@ -363,51 +358,42 @@ def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, out=None, 
     dev = q.device
     if (k is None) != (v is None) or (k_prefix is None) != (v_prefix is None):
         raise ValueError("k and v, and k_prefix and v_prefix, come together")
-    if k is None and k_prefix is None:
-        raise ValueError("neither a prefix nor caches given")
-    p = fa_prefix_params()
-    p.B, p.H, p.T, p.d, p.dtype = B, H, T, d, DTYPE_CODE[q.dtype]
-    p.H_kv = k.shape[1] if k is not None else k_prefix.shape[0]
-    p.scale = 0.0 if scale is None else float(scale)
-    if p.H_kv < 1 or H % p.H_kv:
-        raise ValueError("the number of query heads must be a multiple of the number of K/V heads")
+    P = M = 0
+    ks = vs = kps = vps = (0, 0, 0)
     if k is not None:
-        p.M = k.shape[2]
-        for t, n in ((k, "k"), (v, "v")):
-            _check4(t, n, dev, q.dtype)
-            if tuple(t.shape) != (B, p.H_kv, p.M, d):
-                raise ValueError("k, v must be [B, H_kv, M, d] with the B, d of q")
-            _set_strides(p, n, t)
+        if k.dim() != 4:
+            raise ValueError("k, v must be [B, H_kv, M, d]")
+        Hkv, M = k.shape[1], k.shape[2]
+        ks, vs = _rows(k, "k", q, (B, Hkv, M, d)), _rows(v, "v", q, (B, Hkv, M, d))
+    elif k_prefix is not None:
+        Hkv = k_prefix.shape[0]
+    else:
+        raise ValueError("neither a prefix nor caches given")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("the number of query heads must be a multiple of the number of K/V heads")
     if k_prefix is not None:
-        p.P = k_prefix.shape[1]
-        for t, n in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix")):
-            if t.dim() != 3 or tuple(t.shape) != (p.H_kv, p.P, d):
-                raise ValueError("k_prefix, v_prefix must be [H_kv, P, d]")
-            _check4(t[None], n, dev, q.dtype)
-        p.kp_stride_h, p.kp_stride_n = k_prefix.stride()[:2]
-        p.vp_stride_h, p.vp_stride_n = v_prefix.stride()[:2]
-    _set_strides(p, "q", q)
+        if k_prefix.dim() != 3:
+            raise ValueError("k_prefix, v_prefix must be [H_kv, P, d]")
+        P = k_prefix.shape[1]
+        kps, vps = _rows(k_prefix, "k_prefix", q, (Hkv, P, d)), _rows(v_prefix, "v_prefix", q, (Hkv, P, d))
+    if seqlens_k is None:
+        raise ValueError("seqlens_k must be given")
     with _on(dev, stream) as raw:
         lens = _lens(seqlens_k, B, dev)
-        if lens is None:
-            raise ValueError("seqlens_k must be given")
-        p.seqlens_k = lens.data_ptr()
         if out is None:
             o = torch.empty((B, H, T, d), device=dev, dtype=q.dtype)
             lse = torch.empty((B, H, T), device=dev, dtype=torch.float32)
+            os = o.stride()
         else:
             o, lse = out
-            _check_out(o, q, "o")
-            _check_place(lse, "out lse", dev, torch.float32)
-            if tuple(lse.shape) != (B, H, T) or not lse.is_contiguous():
-                raise ValueError("out lse must be contiguous with shape %s" % ((B, H, T),))
-        _set_strides(p, "o", o)
+            os = _rows(o, "out o", q, q.shape)
+            _flat_f32(lse, "out lse", dev, (B, H, T))
+        p = fa_prefix_params(B, H, Hkv, T, P, M, d, DTYPE_CODE[q.dtype], 0.0 if scale is None else float(scale),
+                             lens.data_ptr(), *q.stride()[:3], *os[:3], *ks[:3], *vs[:3], *kps[:2], *vps[:2])
         a = ctypes.addressof(p)
-        size = _fn("fa_prefix_workspace_size", _vp, restype=ctypes.c_size_t)(a)
-        ws = _need_workspace(workspace, size, dev)
-        f = _fn("fa_prefix_fwd", *([_vp] * 9), ctypes.c_size_t, _vp)
-        st = f(a, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), o.data_ptr(), lse.data_ptr(),
-               ws.data_ptr(), ws.numel(), raw)
+        ws = _need_workspace(workspace, _size_of("fa_prefix_workspace_size")(a), dev)
+        st = _sized("fa_prefix_fwd", 9)(a, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), o.data_ptr(),
+                                        lse.data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if st != FA_OK:
         raise FAError(st, "fa_prefix_fwd")
     prefix_fwd.last_workspace = ws
