@@ -30,14 +30,13 @@
 // Keys behind seqlens_k[b] may hold anything, NaN included: their scores are
 // replaced, and their V rows are zeroed in shared memory before the product
 // (0 x NaN would not be 0).
-#include "common.cuh"
+#include "row_softmax.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kThreads = 384;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 struct DCfg {
   static constexpr int NS = 3;                           // K / V stages
@@ -60,11 +59,6 @@ struct DBars {
   int abort;
 };
 static_assert(sizeof(DBars) <= 512, "barrier block overflows its shared-memory slot");
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  const bool ok = mbar_wait(bar, parity, ctl);
-  return __all_sync(0xffffffffu, ok);
-}
 
 template <typename T, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -245,91 +239,13 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int jmax = a.causal ? min(Lk - 1, i) : (Lk - 1);
     const int jmin = kWin ? i - a.window + 1 : 0;
 
-    float m_run = -INFINITY;
-    float l_true = 0.f, l_rnd = 0.f;
+    RowSoftmax w;
     bool ok = true;
     for (int s = 0; s < n; ++s) {
       const int kv = lo + s;
       if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)s & 1u, ctl))) break;
       tc_fence_after();
-      uint32_t sr[4][32];
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, sr[cc]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) reg_fence32(sr[cc]);
-
-      // mask (only boundary tiles) and row max of the raw scores
-      const int jl = jmax - kv * kTile;
-      const int jlo = jmin - kv * kTile;
-      if (jl < kTile - 1 || (kWin && jlo > 0)) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > jl || (kWin && c < jlo)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-      }
-      float m8[8];
-#pragma unroll
-      for (int t = 0; t < 8; ++t) m8[t] = __uint_as_float(sr[0][t]);
-#pragma unroll
-      for (int c = 8; c < 128; c += 16) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int c0 = c + t, c1 = c + 8 + t;
-          m8[t] = (c1 < 128) ? max3f(m8[t], __uint_as_float(sr[c0 >> 5][c0 & 31]), __uint_as_float(sr[c1 >> 5][c1 & 31]))
-                             : fmaxf(m8[t], __uint_as_float(sr[c0 >> 5][c0 & 31]));
-        }
-      }
-      float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-      mx *= sl2;
-      // running reference max: moved only when the tile max exceeds it by 2^8
-      float m_new = m_run;
-      if (mx > m_run + kRescaleThreshold) m_new = mx;
-      const bool rescale = (m_new != m_run) && (m_run != -INFINITY) && (s > 0);
-      const float alpha = (m_new != m_run && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
-      m_run = m_new;
-      l_true *= alpha;
-      l_rnd *= alpha;
-      const float nmref = (m_run == -INFINITY) ? 0.f : -m_run;
-
-      // P = exp2(S tau log2e - m) in 16 bits (the product's operand type; its
-      // rounding is at most half a step per weight).  l_true sums the unrounded
-      // P for the logsumexp; l_rnd sums exactly what the product consumes, so
-      // O_m / l_rnd is a convex combination of V rows.
-      float lt[4] = {0.f, 0.f, 0.f, 0.f}, lr[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int c2 = 0; c2 < 64; c2 += 2) {
-          const int c = hf * 64 + c2;
-          const int ch = (c >> 1) & 1;
-          float x0, x1;
-          fma2(x0, x1, __uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]), sl2, sl2,
-               nmref, nmref);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          add2(lt[2 * ch], lt[2 * ch + 1], p0, p1);
-          const uint32_t u = Cvt<T>::pack(p0, p1);
-          Cvt<T>::acc2(lr[2 * ch], lr[2 * ch + 1], u);
-          pk[c2 >> 1] = u;
-        }
-        tmem_st32(tS + hf * 32, pk);     // over this row's S, which is in registers
-      }
-      l_true += (lt[0] + lt[1]) + (lt[2] + lt[3]);
-      l_rnd += (lr[0] + lr[1]) + (lr[2] + lr[3]);
-      // S(s) exists, so P V(s-1) is done and O may be rescaled.  The warp does
-      // it together when any of its rows needs it (alpha is 1 for the others).
-      if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-        for (int hf = 0; hf < 4; ++hf) {
-          uint32_t o[32];
-          tmem_ld32(tO + hf * 32, o);
-          tmem_wait_ld();
-          reg_fence32(o);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-          tmem_st32(tO + hf * 32, o);
-        }
-      }
+      w.template step<T, 128, kWin>(tS, tO, jmax - kv * kTile, jmin - kv * kTile, sl2, s == 0);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars->p_full[x]);
@@ -337,7 +253,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
     // ---- epilogue: O = O_1 / l_1 - lambda O_2 / l_2, columns 64 x .. of both tensors
     float* inv_sh = reinterpret_cast<float*>(smem + C::kInv);
-    inv_sh[x * 128 + r] = l_rnd > 0.f ? 1.f / l_rnd : 0.f;
+    inv_sh[x * 128 + r] = w.l_rnd > 0.f ? 1.f / w.l_rnd : 0.f;
     // The last product of this warpgroup's own map; the other map may be phases
     // behind, where a parity wait would pass at once, so its end is learned from
     // the barrier both warpgroups meet at.
@@ -376,18 +292,18 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t w[4], w2[4];
+          uint32_t u[4], u2[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            w[t] = Cvt<T>::pack(o[j * 8 + 2 * t], o[j * 8 + 2 * t + 1]);
-            w2[t] = Cvt<T>::pack(o2[j * 8 + 2 * t], o2[j * 8 + 2 * t + 1]);
+            u[t] = Cvt<T>::pack(o[j * 8 + 2 * t], o[j * 8 + 2 * t + 1]);
+            u2[t] = Cvt<T>::pack(o2[j * 8 + 2 * t], o2[j * 8 + 2 * t + 1]);
           }
           const uint32_t off = r * 128 + ((((hf * 4 + j) ^ r) & 7) << 4);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                       :: "r"(smem_u32(ob + off)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                       :: "r"(smem_u32(ob + off)), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
           if (a.has_o2)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(smem_u32(ob2 + off)), "r"(w2[0]), "r"(w2[1]), "r"(w2[2]), "r"(w2[3]) : "memory");
+                         :: "r"(smem_u32(ob2 + off)), "r"(u2[0]), "r"(u2[1]), "r"(u2[2]), "r"(u2[3]) : "memory");
         }
       }
       fence_proxy_async_smem();
@@ -399,7 +315,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bulk_wait_read0();
       }
       if (row_ok)
-        a.lse[((size_t)b * 2 * a.H + 2 * h + x) * a.N + i] = l_true > 0.f ? (m_run + lg2(l_true)) * kLn2 : -INFINITY;
+        a.lse[((size_t)b * 2 * a.H + 2 * h + x) * a.N + i] = w.l_true > 0.f ? (w.m_run + lg2(w.l_true)) * kLn2 : -INFINITY;
     }
   }
 

@@ -26,13 +26,12 @@
 #include <algorithm>
 #include <cmath>
 
-#include "common.cuh"
+#include "prefix.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kPThreads = 160;   // warps 0-3 compute, 4 TMA
-constexpr int kKT = 64;          // keys per stage
 constexpr int kSlots = 304;      // CTAs resident at once: two on each of 152 SMs
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -44,25 +43,6 @@ template <int D> struct PCfg {
   static constexpr int kV = NS * kTile;
   static constexpr int kBar = kV + NS * kTile;
   static constexpr int kBytes = kBar + 256;
-};
-
-struct PArgs {
-  int B, H, Hkv, T, G;         // G = H / Hkv
-  int P, M;
-  int R, r;                    // rows of a K/V head: B*G*T against the prefix, G*T against an own cache
-  int ptile, stile;            // row tiles: 16 or 64
-  int pt, st;                  // row tiles per head
-  int pchunk, schunk;          // keys per split (multiples of 64)
-  int np, ns;                  // splits
-  int pitems;                  // prefix items
-  const void* q;
-  Strides qs;
-  const int32_t* lens;
-  float scale_log2;
-  float* part;                 // [rows][D] unnormalised O
-  float4* stat;                // [rows]: max (log2), true sum, sum of the rounded weights
-  long long srow0;             // first own-cache row of part / stat
-  int* status;
 };
 
 struct PBars {
@@ -310,11 +290,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
       const int row = rbase + 8 * x;
       qr[x] = nullptr;
       if (row < rows) {
-        const int bb = shared ? row / a.r : b;
-        const int rem = shared ? row - bb * a.r : row;
-        const int j = rem / a.T, t = rem - j * a.T;
-        qr[x] = static_cast<const T*>(a.q) + (int64_t)bb * a.qs.b + (int64_t)(hk * a.G + j) * a.qs.h + (int64_t)t * a.qs.n;
-        lim[x] = shared ? a.P : len - a.T + t + 1;
+        qr[x] = prefix_row<T>(a, hk, shared ? row : b * a.r + row);
+        lim[x] = shared ? a.P : len - a.T + row % a.T + 1;
       }
     }
     w.load_q(qr[0], qr[1], lane);
@@ -448,12 +425,16 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 // times (ragged lengths even out), no split shorter than four key tiles, and
 // prefix splits long against the 64 partial rows they leave where the grid
 // allows it.
+bool use_tc(const fa_prefix_params* p, int rows) {
+  return rows > 128 && p->P >= 256;
+}
+
 void plan(const fa_prefix_params* p, PArgs& a) {
   a.B = p->B; a.H = p->H; a.Hkv = p->H_kv; a.T = p->T; a.G = p->H / p->H_kv;
   a.P = p->P; a.M = p->M;
   a.r = a.G * a.T;
   a.R = a.B * a.r;
-  a.ptile = a.R <= 16 ? 16 : 64;
+  a.ptile = a.R <= 16 ? 16 : use_tc(p, a.R) ? 256 : 64;
   a.stile = a.r <= 16 ? 16 : 64;
   a.pt = (a.R + a.ptile - 1) / a.ptile;
   a.st = (a.r + a.stile - 1) / a.stile;
@@ -462,12 +443,18 @@ void plan(const fa_prefix_params* p, PArgs& a) {
   auto clampll = [](long long x, long long lo, long long hi) { return x < lo ? lo : x > hi ? hi : x; };
   const long long even = (wp + wsuf + 3 * kSlots - 1) / (3 * kSlots);
   long long pc = clampll(even, 4, 1 << 20), sc = clampll(even, 4, 64);
+  if (a.ptile == 256) {
+    // one CTA a SM: key splits such that one wave of 152 covers the heads and row tiles
+    const long long groups = (long long)a.Hkv * a.pt, splits = std::max<long long>(1, 152 / groups);
+    pc = 2 * std::max<long long>(1, ((kp + 1) / 2 + splits - 1) / splits);
+    sc = clampll((wsuf + 3 * kSlots - 1) / (3 * kSlots), 4, 64);
+  }
   if (a.ptile == 64) pc = std::max(pc, std::min<long long>(16, clampll(wp / kSlots, 4, 16)));
   a.pchunk = (int)(pc * kKT);
   a.schunk = (int)(sc * kKT);
   a.np = (int)((a.P + (long long)a.pchunk - 1) / a.pchunk);
   a.ns = (int)((a.M + (long long)a.schunk - 1) / a.schunk);
-  a.pitems = a.Hkv * a.pt * a.np;
+  a.pitems = a.ptile == 256 ? 0 : a.Hkv * a.pt * a.np;
   a.srow0 = (long long)a.np * a.Hkv * a.R;
 }
 
@@ -488,6 +475,8 @@ cudaError_t launch_p(const CUtensorMap (&m)[4], const PArgs& a, void* o, Strides
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D>::kBytes);
   if (e != cudaSuccess) return e;
   const long long items = (long long)a.pitems + (long long)a.B * a.Hkv * a.st * a.ns;
+  if (a.ptile == 256 && (e = launch_prefix_tc(Cvt<T>::kAB ? FA_DT_BF16 : FA_DT_F16, D, m[0], m[1], a, s)) != cudaSuccess)
+    return e;
   if (items > 0) {
     kern<<<(unsigned)items, kPThreads, PCfg<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -1,0 +1,41 @@
+// prefix.cuh -- arguments shared by the two kernels of the shared-prefix attention.
+#pragma once
+#include "common.cuh"
+
+namespace fa {
+
+constexpr int kKT = 64;          // rows of the K / V maps' boxes; keys per stage of the register-product kernel
+
+struct PArgs {
+  int B, H, Hkv, T, G;         // G = H / Hkv
+  int P, M;
+  int R, r;                    // rows of a K/V head: B*G*T against the prefix, G*T against an own cache
+  int ptile, stile;            // row tiles: 16 or 64; the prefix also 256 (tensor-memory kernel)
+  int pt, st;                  // row tiles per head
+  int pchunk, schunk;          // keys per split (multiples of 64, pchunk of 128 with 256-row tiles)
+  int np, ns;                  // splits
+  int pitems;                  // prefix items of the launch
+  const void* q;
+  Strides qs;
+  const int32_t* lens;
+  float scale_log2;
+  float* part;                 // [rows][D] unnormalised O
+  float4* stat;                // [rows]: max (log2), true sum, sum of the rounded weights
+  long long srow0;             // first own-cache row of part / stat
+  int* status;
+};
+
+// Query row `row` of the B*G*T rows that share K/V head hk.
+template <typename T>
+__device__ __forceinline__ const T* prefix_row(const PArgs& a, int hk, int row) {
+  const int b = row / a.r;
+  const int rem = row - b * a.r;
+  const int j = rem / a.T, t = rem - j * a.T;
+  return static_cast<const T*>(a.q) + (int64_t)b * a.qs.b + (int64_t)(hk * a.G + j) * a.qs.h + (int64_t)t * a.qs.n;
+}
+
+// Many rows against the prefix (prefix_tc.cu): items of 256 rows and pchunk keys.
+cudaError_t launch_prefix_tc(int dtype, int d, const CUtensorMap& k, const CUtensorMap& v, const PArgs& a,
+                             cudaStream_t s);
+
+}  // namespace fa

@@ -1,0 +1,269 @@
+// prefix_tc.cu -- many query rows against the shared prefix, on the tensor-memory
+// products.
+//
+// Mathematics: prefix.cu.  Here a K/V head's B G T query rows are many, so the
+// prefix part is a plain dense attention of R rows against P keys, bound by the
+// softmax and the tensor rate rather than HBM.  The register products of
+// prefix.cu reach about a quarter of the tcgen05 rate and re-read K and V from
+// L2 for every 64 rows.
+//
+// Mapping, as in the d = 128 forward (fwd_tc.cu): one CTA = 256 rows (two
+// 128-row slots) and one key split, every K / V tile loaded once for both slots;
+// warps 0-7 softmax (one thread a row), warp 8 TMA, warp 9 the S products, warps
+// 10 and 11 the P V products of slot 0 and 1.  A row's place in q follows from
+// (sequence, head, token), so the softmax threads gather their own Q row into
+// the swizzled tile.  Splits are sized so that one wave of CTAs covers the GPU;
+// each leaves (max, sums, O unnormalised) in float32 for the join.
+// Tensor memory per slot (256 columns): S 128 (P over its first 64) | O.
+#include "prefix.cuh"
+#include "row_softmax.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 384;
+
+template <int D> struct TCfg {
+  static constexpr int kTB = 128 * D * 2;                // one [128 rows][D] tile
+  static constexpr int NC = D / 64;                      // 64-column boxes
+  static constexpr int NS = D == 64 ? 5 : 2;             // K / V stages
+  static constexpr int kQ = 0;
+  static constexpr int kK = 2 * kTB;
+  static constexpr int kV = kK + NS * kTB;
+  static constexpr int kBar = kV + NS * kTB;
+  static constexpr int kBytes = kBar + 512;
+};
+static_assert(TCfg<64>::kBytes <= 232448 && TCfg<128>::kBytes <= 232448, "shared memory over the per-block limit");
+
+struct TBars {
+  uint64_t q_full;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t done[3];
+  uint64_t k_full[5], v_full[5], k_empty[5], v_empty[5];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(TBars) <= 512, "barrier block overflows its shared-memory slot");
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PArgs a) {
+  using C = TCfg<D>;
+  constexpr int NS = C::NS, TB = C::kTB, NC = C::NC;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {       // the 128-byte swizzle's tiles: see diff_fwd.cu
+    if (threadIdx.x == 0) atomicExch(a.status, (int)FA_ERR_CUDA);
+    return;
+  }
+  TBars* bars = reinterpret_cast<TBars*>(smem + C::kBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- work item: row tiles of the same keys run together and share them in L2
+  int it = (int)blockIdx.x;
+  const int rt = it % a.pt;
+  it /= a.pt;
+  const int sp = it % a.np;
+  const int hk = it / a.np;
+  const int k0 = sp * a.pchunk;
+  const int kend = min(a.P, k0 + a.pchunk);
+  const int n = (kend - k0 + kTile - 1) / kTile;          // >= 1
+  const int nact = rt * 256 + 128 < a.R ? 2 : 1;          // slots that have rows
+
+  WaitCtl ctl{a.status, &bars->abort, kWaitSleepNs};
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 128 * nact);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_full[x], 128);
+      mbar_init(&bars->pv_done[x], 1);
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_empty[s], nact);
+    }
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  constexpr int ab = Cvt<T>::kAB;
+  // Register split of the 384 x 168 launch budget, as in fwd_tc.cu
+
+  if (warp >= 8) {
+    regs_dec<56>();
+    if (warp == 8) {
+      // ===================== TMA producer =====================
+      if (lane == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        // a tile is two 64-row boxes per 64 columns
+        auto load = [&](int base, const CUtensorMap* m, uint64_t* bar, int row) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              tma_load_4d(smem + base + c * 16384 + hf * 8192, m, bar, c * 64, row + hf * 64, hk, 0);
+        };
+        int nk = 0, nv = 0;
+        for (int s = 0; s < n; ++s) {
+          const int st = s % NS;
+          const uint32_t ph = (uint32_t)(s / NS) & 1u;
+          // a stage's first use needs no wait
+          if (s >= NS && !mbar_wait(&bars->k_empty[st], ph ^ 1u, ctl)) break;
+          mbar_expect_tx(&bars->k_full[st], TB);
+          load(C::kK + st * TB, &tmK, &bars->k_full[st], k0 + s * kTile);
+          ++nk;
+          if (s >= NS && !mbar_wait(&bars->v_empty[st], ph ^ 1u, ctl)) break;
+          mbar_expect_tx(&bars->v_full[st], TB);
+          load(C::kV + st * TB, &tmV, &bars->v_full[st], k0 + s * kTile);
+          ++nv;
+        }
+        // Before leaving, make sure no load is still writing shared memory.
+        for (int j = max(0, nk - NS); j < nk; ++j) mbar_wait(&bars->k_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
+        for (int j = max(0, nv - NS); j < nv; ++j) mbar_wait(&bars->v_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
+      }
+    } else if (warp == 9) {
+      // ===================== S issuer (both slots) =====================
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
+        const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
+        const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
+        bool ok = mbar_wait(&bars->q_full, 0, ctl);
+        for (int s = 0; s < n && ok; ++s) {
+          const int st = s % NS;
+          if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
+          for (int x = 0; x < nact; ++x) {
+            // S_x(s) overwrites P_x(s-1) once P V_x(s-1) has read it
+            if (s > 0 && !(ok = mbar_wait(&bars->pv_done[x], (uint32_t)(s - 1) & 1u, ctl))) break;
+            tc_fence_after();
+            const uint64_t qd = qd0 + (uint64_t)((x * TB) >> 4), kd = kd0 + (uint64_t)((st * TB) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t o = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
+              mma_ss(tmem + x * 256, qd + o, kd + o, idS, k > 0 ? 1u : 0u);
+            }
+            mma_commit(&bars->s_full[x]);
+          }
+          if (ok) mma_commit(&bars->k_empty[st]);
+        }
+        mma_commit(&bars->done[0]);
+        mbar_wait(&bars->done[0], 0, ctl);
+      }
+    } else if (warp - 10 < nact) {
+      // ===================== P V issuer of slot x =====================
+      const int x = warp - 10;
+      if (lane == 0) {
+        constexpr uint32_t idPV = idesc_f16(128, D, ab, 0, 1);
+        const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
+        const uint32_t tP = tmem + x * 256, tO = tP + 128;
+        bool ok = true;
+        for (int s = 0; s < n && ok; ++s) {
+          const int st = s % NS;
+          if (!(ok = mbar_wait(&bars->p_full[x], (uint32_t)s & 1u, ctl) &&
+                     mbar_wait(&bars->v_full[st], (uint32_t)(s / NS) & 1u, ctl)))
+            break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + (uint64_t)((st * TB) >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tO, tP + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&bars->pv_done[x]);
+          mma_commit(&bars->v_empty[st]);
+        }
+        mma_commit(&bars->done[1 + x]);
+        mbar_wait(&bars->done[1 + x], 0, ctl);
+      }
+    }
+  } else {
+    regs_inc<224>();
+    // ===================== softmax warps =====================
+    const int x = warp >> 2;
+    if (x < nact) {
+      const int quarter = warp & 3;
+      const int r = quarter * 32 + lane;          // row within the slot = TMEM lane
+      const int row = rt * 256 + x * 128 + r;
+      const uint32_t tS = tmem + x * 256 + ((uint32_t)(quarter * 32) << 16), tO = tS + 128;
+      // this thread's Q row into the swizzled tile
+      {
+        uint8_t* qb = smem + C::kQ + x * TB + r * 128;
+        const uint4* src = row < a.R ? reinterpret_cast<const uint4*>(prefix_row<T>(a, hk, row)) : nullptr;
+        uint4 v[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) v[c] = src != nullptr ? src[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(qb + (c >> 3) * 16384 + (((c ^ r) & 7) << 4)) = v[c];
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_full);
+      }
+      RowSoftmax w;
+      bool ok = true;
+      for (int s = 0; s < n; ++s) {
+        if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)s & 1u, ctl))) break;
+        tc_fence_after();
+        w.template step<T, D, false>(tS, tO, a.P - 1 - (k0 + s * kTile), 0, a.scale_log2, s == 0);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[x]);
+      }
+      // ---- this row's maximum, sums and unnormalised O
+      if (ok && warp_wait(&bars->pv_done[x], (uint32_t)(n - 1) & 1u, ctl)) {
+        tc_fence_after();
+        const long long pr = ((long long)sp * a.Hkv + hk) * a.R + row;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+          if (row < a.R) {
+            float* dst = a.part + pr * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                           :: "l"(dst + e), "r"(o[e]), "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]),
+                              "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7]) : "memory");
+          }
+        }
+        if (row < a.R) a.stat[pr] = make_float4(w.m_run, w.l_true, w.l_rnd, 0.f);
+        tc_fence_before();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const CUtensorMap& k, const CUtensorMap& v, const PArgs& a, cudaStream_t s) {
+  auto kern = prefix_tc_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(a.Hkv * a.pt * a.np), kThreads, TCfg<D>::kBytes, s>>>(k, v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(int dtype, int d, const CUtensorMap& k, const CUtensorMap& v, const PArgs& a,
+                             cudaStream_t s) {
+  if (dtype == FA_DT_BF16)
+    return d == 128 ? launch_t<__nv_bfloat16, 128>(k, v, a, s) : launch_t<__nv_bfloat16, 64>(k, v, a, s);
+  return d == 128 ? launch_t<__half, 128>(k, v, a, s) : launch_t<__half, 64>(k, v, a, s);
+}
+
+}  // namespace fa

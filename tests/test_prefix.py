@@ -308,3 +308,24 @@ def test_graph_replay_grows_with_the_caches_and_other_stream():
     s.synchronize()
     b = fa.prefix_fwd(q, kp, vp, k, v, lens)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,T,P", [(33, 8, 2, 1, 256), (65, 4, 1, 1, 700), (129, 2, 2, 1, 385), (16, 8, 1, 3, 4097),
+                                         (300, 2, 2, 1, 1000), (7, 6, 1, 40, 2049)])
+def test_many_rows_against_the_prefix(dtype, d, B, H, Hkv, T, P):
+    # more than 128 rows of a K/V head: 256-row tiles whose second half is empty, ragged or full
+    lens = [(11 * b) % 31 for b in range(B)]
+    run(B, H, Hkv, T, P, 31, d, dtype, lens, seed=B + P)
+
+
+@pytest.mark.gpu
+def test_many_rows_layouts_and_large_scores():
+    B, H, Hkv, T, P, M, d = 50, 8, 2, 1, 900, 20, 128
+    q, kp, vp, k, v = inputs(B, H, Hkv, T, P, M, d, "f16", 9)
+    lens = torch.arange(B, device="cuda", dtype=torch.int32) % 21
+    qs = (q * 15).transpose(0, 1).contiguous().transpose(0, 1)
+    kps = kp.transpose(0, 1).contiguous().transpose(0, 1)
+    check(fa.prefix_fwd(qs, kps, vp, k, v, lens), plain(qs, kp, vp, k, v, lens), "f16")
