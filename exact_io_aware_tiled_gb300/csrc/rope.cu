@@ -12,8 +12,8 @@
 // more than a 16-bit rounding.  Here the turn f / 2 pi is held as a 64-bit
 // binary fraction F = f / 2 pi 2^64 and p F is taken modulo 2^64, which drops
 // whole turns exactly; what is left is the fraction of a turn, read as a signed
-// number in [-1/2, 1/2) and handed to sincospif.  One float64 product per
-// thread and pair makes F; everything else is integer and float32.
+// number in [-1/2, 1/2) and handed to sincospif.  One float64 product per CTA
+// and pair makes F; everything else is integer and float32.
 //
 // What bounds it: HBM.  Each element is read and written once, and the angles
 // are computed, not read.  A thread owns V pairs (16-byte vectors where rot / 2
@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -30,7 +31,6 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeHeads = 4;    // heads whose loads are in flight together
 
 struct RopeArgs {
   const void* x[2];        // q, k
@@ -47,24 +47,54 @@ struct RopeArgs {
   float mscale, sgn;
 };
 
+// V consecutive elements, moved as one load or store.
 template <typename T, int V> struct __align__(sizeof(T) * V) RVec { T e[V]; };
 
-__device__ __forceinline__ float ld_f(float x) { return x; }
-__device__ __forceinline__ float ld_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float ld_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void st_f(float& d, float x) { d = x; }
-__device__ __forceinline__ void st_f(__half& d, float x) { d = __float2half_rn(x); }
-__device__ __forceinline__ void st_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+template <typename T, int V> __device__ __forceinline__ void unpack(const RVec<T, V>& v, float (&f)[V]) {
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = v.e[i];
+  } else if constexpr (V == 1) {
+    f[0] = Cvt<T>::to_f(v.e[0]);
+  } else {
+    uint32_t w[V / 2];
+    memcpy(w, &v, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = Cvt<T>::lo(w[i]);
+      f[2 * i + 1] = Cvt<T>::hi(w[i]);
+    }
+  }
+}
+template <typename T, int V> __device__ __forceinline__ RVec<T, V> pack(const float (&f)[V]) {
+  RVec<T, V> v;
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v.e[i] = f[i];
+  } else if constexpr (V == 1) {
+    v.e[0] = Cvt<T>::from_f(f[0]);
+  } else {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = Cvt<T>::pack(f[2 * i], f[2 * i + 1]);
+    memcpy(&v, w, sizeof(w));
+  }
+  return v;
+}
 
-// m cos and +-m sin of the angle p f
-__device__ __forceinline__ void turn(long long p, double f, float m, float sgn, float& c, float& s) {
+// The turn f / 2 pi as a 64-bit binary fraction (whole turns dropped).
+__device__ __forceinline__ unsigned long long turns_of(double f) {
   double t = f * 0.15915494309189533577;                    // 1 / (2 pi)
   t -= floor(t);
-  const unsigned long long F = __double2ull_rn(t * 18446744073709551616.0);
+  return __double2ull_rn(t * 18446744073709551616.0);
+}
+
+// m cos and +-m sin of the angle p f, F the turn of f
+__device__ __forceinline__ void turn(long long p, unsigned long long F, float m, float sm, float& c, float& s) {
   const long long frac = (long long)((unsigned long long)p * F);
   sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
   c *= m;
-  s *= sgn * m;
+  s *= sm;
 }
 
 // The half layout: V pairs (c0 + e, c0 + rot/2 + e) per rotating thread.
@@ -72,73 +102,84 @@ __device__ __forceinline__ void turn(long long p, double f, float m, float sgn, 
 // rotates its first pairs and copies the rest.
 template <typename T, int V, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+  constexpr int NP = kInter ? (V + 1) / 2 : V;       // pairs of a thread
+  constexpr int HB = kInter ? 8 : 4;                 // heads whose loads are in flight together
+  __shared__ unsigned long long sF[128];
+  const int half = a.rot >> 1;
+  // float64 is slow on this GPU: the turns are made once per CTA, not once per thread
+  for (int i = threadIdx.x; i < half; i += kRopeThreads) sF[i] = turns_of(a.inv_freq[i]);
+  __syncthreads();
   const uint32_t t = blockIdx.x * kRopeThreads + threadIdx.x;
   if (t >= a.total) return;
   const uint32_t token = t / (uint32_t)a.units;
   const int u = (int)(t - token * (uint32_t)a.units);
   const uint32_t b = token / (uint32_t)a.N;
   const uint32_t n = token - b * (uint32_t)a.N;
-  const int h0 = blockIdx.y * a.hp;
-  const int h1 = min(a.heads[0] + a.heads[1], h0 + a.hp);
-  const int half = a.rot >> 1;
   const int nrot = kInter ? (a.rot + V - 1) / V : half / V;
   const bool rotates = u < nrot;
   const int c0 = kInter || rotates ? u * V : a.rot + (u - nrot) * V;
   using Vec = RVec<T, V>;
 
-  float cs[kInter ? (V + 1) / 2 : V], sn[kInter ? (V + 1) / 2 : V];
+  float cs[NP], sn[NP];
   if (rotates) {
     long long p = a.start + (long long)n;
     if (a.pos != nullptr) {
       const int64_t at = (int64_t)b * a.pos_b + (int64_t)n * a.pos_n;
       p = a.pos64 ? static_cast<const long long*>(a.pos)[at] : (long long)static_cast<const int*>(a.pos)[at];
     }
+    const float sm = a.sgn * a.mscale;
 #pragma unroll
-    for (int e = 0; e < (kInter ? V / 2 : V); ++e) {
+    for (int e = 0; e < NP; ++e) {
       const int i = kInter ? c0 / 2 + e : c0 + e;
-      if (!kInter || i < half) turn(p, a.inv_freq[i], a.mscale, a.sgn, cs[e], sn[e]);
+      if (!kInter || i < half) turn(p, sF[i], a.mscale, sm, cs[e], sn[e]);
     }
   }
-  for (int h = h0; h < h1; h += kRopeHeads) {
-    Vec v0[kRopeHeads], v1[kRopeHeads];
-    T* dst[kRopeHeads];
+  const int first = blockIdx.y * a.hp;
+#pragma unroll 1
+  for (int w = 0; w < 2; ++w) {                      // q's heads, then k's
+    const int off = w ? a.heads[0] : 0;
+    const int h0 = max(first - off, 0), h1 = min(first + a.hp - off, a.heads[w]);
+    if (h0 >= h1 || (!rotates && a.inplace[w])) continue;
+    const Strides xs = a.xs[w], ys = a.ys[w];
+    const T* src = static_cast<const T*>(a.x[w]) + (int64_t)b * xs.b + (int64_t)h0 * xs.h + (int64_t)n * xs.n + c0;
+    T* dst = static_cast<T*>(a.y[w]) + (int64_t)b * ys.b + (int64_t)h0 * ys.h + (int64_t)n * ys.n + c0;
+    for (int h = h0; h < h1; h += HB, src += HB * xs.h, dst += HB * ys.h) {
+      Vec v0[HB], v1[HB];
 #pragma unroll
-    for (int j = 0; j < kRopeHeads; ++j) {
-      dst[j] = nullptr;
-      if (h + j >= h1) continue;
-      const int w = h + j >= a.heads[0] ? 1 : 0;
-      const int hh = h + j - (w ? a.heads[0] : 0);
-      if (!rotates && (w ? a.inplace[1] : a.inplace[0])) continue;
-      const Strides xs = w ? a.xs[1] : a.xs[0], ys = w ? a.ys[1] : a.ys[0];
-      const T* src = static_cast<const T*>(w ? a.x[1] : a.x[0]) + (int64_t)b * xs.b + (int64_t)hh * xs.h +
-                     (int64_t)n * xs.n + c0;
-      dst[j] = static_cast<T*>(w ? a.y[1] : a.y[0]) + (int64_t)b * ys.b + (int64_t)hh * ys.h + (int64_t)n * ys.n + c0;
-      v0[j] = *reinterpret_cast<const Vec*>(src);
-      if (!kInter && rotates) v1[j] = *reinterpret_cast<const Vec*>(src + half);
-    }
-#pragma unroll
-    for (int j = 0; j < kRopeHeads; ++j) {
-      if (dst[j] == nullptr) continue;
-      if (rotates) {
-        if constexpr (kInter) {
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            if (c0 / 2 + e >= half) continue;
-            const float x0 = ld_f(v0[j].e[2 * e]), x1 = ld_f(v0[j].e[2 * e + 1]);
-            st_f(v0[j].e[2 * e], x0 * cs[e] - x1 * sn[e]);
-            st_f(v0[j].e[2 * e + 1], x1 * cs[e] + x0 * sn[e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float x0 = ld_f(v0[j].e[e]), x1 = ld_f(v1[j].e[e]);
-            st_f(v0[j].e[e], x0 * cs[e] - x1 * sn[e]);
-            st_f(v1[j].e[e], x1 * cs[e] + x0 * sn[e]);
-          }
-          *reinterpret_cast<Vec*>(dst[j] + half) = v1[j];
-        }
+      for (int j = 0; j < HB; ++j) {
+        if (h + j >= h1) break;
+        v0[j] = *reinterpret_cast<const Vec*>(src + j * xs.h);
+        if (!kInter && rotates) v1[j] = *reinterpret_cast<const Vec*>(src + j * xs.h + half);
       }
-      *reinterpret_cast<Vec*>(dst[j]) = v0[j];
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        if (h + j >= h1) break;
+        if (rotates) {
+          float x0[V];
+          unpack<T, V>(v0[j], x0);
+          if constexpr (kInter) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+              if (c0 / 2 + e >= half) continue;
+              const float y0 = x0[2 * e], y1 = x0[2 * e + 1];
+              x0[2 * e] = y0 * cs[e] - y1 * sn[e];
+              x0[2 * e + 1] = y1 * cs[e] + y0 * sn[e];
+            }
+          } else {
+            float x1[V];
+            unpack<T, V>(v1[j], x1);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float y0 = x0[e], y1 = x1[e];
+              x0[e] = y0 * cs[e] - y1 * sn[e];
+              x1[e] = y1 * cs[e] + y0 * sn[e];
+            }
+            *reinterpret_cast<Vec*>(dst + j * ys.h + half) = pack<T, V>(x1);
+          }
+          v0[j] = pack<T, V>(x0);
+        }
+        *reinterpret_cast<Vec*>(dst + j * ys.h) = v0[j];
+      }
     }
   }
 }
@@ -151,11 +192,12 @@ cudaError_t launch_v(RopeArgs a, int B, int d, int sms, cudaStream_t s) {
   a.total = (uint32_t)total;
   const int heads = a.heads[0] + a.heads[1];
   const unsigned gx = (unsigned)((total + kRopeThreads - 1) / kRopeThreads);
-  // split the heads until about four times the resident threads are asked for
-  const long long want = 4ll * sms * 2048 / kRopeThreads;
+  // split the heads until the grid fills the GPU about twice at 1,024 threads a SM
+  const long long want = 2ll * sms * 1024 / kRopeThreads;
   int split = (int)std::min<long long>((want + gx - 1) / gx, heads);
   split = std::min(split, 65535);
   a.hp = (heads + split - 1) / split;
+  if (a.hp > 4) a.hp = (a.hp + 3) / 4 * 4;          // whole batches of loads
   split = (heads + a.hp - 1) / a.hp;
   rope_kernel<T, V, kInter><<<dim3(gx, (unsigned)split), kRopeThreads, 0, s>>>(a);
   return cudaGetLastError();
