@@ -757,13 +757,13 @@ fa_status fa_prefix_fwd(const fa_prefix_params* in, const void* q, const void* k
   fa_params bn{};
   bn.B = 1;
   bn.N = p.P;
-  if (p.P > 0 && ((s = make_map(&m[0], k_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.kp, 64)) != FA_OK ||
-                  (s = make_map(&m[1], v_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.vp, 64)) != FA_OK))
+  if (p.P > 0 && ((s = make_map(&m[0], k_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.kp, 32)) != FA_OK ||
+                  (s = make_map(&m[1], v_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.vp, 32)) != FA_OK))
     return s;
   bn.B = p.B;
   bn.N = p.M;
-  if (p.M > 0 && ((s = make_map(&m[2], k, dt, 2, p.d, 64, &bn, p.H_kv, sd.k, 64)) != FA_OK ||
-                  (s = make_map(&m[3], v, dt, 2, p.d, 64, &bn, p.H_kv, sd.v, 64)) != FA_OK))
+  if (p.M > 0 && ((s = make_map(&m[2], k, dt, 2, p.d, 64, &bn, p.H_kv, sd.k, 32)) != FA_OK ||
+                  (s = make_map(&m[3], v, dt, 2, p.d, 64, &bn, p.H_kv, sd.v, 32)) != FA_OK))
     return s;
   const float scale = (p.scale > 0.f && std::isfinite(p.scale)) ? p.scale : 1.f / std::sqrt((float)p.d);
   return cuda_status(launch_prefix(&p, m, q, sd.q, o, sd.o, lse, scale * 1.4426950408889634f,

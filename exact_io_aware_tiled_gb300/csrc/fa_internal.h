@@ -179,7 +179,7 @@ cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& 
 // dlam[h] = -sum of the partial sums, in a fixed order.
 cudaError_t launch_diff_dlam(const float* part, float* dlam, int B, int H, int group, int nq, cudaStream_t s);
 // Attention over a shared prefix: the workspace of a checked problem, and the launches.  m: maps of k_prefix,
-// v_prefix, k, v (64-row, 64-column boxes); those of an empty part are not read.
+// v_prefix, k, v (32-row, 64-column boxes); those of an empty part are not read.
 size_t prefix_workspace(const fa_prefix_params* p);
 cudaError_t launch_prefix(const fa_prefix_params* p, const CUtensorMap (&m)[4], const void* q, Strides qs, void* o,
                           Strides os, float* lse, float scale_log2, uint8_t* ws, cudaStream_t s);

@@ -16,13 +16,14 @@
 // products: a decode tile has 1 to 64 rows, and at 16 rows a 128-row tensor-
 // memory tile would be seven eighths empty.
 //
-// Work items (one CTA each, two CTAs on an SM): (prefix, K/V head, row tile,
-// key split) first, then (sequence, K/V head, row tile, key split).  Warp 4
-// streams 64-key tiles of K and V with TMA; warps 0-3 compute:
-//   * up to 16 rows: each warp takes 16 of a tile's 64 keys for all rows, with
-//     its own running maximum, and the four join at the end: every key is read
-//     from shared memory once;
-//   * more rows: each warp takes 16 rows of a 64-row tile and all keys.
+// Work items: (prefix, K/V head, row tile, key split) first, then (sequence, K/V
+// head, row tile, key split), claimed from a counter by persistent CTAs (two or
+// three on an SM).  Warp 4 claims them and streams their 32-key tiles of K and V
+// with TMA, running ahead into the next item while warps 0-3 finish the last;
+// each takes 16 rows, and the four split a tile of 16 / 32 / 64 rows into 1 / 2 /
+// 4 row groups and the 32-key tiles among 4 / 2 / 1 key groups with running
+// maxima of their own, which join at the end of the item.  So a key is read from
+// shared memory once per 16 rows that need it, and few rows still use all warps.
 #include <algorithm>
 #include <cmath>
 
@@ -32,24 +33,78 @@ namespace fa {
 namespace {
 
 constexpr int kPThreads = 160;   // warps 0-3 compute, 4 TMA
-constexpr int kSlots = 304;      // CTAs resident at once: two on each of 152 SMs
+constexpr int kSms = 152;        // the plan's SM count: a workspace's size does not depend on the device at hand
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D> struct PCfg {
   static constexpr int NB = D / 64;                  // 64-column boxes per row
-  static constexpr int kTile = kKT * D * 2;          // one K or V stage
-  static constexpr int NS = D == 64 ? 6 : 3;
+  static constexpr int KS = D == 64 ? 64 : 32;       // keys of a stage
+  static constexpr int kBox = KS * 128;              // one 64-column box of a stage
+  static constexpr int kTile = KS * D * 2;           // one K or V stage
+  static constexpr int NS = 4;                       // a multiple of 4: with split keys stage s is warp s % 4's
+  static constexpr int kCtas = D == 64 ? 3 : 2;      // CTAs per SM
   static constexpr int kK = 0;
   static constexpr int kV = NS * kTile;
-  static constexpr int kBar = kV + NS * kTile;
-  static constexpr int kBytes = kBar + 256;
+  static constexpr int kJoin = kV + NS * kTile;      // [2][16][D] O and [2][16] statistics of two warps
+  static constexpr int kBar = kJoin + 2 * 16 * (D * 4 + 16);
+  static constexpr int kItem = kBar + 256;           // two published items
+  static constexpr int kBytes = kItem + 128;
 };
+static_assert(PCfg<64>::kCtas * (PCfg<64>::kBytes + 1024) <= 233472 && PCfg<128>::kCtas * (PCfg<128>::kBytes + 1024) <= 233472,
+              "the CTAs of one SM exceed its shared memory");
 
 struct PBars {
-  uint64_t full[6], empty[6];
+  uint64_t full[4], empty[4];
+  uint64_t item_full[2], item_empty[2], join;
   int abort;
 };
+static_assert(sizeof(PBars) <= 256, "barrier block overflows its shared-memory slot");
 
+// One work item: rows rt * tile .. of K/V head hk against keys k0 .. kend - 1,
+// of the prefix or of sequence b's cache.
+struct PItem {
+  bool shared;
+  int b, hk, rt, sp;
+  int k0, kend;          // keys of this split; kend <= the part's filled rows
+  int end;               // filled rows of the part
+  int rows, tile;
+  int nt;                // stages, 0: nothing to do; -1 in the mailbox: no more items
+};
+static_assert(sizeof(PItem) <= 64, "an item overflows its mailbox slot");
+
+template <int KS>
+__device__ __forceinline__ PItem prefix_item(const PArgs& a, int u) {
+  PItem it;
+  it.shared = u < a.pitems;
+  it.b = 0;
+  int chunk;
+  if (it.shared) {
+    it.rt = u % a.pt;            // row tiles of the same keys run together and share them in L2
+    u /= a.pt;
+    it.sp = u % a.np;
+    it.hk = u / a.np;
+    it.end = a.P;
+    chunk = a.pchunk; it.rows = a.R; it.tile = a.ptile;
+  } else {
+    u -= a.pitems;
+    it.rt = u % a.st;
+    u /= a.st;
+    it.hk = u % a.Hkv;
+    u /= a.Hkv;
+    it.b = u % a.B;              // every sequence's first split before any second: the long ones start early
+    it.sp = u / a.B;
+    it.end = max(0, min(a.M, a.lens[it.b]));
+    chunk = a.schunk; it.rows = a.r; it.tile = a.stile;
+  }
+  it.k0 = it.sp * chunk;
+  it.kend = min(it.end, it.k0 + chunk);
+  it.nt = it.kend > it.k0 ? (it.kend - it.k0 + KS - 1) / KS : 0;
+  return it;
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(bar)), "r"(n) : "memory");
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -96,12 +151,11 @@ template <typename T, int D> struct Rows {
       q[k][3] = r1 ? *reinterpret_cast<const uint32_t*>(r1 + c + 8) : 0u;
     }
   }
-  // NK keys (a multiple of 16) of a stage, from stage row `row0`; the key of
-  // stage row x is key0 + x.  lim: keys at or past it are hidden, per row;
-  // kend: V rows at or past it may hold anything.
-  template <int NK>
-  __device__ __forceinline__ void step(uint32_t sK, uint32_t sV, int row0, int key0, const int (&lim)[2], int kend,
-                                       float sl2, int lane) {
+  // The keys of one stage, key0 and on.  lim: keys at or past it are hidden, per
+  // row; kend: V rows at or past it may hold anything.
+  __device__ __forceinline__ void step(uint32_t sK, uint32_t sV, int key0, const int (&lim)[2], int kend, float sl2,
+                                       int lane) {
+    constexpr int NK = PCfg<D>::KS, kBox = PCfg<D>::kBox;
     float s[NK / 8][4];
 #pragma unroll
     for (int n = 0; n < NK / 8; ++n)
@@ -113,16 +167,16 @@ template <typename T, int D> struct Rows {
 #pragma unroll
       for (int n = 0; n < NK / 16; ++n) {
         // matrices: keys 0-7 / 8-15 (lm >> 1), columns 0-7 / 8-15 (lm & 1)
-        const uint32_t row = row0 + n * 16 + (lm >> 1) * 8 + lr_;
+        const uint32_t row = n * 16 + (lm >> 1) * 8 + lr_;
         const uint32_t col = (k & 3) * 16 + (lm & 1) * 8;
         uint32_t b[4];
-        ldsm4(b, sK + (k >> 2) * (kKT * 128) + sw128_off(row, col));
+        ldsm4(b, sK + (k >> 2) * kBox + sw128_off(row, col));
         mma16816<T>(s[2 * n], q[k], b[0], b[1]);
         mma16816<T>(s[2 * n + 1], q[k], b[2], b[3]);
       }
     }
-    const int kl = key0 + row0 + 2 * (lane & 3);      // key of s[0][0]
-    if (key0 + row0 + NK > min(lim[0], lim[1])) {
+    const int kl = key0 + 2 * (lane & 3);      // key of s[0][0]
+    if (key0 + NK > min(lim[0], lim[1])) {
 #pragma unroll
       for (int n = 0; n < NK / 8; ++n)
 #pragma unroll
@@ -136,60 +190,115 @@ template <typename T, int D> struct Rows {
       mx[1] = fmaxf(mx[1], fmaxf(s[n][2], s[n][3]));
     }
     float alpha[2], nm[2];
+    bool moved = false;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-      const float m_new = fmaxf(m[x], mx[x] * sl2);
-      alpha[x] = m[x] == -INFINITY ? 1.f : ex2(m[x] - m_new);
+      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2)) * sl2;
+      // the reference maximum moves only when it is exceeded by 2^8: any
+      // reference gives the same quotient, and most steps skip the rescale
+      const float m_new = mx[x] > m[x] + 8.f ? mx[x] : m[x];
+      alpha[x] = 1.f;
+      if (m_new != m[x]) {
+        alpha[x] = m[x] == -INFINITY ? 0.f : ex2(m[x] - m_new);
+        moved = true;
+      }
       m[x] = m_new;
       nm[x] = m_new == -INFINITY ? 0.f : -m_new;
-      lt[x] *= alpha[x];
-      lr[x] *= alpha[x];
     }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= alpha[0];
-        o[n][1] *= alpha[0];
-        o[n][2] *= alpha[1];
-        o[n][3] *= alpha[1];
+      for (int x = 0; x < 2; ++x) {
+        lt[x] *= alpha[x];
+        lr[x] *= alpha[x];
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][2 * x] *= alpha[x];
+          o[n][2 * x + 1] *= alpha[x];
+        }
       }
     }
     // P in 16 bits, the product's operand type (half a step per weight); the
     // rounded sum normalises O, the unrounded one makes the logsumexp
     uint32_t p[NK / 16][4];
+    float st[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, sr[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
     for (int n = 0; n < NK / 8; ++n) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float p0 = ex2(fmaf(s[n][2 * x], sl2, nm[x])), p1 = ex2(fmaf(s[n][2 * x + 1], sl2, nm[x]));
-        lt[x] += p0 + p1;
-        const uint32_t u = Cvt<T>::pack(p0, p1);
-        lr[x] += Cvt<T>::lo(u) + Cvt<T>::hi(u);
+        float e0, e1;
+        fma2(e0, e1, s[n][2 * x], s[n][2 * x + 1], sl2, sl2, nm[x], nm[x]);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        add2(st[x][0], st[x][1], e0, e1);
+        const uint32_t u = Cvt<T>::pack(e0, e1);
+        Cvt<T>::acc2(sr[x][0], sr[x][1], u);
         p[n >> 1][(n & 1) * 2 + x] = u;
       }
     }
-    const bool tail = key0 + row0 + NK > kend;
 #pragma unroll
-    for (int k = 0; k < NK / 16; ++k) {
-      // V rows past kend are replaced by zeros (0 x NaN would not be 0): register
-      // pairs hold keys kp, kp + 1 and kp + 8, kp + 9
+    for (int x = 0; x < 2; ++x) {
+      lt[x] += st[x][0] + st[x][1];
+      lr[x] += sr[x][0] + sr[x][1];
+    }
+    // V rows past kend are replaced by zeros (0 x NaN would not be 0)
+    if (key0 + NK > kend) pv<true>(sV, p, kend - key0, lane);
+    else pv<false>(sV, p, 0, lane);
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void pv(uint32_t sV, const uint32_t (&p)[PCfg<D>::KS / 16][4], int live, int lane) {
+    const int lr_ = lane & 7, lm = lane >> 3;
+#pragma unroll
+    for (int k = 0; k < PCfg<D>::KS / 16; ++k) {
+      // register pairs hold keys kp, kp + 1 and kp + 8, kp + 9
       uint32_t z0 = ~0u, z1 = ~0u;
-      if (tail) {
-        const int kp = key0 + row0 + k * 16 + 2 * (lane & 3);
-        z0 = (kp < kend ? 0xFFFFu : 0u) | (kp + 1 < kend ? 0xFFFF0000u : 0u);
-        z1 = (kp + 8 < kend ? 0xFFFFu : 0u) | (kp + 9 < kend ? 0xFFFF0000u : 0u);
+      if (kTail) {
+        const int kp = k * 16 + 2 * (lane & 3);
+        z0 = (kp < live ? 0xFFFFu : 0u) | (kp + 1 < live ? 0xFFFF0000u : 0u);
+        z1 = (kp + 8 < live ? 0xFFFFu : 0u) | (kp + 9 < live ? 0xFFFF0000u : 0u);
       }
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) {
         // matrices: keys 0-7 / 8-15 (lm & 1), columns 0-7 / 8-15 (lm >> 1)
-        const uint32_t row = row0 + k * 16 + (lm & 1) * 8 + lr_;
+        const uint32_t row = k * 16 + (lm & 1) * 8 + lr_;
         const uint32_t col = (n & 3) * 16 + (lm >> 1) * 8;
         uint32_t b[4];
-        ldsm4t(b, sV + (n >> 2) * (kKT * 128) + sw128_off(row, col));
-        mma16816<T>(o[2 * n], p[k], b[0] & z0, b[1] & z1);
-        mma16816<T>(o[2 * n + 1], p[k], b[2] & z0, b[3] & z1);
+        ldsm4t(b, sV + (n >> 2) * PCfg<D>::kBox + sw128_off(row, col));
+        if (kTail) {
+          b[0] &= z0; b[1] &= z1; b[2] &= z0; b[3] &= z1;
+        }
+        mma16816<T>(o[2 * n], p[k], b[0], b[1]);
+        mma16816<T>(o[2 * n + 1], p[k], b[2], b[3]);
+      }
+    }
+  }
+  // this warp's rows and statistics into shared memory, and another warp's joined to this one's
+  __device__ __forceinline__ void put(float* so, float4* ss, int lane) const {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = (lane >> 2) + 8 * x;
+      float* dst = so + row * D + 2 * (lane & 3);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+      if ((lane & 3) == 0) ss[row] = make_float4(m[x], lt[x], lr[x], 0.f);
+    }
+  }
+  __device__ __forceinline__ void join(const float* so, const float4* ss, int lane) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = (lane >> 2) + 8 * x;
+      const float4 st = ss[row];
+      const float m_new = fmaxf(m[x], st.x);
+      const float fa_ = m[x] == -INFINITY ? 0.f : ex2(m[x] - m_new), fb = st.x == -INFINITY ? 0.f : ex2(st.x - m_new);
+      m[x] = m_new;
+      lt[x] = lt[x] * fa_ + st.y * fb;
+      lr[x] = lr[x] * fa_ + st.z * fb;
+      const float* src = so + row * D + 2 * (lane & 3);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const float2 v = *reinterpret_cast<const float2*>(src + n * 8);
+        o[n][2 * x] = o[n][2 * x] * fa_ + v.x * fb;
+        o[n][2 * x + 1] = o[n][2 * x + 1] * fa_ + v.y * fb;
       }
     }
   }
@@ -205,7 +314,7 @@ template <typename T, int D> struct Rows {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPThreads, 2)
+__global__ void __launch_bounds__(kPThreads, PCfg<D>::kCtas)
 prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ CUtensorMap tmVP,
               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PArgs a) {
   using C = PCfg<D>;
@@ -217,198 +326,235 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
   }
   PBars* bars = reinterpret_cast<PBars*>(smem + C::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- work item
-  int it = (int)blockIdx.x;
-  const bool shared = it < a.pitems;
-  int b = 0, hk, rt, sp, kend, chunk, rows, tile;
-  if (shared) {
-    rt = it % a.pt;            // row tiles of the same keys run together and share them in L2
-    it /= a.pt;
-    sp = it % a.np;
-    hk = it / a.np;
-    kend = a.P;
-    chunk = a.pchunk; rows = a.R; tile = a.ptile;
-  } else {
-    it -= a.pitems;
-    rt = it % a.st;
-    it /= a.st;
-    hk = it % a.Hkv;
-    it /= a.Hkv;
-    b = it % a.B;
-    sp = it / a.B;
-    kend = max(0, min(a.M, a.lens[b]));
-    chunk = a.schunk; rows = a.r; tile = a.stile;
-  }
-  const int k0 = sp * chunk;
-  if (k0 >= kend) return;                     // a split past this sequence's keys: the join does not read it
-  const int len = kend;
-  const int nt = (min(kend - k0, chunk) + kKT - 1) / kKT;
-
   WaitCtl ctl{a.status, &bars->abort, kWaitSleepNs};
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 4);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], 4);
+    }
+    mbar_init(&bars->join, 4);
     bars->abort = 0;
     fence_mbar_init();
   }
   __syncthreads();
 
   if (warp == 4) {
+    // ===================== items and TMA =====================
     if (lane == 0) {
-      const CUtensorMap* mk = shared ? &tmKP : &tmK;
-      const CUtensorMap* mv = shared ? &tmVP : &tmV;
-      int t = 0;
-      for (; t < nt; ++t) {
-        const int st = t % NS;
-        if (t >= NS && !mbar_wait(&bars->empty[st], (uint32_t)(t / NS - 1) & 1u, ctl)) break;
-        mbar_expect_tx(&bars->full[st], 2 * C::kTile);
+      prefetch_tmap(&tmKP);
+      prefetch_tmap(&tmVP);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      int g = 0;                 // stages loaded
+      bool ok = true;
+      // the first item is the CTA's own index, the others come from the counter
+      int u = (int)blockIdx.x;
+      for (int kf = 0; ok; u = (int)gridDim.x + atomicAdd(a.sched, 1)) {
+        PItem it;
+        it.nt = -1;
+        if (u < a.items) {
+          it = prefix_item<C::KS>(a, u);
+          if (it.nt == 0) continue;           // a split past this sequence's keys: the join does not read it
+        }
+        const int slot = kf & 1;
+        if (kf >= 2 && !(ok = mbar_wait(&bars->item_empty[slot], (uint32_t)((kf >> 1) - 1) & 1u, ctl))) break;
+        *reinterpret_cast<PItem*>(smem + C::kItem + slot * 64) = it;
+        mbar_arrive(&bars->item_full[slot]);
+        ++kf;
+        if (it.nt < 0) break;
+        const CUtensorMap* mk = it.shared ? &tmKP : &tmK;
+        const CUtensorMap* mv = it.shared ? &tmVP : &tmV;
+        for (int t = 0; t < it.nt; ++t, ++g) {
+          const int st = g % NS;
+          if (g >= NS && !(ok = mbar_wait(&bars->empty[st], (uint32_t)(g / NS - 1) & 1u, ctl))) break;
+          mbar_expect_tx(&bars->full[st], 2 * C::kTile);
 #pragma unroll
-        for (int c = 0; c < C::NB; ++c) {
-          tma_load_4d(smem + C::kK + st * C::kTile + c * (kKT * 128), mk, &bars->full[st], c * 64, k0 + t * kKT, hk, b);
-          tma_load_4d(smem + C::kV + st * C::kTile + c * (kKT * 128), mv, &bars->full[st], c * 64, k0 + t * kKT, hk, b);
+          for (int c = 0; c < C::NB; ++c)
+#pragma unroll
+            for (int x = 0; x < C::KS; x += kKT) {
+              const int row = it.k0 + t * C::KS + x;
+              uint8_t* dst = smem + st * C::kTile + c * C::kBox + x * 128;
+              tma_load_4d(dst + C::kK, mk, &bars->full[st], c * 64, row, it.hk, it.b);
+              tma_load_4d(dst + C::kV, mv, &bars->full[st], c * 64, row, it.hk, it.b);
+            }
         }
       }
       // no load may still be writing shared memory when the CTA ends
-      for (int j = max(0, t - NS); j < t; ++j) mbar_wait(&bars->full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
+      for (int j = max(0, g - NS); j < g; ++j) mbar_wait(&bars->full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
     }
-    if (tile != 16) return;
+    return;
   }
 
-  Rows<T, D> w;
-  const bool split_keys = tile == 16;
-  const int rbase = rt * tile + (split_keys ? 0 : warp * 16) + (lane >> 2);
-  int lim[2] = {0, 0};
-  bool ok = true;
-  if (warp < 4) {
+  // ===================== compute warps =====================
+  float* so = reinterpret_cast<float*>(smem + C::kJoin);              // [2][16][D]
+  float4* ss = reinterpret_cast<float4*>(so + 2 * 16 * D);            // [2][16]
+  // barrier of the four compute warps: bounded like every wait, so that a warp
+  // that gave up leaves none behind
+  int nj = 0;
+  auto meet = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->join);
+    return __all_sync(0xffffffffu, mbar_wait(&bars->join, (uint32_t)nj++ & 1u, ctl));
+  };
+  int g = 0;
+  for (int kc = 0;; ++kc) {
+    const int slot = kc & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl))) return;
+    const PItem it = *reinterpret_cast<const PItem*>(smem + C::kItem + slot * 64);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
+    if (it.nt < 0) return;
+    // warp = (key group) * rgs + (row group): rgs groups of 16 rows, 4 / rgs of stages
+    const int rgs = it.tile >> 4, kgs = 4 / rgs;
+    const int rg = warp & (rgs - 1), kg = warp / rgs;
+    const int rbase = it.rt * it.tile + rg * 16 + (lane >> 2);
+    Rows<T, D> w;
     w.init();
+    int lim[2] = {0, 0};
     const T* qr[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int row = rbase + 8 * x;
       qr[x] = nullptr;
-      if (row < rows) {
-        qr[x] = prefix_row<T>(a, hk, shared ? row : b * a.r + row);
-        lim[x] = shared ? a.P : len - a.T + row % a.T + 1;
+      if (row < it.rows) {
+        qr[x] = prefix_row<T>(a, it.hk, it.shared ? row : it.b * a.r + row);
+        lim[x] = it.shared ? a.P : it.end - a.T + row % a.T + 1;
       }
     }
     w.load_q(qr[0], qr[1], lane);
-    const bool idle = !split_keys && rt * tile + warp * 16 >= rows;
-    for (int t = 0; t < nt; ++t) {
-      const int st = t % NS;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[st], (uint32_t)(t / NS) & 1u, ctl));
-      if (!ok) break;
+    const bool idle = it.rt * it.tile + rg * 16 >= it.rows;
+    for (int t = 0; t < it.nt; ++t, ++g) {
+      const int st = g % NS;
+      // A stage belongs to one key group for all its phases in an item.  The
+      // other warps do not wait on it (they would lag behind its phases); where
+      // they next do, in an item split otherwise, the join has brought all
+      // warps together.
+      if ((st & (kgs - 1)) != kg) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[st], (uint32_t)(g / NS) & 1u, ctl))) return;
       const uint32_t sK = smem_u32(smem + C::kK + st * C::kTile), sV = smem_u32(smem + C::kV + st * C::kTile);
-      const int key0 = k0 + t * kKT;
-      if (split_keys) {
-        if (key0 + warp * 16 < kend) w.template step<16>(sK, sV, warp * 16, key0, lim, kend, a.scale_log2, lane);
-      } else if (!idle) {
-        w.template step<64>(sK, sV, 0, key0, lim, kend, a.scale_log2, lane);
-      }
+      if (!idle) w.step(sK, sV, it.k0 + t * C::KS, lim, it.kend, a.scale_log2, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->empty[st]);
+      if (lane == 0) mbar_arrive_n(&bars->empty[st], kgs);
     }
     w.sum_lanes();
-  }
-  // row i of this item in the partial arrays
-  const long long prow0 = shared ? ((long long)sp * a.Hkv + hk) * a.R
-                                 : a.srow0 + (((long long)b * a.Hkv + hk) * a.ns + sp) * a.r;
-  if (!split_keys) {
-    if (!ok) return;
+    // ---- join the key groups: warps 2, 3 into 0, 1, then (one row group) 1 into 0
+#pragma unroll 1
+    for (int half = 2; half >= rgs; half >>= 1) {
+      if (warp >= half && warp < 2 * half) w.put(so + (warp - half) * 16 * D, ss + (warp - half) * 16, lane);
+      if (!meet()) return;
+      if (warp < half) w.join(so + warp * 16 * D, ss + warp * 16, lane);
+      if (!meet()) return;
+    }
+    if (kg != 0) continue;
+    // row i of this item in the partial arrays
+    const long long prow0 = it.shared ? ((long long)it.sp * a.Hkv + it.hk) * a.R
+                                      : a.srow0 + (((long long)it.b * a.Hkv + it.hk) * a.ns + it.sp) * a.r;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int row = rbase + 8 * x;
-      if (row >= rows) continue;
+      if (row >= it.rows) continue;
       float* dst = a.part + (prow0 + row) * D + 2 * (lane & 3);
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(w.o[n][2 * x], w.o[n][2 * x + 1]);
       if ((lane & 3) == 0) a.stat[prow0 + row] = make_float4(w.m[x], w.lt[x], w.lr[x], 0.f);
     }
-    return;
-  }
-  // ---- join the four warps' key quarters (the stages are free: every load has landed and been read)
-  float* so = reinterpret_cast<float*>(smem);                       // [4][16][D]
-  float* ss = so + 4 * 16 * D;                                      // [4][16][3]
-  const bool any_bad = __syncthreads_or(!ok || bars->abort);
-  if (any_bad) return;
-  if (warp < 4) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int row = (lane >> 2) + 8 * x;
-      float* dst = so + (warp * 16 + row) * D + 2 * (lane & 3);
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(w.o[n][2 * x], w.o[n][2 * x + 1]);
-      if ((lane & 3) == 0) {
-        float* d = ss + (warp * 16 + row) * 3;
-        d[0] = w.m[x]; d[1] = w.lt[x]; d[2] = w.lr[x];
-      }
-    }
-  }
-  __syncthreads();
-  const int nrow = min(16, rows - rt * 16);
-  for (int e = threadIdx.x; e < nrow * (D / 4); e += kPThreads) {
-    const int row = e / (D / 4), c = (e % (D / 4)) * 4;
-    float m = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) m = fmaxf(m, ss[(g * 16 + row) * 3]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float lt = 0.f, lr = 0.f;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float mg = ss[(g * 16 + row) * 3];
-      const float f = mg == -INFINITY ? 0.f : ex2(mg - m);
-      const float4 v = *reinterpret_cast<const float4*>(so + (g * 16 + row) * D + c);
-      acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
-      lt += f * ss[(g * 16 + row) * 3 + 1];
-      lr += f * ss[(g * 16 + row) * 3 + 2];
-    }
-    const long long pr = prow0 + rt * 16 + row;
-    *reinterpret_cast<float4*>(a.part + pr * D + c) = acc;
-    if (c == 0) a.stat[pr] = make_float4(m, lt, lr, 0.f);
   }
 }
 
-// Joins the splits of each query row: one warp per row, D / 32 columns a lane.
-// Bound by the partial rows it reads (mostly from L2) and its launch.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) prefix_join_kernel(const PArgs a, T* __restrict__ o, Strides os,
+// Joins the splits of each query row: W warps per row (1 for few splits, else 4),
+// D / 32 columns a lane.  The lanes fetch the splits' statistics side by side,
+// then every split's row is an independent load.  Launched to overlap the end of
+// the kernel before it (griddepcontrol.wait before the first read of its rows).
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(128) prefix_join_kernel(const PArgs a, T* __restrict__ o, Strides os,
                                                           float* __restrict__ lse) {
   constexpr int E = D / 32;
-  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)a.B * a.H * a.T) return;
-  const int t = (int)(row % a.T);
-  const long long bh = row / a.T;
-  const int h = (int)(bh % a.H), b = (int)(bh / a.H);
+  __shared__ float sh[W == 1 ? 1 : 4][W == 1 ? 1 : D + 3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = W == 1 ? (int)(blockIdx.x * 4 + warp) : (int)blockIdx.x;       // B H T < 2^26
+  const int w0 = W == 1 ? 0 : warp;
+  const bool live = row < a.B * a.H * a.T;
+  const int bh = live ? row / a.T : 0, t = live ? row - bh * a.T : 0;
+  const int b = bh / a.H, h = bh - b * a.H;
   const int hk = h / a.G, j = h - hk * a.G;
   const int len = max(0, min(a.M, a.lens[b]));
-  const int ns = (len + a.schunk - 1) / a.schunk;
-  const int n = a.np + ns;
+  const int n = live ? a.np + (len + a.schunk - 1) / a.schunk : 0;
   const long long prow = ((long long)b * a.G + j) * a.T + t;             // row of the prefix items
   const long long own = a.srow0 + (((long long)b * a.Hkv + hk) * a.ns) * a.r + (long long)j * a.T + t;
   auto at = [&](int s) -> long long {
     return s < a.np ? ((long long)s * a.Hkv + hk) * a.R + prow : own + (long long)(s - a.np) * a.r;
   };
-  float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, a.stat[at(s)].x);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float m = -INFINITY, acc[E] = {}, lt = 0.f, lr = 0.f;
+  // this warp's splits: w0, w0 + W, ...; 32 statistics at a time
+  for (int s0 = w0; s0 < n; s0 += 32 * W) {
+    const int cnt = min(32, (n - s0 + W - 1) / W);
+    const float4 st = lane < cnt ? a.stat[at(s0 + lane * W)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    float mx = st.x;
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  float acc[E] = {}, lt = 0.f, lr = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const long long p = at(s);
-    const float4 st = a.stat[p];
+    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    const float m_new = fmaxf(m, mx);
+    const float old = m == -INFINITY ? 0.f : ex2(m - m_new);
+    m = m_new;
     const float f = st.x == -INFINITY ? 0.f : ex2(st.x - m);
-    lt += f * st.y;
-    lr += f * st.z;
-    float v[E];
-    if constexpr (E == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part + p * D + lane * E);
-    else *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part + p * D + lane * E);
+    float ft = f * st.y, fr = f * st.z;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+    for (int x = 16; x > 0; x >>= 1) {
+      ft += __shfl_xor_sync(0xffffffffu, ft, x);
+      fr += __shfl_xor_sync(0xffffffffu, fr, x);
+    }
+    lt = lt * old + ft;
+    lr = lr * old + fr;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= old;
+    for (int s1 = 0; s1 < cnt; s1 += 8) {
+      float v[8][E];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float* src = a.part + at(s0 + min(s1 + s, cnt - 1) * W) * D + lane * E;
+        if constexpr (E == 2) *reinterpret_cast<float2*>(v[s]) = *reinterpret_cast<const float2*>(src);
+        else *reinterpret_cast<float4*>(v[s]) = *reinterpret_cast<const float4*>(src);
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float fs = __shfl_sync(0xffffffffu, f, (s1 + s) & 31);
+        if (s1 + s < cnt) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += fs * v[s][e];
+        }
+      }
+    }
   }
+  if constexpr (W > 1) {
+    // the four warps' parts, in warp order
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+      sh[warp][D] = m; sh[warp][D + 1] = lt; sh[warp][D + 2] = lr;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) mm = fmaxf(mm, sh[g][D]);
+    lt = lr = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float f = sh[g][D] == -INFINITY ? 0.f : ex2(sh[g][D] - mm);
+      lt += f * sh[g][D + 1];
+      lr += f * sh[g][D + 2];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += f * sh[g][lane * E + e];
+    }
+    m = mm;
+  }
+  if (!live) return;
   const float inv = lr > 0.f ? 1.f / lr : 0.f;
   T* dst = o + (int64_t)b * os.b + (int64_t)h * os.h + (int64_t)t * os.n + lane * E;
   uint32_t w[E / 2];
@@ -419,42 +565,62 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PArgs a, T* __re
   if (lane == 0) lse[row] = lt > 0.f ? (m + lg2(lt)) * kLn2 : -INFINITY;
 }
 
+template <typename T, int D, int W>
+cudaError_t launch_join(const PArgs& a, void* o, Strides os, float* lse, cudaStream_t s) {
+  const int rows = a.B * a.H * a.T;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(W == 1 ? (rows + 3) / 4 : rows));
+  c.blockDim = dim3(128);
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, prefix_join_kernel<T, D, W>, a, static_cast<T*>(o), os, lse);
+}
+
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Row tiles and key splits.  Enough items to fill the resident CTAs about three
-// times (ragged lengths even out), no split shorter than four key tiles, and
-// prefix splits long against the 64 partial rows they leave where the grid
-// allows it.
 bool use_tc(const fa_prefix_params* p, int rows) {
   return rows > 128 && p->P >= 256;
 }
 
+int row_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// Row tiles and key splits.  The work of a 64-key unit is tile / 16 warp tiles;
+// splits are cut so that the items are about equal in that measure and number
+// three for every resident CTA (ragged lengths and the long prefix items even
+// out), but no shorter than four units.
 void plan(const fa_prefix_params* p, PArgs& a) {
+  constexpr int kU = 64;
   a.B = p->B; a.H = p->H; a.Hkv = p->H_kv; a.T = p->T; a.G = p->H / p->H_kv;
   a.P = p->P; a.M = p->M;
   a.r = a.G * a.T;
   a.R = a.B * a.r;
-  a.ptile = a.R <= 16 ? 16 : use_tc(p, a.R) ? 256 : 64;
-  a.stile = a.r <= 16 ? 16 : 64;
+  a.ptile = use_tc(p, a.R) ? 256 : row_tile(a.R);
+  a.stile = row_tile(a.r);
   a.pt = (a.R + a.ptile - 1) / a.ptile;
   a.st = (a.r + a.stile - 1) / a.stile;
-  const long long kp = (a.P + kKT - 1) / kKT, ks = (a.M + kKT - 1) / kKT;
-  const long long wp = (long long)a.Hkv * a.pt * kp, wsuf = (long long)a.B * a.Hkv * a.st * ks;
-  auto clampll = [](long long x, long long lo, long long hi) { return x < lo ? lo : x > hi ? hi : x; };
-  const long long even = (wp + wsuf + 3 * kSlots - 1) / (3 * kSlots);
-  long long pc = clampll(even, 4, 1 << 20), sc = clampll(even, 4, 64);
+  const long long kp = ((long long)a.P + kU - 1) / kU, ks = ((long long)a.M + kU - 1) / kU;
+  const int pw = a.ptile / 16, sw = a.stile / 16;
+  const long long wp = a.ptile == 256 ? 0 : (long long)a.Hkv * a.pt * kp * pw;
+  const long long wsuf = (long long)a.B * a.Hkv * a.st * ks * sw;
+  const long long items = 3ll * kSms * (p->d == 64 ? PCfg<64>::kCtas : PCfg<128>::kCtas);
+  const long long share = (wp + wsuf + items - 1) / items;
+  long long pc = std::max<long long>(8, share / pw);
+  const long long sc = std::max<long long>(4, share / sw);
   if (a.ptile == 256) {
-    // one CTA a SM: key splits such that one wave of 152 covers the heads and row tiles
-    const long long groups = (long long)a.Hkv * a.pt, splits = std::max<long long>(1, 152 / groups);
+    // one CTA a SM: key splits such that one wave covers the heads and row tiles
+    const long long groups = (long long)a.Hkv * a.pt, splits = std::max<long long>(1, kSms / groups);
     pc = 2 * std::max<long long>(1, ((kp + 1) / 2 + splits - 1) / splits);
-    sc = clampll((wsuf + 3 * kSlots - 1) / (3 * kSlots), 4, 64);
   }
-  if (a.ptile == 64) pc = std::max(pc, std::min<long long>(16, clampll(wp / kSlots, 4, 16)));
-  a.pchunk = (int)(pc * kKT);
-  a.schunk = (int)(sc * kKT);
+  a.pchunk = (int)(std::min<long long>(pc, 1 << 21) * kU);
+  a.schunk = (int)(std::min<long long>(sc, 1 << 21) * kU);
   a.np = (int)((a.P + (long long)a.pchunk - 1) / a.pchunk);
   a.ns = (int)((a.M + (long long)a.schunk - 1) / a.schunk);
   a.pitems = a.ptile == 256 ? 0 : a.Hkv * a.pt * a.np;
+  a.items = a.pitems + a.B * a.Hkv * a.st * a.ns;
   a.srow0 = (long long)a.np * a.Hkv * a.R;
 }
 
@@ -474,16 +640,17 @@ cudaError_t launch_p(const CUtensorMap (&m)[4], const PArgs& a, void* o, Strides
   auto kern = prefix_kernel<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D>::kBytes);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)a.pitems + (long long)a.B * a.Hkv * a.st * a.ns;
   if (a.ptile == 256 && (e = launch_prefix_tc(Cvt<T>::kAB ? FA_DT_BF16 : FA_DT_F16, D, m[0], m[1], a, s)) != cudaSuccess)
     return e;
-  if (items > 0) {
-    kern<<<(unsigned)items, kPThreads, PCfg<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], a);
+  if (a.items > 0) {
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min<long long>(a.items, (long long)PCfg<D>::kCtas * std::max(sms, 1));
+    kern<<<grid, kPThreads, PCfg<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const long long rows = (long long)a.B * a.H * a.T;
-  prefix_join_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, static_cast<T*>(o), os, lse);
-  return cudaGetLastError();
+  return a.np + a.ns <= 8 ? launch_join<T, D, 1>(a, o, os, lse, s) : launch_join<T, D, 4>(a, o, os, lse, s);
 }
 
 }  // namespace
@@ -507,7 +674,8 @@ cudaError_t launch_prefix(const fa_prefix_params* p, const CUtensorMap (&m)[4], 
   a.status = reinterpret_cast<int*>(ws + L.status);
   a.stat = reinterpret_cast<float4*>(ws + L.stat);
   a.part = reinterpret_cast<float*>(ws + L.part);
-  cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int), s);
+  a.sched = a.status + 1;
+  cudaError_t e = cudaMemsetAsync(a.status, 0, 2 * sizeof(int), s);
   if (e != cudaSuccess) return e;
   if (p->dtype == FA_DT_BF16)
     return p->d == 128 ? launch_p<__nv_bfloat16, 128>(m, a, o, os, lse, s) : launch_p<__nv_bfloat16, 64>(m, a, o, os, lse, s);

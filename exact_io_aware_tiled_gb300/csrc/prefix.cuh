@@ -4,17 +4,17 @@
 
 namespace fa {
 
-constexpr int kKT = 64;          // rows of the K / V maps' boxes; keys per stage of the register-product kernel
+constexpr int kKT = 32;          // rows of the K / V maps' boxes; keys per stage of the register-product kernel
 
 struct PArgs {
   int B, H, Hkv, T, G;         // G = H / Hkv
   int P, M;
   int R, r;                    // rows of a K/V head: B*G*T against the prefix, G*T against an own cache
-  int ptile, stile;            // row tiles: 16 or 64; the prefix also 256 (tensor-memory kernel)
+  int ptile, stile;            // row tiles: 16, 32 or 64; the prefix also 256 (tensor-memory kernel)
   int pt, st;                  // row tiles per head
   int pchunk, schunk;          // keys per split (multiples of 64, pchunk of 128 with 256-row tiles)
   int np, ns;                  // splits
-  int pitems;                  // prefix items of the launch
+  int pitems, items;           // prefix items and all items of prefix_kernel
   const void* q;
   Strides qs;
   const int32_t* lens;
@@ -23,6 +23,7 @@ struct PArgs {
   float4* stat;                // [rows]: max (log2), true sum, sum of the rounded weights
   long long srow0;             // first own-cache row of part / stat
   int* status;
+  int* sched;                  // work counter, cleared with the status word
 };
 
 // Query row `row` of the B*G*T rows that share K/V head hk.

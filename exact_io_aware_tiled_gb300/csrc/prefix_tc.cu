@@ -105,13 +105,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       if (lane == 0) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
-        // a tile is two 64-row boxes per 64 columns
+        // a tile is four 32-row boxes per 64 columns
         auto load = [&](int base, const CUtensorMap* m, uint64_t* bar, int row) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              tma_load_4d(smem + base + c * 16384 + hf * 8192, m, bar, c * 64, row + hf * 64, hk, 0);
+            for (int x = 0; x < kTile / kKT; ++x)
+              tma_load_4d(smem + base + c * 16384 + x * kKT * 128, m, bar, c * 64, row + x * kKT, hk, 0);
         };
         int nk = 0, nv = 0;
         for (int s = 0; s < n; ++s) {
