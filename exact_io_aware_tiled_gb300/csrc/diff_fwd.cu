@@ -15,14 +15,19 @@
 // clock and SM) and the latency of the chain S -> softmax -> P V within one
 // map; the two maps are independent chains and cover one another.
 //
-// Mapping.  One CTA = one 128-row query tile of one head pair; the two maps
-// take the places that two query tiles have in the d = 128 kernel (fwd_tc.cu):
+// Mapping.  An item is one 128-row query tile of one head pair; the two maps take
+// the places that two query tiles have in the d = 128 kernel (fwd_tc.cu):
 //   * warps 0-3 / 4-7: softmax of map 1 / 2, one thread per query row;
-//   * warp 8: TMA producer; a ring stage holds K_1, K_2 (16 KB each) and V
-//     (32 KB), so V crosses L2 -> shared memory once for both maps;
+//   * warp 8: claims items and streams them with TMA; a ring stage holds K_1, K_2
+//     (16 KB each) and V (32 KB), so V crosses L2 -> shared memory once for both
+//     maps; Q has two buffers, so the next item's Q, K, V and first scores are
+//     under way while this item's epilogue runs;
 //   * warp 9 issues S_1, S_2; warps 10 / 11 issue O_m += P_m V.
 // Tensor memory per map (256 columns): S 128 | O 128; P (16 bit) overwrites the
 // first 64 columns of S, so the next S of a map waits for its P V.
+// The CTAs are persistent, one on each SM: with one CTA per item the pipeline's
+// fill and drain took a third of the time at short causal rows (GPT-2-medium
+// width, B = 64, N = 1024: 362 us).
 // Epilogue: warpgroup x forms columns 64 x .. 64 x + 63 of O and O_2 for every
 // row from both accumulators (any warp of a lane quarter can read them), after
 // the row sums are exchanged through shared memory.
@@ -30,6 +35,8 @@
 // Keys behind seqlens_k[b] may hold anything, NaN included: their scores are
 // replaced, and their V rows are zeroed in shared memory before the product
 // (0 x NaN would not be 0).
+#include <algorithm>
+
 #include "row_softmax.cuh"
 
 namespace fa {
@@ -39,10 +46,10 @@ constexpr int kThreads = 384;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct DCfg {
-  static constexpr int NS = 3;                           // K / V stages
+  static constexpr int NS = 2;                           // K / V stages
   static constexpr int kTB = 16384;                      // one [128 rows][64 columns] box
-  static constexpr int kQ = 0;                           // Q_1, Q_2; the O boxes at the end
-  static constexpr int kK = 2 * kTB;                     // NS x (K_1, K_2); the O_2 boxes at the end
+  static constexpr int kQ = 0;                           // 2 x (Q_1, Q_2)
+  static constexpr int kK = 4 * kTB;                     // NS x (K_1, K_2)
   static constexpr int kV = kK + NS * 2 * kTB;           // NS x 2 boxes
   static constexpr int kInv = kV + NS * 2 * kTB;         // 2 x 128 floats: 1 / l_m of every row
   static constexpr int kBar = kInv + 1024;
@@ -51,20 +58,59 @@ struct DCfg {
 static_assert(DCfg::kBytes <= 232448, "shared memory over the per-block limit");
 
 struct DBars {
-  uint64_t q_full;
+  uint64_t item_full[2], item_empty[2];
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t done[3];
   uint64_t k_full[DCfg::NS], v_full[DCfg::NS], k_empty[DCfg::NS], v_empty[DCfg::NS];
+  uint64_t meet;
+  int item[2];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(DBars) <= 512, "barrier block overflows its shared-memory slot");
 
+// Item u: query tile qt of head pair h of batch b, and its key tiles lo .. lo + n - 1.
+struct FItem { int b, h, hk, qt, Lk, lo, n; };
+
+template <bool kWin>
+__device__ __forceinline__ FItem make_item(const DiffFwdArgs& a, int u) {
+  FItem it;
+  const int BH = a.B * a.H;
+  const int level = u / BH, bh = u - level * BH;
+  it.qt = a.nq - 1 - level;                    // heaviest tiles first
+  it.b = bh / a.H;
+  it.h = bh - it.b * a.H;
+  it.hk = it.h / a.group;
+  it.Lk = a.N;
+  if (a.seqlens_k != nullptr) it.Lk = max(0, min(a.N, a.seqlens_k[it.b]));
+  int lim = (it.Lk + kTile - 1) / kTile;
+  if (a.causal) lim = min(lim, it.qt + 1);
+  it.lo = kWin ? max(0, it.qt * kTile - a.window + 1) / kTile : 0;
+  it.n = max(0, lim - it.lo);
+  return it;
+}
+
+// 32 columns of one row: two 32-byte stores where the layout allows them
+template <typename T>
+__device__ __forceinline__ void store32(T* p, const uint32_t (&w)[16], int v8) {
+#pragma unroll
+  for (int c = 0; c < 16; c += 8) {
+    if (v8) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                   :: "l"(p + 2 * c), "r"(w[c]), "r"(w[c + 1]), "r"(w[c + 2]), "r"(w[c + 3]), "r"(w[c + 4]),
+                      "r"(w[c + 5]), "r"(w[c + 6]), "r"(w[c + 7]) : "memory");
+    } else {
+      reinterpret_cast<uint4*>(p + 2 * c)[0] = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+      reinterpret_cast<uint4*>(p + 2 * c)[1] = make_uint4(w[c + 4], w[c + 5], w[c + 6], w[c + 7]);
+    }
+  }
+}
+
 template <typename T, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                const __grid_constant__ CUtensorMap tmO2, const DiffFwdArgs a) {
+                const __grid_constant__ CUtensorMap tmV, const DiffFwdArgs a) {
   using C = DCfg;
   constexpr int NS = C::NS;
   constexpr int TB = C::kTB;
@@ -80,24 +126,15 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // ---- work item: (b, head pair, query tile); heaviest tiles launch first
-  const int BH = a.B * a.H;
-  const int qt = a.nq - 1 - (int)(blockIdx.x / BH);
-  const int bh = (int)(blockIdx.x % BH);
-  const int b = bh / a.H, h = bh % a.H;
-  const int hk = h / a.group;
-  int Lk = a.N;
-  if (a.seqlens_k != nullptr) Lk = max(0, min(a.N, a.seqlens_k[b]));
-  int lim = (Lk + kTile - 1) / kTile;
-  if (a.causal) lim = min(lim, qt + 1);
-  const int lo = kWin ? max(0, qt * kTile - a.window + 1) / kTile : 0;
-  const int n = max(0, lim - lo);              // key tiles lo .. lo + n - 1
-
+  const int total = a.nq * a.B * a.H;
   WaitCtl ctl{a.status, &bars->abort, kWaitSleepNs};
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->item_full[x], 1);
+      mbar_init(&bars->item_empty[x], 11);     // warps 0-7 and 9-11
+      mbar_init(&bars->q_full[x], 1);
+      mbar_init(&bars->q_empty[x], 1);
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_full[x], 128);
       mbar_init(&bars->pv_done[x], 1);
@@ -109,6 +146,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       mbar_init(&bars->k_empty[s], 1);
       mbar_init(&bars->v_empty[s], 2);
     }
+    mbar_init(&bars->meet, 256);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -121,105 +159,149 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   constexpr int ab = Cvt<T>::kAB;
+  volatile int* item_u = bars->item;
+  // the next item's index (all lanes of a warp together), or -1
+  int kc = 0;
+  auto fetch = [&]() -> int {
+    const int slot = kc & 1;
+    if (!warp_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl)) return -1;
+    const int u = item_u[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
+    ++kc;
+    return u;
+  };
   // Register split of the 384 x 168 launch budget, as in fwd_tc.cu:
   // 8 x 32 x 224 + 4 x 32 x 56 = 64512 = 384 x 168.
 
   if (warp >= 8) {
     regs_dec<56>();
     if (warp == 8) {
-      // ===================== TMA producer =====================
-      if (lane == 0 && n > 0) {
-        mbar_expect_tx(&bars->q_full, 2 * TB);
-        tma_load_4d(smem + C::kQ, &tmQ, &bars->q_full, 0, qt * kTile, 2 * h, b);
-        tma_load_4d(smem + C::kQ + TB, &tmQ, &bars->q_full, 0, qt * kTile, 2 * h + 1, b);
+      // ===================== items and TMA =====================
+      if (lane == 0) {
+        prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
+        int nk = 0, nv = 0, ni = 0;            // K and V stages and Q buffers loaded
         bool ok = true;
-        for (int s = 0; s < n && ok; ++s) {
-          const int st = s % NS;
-          const uint32_t ph = (uint32_t)(s / NS) & 1u;
-          const int row = (lo + s) * kTile;
-          // a stage's first use needs no wait
-          if (s >= NS && !(ok = mbar_wait(&bars->k_empty[st], ph ^ 1u, ctl))) break;
-          mbar_expect_tx(&bars->k_full[st], 2 * TB);
-          tma_load_4d(smem + C::kK + st * 2 * TB, &tmK, &bars->k_full[st], 0, row, 2 * hk, b);
-          tma_load_4d(smem + C::kK + st * 2 * TB + TB, &tmK, &bars->k_full[st], 0, row, 2 * hk + 1, b);
-          if (s >= NS && !(ok = mbar_wait(&bars->v_empty[st], ph ^ 1u, ctl))) {
-            // K of this step is in flight: it lands before the CTA leaves
-            mbar_wait(&bars->k_full[st], ph, ctl);
-            break;
+        // the first item is the CTA's own index, the others come from the counter
+        int u = (int)blockIdx.x;
+        for (int kf = 0; ok; ++kf, u = (int)gridDim.x + atomicAdd(a.sched, 1)) {
+          const int slot = kf & 1;
+          if (kf >= 2 && !(ok = mbar_wait(&bars->item_empty[slot], (uint32_t)((kf >> 1) - 1) & 1u, ctl))) break;
+          item_u[slot] = u < total ? u : -1;
+          mbar_arrive(&bars->item_full[slot]);
+          if (u >= total) break;
+          const FItem it = make_item<kWin>(a, u);
+          if (it.n == 0) continue;
+          const int qb = ni & 1;
+          if (ni >= 2 && !(ok = mbar_wait(&bars->q_empty[qb], (uint32_t)((ni >> 1) - 1) & 1u, ctl))) break;
+          mbar_expect_tx(&bars->q_full[qb], 2 * TB);
+          for (int x = 0; x < 2; ++x)
+            tma_load_4d(smem + C::kQ + (qb * 2 + x) * TB, &tmQ, &bars->q_full[qb], 0, it.qt * kTile, 2 * it.h + x, it.b);
+          ++ni;
+          for (int s = 0; s < it.n; ++s) {
+            const int st = nk % NS;
+            const uint32_t ph = (uint32_t)(nk / NS) & 1u;
+            const int row = (it.lo + s) * kTile;
+            // a stage's first use needs no wait
+            if (nk >= NS && !(ok = mbar_wait(&bars->k_empty[st], ph ^ 1u, ctl))) break;
+            mbar_expect_tx(&bars->k_full[st], 2 * TB);
+            for (int x = 0; x < 2; ++x)
+              tma_load_4d(smem + C::kK + (st * 2 + x) * TB, &tmK, &bars->k_full[st], 0, row, 2 * it.hk + x, it.b);
+            ++nk;
+            if (nv >= NS && !(ok = mbar_wait(&bars->v_empty[st], ph ^ 1u, ctl))) break;
+            mbar_expect_tx(&bars->v_full[st], 2 * TB);
+            for (int x = 0; x < 2; ++x)
+              tma_load_4d(smem + C::kV + (st * 2 + x) * TB, &tmV, &bars->v_full[st], 64 * x, row, it.hk, it.b);
+            ++nv;
           }
-          mbar_expect_tx(&bars->v_full[st], 2 * TB);
-          tma_load_4d(smem + C::kV + st * 2 * TB, &tmV, &bars->v_full[st], 0, row, hk, b);
-          tma_load_4d(smem + C::kV + st * 2 * TB + TB, &tmV, &bars->v_full[st], 64, row, hk, b);
         }
         // Before leaving, make sure no load is still writing shared memory.
-        for (int j = max(0, n - NS); j < n; ++j) {
-          mbar_wait(&bars->k_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
-          mbar_wait(&bars->v_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
-        }
-        mbar_wait(&bars->q_full, 0, ctl);
+        for (int j = max(0, nk - NS); j < nk; ++j) mbar_wait(&bars->k_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
+        for (int j = max(0, nv - NS); j < nv; ++j) mbar_wait(&bars->v_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
+        for (int j = max(0, ni - 2); j < ni; ++j) mbar_wait(&bars->q_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl);
       }
     } else if (warp == 9) {
       // ===================== S issuer (both maps) =====================
-      if (lane == 0 && n > 0) {
-        constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
-        const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
-        const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
-        bool ok = mbar_wait(&bars->q_full, 0, ctl);
-        for (int s = 0; s < n && ok; ++s) {
-          const int st = s % NS;
-          if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
+      constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
+      const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
+      int g = 0, ni = 0;                       // steps, items with steps
+      bool ok = true;
+      int u;
+      while (ok && (u = fetch()) >= 0) {
+        const FItem it = make_item<kWin>(a, u);
+        if (it.n == 0) continue;
+        if (lane == 0) {
+          const int qb = ni & 1;
+          ok = mbar_wait(&bars->q_full[qb], (uint32_t)(ni >> 1) & 1u, ctl);
+          for (int s = 0; s < it.n && ok; ++s, ++g) {
+            const int st = g % NS;
+            if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            // S_x(s) overwrites P_x(s-1) once P V_x(s-1) has read it
-            if (s > 0 && !(ok = mbar_wait(&bars->pv_done[x], (uint32_t)(s - 1) & 1u, ctl))) break;
-            tc_fence_after();
-            const uint64_t qd = qd0 + (uint64_t)((x * TB) >> 4);
-            const uint64_t kd = kd0 + (uint64_t)(((st * 2 + x) * TB) >> 4);
+            for (int x = 0; x < 2; ++x) {
+              // S_x(g) overwrites P_x(g-1) once P V_x(g-1) has read it
+              if (ok && g > 0) ok = mbar_wait(&bars->pv_done[x], (uint32_t)(g - 1) & 1u, ctl);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t qd = qd0 + (uint64_t)(((qb * 2 + x) * TB) >> 4);
+              const uint64_t kd = kd0 + (uint64_t)(((st * 2 + x) * TB) >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss(tmem + x * 256, qd + (uint64_t)((k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4), idS,
-                     k > 0 ? 1u : 0u);
-            mma_commit(&bars->s_full[x]);
+              for (int k = 0; k < 4; ++k)
+                mma_ss(tmem + x * 256, qd + (uint64_t)((k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4), idS,
+                       k > 0 ? 1u : 0u);
+              mma_commit(&bars->s_full[x]);
+            }
+            if (ok) mma_commit(&bars->k_empty[st]);
           }
-          if (ok) mma_commit(&bars->k_empty[st]);
+          if (ok) mma_commit(&bars->q_empty[qb]);
         }
+        ++ni;
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0) {
         mma_commit(&bars->done[0]);
         mbar_wait(&bars->done[0], 0, ctl);
       }
-    } else if (n > 0) {
+    } else {
       // ===================== P V issuer of map x (the whole warp walks the steps) =====================
       const int x = warp - 10;
       constexpr uint32_t idPV = idesc_f16(128, 128, ab, 0, 1);
       const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
       const uint32_t tP = tmem + x * 256, tO = tmem + x * 256 + 128;
+      int g = 0;
       bool ok = true;
-      for (int s = 0; s < n && ok; ++s) {
-        const int st = s % NS;
-        if (!(ok = warp_wait(&bars->v_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
-        const int live = Lk - (lo + s) * kTile;         // V rows of this tile that count
-        if (live < kTile) {
-          // both maps' issuers write the same zeros, each before its own product
-          uint8_t* vb = smem + C::kV + st * 2 * TB;
-          for (int o = live * 128 + lane * 16; o < TB; o += 512) {
-            *reinterpret_cast<uint4*>(vb + o) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(vb + TB + o) = make_uint4(0, 0, 0, 0);
+      int u;
+      while (ok && (u = fetch()) >= 0) {
+        const FItem it = make_item<kWin>(a, u);
+        for (int s = 0; s < it.n && ok; ++s, ++g) {
+          const int st = g % NS;
+          if (!(ok = warp_wait(&bars->v_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
+          const int live = it.Lk - (it.lo + s) * kTile;         // V rows of this tile that count
+          if (live < kTile) {
+            // both maps' issuers write the same zeros, each before its own product
+            uint8_t* vb = smem + C::kV + st * 2 * TB;
+            for (int o = live * 128 + lane * 16; o < TB; o += 512) {
+              *reinterpret_cast<uint4*>(vb + o) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(vb + TB + o) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          fence_proxy_async_smem();
+          // P_x(g) follows the softmax warps' reads of the last item's O
+          if (!(ok = warp_wait(&bars->p_full[x], (uint32_t)g & 1u, ctl))) break;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)((st * 2 * TB) >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tO, tP + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&bars->pv_done[x]);
+            mma_commit(&bars->v_empty[st]);
+          }
           __syncwarp();
         }
-        if (!(ok = warp_wait(&bars->p_full[x], (uint32_t)s & 1u, ctl))) break;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t vd = vd0 + (uint64_t)((st * 2 * TB) >> 4);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tO, tP + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || k > 0) ? 1u : 0u);
-          mma_commit(&bars->pv_done[x]);
-          mma_commit(&bars->v_empty[st]);
-        }
-        __syncwarp();
       }
       if (lane == 0) {
         mma_commit(&bars->done[1 + x]);
@@ -232,90 +314,88 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int x = warp >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;          // row within the tile = TMEM lane
-    const int i = qt * kTile + r;               // global query row
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + x * 256 + lane_off, tO = tS + 128;
     const float sl2 = a.scale_log2;
-    const int jmax = a.causal ? min(Lk - 1, i) : (Lk - 1);
-    const int jmin = kWin ? i - a.window + 1 : 0;
-
-    RowSoftmax w;
-    bool ok = true;
-    for (int s = 0; s < n; ++s) {
-      const int kv = lo + s;
-      if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)s & 1u, ctl))) break;
-      tc_fence_after();
-      w.template step<T, 128, kWin>(tS, tO, jmax - kv * kTile, jmin - kv * kTile, sl2, s == 0);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars->p_full[x]);
-    }
-
-    // ---- epilogue: O = O_1 / l_1 - lambda O_2 / l_2, columns 64 x .. of both tensors
     float* inv_sh = reinterpret_cast<float*>(smem + C::kInv);
-    inv_sh[x * 128 + r] = w.l_rnd > 0.f ? 1.f / w.l_rnd : 0.f;
-    // The last product of this warpgroup's own map; the other map may be phases
-    // behind, where a parity wait would pass at once, so its end is learned from
-    // the barrier both warpgroups meet at.
-    bool fin = ok;
-    if (ok && n > 0) {
-      fin = warp_wait(&bars->pv_done[x], (uint32_t)(n - 1) & 1u, ctl);
-      tc_fence_after();
-    }
-    tc_fence_before();
-    if (!named_bar_or(1, 256, !fin || bars->abort)) {
-      tc_fence_after();
-      const float inv1 = inv_sh[r], inv2 = inv_sh[128 + r];
-      const float lam = a.lam[h];
+    // barrier of both warpgroups (bounded, so that a warp that gave up leaves none behind)
+    GroupSync meet{&bars->meet, 0};
+    int g = 0;
+    bool ok = true;
+    int u;
+    while (ok && (u = fetch()) >= 0) {
+      const FItem it = make_item<kWin>(a, u);
+      const int i = it.qt * kTile + r;          // global query row
+      const int jmax = a.causal ? min(it.Lk - 1, i) : (it.Lk - 1);
+      const int jmin = kWin ? i - a.window + 1 : 0;
+      RowSoftmax w;
+      for (int s = 0; s < it.n; ++s, ++g) {
+        const int kv = it.lo + s;
+        if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)g & 1u, ctl))) break;
+        tc_fence_after();
+        w.template step<T, 128, kWin>(tS, tO, jmax - kv * kTile, jmin - kv * kTile, sl2, s == 0);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[x]);
+      }
+      if (!ok) break;
+      // ---- epilogue: O = O_1 / l_1 - lambda O_2 / l_2, columns 64 x .. of both tensors
       const bool row_ok = i < a.N;
+      const size_t orow = (size_t)it.b * a.ost.b + (size_t)it.h * a.ost.h + (size_t)i * a.ost.n + x * 64;
+      T* op = static_cast<T*>(a.o) + orow;
+      T* op2 = static_cast<T*>(a.o2) + orow;
+      float inv1 = 0.f, inv2 = 0.f;
+      if (it.n > 0) {
+        inv_sh[x * 128 + r] = w.l_rnd > 0.f ? 1.f / w.l_rnd : 0.f;
+        // The last product of this warpgroup's own map; the other map may be
+        // phases behind, where a parity wait would pass at once, so its end is
+        // learned from the barrier both warpgroups meet at.
+        if (!(ok = warp_wait(&bars->pv_done[x], (uint32_t)(g - 1) & 1u, ctl))) break;
+        tc_fence_after();
+        tc_fence_before();
+        if (!(ok = __all_sync(0xffffffffu, meet.sync(ctl)))) break;
+        tc_fence_after();
+        inv1 = inv_sh[r];
+        inv2 = inv_sh[128 + r];
+      }
+      const float lam = a.lam[it.h];
       const uint32_t t1 = tmem + lane_off + 128 + x * 64, t2 = t1 + 256;
-      uint8_t* ob = smem + C::kQ + x * TB;       // Q and K are dead once every product is done
-      uint8_t* ob2 = smem + C::kK + x * TB;
-#pragma unroll 1
+#pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float o[32], o2[32];
-        if (n > 0) {
-          uint32_t r1[32], r2[32];
+        uint32_t r1[32], r2[32];
+        if (it.n > 0) {
           tmem_ld32(t1 + hf * 32, r1);
           tmem_ld32(t2 + hf * 32, r2);
           tmem_wait_ld();
           reg_fence32(r1);
           reg_fence32(r2);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            o2[c] = __uint_as_float(r2[c]) * inv2;
-            o[c] = __uint_as_float(r1[c]) * inv1 - lam * o2[c];
-          }
         } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = o2[c] = 0.f;
+          for (int c = 0; c < 32; ++c) r1[c] = r2[c] = 0u;
         }
+        uint32_t w1[16], w2[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t u[4], u2[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            u[t] = Cvt<T>::pack(o[j * 8 + 2 * t], o[j * 8 + 2 * t + 1]);
-            u2[t] = Cvt<T>::pack(o2[j * 8 + 2 * t], o2[j * 8 + 2 * t + 1]);
-          }
-          const uint32_t off = r * 128 + ((((hf * 4 + j) ^ r) & 7) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                       :: "r"(smem_u32(ob + off)), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
-          if (a.has_o2)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(smem_u32(ob2 + off)), "r"(u2[0]), "r"(u2[1]), "r"(u2[2]), "r"(u2[3]) : "memory");
+        for (int c = 0; c < 16; ++c) {
+          const float a2 = __uint_as_float(r2[2 * c]) * inv2, b2 = __uint_as_float(r2[2 * c + 1]) * inv2;
+          w1[c] = Cvt<T>::pack(__uint_as_float(r1[2 * c]) * inv1 - lam * a2,
+                               __uint_as_float(r1[2 * c + 1]) * inv1 - lam * b2);
+          w2[c] = Cvt<T>::pack(a2, b2);
+        }
+        if (hf == 1 && it.n > 0) {
+          // both accumulators are read: the next item's products may overwrite
+          // them once every thread of both warpgroups is here
+          tc_fence_before();
+          if (!(ok = __all_sync(0xffffffffu, meet.sync(ctl)))) break;
+        }
+        if (row_ok) {
+          store32(op + hf * 32, w1, a.o_v8);
+          if (a.o2 != nullptr) store32(op2 + hf * 32, w2, a.o_v8);
         }
       }
-      fence_proxy_async_smem();
-      named_bar_sync(2 + x, 128);
-      if (r == 0) {
-        tma_store_4d(&tmO, ob, x * 64, qt * kTile, h, b);
-        if (a.has_o2) tma_store_4d(&tmO2, ob2, x * 64, qt * kTile, h, b);
-        bulk_commit();
-        bulk_wait_read0();
-      }
+      if (!ok) break;
       if (row_ok)
-        a.lse[((size_t)b * 2 * a.H + 2 * h + x) * a.N + i] = w.l_true > 0.f ? (w.m_run + lg2(w.l_true)) * kLn2 : -INFINITY;
+        a.lse[((size_t)it.b * 2 * a.H + 2 * it.h + x) * a.N + i] =
+            w.l_true > 0.f ? (w.m_run + lg2(w.l_true)) * kLn2 : -INFINITY;
     }
   }
 
@@ -328,23 +408,26 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 }
 
 template <typename T, bool kWin>
-cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
-                     const CUtensorMap& o2, const DiffFwdArgs& a, cudaStream_t s) {
+cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const DiffFwdArgs& a,
+                     cudaStream_t s) {
   auto kern = diff_fwd_kernel<T, kWin>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DCfg::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.nq * a.B * a.H), kThreads, DCfg::kBytes, s>>>(q, k, v, o, o2, a);
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const long long total = (long long)a.nq * a.B * a.H;
+  kern<<<(unsigned)std::min<long long>(total, std::max(sms, 1)), kThreads, DCfg::kBytes, s>>>(q, k, v, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_diff_fwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const CUtensorMap& o, const CUtensorMap& o2, const DiffFwdArgs& a, cudaStream_t s) {
+                            const DiffFwdArgs& a, cudaStream_t s) {
   if (dtype == FA_DT_BF16)
-    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, o, o2, a, s)
-                        : launch_t<__nv_bfloat16, false>(q, k, v, o, o2, a, s);
-  return a.window > 0 ? launch_t<__half, true>(q, k, v, o, o2, a, s) : launch_t<__half, false>(q, k, v, o, o2, a, s);
+    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, a, s) : launch_t<__nv_bfloat16, false>(q, k, v, a, s);
+  return a.window > 0 ? launch_t<__half, true>(q, k, v, a, s) : launch_t<__half, false>(q, k, v, a, s);
 }
 
 }  // namespace fa
