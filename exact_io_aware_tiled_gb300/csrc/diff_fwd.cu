@@ -23,8 +23,12 @@
 //     maps; Q has two buffers, so the next item's Q, K, V and first scores are
 //     under way while this item's epilogue runs;
 //   * warp 9 issues S_1, S_2; warps 10 / 11 issue O_m += P_m V.
-// Tensor memory per map (256 columns): S 128 | O 128; P (16 bit) overwrites the
-// first 64 columns of S, so the next S of a map waits for its P V.
+// Tensor memory per map (256 columns): S 128 | O 128.  There is no room for P
+// beside S, so P (16 bit) overwrites S and the next S must wait for the product
+// that reads P: with whole 128-key tiles that makes one serial chain S -> softmax
+// -> P V per map (324 us at the size below).  The tile is therefore worked in two
+// halves of 64 keys with a place each, (S | P over it) 64 columns: while the
+// softmax works on one half, the other half's P V and next S run.
 // The CTAs are persistent, one on each SM: with one CTA per item the pipeline's
 // fill and drain took a third of the time at short causal rows (GPT-2-medium
 // width, B = 64, N = 1024: 362 us).
@@ -60,7 +64,7 @@ static_assert(DCfg::kBytes <= 232448, "shared memory over the per-block limit");
 struct DBars {
   uint64_t item_full[2], item_empty[2];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [map][half]
   uint64_t done[3];
   uint64_t k_full[DCfg::NS], v_full[DCfg::NS], k_empty[DCfg::NS], v_empty[DCfg::NS];
   uint64_t meet;
@@ -135,9 +139,11 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       mbar_init(&bars->item_empty[x], 11);     // warps 0-7 and 9-11
       mbar_init(&bars->q_full[x], 1);
       mbar_init(&bars->q_empty[x], 1);
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], 128);
-      mbar_init(&bars->pv_done[x], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&bars->s_full[x][j], 1);
+        mbar_init(&bars->p_full[x][j], 128);
+        mbar_init(&bars->pv_done[x][j], 1);
+      }
     }
     for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
     for (int s = 0; s < NS; ++s) {
@@ -224,7 +230,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
     } else if (warp == 9) {
       // ===================== S issuer (both maps) =====================
-      constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
+      constexpr uint32_t idS = idesc_f16(128, 64, ab, 0, 0);
       const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
       const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
       int g = 0, ni = 0;                       // steps, items with steps
@@ -240,18 +246,19 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int st = g % NS;
             if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // S_x(g) overwrites P_x(g-1) once P V_x(g-1) has read it
-              if (ok && g > 0) ok = mbar_wait(&bars->pv_done[x], (uint32_t)(g - 1) & 1u, ctl);
+            for (int jx = 0; jx < 4; ++jx) {
+              const int j = jx >> 1, x = jx & 1;       // half by half, map by map
+              // S_xj(g) overwrites P_xj(g-1) once its product has read it
+              if (ok && g > 0) ok = mbar_wait(&bars->pv_done[x][j], (uint32_t)(g - 1) & 1u, ctl);
               if (!ok) break;
               tc_fence_after();
               const uint64_t qd = qd0 + (uint64_t)(((qb * 2 + x) * TB) >> 4);
-              const uint64_t kd = kd0 + (uint64_t)(((st * 2 + x) * TB) >> 4);
+              const uint64_t kd = kd0 + (uint64_t)(((st * 2 + x) * TB + j * 8192) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ss(tmem + x * 256, qd + (uint64_t)((k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4), idS,
+                mma_ss(tmem + x * 256 + j * 64, qd + (uint64_t)((k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4), idS,
                        k > 0 ? 1u : 0u);
-              mma_commit(&bars->s_full[x]);
+              mma_commit(&bars->s_full[x][j]);
             }
             if (ok) mma_commit(&bars->k_empty[st]);
           }
@@ -289,16 +296,20 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             fence_proxy_async_smem();
             __syncwarp();
           }
-          // P_x(g) follows the softmax warps' reads of the last item's O
-          if (!(ok = warp_wait(&bars->p_full[x], (uint32_t)g & 1u, ctl))) break;
-          if (lane == 0) {
-            tc_fence_after();
-            const uint64_t vd = vd0 + (uint64_t)((st * 2 * TB) >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ts(tO, tP + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || k > 0) ? 1u : 0u);
-            mma_commit(&bars->pv_done[x]);
-            mma_commit(&bars->v_empty[st]);
+          for (int j = 0; j < 2; ++j) {
+            // P_xj(g) follows the softmax warps' reads of the last item's O
+            if (ok) ok = warp_wait(&bars->p_full[x][j], (uint32_t)g & 1u, ctl);
+            if (!ok) break;
+            if (lane == 0) {
+              tc_fence_after();
+              const uint64_t vd = vd0 + (uint64_t)((st * 2 * TB + j * 8192) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tO, tP + j * 64 + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || j > 0 || k > 0) ? 1u : 0u);
+              mma_commit(&bars->pv_done[x][j]);
+              if (j == 1) mma_commit(&bars->v_empty[st]);
+            }
           }
           __syncwarp();
         }
@@ -331,12 +342,25 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       RowSoftmax w;
       for (int s = 0; s < it.n; ++s, ++g) {
         const int kv = it.lo + s;
-        if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)g & 1u, ctl))) break;
-        tc_fence_after();
-        w.template step<T, 128, kWin>(tS, tO, jmax - kv * kTile, jmin - kv * kTile, sl2, s == 0);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[x]);
+#pragma unroll 1
+        for (int j = 0; j < 2 && ok; ++j) {
+          if (!(ok = warp_wait(&bars->s_full[x][j], (uint32_t)g & 1u, ctl))) break;
+          tc_fence_after();
+          // the last product into O: the other half's, of this tile or the one before
+          auto o_ready = [&]() -> bool {
+            const bool done = warp_wait(&bars->pv_done[x][j ^ 1], (uint32_t)(j ? g : g - 1) & 1u, ctl);
+            tc_fence_after();
+            return done;
+          };
+          const int key0 = kv * kTile + j * 64;
+          if (!(ok = w.template step<T, 64, 128, kWin>(tS + j * 64, tO, jmax - key0, jmin - key0, sl2, s == 0 && j == 0,
+                                                       o_ready)))
+            break;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[x][j]);
+        }
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- epilogue: O = O_1 / l_1 - lambda O_2 / l_2, columns 64 x .. of both tensors
@@ -350,7 +374,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // The last product of this warpgroup's own map; the other map may be
         // phases behind, where a parity wait would pass at once, so its end is
         // learned from the barrier both warpgroups meet at.
-        if (!(ok = warp_wait(&bars->pv_done[x], (uint32_t)(g - 1) & 1u, ctl))) break;
+        if (!(ok = warp_wait(&bars->pv_done[x][1], (uint32_t)(g - 1) & 1u, ctl))) break;
         tc_fence_after();
         tc_fence_before();
         if (!(ok = __all_sync(0xffffffffu, meet.sync(ctl)))) break;

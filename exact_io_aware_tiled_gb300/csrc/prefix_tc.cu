@@ -210,7 +210,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       for (int s = 0; s < n; ++s) {
         if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)s & 1u, ctl))) break;
         tc_fence_after();
-        w.template step<T, D, false>(tS, tO, a.P - 1 - (k0 + s * kTile), 0, a.scale_log2, s == 0);
+        // S(s) exists, so P V(s-1) is done
+        w.template step<T, 128, D, false>(tS, tO, a.P - 1 - (k0 + s * kTile), 0, a.scale_log2, s == 0,
+                                          [] { return true; });
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars->p_full[x]);

@@ -1,4 +1,4 @@
-// row_softmax.cuh -- one step of the online softmax on a 128 x 128 score tile in
+// row_softmax.cuh -- one step of the online softmax on a score tile of 128 rows in
 // tensor memory, one thread per query row (= tensor-memory lane).  Shared by the
 // forward kernels whose P lies over S (differential attention, shared prefix).
 #pragma once
@@ -18,22 +18,24 @@ struct RowSoftmax {
   float m_run = -INFINITY;                // reference maximum, log2 units
   float l_true = 0.f, l_rnd = 0.f;        // sums of the unrounded and of the rounded weights
 
-  // S of this row (128 columns from tS) -> P in 16 bits over its first 64
+  // S of this row (NC columns from tS) -> P in 16 bits over its first NC / 2
   // columns; O (OC columns from tO) rescaled where the reference maximum moved.
   // Columns c > jl are hidden, with kWin also c < jlo.  `first`: O holds
-  // nothing yet.  The caller has waited for S (which implies that the previous
-  // P V is done) and calls tmem_wait_st, a fence and the arrival afterwards.
-  template <typename T, int OC, bool kWin>
-  __device__ __forceinline__ void step(uint32_t tS, uint32_t tO, int jl, int jlo, float sl2, bool first) {
-    uint32_t sr[4][32];
+  // nothing yet.  The caller has waited for S; o_ready() returns once the last
+  // product into O is done (false: gave up).  The caller calls tmem_wait_st, a
+  // fence and the arrival afterwards.
+  template <typename T, int NC, int OC, bool kWin, typename Ready>
+  __device__ __forceinline__ bool step(uint32_t tS, uint32_t tO, int jl, int jlo, float sl2, bool first,
+                                       Ready&& o_ready) {
+    uint32_t sr[NC / 32][32];
 #pragma unroll
-    for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, sr[cc]);
+    for (int cc = 0; cc < NC / 32; ++cc) tmem_ld32(tS + cc * 32, sr[cc]);
     tmem_wait_ld();
 #pragma unroll
-    for (int cc = 0; cc < 4; ++cc) reg_fence32(sr[cc]);
-    if (jl < kTile - 1 || (kWin && jlo > 0)) {
+    for (int cc = 0; cc < NC / 32; ++cc) reg_fence32(sr[cc]);
+    if (jl < NC - 1 || (kWin && jlo > 0)) {
 #pragma unroll
-      for (int c = 0; c < 128; ++c)
+      for (int c = 0; c < NC; ++c)
         if (c > jl || (kWin && c < jlo)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
     }
     // row max: 8 independent chains of 3-input max, then a short tree
@@ -41,12 +43,12 @@ struct RowSoftmax {
 #pragma unroll
     for (int t = 0; t < 8; ++t) m8[t] = __uint_as_float(sr[0][t]);
 #pragma unroll
-    for (int c = 8; c < 128; c += 16) {
+    for (int c = 8; c < NC; c += 16) {
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const int c0 = c + t, c1 = c + 8 + t;
-        m8[t] = (c1 < 128) ? max3f(m8[t], __uint_as_float(sr[c0 >> 5][c0 & 31]), __uint_as_float(sr[c1 >> 5][c1 & 31]))
-                           : fmaxf(m8[t], __uint_as_float(sr[c0 >> 5][c0 & 31]));
+        m8[t] = (c1 < NC) ? max3f(m8[t], __uint_as_float(sr[c0 >> 5][c0 & 31]), __uint_as_float(sr[c1 >> 5][c1 & 31]))
+                          : fmaxf(m8[t], __uint_as_float(sr[c0 >> 5][c0 & 31]));
       }
     }
     const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * sl2;
@@ -65,7 +67,7 @@ struct RowSoftmax {
     // of V rows.
     float lt[4] = {0.f, 0.f, 0.f, 0.f}, lr[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < NC / 64; ++hf) {
       uint32_t pk[32];
 #pragma unroll
       for (int c2 = 0; c2 < 64; c2 += 2) {
@@ -87,6 +89,7 @@ struct RowSoftmax {
     // tcgen05.ld / st are warp-collective: the warp rescales together when any
     // of its rows needs it (alpha is exactly 1 for the others)
     if (__any_sync(0xffffffffu, moved && !first)) {
+      if (!o_ready()) return false;
 #pragma unroll
       for (int hf = 0; hf < OC / 32; ++hf) {
         uint32_t o[32];
@@ -98,6 +101,7 @@ struct RowSoftmax {
         tmem_st32(tO + hf * 32, o);
       }
     }
+    return true;
   }
 };
 

@@ -3,8 +3,9 @@
 Forward (csrc/diff_fwd.cu): persistent CTAs, an item is one query tile with two
 score maps.  A stage holds the K tiles of both maps (released by the S issuer)
 and one V tile (released by both P V issuers); a stage's first use skips the
-empty waits; S_x(g) waits for P V_x(g-1), because P_x lies over S_x; the two
-softmax groups meet before and after they read both accumulators.
+empty waits; a tile is worked in two halves with a place each for S and, over it,
+P, so S_xj(g) waits for P V_xj(g-1); O is rescaled after the other half's product;
+the two softmax groups meet before and after they read both accumulators.
 
 Backward (csrc/diff_bwd.cu): the roles of the d = 128 backward with a two-stage
 Q / dO ring, and W^T over S_1^T: the S issuer waits for dV(g-1) before S_1(g),
@@ -33,12 +34,13 @@ class Forward:
         self.item_full = [B("item_full%d" % i, 1) for i in range(2)]
         self.item_empty = [B("item_empty%d" % i, 5) for i in range(2)]      # S, two P V issuers, two softmax groups
         self.q_full, self.q_empty = ([B("q_%s%d" % (n, i), 1) for i in range(2)] for n in ("full", "empty"))
-        self.s_full, self.p_full, self.pv_done = ([B("%s%d" % (n, x), 1) for x in range(2)]
+        self.s_full, self.p_full, self.pv_done = ([[B("%s%d%d" % (n, x, j), 1) for j in range(2)] for x in range(2)]
                                                   for n in ("s_full", "p_full", "pv_done"))
         self.k_full, self.v_full, self.k_empty = ([B("%s%d" % (n, i), 1) for i in range(NS)]
                                                   for n in ("k_full", "v_full", "k_empty"))
         self.v_empty = [B("v_empty%d" % i, 1 if plant == "v_one_reader" else 2) for i in range(NS)]
         self.meet = B("meet", 2)
+        self.seed, self.issued = rng.randrange(1 << 30), [0, 0]
         self.mailbox = [None, None]
         self.reading = [False, False]      # a softmax group is reading both accumulators
         self.nloads = 0
@@ -71,7 +73,7 @@ class Forward:
                 if g >= NS:
                     yield ("wait", self.v_empty[st], g // NS - 1)
                 for x in range(2):
-                    if g >= NS and self.pv_done[x].completed < g - NS + 1:
+                    if g >= NS and self.pv_done[x][1].completed < g - NS + 1:
                         raise ProtocolError("V of step %d refilled before map %d read it" % (g - NS, x))
                 self.load(self.v_full[st])
                 g += 1
@@ -101,12 +103,13 @@ class Forward:
             yield ("wait", self.q_full[ni & 1], ni >> 1)
             for _ in range(self.items[u]):
                 yield ("wait", self.k_full[g % NS], g // NS)
-                for x in range(2):
-                    if g > 0 and self.plant != "s_ungated":
-                        yield ("wait", self.pv_done[x], g - 1)
-                    if self.pv_done[x].completed < g:
-                        raise ProtocolError("S_%d(%d) written over P that its product still reads" % (x, g))
-                    self.engine.later("S", self.s_full[x])
+                for j in range(2):
+                    for x in range(2):
+                        if g > 0 and self.plant != "s_ungated":
+                            yield ("wait", self.pv_done[x][j], g - 1)
+                        if self.pv_done[x][j].completed < g:
+                            raise ProtocolError("S_%d(%d) written over P that its product still reads" % (x, g))
+                        self.engine.later("S", self.s_full[x][j])
                 self.engine.later("S", self.k_empty[g % NS])
                 g += 1
             self.engine.later("S", self.q_empty[ni & 1])
@@ -121,30 +124,39 @@ class Forward:
                 return
             for s in range(self.items[u]):
                 yield ("wait", self.v_full[g % NS], g // NS)
-                yield ("wait", self.p_full[x], g)
-                if any(self.reading):
-                    raise ProtocolError("P V_%d(%d) issued while the last O is being read" % (x, g))
-                self.engine.later("PV%d" % x, self.pv_done[x])
+                for j in range(2):
+                    yield ("wait", self.p_full[x][j], g)
+                    if any(self.reading):
+                        raise ProtocolError("P V_%d(%d) issued while the last O is being read" % (x, g))
+                    self.issued[x] += 1
+                    self.engine.later("PV%d" % x, self.pv_done[x][j])
                 self.engine.later("PV%d" % x, self.v_empty[g % NS])
                 g += 1
 
     def softmax(self, x):
         g = kc = nm = 0
+        rng = random.Random(self.seed + x)
         while True:
             u = yield from self.fetch(kc)
             kc += 1
             if u < 0:
                 return
             for s in range(self.items[u]):
-                yield ("wait", self.s_full[x], g)
-                self.p_full[x].arrive()
+                for j in range(2):
+                    yield ("wait", self.s_full[x][j], g)
+                    if (s > 0 or j > 0) and rng.random() < 0.5:      # the reference maximum moved: O is rescaled
+                        if self.plant != "rescale_ungated":
+                            yield ("wait", self.pv_done[x][j ^ 1], g if j else g - 1)
+                        if self.pv_done[x][0].completed + self.pv_done[x][1].completed < self.issued[x]:
+                            raise ProtocolError("O_%d rescaled under a product" % x)
+                    self.p_full[x][j].arrive()
                 g += 1
             if self.items[u] == 0:
                 continue
             # the last product of the group's own map; the other's may be
             # phases behind, so it is learned from the barrier of both groups
             y = 1 - x if self.plant == "waits_for_other_map" else x
-            yield ("wait", self.pv_done[y], g - 1)
+            yield ("wait", self.pv_done[y][1], g - 1)
             self.meet.arrive()
             yield ("wait", self.meet, nm)
             nm += 1
@@ -167,7 +179,8 @@ def test_forward_protocol():
         Forward([rng.choice([0, 1, 1, 2, 3, 5, 9]) for _ in range(rng.randrange(0, 8))], random.Random(rng.random())).run()
 
 
-@pytest.mark.parametrize("plant", ["v_one_reader", "s_ungated", "waits_for_other_map", "no_second_meet"])
+@pytest.mark.parametrize("plant", ["v_one_reader", "s_ungated", "waits_for_other_map", "no_second_meet",
+                                   "rescale_ungated"])
 def test_forward_planted_mistakes_are_caught(plant):
     rng = random.Random(3)
     for _ in range(400):
