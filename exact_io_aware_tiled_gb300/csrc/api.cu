@@ -660,20 +660,18 @@ fa_status fa_diff_fwd(const fa_diff_params* p, const void* q, const void* k, con
   a.seqlens_k = p->seqlens_k;
   a.lam = p->lam;
   a.lse = lse;
-  a.o = o;
-  a.o2 = o2;
-  a.ost = sd.o;
-  a.o_v8 = ((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(o2)) & 31u) == 0 &&
-           (sd.o.n | sd.o.h | sd.o.b) % 16 == 0;
+  a.has_o2 = o2 != nullptr ? 1 : 0;
   a.status = reinterpret_cast<int*>(w + L.status);
   a.sched = a.status + 1;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo, mo2;
   if ((s = diff_map(&mq, q, p, 2 * p->H, 64, sd.q, kTile)) != FA_OK ||
       (s = diff_map(&mk, k, p, 2 * hkv, 64, sd.k, kTile)) != FA_OK ||
-      (s = diff_map(&mv, v, p, hkv, 128, sd.v, kTile)) != FA_OK)
+      (s = diff_map(&mv, v, p, hkv, 128, sd.v, kTile)) != FA_OK ||
+      (s = diff_map(&mo, o, p, p->H, 128, sd.o, kTile)) != FA_OK ||
+      (s = diff_map(&mo2, o2 != nullptr ? o2 : o, p, p->H, 128, sd.o, kTile)) != FA_OK)
     return s;
   if (cudaMemsetAsync(a.status, 0, 2 * sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
-  return cuda_status(launch_diff_fwd(p->dtype, mq, mk, mv, a, st));
+  return cuda_status(launch_diff_fwd(p->dtype, mq, mk, mv, mo, mo2, a, st));
 }
 
 fa_status fa_diff_bwd(const fa_diff_params* p, const void* q, const void* k, const void* v, const void* o,

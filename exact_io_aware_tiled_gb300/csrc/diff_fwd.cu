@@ -20,21 +20,18 @@
 //   * warps 0-3 / 4-7: softmax of map 1 / 2, one thread per query row;
 //   * warp 8: claims items and streams them with TMA; a ring stage holds K_1, K_2
 //     (16 KB each) and V (32 KB), so V crosses L2 -> shared memory once for both
-//     maps; Q has two buffers, so the next item's Q, K, V and first scores are
-//     under way while this item's epilogue runs;
+//     maps; the next item's Q, K, V and first scores are under way while this
+//     item's epilogue runs;
 //   * warp 9 issues S_1, S_2; warps 10 / 11 issue O_m += P_m V.
-// Tensor memory per map (256 columns): S 128 | O 128.  There is no room for P
-// beside S, so P (16 bit) overwrites S and the next S must wait for the product
-// that reads P: with whole 128-key tiles that makes one serial chain S -> softmax
-// -> P V per map (324 us at the size below).  The tile is therefore worked in two
-// halves of 64 keys with a place each, (S | P over it) 64 columns: while the
-// softmax works on one half, the other half's P V and next S run.
-// The CTAs are persistent, one on each SM: with one CTA per item the pipeline's
-// fill and drain took a third of the time at short causal rows (GPT-2-medium
-// width, B = 64, N = 1024: 362 us).
+// Key tiles are worked in two halves of 64 keys; row_softmax.cuh says where S, P
+// and O lie.  Measured at GPT-2-medium width (B = 64, N = 1024, causal, bf16): one
+// CTA per item, whole tiles with P over S (the next S waits for the product that
+// reads P) 362 us; persistent CTAs, one on each SM, 324; 64-key halves with P over
+// S 292; P through shared memory 312 (the store and its proxy fence cost the
+// softmax warps more than the shorter chain gains).
 // Epilogue: warpgroup x forms columns 64 x .. 64 x + 63 of O and O_2 for every
 // row from both accumulators (any warp of a lane quarter can read them), after
-// the row sums are exchanged through shared memory.
+// the row sums are exchanged through shared memory; both leave as TMA stores.
 //
 // Keys behind seqlens_k[b] may hold anything, NaN included: their scores are
 // replaced, and their V rows are zeroed in shared memory before the product
@@ -52,30 +49,34 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct DCfg {
   static constexpr int NS = 2;                           // K / V stages
   static constexpr int kTB = 16384;                      // one [128 rows][64 columns] box
-  static constexpr int kQ = 0;                           // 2 x (Q_1, Q_2)
-  static constexpr int kK = 4 * kTB;                     // NS x (K_1, K_2)
+  static constexpr int kQ = 0;                           // Q_1, Q_2
+  static constexpr int kK = 2 * kTB;                     // NS x (K_1, K_2)
   static constexpr int kV = kK + NS * 2 * kTB;           // NS x 2 boxes
-  static constexpr int kInv = kV + NS * 2 * kTB;         // 2 x 128 floats: 1 / l_m of every row
-  static constexpr int kBar = kInv + 1024;
+  static constexpr int kO = kV + NS * 2 * kTB;           // O's two boxes, then O_2's
+  static constexpr int kInv = kO + 4 * kTB;              // 2 x 128 floats: 1 / l_m of every row
+  static constexpr int kItem = kInv + 1024;              // the two published items
+  static constexpr int kBar = kItem + 64;
   static constexpr int kBytes = kBar + 512;
 };
 static_assert(DCfg::kBytes <= 232448, "shared memory over the per-block limit");
 
 struct DBars {
   uint64_t item_full[2], item_empty[2];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [map][half]
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], s_free[2];                         // [map]
+  uint64_t p_full[2][2], pv_done[2][2];                  // [map][half]
   uint64_t done[3];
   uint64_t k_full[DCfg::NS], v_full[DCfg::NS], k_empty[DCfg::NS], v_empty[DCfg::NS];
-  uint64_t meet;
-  int item[2];
+  uint64_t meet, meet_x[2];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(DBars) <= 512, "barrier block overflows its shared-memory slot");
 
-// Item u: query tile qt of head pair h of batch b, and its key tiles lo .. lo + n - 1.
-struct FItem { int b, h, hk, qt, Lk, lo, n; };
+// Query tile qt of head pair h of batch b, and its key tiles lo .. lo + n - 1
+// (n = -1: no more items).
+struct FItem { int b, h, hk, qt, Lk, lo, n; float lam; };
+static_assert(sizeof(FItem) == 32, "an item overflows its mailbox slot");
 
 template <bool kWin>
 __device__ __forceinline__ FItem make_item(const DiffFwdArgs& a, int u) {
@@ -92,29 +93,15 @@ __device__ __forceinline__ FItem make_item(const DiffFwdArgs& a, int u) {
   if (a.causal) lim = min(lim, it.qt + 1);
   it.lo = kWin ? max(0, it.qt * kTile - a.window + 1) / kTile : 0;
   it.n = max(0, lim - it.lo);
+  it.lam = a.lam[it.h];
   return it;
-}
-
-// 32 columns of one row: two 32-byte stores where the layout allows them
-template <typename T>
-__device__ __forceinline__ void store32(T* p, const uint32_t (&w)[16], int v8) {
-#pragma unroll
-  for (int c = 0; c < 16; c += 8) {
-    if (v8) {
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                   :: "l"(p + 2 * c), "r"(w[c]), "r"(w[c + 1]), "r"(w[c + 2]), "r"(w[c + 3]), "r"(w[c + 4]),
-                      "r"(w[c + 5]), "r"(w[c + 6]), "r"(w[c + 7]) : "memory");
-    } else {
-      reinterpret_cast<uint4*>(p + 2 * c)[0] = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
-      reinterpret_cast<uint4*>(p + 2 * c)[1] = make_uint4(w[c + 4], w[c + 5], w[c + 6], w[c + 7]);
-    }
-  }
 }
 
 template <typename T, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const DiffFwdArgs a) {
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                const __grid_constant__ CUtensorMap tmO2, const DiffFwdArgs a) {
   using C = DCfg;
   constexpr int NS = C::NS;
   constexpr int TB = C::kTB;
@@ -134,16 +121,18 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   WaitCtl ctl{a.status, &bars->abort, kWaitSleepNs};
 
   if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->item_full[x], 1);
       mbar_init(&bars->item_empty[x], 11);     // warps 0-7 and 9-11
-      mbar_init(&bars->q_full[x], 1);
-      mbar_init(&bars->q_empty[x], 1);
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->s_free[x], 128);
       for (int j = 0; j < 2; ++j) {
-        mbar_init(&bars->s_full[x][j], 1);
         mbar_init(&bars->p_full[x][j], 128);
         mbar_init(&bars->pv_done[x][j], 1);
       }
+      mbar_init(&bars->meet_x[x], 4);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
     for (int s = 0; s < NS; ++s) {
@@ -152,7 +141,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       mbar_init(&bars->k_empty[s], 1);
       mbar_init(&bars->v_empty[s], 2);
     }
-    mbar_init(&bars->meet, 256);
+    mbar_init(&bars->meet, 8);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -165,17 +154,18 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   constexpr int ab = Cvt<T>::kAB;
-  volatile int* item_u = bars->item;
-  // the next item's index (all lanes of a warp together), or -1
+  // the next item (all lanes of a warp together); n = -1: none left
   int kc = 0;
-  auto fetch = [&]() -> int {
+  auto fetch = [&]() -> FItem {
     const int slot = kc & 1;
-    if (!warp_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl)) return -1;
-    const int u = item_u[slot];
+    FItem it;
+    it.n = -1;
+    if (!warp_wait(&bars->item_full[slot], (uint32_t)(kc >> 1) & 1u, ctl)) return it;
+    it = *reinterpret_cast<const FItem*>(smem + C::kItem + slot * 32);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
     ++kc;
-    return u;
+    return it;
   };
   // Register split of the 384 x 168 launch budget, as in fwd_tc.cu:
   // 8 x 32 x 224 + 4 x 32 x 56 = 64512 = 384 x 168.
@@ -188,23 +178,24 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
-        int nk = 0, nv = 0, ni = 0;            // K and V stages and Q buffers loaded
+        int nk = 0, nv = 0, ni = 0;            // K and V stages and Q tiles loaded
         bool ok = true;
         // the first item is the CTA's own index, the others come from the counter
         int u = (int)blockIdx.x;
         for (int kf = 0; ok; ++kf, u = (int)gridDim.x + atomicAdd(a.sched, 1)) {
           const int slot = kf & 1;
+          FItem it;
+          it.n = -1;
+          if (u < total) it = make_item<kWin>(a, u);
           if (kf >= 2 && !(ok = mbar_wait(&bars->item_empty[slot], (uint32_t)((kf >> 1) - 1) & 1u, ctl))) break;
-          item_u[slot] = u < total ? u : -1;
+          *reinterpret_cast<FItem*>(smem + C::kItem + slot * 32) = it;
           mbar_arrive(&bars->item_full[slot]);
-          if (u >= total) break;
-          const FItem it = make_item<kWin>(a, u);
+          if (it.n < 0) break;
           if (it.n == 0) continue;
-          const int qb = ni & 1;
-          if (ni >= 2 && !(ok = mbar_wait(&bars->q_empty[qb], (uint32_t)((ni >> 1) - 1) & 1u, ctl))) break;
-          mbar_expect_tx(&bars->q_full[qb], 2 * TB);
+          if (ni >= 1 && !(ok = mbar_wait(&bars->q_empty, (uint32_t)(ni - 1) & 1u, ctl))) break;
+          mbar_expect_tx(&bars->q_full, 2 * TB);
           for (int x = 0; x < 2; ++x)
-            tma_load_4d(smem + C::kQ + (qb * 2 + x) * TB, &tmQ, &bars->q_full[qb], 0, it.qt * kTile, 2 * it.h + x, it.b);
+            tma_load_4d(smem + C::kQ + x * TB, &tmQ, &bars->q_full, 0, it.qt * kTile, 2 * it.h + x, it.b);
           ++ni;
           for (int s = 0; s < it.n; ++s) {
             const int st = nk % NS;
@@ -226,7 +217,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // Before leaving, make sure no load is still writing shared memory.
         for (int j = max(0, nk - NS); j < nk; ++j) mbar_wait(&bars->k_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
         for (int j = max(0, nv - NS); j < nv; ++j) mbar_wait(&bars->v_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
-        for (int j = max(0, ni - 2); j < ni; ++j) mbar_wait(&bars->q_full[j & 1], (uint32_t)(j >> 1) & 1u, ctl);
+        if (ni > 0) mbar_wait(&bars->q_full, (uint32_t)(ni - 1) & 1u, ctl);
       }
     } else if (warp == 9) {
       // ===================== S issuer (both maps) =====================
@@ -235,34 +226,35 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
       int g = 0, ni = 0;                       // steps, items with steps
       bool ok = true;
-      int u;
-      while (ok && (u = fetch()) >= 0) {
-        const FItem it = make_item<kWin>(a, u);
+      while (ok) {
+        const FItem it = fetch();
+        if (it.n < 0) break;
         if (it.n == 0) continue;
         if (lane == 0) {
-          const int qb = ni & 1;
-          ok = mbar_wait(&bars->q_full[qb], (uint32_t)(ni >> 1) & 1u, ctl);
+          ok = mbar_wait(&bars->q_full, (uint32_t)ni & 1u, ctl);
           for (int s = 0; s < it.n && ok; ++s, ++g) {
             const int st = g % NS;
             if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
 #pragma unroll
             for (int jx = 0; jx < 4; ++jx) {
               const int j = jx >> 1, x = jx & 1;       // half by half, map by map
-              // S_xj(g) overwrites P_xj(g-1) once its product has read it
+              // S of half h = 2 g + j overwrites that of half h - 1 once the softmax has read it
+              if (ok && g + j > 0) ok = mbar_wait(&bars->s_free[x], (uint32_t)(j ^ 1), ctl);
+              // and follows the product of half h - 2, so that S(h) tells the softmax P is free as well
               if (ok && g > 0) ok = mbar_wait(&bars->pv_done[x][j], (uint32_t)(g - 1) & 1u, ctl);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t qd = qd0 + (uint64_t)(((qb * 2 + x) * TB) >> 4);
+              const uint64_t qd = qd0 + (uint64_t)((x * TB) >> 4);
               const uint64_t kd = kd0 + (uint64_t)(((st * 2 + x) * TB + j * 8192) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ss(tmem + x * 256 + j * 64, qd + (uint64_t)((k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4), idS,
+                mma_ss(tmem + x * kStream, qd + (uint64_t)((k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4), idS,
                        k > 0 ? 1u : 0u);
-              mma_commit(&bars->s_full[x][j]);
+              mma_commit(&bars->s_full[x]);
             }
             if (ok) mma_commit(&bars->k_empty[st]);
           }
-          if (ok) mma_commit(&bars->q_empty[qb]);
+          if (ok) mma_commit(&bars->q_empty);
         }
         ++ni;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -276,12 +268,12 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const int x = warp - 10;
       constexpr uint32_t idPV = idesc_f16(128, 128, ab, 0, 1);
       const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
-      const uint32_t tP = tmem + x * 256, tO = tmem + x * 256 + 128;
+      const uint32_t tP = tmem + x * kStream + kColP, tO = tmem + x * kStream + kColO;
       int g = 0;
       bool ok = true;
-      int u;
-      while (ok && (u = fetch()) >= 0) {
-        const FItem it = make_item<kWin>(a, u);
+      while (ok) {
+        const FItem it = fetch();
+        if (it.n < 0) break;
         for (int s = 0; s < it.n && ok; ++s, ++g) {
           const int st = g % NS;
           if (!(ok = warp_wait(&bars->v_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
@@ -298,7 +290,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            // P_xj(g) follows the softmax warps' reads of the last item's O
+            // P follows the softmax warps' reads of the last item's O
             if (ok) ok = warp_wait(&bars->p_full[x][j], (uint32_t)g & 1u, ctl);
             if (!ok) break;
             if (lane == 0) {
@@ -306,7 +298,7 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               const uint64_t vd = vd0 + (uint64_t)((st * 2 * TB + j * 8192) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ts(tO, tP + j * 64 + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || j > 0 || k > 0) ? 1u : 0u);
+                mma_ts(tO, tP + j * 32 + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || j > 0 || k > 0) ? 1u : 0u);
               mma_commit(&bars->pv_done[x][j]);
               if (j == 1) mma_commit(&bars->v_empty[st]);
             }
@@ -326,48 +318,42 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;          // row within the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + x * 256 + lane_off, tO = tS + 128;
+    const uint32_t tS = tmem + x * kStream + lane_off, tO = tS + kColO;
     const float sl2 = a.scale_log2;
     float* inv_sh = reinterpret_cast<float*>(smem + C::kInv);
-    // barrier of both warpgroups (bounded, so that a warp that gave up leaves none behind)
-    GroupSync meet{&bars->meet, 0};
+    uint8_t* ob = smem + C::kO + x * TB;        // columns 64 x .. of O
+    uint8_t* ob2 = ob + 2 * TB;                 // and of O_2
+    WarpMeet meet{&bars->meet, 0}, meet_x{&bars->meet_x[x], 0};
     int g = 0;
     bool ok = true;
-    int u;
-    while (ok && (u = fetch()) >= 0) {
-      const FItem it = make_item<kWin>(a, u);
+    while (ok) {
+      const FItem it = fetch();
+      if (it.n < 0) break;
       const int i = it.qt * kTile + r;          // global query row
       const int jmax = a.causal ? min(it.Lk - 1, i) : (it.Lk - 1);
       const int jmin = kWin ? i - a.window + 1 : 0;
       RowSoftmax w;
-      for (int s = 0; s < it.n; ++s, ++g) {
-        const int kv = it.lo + s;
+      for (int s = 0; s < it.n && ok; ++s, ++g) {
 #pragma unroll 1
-        for (int j = 0; j < 2 && ok; ++j) {
-          if (!(ok = warp_wait(&bars->s_full[x][j], (uint32_t)g & 1u, ctl))) break;
+        for (int j = 0; j < 2; ++j) {
+          if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)j, ctl))) break;      // half h = 2 g + j
           tc_fence_after();
-          // the last product into O: the other half's, of this tile or the one before
-          auto o_ready = [&]() -> bool {
-            const bool done = warp_wait(&bars->pv_done[x][j ^ 1], (uint32_t)(j ? g : g - 1) & 1u, ctl);
-            tc_fence_after();
-            return done;
-          };
-          const int key0 = kv * kTile + j * 64;
-          if (!(ok = w.template step<T, 64, 128, kWin>(tS + j * 64, tO, jmax - key0, jmin - key0, sl2, s == 0 && j == 0,
-                                                       o_ready)))
-            break;
-          tmem_wait_st();
-          tc_fence_before();
+          const int key0 = (it.lo + s) * kTile + j * 64;
+          ok = w.template step<T, 128, kWin>(
+              tS, tS + kColP + j * 32, tO, jmax - key0, jmin - key0, sl2, s == 0 && j == 0,
+              [&] { mbar_arrive(&bars->s_free[x]); },
+              [&]() -> bool {       // the product of half h - 1
+                const bool done = warp_wait(&bars->pv_done[x][j ^ 1], (uint32_t)(j ? g : g - 1) & 1u, ctl);
+                tc_fence_after();
+                return done;
+              });
+          if (!ok) break;
           mbar_arrive(&bars->p_full[x][j]);
         }
-        if (!ok) break;
       }
       if (!ok) break;
       // ---- epilogue: O = O_1 / l_1 - lambda O_2 / l_2, columns 64 x .. of both tensors
-      const bool row_ok = i < a.N;
-      const size_t orow = (size_t)it.b * a.ost.b + (size_t)it.h * a.ost.h + (size_t)i * a.ost.n + x * 64;
-      T* op = static_cast<T*>(a.o) + orow;
-      T* op2 = static_cast<T*>(a.o2) + orow;
+      uint32_t r1[2][32], r2[2][32];
       float inv1 = 0.f, inv2 = 0.f;
       if (it.n > 0) {
         inv_sh[x * 128 + r] = w.l_rnd > 0.f ? 1.f / w.l_rnd : 0.f;
@@ -377,50 +363,63 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (!(ok = warp_wait(&bars->pv_done[x][1], (uint32_t)(g - 1) & 1u, ctl))) break;
         tc_fence_after();
         tc_fence_before();
-        if (!(ok = __all_sync(0xffffffffu, meet.sync(ctl)))) break;
+        if (!(ok = meet.sync(ctl))) break;
         tc_fence_after();
         inv1 = inv_sh[r];
         inv2 = inv_sh[128 + r];
+        const uint32_t t1 = tmem + lane_off + kColO + x * 64, t2 = t1 + kStream;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          tmem_ld32(t1 + hf * 32, r1[hf]);
+          tmem_ld32(t2 + hf * 32, r2[hf]);
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          reg_fence32(r1[hf]);
+          reg_fence32(r2[hf]);
+        }
+        // both accumulators are read: the next item's products may overwrite
+        // them once both warpgroups are here
+        tc_fence_before();
+        if (!(ok = meet.sync(ctl))) break;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) r1[c >> 5][c & 31] = r2[c >> 5][c & 31] = 0u;
       }
-      const float lam = a.lam[it.h];
-      const uint32_t t1 = tmem + lane_off + 128 + x * 64, t2 = t1 + 256;
+      // the last item's stores have read the staging boxes
+      if (r == 0) bulk_wait_read0();
+      if (!(ok = meet_x.sync(ctl))) break;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t r1[32], r2[32];
-        if (it.n > 0) {
-          tmem_ld32(t1 + hf * 32, r1);
-          tmem_ld32(t2 + hf * 32, r2);
-          tmem_wait_ld();
-          reg_fence32(r1);
-          reg_fence32(r2);
-        } else {
+      for (int j = 0; j < 8; ++j) {
+        uint32_t u1[4], u2[4];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) r1[c] = r2[c] = 0u;
+        for (int t = 0; t < 4; ++t) {
+          const int c = 8 * j + 2 * t;
+          const float a2 = __uint_as_float(r2[c >> 5][c & 31]) * inv2, b2 = __uint_as_float(r2[c >> 5][(c & 31) + 1]) * inv2;
+          u1[t] = Cvt<T>::pack(__uint_as_float(r1[c >> 5][c & 31]) * inv1 - it.lam * a2,
+                               __uint_as_float(r1[c >> 5][(c & 31) + 1]) * inv1 - it.lam * b2);
+          u2[t] = Cvt<T>::pack(a2, b2);
         }
-        uint32_t w1[16], w2[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float a2 = __uint_as_float(r2[2 * c]) * inv2, b2 = __uint_as_float(r2[2 * c + 1]) * inv2;
-          w1[c] = Cvt<T>::pack(__uint_as_float(r1[2 * c]) * inv1 - lam * a2,
-                               __uint_as_float(r1[2 * c + 1]) * inv1 - lam * b2);
-          w2[c] = Cvt<T>::pack(a2, b2);
-        }
-        if (hf == 1 && it.n > 0) {
-          // both accumulators are read: the next item's products may overwrite
-          // them once every thread of both warpgroups is here
-          tc_fence_before();
-          if (!(ok = __all_sync(0xffffffffu, meet.sync(ctl)))) break;
-        }
-        if (row_ok) {
-          store32(op + hf * 32, w1, a.o_v8);
-          if (a.o2 != nullptr) store32(op2 + hf * 32, w2, a.o_v8);
-        }
+        const uint32_t off = r * 128 + (((j ^ r) & 7) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(smem_u32(ob + off)), "r"(u1[0]), "r"(u1[1]), "r"(u1[2]), "r"(u1[3]) : "memory");
+        if (a.has_o2)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(smem_u32(ob2 + off)), "r"(u2[0]), "r"(u2[1]), "r"(u2[2]), "r"(u2[3]) : "memory");
       }
-      if (!ok) break;
-      if (row_ok)
+      fence_proxy_async_smem();
+      if (!(ok = meet_x.sync(ctl))) break;
+      if (r == 0) {
+        tma_store_4d(&tmO, ob, x * 64, it.qt * kTile, it.h, it.b);
+        if (a.has_o2) tma_store_4d(&tmO2, ob2, x * 64, it.qt * kTile, it.h, it.b);
+        bulk_commit();
+      }
+      if (i < a.N)
         a.lse[((size_t)it.b * 2 * a.H + 2 * it.h + x) * a.N + i] =
             w.l_true > 0.f ? (w.m_run + lg2(w.l_true)) * kLn2 : -INFINITY;
     }
+    if (r == 0) bulk_wait_read0();
   }
 
   tc_fence_before();
@@ -432,8 +431,8 @@ diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 }
 
 template <typename T, bool kWin>
-cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const DiffFwdArgs& a,
-                     cudaStream_t s) {
+cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+                     const CUtensorMap& o2, const DiffFwdArgs& a, cudaStream_t s) {
   auto kern = diff_fwd_kernel<T, kWin>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DCfg::kBytes);
   if (e != cudaSuccess) return e;
@@ -441,17 +440,18 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const long long total = (long long)a.nq * a.B * a.H;
-  kern<<<(unsigned)std::min<long long>(total, std::max(sms, 1)), kThreads, DCfg::kBytes, s>>>(q, k, v, a);
+  kern<<<(unsigned)std::min<long long>(total, std::max(sms, 1)), kThreads, DCfg::kBytes, s>>>(q, k, v, o, o2, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_diff_fwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const DiffFwdArgs& a, cudaStream_t s) {
+                            const CUtensorMap& o, const CUtensorMap& o2, const DiffFwdArgs& a, cudaStream_t s) {
   if (dtype == FA_DT_BF16)
-    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, a, s) : launch_t<__nv_bfloat16, false>(q, k, v, a, s);
-  return a.window > 0 ? launch_t<__half, true>(q, k, v, a, s) : launch_t<__half, false>(q, k, v, a, s);
+    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, o, o2, a, s)
+                        : launch_t<__nv_bfloat16, false>(q, k, v, o, o2, a, s);
+  return a.window > 0 ? launch_t<__half, true>(q, k, v, o, o2, a, s) : launch_t<__half, false>(q, k, v, o, o2, a, s);
 }
 
 }  // namespace fa

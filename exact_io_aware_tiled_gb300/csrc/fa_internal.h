@@ -105,10 +105,7 @@ struct DiffFwdArgs {
   const int32_t* seqlens_k;   // device [B] or nullptr
   const float* lam;           // device [H]
   float* lse;                 // [B,2H,N]
-  void* o;                    // [B,H,N,128], strides ost
-  void* o2;                   // the second map's own output, or nullptr
-  Strides ost;
-  int o_v8;                   // o, o2 allow 32-byte stores
+  int has_o2;                 // also store O_2 (the second map's own output)
   int* sched;                 // work-item counter, cleared with the status word
   int* status;
 };
@@ -171,10 +168,10 @@ cudaError_t launch_dropout_mask(const DropoutArgs& d, int H, int N, int b, int h
 cudaError_t launch_fp8_quantize(int dtype, const Fp8QuantArgs& a, int per_tensor, cudaStream_t s);
 cudaError_t launch_fwd_fp8(int d, const CUtensorMap& q8, const CUtensorMap& k8, const CUtensorMap& v8t,
                            const CUtensorMap& o, const FwdArgs& a, cudaStream_t s);
-// Differential attention.  Maps: q, k over [B,2H,N,64] / [B,2H_kv,N,64], v and dout over [B,H_kv,N,128] /
-// [B,H,N,128], boxes of 64 columns; the backward's q and dout boxes have 64 rows.
+// Differential attention.  Maps: q, k over [B,2H,N,64] / [B,2H_kv,N,64], v over [B,H_kv,N,128], o, o2 and dout
+// over [B,H,N,128], boxes of 64 columns; the backward's q and dout boxes have 64 rows.
 cudaError_t launch_diff_fwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const DiffFwdArgs& a, cudaStream_t s);
+                            const CUtensorMap& o, const CUtensorMap& o2, const DiffFwdArgs& a, cudaStream_t s);
 cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides ost, const void* dout, Strides dost,
                              const float* lse, const float* lam, int B, int H, int N, int npad, float c1, float* rows,
                              float* dqacc, int* sched, cudaStream_t s);

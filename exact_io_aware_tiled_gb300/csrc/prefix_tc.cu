@@ -14,7 +14,7 @@
 // (sequence, head, token), so the softmax threads gather their own Q row into
 // the swizzled tile.  Splits are sized so that one wave of CTAs covers the GPU;
 // each leaves (max, sums, O unnormalised) in float32 for the join.
-// Tensor memory per slot (256 columns): S 128 (P over its first 64) | O.
+// Tiles are worked in two 64-key halves; row_softmax.cuh says where S, P and O lie.
 #include "prefix.cuh"
 #include "row_softmax.cuh"
 
@@ -37,7 +37,8 @@ static_assert(TCfg<64>::kBytes <= 232448 && TCfg<128>::kBytes <= 232448, "shared
 
 struct TBars {
   uint64_t q_full;
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], s_free[2];                         // [slot]
+  uint64_t p_full[2][2], pv_done[2][2];                  // [slot][half]
   uint64_t done[3];
   uint64_t k_full[5], v_full[5], k_empty[5], v_empty[5];
   uint32_t tmem_base;
@@ -74,8 +75,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     mbar_init(&bars->q_full, 128 * nact);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], 128);
-      mbar_init(&bars->pv_done[x], 1);
+      mbar_init(&bars->s_free[x], 128);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&bars->p_full[x][j], 128);
+        mbar_init(&bars->pv_done[x][j], 1);
+      }
     }
     for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
     for (int s = 0; s < NS; ++s) {
@@ -134,22 +138,28 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     } else if (warp == 9) {
       // ===================== S issuer (both slots) =====================
       if (lane == 0) {
-        constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
+        constexpr uint32_t idS = idesc_f16(128, 64, ab, 0, 0);
         const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
         bool ok = mbar_wait(&bars->q_full, 0, ctl);
         for (int s = 0; s < n && ok; ++s) {
           const int st = s % NS;
           if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
-          for (int x = 0; x < nact; ++x) {
-            // S_x(s) overwrites P_x(s-1) once P V_x(s-1) has read it
-            if (s > 0 && !(ok = mbar_wait(&bars->pv_done[x], (uint32_t)(s - 1) & 1u, ctl))) break;
+#pragma unroll
+          for (int jx = 0; jx < 4; ++jx) {
+            const int j = jx >> 1, x = jx & 1;         // half by half, slot by slot
+            if (x >= nact) continue;
+            // S of half h = 2 s + j overwrites that of half h - 1 once the softmax has read it
+            if (ok && s + j > 0) ok = mbar_wait(&bars->s_free[x], (uint32_t)(j ^ 1), ctl);
+            // and follows the product of half h - 2, so that S(h) tells the softmax P is free as well
+            if (ok && s > 0) ok = mbar_wait(&bars->pv_done[x][j], (uint32_t)(s - 1) & 1u, ctl);
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t qd = qd0 + (uint64_t)((x * TB) >> 4), kd = kd0 + (uint64_t)((st * TB) >> 4);
+            const uint64_t qd = qd0 + (uint64_t)((x * TB) >> 4), kd = kd0 + (uint64_t)((st * TB + j * 8192) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint64_t o = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
-              mma_ss(tmem + x * 256, qd + o, kd + o, idS, k > 0 ? 1u : 0u);
+              mma_ss(tmem + x * kStream, qd + o, kd + o, idS, k > 0 ? 1u : 0u);
             }
             mma_commit(&bars->s_full[x]);
           }
@@ -164,19 +174,23 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       if (lane == 0) {
         constexpr uint32_t idPV = idesc_f16(128, D, ab, 0, 1);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
-        const uint32_t tP = tmem + x * 256, tO = tP + 128;
+        const uint32_t tP = tmem + x * kStream + kColP, tO = tmem + x * kStream + kColO;
         bool ok = true;
         for (int s = 0; s < n && ok; ++s) {
           const int st = s % NS;
-          if (!(ok = mbar_wait(&bars->p_full[x], (uint32_t)s & 1u, ctl) &&
-                     mbar_wait(&bars->v_full[st], (uint32_t)(s / NS) & 1u, ctl)))
-            break;
-          tc_fence_after();
-          const uint64_t vd = vd0 + (uint64_t)((st * TB) >> 4);
+          if (!(ok = mbar_wait(&bars->v_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tO, tP + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || k > 0) ? 1u : 0u);
-          mma_commit(&bars->pv_done[x]);
+          for (int j = 0; j < 2; ++j) {
+            if (ok) ok = mbar_wait(&bars->p_full[x][j], (uint32_t)s & 1u, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)((st * TB + j * 8192) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tO, tP + j * 32 + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || j > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&bars->pv_done[x][j]);
+          }
+          if (!ok) break;
           mma_commit(&bars->v_empty[st]);
         }
         mma_commit(&bars->done[1 + x]);
@@ -191,7 +205,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const int quarter = warp & 3;
       const int r = quarter * 32 + lane;          // row within the slot = TMEM lane
       const int row = rt * 256 + x * 128 + r;
-      const uint32_t tS = tmem + x * 256 + ((uint32_t)(quarter * 32) << 16), tO = tS + 128;
+      const uint32_t tS = tmem + x * kStream + ((uint32_t)(quarter * 32) << 16), tO = tS + kColO;
       // this thread's Q row into the swizzled tile
       {
         uint8_t* qb = smem + C::kQ + x * TB + r * 128;
@@ -207,18 +221,25 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       }
       RowSoftmax w;
       bool ok = true;
-      for (int s = 0; s < n; ++s) {
-        if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)s & 1u, ctl))) break;
-        tc_fence_after();
-        // S(s) exists, so P V(s-1) is done
-        w.template step<T, 128, D, false>(tS, tO, a.P - 1 - (k0 + s * kTile), 0, a.scale_log2, s == 0,
-                                          [] { return true; });
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[x]);
+      for (int s = 0; s < n && ok; ++s) {
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)j, ctl))) break;      // half h = 2 s + j
+          tc_fence_after();
+          ok = w.template step<T, D, false>(
+              tS, tS + kColP + j * 32, tO, a.P - 1 - (k0 + s * kTile + j * 64), 0, a.scale_log2, s == 0 && j == 0,
+              [&] { mbar_arrive(&bars->s_free[x]); },
+              [&]() -> bool {       // the product of half h - 1
+                const bool done = warp_wait(&bars->pv_done[x][j ^ 1], (uint32_t)(j ? s : s - 1) & 1u, ctl);
+                tc_fence_after();
+                return done;
+              });
+          if (!ok) break;
+          mbar_arrive(&bars->p_full[x][j]);
+        }
       }
       // ---- this row's maximum, sums and unnormalised O
-      if (ok && warp_wait(&bars->pv_done[x], (uint32_t)(n - 1) & 1u, ctl)) {
+      if (ok && warp_wait(&bars->pv_done[x][1], (uint32_t)(n - 1) & 1u, ctl)) {
         tc_fence_after();
         const long long pr = ((long long)sp * a.Hkv + hk) * a.R + row;
 #pragma unroll 1

@@ -3,9 +3,9 @@
 Forward (csrc/diff_fwd.cu): persistent CTAs, an item is one query tile with two
 score maps.  A stage holds the K tiles of both maps (released by the S issuer)
 and one V tile (released by both P V issuers); a stage's first use skips the
-empty waits; a tile is worked in two halves with a place each for S and, over it,
-P, so S_xj(g) waits for P V_xj(g-1); O is rescaled after the other half's product;
-the two softmax groups meet before and after they read both accumulators.
+empty waits; a tile is worked in two halves h: S(h) waits until the softmax has
+read S(h-1) and the product of half h - 2 is done, which frees P(h)'s place, O is rescaled after
+that of half h - 1; the two softmax groups meet before and after they read both accumulators.
 
 Backward (csrc/diff_bwd.cu): the roles of the d = 128 backward with a two-stage
 Q / dO ring, and W^T over S_1^T: the S issuer waits for dV(g-1) before S_1(g),
@@ -33,9 +33,10 @@ class Forward:
         B = Bar
         self.item_full = [B("item_full%d" % i, 1) for i in range(2)]
         self.item_empty = [B("item_empty%d" % i, 5) for i in range(2)]      # S, two P V issuers, two softmax groups
-        self.q_full, self.q_empty = ([B("q_%s%d" % (n, i), 1) for i in range(2)] for n in ("full", "empty"))
-        self.s_full, self.p_full, self.pv_done = ([[B("%s%d%d" % (n, x, j), 1) for j in range(2)] for x in range(2)]
-                                                  for n in ("s_full", "p_full", "pv_done"))
+        self.q_full, self.q_empty = B("q_full", 1), B("q_empty", 1)
+        self.s_full, self.s_free = ([B("%s%d" % (n, x), 1) for x in range(2)] for n in ("s_full", "s_free"))
+        self.p_full, self.pv_done = ([[B("%s%d%d" % (n, x, j), 1) for j in range(2)] for x in range(2)]
+                                     for n in ("p_full", "pv_done"))
         self.k_full, self.v_full, self.k_empty = ([B("%s%d" % (n, i), 1) for i in range(NS)]
                                                   for n in ("k_full", "v_full", "k_empty"))
         self.v_empty = [B("v_empty%d" % i, 1 if plant == "v_one_reader" else 2) for i in range(NS)]
@@ -61,9 +62,9 @@ class Forward:
                 break
             if self.items[u] == 0:
                 continue
-            if ni >= 2:
-                yield ("wait", self.q_empty[ni & 1], (ni >> 1) - 1)
-            self.load(self.q_full[ni & 1])
+            if ni >= 1:
+                yield ("wait", self.q_empty, ni - 1)
+            self.load(self.q_full)
             ni += 1
             for _ in range(self.items[u]):
                 st = g % NS
@@ -80,8 +81,8 @@ class Forward:
         for j in range(max(0, g - NS), g):
             yield ("wait", self.k_full[j % NS], j // NS)
             yield ("wait", self.v_full[j % NS], j // NS)
-        for j in range(max(0, ni - 2), ni):
-            yield ("wait", self.q_full[j & 1], j >> 1)
+        if ni > 0:
+            yield ("wait", self.q_full, ni - 1)
 
     def fetch(self, kc):
         yield ("wait", self.item_full[kc & 1], kc >> 1)
@@ -100,19 +101,22 @@ class Forward:
                 return
             if self.items[u] == 0:
                 continue
-            yield ("wait", self.q_full[ni & 1], ni >> 1)
+            yield ("wait", self.q_full, ni)
             for _ in range(self.items[u]):
                 yield ("wait", self.k_full[g % NS], g // NS)
                 for j in range(2):
                     for x in range(2):
-                        if g > 0 and self.plant != "s_ungated":
+                        h = 2 * g + j
+                        if h > 0 and self.plant != "s_ungated":
+                            yield ("wait", self.s_free[x], h - 1)
+                        if self.s_free[x].completed < h:
+                            raise ProtocolError("S_%d(%d) written over scores not yet read" % (x, h))
+                        if g > 0 and self.plant != "p_ungated":
                             yield ("wait", self.pv_done[x][j], g - 1)
-                        if self.pv_done[x][j].completed < g:
-                            raise ProtocolError("S_%d(%d) written over P that its product still reads" % (x, g))
-                        self.engine.later("S", self.s_full[x][j])
+                        self.engine.later("S", self.s_full[x])
                 self.engine.later("S", self.k_empty[g % NS])
                 g += 1
-            self.engine.later("S", self.q_empty[ni & 1])
+            self.engine.later("S", self.q_empty)
             ni += 1
 
     def pv_issuer(self, x):
@@ -143,7 +147,10 @@ class Forward:
                 return
             for s in range(self.items[u]):
                 for j in range(2):
-                    yield ("wait", self.s_full[x][j], g)
+                    yield ("wait", self.s_full[x], 2 * g + j)
+                    self.s_free[x].arrive()
+                    if self.pv_done[x][j].completed < g:
+                        raise ProtocolError("P_%d%d(%d) written under the product that reads it" % (x, j, g))
                     if (s > 0 or j > 0) and rng.random() < 0.5:      # the reference maximum moved: O is rescaled
                         if self.plant != "rescale_ungated":
                             yield ("wait", self.pv_done[x][j ^ 1], g if j else g - 1)
@@ -180,7 +187,7 @@ def test_forward_protocol():
 
 
 @pytest.mark.parametrize("plant", ["v_one_reader", "s_ungated", "waits_for_other_map", "no_second_meet",
-                                   "rescale_ungated"])
+                                   "p_ungated", "rescale_ungated"])
 def test_forward_planted_mistakes_are_caught(plant):
     rng = random.Random(3)
     for _ in range(400):
