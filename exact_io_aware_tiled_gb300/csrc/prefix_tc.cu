@@ -9,8 +9,10 @@
 //
 // Mapping, as in the d = 128 forward (fwd_tc.cu): one CTA = 256 rows (two
 // 128-row slots) and one key split, every K / V tile loaded once for both slots;
-// warps 0-7 softmax (one thread a row), warp 8 TMA, warp 9 the S products, warps
-// 10 and 11 the P V products of slot 0 and 1.  A row's place in q follows from
+// warps 0-7 softmax (one thread a row), warp 8 TMA, warps 9 and 10 the S products
+// and 11 and 12 the P V products of slot 0 and 1 (products of one issuer complete
+// one after the other, 8 for each half tile of S at d = 128: one issuer for both
+// slots took 39 us where two take 34, 1,024 rows x 32,769 keys x 2 heads).  A row's place in q follows from
 // (sequence, head, token), so the softmax threads gather their own Q row into
 // the swizzled tile.  Splits are sized so that one wave of CTAs covers the GPU;
 // each leaves (max, sums, O unnormalised) in float32 for the join.
@@ -21,7 +23,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;   // warps 0-7 softmax, 8 TMA, 9 / 10 S issuers, 11 / 12 P V issuers, 13-15 idle
 
 template <int D> struct TCfg {
   static constexpr int kTB = 128 * D * 2;                // one [128 rows][D] tile
@@ -39,7 +41,7 @@ struct TBars {
   uint64_t q_full;
   uint64_t s_full[2], s_free[2];                         // [slot]
   uint64_t p_full[2][2], pv_done[2][2];                  // [slot][half]
-  uint64_t done[3];
+  uint64_t done[4];
   uint64_t k_full[5], v_full[5], k_empty[5], v_empty[5];
   uint32_t tmem_base;
   int abort;
@@ -81,11 +83,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         mbar_init(&bars->pv_done[x][j], 1);
       }
     }
-    for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->done[i], 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->k_empty[s], nact);
       mbar_init(&bars->v_empty[s], nact);
     }
     bars->abort = 0;
@@ -100,7 +102,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   constexpr int ab = Cvt<T>::kAB;
-  // Register split of the 384 x 168 launch budget, as in fwd_tc.cu
+  // Register split of the 512 x 128 launch budget:
+  // 8 x 32 x 200 + 8 x 32 x 56 = 65536 = 512 x 128.
 
   if (warp >= 8) {
     regs_dec<56>();
@@ -135,9 +138,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         for (int j = max(0, nk - NS); j < nk; ++j) mbar_wait(&bars->k_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
         for (int j = max(0, nv - NS); j < nv; ++j) mbar_wait(&bars->v_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
       }
-    } else if (warp == 9) {
-      // ===================== S issuer (both slots) =====================
-      if (lane == 0) {
+    } else if (warp <= 10) {
+      // ===================== S issuer of slot x =====================
+      const int x = warp - 9;
+      if (lane == 0 && x < nact) {
         constexpr uint32_t idS = idesc_f16(128, 64, ab, 0, 0);
         const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
@@ -146,9 +150,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           const int st = s % NS;
           if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
 #pragma unroll
-          for (int jx = 0; jx < 4; ++jx) {
-            const int j = jx >> 1, x = jx & 1;         // half by half, slot by slot
-            if (x >= nact) continue;
+          for (int j = 0; j < 2; ++j) {
             // S of half h = 2 s + j overwrites that of half h - 1 once the softmax has read it
             if (ok && s + j > 0) ok = mbar_wait(&bars->s_free[x], (uint32_t)(j ^ 1), ctl);
             // and follows the product of half h - 2, so that S(h) tells the softmax P is free as well
@@ -165,12 +167,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           }
           if (ok) mma_commit(&bars->k_empty[st]);
         }
-        mma_commit(&bars->done[0]);
-        mbar_wait(&bars->done[0], 0, ctl);
+        mma_commit(&bars->done[x]);
+        mbar_wait(&bars->done[x], 0, ctl);
       }
-    } else if (warp - 10 < nact) {
+    } else if (warp <= 12 && warp - 11 < nact) {
       // ===================== P V issuer of slot x =====================
-      const int x = warp - 10;
+      const int x = warp - 11;
       if (lane == 0) {
         constexpr uint32_t idPV = idesc_f16(128, D, ab, 0, 1);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
@@ -193,12 +195,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (!ok) break;
           mma_commit(&bars->v_empty[st]);
         }
-        mma_commit(&bars->done[1 + x]);
-        mbar_wait(&bars->done[1 + x], 0, ctl);
+        mma_commit(&bars->done[2 + x]);
+        mbar_wait(&bars->done[2 + x], 0, ctl);
       }
     }
   } else {
-    regs_inc<224>();
+    regs_inc<200>();
     // ===================== softmax warps =====================
     const int x = warp >> 2;
     if (x < nact) {
