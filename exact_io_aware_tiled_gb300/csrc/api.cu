@@ -709,23 +709,19 @@ fa_status fa_diff_bwd(const fa_diff_params* p, const void* q, const void* k, con
   a.dkv_v8 = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 &&
              (sd.k.n | sd.k.h | sd.k.b | sd.v.n | sd.v.h | sd.v.b) % 16 == 0;
   float* dqacc = reinterpret_cast<float*>(w + L.dqacc);
-  const Strides acc{(int64_t)2 * p->H * p->N * 64, (int64_t)p->N * 64, 64};
-  fa_params bn{};
-  bn.B = p->B;
-  bn.N = p->N;
-  CUtensorMap mq, mk, mv, mdo, macc;
+  a.dqacc = dqacc;
+  CUtensorMap mq, mk, mv, mdo;
   if ((s = diff_map(&mq, q, p, 2 * p->H, 64, sd.q, 64)) != FA_OK ||
       (s = diff_map(&mk, k, p, 2 * hkv, 64, sd.k, kTile)) != FA_OK ||
       (s = diff_map(&mv, v, p, hkv, 128, sd.v, kTile)) != FA_OK ||
-      (s = diff_map(&mdo, dout, p, p->H, 128, sd.dout, 64)) != FA_OK ||
-      (s = make_map(&macc, dqacc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, 64, 32, &bn, 2 * p->H, acc, 64)) != FA_OK)
+      (s = diff_map(&mdo, dout, p, p->H, 128, sd.dout, 64)) != FA_OK)
     return s;
   if (cudaMemsetAsync(w + L.status, 0, sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
   // bf16 kernels fold tau into dS; see diff_bwd.cu
   const float c1 = p->dtype == FA_DT_BF16 ? a.scale : 1.f;
   cudaError_t e = launch_diff_prep(p->dtype, o, o2, sd.o, dout, sd.dout, lse, p->lam, p->B, p->H, p->N, L.npad, c1,
                                    reinterpret_cast<float*>(w + L.rows), dqacc, a.sched, st);
-  if (e == cudaSuccess) e = launch_diff_bwd(p->dtype, mq, mk, mv, mdo, macc, a, st);
+  if (e == cudaSuccess) e = launch_diff_bwd(p->dtype, mq, mk, mv, mdo, a, st);
   if (e == cudaSuccess) e = launch_dq_convert(p->dtype, dqacc, dq, sd.q, p->B, 2 * p->H, p->N, 64, st);
   if (e == cudaSuccess) e = launch_diff_dlam(a.dlam_part, dlam, p->B, p->H, a.group, L.nq, st);
   return cuda_status(e);

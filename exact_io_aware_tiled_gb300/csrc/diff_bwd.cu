@@ -13,7 +13,10 @@
 //
 // Tiles: 128 keys x 64 query rows a step, keys on the tensor-memory lanes, as in
 // the d = 128 backward (bwd_tc128.cu), whose roles and barriers this kernel
-// keeps.  Tensor memory (512 columns):
+// keeps, except that dQ goes from registers into the float32 accumulator by
+// 128-byte-per-warp adds instead of through a staging tile and a TMA reduce: the
+// 32 KB that frees hold a second pair of K tiles, so an item's first scores do
+// not wait for the last item's products.  Tensor memory (512 columns):
 //   S_1^T 0-63 | S_2^T 64-127 | dP^T 128-191 | dQ^T 192-255 | dK_1, dK_2 256-383 | dV 384-511
 // W^T = (P_1 - lambda P_2)^T, the 16-bit operand of dV, lies over S_1^T (the 16
 // queries of warpgroup w in the first 8 of its own 16 columns), so S_1 of the
@@ -43,19 +46,17 @@ constexpr int kThreads = 640;
 constexpr int kCompute = 512;   // threads of warps 0-15
 constexpr int kQS = 64;         // query rows per step
 constexpr int NQ = 2;           // Q / dO stages
-constexpr int kLag = 3;         // dQ reduce-adds trail the loads by this many steps
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DSmem {
-  static constexpr int kK = 0;                      // K_1 | zeros | K_2, 16 KB each
-  static constexpr int kV = 49152;                  // 32 KB: V [2 boxes][128 keys][64]
-  static constexpr int kQ = 81920;                  // NQ x (Q_1, Q_2: 8 KB each)
+  // K_1 of two items | zeros | K_2 of two items, 16 KB each
+  static constexpr int kK1 = 0, kZ = 32768, kK2 = 49152;
+  static constexpr int kV = 81920;                  // 32 KB: V [2 boxes][128 keys][64]
+  static constexpr int kQ = kV + 32768;             // NQ x (Q_1, Q_2: 8 KB each)
   static constexpr int kDO = kQ + NQ * 16384;       // NQ x 16 KB: dO [2 boxes][64 q][64]
   static constexpr int kDS = kDO + NQ * 16384;      // dS_1^T, dS_2^T [128 keys][64 q], 16 KB each
-  static constexpr int kDQ = kDS + 32768;           // 32 KB: float32 dQ staging [4 boxes][64 q][32]
-  static constexpr int kLD = kDQ + 32768;           // NQ x 4 x 64 floats: LSE_1, LSE_2, e_1, e_2
-  static constexpr int kInfo = kLD + NQ * 1024;     // (first query row, head pair, batch) of the last kLag+1 steps
-  static constexpr int kItem = kInfo + 64;          // the two published work items
+  static constexpr int kLD = kDS + 32768;           // NQ x 4 x 64 floats: LSE_1, LSE_2, e_1, e_2
+  static constexpr int kItem = kLD + NQ * 1024;     // the two published work items
   static constexpr int kBar = kItem + 64;
   static constexpr int kBytes = kBar + 320;
   static constexpr int kDyn = kBytes + 1024;
@@ -64,12 +65,11 @@ static_assert(DSmem::kDyn <= 232448, "shared memory over the per-block limit");
 
 struct DBars {
   uint64_t item_full[2], item_empty[2];
-  uint64_t kv_full, kv_empty;
+  uint64_t k_full[2], k_empty[2], v_full, v_empty;
   uint64_t q_full[NQ], q_empty[NQ];
   uint64_t s_full, p_full, dp_full, ds_full, dq_full, dq_free, dkv_full, pt_free;
   uint64_t dsm_free;
   uint64_t done[3];
-  uint64_t stg_full, stg_free;
   uint32_t tmem_base;
   int abort;
 };
@@ -125,7 +125,7 @@ template <typename T, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                const __grid_constant__ CUtensorMap tmDQ, const DiffBwdArgs a) {
+                const DiffBwdArgs a) {
   using L = DSmem;
   // bf16: tau is folded into dS, so dQ and dK leave the tensor core scaled; not
   // for fp16, whose smaller range would push small dS values into subnormals.
@@ -140,15 +140,19 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
   // the zero tile between K_1 and K_2
   for (int o = threadIdx.x * 16; o < 16384; o += kThreads * 16)
-    *reinterpret_cast<uint4*>(smem + L::kK + 16384 + o) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(smem + L::kZ + o) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->item_full[s], 1);
       mbar_init(&bars->item_empty[s], 3 + kCompute);   // warps 17-19 and the compute threads
     }
-    mbar_init(&bars->kv_full, 1);
-    mbar_init(&bars->kv_empty, 2);      // S^T / dP^T warp and dQ warp read K, V
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 2);  // the S^T and the dQ^T products read K
+    }
+    mbar_init(&bars->v_full, 1);
+    mbar_init(&bars->v_empty, 1);       // the dP^T products read V
     for (int s = 0; s < NQ; ++s) {
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 1);
@@ -163,8 +167,6 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     mbar_init(&bars->pt_free, 1);
     mbar_init(&bars->dsm_free, 2);     // dK and dQ^T both read the shared dS^T tiles
     for (int i = 0; i < 3; ++i) mbar_init(&bars->done[i], 1);
-    mbar_init(&bars->stg_full, kCompute);
-    mbar_init(&bars->stg_free, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -183,7 +185,8 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     constexpr uint32_t idV = idesc_f16(128, 128, ab, 0, 1);    // dV (A in tensor memory, B MN-major)
     constexpr uint32_t idK = idesc_f16(128, 64, ab, 0, 1);     // dK_m (A K-major, B MN-major)
     constexpr uint32_t idQ = idesc_f16(128, 64, ab, 1, 1);     // dQ^T (A = (K_1 | Z)^T or (Z | K_2)^T, B = dS^T, MN-major)
-    const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+    const uint32_t sK1 = smem_u32(smem + L::kK1), sZ = smem_u32(smem + L::kZ), sK2 = smem_u32(smem + L::kK2);
+    const uint32_t sV = smem_u32(smem + L::kV);
     const uint32_t sQ = smem_u32(smem + L::kQ), sDO = smem_u32(smem + L::kDO);
     const uint32_t sDS = smem_u32(smem + L::kDS);
     volatile int* item_u = reinterpret_cast<volatile int*>(smem + L::kItem);
@@ -197,30 +200,12 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       return v;
     };
     if (warp == 16) {
-      // ===================== TMA producer + dQ reduce =====================
+      // ===================== items and TMA =====================
       if (lane == 0) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmDO);
-        prefetch_tmap(&tmDQ);
-        int4* info = reinterpret_cast<int4*>(smem + L::kInfo);
         int g = 0, nkv = 0;
         bool ok = true;
-        // the staged dQ of step r: 32-column boxes of both maps; a half tile
-        // that starts at or past N has nothing to add
-        auto reduce = [&](int r) -> bool {
-          if (!mbar_wait(&bars->stg_full, (uint32_t)r & 1u, ctl)) return false;
-          const uint8_t* sb = smem + L::kDQ;
-          const int4 inf = info[r & 3];
-          if (inf.x < a.N) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tma_reduce_add_4d(&tmDQ, sb + c * 8192, (c & 1) * 32, inf.x, 2 * inf.y + (c >> 1), inf.z);
-            bulk_commit();
-            bulk_wait_read0();
-          }
-          mbar_arrive(&bars->stg_free);
-          return true;
-        };
         int kf = 0;
         auto publish = [&]() -> int {
           const int slot = kf & 1;
@@ -232,34 +217,22 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           ++kf;
           return v;
         };
-        int rd = 0;
-        auto reduce_to = [&](int last) -> bool {
-          for (; rd <= last; ++rd)
-            if (!reduce(rd)) return false;
-          return true;
-        };
-        int u;
+        int nv = 0;                       // V loads issued
         while (ok) {
-          if (!(ok = reduce_to(g - kLag))) break;
-          u = publish();
-          if (u < 0) {
-            ok = u == -1;
-            break;
-          }
+          const int u = publish();
+          if (u < 0) break;
           const DItem it = make_item(a, u);
           if (it.steps == 0) continue;
-          // K, V: one buffer each, free once the previous item's S^T, dP^T and dQ^T products are done
-          if (!(ok = mbar_wait(&bars->kv_empty, ((uint32_t)nkv & 1u) ^ 1u, ctl))) break;
-          mbar_expect_tx(&bars->kv_full, 65536);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tma_load_4d(smem + L::kK + c * 32768, &tmK, &bars->kv_full, 0, it.jt * kTile, 2 * it.hk + c, it.b);
-            tma_load_4d(smem + L::kV + c * 16384, &tmV, &bars->kv_full, c * 64, it.jt * kTile, it.hk, it.b);
-          }
+          // K: two buffers, so the next item's K lands while this item's last products run
+          const int kb = nkv & 1;
+          if (!(ok = mbar_wait(&bars->k_empty[kb], ((uint32_t)(nkv >> 1) & 1u) ^ 1u, ctl))) break;
+          mbar_expect_tx(&bars->k_full[kb], 32768);
+          tma_load_4d(smem + L::kK1 + kb * 16384, &tmK, &bars->k_full[kb], 0, it.jt * kTile, 2 * it.hk, it.b);
+          tma_load_4d(smem + L::kK2 + kb * 16384, &tmK, &bars->k_full[kb], 0, it.jt * kTile, 2 * it.hk + 1, it.b);
           ++nkv;
           StepPos sp;
           sp.hq = it.h0;
-          for (int t = 0; t < it.steps && ok; ++t, ++g, sp.next(it)) {
+          for (int t = 0; t < it.steps; ++t, sp.next(it)) {
             const int st = g % NQ;
             if (!(ok = mbar_wait(&bars->q_empty[st], ((uint32_t)(g / NQ) & 1u) ^ 1u, ctl))) break;
             const int q0 = (it.i0 + sp.qu) * kTile + sp.hf * kQS;
@@ -271,17 +244,22 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               tma_load_4d(smem + L::kDO + st * 16384 + c * 8192, &tmDO, &bars->q_full[st], c * 64, q0, sp.hq, it.b);
             }
             bulk_load(smem + L::kLD + st * 1024, a.rows + ld_row, 1024, &bars->q_full[st]);
-            info[g & 3] = make_int4(q0, sp.hq, it.b, 0);
-            if (!(ok = reduce_to(g - kLag))) {
-              ++g;                       // this step's loads are in flight
-              break;
+            ++g;
+            if (t == 0) {
+              // V: one buffer, free once the last item's dP^T products are done
+              if (!(ok = mbar_wait(&bars->v_empty, ((uint32_t)nv & 1u) ^ 1u, ctl))) break;
+              mbar_expect_tx(&bars->v_full, 32768);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                tma_load_4d(smem + L::kV + c * 16384, &tmV, &bars->v_full, c * 64, it.jt * kTile, it.hk, it.b);
+              ++nv;
             }
           }
         }
-        if (ok) ok = reduce_to(g - 1);
+        // before leaving, make sure no load is still writing shared memory
         for (int t = max(0, g - NQ); t < g; ++t) mbar_wait(&bars->q_full[t % NQ], (uint32_t)(t / NQ) & 1u, ctl);
-        if (nkv > 0) mbar_wait(&bars->kv_full, (uint32_t)(nkv - 1) & 1u, ctl);
-        bulk_wait_read0();
+        for (int t = max(0, nkv - 2); t < nkv; ++t) mbar_wait(&bars->k_full[t & 1], (uint32_t)(t >> 1) & 1u, ctl);
+        if (nv > 0) mbar_wait(&bars->v_full, (uint32_t)(nv - 1) & 1u, ctl);
       }
     } else if (warp == 17) {
       // ===================== S^T / dP^T issuer =====================
@@ -292,8 +270,8 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         while (ok && (u = fetch()) >= 0) {
           const DItem it = make_item(a, u);
           if (it.steps == 0) continue;
-          if (!(ok = mbar_wait(&bars->kv_full, (uint32_t)nkv & 1u, ctl))) break;
-          ++nkv;
+          const int kb = nkv & 1;
+          if (!(ok = mbar_wait(&bars->k_full[kb], (uint32_t)(nkv >> 1) & 1u, ctl))) break;
           for (int t = 0; t < it.steps && ok; ++t, ++g) {
             const int st = g % NQ;
             // S_2^T(g) once part 1 of step g-1 has read S_2^T(g-1); S_1^T(g) also
@@ -303,17 +281,19 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss(tmem + kColS2, sdesc_sw128(sK + 32768 + k * 32, 16, 1024),
+              mma_ss(tmem + kColS2, sdesc_sw128(sK2 + kb * 16384 + k * 32, 16, 1024),
                      sdesc_sw128(sQ + st * 16384 + 8192 + k * 32, 16, 1024), idST, k > 0 ? 1u : 0u);
             if (g > 0 && !(ok = mbar_wait(&bars->pt_free, (uint32_t)(g - 1) & 1u, ctl))) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss(tmem + kColS1, sdesc_sw128(sK + k * 32, 16, 1024), sdesc_sw128(sQ + st * 16384 + k * 32, 16, 1024),
-                     idST, k > 0 ? 1u : 0u);
+              mma_ss(tmem + kColS1, sdesc_sw128(sK1 + kb * 16384 + k * 32, 16, 1024),
+                     sdesc_sw128(sQ + st * 16384 + k * 32, 16, 1024), idST, k > 0 ? 1u : 0u);
             mma_commit(&bars->s_full);
+            if (t == it.steps - 1) mma_commit(&bars->k_empty[kb]);   // this item's S^T are done with K
             // dP^T(g) = V dO_g^T once part 2 of step g-1 has read dP^T(g-1)
             if (g > 0 && !(ok = mbar_wait(&bars->ds_full, (uint32_t)(g - 1) & 1u, ctl))) break;
+            if (t == 0 && !(ok = mbar_wait(&bars->v_full, (uint32_t)nkv & 1u, ctl))) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -321,7 +301,8 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                      sdesc_sw128(sDO + st * 16384 + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), idST, k > 0 ? 1u : 0u);
             mma_commit(&bars->dp_full);
           }
-          mma_commit(&bars->kv_empty);    // this item's S^T and dP^T are done with K, V
+          mma_commit(&bars->v_empty);     // this item's dP^T are done with V
+          ++nkv;
         }
         mma_commit(&bars->done[0]);
         mbar_wait(&bars->done[0], 0, ctl);
@@ -378,12 +359,13 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (u < 0) break;
         const DItem it = make_item(a, u);
         if (it.steps == 0) continue;
+        const int kb = nkv & 1;
         const int live = it.Lk - it.jt * kTile;       // K rows of this tile that count
         if (live < kTile) {
-          if (!(ok = warp_wait(&bars->kv_full, (uint32_t)nkv & 1u, ctl))) break;
+          if (!(ok = warp_wait(&bars->k_full[kb], (uint32_t)(nkv >> 1) & 1u, ctl))) break;
           for (int o = live * 128 + lane * 16; o < 16384; o += 512) {
-            *reinterpret_cast<uint4*>(smem + L::kK + o) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + L::kK + 32768 + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + L::kK1 + kb * 16384 + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + L::kK2 + kb * 16384 + o) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -394,18 +376,23 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           if (g > 0 && !(ok = warp_wait(&bars->dq_free, (uint32_t)(g - 1) & 1u, ctl))) break;
           if (lane == 0) {
             tc_fence_after();
+            // the second 64 rows of A lie one leading offset behind the first: zeros
+            // behind K_1, K_2 behind the zeros
+            const uint32_t a1 = sK1 + kb * 16384, a2 = sK2 + kb * 16384;
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int k = 0; k < 8; ++k)
+              mma_ss(tmem + kColDQ, sdesc_sw128(a1 + k * 2048, sZ - a1, 1024), sdesc_sw128(sDS + k * 2048, 8192, 1024), idQ,
+                     k > 0 ? 1u : 0u);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ss(tmem + kColDQ, sdesc_sw128(sK + m * 16384 + k * 2048, 16384, 1024),
-                       sdesc_sw128(sDS + m * 16384 + k * 2048, 8192, 1024), idQ, (m > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 8; ++k)
+              mma_ss(tmem + kColDQ, sdesc_sw128(sZ + k * 2048, a2 - sZ, 1024),
+                     sdesc_sw128(sDS + 16384 + k * 2048, 8192, 1024), idQ, 1u);
             mma_commit(&bars->dq_full);
             mma_commit(&bars->dsm_free);
           }
           __syncwarp();
         }
-        if (lane == 0) mma_commit(&bars->kv_empty);   // this item's dQ^T products are done with K
+        if (lane == 0) mma_commit(&bars->k_empty[kb]);   // this item's dQ^T products are done with K
         __syncwarp();
       }
       if (lane == 0) {
@@ -425,9 +412,11 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int c0 = wg * 16;                   // first query column of this warpgroup
     bool ok = true;
 
-    // dQ_t: row r of the stacked dQ^T, this warpgroup's 16 queries -> x tau
-    // (fp16) -> float32 staging box r / 32 (128-byte rows of queries, 128-byte swizzle)
-    auto drain_dq = [&](int t) -> bool {
+    // dQ_t: row r of the stacked dQ^T, this warpgroup's 16 queries -> x tau (fp16)
+    // -> added to the float32 accumulator.  A warp's 32 lanes are 32 consecutive
+    // head dims of one query, so every add instruction is one 128-byte line.
+    // (qn: rows of the step that exist, counted from this warpgroup's first.)
+    auto drain_dq = [&](int t, float* dst, int qn) -> bool {
       if (!warp_wait(&bars->dq_full, (uint32_t)t & 1u, ctl)) return false;
       tc_fence_after();
       uint32_t g[16];
@@ -436,19 +425,16 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       reg_fence16(g);
       tc_fence_before();
       mbar_arrive(&bars->dq_free);
-      if (t >= 1 && !warp_wait(&bars->stg_free, (uint32_t)(t - 1) & 1u, ctl)) return false;
-      uint8_t* sb = smem + L::kDQ + quarter * 8192;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const int q = c0 + c;
-        const uint32_t off = q * 128 + ((((lane >> 2) ^ q) & 7) << 4) + (lane & 3) * 4;
         const float v = kFold ? __uint_as_float(g[c]) : __uint_as_float(g[c]) * a.scale;
-        asm volatile("st.shared.f32 [%0], %1;" :: "r"(smem_u32(sb + off)), "f"(v) : "memory");
+        if (c < qn) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" :: "l"(dst + c * 64), "f"(v) : "memory");
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->stg_full);
       return true;
     };
+    // this thread's place in the accumulator for the step whose dQ is drained next
+    float* dq_dst = nullptr;
+    int dq_n = 0;
 
     // dK (x tau for fp16) and dV of an item: columns 32 wg .. 32 wg + 31 of the
     // stacked (dK_1 | dK_2) row and of the dV row, in two halves of 16
@@ -631,7 +617,9 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           if (tt + 1 < it.steps) lam = a.lam[sp.hq + 1];
         }
         // ---- drain dQ of the previous step
-        if (t > 0 && !(ok = drain_dq(t - 1))) break;
+        if (t > 0 && !(ok = drain_dq(t - 1, dq_dst, dq_n))) break;
+        dq_dst = a.dqacc + (((size_t)it.b * 2 * a.H + 2 * sp.hq + (r >> 6)) * a.N + q0 + c0) * 64 + (r & 63);
+        dq_n = a.N - q0 - c0;
       }
       if (!ok) break;
       // ---- item end: dK, dV out of tensor memory (the next item's first dV /
@@ -651,7 +639,7 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
       tc_fence_before();
     }
-    if (ok && t > 0) ok = drain_dq(t - 1);
+    if (ok && t > 0) ok = drain_dq(t - 1, dq_dst, dq_n);
   }
 
   tc_fence_before();
@@ -746,7 +734,7 @@ __global__ void diff_dlam_kernel(const float* __restrict__ part, float* __restri
 
 template <typename T, bool kWin>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
-                     const CUtensorMap& dqacc, const DiffBwdArgs& a, cudaStream_t s) {
+                     const DiffBwdArgs& a, cudaStream_t s) {
   auto kern = diff_bwd_kernel<T, kWin>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DSmem::kDyn);
   if (e != cudaSuccess) return e;
@@ -755,7 +743,7 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<long long>(total, (long long)std::max(sms, 1));
-  kern<<<grid, kThreads, DSmem::kDyn, s>>>(q, k, v, dout, dqacc, a);
+  kern<<<grid, kThreads, DSmem::kDyn, s>>>(q, k, v, dout, a);
   return cudaGetLastError();
 }
 
@@ -782,12 +770,11 @@ cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides o
 }
 
 cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const CUtensorMap& dout, const CUtensorMap& dqacc, const DiffBwdArgs& a, cudaStream_t s) {
+                            const CUtensorMap& dout, const DiffBwdArgs& a, cudaStream_t s) {
   if (dtype == FA_DT_BF16)
-    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, dout, dqacc, a, s)
-                        : launch_t<__nv_bfloat16, false>(q, k, v, dout, dqacc, a, s);
-  return a.window > 0 ? launch_t<__half, true>(q, k, v, dout, dqacc, a, s)
-                      : launch_t<__half, false>(q, k, v, dout, dqacc, a, s);
+    return a.window > 0 ? launch_t<__nv_bfloat16, true>(q, k, v, dout, a, s)
+                        : launch_t<__nv_bfloat16, false>(q, k, v, dout, a, s);
+  return a.window > 0 ? launch_t<__half, true>(q, k, v, dout, a, s) : launch_t<__half, false>(q, k, v, dout, a, s);
 }
 
 cudaError_t launch_diff_dlam(const float* part, float* dlam, int B, int H, int group, int nq, cudaStream_t s) {

@@ -119,6 +119,7 @@ struct DiffBwdArgs {
   const int32_t* seqlens_k;
   const float* lam;
   const float* rows;          // [B*H][npad/64][4][64]: per 64 query rows the two maps' LSE*log2e, then e_1, e_2
+  float* dqacc;               // [B,2H,N,64] float32, cleared by the prepass
   float* dlam_part;           // [items * group][16]: per-warp sums of P_2 o dP
   void* dk;                   // [B,2H_kv,N,64], strides kst
   void* dv;                   // [B,H_kv,N,128], strides vst
@@ -176,7 +177,7 @@ cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides o
                              const float* lse, const float* lam, int B, int H, int N, int npad, float c1, float* rows,
                              float* dqacc, int* sched, cudaStream_t s);
 cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                            const CUtensorMap& dout, const CUtensorMap& dqacc, const DiffBwdArgs& a, cudaStream_t s);
+                            const CUtensorMap& dout, const DiffBwdArgs& a, cudaStream_t s);
 // dlam[h] = -sum of the partial sums, in a fixed order.
 cudaError_t launch_diff_dlam(const float* part, float* dlam, int B, int H, int group, int nq, cudaStream_t s);
 // Attention over a shared prefix: the workspace of a checked problem, and the launches.  m: maps of k_prefix,

@@ -8,8 +8,8 @@ read S(h-1) and the product of half h - 2 is done, which frees P(h)'s place, O i
 that of half h - 1; the two softmax groups meet before and after they read both accumulators.
 
 Backward (csrc/diff_bwd.cu): the roles of the d = 128 backward with a two-stage
-Q / dO ring, and W^T over S_1^T: the S issuer waits for dV(g-1) before S_1(g),
-the compute warps do not wait for it.
+Q / dO ring, K double-buffered per item and one V buffer, and W^T over S_1^T: the
+S issuer waits for dV(g-1) before S_1(g), the compute warps do not wait for it.
 
 tests/protocol_sim.py checks for deadlocks and for parity waits that pass early
 or alias; here also that nothing reads a buffer that is being refilled.
@@ -199,7 +199,6 @@ def test_forward_planted_mistakes_are_caught(plant):
 
 
 NQ = 2       # Q / dO ring stages
-KLAG = 3     # the dQ reduce of step g - KLAG follows the loads of step g
 
 
 class Backward:
@@ -210,12 +209,14 @@ class Backward:
         self.item_empty = [B("item_empty%d" % i, 4) for i in range(2)]
         self.q_full = [B("q_full%d" % i, 1) for i in range(NQ)]
         self.q_empty = [B("q_empty%d" % i, 1) for i in range(NQ)]
-        self.kv_full, self.kv_empty = B("kv_full", 1), B("kv_empty", 2)
-        for n in ("s_full", "p_full", "dp_full", "ds_full", "dq_full", "dq_free", "dkv_full", "pt_free", "stg_full",
-                  "stg_free"):
+        self.k_full = [B("k_full%d" % i, 1) for i in range(2)]
+        self.k_empty = [B("k_empty%d" % i, 1 if plant == "k_one_reader" else 2) for i in range(2)]   # S and dQ issuers
+        self.v_full, self.v_empty = B("v_full", 1), B("v_empty", 1)
+        self.k_read = {}
+        for n in ("s_full", "p_full", "dp_full", "ds_full", "dq_full", "dq_free", "dkv_full", "pt_free"):
             setattr(self, n, B(n, 1))
         self.dsm_free = B("dsm_free", 2)
-        self.mailbox, self.info = [None, None], [None] * 4
+        self.mailbox = [None, None]
         self.engine = Engine(rng)
         self.nloads = 0
 
@@ -227,41 +228,36 @@ class Backward:
         self.engine.later(("tma", self.nloads), bar)
 
     def producer(self):
-        st = {"g": 0, "rd": 0, "kf": 0, "next": 0, "nkv": 0}
-
-        def reduce_to(last):
-            while st["rd"] <= last:
-                r = st["rd"]
-                yield ("wait", self.stg_full, r)
-                if self.info[r & 3] != r:
-                    raise ProtocolError("step coordinates of %d overwritten before its reduce" % r)
-                self.stg_free.arrive()
-                st["rd"] += 1
-
-        while True:
-            yield from reduce_to(st["g"] - KLAG)
-            slot = st["kf"] & 1
-            yield ("wait", self.item_empty[slot], (st["kf"] >> 1) - 1)
-            u = st["next"] if st["next"] < len(self.items) else -1
-            st["next"] += 1
+        g = kf = nkv = 0
+        for u in list(range(len(self.items))) + [-1]:
+            slot = kf & 1
+            yield ("wait", self.item_empty[slot], (kf >> 1) - 1)
             self.mailbox[slot] = u
             self.item_full[slot].arrive()
-            st["kf"] += 1
-            if u < 0:
-                break
-            if self.items[u] == 0:
+            kf += 1
+            if u < 0 or self.items[u] == 0:
                 continue
-            yield ("wait", self.kv_empty, st["nkv"] - 1)
-            self.load(self.kv_full)
-            st["nkv"] += 1
-            for _ in range(self.items[u]):
-                g = st["g"]
+            yield ("wait", self.k_empty[nkv & 1], (nkv >> 1) - 1)
+            if nkv >= 2 and self.k_read.get(nkv - 2, 0) != 2:
+                raise ProtocolError("K of item %d refilled before both readers finished" % (nkv - 2))
+            self.load(self.k_full[nkv & 1])
+            for t in range(self.items[u]):
                 yield ("wait", self.q_empty[g % NQ], g // NQ - 1)
                 self.load(self.q_full[g % NQ])
-                self.info[g & 3] = g
-                yield from reduce_to(g - (KLAG - 3 if self.plant == "lag_too_short" else KLAG))
-                st["g"] += 1
-        yield from reduce_to(st["g"] - 1)
+                g += 1
+                if t == 0:
+                    if self.plant != "v_ungated":
+                        yield ("wait", self.v_empty, nkv - 1)
+                    if self.v_empty.completed < nkv:
+                        raise ProtocolError("V refilled under the last item's products")
+                    self.load(self.v_full)
+            nkv += 1
+        for t in range(max(0, g - NQ), g):
+            yield ("wait", self.q_full[t % NQ], t // NQ)
+        for t in range(max(0, nkv - 2), nkv):
+            yield ("wait", self.k_full[t & 1], t >> 1)
+        if nkv:
+            yield ("wait", self.v_full, nkv - 1)
 
     def fetch(self, kc):
         slot = kc & 1
@@ -279,9 +275,8 @@ class Backward:
                 return
             if self.items[u] == 0:
                 continue
-            yield ("wait", self.kv_full, nkv)
-            nkv += 1
-            for _ in range(self.items[u]):
+            yield ("wait", self.k_full[nkv & 1], nkv >> 1)
+            for t in range(self.items[u]):
                 if g > 0:
                     yield ("wait", self.p_full, g - 1)
                 yield ("wait", self.q_full[g % NQ], g // NQ)
@@ -290,11 +285,17 @@ class Backward:
                 if self.pt_free.completed < g:
                     raise ProtocolError("S_1(%d) written over W that dV still reads" % g)
                 self.commit("S", self.s_full)
+                if t == self.items[u] - 1:
+                    self.k_read[nkv] = self.k_read.get(nkv, 0) + 1
+                    self.commit("S", self.k_empty[nkv & 1])
                 if g > 0:
                     yield ("wait", self.ds_full, g - 1)
+                if t == 0:
+                    yield ("wait", self.v_full, nkv)
                 self.commit("S", self.dp_full)
                 g += 1
-            self.commit("S", self.kv_empty)
+            self.commit("S", self.v_empty)
+            nkv += 1
 
     def dvdk_issuer(self):
         kc = g = 0
@@ -325,8 +326,7 @@ class Backward:
             if self.items[u] == 0:
                 continue
             if self.items[u] % 2:                 # some items end inside a tile: K is cleaned first
-                yield ("wait", self.kv_full, nkv)
-            nkv += 1
+                yield ("wait", self.k_full[nkv & 1], nkv >> 1)
             for _ in range(self.items[u]):
                 yield ("wait", self.ds_full, g)
                 if g > 0:
@@ -334,7 +334,9 @@ class Backward:
                 self.commit("Q", self.dq_full)
                 self.commit("Q", self.dsm_free)
                 g += 1
-            self.commit("Q", self.kv_empty)
+            self.k_read[nkv] = self.k_read.get(nkv, 0) + 1
+            self.commit("Q", self.k_empty[nkv & 1])
+            nkv += 1
 
     def compute(self):
         t = nit = kc = 0
@@ -342,9 +344,6 @@ class Backward:
         def drain(r):
             yield ("wait", self.dq_full, r)
             self.dq_free.arrive()
-            if r >= 1:
-                yield ("wait", self.stg_free, r - 1)
-            self.stg_full.arrive()
 
         while True:
             u = yield from self.fetch(kc)
@@ -387,7 +386,7 @@ def test_backward_protocol():
             Backward(items, random.Random(seed)).run()
 
 
-@pytest.mark.parametrize("plant", ["s1_ungated", "lag_too_short"])
+@pytest.mark.parametrize("plant", ["s1_ungated", "k_one_reader", "v_ungated"])
 def test_backward_planted_mistakes_are_caught(plant):
     rng = random.Random(8)
     for trial in range(300):
