@@ -712,20 +712,25 @@ __global__ void diff_prep_kernel(const T* __restrict__ o, const T* __restrict__ 
 }
 
 // dlambda of head pair blockIdx.x: every item's and warp's part, in a fixed order.
-__global__ void diff_dlam_kernel(const float* __restrict__ part, float* __restrict__ dlam, int B, int H, int group,
-                                 int nq) {
-  __shared__ float sh[256];
-  const int h = blockIdx.x, hk = h / group, j = h % group, hkv = H / group;
-  const long long n = (long long)B * nq * 16;
+// Bound by the latency of its loads: 1,024 threads take an item's 16 sums in four
+// 16-byte pieces.
+__global__ void __launch_bounds__(1024) diff_dlam_kernel(const float* __restrict__ part, float* __restrict__ dlam, int B,
+                                                         int H, int group, int nq) {
+  __shared__ float sh[1024];
+  const int h = blockIdx.x, hk = h / group, j = h - hk * group, hkv = H / group;
+  const int n = B * nq;                       // items of this head pair's K/V pair (total items fit an int)
   float s = 0.f;
-  for (long long e = threadIdx.x; e < n; e += 256) {
-    const long long it = e >> 4;
-    const long long b = it / nq, jt = it - b * nq;
-    s += part[(((b * hkv + hk) * nq + jt) * group + j) * 16 + (e & 15)];
+#pragma unroll 4
+  for (int e = threadIdx.x; e < 4 * n; e += 1024) {
+    const int it = e >> 2;
+    const int b = it / nq, jt = it - b * nq;
+    const float4 v = *reinterpret_cast<const float4*>(
+        part + ((((size_t)b * hkv + hk) * nq + jt) * group + j) * 16 + (e & 3) * 4);
+    s += (v.x + v.y) + (v.z + v.w);
   }
   sh[threadIdx.x] = s;
   __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
+  for (int o = 512; o > 0; o >>= 1) {
     if (threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
     __syncthreads();
   }
@@ -778,7 +783,7 @@ cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& 
 }
 
 cudaError_t launch_diff_dlam(const float* part, float* dlam, int B, int H, int group, int nq, cudaStream_t s) {
-  diff_dlam_kernel<<<H, 256, 0, s>>>(part, dlam, B, H, group, nq);
+  diff_dlam_kernel<<<H, 1024, 0, s>>>(part, dlam, B, H, group, nq);
   return cudaGetLastError();
 }
 
