@@ -340,10 +340,10 @@ class fa_prefix_params(ctypes.Structure):
     _fields_ = ([(n, _i32) for n in ("B", "H", "H_kv", "T", "P", "M", "d", "dtype")] +
                 [("scale", _f32), ("seqlens_k", _vp)] +
                 [("%s_stride_%s" % (t, x), _i64) for t in ("q", "o", "k", "v") for x in "bhn"] +
-                [("%s_stride_%s" % (t, x), _i64) for t in ("kp", "vp") for x in "hn"])
+                [("%s_stride_%s" % (t, x), _i64) for t in ("kp", "vp") for x in "hn"] + [("lam", _vp)])
 
 
-def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, out=None, workspace=None, stream=None):
+def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, lam=None, scale=None, out=None, workspace=None, stream=None):
     """Attention of B sequences that share a prefix (fa_prefix_fwd): (o, lse).
 
     q [B,H,T,d] holds the T new tokens of each sequence (T = 1: one decoding
@@ -352,10 +352,20 @@ def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, out=None, 
     filled, the new tokens' included.  Query t sees the whole prefix and the
     own keys j <= seqlens_k[b] - T + t.  P = 0 is plain cached attention;
     k_prefix, v_prefix (or k, v) may then be None.  o [B,H,T,d], lse float32
-    [B,H,T].  ``out`` = (o, lse)."""
+    [B,H,T].  ``out`` = (o, lse).
+
+    With ``lam`` (float32 [H]) it is :func:`diff_fwd`'s step for few tokens: q
+    [B,2H,T,64], k_prefix [2H_kv,P,64], k [B,2H_kv,M,64], v_prefix
+    [H_kv,P,128], v [B,H_kv,M,128], o [B,H,T,128], lse [B,2H,T]."""
     _check4(q, "q")
-    B, H, T, d = q.shape
+    B, SH, T, d = q.shape
     dev = q.device
+    maps = 1 if lam is None else 2            # score heads per head
+    H, dv = SH // maps, maps * d
+    if lam is not None:
+        if SH % 2 or d != 64:
+            raise ValueError("with lam, q must be [B, 2H, T, 64]")
+        _flat_f32(lam, "lam", dev, (H,))
     if (k is None) != (v is None) or (k_prefix is None) != (v_prefix is None):
         raise ValueError("k and v, and k_prefix and v_prefix, come together")
     P = M = 0
@@ -363,10 +373,10 @@ def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, out=None, 
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k, v must be [B, H_kv, M, d]")
-        Hkv, M = k.shape[1], k.shape[2]
-        ks, vs = _rows(k, "k", q, (B, Hkv, M, d)), _rows(v, "v", q, (B, Hkv, M, d))
+        Hkv, M = k.shape[1] // maps, k.shape[2]
+        ks, vs = _rows(k, "k", q, (B, maps * Hkv, M, d)), _rows(v, "v", q, (B, Hkv, M, dv))
     elif k_prefix is not None:
-        Hkv = k_prefix.shape[0]
+        Hkv = k_prefix.shape[0] // maps
     else:
         raise ValueError("neither a prefix nor caches given")
     if Hkv < 1 or H % Hkv:
@@ -375,21 +385,23 @@ def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, out=None, 
         if k_prefix.dim() != 3:
             raise ValueError("k_prefix, v_prefix must be [H_kv, P, d]")
         P = k_prefix.shape[1]
-        kps, vps = _rows(k_prefix, "k_prefix", q, (Hkv, P, d)), _rows(v_prefix, "v_prefix", q, (Hkv, P, d))
+        kps = _rows(k_prefix, "k_prefix", q, (maps * Hkv, P, d))
+        vps = _rows(v_prefix, "v_prefix", q, (Hkv, P, dv))
     if seqlens_k is None:
         raise ValueError("seqlens_k must be given")
     with _on(dev, stream) as raw:
         lens = _lens(seqlens_k, B, dev)
         if out is None:
-            o = torch.empty((B, H, T, d), device=dev, dtype=q.dtype)
-            lse = torch.empty((B, H, T), device=dev, dtype=torch.float32)
+            o = torch.empty((B, H, T, dv), device=dev, dtype=q.dtype)
+            lse = torch.empty((B, SH, T), device=dev, dtype=torch.float32)
             os = o.stride()
         else:
             o, lse = out
-            os = _rows(o, "out o", q, q.shape)
-            _flat_f32(lse, "out lse", dev, (B, H, T))
+            os = _rows(o, "out o", q, (B, H, T, dv))
+            _flat_f32(lse, "out lse", dev, (B, SH, T))
         p = fa_prefix_params(B, H, Hkv, T, P, M, d, DTYPE_CODE[q.dtype], 0.0 if scale is None else float(scale),
-                             lens.data_ptr(), *q.stride()[:3], *os[:3], *ks[:3], *vs[:3], *kps[:2], *vps[:2])
+                             lens.data_ptr(), *q.stride()[:3], *os[:3], *ks[:3], *vs[:3], *kps[:2], *vps[:2],
+                             None if lam is None else lam.data_ptr())
         a = ctypes.addressof(p)
         ws = _need_workspace(workspace, _size_of("fa_prefix_workspace_size")(a), dev)
         st = _sized("fa_prefix_fwd", 9)(a, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), o.data_ptr(),

@@ -360,9 +360,12 @@ fa_status check_prefix(const fa_prefix_params* in, fa_prefix_params& p, PrefixSt
   if (p.B < 1 || p.H < 1 || p.T < 1 || p.d < 1 || p.H_kv < 0 || p.P < 0 || p.M < 0) return FA_ERR_INVALID_ARG;
   if (p.dtype != FA_DT_F32 && p.dtype != FA_DT_F16 && p.dtype != FA_DT_BF16) return FA_ERR_INVALID_ARG;
   if ((p.d != 64 && p.d != 128) || p.dtype == FA_DT_F32) return FA_ERR_UNSUPPORTED;
+  if (p.lam != nullptr && p.d != 64) return FA_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(p.lam) & 3u) return FA_ERR_MISALIGNED;
+  const int maps = p.lam != nullptr ? 2 : 1, dv = maps * p.d;      // score heads per head, value columns
   if (p.H_kv == 0) p.H_kv = p.H;
   if (p.H % p.H_kv != 0) return FA_ERR_INVALID_ARG;
-  if ((double)p.B * p.H * p.T >= (double)(1 << 26) || p.P > (1 << 28) || p.M > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  if ((double)maps * p.B * p.H * p.T >= (double)(1 << 26) || p.P > (1 << 28) || p.M > (1 << 28)) return FA_ERR_UNSUPPORTED;
   s.q = {p.q_stride_b, p.q_stride_h, p.q_stride_n};
   s.o = {p.o_stride_b, p.o_stride_h, p.o_stride_n};
   s.k = {p.k_stride_b, p.k_stride_h, p.k_stride_n};
@@ -370,13 +373,13 @@ fa_status check_prefix(const fa_prefix_params* in, fa_prefix_params& p, PrefixSt
   s.kp = {0, p.kp_stride_h, p.kp_stride_n};
   s.vp = {0, p.vp_stride_h, p.vp_stride_n};
   fa_status e;
-  if ((e = row_strides(s.q, p.B, p.H, p.T, p.d)) != FA_OK || (e = row_strides(s.o, p.B, p.H, p.T, p.d)) != FA_OK)
+  if ((e = row_strides(s.q, p.B, maps * p.H, p.T, p.d)) != FA_OK || (e = row_strides(s.o, p.B, p.H, p.T, dv)) != FA_OK)
     return e;
-  if (p.M > 0 && ((e = row_strides(s.k, p.B, p.H_kv, p.M, p.d)) != FA_OK ||
-                  (e = row_strides(s.v, p.B, p.H_kv, p.M, p.d)) != FA_OK))
+  if (p.M > 0 && ((e = row_strides(s.k, p.B, maps * p.H_kv, p.M, p.d)) != FA_OK ||
+                  (e = row_strides(s.v, p.B, p.H_kv, p.M, dv)) != FA_OK))
     return e;
-  if (p.P > 0 && ((e = row_strides(s.kp, 1, p.H_kv, p.P, p.d)) != FA_OK ||
-                  (e = row_strides(s.vp, 1, p.H_kv, p.P, p.d)) != FA_OK))
+  if (p.P > 0 && ((e = row_strides(s.kp, 1, maps * p.H_kv, p.P, p.d)) != FA_OK ||
+                  (e = row_strides(s.vp, 1, p.H_kv, p.P, dv)) != FA_OK))
     return e;
   return FA_OK;
 }
@@ -749,18 +752,19 @@ fa_status fa_prefix_fwd(const fa_prefix_params* in, const void* q, const void* k
     return FA_ERR_MISALIGNED;
   if (ws == nullptr || !aligned16(ws) || ws_bytes < prefix_workspace(&p)) return FA_ERR_WORKSPACE;
   CUtensorMap m[4] = {};
+  const int maps = p.lam != nullptr ? 2 : 1;
   const CUtensorMapDataType dt =
       p.dtype == FA_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   fa_params bn{};
   bn.B = 1;
   bn.N = p.P;
-  if (p.P > 0 && ((s = make_map(&m[0], k_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.kp, 32)) != FA_OK ||
-                  (s = make_map(&m[1], v_prefix, dt, 2, p.d, 64, &bn, p.H_kv, sd.vp, 32)) != FA_OK))
+  if (p.P > 0 && ((s = make_map(&m[0], k_prefix, dt, 2, p.d, 64, &bn, maps * p.H_kv, sd.kp, 32)) != FA_OK ||
+                  (s = make_map(&m[1], v_prefix, dt, 2, maps * p.d, 64, &bn, p.H_kv, sd.vp, 32)) != FA_OK))
     return s;
   bn.B = p.B;
   bn.N = p.M;
-  if (p.M > 0 && ((s = make_map(&m[2], k, dt, 2, p.d, 64, &bn, p.H_kv, sd.k, 32)) != FA_OK ||
-                  (s = make_map(&m[3], v, dt, 2, p.d, 64, &bn, p.H_kv, sd.v, 32)) != FA_OK))
+  if (p.M > 0 && ((s = make_map(&m[2], k, dt, 2, p.d, 64, &bn, maps * p.H_kv, sd.k, 32)) != FA_OK ||
+                  (s = make_map(&m[3], v, dt, 2, maps * p.d, 64, &bn, p.H_kv, sd.v, 32)) != FA_OK))
     return s;
   const float scale = (p.scale > 0.f && std::isfinite(p.scale)) ? p.scale : 1.f / std::sqrt((float)p.d);
   return cuda_status(launch_prefix(&p, m, q, sd.q, o, sd.o, lse, scale * 1.4426950408889634f,

@@ -36,22 +36,21 @@ constexpr int kPThreads = 160;   // warps 0-3 compute, 4 TMA
 constexpr int kSms = 152;        // the plan's SM count: a workspace's size does not depend on the device at hand
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D> struct PCfg {
-  static constexpr int NB = D / 64;                  // 64-column boxes per row
+template <int D, int DV> struct PCfg {               // columns of q and k, and of v and o
   static constexpr int KS = D == 64 ? 64 : 32;       // keys of a stage
   static constexpr int kBox = KS * 128;              // one 64-column box of a stage
-  static constexpr int kTile = KS * D * 2;           // one K or V stage
+  static constexpr int kKTile = KS * D * 2, kVTile = KS * DV * 2;   // one stage
   static constexpr int NS = 4;                       // a multiple of 4: with split keys stage s is warp s % 4's
-  static constexpr int kCtas = D == 64 ? 3 : 2;      // CTAs per SM
+  static constexpr int kCtas = DV == 64 ? 3 : 2;     // CTAs per SM
   static constexpr int kK = 0;
-  static constexpr int kV = NS * kTile;
-  static constexpr int kJoin = kV + NS * kTile;      // [2][16][D] O and [2][16] statistics of two warps
-  static constexpr int kBar = kJoin + 2 * 16 * (D * 4 + 16);
+  static constexpr int kV = NS * kKTile;
+  static constexpr int kJoin = kV + NS * kVTile;     // [2][16][DV] O and [2][16] statistics of two warps
+  static constexpr int kBar = kJoin + 2 * 16 * (DV * 4 + 16);
   static constexpr int kItem = kBar + 256;           // two published items
   static constexpr int kBytes = kItem + 128;
 };
-static_assert(PCfg<64>::kCtas * (PCfg<64>::kBytes + 1024) <= 233472 && PCfg<128>::kCtas * (PCfg<128>::kBytes + 1024) <= 233472,
-              "the CTAs of one SM exceed its shared memory");
+template <int D, int DV> constexpr bool fits() { return PCfg<D, DV>::kCtas * (PCfg<D, DV>::kBytes + 1024) <= 233472; }
+static_assert(fits<64, 64>() && fits<128, 128>() && fits<64, 128>(), "the CTAs of one SM exceed its shared memory");
 
 struct PBars {
   uint64_t full[4], empty[4];
@@ -127,14 +126,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 // State of 16 query rows in one warp: thread (lane / 4, lane % 4) holds rows
 // lane / 4 and lane / 4 + 8, columns 2 (lane % 4) + {0, 1} of every 8.
-template <typename T, int D> struct Rows {
+template <typename T, int D, int DV> struct Rows {
   uint32_t q[D / 16][4];
-  float o[D / 8][4];
+  float o[DV / 8][4];
   float m[2], lt[2], lr[2];
 
   __device__ __forceinline__ void init() {
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < DV / 8; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     m[0] = m[1] = -INFINITY;
@@ -155,7 +154,7 @@ template <typename T, int D> struct Rows {
   // row; kend: V rows at or past it may hold anything.
   __device__ __forceinline__ void step(uint32_t sK, uint32_t sV, int key0, const int (&lim)[2], int kend, float sl2,
                                        int lane) {
-    constexpr int NK = PCfg<D>::KS, kBox = PCfg<D>::kBox;
+    constexpr int NK = PCfg<D, DV>::KS, kBox = PCfg<D, DV>::kBox;
     float s[NK / 8][4];
 #pragma unroll
     for (int n = 0; n < NK / 8; ++n)
@@ -212,7 +211,7 @@ template <typename T, int D> struct Rows {
         lt[x] *= alpha[x];
         lr[x] *= alpha[x];
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
+        for (int n = 0; n < DV / 8; ++n) {
           o[n][2 * x] *= alpha[x];
           o[n][2 * x + 1] *= alpha[x];
         }
@@ -246,10 +245,10 @@ template <typename T, int D> struct Rows {
     else pv<false>(sV, p, 0, lane);
   }
   template <bool kTail>
-  __device__ __forceinline__ void pv(uint32_t sV, const uint32_t (&p)[PCfg<D>::KS / 16][4], int live, int lane) {
+  __device__ __forceinline__ void pv(uint32_t sV, const uint32_t (&p)[PCfg<D, DV>::KS / 16][4], int live, int lane) {
     const int lr_ = lane & 7, lm = lane >> 3;
 #pragma unroll
-    for (int k = 0; k < PCfg<D>::KS / 16; ++k) {
+    for (int k = 0; k < PCfg<D, DV>::KS / 16; ++k) {
       // register pairs hold keys kp, kp + 1 and kp + 8, kp + 9
       uint32_t z0 = ~0u, z1 = ~0u;
       if (kTail) {
@@ -258,12 +257,12 @@ template <typename T, int D> struct Rows {
         z1 = (kp + 8 < live ? 0xFFFFu : 0u) | (kp + 9 < live ? 0xFFFF0000u : 0u);
       }
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
+      for (int n = 0; n < DV / 16; ++n) {
         // matrices: keys 0-7 / 8-15 (lm & 1), columns 0-7 / 8-15 (lm >> 1)
         const uint32_t row = k * 16 + (lm & 1) * 8 + lr_;
         const uint32_t col = (n & 3) * 16 + (lm >> 1) * 8;
         uint32_t b[4];
-        ldsm4t(b, sV + (n >> 2) * PCfg<D>::kBox + sw128_off(row, col));
+        ldsm4t(b, sV + (n >> 2) * PCfg<D, DV>::kBox + sw128_off(row, col));
         if (kTail) {
           b[0] &= z0; b[1] &= z1; b[2] &= z0; b[3] &= z1;
         }
@@ -277,9 +276,9 @@ template <typename T, int D> struct Rows {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int row = (lane >> 2) + 8 * x;
-      float* dst = so + row * D + 2 * (lane & 3);
+      float* dst = so + row * DV + 2 * (lane & 3);
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+      for (int n = 0; n < DV / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
       if ((lane & 3) == 0) ss[row] = make_float4(m[x], lt[x], lr[x], 0.f);
     }
   }
@@ -293,9 +292,9 @@ template <typename T, int D> struct Rows {
       m[x] = m_new;
       lt[x] = lt[x] * fa_ + st.y * fb;
       lr[x] = lr[x] * fa_ + st.z * fb;
-      const float* src = so + row * D + 2 * (lane & 3);
+      const float* src = so + row * DV + 2 * (lane & 3);
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
+      for (int n = 0; n < DV / 8; ++n) {
         const float2 v = *reinterpret_cast<const float2*>(src + n * 8);
         o[n][2 * x] = o[n][2 * x] * fa_ + v.x * fb;
         o[n][2 * x + 1] = o[n][2 * x + 1] * fa_ + v.y * fb;
@@ -313,11 +312,12 @@ template <typename T, int D> struct Rows {
   }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kPThreads, PCfg<D>::kCtas)
+template <typename T, int D, int DV>
+__global__ void __launch_bounds__(kPThreads, (PCfg<D, DV>::kCtas))
 prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ CUtensorMap tmVP,
               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PArgs a) {
-  using C = PCfg<D>;
+  using C = PCfg<D, DV>;
+  constexpr bool kDiff = D != DV;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {       // the 128-byte swizzle's tiles: see diff_fwd.cu
@@ -371,15 +371,16 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
         for (int t = 0; t < it.nt; ++t, ++g) {
           const int st = g % NS;
           if (g >= NS && !(ok = mbar_wait(&bars->empty[st], (uint32_t)(g / NS - 1) & 1u, ctl))) break;
-          mbar_expect_tx(&bars->full[st], 2 * C::kTile);
+          mbar_expect_tx(&bars->full[st], C::kKTile + C::kVTile);
 #pragma unroll
-          for (int c = 0; c < C::NB; ++c)
+          for (int c = 0; c < DV / 64; ++c)
 #pragma unroll
             for (int x = 0; x < C::KS; x += kKT) {
-              const int row = it.k0 + t * C::KS + x;
-              uint8_t* dst = smem + st * C::kTile + c * C::kBox + x * 128;
-              tma_load_4d(dst + C::kK, mk, &bars->full[st], c * 64, row, it.hk, it.b);
-              tma_load_4d(dst + C::kV, mv, &bars->full[st], c * 64, row, it.hk, it.b);
+              const int row = it.k0 + t * C::KS + x, at = c * C::kBox + x * 128;
+              if (c < D / 64)
+                tma_load_4d(smem + C::kK + st * C::kKTile + at, mk, &bars->full[st], c * 64, row, it.hk, it.b);
+              tma_load_4d(smem + C::kV + st * C::kVTile + at, mv, &bars->full[st], c * 64, row, value_head<kDiff>(it.hk),
+                          it.b);
             }
         }
       }
@@ -390,8 +391,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
   }
 
   // ===================== compute warps =====================
-  float* so = reinterpret_cast<float*>(smem + C::kJoin);              // [2][16][D]
-  float4* ss = reinterpret_cast<float4*>(so + 2 * 16 * D);            // [2][16]
+  float* so = reinterpret_cast<float*>(smem + C::kJoin);              // [2][16][DV]
+  float4* ss = reinterpret_cast<float4*>(so + 2 * 16 * DV);            // [2][16]
   // barrier of the four compute warps: bounded like every wait, so that a warp
   // that gave up leaves none behind
   int nj = 0;
@@ -412,7 +413,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
     const int rgs = it.tile >> 4, kgs = 4 / rgs;
     const int rg = warp & (rgs - 1), kg = warp / rgs;
     const int rbase = it.rt * it.tile + rg * 16 + (lane >> 2);
-    Rows<T, D> w;
+    Rows<T, D, DV> w;
     w.init();
     int lim[2] = {0, 0};
     const T* qr[2];
@@ -421,7 +422,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
       const int row = rbase + 8 * x;
       qr[x] = nullptr;
       if (row < it.rows) {
-        qr[x] = prefix_row<T>(a, it.hk, it.shared ? row : it.b * a.r + row);
+        qr[x] = prefix_row<T, kDiff>(a, it.hk, it.shared ? row : it.b * a.r + row);
         lim[x] = it.shared ? a.P : it.end - a.T + row % a.T + 1;
       }
     }
@@ -435,7 +436,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
       // warps together.
       if ((st & (kgs - 1)) != kg) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[st], (uint32_t)(g / NS) & 1u, ctl))) return;
-      const uint32_t sK = smem_u32(smem + C::kK + st * C::kTile), sV = smem_u32(smem + C::kV + st * C::kTile);
+      const uint32_t sK = smem_u32(smem + C::kK + st * C::kKTile), sV = smem_u32(smem + C::kV + st * C::kVTile);
       if (!idle) w.step(sK, sV, it.k0 + t * C::KS, lim, it.kend, a.scale_log2, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive_n(&bars->empty[st], kgs);
@@ -444,9 +445,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
     // ---- join the key groups: warps 2, 3 into 0, 1, then (one row group) 1 into 0
 #pragma unroll 1
     for (int half = 2; half >= rgs; half >>= 1) {
-      if (warp >= half && warp < 2 * half) w.put(so + (warp - half) * 16 * D, ss + (warp - half) * 16, lane);
+      if (warp >= half && warp < 2 * half) w.put(so + (warp - half) * 16 * DV, ss + (warp - half) * 16, lane);
       if (!meet()) return;
-      if (warp < half) w.join(so + warp * 16 * D, ss + warp * 16, lane);
+      if (warp < half) w.join(so + warp * 16 * DV, ss + warp * 16, lane);
       if (!meet()) return;
     }
     if (kg != 0) continue;
@@ -457,117 +458,128 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
     for (int x = 0; x < 2; ++x) {
       const int row = rbase + 8 * x;
       if (row >= it.rows) continue;
-      float* dst = a.part + (prow0 + row) * D + 2 * (lane & 3);
+      float* dst = a.part + (prow0 + row) * DV + 2 * (lane & 3);
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(w.o[n][2 * x], w.o[n][2 * x + 1]);
+      for (int n = 0; n < DV / 8; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(w.o[n][2 * x], w.o[n][2 * x + 1]);
       if ((lane & 3) == 0) a.stat[prow0 + row] = make_float4(w.m[x], w.lt[x], w.lr[x], 0.f);
     }
   }
 }
 
 // Joins the splits of each query row: W warps per row (1 for few splits, else 4),
-// D / 32 columns a lane.  The lanes fetch the splits' statistics side by side,
-// then every split's row is an independent load.  Launched to overlap the end of
+// DV / 32 columns a lane.  The lanes fetch the splits' statistics side by side,
+// then every split's row is an independent load.  The differential form joins
+// both maps' rows and leaves their difference.  Launched to overlap the end of
 // the kernel before it (griddepcontrol.wait before the first read of its rows).
-template <typename T, int D, int W>
+template <typename T, int DV, int W, bool kDiff>
 __global__ void __launch_bounds__(128) prefix_join_kernel(const PArgs a, T* __restrict__ o, Strides os,
                                                           float* __restrict__ lse) {
-  constexpr int E = D / 32;
-  __shared__ float sh[W == 1 ? 1 : 4][W == 1 ? 1 : D + 3];
+  constexpr int E = DV / 32;
+  __shared__ float sh[W == 1 ? 1 : 4][W == 1 ? 1 : DV + 3];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = W == 1 ? (int)(blockIdx.x * 4 + warp) : (int)blockIdx.x;       // B H T < 2^26
   const int w0 = W == 1 ? 0 : warp;
-  const bool live = row < a.B * a.H * a.T;
+  const int OH = kDiff ? a.H / 2 : a.H;                                          // heads of o
+  const bool live = row < a.B * OH * a.T;
   const int bh = live ? row / a.T : 0, t = live ? row - bh * a.T : 0;
-  const int b = bh / a.H, h = bh - b * a.H;
-  const int hk = h / a.G, j = h - hk * a.G;
+  const int b = bh / OH, h = bh - b * OH;
+  const int p = h / a.G, j = h - p * a.G;                                        // K/V head (pair) and place in its group
   const int len = max(0, min(a.M, a.lens[b]));
   const int n = live ? a.np + (len + a.schunk - 1) / a.schunk : 0;
   const long long prow = ((long long)b * a.G + j) * a.T + t;             // row of the prefix items
-  const long long own = a.srow0 + (((long long)b * a.Hkv + hk) * a.ns) * a.r + (long long)j * a.T + t;
-  auto at = [&](int s) -> long long {
-    return s < a.np ? ((long long)s * a.Hkv + hk) * a.R + prow : own + (long long)(s - a.np) * a.r;
-  };
+  float out[E] = {};
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float m = -INFINITY, acc[E] = {}, lt = 0.f, lr = 0.f;
-  // this warp's splits: w0, w0 + W, ...; 32 statistics at a time
-  for (int s0 = w0; s0 < n; s0 += 32 * W) {
-    const int cnt = min(32, (n - s0 + W - 1) / W);
-    const float4 st = lane < cnt ? a.stat[at(s0 + lane * W)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    float mx = st.x;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-    const float m_new = fmaxf(m, mx);
-    const float old = m == -INFINITY ? 0.f : ex2(m - m_new);
-    m = m_new;
-    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - m);
-    float ft = f * st.y, fr = f * st.z;
+  for (int x = 0; x < (kDiff ? 2 : 1); ++x) {
+    const int hk = kDiff ? 2 * p + x : p;
+    const long long own = a.srow0 + (((long long)b * a.Hkv + hk) * a.ns) * a.r + (long long)j * a.T + t;
+    auto at = [&](int s) -> long long {
+      return s < a.np ? ((long long)s * a.Hkv + hk) * a.R + prow : own + (long long)(s - a.np) * a.r;
+    };
+    float m = -INFINITY, acc[E] = {}, lt = 0.f, lr = 0.f;
+    // this warp's splits: w0, w0 + W, ...; 32 statistics at a time
+    for (int s0 = w0; s0 < n; s0 += 32 * W) {
+      const int cnt = min(32, (n - s0 + W - 1) / W);
+      const float4 st = lane < cnt ? a.stat[at(s0 + lane * W)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      float mx = st.x;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-      ft += __shfl_xor_sync(0xffffffffu, ft, x);
-      fr += __shfl_xor_sync(0xffffffffu, fr, x);
-    }
-    lt = lt * old + ft;
-    lr = lr * old + fr;
+      for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+      const float m_new = fmaxf(m, mx);
+      const float old = m == -INFINITY ? 0.f : ex2(m - m_new);
+      m = m_new;
+      const float f = st.x == -INFINITY ? 0.f : ex2(st.x - m);
+      float ft = f * st.y, fr = f * st.z;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= old;
-    for (int s1 = 0; s1 < cnt; s1 += 8) {
-      float v[8][E];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const float* src = a.part + at(s0 + min(s1 + s, cnt - 1) * W) * D + lane * E;
-        if constexpr (E == 2) *reinterpret_cast<float2*>(v[s]) = *reinterpret_cast<const float2*>(src);
-        else *reinterpret_cast<float4*>(v[s]) = *reinterpret_cast<const float4*>(src);
+      for (int y = 16; y > 0; y >>= 1) {
+        ft += __shfl_xor_sync(0xffffffffu, ft, y);
+        fr += __shfl_xor_sync(0xffffffffu, fr, y);
       }
+      lt = lt * old + ft;
+      lr = lr * old + fr;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const float fs = __shfl_sync(0xffffffffu, f, (s1 + s) & 31);
-        if (s1 + s < cnt) {
+      for (int e = 0; e < E; ++e) acc[e] *= old;
+      for (int s1 = 0; s1 < cnt; s1 += 8) {
+        float v[8][E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += fs * v[s][e];
+        for (int s = 0; s < 8; ++s) {
+          const float* src = a.part + at(s0 + min(s1 + s, cnt - 1) * W) * DV + lane * E;
+          if constexpr (E == 2) *reinterpret_cast<float2*>(v[s]) = *reinterpret_cast<const float2*>(src);
+          else *reinterpret_cast<float4*>(v[s]) = *reinterpret_cast<const float4*>(src);
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const float fs = __shfl_sync(0xffffffffu, f, (s1 + s) & 31);
+          if (s1 + s < cnt) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += fs * v[s][e];
+          }
         }
       }
     }
-  }
-  if constexpr (W > 1) {
-    // the four warps' parts, in warp order
+    if constexpr (W > 1) {
+      // the four warps' parts, in warp order
+      if (x > 0) __syncthreads();          // the first map's parts have been read
 #pragma unroll
-    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = acc[e];
-    if (lane == 0) {
-      sh[warp][D] = m; sh[warp][D + 1] = lt; sh[warp][D + 2] = lr;
+      for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = acc[e];
+      if (lane == 0) {
+        sh[warp][DV] = m; sh[warp][DV + 1] = lt; sh[warp][DV + 2] = lr;
+      }
+      __syncthreads();
+      float mm = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) mm = fmaxf(mm, sh[g][DV]);
+      lt = lr = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float f = sh[g][DV] == -INFINITY ? 0.f : ex2(sh[g][DV] - mm);
+        lt += f * sh[g][DV + 1];
+        lr += f * sh[g][DV + 2];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += f * sh[g][lane * E + e];
+      }
+      m = mm;
     }
-    __syncthreads();
-    if (warp != 0) return;
-    float mm = -INFINITY;
+    const float inv = lr > 0.f ? 1.f / lr : 0.f;
+    const float c = x == 0 ? inv : -a.lam[h] * inv;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) mm = fmaxf(mm, sh[g][D]);
-    lt = lr = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float f = sh[g][D] == -INFINITY ? 0.f : ex2(sh[g][D] - mm);
-      lt += f * sh[g][D + 1];
-      lr += f * sh[g][D + 2];
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * sh[g][lane * E + e];
-    }
-    m = mm;
+    for (int e = 0; e < E; ++e) out[e] += c * acc[e];
+    if (live && lane == 0 && (W == 1 || warp == 0))
+      lse[((long long)b * a.H + (kDiff ? 2 * h + x : h)) * a.T + t] = lt > 0.f ? (m + lg2(lt)) * kLn2 : -INFINITY;
   }
-  if (!live) return;
-  const float inv = lr > 0.f ? 1.f / lr : 0.f;
+  if (!live || (W > 1 && warp != 0)) return;
   T* dst = o + (int64_t)b * os.b + (int64_t)h * os.h + (int64_t)t * os.n + lane * E;
   uint32_t w[E / 2];
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) w[e] = Cvt<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int e = 0; e < E / 2; ++e) w[e] = Cvt<T>::pack(out[2 * e], out[2 * e + 1]);
   if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
   else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  if (lane == 0) lse[row] = lt > 0.f ? (m + lg2(lt)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int D, int W>
+template <typename T, int DV, int W, bool kDiff>
 cudaError_t launch_join(const PArgs& a, void* o, Strides os, float* lse, cudaStream_t s) {
-  const int rows = a.B * a.H * a.T;
+  const int rows = a.B * (kDiff ? a.H / 2 : a.H) * a.T;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)(W == 1 ? (rows + 3) / 4 : rows));
   c.blockDim = dim3(128);
@@ -577,7 +589,7 @@ cudaError_t launch_join(const PArgs& a, void* o, Strides os, float* lse, cudaStr
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, prefix_join_kernel<T, D, W>, a, static_cast<T*>(o), os, lse);
+  return cudaLaunchKernelEx(&c, prefix_join_kernel<T, DV, W, kDiff>, a, static_cast<T*>(o), os, lse);
 }
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -594,7 +606,9 @@ int row_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // out), but no shorter than four units.
 void plan(const fa_prefix_params* p, PArgs& a) {
   constexpr int kU = 64;
-  a.B = p->B; a.H = p->H; a.Hkv = p->H_kv; a.T = p->T; a.G = p->H / p->H_kv;
+  const int maps = p->lam != nullptr ? 2 : 1;      // score heads per head
+  a.B = p->B; a.H = maps * p->H; a.Hkv = maps * p->H_kv; a.T = p->T; a.G = p->H / p->H_kv;
+  a.lam = p->lam;
   a.P = p->P; a.M = p->M;
   a.r = a.G * a.T;
   a.R = a.B * a.r;
@@ -606,7 +620,7 @@ void plan(const fa_prefix_params* p, PArgs& a) {
   const int pw = a.ptile / 16, sw = a.stile / 16;
   const long long wp = a.ptile == 256 ? 0 : (long long)a.Hkv * a.pt * kp * pw;
   const long long wsuf = (long long)a.B * a.Hkv * a.st * ks * sw;
-  const long long items = 3ll * kSms * (p->d == 64 ? PCfg<64>::kCtas : PCfg<128>::kCtas);
+  const long long items = 3ll * kSms * (p->d == 64 && maps == 1 ? PCfg<64, 64>::kCtas : PCfg<128, 128>::kCtas);
   const long long share = (wp + wsuf + items - 1) / items;
   long long pc = std::max<long long>(8, share / pw);
   const long long sc = std::max<long long>(4, share / sw);
@@ -625,7 +639,7 @@ void plan(const fa_prefix_params* p, PArgs& a) {
 }
 
 struct PLayout { size_t status, stat, part, total; };
-PLayout playout(const PArgs& a, int d) {
+PLayout playout(const PArgs& a, int d) {      // d: value columns
   PLayout L;
   const size_t rows = (size_t)a.srow0 + (size_t)a.B * a.Hkv * a.ns * a.r;
   L.status = 0;
@@ -635,10 +649,12 @@ PLayout playout(const PArgs& a, int d) {
   return L;
 }
 
-template <typename T, int D>
+template <typename T, int D, int DV>
 cudaError_t launch_p(const CUtensorMap (&m)[4], const PArgs& a, void* o, Strides os, float* lse, cudaStream_t s) {
-  auto kern = prefix_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D>::kBytes);
+  using C = PCfg<D, DV>;
+  constexpr bool kDiff = D != DV;
+  auto kern = prefix_kernel<T, D, DV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
   if (a.ptile == 256 && (e = launch_prefix_tc(Cvt<T>::kAB ? FA_DT_BF16 : FA_DT_F16, D, m[0], m[1], a, s)) != cudaSuccess)
     return e;
@@ -646,11 +662,11 @@ cudaError_t launch_p(const CUtensorMap (&m)[4], const PArgs& a, void* o, Strides
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::min<long long>(a.items, (long long)PCfg<D>::kCtas * std::max(sms, 1));
-    kern<<<grid, kPThreads, PCfg<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], a);
+    const unsigned grid = (unsigned)std::min<long long>(a.items, (long long)C::kCtas * std::max(sms, 1));
+    kern<<<grid, kPThreads, C::kBytes, s>>>(m[0], m[1], m[2], m[3], a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return a.np + a.ns <= 8 ? launch_join<T, D, 1>(a, o, os, lse, s) : launch_join<T, D, 4>(a, o, os, lse, s);
+  return a.np + a.ns <= 8 ? launch_join<T, DV, 1, kDiff>(a, o, os, lse, s) : launch_join<T, DV, 4, kDiff>(a, o, os, lse, s);
 }
 
 }  // namespace
@@ -659,14 +675,14 @@ cudaError_t launch_p(const CUtensorMap (&m)[4], const PArgs& a, void* o, Strides
 size_t prefix_workspace(const fa_prefix_params* p) {
   PArgs a{};
   plan(p, a);
-  return playout(a, p->d).total;
+  return playout(a, p->lam != nullptr ? 2 * p->d : p->d).total;
 }
 
 cudaError_t launch_prefix(const fa_prefix_params* p, const CUtensorMap (&m)[4], const void* q, Strides qs, void* o,
                           Strides os, float* lse, float scale_log2, uint8_t* ws, cudaStream_t s) {
   PArgs a{};
   plan(p, a);
-  const PLayout L = playout(a, p->d);
+  const PLayout L = playout(a, p->lam != nullptr ? 2 * p->d : p->d);
   a.q = q;
   a.qs = qs;
   a.lens = p->seqlens_k;
@@ -677,9 +693,13 @@ cudaError_t launch_prefix(const fa_prefix_params* p, const CUtensorMap (&m)[4], 
   a.sched = a.status + 1;
   cudaError_t e = cudaMemsetAsync(a.status, 0, 2 * sizeof(int), s);
   if (e != cudaSuccess) return e;
-  if (p->dtype == FA_DT_BF16)
-    return p->d == 128 ? launch_p<__nv_bfloat16, 128>(m, a, o, os, lse, s) : launch_p<__nv_bfloat16, 64>(m, a, o, os, lse, s);
-  return p->d == 128 ? launch_p<__half, 128>(m, a, o, os, lse, s) : launch_p<__half, 64>(m, a, o, os, lse, s);
+  using B16 = __nv_bfloat16;
+  const bool bf = p->dtype == FA_DT_BF16;
+  if (p->lam != nullptr)
+    return bf ? launch_p<B16, 64, 128>(m, a, o, os, lse, s) : launch_p<__half, 64, 128>(m, a, o, os, lse, s);
+  if (p->d == 128)
+    return bf ? launch_p<B16, 128, 128>(m, a, o, os, lse, s) : launch_p<__half, 128, 128>(m, a, o, os, lse, s);
+  return bf ? launch_p<B16, 64, 64>(m, a, o, os, lse, s) : launch_p<__half, 64, 64>(m, a, o, os, lse, s);
 }
 
 }  // namespace fa

@@ -25,17 +25,18 @@ namespace {
 
 constexpr int kThreads = 512;   // warps 0-7 softmax, 8 TMA, 9 / 10 S issuers, 11 / 12 P V issuers, 13-15 idle
 
-template <int D> struct TCfg {
-  static constexpr int kTB = 128 * D * 2;                // one [128 rows][D] tile
-  static constexpr int NC = D / 64;                      // 64-column boxes
-  static constexpr int NS = D == 64 ? 5 : 2;             // K / V stages
+template <int D, int DV> struct TCfg {                   // columns of q and k, and of v and o
+  static constexpr int kTB = 128 * D * 2;                // one [128 rows][D] tile of Q or K
+  static constexpr int kVB = 128 * DV * 2;               // one [128 rows][DV] tile of V
+  static constexpr int NS = DV == 64 ? 5 : D == 64 ? 4 : 2;   // K / V stages
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kTB;
   static constexpr int kV = kK + NS * kTB;
-  static constexpr int kBar = kV + NS * kTB;
+  static constexpr int kBar = kV + NS * kVB;
   static constexpr int kBytes = kBar + 512;
 };
-static_assert(TCfg<64>::kBytes <= 232448 && TCfg<128>::kBytes <= 232448, "shared memory over the per-block limit");
+template <int D, int DV> constexpr bool fits() { return TCfg<D, DV>::kBytes <= 232448; }
+static_assert(fits<64, 64>() && fits<128, 128>() && fits<64, 128>(), "shared memory over the per-block limit");
 
 struct TBars {
   uint64_t q_full;
@@ -48,11 +49,12 @@ struct TBars {
 };
 static_assert(sizeof(TBars) <= 512, "barrier block overflows its shared-memory slot");
 
-template <typename T, int D>
+template <typename T, int D, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PArgs a) {
-  using C = TCfg<D>;
-  constexpr int NS = C::NS, TB = C::kTB, NC = C::NC;
+  using C = TCfg<D, DV>;
+  constexpr int NS = C::NS, TB = C::kTB, VB = C::kVB;
+  constexpr bool kDiff = D != DV;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {       // the 128-byte swizzle's tiles: see diff_fwd.cu
     if (threadIdx.x == 0) atomicExch(a.status, (int)FA_ERR_CUDA);
@@ -113,12 +115,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
         // a tile is four 32-row boxes per 64 columns
-        auto load = [&](int base, const CUtensorMap* m, uint64_t* bar, int row) {
+        auto load = [&](int base, int boxes, const CUtensorMap* m, uint64_t* bar, int row, int head) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
+          for (int c = 0; c < boxes; ++c)
 #pragma unroll
             for (int x = 0; x < kTile / kKT; ++x)
-              tma_load_4d(smem + base + c * 16384 + x * kKT * 128, m, bar, c * 64, row + x * kKT, hk, 0);
+              tma_load_4d(smem + base + c * 16384 + x * kKT * 128, m, bar, c * 64, row + x * kKT, head, 0);
         };
         int nk = 0, nv = 0;
         for (int s = 0; s < n; ++s) {
@@ -127,11 +129,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           // a stage's first use needs no wait
           if (s >= NS && !mbar_wait(&bars->k_empty[st], ph ^ 1u, ctl)) break;
           mbar_expect_tx(&bars->k_full[st], TB);
-          load(C::kK + st * TB, &tmK, &bars->k_full[st], k0 + s * kTile);
+          load(C::kK + st * TB, D / 64, &tmK, &bars->k_full[st], k0 + s * kTile, hk);
           ++nk;
           if (s >= NS && !mbar_wait(&bars->v_empty[st], ph ^ 1u, ctl)) break;
-          mbar_expect_tx(&bars->v_full[st], TB);
-          load(C::kV + st * TB, &tmV, &bars->v_full[st], k0 + s * kTile);
+          mbar_expect_tx(&bars->v_full[st], VB);
+          load(C::kV + st * VB, DV / 64, &tmV, &bars->v_full[st], k0 + s * kTile, value_head<kDiff>(hk));
           ++nv;
         }
         // Before leaving, make sure no load is still writing shared memory.
@@ -174,7 +176,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // ===================== P V issuer of slot x =====================
       const int x = warp - 11;
       if (lane == 0) {
-        constexpr uint32_t idPV = idesc_f16(128, D, ab, 0, 1);
+        constexpr uint32_t idPV = idesc_f16(128, DV, ab, 0, 1);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
         const uint32_t tP = tmem + x * kStream + kColP, tO = tmem + x * kStream + kColO;
         bool ok = true;
@@ -186,7 +188,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             if (ok) ok = mbar_wait(&bars->p_full[x][j], (uint32_t)s & 1u, ctl);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = vd0 + (uint64_t)((st * TB + j * 8192) >> 4);
+            const uint64_t vd = vd0 + (uint64_t)((st * VB + j * 8192) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ts(tO, tP + j * 32 + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idPV, (s > 0 || j > 0 || k > 0) ? 1u : 0u);
@@ -211,7 +213,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // this thread's Q row into the swizzled tile
       {
         uint8_t* qb = smem + C::kQ + x * TB + r * 128;
-        const uint4* src = row < a.R ? reinterpret_cast<const uint4*>(prefix_row<T>(a, hk, row)) : nullptr;
+        const uint4* src = row < a.R ? reinterpret_cast<const uint4*>(prefix_row<T, kDiff>(a, hk, row)) : nullptr;
         uint4 v[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) v[c] = src != nullptr ? src[c] : make_uint4(0, 0, 0, 0);
@@ -228,7 +230,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         for (int j = 0; j < 2; ++j) {
           if (!(ok = warp_wait(&bars->s_full[x], (uint32_t)j, ctl))) break;      // half h = 2 s + j
           tc_fence_after();
-          ok = w.template step<T, D, false>(
+          ok = w.template step<T, DV, false>(
               tS, tS + kColP + j * 32, tO, a.P - 1 - (k0 + s * kTile + j * 64), 0, a.scale_log2, s == 0 && j == 0,
               [&] { mbar_arrive(&bars->s_free[x]); },
               [&]() -> bool {       // the product of half h - 1
@@ -245,13 +247,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         tc_fence_after();
         const long long pr = ((long long)sp * a.Hkv + hk) * a.R + row;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < DV; c += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c, o);
           tmem_wait_ld();
           reg_fence32(o);
           if (row < a.R) {
-            float* dst = a.part + pr * D + c;
+            float* dst = a.part + pr * DV + c;
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
               asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -273,12 +275,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int DV>
 cudaError_t launch_t(const CUtensorMap& k, const CUtensorMap& v, const PArgs& a, cudaStream_t s) {
-  auto kern = prefix_tc_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D>::kBytes);
+  auto kern = prefix_tc_kernel<T, D, DV>;
+  constexpr int bytes = TCfg<D, DV>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.Hkv * a.pt * a.np), kThreads, TCfg<D>::kBytes, s>>>(k, v, a);
+  kern<<<(unsigned)(a.Hkv * a.pt * a.np), kThreads, bytes, s>>>(k, v, a);
   return cudaGetLastError();
 }
 
@@ -286,9 +289,11 @@ cudaError_t launch_t(const CUtensorMap& k, const CUtensorMap& v, const PArgs& a,
 
 cudaError_t launch_prefix_tc(int dtype, int d, const CUtensorMap& k, const CUtensorMap& v, const PArgs& a,
                              cudaStream_t s) {
-  if (dtype == FA_DT_BF16)
-    return d == 128 ? launch_t<__nv_bfloat16, 128>(k, v, a, s) : launch_t<__nv_bfloat16, 64>(k, v, a, s);
-  return d == 128 ? launch_t<__half, 128>(k, v, a, s) : launch_t<__half, 64>(k, v, a, s);
+  using B16 = __nv_bfloat16;
+  const bool bf = dtype == FA_DT_BF16;
+  if (a.lam != nullptr) return bf ? launch_t<B16, 64, 128>(k, v, a, s) : launch_t<__half, 64, 128>(k, v, a, s);
+  if (d == 128) return bf ? launch_t<B16, 128, 128>(k, v, a, s) : launch_t<__half, 128, 128>(k, v, a, s);
+  return bf ? launch_t<B16, 64, 64>(k, v, a, s) : launch_t<__half, 64, 64>(k, v, a, s);
 }
 
 }  // namespace fa

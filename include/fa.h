@@ -452,8 +452,13 @@ fa_status fa_diff_bwd(const fa_diff_params *p, const void *q, const void *k, con
  *     not written.
  *   - float16, bfloat16; d = 64 or 128.  Weights are rounded to the dtype
  *     before the product with V; sums, statistics and joins are float32.
+ *   - lam: differential attention over the same prefix and caches (fa_diff_fwd's
+ *     step for few tokens).  H and H_kv then count head pairs: q is
+ *     [B,2H,T,64], k_prefix [2H_kv,P,64], k [B,2H_kv,M,64] with the two maps of
+ *     pair h in heads 2h and 2h + 1, v_prefix [H_kv,P,128], v [B,H_kv,M,128],
+ *     o [B,H,T,128], lse [B,2H,T], and O = O_1 - lam[h] O_2.  d = 64 only.
  *   - Results repeat bit for bit; they do not depend on what else runs.
- *   - B*H*T < 2^26, P and M <= 2^28.  16-byte rule for bases and strides (a
+ *   - B*H*T (twice that with lam) < 2^26, P and M <= 2^28.  16-byte rule for bases and strides (a
  *     dimension of one element may have any stride); offsets are 64-bit.
  * The prefix is read once per K/V head for up to 64 query rows together
  * (B * H / H_kv * T of them), not once per sequence.  Workspace:
@@ -472,6 +477,7 @@ typedef struct {
   int64_t v_stride_b, v_stride_h, v_stride_n;
   int64_t kp_stride_h, kp_stride_n;
   int64_t vp_stride_h, vp_stride_n;
+  const float *lam;          /* NULL, or device float32 [H]: differential form  */
 } fa_prefix_params;
 
 size_t fa_prefix_workspace_size(const fa_prefix_params *p);

@@ -76,7 +76,7 @@ def _size(p):
     (dict(P=(1 << 28) + 1), 2), (dict(M=(1 << 28) + 1), 2), (dict(B=1 << 22, T=64), 2),
     (dict(seqlens_k=0), 1), (dict(seqlens_k=(1 << 22) + 2), 3),
     (dict(q_stride_n=68), 3), (dict(k_stride_n=32), 1), (dict(kp_stride_h=4), 3), (dict(vp_stride_n=66), 3),
-    (dict(v_stride_b=0), 1),
+    (dict(v_stride_b=0), 1), (dict(lam=(1 << 22) + 2), 3), (dict(lam=1 << 22), 1), (dict(lam=1 << 22, d=128), 2),
 ])
 def test_refusals_before_launch(mut, code):
     assert _call(_params(**mut)) == code
@@ -124,10 +124,10 @@ def plain(q, kp, vp, k, v, lens, scale=None):
     """Float64: o, lse, sum P |v|."""
     B, H, T, d = q.shape
     Hkv, P = kp.shape[:2]
-    M, G = k.shape[2], H // Hkv
+    M, G, dv = k.shape[2], H // Hkv, v.shape[3]
     scale = d ** -0.5 if scale is None else scale
     kk = torch.cat((kp[None].expand(B, Hkv, P, d), k), 2).double()
-    vv = torch.cat((vp[None].expand(B, Hkv, P, d), v), 2).double()
+    vv = torch.cat((vp[None].expand(B, Hkv, P, dv), v), 2).double()
     j = torch.arange(M, device=q.device)
     t = torch.arange(T, device=q.device)
     lens = lens.clamp(0, M)
@@ -143,7 +143,7 @@ def plain(q, kp, vp, k, v, lens, scale=None):
     p = torch.softmax(s, -1) * ~none
     o, mag = p @ vv, p @ vv.abs()
     lse = torch.logsumexp(s, -1).masked_fill(none.squeeze(-1), -math.inf)
-    return o.reshape(B, H, T, d), lse.reshape(B, H, T), mag.reshape(B, H, T, d)
+    return o.reshape(B, H, T, dv), lse.reshape(B, H, T), mag.reshape(B, H, T, dv)
 
 
 def check(got, want, dtype):
@@ -329,3 +329,62 @@ def test_many_rows_layouts_and_large_scores():
     qs = (q * 15).transpose(0, 1).contiguous().transpose(0, 1)
     kps = kp.transpose(0, 1).contiguous().transpose(0, 1)
     check(fa.prefix_fwd(qs, kps, vp, k, v, lens), plain(qs, kp, vp, k, v, lens), "f16")
+
+
+# ---- differential form --------------------------------------------------------------------------------------
+def diff_inputs(B, H, Hkv, T, P, M, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(DT[dtype])  # noqa: E731
+    lam = torch.rand(H, generator=g, device="cuda") * 0.9 + 0.05
+    return (r(B, 2 * H, T, 64), r(2 * Hkv, P, 64), r(Hkv, P, 128), r(B, 2 * Hkv, M, 64), r(B, Hkv, M, 128)), lam
+
+
+def diff_plain(q, kp, vp, k, v, lens, lam, scale=None):
+    a, b = (plain(q[:, x::2], kp[x::2], vp, k[:, x::2], v, lens, scale) for x in range(2))
+    w = lam.double()[None, :, None, None]
+    return a[0] - w * b[0], torch.stack((a[1], b[1]), 2).flatten(1, 2), a[2] + w.abs() * b[2]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,H,Hkv,T,P,M", [(1, 1, 1, 1, 0, 5), (2, 4, 4, 1, 130, 40), (5, 6, 2, 1, 700, 300),
+                                          (3, 4, 1, 5, 65, 64), (33, 8, 2, 1, 300, 20), (70, 8, 1, 2, 1025, 9),
+                                          (9, 2, 2, 3, 0, 600), (2, 16, 4, 1, 20000, 50)])
+def test_differential_steps(dtype, B, H, Hkv, T, P, M):
+    x, lam = diff_inputs(B, H, Hkv, T, P, M, dtype, seed=B + P)
+    lens = (torch.arange(B, device="cuda", dtype=torch.int32) * 7 + T) % (M + 1)
+    got = fa.prefix_fwd(*x, lens, lam=lam)
+    assert fa.check_status(fa.prefix_fwd.last_workspace) == 0
+    check(got, diff_plain(*x, lens, lam), dtype)
+
+
+@pytest.mark.gpu
+def test_differential_step_is_the_forward_pass_last_row():
+    from tests import test_diff
+    B, H, Hkv, N = 2, 4, 2, 211
+    q, k, v, lam, _ = test_diff.inputs(B, H, Hkv, N, "bf16", 3)
+    o, lse, _ = fa.diff_fwd(q, k, v, lam, causal=True)
+    lens = torch.full((B,), N, device="cuda", dtype=torch.int32)
+    got = fa.prefix_fwd(q[:, :, -3:], None, None, k, v, lens, lam=lam)       # the last three tokens
+    # each side rounds its weights once (2u of sum P |v|) and O once
+    u = 2.0 ** -8
+    bound = 2 * (2 * u * 2 * v.float().abs().amax() + u * o.float().abs().amax())
+    assert float((got[0] - o[:, :, -3:]).float().abs().max()) <= bound
+    assert torch.allclose(got[1], lse[:, :, -3:], atol=2e-5)
+
+
+@pytest.mark.gpu
+def test_differential_form_masks_nan_and_refuses():
+    x, lam = diff_inputs(3, 4, 2, 2, 100, 60, "bf16", 4)
+    lens = torch.tensor([0, 60, 17], device="cuda", dtype=torch.int32)
+    want = fa.prefix_fwd(*x, lens, lam=lam)
+    k, v = x[3].clone(), x[4].clone()
+    for b, n in enumerate(lens.tolist()):
+        k[b, :, n:], v[b, :, n:] = float("nan"), float("nan")
+    got = fa.prefix_fwd(*x[:3], k, v, lens, lam=lam)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    none = fa.prefix_fwd(x[0], None, None, x[3], x[4], torch.zeros_like(lens), lam=lam)
+    assert bool((none[0] == 0).all()) and bool((none[1] == -math.inf).all())
+    for bad in (dict(lam=lam[:3]), dict(lam=lam.double()), dict()):
+        with pytest.raises(ValueError):
+            fa.prefix_fwd(*x, lens, **bad)
