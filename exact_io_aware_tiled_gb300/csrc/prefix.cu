@@ -151,9 +151,10 @@ template <typename T, int D, int DV> struct Rows {
     }
   }
   // The keys of one stage, key0 and on.  lim: keys at or past it are hidden, per
-  // row; kend: V rows at or past it may hold anything.
+  // row; kend: V rows at or past it may hold anything.  nx = 1: only rows 0-7 of
+  // the 16 exist (one token of up to 8 heads), the others' softmax is left out.
   __device__ __forceinline__ void step(uint32_t sK, uint32_t sV, int key0, const int (&lim)[2], int kend, float sl2,
-                                       int lane) {
+                                       int lane, int nx) {
     constexpr int NK = PCfg<D, DV>::KS, kBox = PCfg<D, DV>::kBox;
     float s[NK / 8][4];
 #pragma unroll
@@ -185,8 +186,8 @@ template <typename T, int D, int DV> struct Rows {
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int n = 0; n < NK / 8; ++n) {
-      mx[0] = fmaxf(mx[0], fmaxf(s[n][0], s[n][1]));
-      mx[1] = fmaxf(mx[1], fmaxf(s[n][2], s[n][3]));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) mx[x] = max3f(mx[x], s[n][2 * x], s[n][2 * x + 1]);
     }
     float alpha[2], nm[2];
     bool moved = false;
@@ -220,25 +221,27 @@ template <typename T, int D, int DV> struct Rows {
     // P in 16 bits, the product's operand type (half a step per weight); the
     // rounded sum normalises O, the unrounded one makes the logsumexp
     uint32_t p[NK / 16][4];
-    float st[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, sr[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-    for (int n = 0; n < NK / 8; ++n) {
+    for (int x = 0; x < 2; ++x) {
+      if (x >= nx) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+        for (int n = 0; n < NK / 8; ++n) p[n >> 1][(n & 1) * 2 + x] = 0u;
+        break;
+      }
+      float st[2] = {0.f, 0.f}, sr[2] = {0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < NK / 8; ++n) {
         float e0, e1;
         fma2(e0, e1, s[n][2 * x], s[n][2 * x + 1], sl2, sl2, nm[x], nm[x]);
         e0 = ex2(e0);
         e1 = ex2(e1);
-        add2(st[x][0], st[x][1], e0, e1);
+        add2(st[0], st[1], e0, e1);
         const uint32_t u = Cvt<T>::pack(e0, e1);
-        Cvt<T>::acc2(sr[x][0], sr[x][1], u);
+        Cvt<T>::acc2(sr[0], sr[1], u);
         p[n >> 1][(n & 1) * 2 + x] = u;
       }
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      lt[x] += st[x][0] + st[x][1];
-      lr[x] += sr[x][0] + sr[x][1];
+      lt[x] += st[0] + st[1];
+      lr[x] += sr[0] + sr[1];
     }
     // V rows past kend are replaced by zeros (0 x NaN would not be 0)
     if (key0 + NK > kend) pv<true>(sV, p, kend - key0, lane);
@@ -272,9 +275,10 @@ template <typename T, int D, int DV> struct Rows {
     }
   }
   // this warp's rows and statistics into shared memory, and another warp's joined to this one's
-  __device__ __forceinline__ void put(float* so, float4* ss, int lane) const {
+  __device__ __forceinline__ void put(float* so, float4* ss, int lane, int nx) const {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
+      if (x >= nx) break;
       const int row = (lane >> 2) + 8 * x;
       float* dst = so + row * DV + 2 * (lane & 3);
 #pragma unroll
@@ -282,9 +286,10 @@ template <typename T, int D, int DV> struct Rows {
       if ((lane & 3) == 0) ss[row] = make_float4(m[x], lt[x], lr[x], 0.f);
     }
   }
-  __device__ __forceinline__ void join(const float* so, const float4* ss, int lane) {
+  __device__ __forceinline__ void join(const float* so, const float4* ss, int lane, int nx) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
+      if (x >= nx) break;
       const int row = (lane >> 2) + 8 * x;
       const float4 st = ss[row];
       const float m_new = fmaxf(m[x], st.x);
@@ -422,12 +427,17 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
       const int row = rbase + 8 * x;
       qr[x] = nullptr;
       if (row < it.rows) {
-        qr[x] = prefix_row<T, kDiff>(a, it.hk, it.shared ? row : it.b * a.r + row);
-        lim[x] = it.shared ? a.P : it.end - a.T + row % a.T + 1;
+        // shared: row (b, j, t) of all sequences; else (j, t) of sequence it.b
+        const int b = it.shared ? row / a.r : it.b;
+        const int rem = it.shared ? row - b * a.r : row;
+        const int j = a.T == 1 ? rem : rem / a.T, t = rem - j * a.T;
+        qr[x] = prefix_row<T, kDiff>(a, it.hk, b, j, t);
+        lim[x] = it.shared ? a.P : it.end - a.T + t + 1;
       }
     }
     w.load_q(qr[0], qr[1], lane);
-    const bool idle = it.rt * it.tile + rg * 16 >= it.rows;
+    const int left = it.rows - it.rt * it.tile - rg * 16;            // rows of this warp's 16
+    const int nx = left <= 0 ? 0 : left <= 8 ? 1 : 2;                 // eights of rows that exist
     for (int t = 0; t < it.nt; ++t, ++g) {
       const int st = g % NS;
       // A stage belongs to one key group for all its phases in an item.  The
@@ -437,7 +447,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
       if ((st & (kgs - 1)) != kg) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[st], (uint32_t)(g / NS) & 1u, ctl))) return;
       const uint32_t sK = smem_u32(smem + C::kK + st * C::kKTile), sV = smem_u32(smem + C::kV + st * C::kVTile);
-      if (!idle) w.step(sK, sV, it.k0 + t * C::KS, lim, it.kend, a.scale_log2, lane);
+      const int key0 = it.k0 + t * C::KS;
+      if (nx > 0) w.step(sK, sV, key0, lim, it.kend, a.scale_log2, lane, nx);
       __syncwarp();
       if (lane == 0) mbar_arrive_n(&bars->empty[st], kgs);
     }
@@ -445,9 +456,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
     // ---- join the key groups: warps 2, 3 into 0, 1, then (one row group) 1 into 0
 #pragma unroll 1
     for (int half = 2; half >= rgs; half >>= 1) {
-      if (warp >= half && warp < 2 * half) w.put(so + (warp - half) * 16 * DV, ss + (warp - half) * 16, lane);
+      if (warp >= half && warp < 2 * half) w.put(so + (warp - half) * 16 * DV, ss + (warp - half) * 16, lane, nx);
       if (!meet()) return;
-      if (warp < half) w.join(so + warp * 16 * DV, ss + warp * 16, lane);
+      if (warp < half) w.join(so + warp * 16 * DV, ss + warp * 16, lane, nx);
       if (!meet()) return;
     }
     if (kg != 0) continue;
@@ -500,6 +511,18 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PArgs a, T* __re
     // this warp's splits: w0, w0 + W, ...; 32 statistics at a time
     for (int s0 = w0; s0 < n; s0 += 32 * W) {
       const int cnt = min(32, (n - s0 + W - 1) / W);
+      // eight splits' rows at a time, the first eight on their way before the
+      // statistics that weigh them are in
+      float v[8][E];
+      auto fetch8 = [&](int s1) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const float* src = a.part + at(s0 + min(s1 + s, cnt - 1) * W) * DV + lane * E;
+          if constexpr (E == 2) *reinterpret_cast<float2*>(v[s]) = *reinterpret_cast<const float2*>(src);
+          else *reinterpret_cast<float4*>(v[s]) = *reinterpret_cast<const float4*>(src);
+        }
+      };
+      fetch8(0);
       const float4 st = lane < cnt ? a.stat[at(s0 + lane * W)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
       float mx = st.x;
 #pragma unroll
@@ -519,13 +542,7 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PArgs a, T* __re
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= old;
       for (int s1 = 0; s1 < cnt; s1 += 8) {
-        float v[8][E];
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const float* src = a.part + at(s0 + min(s1 + s, cnt - 1) * W) * DV + lane * E;
-          if constexpr (E == 2) *reinterpret_cast<float2*>(v[s]) = *reinterpret_cast<const float2*>(src);
-          else *reinterpret_cast<float4*>(v[s]) = *reinterpret_cast<const float4*>(src);
-        }
+        if (s1 > 0) fetch8(s1);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           const float fs = __shfl_sync(0xffffffffu, f, (s1 + s) & 31);
@@ -603,7 +620,8 @@ int row_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // Row tiles and key splits.  The work of a 64-key unit is tile / 16 warp tiles;
 // splits are cut so that the items are about equal in that measure and number
 // three for every resident CTA (ragged lengths and the long prefix items even
-// out), but no shorter than four units.
+// out; six cost 4 % more than they even out), but no shorter than four units, the
+// prefix's than eight.
 void plan(const fa_prefix_params* p, PArgs& a) {
   constexpr int kU = 64;
   const int maps = p->lam != nullptr ? 2 : 1;      // score heads per head
@@ -620,10 +638,18 @@ void plan(const fa_prefix_params* p, PArgs& a) {
   const int pw = a.ptile / 16, sw = a.stile / 16;
   const long long wp = a.ptile == 256 ? 0 : (long long)a.Hkv * a.pt * kp * pw;
   const long long wsuf = (long long)a.B * a.Hkv * a.st * ks * sw;
-  const long long items = 3ll * kSms * (p->d == 64 && maps == 1 ? PCfg<64, 64>::kCtas : PCfg<128, 128>::kCtas);
-  const long long share = (wp + wsuf + items - 1) / items;
+  const long long ctas = (long long)kSms * (p->d == 64 && maps == 1 ? PCfg<64, 64>::kCtas : PCfg<128, 128>::kCtas);
+  const long long share = (wp + wsuf + 3 * ctas - 1) / (3 * ctas);
   long long pc = std::max<long long>(8, share / pw);
   const long long sc = std::max<long long>(4, share / sw);
+  // A little more than one item for every CTA would take two rounds: lengthen the
+  // prefix splits to one round where that at most doubles them (72 tokens against
+  // 23,400 keys x 12 heads: 19.0 -> 15.9 us).
+  const long long own = (long long)a.B * a.Hkv * a.st * ((ks + sc - 1) / sc), heads = (long long)a.Hkv * a.pt;
+  if (a.ptile != 256 && heads > 0 && own < ctas) {
+    const long long room = (ctas - own) / heads;      // prefix splits that fit
+    if (room > 0 && (kp + room - 1) / room <= 2 * pc) pc = std::max(pc, (kp + room - 1) / room);
+  }
   if (a.ptile == 256) {
     // one CTA a SM: key splits such that one wave covers the heads and row tiles
     const long long groups = (long long)a.Hkv * a.pt, splits = std::max<long long>(1, kSms / groups);

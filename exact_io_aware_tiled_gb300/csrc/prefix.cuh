@@ -35,12 +35,9 @@ template <bool kDiff> __device__ __forceinline__ int query_head(const PArgs& a, 
   return kDiff ? 2 * ((hk >> 1) * a.G + j) + (hk & 1) : hk * a.G + j;
 }
 
-// Query row `row` of the B*G*T rows that share K head hk.
+// Token t of sequence b in the j-th query head that reads K head hk.
 template <typename T, bool kDiff>
-__device__ __forceinline__ const T* prefix_row(const PArgs& a, int hk, int row) {
-  const int b = row / a.r;
-  const int rem = row - b * a.r;
-  const int j = rem / a.T, t = rem - j * a.T;
+__device__ __forceinline__ const T* prefix_row(const PArgs& a, int hk, int b, int j, int t) {
   return static_cast<const T*>(a.q) + (int64_t)b * a.qs.b + (int64_t)query_head<kDiff>(a, hk, j) * a.qs.h + (int64_t)t * a.qs.n;
 }
 

@@ -213,7 +213,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // this thread's Q row into the swizzled tile
       {
         uint8_t* qb = smem + C::kQ + x * TB + r * 128;
-        const uint4* src = row < a.R ? reinterpret_cast<const uint4*>(prefix_row<T, kDiff>(a, hk, row)) : nullptr;
+        const int b = row / a.r, rem = row - b * a.r;
+        const int j = rem / a.T, t = rem - j * a.T;
+        const uint4* src =
+            row < a.R ? reinterpret_cast<const uint4*>(prefix_row<T, kDiff>(a, hk, b, j, t)) : nullptr;
         uint4 v[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) v[c] = src != nullptr ? src[c] : make_uint4(0, 0, 0, 0);
