@@ -55,7 +55,7 @@ struct DSmem {
   static constexpr int kQ = kV + 32768;             // NQ x (Q_1, Q_2: 8 KB each)
   static constexpr int kDO = kQ + NQ * 16384;       // NQ x 16 KB: dO [2 boxes][64 q][64]
   static constexpr int kDS = kDO + NQ * 16384;      // dS_1^T, dS_2^T [128 keys][64 q], 16 KB each
-  static constexpr int kLD = kDS + 32768;           // NQ x 4 x 64 floats: LSE_1, LSE_2, e_1, e_2
+  static constexpr int kLD = kDS + 32768;           // NQ x 4 x 64 floats: -LSE_1, -LSE_2, e_1, e_2
   static constexpr int kItem = kLD + NQ * 1024;     // the two published work items
   static constexpr int kBar = kItem + 64;
   static constexpr int kBytes = kBar + 320;
@@ -425,10 +425,17 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       reg_fence16(g);
       tc_fence_before();
       mbar_arrive(&bars->dq_free);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      auto add = [&](int c) {
         const float v = kFold ? __uint_as_float(g[c]) : __uint_as_float(g[c]) * a.scale;
-        if (c < qn) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" :: "l"(dst + c * 64), "f"(v) : "memory");
+        asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" :: "l"(dst + c * 64), "f"(v) : "memory");
+      };
+      if (qn >= 16) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) add(c);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          if (c < qn) add(c);
       }
       return true;
     };
@@ -527,10 +534,10 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         for (int q4 = 0; q4 < 4; ++q4) {
           const int cc = q4 * 4;
           const float4 l1 = lds128(s_ld + cc * 4), l2 = lds128(s_ld + 256 + cc * 4);
-          fma2(p1[cc], p1[cc + 1], __uint_as_float(s1[cc]), __uint_as_float(s1[cc + 1]), sl2, sl2, -l1.x, -l1.y);
-          fma2(p1[cc + 2], p1[cc + 3], __uint_as_float(s1[cc + 2]), __uint_as_float(s1[cc + 3]), sl2, sl2, -l1.z, -l1.w);
-          fma2(p2[cc], p2[cc + 1], __uint_as_float(s2[cc]), __uint_as_float(s2[cc + 1]), sl2, sl2, -l2.x, -l2.y);
-          fma2(p2[cc + 2], p2[cc + 3], __uint_as_float(s2[cc + 2]), __uint_as_float(s2[cc + 3]), sl2, sl2, -l2.z, -l2.w);
+          fma2(p1[cc], p1[cc + 1], __uint_as_float(s1[cc]), __uint_as_float(s1[cc + 1]), sl2, sl2, l1.x, l1.y);
+          fma2(p1[cc + 2], p1[cc + 3], __uint_as_float(s1[cc + 2]), __uint_as_float(s1[cc + 3]), sl2, sl2, l1.z, l1.w);
+          fma2(p2[cc], p2[cc + 1], __uint_as_float(s2[cc]), __uint_as_float(s2[cc + 1]), sl2, sl2, l2.x, l2.y);
+          fma2(p2[cc + 2], p2[cc + 3], __uint_as_float(s2[cc + 2]), __uint_as_float(s2[cc + 3]), sl2, sl2, l2.z, l2.w);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             p1[cc + e] = ex2(p1[cc + e]);
@@ -695,13 +702,14 @@ __global__ void diff_prep_kernel(const T* __restrict__ o, const T* __restrict__ 
     d2 += __shfl_xor_sync(0xffffffffu, d2, s);
   }
   if (live && part < 4) {
-    // part 0, 1: LSE of map 1, 2 in log2 units; part 2, 3: e_1 = -c_1 D_1, e_2 = lambda c_1 D_2
+    // part 0, 1: -LSE of map 1, 2 in log2 units (P = exp2(S tau log2e - LSE) is one
+    // packed FMA, which cannot negate an operand); part 2, 3: e_1 = -c_1 D_1, e_2 = lambda c_1 D_2
     float v;
     if (part < 2) {
-      v = INFINITY;
+      v = -INFINITY;                 // a row without keys, or past N: P = 0
       if (i < N) {
         const float l = lse[((size_t)bh * 2 + part) * N + i];
-        v = l == -INFINITY ? INFINITY : l * kLog2e;
+        if (l != -INFINITY) v = -l * kLog2e;
       }
     } else {
       const float lm = lam[h];

@@ -118,7 +118,7 @@ struct DiffBwdArgs {
   float scale, scale_log2;    // tau, tau * log2(e)
   const int32_t* seqlens_k;
   const float* lam;
-  const float* rows;          // [B*H][npad/64][4][64]: per 64 query rows the two maps' LSE*log2e, then e_1, e_2
+  const float* rows;          // [B*H][npad/64][4][64]: per 64 query rows the two maps' -LSE*log2e, then e_1, e_2
   float* dqacc;               // [B,2H,N,64] float32, cleared by the prepass
   float* dlam_part;           // [items * group][16]: per-warp sums of P_2 o dP
   void* dk;                   // [B,2H_kv,N,64], strides kst
