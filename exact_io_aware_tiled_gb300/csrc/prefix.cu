@@ -611,8 +611,24 @@ cudaError_t launch_join(const PArgs& a, void* o, Strides os, float* lse, cudaStr
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-bool use_tc(const fa_prefix_params* p, int rows) {
-  return rows > 128 && p->P >= 256;
+// Whether the shared keys go to the tensor-memory kernel.  It wins where there is
+// enough work, 64-row tiles x shared keys x d, to pay for a launch of its own.
+// us here / there, 8 heads, 512 own keys a sequence, d = 128: 64 rows x 16,384 keys
+// 51 / 52, 65 rows x 8,192 46 / 47, 33 rows x 65,536 84 / 68, 256 rows x 65,536
+// 310 / 159; d = 64: 65 rows x 16,384 31 / 33, 129 rows x 16,384 51 / 55, 64 rows x
+// 65,536 59 / 52, 256 rows x 65,536 153 / 104.  Up to 32 rows the two are level
+// without own keys.
+bool use_tc(const fa_prefix_params* p, int rows, int heads) {
+  return rows > 32 && (long long)heads * ((rows + 63) / 64) * p->P >= (1 << 24) / p->d;
+}
+
+// Whether the tensor-memory kernel's two slots take two key splits of the same rows.
+// That keeps the second slot busy where the rows fill one, and gives the join twice
+// the splits.  us one slot / folded, d = 64, 64 rows: 16 heads x 8,192 keys 17.1 / 17.4,
+// x 16,384 26.5 / 23.6, x 65,536 72 / 57.  At d = 128 a slot would have one stage of K
+// and V to itself: 91 / 95.
+bool use_fold(const fa_prefix_params* p, int rows, int heads) {
+  return p->d == 64 && rows <= 128 && (long long)heads * p->P >= 1 << 18;
 }
 
 int row_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -621,7 +637,7 @@ int row_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // splits are cut so that the items are about equal in that measure and number
 // three for every resident CTA (ragged lengths and the long prefix items even
 // out; six cost 4 % more than they even out), but no shorter than four units, the
-// prefix's than eight.
+// prefix's than eight, unless CTAs would be left without an item.
 void plan(const fa_prefix_params* p, PArgs& a) {
   constexpr int kU = 64;
   const int maps = p->lam != nullptr ? 2 : 1;      // score heads per head
@@ -630,7 +646,7 @@ void plan(const fa_prefix_params* p, PArgs& a) {
   a.P = p->P; a.M = p->M;
   a.r = a.G * a.T;
   a.R = a.B * a.r;
-  a.ptile = use_tc(p, a.R) ? 256 : row_tile(a.R);
+  a.ptile = use_tc(p, a.R, a.Hkv) ? 256 : row_tile(a.R);
   a.stile = row_tile(a.r);
   a.pt = (a.R + a.ptile - 1) / a.ptile;
   a.st = (a.r + a.stile - 1) / a.stile;
@@ -640,19 +656,26 @@ void plan(const fa_prefix_params* p, PArgs& a) {
   const long long wsuf = (long long)a.B * a.Hkv * a.st * ks * sw;
   const long long ctas = (long long)kSms * (p->d == 64 && maps == 1 ? PCfg<64, 64>::kCtas : PCfg<128, 128>::kCtas);
   const long long share = (wp + wsuf + 3 * ctas - 1) / (3 * ctas);
+  const long long least = std::clamp<long long>(((long long)a.B * a.Hkv * a.st * ks + ctas - 1) / ctas, 2, 4);
+  const long long sc = std::max(least, share / sw);
   long long pc = std::max<long long>(8, share / pw);
-  const long long sc = std::max<long long>(4, share / sw);
-  // A little more than one item for every CTA would take two rounds: lengthen the
-  // prefix splits to one round where that at most doubles them (72 tokens against
-  // 23,400 keys x 12 heads: 19.0 -> 15.9 us).
+  // Where the own keys leave room, prefix splits that fill one round exactly: down
+  // to two units (1,024 shared keys, 2 heads of 128: 14.4 -> 10.3 us) but not above
+  // 64 splits for that (the join reads them one after another), and up to twice the
+  // length above rather than a little over one round (72 tokens against 23,400 keys
+  // x 12 heads: 19.0 -> 15.9 us).
   const long long own = (long long)a.B * a.Hkv * a.st * ((ks + sc - 1) / sc), heads = (long long)a.Hkv * a.pt;
-  if (a.ptile != 256 && heads > 0 && own < ctas) {
-    const long long room = (ctas - own) / heads;      // prefix splits that fit
-    if (room > 0 && (kp + room - 1) / room <= 2 * pc) pc = std::max(pc, (kp + room - 1) / room);
+  if (a.ptile != 256 && heads > 0 && ctas - own >= heads) {
+    const long long splits = (ctas - own) / heads, fit = (kp + splits - 1) / splits;
+    const long long low = std::clamp<long long>((kp + 63) / 64, 2, 8);
+    if (fit <= 2 * pc) pc = std::max({fit, low, share / pw});
   }
   if (a.ptile == 256) {
+    a.fold = use_fold(p, a.R, a.Hkv);
     // one CTA a SM: key splits such that one wave covers the heads and row tiles
-    const long long groups = (long long)a.Hkv * a.pt, splits = std::max<long long>(1, kSms / groups);
+    // (two splits a CTA where the rows fill one slot)
+    const long long groups = (long long)a.Hkv * a.pt;
+    const long long splits = (1 + a.fold) * std::max<long long>(1, kSms / groups);
     pc = 2 * std::max<long long>(1, ((kp + 1) / 2 + splits - 1) / splits);
   }
   a.pchunk = (int)(std::min<long long>(pc, 1 << 21) * kU);

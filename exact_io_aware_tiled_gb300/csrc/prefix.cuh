@@ -14,6 +14,7 @@ struct PArgs {
   int pt, st;                  // row tiles per head
   int pchunk, schunk;          // keys per split (multiples of 64, pchunk of 128 with 256-row tiles)
   int np, ns;                  // splits
+  int fold;                    // tensor-memory kernel: a CTA works at two splits of one 128-row tile
   int pitems, items;           // prefix items and all items of prefix_kernel
   const void* q;
   Strides qs;
@@ -41,7 +42,8 @@ __device__ __forceinline__ const T* prefix_row(const PArgs& a, int hk, int b, in
   return static_cast<const T*>(a.q) + (int64_t)b * a.qs.b + (int64_t)query_head<kDiff>(a, hk, j) * a.qs.h + (int64_t)t * a.qs.n;
 }
 
-// Many rows against the prefix (prefix_tc.cu): items of 256 rows and pchunk keys.
+// Many rows against the prefix (prefix_tc.cu): items of 256 rows and pchunk keys, or of
+// up to 128 rows and two splits.
 // d: columns of q and k; the differential form (a.lam set) has d = 64 and 128 value columns.
 cudaError_t launch_prefix_tc(int dtype, int d, const CUtensorMap& k, const CUtensorMap& v, const PArgs& a,
                              cudaStream_t s);

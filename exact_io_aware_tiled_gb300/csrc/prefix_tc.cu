@@ -49,11 +49,12 @@ struct TBars {
 };
 static_assert(sizeof(TBars) <= 512, "barrier block overflows its shared-memory slot");
 
-template <typename T, int D, int DV>
+template <typename T, int D, int DV, bool kFold>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PArgs a) {
   using C = TCfg<D, DV>;
-  constexpr int NS = C::NS, TB = C::kTB, VB = C::kVB;
+  // stages; folded, the even ones are slot 0's, the odd ones slot 1's
+  constexpr int NS = kFold ? C::NS & ~1 : C::NS, TB = C::kTB, VB = C::kVB;
   constexpr bool kDiff = D != DV;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {       // the 128-byte swizzle's tiles: see diff_fwd.cu
@@ -64,15 +65,18 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- work item: row tiles of the same keys run together and share them in L2
+  const int rts = kFold ? 1 : a.pt, sps = kFold ? (a.np + 1) / 2 : a.np;
   int it = (int)blockIdx.x;
-  const int rt = it % a.pt;
-  it /= a.pt;
-  const int sp = it % a.np;
-  const int hk = it / a.np;
-  const int k0 = sp * a.pchunk;
-  const int kend = min(a.P, k0 + a.pchunk);
-  const int n = (kend - k0 + kTile - 1) / kTile;          // >= 1
-  const int nact = rt * 256 + 128 < a.R ? 2 : 1;          // slots that have rows
+  const int rt = it % rts;
+  it /= rts;
+  const int sp0 = (kFold ? 2 : 1) * (it % sps);           // split of slot 0
+  const int hk = it / sps;
+  // slots at work: two that share the keys if there are rows, or two splits of one row tile
+  const int nact = (kFold ? sp0 + 1 < a.np : rt * 256 + 128 < a.R) ? 2 : 1;
+  auto split = [&](int x) { return kFold ? sp0 + x : sp0; };
+  auto tiles = [&](int x) { return (min(a.P, (split(x) + 1) * a.pchunk) - split(x) * a.pchunk + kTile - 1) / kTile; };
+  // ring place of tile s of slot x
+  auto place = [&](int s, int x) { return kFold ? 2 * s + x : s; };
 
   WaitCtl ctl{a.status, &bars->abort, kWaitSleepNs};
   if (threadIdx.x == 0) {
@@ -89,8 +93,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->k_empty[s], nact);
-      mbar_init(&bars->v_empty[s], nact);
+      mbar_init(&bars->k_empty[s], kFold ? 1 : nact);
+      mbar_init(&bars->v_empty[s], kFold ? 1 : nact);
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -122,23 +126,34 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             for (int x = 0; x < kTile / kKT; ++x)
               tma_load_4d(smem + base + c * 16384 + x * kKT * 128, m, bar, c * 64, row + x * kKT, head, 0);
         };
-        int nk = 0, nv = 0;
-        for (int s = 0; s < n; ++s) {
-          const int st = s % NS;
-          const uint32_t ph = (uint32_t)(s / NS) & 1u;
-          // a stage's first use needs no wait
-          if (s >= NS && !mbar_wait(&bars->k_empty[st], ph ^ 1u, ctl)) break;
-          mbar_expect_tx(&bars->k_full[st], TB);
-          load(C::kK + st * TB, D / 64, &tmK, &bars->k_full[st], k0 + s * kTile, hk);
-          ++nk;
-          if (s >= NS && !mbar_wait(&bars->v_empty[st], ph ^ 1u, ctl)) break;
-          mbar_expect_tx(&bars->v_full[st], VB);
-          load(C::kV + st * VB, DV / 64, &tmV, &bars->v_full[st], k0 + s * kTile, value_head<kDiff>(hk));
-          ++nv;
+        bool ok = true;
+        const int n = tiles(0);                            // slot 1 has as many or fewer
+        int nk[2] = {0, 0}, nv[2] = {0, 0};
+        for (int s = 0; s < n && ok; ++s) {
+#pragma unroll
+          for (int x = 0; x < (kFold ? 2 : 1); ++x) {
+            if (x >= nact || s >= tiles(x)) continue;
+            const int g = place(s, x), st = g % NS, row = split(x) * a.pchunk + s * kTile;
+            const uint32_t ph = (uint32_t)(g / NS) & 1u;
+            // a stage's first use needs no wait
+            if (g >= NS && !(ok = mbar_wait(&bars->k_empty[st], ph ^ 1u, ctl))) break;
+            mbar_expect_tx(&bars->k_full[st], TB);
+            load(C::kK + st * TB, D / 64, &tmK, &bars->k_full[st], row, hk);
+            ++nk[x];
+            if (g >= NS && !(ok = mbar_wait(&bars->v_empty[st], ph ^ 1u, ctl))) break;
+            mbar_expect_tx(&bars->v_full[st], VB);
+            load(C::kV + st * VB, DV / 64, &tmV, &bars->v_full[st], row, value_head<kDiff>(hk));
+            ++nv[x];
+          }
         }
         // Before leaving, make sure no load is still writing shared memory.
-        for (int j = max(0, nk - NS); j < nk; ++j) mbar_wait(&bars->k_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
-        for (int j = max(0, nv - NS); j < nv; ++j) mbar_wait(&bars->v_full[j % NS], (uint32_t)(j / NS) & 1u, ctl);
+        constexpr int kOwn = kFold ? NS / 2 : NS;          // stages of a slot
+        for (int x = 0; x < (kFold ? 2 : 1); ++x) {
+          for (int s = max(0, nk[x] - kOwn); s < nk[x]; ++s)
+            mbar_wait(&bars->k_full[place(s, x) % NS], (uint32_t)(place(s, x) / NS) & 1u, ctl);
+          for (int s = max(0, nv[x] - kOwn); s < nv[x]; ++s)
+            mbar_wait(&bars->v_full[place(s, x) % NS], (uint32_t)(place(s, x) / NS) & 1u, ctl);
+        }
       }
     } else if (warp <= 10) {
       // ===================== S issuer of slot x =====================
@@ -148,9 +163,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kK), 16, 1024);
         bool ok = mbar_wait(&bars->q_full, 0, ctl);
+        const int n = tiles(x);
         for (int s = 0; s < n && ok; ++s) {
-          const int st = s % NS;
-          if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
+          const int g = place(s, x), st = g % NS;
+          if (!(ok = mbar_wait(&bars->k_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // S of half h = 2 s + j overwrites that of half h - 1 once the softmax has read it
@@ -180,9 +196,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kV), 16384, 1024);
         const uint32_t tP = tmem + x * kStream + kColP, tO = tmem + x * kStream + kColO;
         bool ok = true;
+        const int n = tiles(x);
         for (int s = 0; s < n && ok; ++s) {
-          const int st = s % NS;
-          if (!(ok = mbar_wait(&bars->v_full[st], (uint32_t)(s / NS) & 1u, ctl))) break;
+          const int g = place(s, x), st = g % NS;
+          if (!(ok = mbar_wait(&bars->v_full[st], (uint32_t)(g / NS) & 1u, ctl))) break;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (ok) ok = mbar_wait(&bars->p_full[x][j], (uint32_t)s & 1u, ctl);
@@ -208,7 +225,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     if (x < nact) {
       const int quarter = warp & 3;
       const int r = quarter * 32 + lane;          // row within the slot = TMEM lane
-      const int row = rt * 256 + x * 128 + r;
+      const int row = kFold ? r : rt * 256 + x * 128 + r;
+      const int n = tiles(x), k0 = split(x) * a.pchunk;
       const uint32_t tS = tmem + x * kStream + ((uint32_t)(quarter * 32) << 16), tO = tS + kColO;
       // this thread's Q row into the swizzled tile
       {
@@ -248,7 +266,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // ---- this row's maximum, sums and unnormalised O
       if (ok && warp_wait(&bars->pv_done[x][1], (uint32_t)(n - 1) & 1u, ctl)) {
         tc_fence_after();
-        const long long pr = ((long long)sp * a.Hkv + hk) * a.R + row;
+        const long long pr = ((long long)split(x) * a.Hkv + hk) * a.R + row;
 #pragma unroll 1
         for (int c = 0; c < DV; c += 32) {
           uint32_t o[32];
@@ -278,14 +296,20 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   }
 }
 
-template <typename T, int D, int DV>
-cudaError_t launch_t(const CUtensorMap& k, const CUtensorMap& v, const PArgs& a, cudaStream_t s) {
-  auto kern = prefix_tc_kernel<T, D, DV>;
+template <typename T, int D, int DV, bool kFold>
+cudaError_t launch_f(const CUtensorMap& k, const CUtensorMap& v, const PArgs& a, cudaStream_t s) {
+  auto kern = prefix_tc_kernel<T, D, DV, kFold>;
   constexpr int bytes = TCfg<D, DV>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.Hkv * a.pt * a.np), kThreads, bytes, s>>>(k, v, a);
+  kern<<<(unsigned)(a.Hkv * (kFold ? (a.np + 1) / 2 : a.pt * a.np)), kThreads, bytes, s>>>(k, v, a);
   return cudaGetLastError();
+}
+
+template <typename T, int D, int DV>
+cudaError_t launch_t(const CUtensorMap& k, const CUtensorMap& v, const PArgs& a, cudaStream_t s) {
+  if constexpr (D == 64) if (a.fold) return launch_f<T, D, DV, true>(k, v, a, s);
+  return launch_f<T, D, DV, false>(k, v, a, s);
 }
 
 }  // namespace

@@ -316,7 +316,7 @@ def test_graph_replay_grows_with_the_caches_and_other_stream():
 @pytest.mark.parametrize("B,H,Hkv,T,P", [(33, 8, 2, 1, 256), (65, 4, 1, 1, 700), (129, 2, 2, 1, 385), (16, 8, 1, 3, 4097),
                                          (300, 2, 2, 1, 1000), (7, 6, 1, 40, 2049)])
 def test_many_rows_against_the_prefix(dtype, d, B, H, Hkv, T, P):
-    # more than 128 rows of a K/V head: 256-row tiles whose second half is empty, ragged or full
+    # row tiles of 64 that the last rows fill in part
     lens = [(11 * b) % 31 for b in range(B)]
     run(B, H, Hkv, T, P, 31, d, dtype, lens, seed=B + P)
 
@@ -388,3 +388,51 @@ def test_differential_form_masks_nan_and_refuses():
     for bad in (dict(lam=lam[:3]), dict(lam=lam.double()), dict()):
         with pytest.raises(ValueError):
             fa.prefix_fwd(*x, lens, **bad)
+
+
+# ---- the tensor-memory kernel: more than 32 rows and a long prefix ------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,H,Hkv,T,P,d", [
+    (1, 16, 4, 10, 65637, 64), (2, 8, 8, 33, 33001, 64), (1, 128, 4, 4, 70000, 64),    # two splits a CTA: 40, 66, 128 rows
+    (2, 32, 4, 10, 30001, 64), (1, 16, 2, 129, 8000, 64), (16, 8, 1, 3, 60001, 64),    # 256-row tiles: 160, 1,032, 384 rows
+    (1, 16, 4, 10, 33000, 128), (2, 32, 4, 10, 11001, 128), (1, 16, 2, 129, 3900, 128)])
+def test_long_prefix(dtype, B, H, Hkv, T, P, d):
+    lens = [(11 * b) % 31 for b in range(B)]
+    run(B, H, Hkv, T, P, 31, d, dtype, lens, seed=B + P)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,P", [(64, 65600), (128, 33000)])
+def test_long_prefix_layouts_and_large_scores(d, P):
+    B, H, Hkv, T, M = 3, 8, 4, 10, 20
+    q, kp, vp, k, v = inputs(B, H, Hkv, T, P, M, d, "f16", 9)
+    lens = torch.tensor([0, 20, 13], device="cuda", dtype=torch.int32)
+    qs = (q * 15).transpose(0, 1).contiguous().transpose(0, 1)
+    kps = kp.transpose(0, 1).contiguous().transpose(0, 1)
+    want = plain(qs, kp, vp, k, v, lens)
+    check(fa.prefix_fwd(qs, kps, vp, k, v, lens), want, "f16")
+    # without caches of their own
+    got = fa.prefix_fwd(qs, kps, vp, None, None, torch.zeros_like(lens))
+    check(got, plain(qs, kp, vp, k[:, :, :0], v[:, :, :0], torch.zeros_like(lens)), "f16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,H,Hkv,T,P", [(1, 8, 4, 20, 40000), (3, 4, 2, 50, 14001)])
+def test_long_prefix_differential(dtype, B, H, Hkv, T, P):
+    x, lam = diff_inputs(B, H, Hkv, T, P, 60, dtype, seed=P)
+    lens = (torch.arange(B, device="cuda", dtype=torch.int32) * 7 + T) % 61
+    got = fa.prefix_fwd(*x, lens, lam=lam)
+    assert fa.check_status(fa.prefix_fwd.last_workspace) == 0
+    check(got, diff_plain(*x, lens, lam), dtype)
+
+
+@pytest.mark.gpu
+def test_no_keys_at_all():
+    q, kp, vp, k, v = inputs(5, 4, 2, 3, 0, 0, 64, "bf16")
+    lens = torch.tensor([0, 7, 0, 2, 1], device="cuda", dtype=torch.int32)
+    for x in ((kp, vp, k, v), (kp, vp, None, None), (None, None, k, v)):
+        o, lse = fa.prefix_fwd(q, *x, lens)
+        assert fa.check_status(fa.prefix_fwd.last_workspace) == 0
+        assert bool((o == 0).all()) and bool((lse == -math.inf).all())
