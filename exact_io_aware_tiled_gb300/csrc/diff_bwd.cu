@@ -31,6 +31,12 @@
 //
 // What bounds it: the chain S -> P -> dS -> dQ of a step and the compute warps'
 // instructions (two exponentials and two dS per pair), not the tensor core.
+// Measured at GPT-2-medium width (B = 64, N = 1024, causal, bf16): 574 us, 344
+// GFLOP under the mask: 599 TFLOP/s; tensor pipe 29 %, issue slots 36 %.
+// dQ by a separate drain warpgroup 655-830 us (its registers come from the compute
+// warps); dQ loaded before this step's dS is published, so that the next product
+// starts earlier, 702; dS in two buffers against one pair of K tiles 631; sleeping
+// waits in the compute warps 591.
 //
 // Keys behind seqlens_k[b] may hold anything: their P and dP are replaced, and
 // their K rows are zeroed in shared memory before dQ reads them.

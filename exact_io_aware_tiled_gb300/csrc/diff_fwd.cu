@@ -27,8 +27,10 @@
 // and O lie.  Measured at GPT-2-medium width (B = 64, N = 1024, causal, bf16): one
 // CTA per item, whole tiles with P over S (the next S waits for the product that
 // reads P) 362 us; persistent CTAs, one on each SM, 324; 64-key halves with P over
-// S 292; P through shared memory 312 (the store and its proxy fence cost the
-// softmax warps more than the shorter chain gains).
+// S 292, with P in columns of its own 260 (138 GFLOP under the mask: 529 TFLOP/s;
+// tensor pipe a third busy, issue slots 45 %).  P through shared memory
+// instead of over S: 312 (the store and its proxy fence cost the softmax warps
+// more than the shorter chain gains); an S issuer for each map: 267.
 // Epilogue: warpgroup x forms columns 64 x .. 64 x + 63 of O and O_2 for every
 // row from both accumulators (any warp of a lane quarter can read them), after
 // the row sums are exchanged through shared memory; both leave as TMA stores.

@@ -12,10 +12,14 @@
 // warps 0-7 softmax (one thread a row), warp 8 TMA, warps 9 and 10 the S products
 // and 11 and 12 the P V products of slot 0 and 1 (products of one issuer complete
 // one after the other, 8 for each half tile of S at d = 128: one issuer for both
-// slots took 39 us where two take 34, 1,024 rows x 32,769 keys x 2 heads).  A row's place in q follows from
-// (sequence, head, token), so the softmax threads gather their own Q row into
-// the swizzled tile.  Splits are sized so that one wave of CTAs covers the GPU;
-// each leaves (max, sums, O unnormalised) in float32 for the join.
+// slots took 39 us where two take 34, 1,024 rows x 32,769 keys x 2 heads, 1.0
+// PFLOP/s).  Folded (kFold), the slots have the same rows and a key split each.
+// A row's place in q follows from (sequence, head, token), so the softmax threads
+// gather their own Q row into the swizzled tile.  Splits are sized so that one
+// wave of CTAs covers the GPU; each leaves (max, sums, O unnormalised) in float32
+// for the join.  Starting the own keys' kernel or the join beside this one
+// (griddepcontrol.launch_dependents) gains nothing: from the first instruction on
+// it halves this kernel's speed, from its last tile on it changes no total.
 // Tiles are worked in two 64-key halves; row_softmax.cuh says where S, P and O lie.
 #include "prefix.cuh"
 #include "row_softmax.cuh"

@@ -460,8 +460,8 @@ fa_status fa_diff_bwd(const fa_diff_params *p, const void *q, const void *k, con
  *   - Results repeat bit for bit; they do not depend on what else runs.
  *   - B*H*T (twice that with lam) < 2^26, P and M <= 2^28.  16-byte rule for bases and strides (a
  *     dimension of one element may have any stride); offsets are 64-bit.
- * The prefix is read once per K/V head for up to 64 query rows together
- * (B * H / H_kv * T of them), not once per sequence.  Workspace:
+ * The prefix is read once per K/V head for up to 64 query rows together (256 where
+ * there is much work) of all B * H / H_kv * T, not once per sequence.  Workspace:
  * fa_prefix_workspace_size bytes, 16-byte aligned, nothing persists in it;
  * status word at its start, read by fa_check_status.
  * ------------------------------------------------------------------------- */

@@ -4,8 +4,8 @@ CPU: struct layout, workspace sizes, refusals.  GPU: both dtypes over ragged
 lengths, grouped heads, padding, windows and layouts against a 64-bit plain
 form whose gradients come from autograd.
 
-Tolerances, for a dtype of relative half step u = eps / 2 (bf16 2^-8 / 2 ... :
-torch's eps is the whole step):
+Tolerances, for a dtype whose rounding is off by at most u = torch.finfo.eps / 2
+relative to the value (bf16 2^-8, fp16 2^-11):
 * O: a convex combination of V rows with weights rounded once (u each) and
   normalised by the sum of the rounded weights, twice, then one rounding of O:
   |error| <= 2u (O_1bar + |lambda| O_2bar) + u |O| with O_mbar = sum P_m |V|.
