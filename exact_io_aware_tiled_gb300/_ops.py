@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -23,6 +24,15 @@ ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
 
+def _packer(cls):
+    """A function of the fields of a parameter struct, pointers as integers, that returns its bytes (a call takes
+    them as they are; filling a ctypes structure costs three times as long)."""
+    code = {_i32: "i", _i64: "q", _vp: "P", _f32: "f"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")     # padded to its alignment
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
 class fa_rope_params(ctypes.Structure):
     _fields_ = ([(n, _i32) for n in ("B", "H", "H_kv", "N", "d", "rot", "dtype", "interleaved", "backward",
                                      "positions_i64")] +
@@ -30,6 +40,8 @@ class fa_rope_params(ctypes.Structure):
                 [("positions", _vp), ("pos_stride_b", _i64), ("pos_stride_n", _i64), ("start", _i64),
                  ("inv_freq", _vp), ("mscale", _f32)])
 
+
+_pack_rope = _packer(fa_rope_params)
 
 _typed = {}
 
@@ -181,7 +193,7 @@ def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleave
     if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or \
             not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor [rot/2] on q's device")
-    pos, wide, pos_b, pos_n = None, 0, 0, 0
+    pos, wide, pos_b, pos_n = 0, 0, 0, 0
     if positions is not None:
         wide = positions.dtype is torch.int64
         if not (wide or positions.dtype is torch.int32) or positions.get_device() != q.get_device():
@@ -201,10 +213,10 @@ def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleave
             qo, ko = (out, None) if k is None else out
             qos = _rows(qo, "out q", q, q.shape)[:3]
             kos = ks if k is None else _rows(ko, "out k", q, k.shape)[:3]
-        p = fa_rope_params(B, H, Hkv, N, d, 2 * inv_freq.shape[0], DTYPE_CODE[q.dtype], bool(interleaved),
-                           bool(backward), wide, *q.stride()[:3], *ks, *qos, *kos, pos, pos_b, pos_n, int(start),
-                           inv_freq.data_ptr(), float(mscale))
-        st = _ptrs("fa_rope", 6)(ctypes.addressof(p), q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(),
+        p = _pack_rope(B, H, Hkv, N, d, 2 * inv_freq.shape[0], DTYPE_CODE[q.dtype], bool(interleaved),
+                       bool(backward), wide, *q.stride()[:3], *ks, *qos, *kos, pos, pos_b, pos_n, int(start),
+                       inv_freq.data_ptr(), float(mscale))
+        st = _ptrs("fa_rope", 6)(p, q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(),
                                  None if k is None else ko.data_ptr(), raw)
     if st != FA_OK:
         raise FAError(st, "fa_rope")
@@ -216,6 +228,8 @@ class fa_diff_params(ctypes.Structure):
                 [("scale", _f32), ("seqlens_k", _vp), ("lam", _vp)] +
                 [("%s_stride_%s" % (t, x), _i64) for t in ("q", "k", "v", "o", "do") for x in "bhn"])
 
+
+_pack_diff = _packer(fa_diff_params)
 
 def _lens(seqlens, B, device, name="seqlens_k"):
     """int32 [B] lengths on `device` (converted on the current stream where they are something else)."""
@@ -241,10 +255,9 @@ def _need_workspace(workspace, size, device):
 
 def _diff_args(q, k, v, lam, causal, window, scale, lens, os, dos):
     """fa_diff_params of checked tensors; os, dos: strides of o (and o2) and of dO."""
-    return fa_diff_params(q.shape[0], q.shape[1] // 2, v.shape[1], q.shape[2], 64, DTYPE_CODE[q.dtype], bool(causal),
-                          int(window), 0.0 if scale is None else float(scale),
-                          None if lens is None else lens.data_ptr(), lam.data_ptr(), *q.stride()[:3], *k.stride()[:3],
-                          *v.stride()[:3], *os[:3], *dos[:3])
+    return _pack_diff(q.shape[0], q.shape[1] // 2, v.shape[1], q.shape[2], 64, DTYPE_CODE[q.dtype], bool(causal),
+                      int(window), 0.0 if scale is None else float(scale), 0 if lens is None else lens.data_ptr(),
+                      lam.data_ptr(), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *os[:3], *dos[:3])
 
 
 def _check_diff(q, k, v, lam):
@@ -288,8 +301,7 @@ def diff_fwd(q, k, v, lam, *, causal=False, seqlens_k=None, window=0, scale=None
             if o2 is not None and _rows(o2, "out o2", q, (B, H, N, 128)) != os:
                 raise ValueError("out o and o2 must share their strides")
             _flat_f32(lse, "out lse", dev, (B, 2 * H, N))
-        p = _diff_args(q, k, v, lam, causal, window, scale, lens, os, (0, 0, 0))
-        a = ctypes.addressof(p)
+        a = _diff_args(q, k, v, lam, causal, window, scale, lens, os, (0, 0, 0))
         ws = _need_workspace(workspace, _size_of("fa_diff_fwd_workspace_size")(a), dev)
         st = _sized("fa_diff_fwd", 8)(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                       None if o2 is None else o2.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -324,8 +336,7 @@ def diff_bwd(q, k, v, lam, o, o2, do, lse, *, causal=False, seqlens_k=None, wind
                 if _rows(t, "out " + n, q, like.shape) != like.stride():
                     raise ValueError("out %s must have the strides %s" % (n, like.stride()))
             _flat_f32(dlam, "out dlam", dev, (H,))
-        p = _diff_args(q, k, v, lam, causal, window, scale, lens, os, dos)
-        a = ctypes.addressof(p)
+        a = _diff_args(q, k, v, lam, causal, window, scale, lens, os, dos)
         ws = _need_workspace(workspace, _size_of("fa_diff_bwd_workspace_size")(a), dev)
         st = _sized("fa_diff_bwd", 13)(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), o2.data_ptr(),
                                        do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
@@ -342,6 +353,8 @@ class fa_prefix_params(ctypes.Structure):
                 [("%s_stride_%s" % (t, x), _i64) for t in ("q", "o", "k", "v") for x in "bhn"] +
                 [("%s_stride_%s" % (t, x), _i64) for t in ("kp", "vp") for x in "hn"] + [("lam", _vp)])
 
+
+_pack_prefix = _packer(fa_prefix_params)
 
 def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, lam=None, scale=None, out=None, workspace=None, stream=None):
     """Attention of B sequences that share a prefix (fa_prefix_fwd): (o, lse).
@@ -399,10 +412,9 @@ def prefix_fwd(q, k_prefix, v_prefix, k, v, seqlens_k, *, lam=None, scale=None, 
             o, lse = out
             os = _rows(o, "out o", q, (B, H, T, dv))
             _flat_f32(lse, "out lse", dev, (B, SH, T))
-        p = fa_prefix_params(B, H, Hkv, T, P, M, d, DTYPE_CODE[q.dtype], 0.0 if scale is None else float(scale),
-                             lens.data_ptr(), *q.stride()[:3], *os[:3], *ks[:3], *vs[:3], *kps[:2], *vps[:2],
-                             None if lam is None else lam.data_ptr())
-        a = ctypes.addressof(p)
+        a = _pack_prefix(B, H, Hkv, T, P, M, d, DTYPE_CODE[q.dtype], 0.0 if scale is None else float(scale),
+                         lens.data_ptr(), *q.stride()[:3], *os[:3], *ks[:3], *vs[:3], *kps[:2], *vps[:2],
+                         0 if lam is None else lam.data_ptr())
         ws = _need_workspace(workspace, _size_of("fa_prefix_workspace_size")(a), dev)
         st = _sized("fa_prefix_fwd", 9)(a, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), o.data_ptr(),
                                         lse.data_ptr(), ws.data_ptr(), ws.numel(), raw)
