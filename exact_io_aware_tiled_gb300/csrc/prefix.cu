@@ -690,6 +690,10 @@ void plan(const fa_prefix_params* p, PArgs& a) {
   a.srow0 = (long long)a.np * a.Hkv * a.R;
 }
 
+// The workspace is 16-byte aligned, prefix_tc_kernel's 32-byte stores of partial rows want 32: the launch rounds
+// part's address up, and the size leaves room for that.
+constexpr size_t kPartAlign = 32;
+
 struct PLayout { size_t status, stat, part, total; };
 PLayout playout(const PArgs& a, int d) {      // d: value columns
   PLayout L;
@@ -697,7 +701,7 @@ PLayout playout(const PArgs& a, int d) {      // d: value columns
   L.status = 0;
   L.stat = 256;
   L.part = L.stat + al256(rows * sizeof(float4));
-  L.total = L.part + al256(rows * d * sizeof(float));
+  L.total = L.part + al256(rows * d * sizeof(float)) + kPartAlign;
   return L;
 }
 
@@ -741,7 +745,7 @@ cudaError_t launch_prefix(const fa_prefix_params* p, const CUtensorMap (&m)[4], 
   a.scale_log2 = scale_log2;
   a.status = reinterpret_cast<int*>(ws + L.status);
   a.stat = reinterpret_cast<float4*>(ws + L.stat);
-  a.part = reinterpret_cast<float*>(ws + L.part);
+  a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws + L.part) + kPartAlign - 1) & ~uintptr_t(kPartAlign - 1));
   a.sched = a.status + 1;
   cudaError_t e = cudaMemsetAsync(a.status, 0, 2 * sizeof(int), s);
   if (e != cudaSuccess) return e;

@@ -278,7 +278,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           tmem_wait_ld();
           reg_fence32(o);
           if (row < a.R) {
-            float* dst = a.part + pr * DV + c;
+            float* dst = a.part + pr * DV + c;           // 32-byte aligned: see launch_prefix
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
               asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
