@@ -420,6 +420,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
     // warp = (key group) * rgs + (row group): rgs groups of 16 rows, 4 / rgs of stages
     const int rgs = it.tile >> 4, kgs = 4 / rgs;
     const int rg = warp & (rgs - 1), kg = warp / rgs;
+    // This warp's key group counted from the item's first stage: group lk has stages lk,
+    // lk + kgs, ... of the item, wherever in the ring the item starts.  The joins go by it,
+    // so a result's bits follow from the item alone, not from the items before it.
+    const int lk = (kg - g) & (kgs - 1), lw = lk * rgs + rg;
     const int rbase = it.rt * it.tile + rg * 16 + (lane >> 2);
     Rows<T, D, DV> w;
     w.init();
@@ -456,15 +460,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ 
       if (lane == 0) mbar_arrive_n(&bars->empty[st], kgs);
     }
     w.sum_lanes();
-    // ---- join the key groups: warps 2, 3 into 0, 1, then (one row group) 1 into 0
+    // ---- join the key groups: lw 2, 3 into 0, 1, then (one row group) 1 into 0
 #pragma unroll 1
     for (int half = 2; half >= rgs; half >>= 1) {
-      if (warp >= half && warp < 2 * half) w.put(so + (warp - half) * 16 * DV, ss + (warp - half) * 16, lane, nx);
+      if (lw >= half && lw < 2 * half) w.put(so + (lw - half) * 16 * DV, ss + (lw - half) * 16, lane, nx);
       if (!meet()) return;
-      if (warp < half) w.join(so + warp * 16 * DV, ss + warp * 16, lane, nx);
+      if (lw < half) w.join(so + lw * 16 * DV, ss + lw * 16, lane, nx);
       if (!meet()) return;
     }
-    if (kg != 0) continue;
+    if (lk != 0) continue;
     // row i of this item in the partial arrays
     const long long prow0 = it.shared ? ((long long)it.sp * a.Hkv + it.hk) * a.R
                                       : a.srow0 + (((long long)it.b * a.Hkv + it.hk) * a.ns + it.sp) * a.r;
