@@ -724,6 +724,7 @@ fa_status fa_diff_bwd(const fa_diff_params* p, const void* q, const void* k, con
   const float c1 = p->dtype == FA_DT_BF16 ? a.scale : 1.f;
   cudaError_t e = launch_diff_prep(p->dtype, o, o2, sd.o, dout, sd.dout, lse, p->lam, p->B, p->H, p->N, L.npad, c1,
                                    reinterpret_cast<float*>(w + L.rows), dqacc, a.sched, st);
+  if (e == cudaSuccess) e = launch_diff_d1(p->dtype, q, k, v, dout, sd.q, sd.dout, c1, lse, a, st);
   if (e == cudaSuccess) e = launch_diff_bwd(p->dtype, mq, mk, mv, mdo, a, st);
   if (e == cudaSuccess) e = launch_dq_convert(p->dtype, dqacc, dq, sd.q, p->B, 2 * p->H, p->N, 64, st);
   if (e == cudaSuccess) e = launch_diff_dlam(a.dlam_part, dlam, p->B, p->H, a.group, L.nq, st);

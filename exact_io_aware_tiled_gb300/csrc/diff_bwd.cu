@@ -43,7 +43,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
+#include "register_mma.cuh"
 
 namespace fa {
 namespace {
@@ -725,6 +725,157 @@ __global__ void diff_prep_kernel(const T* __restrict__ o, const T* __restrict__ 
   }
 }
 
+// D_1 of the head pairs with |lambda| > kD1Direct, from the products themselves:
+//     D_1 = rowsum(P_1 o dP),  P_1 = exp(tau Q_1 K_1^T - LSE_1),  dP = dO V^T,
+// all in float32, over the prepass's dO . O + lambda dO . O_2.  There the rounding
+// of O and lambda times that of O_2 stay when lambda dO . O_2 cancels, so the
+// error of D_1, and of dQ_1 and dK_1, grows with |lambda| while their values do
+// not.  Relative error of dQ_1 (bf16, N = 257, causal, normal inputs) with the
+// prepass's D_1: lambda 0.5 0.0025, 1 0.0026, 2 0.0031, 4 0.0050, 8 0.010, 30 0.038,
+// 100 0.129; with this one 0.0024 throughout, the rounding of dS and of dQ.  So the
+// prepass's is kept up to 2.
+//
+// A CTA takes 64 query rows, 16 a warp, against 64-key tiles of K_1 and V that
+// it loads ahead: 384 flops a pair on the register products, which bound it.  At
+// GPT-2-medium width (B = 64, N = 1024, causal, bf16) 1.9 us where no head pair is
+// above the limit, 82 with one of the eight, 630 with all (164 TFLOP/s under the
+// mask; the main kernel takes 574).
+constexpr float kD1Direct = 2.f;
+constexpr int kD1Threads = 128;
+constexpr int kD1Stage = 8192 + 16384;           // K_1 [64 keys][64], V [2 boxes][64 keys][64]
+
+struct D1Args {
+  const void *q, *k, *v, *dout;
+  Strides qs, ks, vs, ds;
+  const float *lse, *lam;
+  const int32_t* seqlens_k;
+  int B, H, group, N, npad, causal, window;
+  float sl2, c1;
+  float* rows;
+};
+
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kD1Threads, 3) diff_d1_kernel(const D1Args a) {
+  __shared__ __align__(1024) uint8_t smem[2 * kD1Stage];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = (a.N + 63) / 64;
+  const long long units = (long long)a.B * tiles;
+#pragma unroll 1
+  for (int h = 0; h < a.H; ++h) {
+    // 128 heads are looked at together
+    if (h % kD1Threads == 0) {
+      const int x = h + tid;
+      if (!__syncthreads_or(x < a.H && fabsf(a.lam[x]) > kD1Direct)) {
+        h += kD1Threads - 1;
+        continue;
+      }
+    }
+    if (!(fabsf(a.lam[h]) > kD1Direct)) continue;
+    const int hk = h / a.group;
+#pragma unroll 1
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+      const int b = (int)(u % a.B), i0 = (tiles - 1 - (int)(u / a.B)) * 64;      // long rows first
+      int Lk = a.N;
+      if (a.seqlens_k != nullptr) Lk = max(0, min(a.N, a.seqlens_k[b]));
+      const int hi = a.causal ? min(Lk, i0 + 64) : Lk;
+      const int lo = a.window > 0 ? max(0, i0 - a.window + 1) / 64 * 64 : 0;
+      const int n = hi > lo ? (hi - lo + 63) / 64 : 0;
+      const T* kb = static_cast<const T*>(a.k) + (int64_t)b * a.ks.b + (int64_t)(2 * hk) * a.ks.h;
+      const T* vb = static_cast<const T*>(a.v) + (int64_t)b * a.vs.b + (int64_t)hk * a.vs.h;
+      auto load = [&](int t) {
+        const uint32_t s = smem_u32(smem + (t & 1) * kD1Stage);
+        for (int e = tid; e < 64 * 24; e += kD1Threads) {        // 8 pieces of K_1, 16 of V a key
+          const int r = e / 24, c = e - r * 24, j = lo + t * 64 + r;
+          const bool live = j < Lk;                              // rows past it may hold anything, or nothing
+          const int64_t jj = live ? j : 0;
+          const T* src = c < 8 ? kb + jj * a.ks.n + c * 8 : vb + jj * a.vs.n + (c - 8) * 8;
+          copy16(s + (c >> 3) * 8192 + sw128_off(r, (c & 7) * 8), src, live);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      if (n > 0) load(0);
+      // this thread's two rows of Q_1 and dO, as operands
+      uint32_t q[4][4], g[8][4];
+      float nl[2], d[2] = {0.f, 0.f};
+      const int i = i0 + warp * 16 + (lane >> 2);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int ix = i + 8 * x;
+        const bool live = ix < a.N;
+        const int64_t in = live ? ix : 0;
+        const T* qr = static_cast<const T*>(a.q) + (int64_t)b * a.qs.b + (int64_t)(2 * h) * a.qs.h + in * a.qs.n + 2 * (lane & 3);
+        const T* dr = static_cast<const T*>(a.dout) + (int64_t)b * a.ds.b + (int64_t)h * a.ds.h + in * a.ds.n + 2 * (lane & 3);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[k][2 * c + x] = live ? *reinterpret_cast<const uint32_t*>(qr + k * 16 + c * 8) : 0u;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[k][2 * c + x] = live ? *reinterpret_cast<const uint32_t*>(dr + k * 16 + c * 8) : 0u;
+        }
+        nl[x] = live ? -a.lse[((int64_t)b * 2 * a.H + 2 * h) * a.N + in] * kLog2e : 0.f;
+      }
+      const int lr = lane & 7, lm = lane >> 3;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        if (t + 1 < n) {
+          load(t + 1);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();
+        const uint32_t sK = smem_u32(smem + (t & 1) * kD1Stage), sV = sK + 8192;
+        const int j0 = lo + t * 64;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {                            // 16 keys
+          float s[2][4] = {}, dp[2][4] = {};
+          // matrices: keys 0-7 / 8-15 (lm >> 1), columns 0-7 / 8-15 (lm & 1)
+          const uint32_t row = m * 16 + (lm >> 1) * 8 + lr;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+            ldsm4(w, sK + sw128_off(row, k * 16 + (lm & 1) * 8));
+            mma16816<T>(s[0], q[k], w[0], w[1]);
+            mma16816<T>(s[1], q[k], w[2], w[3]);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t w[4];
+            ldsm4(w, sV + (k >> 2) * 8192 + sw128_off(row, (k & 3) * 16 + (lm & 1) * 8));
+            mma16816<T>(dp[0], g[k], w[0], w[1]);
+            mma16816<T>(dp[1], g[k], w[2], w[3]);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int ix = i + 8 * (e >> 1), j = j0 + m * 16 + y * 8 + 2 * (lane & 3) + (e & 1);
+              const bool see = j < hi && (!a.causal || j <= ix) && (a.window == 0 || j > ix - a.window);
+              const float p = ex2(s[y][e] * a.sl2 + nl[e >> 1]);
+              d[e >> 1] += see ? p * dp[y][e] : 0.f;
+            }
+        }
+        __syncthreads();                                         // the tile has been read
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        d[x] += __shfl_xor_sync(0xffffffffu, d[x], 1);
+        d[x] += __shfl_xor_sync(0xffffffffu, d[x], 2);
+        const int ix = i + 8 * x;
+        if ((lane & 3) == 0 && ix < a.N) {
+          const long long r = ((long long)b * a.H + h) * a.npad + ix;
+          a.rows[(r >> 6) * 256 + 128 + (r & 63)] = -a.c1 * d[x];
+        }
+      }
+    }
+  }
+}
+
 // dlambda of head pair blockIdx.x: every item's and warp's part, in a fixed order.
 // Bound by the latency of its loads: 1,024 threads take an item's 16 sums in four
 // 16-byte pieces.
@@ -778,7 +929,32 @@ cudaError_t prep_t(const void* o, const void* o2, Strides ost, const void* dout,
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t d1_t(const D1Args& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)a.B * ((a.N + 63) / 64);
+  diff_d1_kernel<T><<<(unsigned)std::min<long long>(units, 3ll * std::max(sms, 1)), kD1Threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_diff_d1(int dtype, const void* q, const void* k, const void* v, const void* dout, Strides qst,
+                           Strides dst, float c1, const float* lse, const DiffBwdArgs& m, cudaStream_t s) {
+  D1Args a{};
+  a.q = q; a.k = k; a.v = v; a.dout = dout;
+  a.qs = qst; a.ks = m.kst; a.vs = m.vst; a.ds = dst;
+  a.lse = lse; a.lam = m.lam;
+  a.seqlens_k = m.seqlens_k;
+  a.B = m.B; a.H = m.H; a.group = m.group; a.N = m.N; a.npad = m.npad;
+  a.causal = m.causal; a.window = m.window;
+  a.sl2 = m.scale_log2; a.c1 = c1;
+  a.rows = const_cast<float*>(m.rows);
+  return dtype == FA_DT_BF16 ? d1_t<__nv_bfloat16>(a, s) : d1_t<__half>(a, s);
+}
 
 cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides ost, const void* dout, Strides dost,
                              const float* lse, const float* lam, int B, int H, int N, int npad, float c1, float* rows,

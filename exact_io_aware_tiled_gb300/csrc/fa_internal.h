@@ -176,6 +176,9 @@ cudaError_t launch_diff_fwd(int dtype, const CUtensorMap& q, const CUtensorMap& 
 cudaError_t launch_diff_prep(int dtype, const void* o, const void* o2, Strides ost, const void* dout, Strides dost,
                              const float* lse, const float* lam, int B, int H, int N, int npad, float c1, float* rows,
                              float* dqacc, int* sched, cudaStream_t s);
+// Replaces the prepass's D_1 of the head pairs whose |lambda| is large (after the prepass, before the main kernel).
+cudaError_t launch_diff_d1(int dtype, const void* q, const void* k, const void* v, const void* dout, Strides qst,
+                           Strides dst, float c1, const float* lse, const DiffBwdArgs& m, cudaStream_t s);
 cudaError_t launch_diff_bwd(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                             const CUtensorMap& dout, const DiffBwdArgs& a, cudaStream_t s);
 // dlam[h] = -sum of the partial sums, in a fixed order.

@@ -389,7 +389,8 @@ fa_status fa_rope_frequencies(int32_t rot, double base, int32_t scaling, double 
  *     lse: contiguous float32 [B,2H,N], natural log, one row set per map.
  *     Query pair h reads K/V pair h / (H / H_kv); H_kv = 0 selects H.
  *   - float16 or bfloat16, d = 64 (128 value columns); others return
- *     FA_ERR_UNSUPPORTED.  lam: device float32 [H], any finite values.
+ *     FA_ERR_UNSUPPORTED.  lam: device float32 [H], any finite values for which
+ *     the dtype holds O, P_1 - lam P_2 and the gradients (float16 ends at 65504).
  *   - Masks: causal, seqlens_k (keys j >= L_b are masked; K and V rows there
  *     may hold anything, NaN included), window (causal only).  A query row
  *     that sees no key has O = 0, O_2 = 0, both logsumexps -inf and no part
@@ -408,7 +409,10 @@ fa_status fa_rope_frequencies(int32_t rot, double base, int32_t scaling, double 
  *     dQ_m = tau dS_m K_m, dK_m = tau dS_m^T Q_m, dlam = -sum D_2
  * with dq, dk, dv in q's, k's and v's strides (no broadcast strides) and dlam
  * float32 [H].  D_m comes from dO and the rounded O and O_2, so a row whose
- * exact dS vanishes (one visible key) gets a residue of their rounding.  dQ is
+ * exact dS vanishes (one visible key) gets a residue of their rounding.  For head
+ * pairs with |lam| > 2, where that residue would outgrow dS_1, D_1 is summed from
+ * float32 P_1 and dP instead, which costs such pairs about as much again as the
+ * rest of their backward pass.  dQ is
  * accumulated in float32 in the order in which the key tiles finish: its last
  * bit may differ from run to run; every other output repeats bit for bit.
  * Workspace: fa_diff_*_workspace_size bytes, 16-byte aligned; status word at
