@@ -187,12 +187,23 @@ def _check(q, name="q"):
         raise ValueError("unsupported dtype %s" % q.dtype)
 
 
+def int32_lengths(t: torch.Tensor, device) -> torch.Tensor:
+    """t as a contiguous int32 tensor on `device`.  Whole numbers that int32 does not hold become its ends: narrowed
+    as they are, 2^31 and more would turn negative and lose a sequence its keys."""
+    if t.dtype in (torch.int64, torch.uint32, torch.uint64):
+        wide = t.to(torch.int64)
+        if t.dtype is torch.uint64:                  # 2^63 and more came out negative
+            wide = wide.masked_fill(wide < 0, 2 ** 31 - 1)
+        t = wide.clamp(-2 ** 31, 2 ** 31 - 1)
+    return t.to(device=device, dtype=torch.int32).contiguous()
+
+
 def _aux(seqlens_k, block_mask, q):
     B, N = q.shape[0], q.shape[2]
     if seqlens_k is not None:
         if tuple(seqlens_k.shape) != (B,):
             raise ValueError("seqlens_k must have shape [B]")
-        seqlens_k = seqlens_k.to(device=q.device, dtype=torch.int32).contiguous()
+        seqlens_k = int32_lengths(seqlens_k, q.device)
     if block_mask is not None:
         nb = -(-N // 128)
         if tuple(block_mask.shape) != (nb, nb):

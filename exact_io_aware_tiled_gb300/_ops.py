@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import DTYPE_CODE, FA_OK, FAError, load
+from ._lib import DTYPE_CODE, FA_OK, FAError, int32_lengths, load
 
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -241,7 +241,7 @@ def _lens(seqlens, B, device, name="seqlens_k"):
         return seqlens
     if seqlens.dtype.is_floating_point or seqlens.dtype == torch.bool:
         raise ValueError("%s must hold whole numbers" % name)
-    return seqlens.to(device=device, dtype=torch.int32).contiguous()
+    return int32_lengths(seqlens, device)
 
 
 def _need_workspace(workspace, size, device):
