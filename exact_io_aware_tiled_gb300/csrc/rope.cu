@@ -110,9 +110,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   // bf16: 2 -> 91, 4 -> 93, 8 -> 110; 63 MB of float32: 2 -> 20.0, 4 -> 18.7 us
   constexpr int HB = kInter ? 2 : 4;
   __shared__ unsigned long long sF[128];
+  __shared__ float sM[128];                          // m, or NaN where the frequency is not finite
   const int half = a.rot >> 1;
   // float64 is slow on this GPU: the turns are made once per CTA, not once per thread
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) sF[i] = turns_of(a.inv_freq[i]);
+  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
+    const double f = a.inv_freq[i];
+    sF[i] = turns_of(f);
+    sM[i] = isfinite(f) ? a.mscale : nanf("");
+  }
   __syncthreads();
   const uint32_t t = blockIdx.x * kRopeThreads + threadIdx.x;
   if (t >= a.total) return;
@@ -132,11 +137,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       const int64_t at = (int64_t)b * a.pos_b + (int64_t)n * a.pos_n;
       p = a.pos64 ? static_cast<const long long*>(a.pos)[at] : (long long)static_cast<const int*>(a.pos)[at];
     }
-    const float sm = a.sgn * a.mscale;
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
       const int i = kInter ? c0 / 2 + e : c0 + e;
-      if (!kInter || i < half) turn(p, sF[i], a.mscale, sm, cs[e], sn[e]);
+      if (!kInter || i < half) turn(p, sF[i], sM[i], a.sgn * sM[i], cs[e], sn[e]);
     }
   }
   const int first = blockIdx.y * a.hp;

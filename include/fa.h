@@ -340,7 +340,8 @@ fa_status fa_fwd_fp8(const fa_params *p, const fa_fp8_params *f, const void *buf
  *     Positions may be negative.  The angle is reduced to a fraction of a
  *     turn exactly, in 64-bit integers, so it does not lose accuracy with
  *     the position (float64's own 2^-53 of p f remains).
- *   - inv_freq: device float64 [rot/2], read on the stream.
+ *   - inv_freq: device float64 [rot/2], read on the stream.  A NaN or infinite
+ *     frequency makes its pair's two columns NaN at every position.
  *   - Products and sums are float32, rounded once to the dtype.
  *   - No workspace, one launch.  B*N*d < 2^32 - 4096.
  * ------------------------------------------------------------------------- */
