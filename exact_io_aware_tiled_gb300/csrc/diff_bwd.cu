@@ -736,10 +736,13 @@ __global__ void diff_prep_kernel(const T* __restrict__ o, const T* __restrict__ 
 // prepass's is kept up to 2.
 //
 // A CTA takes 64 query rows, 16 a warp, against 64-key tiles of K_1 and V that
-// it loads ahead: 384 flops a pair on the register products, which bound it.  At
-// GPT-2-medium width (B = 64, N = 1024, causal, bf16) 1.9 us where no head pair is
-// above the limit, 82 with one of the eight, 630 with all (164 TFLOP/s under the
-// mask; the main kernel takes 574).
+// it loads ahead: 384 flops a pair on the register products.  Issue slots (51 %)
+// and the products' latency (tensor pipe 35 %) bound it.  The head pairs above the
+// limit are gathered first, so that all of them share one order of items, long
+// rows first (head after head, the same CTAs had the long rows of each: 630 us
+// for 517, 318 for 138 at B = 16).  At GPT-2-medium width (B = 64, N = 1024, causal,
+// bf16) 1.9 us where no head pair is above the limit, 80 with one of the eight,
+// 517 with all (199 TFLOP/s under the mask; the main kernel takes 574).
 constexpr float kD1Direct = 2.f;
 constexpr int kD1Threads = 128;
 constexpr int kD1Stage = 8192 + 16384;           // K_1 [64 keys][64], V [2 boxes][64 keys][64]
@@ -761,25 +764,32 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live)
 
 template <typename T>
 __global__ void __launch_bounds__(kD1Threads, 3) diff_d1_kernel(const D1Args a) {
-  __shared__ __align__(1024) uint8_t smem[2 * kD1Stage];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint32_t masks[kD1Threads / 32];
+  __shared__ int heads[kD1Threads];
   const int tiles = (a.N + 63) / 64;
-  const long long units = (long long)a.B * tiles;
 #pragma unroll 1
-  for (int h = 0; h < a.H; ++h) {
-    // 128 heads are looked at together
-    if (h % kD1Threads == 0) {
-      const int x = h + tid;
-      if (!__syncthreads_or(x < a.H && fabsf(a.lam[x]) > kD1Direct)) {
-        h += kD1Threads - 1;
-        continue;
-      }
+  for (int h0 = 0; h0 < a.H; h0 += kD1Threads) {
+    // those of 128 head pairs that are above the limit, in order
+    const bool large = h0 + tid < a.H && fabsf(a.lam[h0 + tid]) > kD1Direct;
+    const uint32_t mask = __ballot_sync(0xffffffffu, large);
+    if (lane == 0) masks[warp] = mask;
+    __syncthreads();
+    int nh = 0, before = __popc(mask & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < kD1Threads / 32; ++w) {
+      nh += __popc(masks[w]);
+      if (w < warp) before += __popc(masks[w]);
     }
-    if (!(fabsf(a.lam[h]) > kD1Direct)) continue;
-    const int hk = h / a.group;
+    if (large) heads[before] = h0 + tid;
+    __syncthreads();
+    const int wide = a.B * nh;                                   // B H < 2^31
 #pragma unroll 1
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const int b = (int)(u % a.B), i0 = (tiles - 1 - (int)(u / a.B)) * 64;      // long rows first
+    for (long long u = blockIdx.x; u < (long long)wide * tiles; u += gridDim.x) {
+      const int level = (int)(u / wide), bh = (int)(u - (long long)level * wide);
+      const int b = bh / nh, h = heads[bh - b * nh], hk = h / a.group;
+      const int i0 = (tiles - 1 - level) * 64;                   // long rows first
       int Lk = a.N;
       if (a.seqlens_k != nullptr) Lk = max(0, min(a.N, a.seqlens_k[b]));
       const int hi = a.causal ? min(Lk, i0 + 64) : Lk;
@@ -932,11 +942,12 @@ cudaError_t prep_t(const void* o, const void* o2, Strides ost, const void* dout,
 template <typename T>
 cudaError_t d1_t(const D1Args& a, cudaStream_t s) {
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaFuncSetAttribute(diff_d1_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kD1Stage);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long units = (long long)a.B * ((a.N + 63) / 64);
-  diff_d1_kernel<T><<<(unsigned)std::min<long long>(units, 3ll * std::max(sms, 1)), kD1Threads, 0, s>>>(a);
+  const long long most = (long long)a.B * a.H * ((a.N + 63) / 64);
+  diff_d1_kernel<T><<<(unsigned)std::min<long long>(most, 3ll * std::max(sms, 1)), kD1Threads, 2 * kD1Stage, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -412,8 +412,8 @@ fa_status fa_rope_frequencies(int32_t rot, double base, int32_t scaling, double 
  * float32 [H].  D_m comes from dO and the rounded O and O_2, so a row whose
  * exact dS vanishes (one visible key) gets a residue of their rounding.  For head
  * pairs with |lam| > 2, where that residue would outgrow dS_1, D_1 is summed from
- * float32 P_1 and dP instead, which costs such pairs about as much again as the
- * rest of their backward pass.  dQ is
+ * float32 P_1 and dP instead, which makes the backward pass of such pairs about
+ * 1.7 times as long.  dQ is
  * accumulated in float32 in the order in which the key tiles finish: its last
  * bit may differ from run to run; every other output repeats bit for bit.
  * Workspace: fa_diff_*_workspace_size bytes, 16-byte aligned; status word at
