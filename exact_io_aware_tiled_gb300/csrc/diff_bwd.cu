@@ -11,6 +11,10 @@
 // (Q, K padded) would do 2560.  dlambda is summed from the float32 P_2 and dP,
 // not from rounded outputs: it is a long sum of both signs.
 //
+// Roundings: P_1 - lambda P_2, dS_1 and dS_2 become 16-bit operands of the products
+// that take them, half a step of each element; dQ, dK and dV are rounded once at
+// the end (0.0024 relative in bf16, both together).  P, dP, D and all sums are float32.
+//
 // Tiles: 128 keys x 64 query rows a step, keys on the tensor-memory lanes, as in
 // the d = 128 backward (bwd_tc128.cu), whose roles and barriers this kernel
 // keeps, except that dQ goes from registers into the float32 accumulator by
@@ -664,7 +668,7 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 }
 
 // D_1 and D_2 of every query row from dO . O and dO . O_2 (D_1 = dO . O +
-// lambda D_2), the logsumexps in log2 units, all in the 64-row groups that a
+// lambda D_2; diff_d1_kernel replaces it where lambda is large), the logsumexps in log2 units, all in the 64-row groups that a
 // step loads in one piece; the dQ accumulator is cleared on the way.  Eight
 // threads a row, 16 columns each.  Bound by HBM: three 256-byte rows read, two
 // 256-byte accumulator rows written.

@@ -11,9 +11,10 @@
 //
 // Work per visible (query, key) pair: 2 x 128 flops of scores, 2 x 256 of
 // P V (512 if the maps could be joined before the product), two exponentials.
-// What bounds it: the softmax warps (two exponentials a pair against 16 per
-// clock and SM) and the latency of the chain S -> softmax -> P V within one
-// map; the two maps are independent chains and cover one another.
+// What bounds it: the softmax warps' instructions and the latency of the chain
+// S -> softmax -> P V within one map; the two maps are independent chains and
+// cover one another.  The exponentials do not: two a pair at the 30 per clock and
+// SM that a loop of them reaches are a quarter of the time.
 //
 // Mapping.  An item is one 128-row query tile of one head pair; the two maps take
 // the places that two query tiles have in the d = 128 kernel (fwd_tc.cu):

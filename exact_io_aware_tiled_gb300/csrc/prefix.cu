@@ -600,13 +600,14 @@ cudaError_t launch_join(const PArgs& a, void* o, Strides os, float* lse, cudaStr
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Whether the shared keys go to the tensor-memory kernel.  It wins where there is
-// enough work, 64-row tiles x shared keys x d, to pay for a launch of its own.
-// us here / there, 8 heads, 512 own keys a sequence, d = 128: 64 rows x 16,384 keys
-// 51 / 52, 65 rows x 8,192 46 / 47, 33 rows x 65,536 84 / 68, 256 rows x 65,536
-// 310 / 159; d = 64: 65 rows x 16,384 31 / 33, 129 rows x 16,384 51 / 55, 64 rows x
-// 65,536 59 / 52, 256 rows x 65,536 153 / 104.  Up to 32 rows the two are level
-// without own keys.
+// Whether the shared keys go to the tensor-memory kernel: by the work, 64-row tiles x
+// shared keys x d, that has to pay for a launch of its own.  us here / there, 8 heads,
+// 512 own keys a sequence.  Well above the limit it wins: d = 128, 33 rows x 65,536
+// keys 84 / 68, 256 rows x 65,536 310 / 159; d = 64, 64 rows x 65,536 59 / 52, 256
+// rows x 65,536 153 / 104.  At the limit and up to three times it the rule takes the
+// slower side by a little: d = 128, 64 rows x 16,384 51 / 52, 65 rows x 8,192 46 / 47;
+// d = 64, 65 rows x 16,384 31 / 33, 129 rows x 16,384 51 / 55.  Up to 32 rows the two
+// are level without own keys.
 bool use_tc(const fa_prefix_params* p, int rows, int heads) {
   return rows > 32 && (long long)heads * ((rows + 63) / 64) * p->P >= (1 << 24) / p->d;
 }

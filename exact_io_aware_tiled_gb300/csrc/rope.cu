@@ -13,7 +13,10 @@
 // binary fraction F = f / 2 pi 2^64 and p F is taken modulo 2^64, which drops
 // whole turns exactly; what is left is the fraction of a turn, read as a signed
 // number in [-1/2, 1/2) and handed to sincospif.  One float64 product per CTA
-// and pair makes F; everything else is integer and float32.
+// and pair makes F; everything else is integer and float32.  Rounded to float32 the
+// fraction is off by up to 2^-25 half turns (9e-8 radians), as much as sincospif's
+// own result: float32 outputs lose a fifth to it against 64-bit angles, 16-bit ones
+// nothing, and float64 sines are slow on this GPU.
 //
 // What bounds it: HBM.  Each element is read and written once, and the angles
 // are computed, not read.  A thread owns V pairs (16-byte vectors where rot / 2

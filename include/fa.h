@@ -395,8 +395,9 @@ fa_status fa_rope_frequencies(int32_t rot, double base, int32_t scaling, double 
  *   - Masks: causal, seqlens_k (keys j >= L_b are masked; K and V rows there
  *     may hold anything, NaN included), window (causal only).  A query row
  *     that sees no key has O = 0, O_2 = 0, both logsumexps -inf and no part
- *     in any gradient.  Every other K and V row should be finite: the tile
- *     products spread a NaN or infinity over the query rows of its tile.
+ *     in any gradient.  Its q and dO rows, like every K and V row that is not
+ *     masked, should be finite all the same: the tile products take masked
+ *     places times zero, which spreads a NaN or infinity over its tile.
  *   - Weights are rounded to the dtype before the product with V, which is
  *     summed in float32 and normalised by the sum of the rounded weights.
  *   - 2*B*H*N < 2^32.  16-byte rule for bases and strides (a dimension of one
