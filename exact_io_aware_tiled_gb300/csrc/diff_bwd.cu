@@ -188,6 +188,8 @@ diff_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  // the kernels before are done (the launch overlaps the end of the last of them)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp >= 16) {
     constexpr int ab = Cvt<T>::kAB;
@@ -746,7 +748,10 @@ __global__ void diff_prep_kernel(const T* __restrict__ o, const T* __restrict__ 
 // rows first (head after head, the same CTAs had the long rows of each: 630 us
 // for 517, 318 for 138 at B = 16).  At GPT-2-medium width (B = 64, N = 1024, causal,
 // bf16) 1.9 us where no head pair is above the limit, 80 with one of the eight,
-// 517 with all (199 TFLOP/s under the mask; the main kernel takes 574).
+// 517 with all (199 TFLOP/s under the mask; the main kernel takes 574).  This kernel
+// and the main one are launched over the end of the one before, which hides the
+// 1.9 us: a training step takes 1,011 us as it did without (1,016 launched plainly;
+// B = 32, N = 509, fp16, padded: 214 for 216, 220 launched plainly).
 constexpr float kD1Direct = 2.f;
 constexpr int kD1Threads = 128;
 constexpr int kD1Stage = 8192 + 16384;           // K_1 [64 keys][64], V [2 boxes][64 keys][64]
@@ -788,6 +793,8 @@ __global__ void __launch_bounds__(kD1Threads, 3) diff_d1_kernel(const D1Args a) 
     }
     if (large) heads[before] = h0 + tid;
     __syncthreads();
+    // the prepass has written its rows (the launch overlaps its end)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int wide = a.B * nh;                                   // B H < 2^31
 #pragma unroll 1
     for (long long u = blockIdx.x; u < (long long)wide * tiles; u += gridDim.x) {
@@ -916,6 +923,24 @@ __global__ void __launch_bounds__(1024) diff_dlam_kernel(const float* __restrict
   if (threadIdx.x == 0) dlam[h] = -sh[0];
 }
 
+// A launch that may begin while the kernel before it in the stream ends: the kernel
+// waits (griddepcontrol.wait) before it touches what that one wrote.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                              const A&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args...);
+}
+
 template <typename T, bool kWin>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
                      const DiffBwdArgs& a, cudaStream_t s) {
@@ -927,8 +952,7 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<long long>(total, (long long)std::max(sms, 1));
-  kern<<<grid, kThreads, DSmem::kDyn, s>>>(q, k, v, dout, a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, grid, kThreads, DSmem::kDyn, s, q, k, v, dout, a);
 }
 
 template <typename T>
@@ -951,8 +975,8 @@ cudaError_t d1_t(const D1Args& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const long long most = (long long)a.B * a.H * ((a.N + 63) / 64);
-  diff_d1_kernel<T><<<(unsigned)std::min<long long>(most, 3ll * std::max(sms, 1)), kD1Threads, 2 * kD1Stage, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(diff_d1_kernel<T>, (unsigned)std::min<long long>(most, 3ll * std::max(sms, 1)), kD1Threads,
+                           2 * kD1Stage, s, a);
 }
 
 }  // namespace
