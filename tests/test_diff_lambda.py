@@ -15,6 +15,7 @@ import torch
 
 import exact_io_aware_tiled_gb300 as fa
 from tests.test_diff import DT, inputs, plain, rel
+from tests.test_operator_ranges import Field
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +122,46 @@ def test_strides_repeats_and_graph():
     graph.replay()
     want = fa.diff_bwd(q, k, v, lam, o, o2, do, lse, causal=True)
     assert all(torch.equal(a, b) for a, b in zip(c[1:], want[1:]))
+
+
+@pytest.mark.parametrize("dim", [0, 1])
+def test_offsets_pass_32_bits(dim):
+    f = Field()
+    # two sequences of one pair, or the two maps of one pair (v and dO then have one head)
+    q, k, v, _, do = inputs(2 if dim == 0 else 1, 1, 1, 200, "bf16", 3)
+    lam = torch.tensor([-12.0], device="cuda")
+    far = (lambda t: f.copy(t, dim) if t.shape[dim] == 2 else t)
+    o, lse, o2 = fa.diff_fwd(q, k, v, lam, causal=True)
+    want = fa.diff_bwd(q, k, v, lam, o, o2, do, lse, causal=True)
+    x = [far(t) for t in (q, k, v)]
+    grads = [f.empty_like(t, dim) if t.shape[dim] == 2 else torch.empty_like(t) for t in (q, k, v)]
+    got = fa.diff_bwd(*x, lam, o, o2, far(do), lse, causal=True, out=(*grads, torch.empty_like(lam)))
+    assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+    assert rel(got[0], want[0].double()) <= 1e-4
+
+
+def test_many_sequences_of_one_token():
+    B = 70000
+    q, k = (torch.randn(B, 2, 1, 64, device="cuda", dtype=torch.float16) for _ in range(2))
+    v, do = (torch.randn(B, 1, 1, 128, device="cuda", dtype=torch.float16) for _ in range(2))
+    lam = torch.tensor([5.0], device="cuda")
+    o, lse, o2 = fa.diff_fwd(q, k, v, lam)
+    dq, dk, dv, _ = fa.diff_bwd(q, k, v, lam, o, o2, do, lse)
+    # one key: dS_1 is 2^-18 (P_1 against 1) of dP; each weight is rounded, and their difference is
+    dp = (do.double().abs() * v.double().abs()).sum(-1, keepdim=True)
+    assert bool((dq[:, :1].double().abs() <= 2.0 ** -16 * 0.125 * dp * k[:, :1].double().abs() + 2.0 ** -24).all())
+    assert bool((dk[:, :1].double().abs() <= 2.0 ** -16 * 0.125 * dp * q[:, :1].double().abs() + 2.0 ** -24).all())
+    ref = do.double() * -4.0
+    assert bool(((dv.double() - ref).abs() <= 3 * 2.0 ** -11 * do.double().abs() * 6 + 2.0 ** -24).all())
+
+
+def test_two_calls_at_once():
+    q, k, v, _, do = inputs(3, 4, 2, 500, "bf16", 8)
+    lam = torch.tensor([0.5, -30.0, 4.0, 1.0], device="cuda")
+    o, lse, o2 = fa.diff_fwd(q, k, v, lam, causal=True)
+    want = fa.diff_bwd(q, k, v, lam, o, o2, do, lse, causal=True)
+    torch.cuda.synchronize()
+    got = [fa.diff_bwd(q, k, v, lam, o, o2, do, lse, causal=True, stream=torch.cuda.Stream()) for _ in range(6)]
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g[1:], want[1:])) and rel(g[0], want[0].double()) <= 2.0 ** -8

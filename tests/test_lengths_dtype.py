@@ -47,8 +47,10 @@ def test_calls():
     full = torch.tensor([10 ** 6, 10 ** 6, 40, 0], device="cuda", dtype=torch.int32)
     for P in (90, 0):
         x = test_prefix.inputs(4, 4, 2, 1, P, 50, 64, "bf16", 2)
-        got, want = fa.prefix_fwd(*x, wide), fa.prefix_fwd(*x, full)
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        want = fa.prefix_fwd(*x, full)
+        for t in (wide, torch.tensor([2 ** 31, 2 ** 32 - 1, 40, 0], dtype=torch.uint32, device="cuda")):
+            got = fa.prefix_fwd(*x, t)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     q, k, v, lam, do = test_diff.inputs(4, 2, 2, 70, "bf16", 3)
     got, want = (fa.diff_fwd(q, k, v, lam, seqlens_k=t) for t in (wide, full))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
