@@ -172,6 +172,26 @@ def rope_frequencies(rot, *, base=10000.0, scaling="none", factor=1.0, original_
     return torch.tensor(list(buf), dtype=torch.float64).to(device), float(m.value)
 
 
+def _check_freq(inv_freq, q):
+    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or \
+            not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 tensor [rot/2] on q's device")
+
+
+def _positions(positions, q):
+    """(pointer, int64?, stride over sequences, stride over tokens) of the positions of q's tokens; zeros for None."""
+    if positions is None:
+        return 0, 0, 0, 0
+    B, N = q.shape[0], q.shape[2]
+    wide = positions.dtype is torch.int64
+    if not (wide or positions.dtype is torch.int32) or positions.get_device() != q.get_device():
+        raise ValueError("positions must be an int32 or int64 tensor on q's device")
+    ps = positions.shape
+    if not (ps == (N,) or ps == (B, N) or ps == (1, N)):
+        raise ValueError("positions must have shape [N], [1, N] or [B, N]")
+    return positions.data_ptr(), wide, positions.stride(0) if len(ps) == 2 and ps[0] > 1 else 0, positions.stride(-1)
+
+
 def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleaved=False, backward=False, out=None,
          stream=None):
     """q and k rotated by their positions (fa_rope), as (q_out, k_out); q_out alone without k.
@@ -190,20 +210,8 @@ def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleave
             raise ValueError("k must be [B, H_kv, N, d]")
         Hkv = k.shape[1]
         ks = _rows(k, "k", q, (B, Hkv, N, d))[:3]
-    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or \
-            not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 tensor [rot/2] on q's device")
-    pos, wide, pos_b, pos_n = 0, 0, 0, 0
-    if positions is not None:
-        wide = positions.dtype is torch.int64
-        if not (wide or positions.dtype is torch.int32) or positions.get_device() != q.get_device():
-            raise ValueError("positions must be an int32 or int64 tensor on q's device")
-        ps = positions.shape
-        if not (ps == (N,) or ps == (B, N) or ps == (1, N)):
-            raise ValueError("positions must have shape [N], [1, N] or [B, N]")
-        pos, pos_n = positions.data_ptr(), positions.stride(-1)
-        if len(ps) == 2 and ps[0] > 1:
-            pos_b = positions.stride(0)
+    _check_freq(inv_freq, q)
+    pos, wide, pos_b, pos_n = _positions(positions, q)
     with _on(q.device, stream) as raw:
         if out is None:
             qo = torch.empty_like(q)
@@ -221,6 +229,99 @@ def rope(q, k=None, *, inv_freq, positions=None, start=0, mscale=1.0, interleave
     if st != FA_OK:
         raise FAError(st, "fa_rope")
     return qo if k is None else (qo, ko)
+
+
+class fa_norm_rope_params(ctypes.Structure):
+    _fields_ = ([(n, _i32) for n in ("B", "H", "H_kv", "N", "d", "rot", "dtype", "interleaved", "positions_i64")] +
+                [("%s_stride_%s" % (t, x), _i64) for t in ("q", "k", "q_out", "k_out", "dq", "dk") for x in "bhn"] +
+                [("positions", _vp), ("pos_stride_b", _i64), ("pos_stride_n", _i64), ("start", _i64),
+                 ("inv_freq", _vp), ("mscale", _f32), ("eps", _f32)])
+
+
+_pack_norm = _packer(fa_norm_rope_params)
+
+
+def _norm_args(q, k, q_weight, k_weight, inv_freq, out, what):
+    """Checks of both directions' arguments: (H_kv, k's strides, rot, checked outputs or None)."""
+    _check4(q, "q")
+    B, H, N, d = q.shape
+    Hkv, ks = 0, (0, 0, 0)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must be [B, H_kv, N, d]")
+        Hkv = k.shape[1]
+        ks = _rows(k, "k", q, (B, Hkv, N, d))[:3]
+    elif k_weight is not None:
+        raise ValueError("k_weight is given without k")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _flat_f32(t, n, q.device, (d,))
+    if inv_freq is not None:
+        _check_freq(inv_freq, q)
+    if out is not None:
+        out = (out, None) if k is None and isinstance(out, torch.Tensor) else out
+        _rows(out[0], "out " + what[0], q, q.shape)
+        if k is not None:
+            _rows(out[1], "out " + what[1], q, k.shape)
+    return Hkv, ks, 0 if inv_freq is None else 2 * inv_freq.shape[0], out
+
+
+def norm_rope(q, k=None, *, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None, positions=None, start=0, mscale=1.0,
+              interleaved=False, out=None, stream=None):
+    """q and k normalised for each head and rotated by their positions in one
+    pass (fa_norm_rope), as (q_out, k_out); q_out alone without k.
+
+    A row x (one token of one head) becomes R_p (w * x / sqrt(mean(x^2) + eps)).
+    q [B,H,N,d], k [B,H_kv,N,d]; ``q_weight`` and ``k_weight`` float32 [d] or
+    None (ones).  ``inv_freq`` (None: no rotation), ``positions``, ``start``,
+    ``mscale`` and ``interleaved`` as in :func:`rope`.  ``out`` = (q_out,
+    k_out), or q_out without k, may be the inputs themselves (but the backward
+    pass needs q and k as they were)."""
+    Hkv, ks, rot, out = _norm_args(q, k, q_weight, k_weight, inv_freq, out, ("q", "k"))
+    B, H, N, d = q.shape
+    pos, wide, pos_b, pos_n = _positions(positions, q)
+    with _on(q.device, stream) as raw:
+        qo, ko = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
+        p = _pack_norm(B, H, Hkv, N, d, rot, DTYPE_CODE[q.dtype], bool(interleaved), wide, *q.stride()[:3], *ks,
+                       *qo.stride()[:3], *(ks if k is None else ko.stride()[:3]), 0, 0, 0, 0, 0, 0, pos, pos_b, pos_n,
+                       int(start), 0 if inv_freq is None else inv_freq.data_ptr(), float(mscale), float(eps))
+        st = _ptrs("fa_norm_rope", 8)(p, q.data_ptr(), None if k is None else k.data_ptr(), _ptr(q_weight),
+                                      _ptr(k_weight), qo.data_ptr(), None if k is None else ko.data_ptr(), raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_norm_rope")
+    return qo if k is None else (qo, ko)
+
+
+def norm_rope_bwd(q, k, dq_out, dk_out=None, *, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None, positions=None,
+                  start=0, mscale=1.0, interleaved=False, out=None, workspace=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of :func:`norm_rope` (fa_norm_rope_bwd)
+    for the gradients ``dq_out``, ``dk_out`` of its outputs; q, k and the other
+    arguments are the forward call's.  The gradient of a weight that is None,
+    and everything of a k that is None, is None.  The weights' gradients are
+    float32 [d].  ``out`` = (dq, dk) may be the tensors dq_out, dk_out."""
+    Hkv, ks, rot, out = _norm_args(q, k, q_weight, k_weight, inv_freq, out, ("dq", "dk"))
+    B, H, N, d = q.shape
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out come together")
+    gqs = _rows(dq_out, "dq_out", q, q.shape)[:3]
+    gks = (0, 0, 0) if k is None else _rows(dk_out, "dk_out", q, k.shape)[:3]
+    pos, wide, pos_b, pos_n = _positions(positions, q)
+    dev = q.device
+    with _on(dev, stream) as raw:
+        dq, dk = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
+        dwq = None if q_weight is None else torch.empty((d,), device=dev, dtype=torch.float32)
+        dwk = None if k_weight is None else torch.empty((d,), device=dev, dtype=torch.float32)
+        p = _pack_norm(B, H, Hkv, N, d, rot, DTYPE_CODE[q.dtype], bool(interleaved), wide, *q.stride()[:3], *ks,
+                       *dq.stride()[:3], *(ks if k is None else dk.stride()[:3]), *gqs, *gks, pos, pos_b, pos_n,
+                       int(start), 0 if inv_freq is None else inv_freq.data_ptr(), float(mscale), float(eps))
+        ws = _need_workspace(workspace, _size_of("fa_norm_rope_bwd_workspace_size")(p), dev)
+        st = _sized("fa_norm_rope_bwd", 12)(p, q.data_ptr(), None if k is None else k.data_ptr(), dq_out.data_ptr(),
+                                            None if k is None else dk_out.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+                                            dq.data_ptr(), None if k is None else dk.data_ptr(), _ptr(dwq), _ptr(dwk),
+                                            ws.data_ptr(), ws.numel(), raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_norm_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 class fa_diff_params(ctypes.Structure):

@@ -785,6 +785,6 @@ const char* fa_status_string(fa_status s) {
   return "FA_ERR_UNKNOWN";
 }
 
-int32_t fa_version(void) { return 104; }
+int32_t fa_version(void) { return 105; }
 
 }  // extern "C"

@@ -1,0 +1,568 @@
+// norm_rope.cu -- q and k normalised for each head and rotated by their
+// positions in one pass, and the gradients of that.
+//
+// Mathematics.  A row x of d columns (one token of one head) becomes
+//     h = x r,  r = 1 / sqrt(mean(x^2) + eps),   y = R_p (w o h),
+// with w the d weights that all heads of q (of k) share and R_p the rotation of
+// rope.cu.  For the gradient dy of y:
+//     dz = R_p^T dy,  g = w o dz,
+//     dx = r g - x r^3 (g . x) / d,   dw = sum over rows of dz o h.
+// x^2 and g . x do not need each other, so one round of shuffles sums both.  r
+// is made again from x instead of being kept: x has to be read anyway.
+//
+// What bounds it: HBM.  The forward pass reads and writes each element once, the
+// backward reads x and dy and writes dx.  As in rope.cu a thread owns 16 (8)
+// columns of one token and walks over the heads, so that a sine and cosine
+// serve them all; a row is the columns of a group of 2^n lanes, which shuffles
+// sum.  dw is summed by a thread over its rows in registers, by a CTA through
+// shared memory and over the CTAs by a second kernel, each in a fixed order.
+#include <algorithm>
+#include <cmath>
+
+#include "rope.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kNThreads = 128;
+
+// Where the pairs of a thread's columns lie.
+enum Pairs {
+  kHalves = 0,   // (i, i + rot/2), rot/2 a multiple of 8: a thread owns 8 columns of each half, or 8 that do not turn
+  kAdjacent,     // (2i, 2i + 1): 8 columns
+  kShared        // (i, i + rot/2), any rot: 8 columns, the partners through shared memory
+};
+
+struct NormArgs {
+  const void* x[2];        // q, k
+  const void* dy[2];       // backward only
+  void* y[2];              // y, or dx
+  const float* w[2];       // [d] or nullptr (ones)
+  Strides xs[2], ds[2], ys[2];
+  int heads[2];
+  int N, d, rot, units, lg;   // units: threads that own columns of a row; 2^lg lanes a row
+  int hp;                  // heads per blockIdx.y (forward), per work item (backward)
+  uint32_t tokens;         // B * N
+  const void* pos;
+  int pos64;
+  int64_t pos_b, pos_n, start;
+  const double* inv_freq;
+  float mscale, eps, inv_d;
+  // backward: CTAs of q, then of k; each walks over items of (tokens, heads) and leaves one row of sums
+  int ctas[2];
+  float* part;             // [ctas[0] + ctas[1]][d]
+  float* dw[2];            // [d] or nullptr
+};
+
+// 8 consecutive elements
+template <typename T> struct V8;
+template <> struct V8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* f) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <typename T> struct V8 {
+  uint4 a;
+  __device__ __forceinline__ void load(const T* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = Cvt<T>::lo(w[i]);
+      f[2 * i + 1] = Cvt<T>::hi(w[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float* f) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(Cvt<T>::pack(f[0], f[1]), Cvt<T>::pack(f[2], f[3]),
+                                              Cvt<T>::pack(f[4], f[5]), Cvt<T>::pack(f[6], f[7]));
+  }
+};
+
+// The sines, cosines and weights of one thread's columns.  Columns of the
+// thread: c0 .. c0 + 7 and, in kHalves where they turn, c1 .. c1 + 7.
+template <int kPairs> struct Turn {
+  static constexpr int NC = kPairs == kHalves ? 16 : 8;
+  static constexpr int NP = kPairs == kAdjacent ? 4 : 8;
+  bool live, rotates, two;         // owns columns; some of them turn; owns the second eight
+  int c0, c1, half;
+  float cs[NP], sn[NP], w[NC];
+
+  __device__ __forceinline__ void place(int u, int rot, int units) {
+    half = rot >> 1;
+    live = u < units;
+    if constexpr (kPairs == kHalves) {
+      const int nrot = half >> 3;
+      two = rotates = u < nrot;
+      c0 = rotates ? u * 8 : rot + (u - nrot) * 8;
+    } else {
+      two = false;
+      c0 = u * 8;
+      rotates = c0 < rot;
+    }
+    c1 = two ? c0 + half : c0;
+    if (!live) rotates = two = false;
+  }
+  __device__ __forceinline__ void angles(long long p, const unsigned long long* sF, const float* sM, float sgn) {
+    if (!rotates) return;
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      int i = kPairs == kAdjacent ? (c0 >> 1) + e : c0 + e;
+      if (kPairs == kShared && i >= half) i -= half;
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+      if (kPairs == kHalves || i < half) turn(p, sF[i], sM[i], sgn * sM[i], cs[e], sn[e]);
+    }
+  }
+  __device__ __forceinline__ void weights(const float* g) {
+#pragma unroll
+    for (int e = 0; e < NC; ++e) {
+      const int c = e < 8 ? c0 + e : c1 + e - 8;
+      w[e] = g != nullptr && live && (e < 8 || two) ? g[c] : 1.f;
+    }
+  }
+  // v turned (kShared: `row` is the shared memory of this row, which its lanes have to themselves)
+  __device__ __forceinline__ void apply(float (&v)[NC], float* row) const {
+    if constexpr (kPairs == kShared) {
+      __syncwarp();
+      if (live) {
+        reinterpret_cast<float4*>(row + c0)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(row + c0)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+      __syncwarp();
+      if (rotates) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = c0 + e;
+          if (c < half) v[e] = v[e] * cs[e] - row[c + half] * sn[e];
+          else if (c < 2 * half) v[e] = v[e] * cs[e] + row[c - half] * sn[e];
+        }
+      }
+    } else if (rotates) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        const int a = kPairs == kHalves ? e : 2 * e, b = kPairs == kHalves ? 8 + e : 2 * e + 1;
+        if (kPairs == kAdjacent && (c0 >> 1) + e >= half) continue;
+        const float x0 = v[a], x1 = v[b];
+        v[a] = x0 * cs[e] - x1 * sn[e];
+        v[b] = x1 * cs[e] + x0 * sn[e];
+      }
+    }
+  }
+};
+
+// sum over the 2^lg lanes of a row (every lane of the warp takes part)
+__device__ __forceinline__ float row_sum(float s, int lg) {
+  for (int o = 1 << lg >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+__device__ __forceinline__ void load_turns(const NormArgs& a, unsigned long long* sF, float* sM) {
+  // float64 is slow on this GPU: the turns are made once per CTA, not once per thread
+  for (int i = threadIdx.x; i < a.rot >> 1; i += kNThreads) {
+    const double f = a.inv_freq[i];
+    sF[i] = turns_of(f);
+    sM[i] = isfinite(f) ? a.mscale : nanf("");
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ long long position(const NormArgs& a, uint32_t b, uint32_t n) {
+  if (a.pos == nullptr) return a.start + (long long)n;
+  const int64_t at = (int64_t)b * a.pos_b + (int64_t)n * a.pos_n;
+  return a.pos64 ? static_cast<const long long*>(a.pos)[at] : (long long)static_cast<const int*>(a.pos)[at];
+}
+
+template <typename T, int kPairs>
+__global__ void __launch_bounds__(kNThreads) norm_rope_kernel(const NormArgs a) {
+  using R = Turn<kPairs>;
+  constexpr int HB = sizeof(T) == 4 ? 2 : 4;         // rows whose loads are in flight together
+  __shared__ unsigned long long sF[128];
+  __shared__ float sM[128];
+  __shared__ float rows[kPairs == kShared ? kNThreads * 8 : 8];
+  load_turns(a, sF, sM);
+  const uint32_t t = blockIdx.x * kNThreads + threadIdx.x;
+  const uint32_t token = t >> a.lg;
+  R r;
+  r.place((int)(t & ((1u << a.lg) - 1)), a.rot, a.units);
+  if (token >= a.tokens) r.live = r.rotates = r.two = false;
+  const uint32_t tk = min(token, a.tokens - 1);
+  const uint32_t b = tk / (uint32_t)a.N, n = tk - b * (uint32_t)a.N;
+  r.angles(position(a, b, n), sF, sM, 1.f);
+  float* row = rows + (kPairs == kShared ? (threadIdx.x >> a.lg << a.lg) * 8 : 0);
+  const int first = blockIdx.y * a.hp;
+#pragma unroll 1
+  for (int v = 0; v < 2; ++v) {                      // q's heads, then k's
+    const int off = v ? a.heads[0] : 0;
+    const int h0 = max(first - off, 0), h1 = min(first + a.hp - off, a.heads[v]);
+    if (h0 >= h1) continue;
+    r.weights(a.w[v]);
+    const Strides xs = a.xs[v], ys = a.ys[v];
+    const T* src = static_cast<const T*>(a.x[v]) + (int64_t)b * xs.b + (int64_t)h0 * xs.h + (int64_t)n * xs.n;
+    T* dst = static_cast<T*>(a.y[v]) + (int64_t)b * ys.b + (int64_t)h0 * ys.h + (int64_t)n * ys.n;
+    for (int h = h0; h < h1; h += HB, src += HB * xs.h, dst += HB * ys.h) {
+      V8<T> v0[HB], v1[HB];
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        if (h + j >= h1) break;
+        if (r.live) v0[j].load(src + j * xs.h + r.c0);
+        if (r.two) v1[j].load(src + j * xs.h + r.c1);
+      }
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        if (h + j >= h1) break;
+        float x[R::NC] = {};
+        if (r.live) v0[j].get(x);
+        if (R::NC > 8 && r.two) v1[j].get(x + (R::NC - 8));
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < R::NC; ++e) s += x[e] * x[e];
+        s = rsqrtf(row_sum(s, a.lg) * a.inv_d + a.eps);
+#pragma unroll
+        for (int e = 0; e < R::NC; ++e) x[e] = x[e] * s * r.w[e];
+        r.apply(x, row);
+        if (r.live) V8<T>::store(dst + j * ys.h + r.c0, x);
+        if (R::NC > 8 && r.two) V8<T>::store(dst + j * ys.h + r.c1, x + (R::NC - 8));
+      }
+    }
+  }
+}
+
+// Backward.  CTA c of q (of k) takes work items c, c + ctas, ...: kNThreads >> lg
+// tokens and hp heads each.
+template <typename T, int kPairs>
+__global__ void __launch_bounds__(kNThreads) norm_rope_bwd_kernel(const NormArgs a) {
+  using R = Turn<kPairs>;
+  constexpr int HB = sizeof(T) == 4 ? 1 : 2;
+  __shared__ unsigned long long sF[128];
+  __shared__ float sM[128];
+  __shared__ float rows[kPairs == kShared ? kNThreads * 8 : 8];
+  __shared__ float sums[kNThreads * R::NC];
+  load_turns(a, sF, sM);
+  const int v = (int)blockIdx.x < a.ctas[0] ? 0 : 1;
+  const int c = (int)blockIdx.x - (v ? a.ctas[0] : 0);
+  const int per = kNThreads >> a.lg;                 // tokens of an item
+  const uint32_t tiles = (a.tokens + per - 1) / per;
+  const int splits = (a.heads[v] + a.hp - 1) / a.hp;
+  R r;
+  r.place((int)threadIdx.x & ((1 << a.lg) - 1), a.rot, a.units);
+  r.weights(a.w[v]);
+  const R all = r;
+  float* row = rows + (kPairs == kShared ? (threadIdx.x >> a.lg << a.lg) * 8 : 0);
+  const Strides xs = a.xs[v], ds = a.ds[v], ys = a.ys[v];
+  float acc[R::NC] = {};
+  for (unsigned long long u = c; u < (unsigned long long)tiles * splits; u += a.ctas[v]) {
+    const uint32_t tile = (uint32_t)(u % tiles);
+    const int h0 = (int)(u / tiles) * a.hp, h1 = min(h0 + a.hp, a.heads[v]);
+    const uint32_t token = tile * per + (threadIdx.x >> a.lg);
+    r.live = all.live && token < a.tokens;
+    r.two = all.two && token < a.tokens;
+    r.rotates = all.rotates && token < a.tokens;
+    const uint32_t tk = min(token, a.tokens - 1);
+    const uint32_t b = tk / (uint32_t)a.N, n = tk - b * (uint32_t)a.N;
+    r.angles(position(a, b, n), sF, sM, -1.f);       // the transposed rotation
+    const T* src = static_cast<const T*>(a.x[v]) + (int64_t)b * xs.b + (int64_t)h0 * xs.h + (int64_t)n * xs.n;
+    const T* grd = static_cast<const T*>(a.dy[v]) + (int64_t)b * ds.b + (int64_t)h0 * ds.h + (int64_t)n * ds.n;
+    T* dst = static_cast<T*>(a.y[v]) + (int64_t)b * ys.b + (int64_t)h0 * ys.h + (int64_t)n * ys.n;
+    for (int h = h0; h < h1; h += HB, src += HB * xs.h, grd += HB * ds.h, dst += HB * ys.h) {
+      V8<T> x0[HB], x1[HB], g0[HB], g1[HB];
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        if (h + j >= h1) break;
+        if (r.live) {
+          x0[j].load(src + j * xs.h + r.c0);
+          g0[j].load(grd + j * ds.h + r.c0);
+        }
+        if (r.two) {
+          x1[j].load(src + j * xs.h + r.c1);
+          g1[j].load(grd + j * ds.h + r.c1);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        if (h + j >= h1) break;
+        float x[R::NC] = {}, g[R::NC] = {};
+        if (r.live) {
+          x0[j].get(x);
+          g0[j].get(g);
+        }
+        if (R::NC > 8 && r.two) {
+          x1[j].get(x + (R::NC - 8));
+          g1[j].get(g + (R::NC - 8));
+        }
+        r.apply(g, row);                             // dz
+        float sx = 0.f, sg = 0.f;
+#pragma unroll
+        for (int e = 0; e < R::NC; ++e) {
+          sx += x[e] * x[e];
+          sg += g[e] * r.w[e] * x[e];
+        }
+        for (int o = 1 << a.lg >> 1; o > 0; o >>= 1) {
+          sx += __shfl_xor_sync(0xffffffffu, sx, o);
+          sg += __shfl_xor_sync(0xffffffffu, sg, o);
+        }
+        const float rs = rsqrtf(sx * a.inv_d + a.eps);
+        const float k = rs * rs * sg * a.inv_d;      // dx = rs (w dz - x rs^2 (g . x) / d)
+#pragma unroll
+        for (int e = 0; e < R::NC; ++e) {
+          acc[e] += g[e] * (x[e] * rs);
+          x[e] = rs * (g[e] * r.w[e] - x[e] * k);
+        }
+        if (r.live) V8<T>::store(dst + j * ys.h + r.c0, x);
+        if (R::NC > 8 && r.two) V8<T>::store(dst + j * ys.h + r.c1, x + (R::NC - 8));
+      }
+    }
+  }
+  if (a.dw[v] == nullptr) return;
+  // the CTA's sums: the groups' partial sums of a column, in the order of the groups
+#pragma unroll
+  for (int e = 0; e < R::NC; ++e) sums[e * kNThreads + threadIdx.x] = acc[e];
+  __syncthreads();
+  if ((int)threadIdx.x >= 1 << a.lg || !all.live) return;
+#pragma unroll
+  for (int e = 0; e < R::NC; ++e) {
+    if (e >= 8 && !all.two) break;
+    float s = 0.f;
+    for (int g = 0; g < per; ++g) s += sums[e * kNThreads + (g << a.lg) + threadIdx.x];
+    a.part[(size_t)blockIdx.x * a.d + (e < 8 ? all.c0 + e : all.c1 + e - 8)] = s;
+  }
+}
+
+// dw of q (block 0) and k (block 1): a column's partial sums, 1024 / d (rounded
+// down) threads a column, joined in their order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int d, int n0, int n1, float* dq,
+                                                       float* dk) {
+  __shared__ float sh[1024];
+  float* out = blockIdx.x ? dk : dq;
+  if (out == nullptr) return;
+  const int n = blockIdx.x ? n1 : n0;
+  part += blockIdx.x ? (size_t)n0 * d : 0;
+  const int g = (int)threadIdx.x / d, c = (int)threadIdx.x - g * d, ng = 1024 / d;
+  float s = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (g < ng) {
+#pragma unroll 8
+    for (int i = g; i < n; i += ng) s += part[(size_t)i * d + c];
+  }
+  sh[threadIdx.x] = s;
+  __syncthreads();
+  if (g != 0) return;
+  s = 0.f;
+  for (int i = 0; i < ng; ++i) s += sh[i * d + c];
+  out[c] = s;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+bool n16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+fa_status norm_strides(Strides& s, int B, int heads, int N, int d, int unit, bool output) {
+  if (N == 1) s.n = d;
+  if (heads == 1) s.h = (int64_t)N * s.n;
+  if (B == 1) s.b = (int64_t)heads * s.h;
+  const int64_t least = output ? 1 : 0;          // an input may be broadcast (stride 0)
+  if (s.n < (output ? d : 0) || s.h < least || s.b < least) return FA_ERR_INVALID_ARG;
+  if (s.n % unit || s.h % unit || s.b % unit) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+Pairs pairs_of(const fa_norm_rope_params* p) {
+  if (p->interleaved) return kAdjacent;
+  return p->rot % 16 == 0 ? kHalves : kShared;
+}
+
+int units_of(const fa_norm_rope_params* p) {
+  return pairs_of(p) == kHalves ? (p->d - p->rot / 2) / 8 : p->d / 8;
+}
+
+int lg_of(int units) {
+  int lg = 0;
+  while ((1 << lg) < units) ++lg;
+  return lg;
+}
+
+// the shape alone
+fa_status check_norm(const fa_norm_rope_params* p) {
+  if (p == nullptr) return FA_ERR_INVALID_ARG;
+  if (p->B < 1 || p->H < 1 || p->H_kv < 0 || p->N < 1 || p->d < 1) return FA_ERR_INVALID_ARG;
+  if (p->dtype != FA_DT_F32 && p->dtype != FA_DT_F16 && p->dtype != FA_DT_BF16) return FA_ERR_INVALID_ARG;
+  if (p->rot < 0 || p->rot > p->d || (p->rot & 1)) return FA_ERR_INVALID_ARG;
+  if (p->d % 8 != 0 || p->d > 256) return FA_ERR_UNSUPPORTED;
+  if (!std::isfinite(p->mscale) || !std::isfinite(p->eps) || !(p->eps > 0.f)) return FA_ERR_INVALID_ARG;
+  if (p->rot > 0 && p->inv_freq == nullptr) return FA_ERR_INVALID_ARG;
+  // 32-bit thread and token indexes
+  if ((unsigned long long)p->B * p->N * p->d >= (1ull << 32) - 4096) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status sm_count(int& sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return FA_OK;
+}
+
+constexpr int kNormCtas = 152 * 5;     // of the backward pass, at most: a workspace's size does not depend on the device
+
+// CTAs of q and of k: by their heads, no more than there are tokens' tiles x heads
+void bwd_ctas(const fa_norm_rope_params* p, int (&n)[2]) {
+  const int heads[2] = {p->H, p->H_kv};
+  const int per = kNThreads >> lg_of(units_of(p));
+  const long long tiles = ((long long)p->B * p->N + per - 1) / per;
+  for (int v = 0; v < 2; ++v) {
+    const long long share = std::max<long long>(1, (long long)kNormCtas * heads[v] / (p->H + p->H_kv));
+    n[v] = heads[v] == 0 ? 0 : (int)std::min(share, tiles * heads[v]);
+  }
+}
+
+// What both directions check and fill in.  t: x, dy (backward), y
+fa_status fill(const fa_norm_rope_params* p, const void* const (&x)[2], const void* const (&dy)[2], void* const (&y)[2],
+               const float* const (&w)[2], bool bwd, NormArgs& a) {
+  fa_status s = check_norm(p);
+  if (s != FA_OK) return s;
+  const int nt = p->H_kv > 0 ? 2 : 1;
+  for (int v = 0; v < nt; ++v)
+    if (x[v] == nullptr || y[v] == nullptr || (bwd && dy[v] == nullptr)) return FA_ERR_INVALID_ARG;
+  for (int v = 0; v < nt; ++v) {
+    if (!n16(x[v]) || !n16(y[v]) || (bwd && !n16(dy[v]))) return FA_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(w[v]) & 3u) return FA_ERR_MISALIGNED;
+  }
+  if (reinterpret_cast<uintptr_t>(p->inv_freq) & 7u) return FA_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(p->positions) & (p->positions_i64 ? 7u : 3u)) return FA_ERR_MISALIGNED;
+  const int unit = p->dtype == FA_DT_F32 ? 4 : 8;
+  a.xs[0] = {p->q_stride_b, p->q_stride_h, p->q_stride_n};
+  a.ys[0] = {p->q_out_stride_b, p->q_out_stride_h, p->q_out_stride_n};
+  a.ds[0] = {p->dq_stride_b, p->dq_stride_h, p->dq_stride_n};
+  a.xs[1] = {p->k_stride_b, p->k_stride_h, p->k_stride_n};
+  a.ys[1] = {p->k_out_stride_b, p->k_out_stride_h, p->k_out_stride_n};
+  a.ds[1] = {p->dk_stride_b, p->dk_stride_h, p->dk_stride_n};
+  a.heads[0] = p->H; a.heads[1] = p->H_kv;
+  for (int v = 0; v < nt; ++v) {
+    s = norm_strides(a.xs[v], p->B, a.heads[v], p->N, p->d, unit, false);
+    if (s == FA_OK) s = norm_strides(a.ys[v], p->B, a.heads[v], p->N, p->d, unit, true);
+    if (s == FA_OK && bwd) s = norm_strides(a.ds[v], p->B, a.heads[v], p->N, p->d, unit, false);
+    if (s != FA_OK) return s;
+    // an output in an input's place needs the input's strides: rows would overwrite one another
+    const void* in[2] = {x[v], bwd ? dy[v] : nullptr};
+    const Strides st[2] = {a.xs[v], a.ds[v]};
+    for (int i = 0; i < 2; ++i)
+      if (in[i] == y[v] && (st[i].b != a.ys[v].b || st[i].h != a.ys[v].h || st[i].n != a.ys[v].n))
+        return FA_ERR_INVALID_ARG;
+    a.x[v] = x[v]; a.dy[v] = dy[v]; a.y[v] = y[v]; a.w[v] = w[v];
+  }
+  a.N = p->N; a.d = p->d; a.rot = p->rot;
+  a.units = units_of(p);
+  a.lg = lg_of(a.units);
+  a.tokens = (uint32_t)((long long)p->B * p->N);
+  a.pos = p->positions; a.pos64 = p->positions_i64;
+  a.pos_b = p->pos_stride_b; a.pos_n = p->pos_stride_n; a.start = p->start;
+  a.inv_freq = p->inv_freq;
+  a.mscale = p->mscale; a.eps = p->eps; a.inv_d = 1.f / (float)p->d;
+  return FA_OK;
+}
+
+template <typename T, int kPairs> cudaError_t launch_fwd(NormArgs a, int sms, cudaStream_t s) {
+  const unsigned long long threads = (unsigned long long)a.tokens << a.lg;
+  const unsigned gx = (unsigned)((threads + kNThreads - 1) / kNThreads);
+  const int heads = a.heads[0] + a.heads[1];
+  // split the heads until the grid fills the GPU about twice at 1,024 threads a SM, as in rope.cu
+  const long long want = 2ll * sms * 1024 / kNThreads;
+  int split = (int)std::min<long long>((want + gx - 1) / gx, heads);
+  split = std::min(split, 65535);
+  a.hp = (heads + split - 1) / split;
+  if (a.hp > 4) a.hp = (a.hp + 3) / 4 * 4;          // whole batches of loads
+  split = (heads + a.hp - 1) / a.hp;
+  norm_rope_kernel<T, kPairs><<<dim3(gx, (unsigned)split), kNThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int kPairs> cudaError_t launch_bwd(NormArgs a, cudaStream_t s) {
+  // heads of an item: all, unless there are fewer tiles of tokens than CTAs
+  const int per = kNThreads >> a.lg;
+  const long long tiles = ((long long)a.tokens + per - 1) / per;
+  a.hp = 1;
+  for (int v = 0; v < 2; ++v)
+    if (a.heads[v] > 0) {
+      const long long splits = std::min<long long>(a.heads[v], (a.ctas[v] + tiles - 1) / tiles);
+      a.hp = std::max(a.hp, (int)((a.heads[v] + splits - 1) / splits));
+    }
+  norm_rope_bwd_kernel<T, kPairs><<<(unsigned)(a.ctas[0] + a.ctas[1]), kNThreads, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(2);
+  c.blockDim = dim3(1024);
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, norm_dw_kernel, (const float*)a.part, a.d, a.ctas[0], a.ctas[1], a.dw[0], a.dw[1]);
+}
+
+template <typename T> cudaError_t launch(const NormArgs& a, Pairs m, bool bwd, int sms, cudaStream_t s) {
+  switch (m) {
+    case kHalves: return bwd ? launch_bwd<T, kHalves>(a, s) : launch_fwd<T, kHalves>(a, sms, s);
+    case kAdjacent: return bwd ? launch_bwd<T, kAdjacent>(a, s) : launch_fwd<T, kAdjacent>(a, sms, s);
+    default: return bwd ? launch_bwd<T, kShared>(a, s) : launch_fwd<T, kShared>(a, sms, s);
+  }
+}
+
+cudaError_t launch_dt(const fa_norm_rope_params* p, const NormArgs& a, bool bwd, int sms, cudaStream_t s) {
+  const Pairs m = pairs_of(p);
+  if (p->dtype == FA_DT_F32) return launch<float>(a, m, bwd, sms, s);
+  if (p->dtype == FA_DT_F16) return launch<__half>(a, m, bwd, sms, s);
+  return launch<__nv_bfloat16>(a, m, bwd, sms, s);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_norm_rope(const fa_norm_rope_params* p, const void* q, const void* k, const float* q_weight,
+                       const float* k_weight, void* q_out, void* k_out, void* stream) {
+  NormArgs a{};
+  fa_status s = fill(p, {q, k}, {nullptr, nullptr}, {q_out, k_out}, {q_weight, k_weight}, false, a);
+  int sms = 0;
+  if (s != FA_OK || (s = sm_count(sms)) != FA_OK) return s;
+  return launch_dt(p, a, false, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_norm_rope_bwd_workspace_size(const fa_norm_rope_params* p) {
+  if (check_norm(p) != FA_OK) return 256;
+  int n[2];
+  bwd_ctas(p, n);
+  return 256 + (size_t)(n[0] + n[1]) * p->d * sizeof(float);
+}
+
+fa_status fa_norm_rope_bwd(const fa_norm_rope_params* p, const void* q, const void* k, const void* dq_out,
+                           const void* dk_out, const float* q_weight, const float* k_weight, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes, void* stream) {
+  NormArgs a{};
+  fa_status s = fill(p, {q, k}, {dq_out, dk_out}, {dq, dk}, {q_weight, k_weight}, true, a);
+  if (s != FA_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) return FA_ERR_MISALIGNED;
+  if (ws == nullptr || ws_bytes < fa_norm_rope_bwd_workspace_size(p) || !n16(ws)) return FA_ERR_WORKSPACE;
+  bwd_ctas(p, a.ctas);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+  a.dw[0] = dq_weight;
+  a.dw[1] = p->H_kv > 0 ? dk_weight : nullptr;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return launch_dt(p, a, true, 0, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -490,13 +490,67 @@ size_t fa_prefix_workspace_size(const fa_prefix_params *p);
 fa_status fa_prefix_fwd(const fa_prefix_params *p, const void *q, const void *k_prefix, const void *v_prefix,
                         const void *k, const void *v, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Norms of q and k with the rotation (ABI 1.5).
+ * fa_norm_rope normalises every row of q and k (one token of one head) and
+ * rotates it, in one pass:
+ *     y = R_p (w o x / sqrt(mean(x^2) + eps)),
+ * with w the weights of q or of k (device float32 [d], NULL: ones) and R_p
+ * fa_rope's rotation of the first `rot` columns by the row's position (rot = 0:
+ * the norm alone; inv_freq may then be NULL).
+ * fa_norm_rope_bwd takes x (q, k) and the gradients of y (dq_out, dk_out) and
+ * writes the gradients of x (dq, dk) and of the weights, summed over all rows
+ * (dq_weight, dk_weight: device float32 [d], NULL: not wanted):
+ *     dz = R_p^T dy, h = x r, r = 1 / sqrt(mean(x^2) + eps), g = w o dz,
+ *     dx = r (g - h mean(g o h)),   dw = sum dz o h.
+ *   - q, q_out, dq_out, dq are [B,H,N,d], the others [B,H_kv,N,d] tensors of one
+ *     dtype (float32, float16, bfloat16), each with its own element strides: x in
+ *     q_stride_*, k_stride_*; what is written (y, or dx) in q_out_stride_*,
+ *     k_out_stride_*; dy in dq_stride_*, dk_stride_* (backward only).  H_kv = 0: no
+ *     k.  Inputs may be broadcast (stride 0).  An output may be an input in its
+ *     place (same base, same strides); any other overlap is an error of the caller.
+ *   - d, rot, positions, start, inv_freq and mscale as in fa_rope (rot = 0 too); eps > 0.
+ *   - Sums and products are float32, rounded once to the dtype: rows whose squares
+ *     sum to more than float32 holds become zeros.  A NaN or infinity makes its row
+ *     NaN (and, backward, the weights' gradients).
+ *   - Results repeat bit for bit; the weights' gradients depend on no atomics.
+ *   - The forward call is one launch without workspace.  Backward workspace:
+ *     fa_norm_rope_bwd_workspace_size bytes, 16-byte aligned; nothing persists in it.
+ *   - B*N*d < 2^32 - 4096.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, H, H_kv, N, d;
+  int32_t rot;               /* rotated leading columns, even; 0: no rotation   */
+  int32_t dtype;             /* fa_dtype                                        */
+  int32_t interleaved;       /* 0: pairs (i, i + rot/2); else (2i, 2i + 1)      */
+  int32_t positions_i64;     /* positions are int64                             */
+  int64_t q_stride_b, q_stride_h, q_stride_n;
+  int64_t k_stride_b, k_stride_h, k_stride_n;
+  int64_t q_out_stride_b, q_out_stride_h, q_out_stride_n;
+  int64_t k_out_stride_b, k_out_stride_h, k_out_stride_n;
+  int64_t dq_stride_b, dq_stride_h, dq_stride_n;
+  int64_t dk_stride_b, dk_stride_h, dk_stride_n;
+  const void *positions;     /* device, or NULL                                 */
+  int64_t pos_stride_b, pos_stride_n;
+  int64_t start;             /* position of token 0 when positions is NULL      */
+  const double *inv_freq;    /* device float64 [rot/2]                          */
+  float mscale, eps;
+} fa_norm_rope_params;
+
+fa_status fa_norm_rope(const fa_norm_rope_params *p, const void *q, const void *k, const float *q_weight,
+                       const float *k_weight, void *q_out, void *k_out, void *stream);
+size_t fa_norm_rope_bwd_workspace_size(const fa_norm_rope_params *p);
+fa_status fa_norm_rope_bwd(const fa_norm_rope_params *p, const void *q, const void *k, const void *dq_out,
+                           const void *dk_out, const float *q_weight, const float *k_weight, void *dq, void *dk,
+                           float *dq_weight, float *dk_weight, void *ws, size_t ws_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fa_status_string(fa_status s);
 
 /* Library ABI version (major * 100 + minor): 101 adds H_kv, kv_stride_*
  * and window to fa_params; 102 adds the FP8 forward; 103 adds fwd_kernel,
  * fa_noalloc_check_status and fa_noalloc_scratch; 104 adds fa_rope,
- * fa_diff_* and fa_prefix_*. */
+ * fa_diff_* and fa_prefix_*; 105 adds fa_norm_rope*. */
 int32_t fa_version(void);
 
 #ifdef __cplusplus
