@@ -12,4 +12,5 @@ from ._lib import (FAError, bwd, check_status, dropout_mask, fwd, load, make_par
 from ._lib import bwd_noalloc, noalloc_check_status, noalloc_scratch, selftest_wait_timeout  # noqa: F401
 from ._lib import fp8_layout, fp8_quantize, fp8_views, fwd_fp8  # noqa: F401
 from ._ops import diff_bwd, diff_fwd, norm_rope, norm_rope_bwd, prefix_fwd, rope, rope_frequencies  # noqa: F401
+from ._cache8 import cache8_append, cache8_fwd, cache8_read  # noqa: F401
 from ._build import build, LIB  # noqa: F401

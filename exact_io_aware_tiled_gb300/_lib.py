@@ -26,7 +26,7 @@ EXPORTED = ["fa_fwd_workspace_size", "fa_bwd_workspace_size", "fa_fwd", "fa_bwd"
             "fa_fp8_buffer_layout", "fa_fp8_quantize", "fa_fwd_fp8", "fa_rope", "fa_rope_frequencies",
             "fa_diff_fwd_workspace_size", "fa_diff_bwd_workspace_size", "fa_diff_fwd", "fa_diff_bwd",
             "fa_prefix_workspace_size", "fa_prefix_fwd", "fa_norm_rope", "fa_norm_rope_bwd_workspace_size",
-            "fa_norm_rope_bwd"]
+            "fa_norm_rope_bwd", "fa_cache8_append", "fa_cache8_read", "fa_cache8_workspace_size", "fa_cache8_fwd"]
 
 
 class fa_params(ctypes.Structure):

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache8.cuh"
 #include "fa_internal.h"
 
 namespace fa {
@@ -382,6 +383,75 @@ fa_status check_prefix(const fa_prefix_params* in, fa_prefix_params& p, PrefixSt
                   (e = row_strides(s.vp, 1, p.H_kv, p.P, dv)) != FA_OK))
     return e;
   return FA_OK;
+}
+
+// ---- paged cache in 8 bits ------------------------------------------------------
+struct Cache8Strides { Strides q, o, k, v, kc, vc; };
+
+// strides in bytes of a [pages,H_kv,page,d] code array
+fa_status code_strides(Strides& s, const fa_cache8_params& p) {
+  if (p.H_kv == 1) s.h = (int64_t)p.page * s.n;
+  if (p.pages == 1) s.b = (int64_t)p.H_kv * s.h;
+  if (s.n < p.d || s.h < 1 || s.b < 1) return FA_ERR_INVALID_ARG;
+  if (s.n % 16 || s.h % 16 || s.b % 16) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+// The problem with H_kv filled in, its strides normalised.  rows: append and read (k, v), else the attention (q, o)
+fa_status check_cache8(const fa_cache8_params* in, fa_cache8_params& p, Cache8Strides& s, bool rows) {
+  if (in == nullptr) return FA_ERR_INVALID_ARG;
+  p = *in;
+  if (p.B < 1 || p.H < 1 || p.T < 1 || p.d < 1 || p.H_kv < 0 || p.pages < 1 || p.width < 1) return FA_ERR_INVALID_ARG;
+  if (p.dtype != FA_DT_F32 && p.dtype != FA_DT_F16 && p.dtype != FA_DT_BF16) return FA_ERR_INVALID_ARG;
+  if ((p.d != 64 && p.d != 128) || p.dtype == FA_DT_F32) return FA_ERR_UNSUPPORTED;
+  if (p.page != 16 && p.page != 32 && p.page != 64 && p.page != 128) return FA_ERR_UNSUPPORTED;
+  if (p.H_kv == 0) p.H_kv = p.H;
+  if (p.H % p.H_kv != 0 || p.window < 0 || p.sinks < 0) return FA_ERR_INVALID_ARG;
+  if (p.B > 1 && p.table_stride < p.width) return FA_ERR_INVALID_ARG;
+  if (p.seqlens_k == nullptr || p.table == nullptr) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(p.seqlens_k) | reinterpret_cast<uintptr_t>(p.table)) & 3u) return FA_ERR_MISALIGNED;
+  if ((double)p.B * p.H * p.T >= (double)(1 << 26) || (long long)p.width * p.page > (1 << 28) ||
+      (long long)p.pages * p.H_kv >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  s.kc = {p.kc_stride_p, p.kc_stride_h, p.kc_stride_n};
+  s.vc = {p.vc_stride_p, p.vc_stride_h, p.vc_stride_n};
+  fa_status e;
+  if ((e = code_strides(s.kc, p)) != FA_OK || (e = code_strides(s.vc, p)) != FA_OK) return e;
+  if (rows) {
+    s.k = {p.k_stride_b, p.k_stride_h, p.k_stride_n};
+    s.v = {p.v_stride_b, p.v_stride_h, p.v_stride_n};
+    if ((e = row_strides(s.k, p.B, p.H_kv, p.T, p.d)) != FA_OK) return e;
+    return row_strides(s.v, p.B, p.H_kv, p.T, p.d);
+  }
+  s.q = {p.q_stride_b, p.q_stride_h, p.q_stride_n};
+  s.o = {p.o_stride_b, p.o_stride_h, p.o_stride_n};
+  if ((e = row_strides(s.q, p.B, p.H, p.T, p.d)) != FA_OK) return e;
+  return row_strides(s.o, p.B, p.H, p.T, p.d);
+}
+
+fa_status cache8_pointers(const void* kc, const void* vc, const float* ks, const float* vs) {
+  if (!kc || !vc || !ks || !vs) return FA_ERR_INVALID_ARG;
+  if (!aligned16(kc) || !aligned16(vc) || ((reinterpret_cast<uintptr_t>(ks) | reinterpret_cast<uintptr_t>(vs)) & 3u))
+    return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+Cache8Rows cache8_rows(const fa_cache8_params& p, const Cache8Strides& s, const void* kc, const void* vc,
+                       const float* ks, const float* vs, const void* k, const void* v) {
+  Cache8Rows a{};
+  a.B = p.B; a.Hkv = p.H_kv; a.T = p.T; a.d = p.d;
+  a.page = p.page; a.pages = p.pages; a.width = p.width;
+  while ((1 << a.lg) < p.page) ++a.lg;
+  a.lens = p.seqlens_k;
+  a.table = p.table;
+  a.table_stride = p.table_stride;
+  a.x[0] = const_cast<void*>(k); a.x[1] = const_cast<void*>(v);
+  a.xs[0] = s.k; a.xs[1] = s.v;
+  a.code[0] = static_cast<uint8_t*>(const_cast<void*>(kc));
+  a.code[1] = static_cast<uint8_t*>(const_cast<void*>(vc));
+  a.cs[0] = s.kc; a.cs[1] = s.vc;
+  a.scale[0] = const_cast<float*>(ks); a.scale[1] = const_cast<float*>(vs);
+  return a;
 }
 
 }  // namespace
@@ -770,6 +840,73 @@ fa_status fa_prefix_fwd(const fa_prefix_params* in, const void* q, const void* k
   const float scale = (p.scale > 0.f && std::isfinite(p.scale)) ? p.scale : 1.f / std::sqrt((float)p.d);
   return cuda_status(launch_prefix(&p, m, q, sd.q, o, sd.o, lse, scale * 1.4426950408889634f,
                                    static_cast<uint8_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache8_append(const fa_cache8_params* in, const void* k, const void* v, void* k_cache, void* v_cache,
+                           float* k_scale, float* v_scale, void* stream) {
+  fa_cache8_params p;
+  Cache8Strides sd;
+  fa_status s = check_cache8(in, p, sd, true);
+  if (s != FA_OK || (s = cache8_pointers(k_cache, v_cache, k_scale, v_scale)) != FA_OK) return s;
+  if (!k || !v) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
+  return cuda_status(launch_cache8_append(p.dtype, cache8_rows(p, sd, k_cache, v_cache, k_scale, v_scale, k, v),
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache8_read(const fa_cache8_params* in, const void* k_cache, const void* v_cache, const float* k_scale,
+                         const float* v_scale, void* k, void* v, void* stream) {
+  fa_cache8_params p;
+  Cache8Strides sd;
+  fa_status s = check_cache8(in, p, sd, true);
+  if (s != FA_OK || (s = cache8_pointers(k_cache, v_cache, k_scale, v_scale)) != FA_OK) return s;
+  if (!k || !v) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
+  return cuda_status(launch_cache8_read(p.dtype, cache8_rows(p, sd, k_cache, v_cache, k_scale, v_scale, k, v),
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_cache8_workspace_size(const fa_cache8_params* in) {
+  fa_cache8_params p;
+  Cache8Strides sd;
+  if (check_cache8(in, p, sd, false) != FA_OK) return 256;
+  return cache8_workspace(&p);
+}
+
+fa_status fa_cache8_fwd(const fa_cache8_params* in, const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                        void* stream) {
+  fa_cache8_params p;
+  Cache8Strides sd;
+  fa_status s = check_cache8(in, p, sd, false);
+  if (s != FA_OK || (s = cache8_pointers(k_cache, v_cache, k_scale, v_scale)) != FA_OK) return s;
+  if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return FA_ERR_MISALIGNED;
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < cache8_workspace(&p)) return FA_ERR_WORKSPACE;
+  const Cache8Rows rows = cache8_rows(p, sd, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr);
+  // boxes of up to one stage of the kernel; rows of d bytes: 64-byte swizzle for d = 64, 128-byte for d = 128
+  const cuuint32_t box = (cuuint32_t)std::min(p.page, p.d == 64 ? 64 : 32);
+  const CUtensorMapSwizzle sw = p.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const cuuint64_t d = (cuuint64_t)p.d, n = (cuuint64_t)p.page, h = (cuuint64_t)p.H_kv, np = (cuuint64_t)p.pages;
+  CUtensorMap m[2];
+  for (int y = 0; y < 2; ++y) {
+    const Strides& c = rows.cs[y];
+    if ((s = map_u8(&m[y], rows.code[y], {d, n, h, np}, {(cuuint64_t)c.n, (cuuint64_t)c.h, (cuuint64_t)c.b},
+                    (cuuint32_t)p.d, box, sw)) != FA_OK)
+      return s;
+  }
+  Cache8Args a{};
+  a.B = p.B; a.H = p.H; a.Hkv = p.H_kv; a.T = p.T; a.G = p.H / p.H_kv;
+  a.page = p.page; a.lg = rows.lg; a.pages = p.pages; a.width = p.width; a.cap = p.width * p.page;
+  a.window = std::min(p.window, a.cap);          // a window as long as the longest sequence hides nothing
+  a.sinks = p.sinks;
+  a.q = q; a.o = o; a.qs = sd.q; a.os = sd.o;
+  a.lse = lse;
+  a.lens = p.seqlens_k; a.table = p.table; a.table_stride = p.table_stride;
+  a.ks = k_scale; a.vs = v_scale;
+  a.scale_log2 = ((p.scale > 0.f && std::isfinite(p.scale)) ? p.scale : 1.f / std::sqrt((float)p.d)) * 1.4426950408889634f;
+  return cuda_status(launch_cache8_fwd(p.dtype, p.d, m[0], m[1], a, static_cast<uint8_t*>(ws),
+                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char* fa_status_string(fa_status s) {

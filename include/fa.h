@@ -544,13 +544,83 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params *p, const void *q, const vo
                            const void *dk_out, const float *q_weight, const float *k_weight, void *dq, void *dk,
                            float *dq_weight, float *dk_weight, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache in 8 bits (ABI 1.5): keys and values as E4M3 codes with one scale
+ * for each page (a block of `page` tokens) and K/V head.
+ *   - k_cache, v_cache: device uint8 [pages,H_kv,page,d] with their own byte strides
+ *     (kc_stride_*, vc_stride_*; rows contiguous); k_scale, v_scale: contiguous device
+ *     float32 [pages,H_kv].  A value is code * scale.
+ *   - table: device int32, row b (at b*table_stride, contiguous) the `width` pages of
+ *     sequence b in the order of its tokens: token j lies in row j % page of page
+ *     table[b][j / page].  An entry outside [0, pages) is an absent page: its tokens are
+ *     not seen, not written and read as zeros.  Entries behind the last row are not read.
+ *     Sequences may share pages that are only read; a page that is written must belong
+ *     to one sequence.
+ *   - seqlens_k: device int32 [B], rows filled, L_b, taken into [0, width*page]; the T new
+ *     tokens are the last T of them (L_b counts them).  Where L_b < T the first T - L_b
+ *     tokens do not exist: they are not written and see nothing.
+ *   - page 16, 32, 64 or 128; d = 64 or 128; dtype float16 or bfloat16 (of q, o, k, v).
+ *   - Rows of a page at or past L_b may hold anything; rows below L_b of present pages
+ *     should be finite.
+ * fa_cache8_append quantises k, v [B,H_kv,T,d] into the pages.  A page's scale is
+ * 2^e with the smallest whole e (-126 at least) for which max |x| <= 448 2^e over the
+ * finite values written to it (0 where all are zero); codes are E4M3(x / scale), round to
+ * nearest even.  A token that is the first row of its page starts the page's scale
+ * afresh; where rows precede it, the larger of the old scale and the new one holds, and
+ * if the scale grows the rows before are rounded again.  NaN stays NaN; an infinity becomes
+ * the largest code (NaN in a page without other values than zero).  Writing the same tokens
+ * once more changes nothing.
+ * fa_cache8_read writes rows 0 .. T-1 of every sequence to k, v [B,H_kv,T,d]: values of the
+ * dtype, zeros at and past L_b and for absent pages.
+ * fa_cache8_fwd attends: query t of sequence b, at position p = L_b - T + t, sees the keys
+ * j <= p and, with window > 0, of those only j > p - window or j < sinks.
+ *   - q, o: [B,H,T,d]; query head h reads K/V head h / (H / H_kv); H_kv = 0 selects H.
+ *     lse: contiguous float32 [B,H,T], natural log.  A query that sees no key has O = 0
+ *     and lse -inf.
+ *   - Scores from q rounded to 11 bits (exact for both dtypes) and the codes, float32 sums;
+ *     weights times their page's V scale are rounded to 11 bits before the product with
+ *     the codes, sums and joins are float32.  Any positive scale serves, 0 for a page of
+ *     zeros; the V scales of a sequence's pages have to lie within 2^-100 .. 2^100.
+ *   - Results repeat bit for bit for the same batch; how the keys are cut follows from all
+ *     lengths, so a sequence's last bit may change with the others' lengths.
+ *   - Workspace: fa_cache8_workspace_size bytes, 16-byte aligned, independent of the lengths
+ *     and the table's width; nothing persists in it; status word at its start.
+ *   - B*H*T < 2^26, width*page <= 2^28, pages*H_kv < 2^31.  16-byte rule for bases and
+ *     strides (a dimension of one element may have any stride); offsets are 64-bit.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, H, H_kv, T, d, dtype;
+  int32_t page, pages, width;  /* tokens of a page; pages of the cache; entries of a row of the table */
+  int32_t window, sinks;       /* fa_cache8_fwd: 0 = no window; first tokens that stay visible */
+  float scale;                 /* tau; <= 0 selects 1/sqrt(d)                     */
+  const int32_t *seqlens_k;
+  const int32_t *table;
+  int64_t table_stride;
+  int64_t q_stride_b, q_stride_h, q_stride_n;
+  int64_t o_stride_b, o_stride_h, o_stride_n;
+  int64_t k_stride_b, k_stride_h, k_stride_n;   /* fa_cache8_append, fa_cache8_read */
+  int64_t v_stride_b, v_stride_h, v_stride_n;
+  int64_t kc_stride_p, kc_stride_h, kc_stride_n;
+  int64_t vc_stride_p, vc_stride_h, vc_stride_n;
+} fa_cache8_params;
+
+fa_status fa_cache8_append(const fa_cache8_params *p, const void *k, const void *v, void *k_cache, void *v_cache,
+                           float *k_scale, float *v_scale, void *stream);
+fa_status fa_cache8_read(const fa_cache8_params *p, const void *k_cache, const void *v_cache, const float *k_scale,
+                         const float *v_scale, void *k, void *v, void *stream);
+size_t fa_cache8_workspace_size(const fa_cache8_params *p);
+fa_status fa_cache8_fwd(const fa_cache8_params *p, const void *q, const void *k_cache, const void *v_cache,
+                        const float *k_scale, const float *v_scale, void *o, float *lse, void *ws, size_t ws_bytes,
+                        void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fa_status_string(fa_status s);
 
 /* Library ABI version (major * 100 + minor): 101 adds H_kv, kv_stride_*
  * and window to fa_params; 102 adds the FP8 forward; 103 adds fwd_kernel,
  * fa_noalloc_check_status and fa_noalloc_scratch; 104 adds fa_rope,
- * fa_diff_* and fa_prefix_*; 105 adds fa_norm_rope*. */
+ * fa_diff_* and fa_prefix_*; 105 adds fa_norm_rope* and
+ * fa_cache8_*. */
 int32_t fa_version(void);
 
 #ifdef __cplusplus
