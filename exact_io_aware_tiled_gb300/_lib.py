@@ -26,7 +26,8 @@ EXPORTED = ["fa_fwd_workspace_size", "fa_bwd_workspace_size", "fa_fwd", "fa_bwd"
             "fa_fp8_buffer_layout", "fa_fp8_quantize", "fa_fwd_fp8", "fa_rope", "fa_rope_frequencies",
             "fa_diff_fwd_workspace_size", "fa_diff_bwd_workspace_size", "fa_diff_fwd", "fa_diff_bwd",
             "fa_prefix_workspace_size", "fa_prefix_fwd", "fa_norm_rope", "fa_norm_rope_bwd_workspace_size",
-            "fa_norm_rope_bwd", "fa_cache8_append", "fa_cache8_read", "fa_cache8_workspace_size", "fa_cache8_fwd"]
+            "fa_norm_rope_bwd", "fa_cache8_append", "fa_cache8_read", "fa_cache8_workspace_size", "fa_cache8_fwd",
+            "fa_fwd_sinks", "fa_bwd_sinks_workspace_size", "fa_bwd_sinks"]
 
 
 class fa_params(ctypes.Structure):
@@ -86,6 +87,12 @@ def load():
     lib.fa_fwd.restype = ctypes.c_int
     lib.fa_bwd.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fa_bwd.restype = ctypes.c_int
+    lib.fa_fwd_sinks.argtypes = [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_fwd_sinks.restype = ctypes.c_int
+    lib.fa_bwd_sinks_workspace_size.argtypes = [P, ctypes.c_int32]
+    lib.fa_bwd_sinks_workspace_size.restype = sz
+    lib.fa_bwd_sinks.argtypes = [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_bwd_sinks.restype = ctypes.c_int
     lib.fa_check_status.argtypes = [vp, vp]
     lib.fa_check_status.restype = ctypes.c_int
     lib.fa_dropout_mask.argtypes = [P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp]
@@ -240,11 +247,13 @@ def _workspace(lib_size, workspace, device):
 
 
 def fwd(q, k, v, *, causal=False, seqlens_k=None, dropout_p=0.0, seed=0, offset=0, block_mask=None,
-        scale=None, return_o_f32=False, stream=None, prof=None, window=0, out=None, workspace=None, fwd_kernel=0):
+        scale=None, return_o_f32=False, stream=None, prof=None, window=0, out=None, workspace=None, fwd_kernel=0,
+        sinks=0):
     """O, LSE (and optionally the float32 O before rounding) via fa_fwd.
 
     k, v may have fewer heads than q (grouped-query attention); ``window`` > 0
-    (with ``causal``) restricts query i to keys i - window < j <= i.  ``out``
+    (with ``causal``) restricts query i to keys i - window < j <= i and, with
+    ``sinks`` > 0 (fa_fwd_sinks), the first ``sinks`` keys.  ``out``
     = (o, lse) and ``workspace`` (uint8, fa_fwd_workspace_size bytes) let a
     caller reuse its own buffers instead of allocating on every call.
     ``fwd_kernel`` (head dimension 64): 0 lets the library choose, 1 / 2
@@ -262,19 +271,21 @@ def fwd(q, k, v, *, causal=False, seqlens_k=None, dropout_p=0.0, seed=0, offset=
                     block_mask=block_mask, scale=scale, o_f32=o32, prof=prof, window=window, fwd_kernel=fwd_kernel)
     wsz = lib.fa_fwd_workspace_size(ctypes.byref(p))
     ws = _workspace(wsz, workspace, q.device)
-    st = lib.fa_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(ws), wsz, _stream(stream))
+    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(ws), wsz, _stream(stream))
+    st = lib.fa_fwd_sinks(ctypes.byref(p), int(sinks), *args) if sinks else lib.fa_fwd(ctypes.byref(p), *args)
     if st != FA_OK:
-        raise FAError(st, "fa_fwd")
+        raise FAError(st, "fa_fwd_sinks" if sinks else "fa_fwd")
     fwd.last_workspace = ws
     return (o, lse, o32) if return_o_f32 else (o, lse)
 
 
 def bwd(q, k, v, o, do, lse, *, causal=False, seqlens_k=None, dropout_p=0.0, seed=0, offset=0, block_mask=None,
-        scale=None, stream=None, prof=None, window=0, out=None, workspace=None):
+        scale=None, stream=None, prof=None, window=0, out=None, workspace=None, sinks=0):
     """dQ, dK, dV via fa_bwd (dK, dV have the K/V heads of k, v).  ``out`` =
     (dq, dk, dv) and ``workspace`` (uint8, fa_bwd_workspace_size bytes) let a
     caller reuse its own buffers; the outputs must then share q's / k's
-    (contiguous) layout."""
+    (contiguous) layout.  ``sinks`` as in :func:`fwd` (fa_bwd_sinks; the
+    workspace is then fa_bwd_sinks_workspace_size bytes)."""
     _check(q)
     (q, o, do), (k, v) = _layouts([q, o, do], [k, v])
     if out is not None and (not q.is_contiguous() or not k.is_contiguous()):
@@ -286,12 +297,14 @@ def bwd(q, k, v, o, do, lse, *, causal=False, seqlens_k=None, dropout_p=0.0, see
     dq, dk, dv = _outputs(out, [q, k, v])
     p = make_params(q, k=k, causal=causal, seqlens_k=seqlens_k, dropout_p=dropout_p, seed=seed, offset=offset,
                     block_mask=block_mask, scale=scale, prof=prof, window=window)
-    wsz = lib.fa_bwd_workspace_size(ctypes.byref(p))
+    wsz = lib.fa_bwd_sinks_workspace_size(ctypes.byref(p), int(sinks)) if sinks else \
+        lib.fa_bwd_workspace_size(ctypes.byref(p))
     ws = _workspace(wsz, workspace, q.device)
-    st = lib.fa_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk),
-                    _ptr(dv), _ptr(ws), wsz, _stream(stream))
+    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), wsz,
+            _stream(stream))
+    st = lib.fa_bwd_sinks(ctypes.byref(p), int(sinks), *args) if sinks else lib.fa_bwd(ctypes.byref(p), *args)
     if st != FA_OK:
-        raise FAError(st, "fa_bwd")
+        raise FAError(st, "fa_bwd_sinks" if sinks else "fa_bwd")
     bwd.last_workspace = ws
     return dq, dk, dv
 

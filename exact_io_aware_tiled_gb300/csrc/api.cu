@@ -35,13 +35,42 @@ EncodeTiledFn encode_fn() {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The window and its first keys as the kernels take them (a window or first keys that hide nothing: none of either),
+// and the items of the first key tiles in the backward pass.
+struct SinkPlan {
+  int window = 0, sinks = 0;
+  int tiles = 0, chunks = 0, steps = 0;
+};
+
+SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
+  SinkPlan k;
+  k.window = p->window;
+  if (sinks <= 0 || p->window <= 0) return k;
+  if (p->window >= p->N || sinks >= p->N) {
+    k.window = 0;
+    return k;
+  }
+  k.sinks = sinks;
+  k.tiles = (sinks + kTile - 1) / kTile;
+  const int hkv = p->H_kv == 0 ? p->H : p->H_kv;
+  const long long steps = (long long)((p->N + kTile - 1) / kTile) * (p->H / hkv);
+  // Items of 16 query tiles where there are few first key tiles, and no more than about four for each CTA: their dK and
+  // dV take 64 KB each (d = 128: 128 KB).
+  const long long most = std::max<long long>(1, 4 * 152 / ((long long)p->B * hkv * k.tiles));
+  const long long chunks = std::min((steps + 15) / 16, most);
+  k.steps = (int)((steps + chunks - 1) / chunks);
+  k.chunks = (int)((steps + k.steps - 1) / k.steps);
+  return k;
+}
+
 struct Layout {
-  size_t status = 0, rlist = 0, rcnt = 0, clist = 0, ccnt = 0, lse2 = 0, dvec = 0, dqacc = 0, sched = 0, total = 0;
+  size_t status = 0, rlist = 0, rcnt = 0, clist = 0, ccnt = 0, lse2 = 0, dvec = 0, dqacc = 0, sched = 0, part = 0,
+         total = 0;
   bool sparse = false;
   int nb = 0, nq = 0, npad = 0;
 };
 
-Layout layout(const fa_params* p, bool bwd) {
+Layout layout(const fa_params* p, bool bwd, const SinkPlan& sk = SinkPlan()) {
   Layout L;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -66,6 +95,8 @@ Layout layout(const fa_params* p, bool bwd) {
     L.dvec = take(rows * sizeof(float));
     if (p->dtype != FA_DT_F32) L.dqacc = take((size_t)p->B * p->H * p->N * p->d * sizeof(float));
     L.sched = take(sizeof(int));
+    if (sk.chunks > 1)
+      L.part = take((size_t)p->B * (p->H_kv == 0 ? p->H : p->H_kv) * sk.tiles * sk.chunks * kTile * 2 * p->d * sizeof(float));
   }
   L.total = off;
   return L;
@@ -170,10 +201,11 @@ fa_status map16(CUtensorMap* m, const void* base, const fa_params* p, int heads,
   return make_map(m, base, dt, 2, p->d, 64, p, heads, s, rows);   // 64-column (128-byte) boxes
 }
 
-MaskArgs mask_of(const fa_params* p, const Layout& L, uint8_t* ws) {
+MaskArgs mask_of(const fa_params* p, const Layout& L, uint8_t* ws, const SinkPlan& sk) {
   MaskArgs m{};
   m.causal = p->causal ? 1 : 0;
-  m.window = p->window;
+  m.window = sk.window;
+  m.sinks = sk.sinks;
   m.seqlens_k = p->seqlens_k;
   if (L.sparse) {
     m.row_list = reinterpret_cast<const int16_t*>(ws + L.rlist);
@@ -473,10 +505,17 @@ size_t fa_bwd_workspace_size(const fa_params* p) {
 
 fa_status fa_fwd(const fa_params* p, const void* q, const void* k, const void* v, void* o, float* lse, void* ws,
                  size_t ws_bytes, void* stream) {
+  return fa_fwd_sinks(p, 0, q, k, v, o, lse, ws, ws_bytes, stream);
+}
+
+fa_status fa_fwd_sinks(const fa_params* p, int32_t sinks, const void* q, const void* k, const void* v, void* o,
+                       float* lse, void* ws, size_t ws_bytes, void* stream) {
   fa_status s = check_params(p);
   if (s != FA_OK) return s;
+  if (sinks < 0) return FA_ERR_INVALID_ARG;
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return FA_ERR_MISALIGNED;
+  const SinkPlan sk = sink_plan(p, sinks);
   const Layout L = layout(p, false);
   if (ws == nullptr || ws_bytes < L.total || !aligned16(ws)) return FA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -490,7 +529,7 @@ fa_status fa_fwd(const fa_params* p, const void* q, const void* k, const void* v
   a.nq = L.nq;
   a.npairs = (L.nq + 1) / 2;
   a.scale_log2 = scale_of(p) * 1.4426950408889634f;
-  a.mask = mask_of(p, L, w);
+  a.mask = mask_of(p, L, w, sk);
   a.drop = dropout_of(p);
   a.fwd_kernel = p->fwd_kernel;
   a.lse = lse;
@@ -514,13 +553,28 @@ fa_status fa_fwd(const fa_params* p, const void* q, const void* k, const void* v
 
 fa_status fa_bwd(const fa_params* p, const void* q, const void* k, const void* v, const void* o, const void* dout,
                  const float* lse, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
+  return fa_bwd_sinks(p, 0, q, k, v, o, dout, lse, dq, dk, dv, ws, ws_bytes, stream);
+}
+
+size_t fa_bwd_sinks_workspace_size(const fa_params* p, int32_t sinks) {
+  if (p == nullptr || p->N < 1 || p->B < 1 || p->H < 1) return 256;
+  const int hkv = p->H_kv == 0 ? p->H : p->H_kv;
+  if (hkv < 1 || p->H % hkv != 0) return 256;
+  return layout(p, true, sink_plan(p, sinks)).total;
+}
+
+fa_status fa_bwd_sinks(const fa_params* p, int32_t sinks, const void* q, const void* k, const void* v, const void* o,
+                       const void* dout, const float* lse, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                       void* stream) {
   fa_status s = check_params(p);
   if (s != FA_OK) return s;
+  if (sinks < 0) return FA_ERR_INVALID_ARG;
   if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) || !aligned16(lse) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return FA_ERR_MISALIGNED;
-  const Layout L = layout(p, true);
+  const SinkPlan sk = sink_plan(p, sinks);
+  const Layout L = layout(p, true, sk);
   if (ws == nullptr || ws_bytes < L.total || !aligned16(ws)) return FA_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -535,7 +589,14 @@ fa_status fa_bwd(const fa_params* p, const void* q, const void* k, const void* v
   a.npad = L.npad;
   a.scale = scale_of(p);
   a.scale_log2 = a.scale * 1.4426950408889634f;
-  a.mask = mask_of(p, L, w);
+  a.mask = mask_of(p, L, w, sk);
+  a.sink_tiles = sk.tiles;
+  a.sink_chunks = sk.chunks;
+  a.sink_steps = sk.steps;
+  a.part = reinterpret_cast<float*>(w + L.part);
+  a.dk = dk;
+  a.dv = dv;
+  a.kst = skv;
   a.drop = dropout_of(p);
   a.lse2 = reinterpret_cast<const float*>(w + L.lse2);
   a.dvec = reinterpret_cast<const float*>(w + L.dvec);
@@ -554,8 +615,9 @@ fa_status fa_bwd(const fa_params* p, const void* q, const void* k, const void* v
   if (e != cudaSuccess) return FA_ERR_CUDA;
   if (p->dtype == FA_DT_F32) {
     ProfScope prof(p, st);
-    return cuda_status(launch_bwd_simt((const float*)q, (const float*)k, (const float*)v, (const float*)dout,
-                                       (float*)dq, (float*)dk, (float*)dv, sd, skv, a, st));
+    e = launch_bwd_simt((const float*)q, (const float*)k, (const float*)v, (const float*)dout, (float*)dq, (float*)dk,
+                        (float*)dv, sd, skv, a, st);
+    return cuda_status(e == cudaSuccess ? launch_sink_sum(p->dtype, p->d, a, a.scale, st) : e);
   }
   // d = 64: 128-row query steps; d = 128: 64-row query steps (Q, dO and the
   // float32 dQ accumulator are moved in 64-row boxes)
@@ -566,9 +628,6 @@ fa_status fa_bwd(const fa_params* p, const void* q, const void* k, const void* v
       (s = map16(&mv, v, p, hkv, skv)) != FA_OK || (s = map16(&mdo, dout, p, p->H, sd, qrows)) != FA_OK ||
       (s = make_map(&macc, dqacc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p->d, 32, p, p->H, acc_st, qrows)) != FA_OK)
     return s;
-  a.dk = dk;
-  a.dv = dv;
-  a.kst = skv;
   // 32-byte row pieces (16 columns of 16 bits) can go out as single 32-byte stores
   a.dkv_v8 = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 &&
              skv.n % 16 == 0 && skv.h % 16 == 0 && skv.b % 16 == 0;
@@ -578,6 +637,8 @@ fa_status fa_bwd(const fa_params* p, const void* q, const void* k, const void* v
                     : launch_bwd_tc(p->dtype, mq, mk, mv, mdo, macc, a, st);
     if (e != cudaSuccess) return FA_ERR_CUDA;
   }
+  // bf16: dK comes out scaled
+  if (launch_sink_sum(p->dtype, p->d, a, p->dtype == FA_DT_BF16 ? 1.f : a.scale, st) != cudaSuccess) return FA_ERR_CUDA;
   return cuda_status(launch_dq_convert(p->dtype, dqacc, dq, sd, p->B, p->H, p->N, p->d, st));
 }
 
@@ -670,7 +731,7 @@ fa_status fa_fwd_fp8(const fa_params* p, const fa_fp8_params* f, const void* buf
   a.nq = L.nq;
   a.npairs = (L.nq + 1) / 2;
   a.scale_log2 = scale_of(p) * 1.4426950408889634f;
-  a.mask = mask_of(p, L, w);
+  a.mask = mask_of(p, L, w, sink_plan(p, 0));
   a.drop = dropout_of(p);
   a.lse = lse;
   a.o_f32 = p->o_f32;

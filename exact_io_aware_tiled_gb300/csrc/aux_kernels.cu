@@ -8,9 +8,13 @@
 //   * block_lists: row / column index lists of a block-sparse mask
 //     (agihunt.info, block-sparse paragraph: only nonzero blocks are visited);
 //   * dropout_mask: the keep-mask of the Philox mapping, for tests;
+//   * sink_sum: dK and dV of the first key tiles under a window with sinks, from
+//     the parts that their items left;
 //   * wait_selftest: the bounded-wait path of the attention kernels, run on
 //     mbarriers that nothing ever arrives at.
-#include "common.cuh"
+#include <type_traits>
+
+#include "bwd_items.cuh"
 
 namespace fa {
 namespace {
@@ -200,6 +204,43 @@ cudaError_t launch_dropout_mask(const DropoutArgs& d, int H, int N, int b, int h
   const int threads = 256;
   dropout_mask_kernel<<<(unsigned)((groups + threads - 1) / threads), threads, 0, s>>>(d, H, N, b, h, row0, nrows,
                                                                                          out);
+  return cudaGetLastError();
+}
+
+// Key tile blockIdx.x of the first ones: a thread adds four columns of a key row of
+// dK or dV over the tile's parts, in their order, and rounds once.
+template <typename T>
+__global__ void __launch_bounds__(256) sink_sum_kernel(const BwdArgs a, int d, float kscale) {
+  const int tile = blockIdx.x;
+  const Item it = make_item<kWindowSinks>(a, tile * a.sink_chunks);
+  const int used = min(a.sink_chunks, (it.n * a.group + a.sink_steps - 1) / a.sink_steps);
+  const int per = d >> 2;
+  const int x = blockIdx.y * 256 + threadIdx.x;         // (row, dK or dV, columns / 4)
+  const int c = x % per, y = (x / per) & 1, r = x / (2 * per);
+  const int j = it.jt * kTile + r;
+  if (r >= kTile || j >= a.N) return;
+  const size_t step = (size_t)kTile * 2 * d;
+  const float* src = a.part + (size_t)tile * a.sink_chunks * step + (size_t)(2 * r + y) * d + 4 * c;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < used; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(src + i * step);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  const float f = y ? 1.f : kscale;
+  T* dst = static_cast<T*>(y ? a.dv : a.dk) + (size_t)it.b * a.kst.b + (size_t)it.hk * a.kst.h + (size_t)j * a.kst.n + 4 * c;
+  if constexpr (std::is_same<T, float>::value)
+    *reinterpret_cast<float4*>(dst) = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+  else
+    *reinterpret_cast<uint2*>(dst) = make_uint2(Cvt<T>::pack(s.x * f, s.y * f), Cvt<T>::pack(s.z * f, s.w * f));
+}
+
+cudaError_t launch_sink_sum(int dtype, int d, const BwdArgs& a, float kscale, cudaStream_t s) {
+  if (a.sink_tiles == 0 || a.sink_chunks <= 1) return cudaSuccess;
+  const dim3 grid((unsigned)(a.B * a.H_kv * a.sink_tiles), (unsigned)(kTile * 2 * (d / 4) / 256));
+  if (dtype == FA_DT_F32) sink_sum_kernel<float><<<grid, 256, 0, s>>>(a, d, kscale);
+  else if (dtype == FA_DT_F16) sink_sum_kernel<__half><<<grid, 256, 0, s>>>(a, d, kscale);
+  else sink_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, d, kscale);
   return cudaGetLastError();
 }
 

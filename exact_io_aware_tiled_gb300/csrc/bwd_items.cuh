@@ -17,14 +17,46 @@ struct Item {
   int i0;                 // first query tile (dense)
   int h0;                 // first query head of the group
   const int16_t* list;    // sparse list or nullptr
-  int steps;              // n * g
+  int steps;              // n * g; of a first key tile's item, its part of them
+  int t0;                 // kWindowSinks: the first step's number among the tile's
+  int part;               // where dK and dV go: -1 the tensors, else this place of BwdArgs::part
   __device__ __forceinline__ int qt(int u) const { return list ? (int)list[u] : i0 + u; }
 };
 
+// Work items of the launch.
+template <int kWin> __device__ __forceinline__ int item_count(const BwdArgs& a) {
+  const int heads = a.B * a.H_kv;
+  if constexpr (kWin == kWindowSinks) return heads * (a.sink_tiles * a.sink_chunks + a.nq - a.sink_tiles);
+  return a.nq * heads;
+}
+
+// Under kWindowSinks the items of the first key tiles come first, the longest ones: every query tile sees those, so
+// that one item of them would outlast all others, and each is cut into sink_chunks items of sink_steps steps.
+template <int kWin>
 __device__ __forceinline__ Item make_item(const BwdArgs& a, int u) {
   Item it;
-  const int bk = u / a.nq;
-  it.jt = u - bk * a.nq;
+  int bk, chunk = 0;
+  bool first_keys = false;
+  it.t0 = 0;
+  it.part = -1;
+  if constexpr (kWin == kWindowSinks) {
+    const int first = a.B * a.H_kv * a.sink_tiles * a.sink_chunks;
+    if (u < first) {
+      first_keys = true;
+      if (a.sink_chunks > 1) it.part = u;
+      const int tile = u / a.sink_chunks;
+      chunk = u - tile * a.sink_chunks;
+      bk = tile / a.sink_tiles;
+      it.jt = tile - bk * a.sink_tiles;
+    } else {
+      const int rest = a.nq - a.sink_tiles;
+      bk = (u - first) / rest;
+      it.jt = a.sink_tiles + (u - first) - bk * rest;
+    }
+  } else {
+    bk = u / a.nq;
+    it.jt = u - bk * a.nq;
+  }
   it.b = bk / a.H_kv;
   it.hk = bk - it.b * a.H_kv;
   it.Lk = a.N;
@@ -36,7 +68,7 @@ __device__ __forceinline__ Item make_item(const BwdArgs& a, int u) {
   // last query tile that sees this key tile: under a sliding window of w keys,
   // key j is seen by queries j .. j + w - 1
   int qlast = a.nq - 1;
-  if (a.mask.window > 0) qlast = min(qlast, (it.jt * kTile + kTile - 1 + a.mask.window - 1) / kTile);
+  if (a.mask.window > 0 && !first_keys) qlast = min(qlast, (it.jt * kTile + kTile - 1 + a.mask.window - 1) / kTile);
   if (it.jt * kTile < it.Lk) {
     if (a.mask.col_list != nullptr) {
       const int16_t* list = a.mask.col_list + (size_t)it.jt * a.mask.nb;
@@ -52,6 +84,12 @@ __device__ __forceinline__ Item make_item(const BwdArgs& a, int u) {
     }
   }
   it.steps = it.n * a.group;
+  if constexpr (kWin == kWindowSinks) {
+    if (it.part >= 0) {
+      it.t0 = chunk * a.sink_steps;
+      it.steps = max(0, min(a.sink_steps, it.steps - it.t0));
+    }
+  }
   return it;
 }
 

@@ -104,7 +104,7 @@ static_assert(BwdSmem::kDyn <= 232448, "shared memory over the per-block limit")
 
 constexpr uint32_t kColST = 0, kColDP = 128, kColDK = 256, kColDV = 320, kColDQ = 384, kColPT = 448;
 
-template <typename T, bool kDrop, bool kWin>
+template <typename T, bool kDrop, int kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -120,7 +120,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   BBars* bars = reinterpret_cast<BBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int total = a.nq * a.B * a.H_kv;
+  const int total = item_count<kWin>(a);
   WaitCtl ctl{a.status, &bars->abort};
 
   if (threadIdx.x == 0) {
@@ -242,7 +242,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             ok = u == -1;
             break;
           }
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) {
             // An empty item loads nothing, so the reduce that normally follows
             // a load is not reached; do the reduces the compute threads need to
@@ -258,6 +258,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
           const int vi = nkv;
           ++nkv;
           int qu = 0, hq = it.h0;
+          if (kWin == kWindowSinks) { hq += it.t0 / it.n; qu = it.t0 % it.n; }
           for (int t = 0; t < it.steps && ok; ++t, ++g) {
             const int st = g % NSB;
             if (!(ok = mbar_wait(&bars->q_empty[st], ((uint32_t)(g / NSB) & 1u) ^ 1u, ctl))) break;
@@ -293,7 +294,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bool ok = true;
         int u;
         while (ok && (u = fetch()) >= 0) {
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) continue;
           const int kb = nkv & 1;
           if (!(ok = mbar_wait(&bars->k_full[kb], (uint32_t)(nkv >> 1) & 1u, ctl))) break;
@@ -337,7 +338,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bool ok = true;
         int u;
         while (ok && (u = fetch()) >= 0) {
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) continue;
           for (int t = 0; t < it.steps && ok; ++t, ++g) {
             const int st = g % NSB;
@@ -373,7 +374,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bool ok = true;
         int u;
         while (ok && (u = fetch()) >= 0) {
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) continue;
           const int kb = nkv & 1;
           ++nkv;
@@ -474,6 +475,20 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       dv[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
     };
 
+    // the same, unscaled and in float32, to the part of an item of a first key tile
+    auto store_part = [&](const Item& it, const uint32_t (&kraw)[16], const uint32_t (&vraw)[16]) {
+      float* dst = a.part + (((size_t)it.part * kTile + r) * 2) * 64 + wg * 16;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        reinterpret_cast<float4*>(dst)[c] =
+            make_float4(__uint_as_float(kraw[4 * c]), __uint_as_float(kraw[4 * c + 1]), __uint_as_float(kraw[4 * c + 2]),
+                        __uint_as_float(kraw[4 * c + 3]));
+        reinterpret_cast<float4*>(dst + 64)[c] =
+            make_float4(__uint_as_float(vraw[4 * c]), __uint_as_float(vraw[4 * c + 1]), __uint_as_float(vraw[4 * c + 2]),
+                        __uint_as_float(vraw[4 * c + 3]));
+      }
+    };
+
     // With dropout, the item end instead has warpgroups 0-1 write dK (x tau
     // for fp16) and 2-3 write dV, each warp 16 key rows of its lane quarter
     // (wg & 1 picks which 16).  The 16x256b tensor-memory shape gives each
@@ -555,8 +570,9 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     int nit = 0;      // items with steps (dkv_full phases)
     int u;
     while (ok && (u = fetch()) >= 0) {
-      const Item it = make_item(a, u);
+      const Item it = make_item<kWin>(a, u);
       if (it.steps == 0) {            // no query tile sees this key tile: dK = dV = 0
+        if (kWin == kWindowSinks && it.part >= 0) continue;      // the sum leaves empty parts out
         if constexpr (kDrop) {
           const uint32_t zero[32] = {};
           store_dkv_rows(it, zero, false);
@@ -571,6 +587,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       // qu: tile position within the current query head qh of the item;
       // t: the global step (across items), which every ring and phase follows
       int qu = 0, qh = it.h0;
+      if (kWin == kWindowSinks) { qh += it.t0 / it.n; qu = it.t0 % it.n; }
       for (int tt = 0; tt < it.steps && ok; ++tt, ++t, qu = (qu + 1 == it.n) ? 0 : qu + 1, qh += (qu == 0) ? 1 : 0) {
       const int st = t % NSB;
       const int qi = it.qt(qu);
@@ -581,7 +598,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         // query column c of the tile is hidden from this key under causal iff
         // c < qlo, and outside its sliding window iff c >= qhe
         const int qlo = a.mask.causal ? (j - qi * kTile) : -1;
-        const int qhe = kWin ? (j + a.mask.window - qi * kTile) : kTile;
+        const int qhe = kWin == kWindowSinks && j < a.mask.sinks ? kTile : kWin ? (j + a.mask.window - qi * kTile) : kTile;
         const bool any_mask = !key_ok || qlo > c0 || (kWin && qhe < c0 + 32);
 
         // ---- part 1: P from S^T, in two halves of 16 query columns; the
@@ -720,7 +737,16 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       if (!(ok = warp_wait(&bars->dkv_full, (uint32_t)nit & 1u, ctl))) break;
       ++nit;
       tc_fence_after();
-      if constexpr (kDrop) {
+      if (kWin == kWindowSinks && it.part >= 0) {
+        uint32_t kraw[16], vraw[16];
+        tmem_ld16(tl + kColDK + wg * 16, kraw);
+        tmem_ld16(tl + kColDV + wg * 16, vraw);
+        tmem_wait_ld();
+        reg_fence16(kraw);
+        reg_fence16(vraw);
+        tc_fence_before();
+        store_part(it, kraw, vraw);
+      } else if constexpr (kDrop) {
         uint32_t raw[32];
         tmem_ld16x256b_x8(kv_taddr, raw);
         tmem_wait_ld();
@@ -749,13 +775,14 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   }
 }
 
-template <typename T, bool kDrop, bool kWin>
+template <typename T, bool kDrop, int kWin>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
                      const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
   auto kern = bwd_tc_kernel<T, kDrop, kWin>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem::kDyn);
   if (e != cudaSuccess) return e;
-  const long long total = (long long)a.nq * a.B * a.H_kv;
+  const long long total =
+      (long long)a.B * a.H_kv * (kWin == kWindowSinks ? a.sink_tiles * a.sink_chunks + a.nq - a.sink_tiles : a.nq);
   if (total == 0) return cudaSuccess;
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -765,26 +792,26 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
+                     const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
+  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.mask.sinks > 0 ? 4 : 0);
+  switch (sel) {
+    case 0: return launch_t<T, false, kAllKeys>(q, k, v, dout, dqacc, a, s);
+    case 1: return launch_t<T, true, kAllKeys>(q, k, v, dout, dqacc, a, s);
+    case 2: return launch_t<T, false, kWindow>(q, k, v, dout, dqacc, a, s);
+    case 3: return launch_t<T, true, kWindow>(q, k, v, dout, dqacc, a, s);
+    case 6: return launch_t<T, false, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+    default: return launch_t<T, true, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_bwd_tc(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           const CUtensorMap& dout, const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
-  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0);
-  if (dtype == FA_DT_BF16) {
-    using B = __nv_bfloat16;
-    switch (sel) {
-      case 0: return launch_t<B, false, false>(q, k, v, dout, dqacc, a, s);
-      case 1: return launch_t<B, true, false>(q, k, v, dout, dqacc, a, s);
-      case 2: return launch_t<B, false, true>(q, k, v, dout, dqacc, a, s);
-      default: return launch_t<B, true, true>(q, k, v, dout, dqacc, a, s);
-    }
-  }
-  switch (sel) {
-    case 0: return launch_t<__half, false, false>(q, k, v, dout, dqacc, a, s);
-    case 1: return launch_t<__half, true, false>(q, k, v, dout, dqacc, a, s);
-    case 2: return launch_t<__half, false, true>(q, k, v, dout, dqacc, a, s);
-    default: return launch_t<__half, true, true>(q, k, v, dout, dqacc, a, s);
-  }
+  return dtype == FA_DT_BF16 ? launch_d<__nv_bfloat16>(q, k, v, dout, dqacc, a, s)
+                             : launch_d<__half>(q, k, v, dout, dqacc, a, s);
 }
 
 }  // namespace fa

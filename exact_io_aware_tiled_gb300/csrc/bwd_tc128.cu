@@ -89,7 +89,7 @@ struct StepPos {
   }
 };
 
-template <typename T, bool kDrop, bool kWin>
+template <typename T, bool kDrop, int kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -105,7 +105,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   Bars128* bars = reinterpret_cast<Bars128*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int total = a.nq * a.B * a.H_kv;
+  const int total = item_count<kWin>(a);
   WaitCtl ctl{a.status, &bars->abort};
 
   if (threadIdx.x == 0) {
@@ -217,7 +217,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             ok = u == -1;
             break;
           }
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) {
             // no load follows, so do the reduces the compute threads need to
             // finish their current item (a run of empty items would
@@ -237,6 +237,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           ++nkv;
           StepPos sp;
           sp.hq = it.h0;
+          if (kWin == kWindowSinks) { sp.hq += it.t0 / it.n; sp.qu = it.t0 % it.n; }
           const int nsteps = 2 * it.steps;
           for (int t = 0; t < nsteps && ok; ++t, ++g, sp.next(it)) {
             const int st = g % NQ;
@@ -267,7 +268,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool ok = true;
         int u;
         while (ok && (u = fetch()) >= 0) {
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) continue;
           if (!(ok = mbar_wait(&bars->kv_full, (uint32_t)nkv & 1u, ctl))) break;
           ++nkv;
@@ -305,7 +306,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool ok = true;
         int u;
         while (ok && (u = fetch()) >= 0) {
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) continue;
           const int nsteps = 2 * it.steps;
           for (int t = 0; t < nsteps && ok; ++t, ++g) {
@@ -343,7 +344,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool ok = true;
         int u;
         while (ok && (u = fetch()) >= 0) {
-          const Item it = make_item(a, u);
+          const Item it = make_item<kWin>(a, u);
           if (it.steps == 0) continue;
           const int nsteps = 2 * it.steps;
           for (int t = 0; t < nsteps && ok; ++t, ++g) {
@@ -437,6 +438,20 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       dv[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
     };
 
+    // the same, unscaled and in float32, to the part of an item of a first key tile
+    auto store_part = [&](const Item& it, int half, const uint32_t (&kraw)[16], const uint32_t (&vraw)[16]) {
+      float* dst = a.part + (((size_t)it.part * kTile + r) * 2) * 128 + wg * 32 + half * 16;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        reinterpret_cast<float4*>(dst)[c] =
+            make_float4(__uint_as_float(kraw[4 * c]), __uint_as_float(kraw[4 * c + 1]), __uint_as_float(kraw[4 * c + 2]),
+                        __uint_as_float(kraw[4 * c + 3]));
+        reinterpret_cast<float4*>(dst + 128)[c] =
+            make_float4(__uint_as_float(vraw[4 * c]), __uint_as_float(vraw[4 * c + 1]), __uint_as_float(vraw[4 * c + 2]),
+                        __uint_as_float(vraw[4 * c + 3]));
+      }
+    };
+
     volatile int* item_u = reinterpret_cast<volatile int*>(smem + L::kItem);
     int kc = 0;
     auto fetch = [&]() -> int {
@@ -451,8 +466,9 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int nit = 0;      // items with steps (dkv_full phases)
     int u;
     while (ok && (u = fetch()) >= 0) {
-      const Item it = make_item(a, u);
+      const Item it = make_item<kWin>(a, u);
       if (it.steps == 0) {            // no query tile sees this key tile: dK = dV = 0
+        if (kWin == kWindowSinks && it.part >= 0) continue;      // the sum leaves empty parts out
         const uint32_t zero[16] = {};
         store_dkv(it, 0, zero, zero, false);
         store_dkv(it, 1, zero, zero, false);
@@ -462,6 +478,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool key_ok = j < it.Lk;
       StepPos sp;
       sp.hq = it.h0;
+      if (kWin == kWindowSinks) { sp.hq += it.t0 / it.n; sp.qu = it.t0 % it.n; }
       const int nsteps = 2 * it.steps;
       for (int tt = 0; tt < nsteps && ok; ++tt, ++t, sp.next(it)) {
         const int st = t % NQ;
@@ -472,7 +489,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // query column c of the step is hidden from this key under causal iff
         // c < qlo, and outside its sliding window iff c >= qhe
         const int qlo = a.mask.causal ? (j - q0) : -1;
-        const int qhe = kWin ? (j + a.mask.window - q0) : kQS;
+        const int qhe = kWin == kWindowSinks && j < a.mask.sinks ? kQS : kWin ? (j + a.mask.window - q0) : kQS;
         const bool any_mask = !key_ok || qlo > c0 || (kWin && qhe < c0 + 16);
 
         // ---- part 1: P from S^T (16 query columns)
@@ -608,7 +625,8 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_wait_ld();
         reg_fence16(kraw);
         reg_fence16(vraw);
-        store_dkv(it, half, kraw, vraw, true);
+        if (kWin == kWindowSinks && it.part >= 0) store_part(it, half, kraw, vraw);
+        else store_dkv(it, half, kraw, vraw, true);
       }
       tc_fence_before();
     }
@@ -623,13 +641,14 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-template <typename T, bool kDrop, bool kWin>
+template <typename T, bool kDrop, int kWin>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
                      const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
   auto kern = bwd_tc128_kernel<T, kDrop, kWin>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem128::kDyn);
   if (e != cudaSuccess) return e;
-  const long long total = (long long)a.nq * a.B * a.H_kv;
+  const long long total =
+      (long long)a.B * a.H_kv * (kWin == kWindowSinks ? a.sink_tiles * a.sink_chunks + a.nq - a.sink_tiles : a.nq);
   if (total == 0) return cudaSuccess;
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -639,26 +658,26 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
+                     const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
+  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.mask.sinks > 0 ? 4 : 0);
+  switch (sel) {
+    case 0: return launch_t<T, false, kAllKeys>(q, k, v, dout, dqacc, a, s);
+    case 1: return launch_t<T, true, kAllKeys>(q, k, v, dout, dqacc, a, s);
+    case 2: return launch_t<T, false, kWindow>(q, k, v, dout, dqacc, a, s);
+    case 3: return launch_t<T, true, kWindow>(q, k, v, dout, dqacc, a, s);
+    case 6: return launch_t<T, false, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+    default: return launch_t<T, true, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_bwd_tc128(int dtype, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                              const CUtensorMap& dout, const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
-  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0);
-  if (dtype == FA_DT_BF16) {
-    using B = __nv_bfloat16;
-    switch (sel) {
-      case 0: return launch_t<B, false, false>(q, k, v, dout, dqacc, a, s);
-      case 1: return launch_t<B, true, false>(q, k, v, dout, dqacc, a, s);
-      case 2: return launch_t<B, false, true>(q, k, v, dout, dqacc, a, s);
-      default: return launch_t<B, true, true>(q, k, v, dout, dqacc, a, s);
-    }
-  }
-  switch (sel) {
-    case 0: return launch_t<__half, false, false>(q, k, v, dout, dqacc, a, s);
-    case 1: return launch_t<__half, true, false>(q, k, v, dout, dqacc, a, s);
-    case 2: return launch_t<__half, false, true>(q, k, v, dout, dqacc, a, s);
-    default: return launch_t<__half, true, true>(q, k, v, dout, dqacc, a, s);
-  }
+  return dtype == FA_DT_BF16 ? launch_d<__nv_bfloat16>(q, k, v, dout, dqacc, a, s)
+                             : launch_d<__half>(q, k, v, dout, dqacc, a, s);
 }
 
 }  // namespace fa

@@ -68,6 +68,9 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
+// Key tiles that hold the first `sinks` keys.
+__device__ __forceinline__ int sink_tiles(int sinks) { return (sinks + kTile - 1) / kTile; }
+
 // ----------------------------------------------------------------------------
 // mbarrier
 // ----------------------------------------------------------------------------

@@ -14,6 +14,9 @@ constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 
 constexpr int kTile = 128;       // query rows (and key rows) per tile
 
+// Which keys a query sees of those before it: all, a window's, or a window's and the first ones.
+enum WindowKind { kAllKeys = 0, kWindow = 1, kWindowSinks = 2 };
+
 struct Strides { int64_t b, h, n; };
 
 struct DropoutArgs {
@@ -28,6 +31,7 @@ struct DropoutArgs {
 struct MaskArgs {
   int causal;
   int window;                 // sliding window w (causal only), 0 = none
+  int sinks;                  // first keys that stay visible under a window, < N
   const int32_t* seqlens_k;   // device [B] or nullptr
   const int16_t* row_list;    // [nb][nb]: kept kv tiles of each q tile, ascending
   const int32_t* row_cnt;     // [nb]
@@ -93,6 +97,11 @@ struct BwdArgs {
   int dkv_v8;                 // dk, dv and kst allow 32-byte stores
   int* sched;                 // work-item counter of the persistent kernel (zeroed by the prepass)
   int* status;
+  // mask.sinks > 0: the first sink_tiles key tiles, which every query tile sees, are split into sink_chunks items of
+  // sink_steps query tiles (of all heads of a group); with more than one, their dK and dV go to part and are summed by
+  // launch_sink_sum
+  int sink_tiles, sink_chunks, sink_steps;
+  float* part;                // [B*H_kv][sink_tiles][sink_chunks][128][2][d]
 };
 
 // Differential attention: head pair h of H has score maps 2h and 2h + 1.
@@ -156,6 +165,8 @@ cudaError_t launch_bwd_simt(const float* q, const float* k, const float* v, cons
 cudaError_t launch_bwd_prep(int dtype, const void* o, const void* dout, Strides st, const float* lse,
                             int B, int H, int N, int npad, int d, float* lse2, float* dvec, float* dqacc,
                             int* sched, float dscale, cudaStream_t s);
+// dK, dV of the first key tiles: the sums of their items' parts, in order, dK times kscale.
+cudaError_t launch_sink_sum(int dtype, int d, const BwdArgs& a, float kscale, cudaStream_t s);
 // dq = dqacc (already scaled) cast to dtype with strides.
 cudaError_t launch_dq_convert(int dtype, const float* dqacc, void* dq, Strides st, int B, int H, int N, int d,
                               cudaStream_t s);

@@ -101,8 +101,8 @@ fwd_fp8_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   int Lk = a.N;
   if (a.mask.seqlens_k != nullptr) Lk = max(0, min(a.N, a.mask.seqlens_k[b]));
   Slot sl[2];
-  sl[0] = make_slot(a, 2 * pair, Lk);
-  sl[1] = make_slot(a, 2 * pair + 1, Lk);
+  sl[0] = make_slot<kWin ? kWindow : kAllKeys>(a, 2 * pair, Lk);
+  sl[1] = make_slot<kWin ? kWindow : kAllKeys>(a, 2 * pair + 1, Lk);
   const int smax = max(sl[0].n, sl[1].n);
 
   // The role threads mostly wait on the softmax warps: they sleep while they

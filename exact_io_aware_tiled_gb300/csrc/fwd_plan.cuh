@@ -18,18 +18,26 @@ struct Slot {
   int qt;                 // query tile index
   int n;                  // kv steps
   int lo;                 // first kv tile (dense)
+  int head, gap;          // kWindowSinks: steps at the first keys' tiles, and what lies between those and the window's
   const int16_t* list;    // sparse kv list or nullptr
   // kv tile of step s (lo is nonzero only under a sliding window)
-  template <bool kWin>
-  __device__ __forceinline__ int kv(int s) const { return list ? (int)list[s] : (kWin ? lo + s : s); }
+  template <int kWin>
+  __device__ __forceinline__ int kv(int s) const {
+    if constexpr (kWin == kWindowSinks) {
+      const int t = s < head ? s : s + gap;
+      return list ? (int)list[t] : t;
+    }
+    return list ? (int)list[s] : (kWin ? lo + s : s);
+  }
 };
 
+template <int kWin>
 __device__ __forceinline__ Slot make_slot(const FwdArgs& a, int qt, int Lk) {
   Slot sl;
   sl.qt = qt;
   sl.list = nullptr;
   sl.n = 0;
-  sl.lo = 0;
+  sl.lo = sl.head = sl.gap = 0;
   if (qt >= a.nq) return sl;
   int lim = (Lk + kTile - 1) / kTile;
   if (a.mask.causal) lim = min(lim, qt + 1);
@@ -39,13 +47,29 @@ __device__ __forceinline__ Slot make_slot(const FwdArgs& a, int qt, int Lk) {
     const int16_t* list = a.mask.row_list + (size_t)qt * a.mask.nb;
     const int cnt = a.mask.row_cnt[qt];
     int s0 = 0;
+    if constexpr (kWin == kWindowSinks) {
+      const int tiles = min(sink_tiles(a.mask.sinks), min(sl.lo, lim));
+      while (sl.head < cnt && list[sl.head] < tiles) ++sl.head;
+      s0 = sl.head;
+    }
     while (s0 < cnt && list[s0] < sl.lo) ++s0;
     int n = s0;
     while (n < cnt && list[n] < lim) ++n;
-    sl.list = list + s0;
-    sl.n = n - s0;
+    if constexpr (kWin == kWindowSinks) {
+      sl.list = list;
+      sl.gap = s0 - sl.head;
+      sl.n = sl.head + n - s0;
+    } else {
+      sl.list = list + s0;
+      sl.n = n - s0;
+    }
   } else {
     sl.n = max(0, lim - sl.lo);
+    if constexpr (kWin == kWindowSinks) {
+      sl.head = min(sink_tiles(a.mask.sinks), min(sl.lo, lim));
+      sl.gap = sl.lo - sl.head;
+      sl.n += sl.head;
+    }
   }
   return sl;
 }
@@ -67,7 +91,7 @@ struct StepPlan {
   __device__ __forceinline__ int load_of(int x) const { return x ? use[1] : use[0]; }
 };
 
-template <int NS, bool kWin>
+template <int NS, int kWin>
 __device__ __forceinline__ StepPlan plan_step(const Slot (&sl)[2], int s, int& ld) {
   StepPlan p;
   p.nl = 0;

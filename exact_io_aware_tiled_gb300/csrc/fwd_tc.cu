@@ -73,7 +73,7 @@ struct Bars {
   int abort;
 };
 
-template <typename T, int D, bool kDrop, bool kWin>
+template <typename T, int D, bool kDrop, int kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -103,8 +103,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   int Lk = a.N;
   if (a.mask.seqlens_k != nullptr) Lk = max(0, min(a.N, a.mask.seqlens_k[b]));
   Slot sl[2];
-  sl[0] = make_slot(a, 2 * pair, Lk);
-  sl[1] = make_slot(a, 2 * pair + 1, Lk);
+  sl[0] = make_slot<kWin>(a, 2 * pair, Lk);
+  sl[1] = make_slot<kWin>(a, 2 * pair + 1, Lk);
   const int smax = max(sl[0].n, sl[1].n);
 
   // The role threads mostly wait on the softmax warps: they sleep while they
@@ -302,10 +302,11 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       // mask (only boundary tiles) and row max of the raw scores
       const int jl = jmax - kv * kTile;
       const int jlo = jmin - kv * kTile;
+      const int js = kWin == kWindowSinks ? a.mask.sinks - kv * kTile : 0;   // columns below it stay visible
       if (jl < kTile - 1 || (kWin && jlo > 0)) {
 #pragma unroll
         for (int c = 0; c < 128; ++c)
-          if (c > jl || (kWin && c < jlo)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          if (c > jl || (kWin && c < jlo && (kWin != kWindowSinks || c >= js))) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
       }
       // row max: 8 independent chains of 3-input max, then a short tree
       float m8[8];
@@ -472,7 +473,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   }
 }
 
-template <typename T, int D, bool kDrop, bool kWin>
+template <typename T, int D, bool kDrop, int kWin>
 cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                      const FwdArgs& a, cudaStream_t s) {
   auto kern = fwd_tc_kernel<T, D, kDrop, kWin>;
@@ -487,12 +488,14 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
 template <typename T, int D>
 cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                      const FwdArgs& a, cudaStream_t s) {
-  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0);
+  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.mask.sinks > 0 ? 4 : 0);
   switch (sel) {
-    case 0: return launch_t<T, D, false, false>(q, k, v, o, a, s);
-    case 1: return launch_t<T, D, true, false>(q, k, v, o, a, s);
-    case 2: return launch_t<T, D, false, true>(q, k, v, o, a, s);
-    default: return launch_t<T, D, true, true>(q, k, v, o, a, s);
+    case 0: return launch_t<T, D, false, kAllKeys>(q, k, v, o, a, s);
+    case 1: return launch_t<T, D, true, kAllKeys>(q, k, v, o, a, s);
+    case 2: return launch_t<T, D, false, kWindow>(q, k, v, o, a, s);
+    case 3: return launch_t<T, D, true, kWindow>(q, k, v, o, a, s);
+    case 6: return launch_t<T, D, false, kWindowSinks>(q, k, v, o, a, s);
+    default: return launch_t<T, D, true, kWindowSinks>(q, k, v, o, a, s);
   }
 }
 

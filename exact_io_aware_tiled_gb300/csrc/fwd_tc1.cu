@@ -67,17 +67,25 @@ static_assert(sizeof(Bars1) <= 256, "barrier block overflows its shared-memory s
 // reaches; block-sparse: the tile's row list).
 struct Tile1 {
   int qt, n, lo;
+  int head, gap;          // kWindowSinks: steps at the first keys' tiles, and what lies between those and the window's
   const int16_t* list;
-  template <bool kWin>
-  __device__ __forceinline__ int kv(int s) const { return list ? (int)list[s] : (kWin ? lo + s : s); }
+  template <int kWin>
+  __device__ __forceinline__ int kv(int s) const {
+    if constexpr (kWin == kWindowSinks) {
+      const int t = s < head ? s : s + gap;
+      return list ? (int)list[t] : t;
+    }
+    return list ? (int)list[s] : (kWin ? lo + s : s);
+  }
 };
 
+template <int kWin>
 __device__ __forceinline__ Tile1 make_tile1(const FwdArgs& a, int qt, int Lk) {
   Tile1 t;
   t.qt = qt;
   t.list = nullptr;
   t.n = 0;
-  t.lo = 0;
+  t.lo = t.head = t.gap = 0;
   int lim = (Lk + kTile - 1) / kTile;
   if (a.mask.causal) lim = min(lim, qt + 1);
   if (a.mask.window > 0) t.lo = max(0, qt * kTile - a.mask.window + 1) / kTile;
@@ -85,13 +93,29 @@ __device__ __forceinline__ Tile1 make_tile1(const FwdArgs& a, int qt, int Lk) {
     const int16_t* list = a.mask.row_list + (size_t)qt * a.mask.nb;
     const int cnt = a.mask.row_cnt[qt];
     int s0 = 0;
+    if constexpr (kWin == kWindowSinks) {
+      const int tiles = min(sink_tiles(a.mask.sinks), min(t.lo, lim));
+      while (t.head < cnt && list[t.head] < tiles) ++t.head;
+      s0 = t.head;
+    }
     while (s0 < cnt && list[s0] < t.lo) ++s0;
     int n = s0;
     while (n < cnt && list[n] < lim) ++n;
-    t.list = list + s0;
-    t.n = n - s0;
+    if constexpr (kWin == kWindowSinks) {
+      t.list = list;
+      t.gap = s0 - t.head;
+      t.n = t.head + n - s0;
+    } else {
+      t.list = list + s0;
+      t.n = n - s0;
+    }
   } else {
     t.n = max(0, lim - t.lo);
+    if constexpr (kWin == kWindowSinks) {
+      t.head = min(sink_tiles(a.mask.sinks), min(t.lo, lim));
+      t.gap = t.lo - t.head;
+      t.n += t.head;
+    }
   }
   return t;
 }
@@ -101,7 +125,7 @@ __device__ __forceinline__ bool warp_wait1(uint64_t* bar, uint32_t parity, const
   return __all_sync(0xffffffffu, ok);
 }
 
-template <typename T, bool kDrop, bool kWin>
+template <typename T, bool kDrop, int kWin>
 __global__ void __launch_bounds__(kThreads1, 2)
 fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -131,7 +155,7 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   const int hk = h / a.group;
   int Lk = a.N;
   if (a.mask.seqlens_k != nullptr) Lk = max(0, min(a.N, a.mask.seqlens_k[b]));
-  const Tile1 tile = make_tile1(a, qt, Lk);
+  const Tile1 tile = make_tile1<kWin>(a, qt, Lk);
   const int n = tile.n;
 
   // The role threads mostly wait on the softmax warps: they sleep while they
@@ -298,10 +322,11 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // mask (only boundary tiles) and row max of the raw scores
       const int jl = jmax - kv * kTile;
       const int jlo = jmin - kv * kTile;
+      const int js = kWin == kWindowSinks ? a.mask.sinks - kv * kTile : 0;   // columns below it stay visible
       if (jl < kTile - 1 || (kWin && jlo > 0)) {
 #pragma unroll
         for (int c = 0; c < 128; ++c)
-          if (c > jl || (kWin && c < jlo)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          if (c > jl || (kWin && c < jlo && (kWin != kWindowSinks || c >= js))) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
       }
       // row max: 8 independent chains of 3-input max, then a short tree
       float m8[8];
@@ -462,7 +487,7 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   }
 }
 
-template <typename T, bool kDrop, bool kWin>
+template <typename T, bool kDrop, int kWin>
 cudaError_t launch_t1(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                       const FwdArgs& a, cudaStream_t s) {
   auto kern = fwd_tc1_kernel<T, kDrop, kWin>;
@@ -477,12 +502,14 @@ cudaError_t launch_t1(const CUtensorMap& q, const CUtensorMap& k, const CUtensor
 template <typename T>
 cudaError_t launch_d1(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                       const FwdArgs& a, cudaStream_t s) {
-  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0);
+  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.mask.sinks > 0 ? 4 : 0);
   switch (sel) {
-    case 0: return launch_t1<T, false, false>(q, k, v, o, a, s);
-    case 1: return launch_t1<T, true, false>(q, k, v, o, a, s);
-    case 2: return launch_t1<T, false, true>(q, k, v, o, a, s);
-    default: return launch_t1<T, true, true>(q, k, v, o, a, s);
+    case 0: return launch_t1<T, false, kAllKeys>(q, k, v, o, a, s);
+    case 1: return launch_t1<T, true, kAllKeys>(q, k, v, o, a, s);
+    case 2: return launch_t1<T, false, kWindow>(q, k, v, o, a, s);
+    case 3: return launch_t1<T, true, kWindow>(q, k, v, o, a, s);
+    case 6: return launch_t1<T, false, kWindowSinks>(q, k, v, o, a, s);
+    default: return launch_t1<T, true, kWindowSinks>(q, k, v, o, a, s);
   }
 }
 

@@ -28,37 +28,44 @@ __device__ __forceinline__ int kv_limit_tiles(int Lk) { return (Lk + kTile - 1) 
 // tile at position s of that list.
 struct TileList {
   int n;
-  int first;
+  int head, gap;          // steps at the first keys' tiles, and what lies between those and the others
   const int16_t* list;
-  __device__ __forceinline__ int at(int s) const { return list ? (int)list[s] : first + s; }
+  __device__ __forceinline__ int at(int s) const {
+    const int t = s < head ? s : s + gap;
+    return list ? (int)list[t] : t;
+  }
 };
 
 __device__ __forceinline__ TileList fwd_list(const MaskArgs& m, int qt, int Lk) {
-  TileList tl{0, 0, nullptr};
+  TileList tl{0, 0, 0, nullptr};
   int lim = kv_limit_tiles(Lk);
   if (m.causal) lim = min(lim, qt + 1);
   const int lo = m.window > 0 ? max(0, qt * kTile - m.window + 1) / kTile : 0;
+  const int tiles = min(sink_tiles(m.sinks), min(lo, lim));
   if (m.row_list) {
     const int16_t* list = m.row_list + (size_t)qt * m.nb;
     const int cnt = m.row_cnt[qt];
-    int s0 = 0;
+    while (tl.head < cnt && list[tl.head] < tiles) ++tl.head;
+    int s0 = tl.head;
     while (s0 < cnt && list[s0] < lo) ++s0;
     int n = s0;
     while (n < cnt && list[n] < lim) ++n;
-    tl.list = list + s0;
-    tl.n = n - s0;
+    tl.list = list;
+    tl.gap = s0 - tl.head;
+    tl.n = tl.head + n - s0;
   } else {
-    tl.first = lo;
-    tl.n = max(0, lim - lo);
+    tl.head = tiles;
+    tl.gap = lo - tiles;
+    tl.n = tiles + max(0, lim - lo);
   }
   return tl;
 }
 
 __device__ __forceinline__ TileList bwd_list(const MaskArgs& m, int jt, int nq, int Lk) {
-  TileList tl{0, 0, nullptr};
+  TileList tl{0, 0, 0, nullptr};
   if (jt * kTile >= Lk) return tl;
   int qlast = nq - 1;   // key j is seen by queries j .. j + w - 1 under a window
-  if (m.window > 0) qlast = min(qlast, (jt * kTile + kTile - 1 + m.window - 1) / kTile);
+  if (m.window > 0 && jt >= sink_tiles(m.sinks)) qlast = min(qlast, (jt * kTile + kTile - 1 + m.window - 1) / kTile);
   if (m.col_list) {
     const int16_t* list = m.col_list + (size_t)jt * m.nb;
     const int cnt = m.col_cnt[jt];
@@ -66,11 +73,12 @@ __device__ __forceinline__ TileList bwd_list(const MaskArgs& m, int jt, int nq, 
     if (m.causal) while (s0 < cnt && list[s0] < jt) ++s0;
     int e = s0;
     while (e < cnt && list[e] <= qlast) ++e;
-    tl.list = list + s0;
+    tl.list = list;
+    tl.gap = s0;
     tl.n = e - s0;
   } else {
-    tl.first = m.causal ? jt : 0;
-    tl.n = max(0, qlast - tl.first + 1);
+    tl.gap = m.causal ? jt : 0;
+    tl.n = max(0, qlast - tl.gap + 1);
   }
   return tl;
 }
@@ -119,7 +127,7 @@ fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
         float d = 0.f;
 #pragma unroll
         for (int c = 0; c < kD; ++c) d = fmaf(qr[c], Ks[jj][c], d);
-        sc[jj] = (j0 + jj <= jmax && j0 + jj >= jmin) ? d * sl2 : -INFINITY;
+        sc[jj] = (j0 + jj <= jmax && (j0 + jj >= jmin || j0 + jj < a.mask.sinks)) ? d * sl2 : -INFINITY;
         mx = fmaxf(mx, sc[jj]);
       }
       const float mn = fmaxf(m, mx);
@@ -154,7 +162,8 @@ fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
   }
 }
 
-// dK, dV: one thread per key row.
+// dK, dV: one thread per key row.  Blocks past the nq key tiles take the parts of
+// the first ones (BwdArgs::part).
 __global__ void __launch_bounds__(kRows)
 bwd_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                      const float* __restrict__ dout, float* __restrict__ dk, float* __restrict__ dv, Strides st,
@@ -164,8 +173,15 @@ bwd_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, c
   __shared__ float Qs[kSub][kD];
   __shared__ float Ds[kSub][kD];
   __shared__ float Ls[kSub], Dv[kSub];
-  const int jt = blockIdx.x;
+  int jt = blockIdx.x, chunk = 0;
   const int bk = blockIdx.y;                  // (b, K/V head)
+  const bool cut = a.sink_tiles > 0 && a.sink_chunks > 1;
+  if (jt >= a.nq) {
+    chunk = (jt - a.nq) % a.sink_chunks;
+    jt = (jt - a.nq) / a.sink_chunks;
+  } else if (cut && jt < a.sink_tiles) {
+    return;
+  }
   const int b = bk / a.H_kv, hk = bk % a.H_kv;
   const int r = threadIdx.x;
   const int j = jt * kRows + r;
@@ -182,7 +198,9 @@ bwd_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, c
   const bool key_ok = j < Lk;
   const TileList tl = bwd_list(a.mask, jt, a.nq, Lk);
   const float rp = a.drop.enabled ? a.drop.rp : 1.f;
-  for (int s = 0; s < tl.n * a.group; ++s) {
+  const bool part = cut && jt < a.sink_tiles;
+  const int send = part ? min(tl.n * a.group, (chunk + 1) * a.sink_steps) : tl.n * a.group;
+  for (int s = part ? chunk * a.sink_steps : 0; s < send; ++s) {
     const int qti = tl.at(s % tl.n);
     const int h = hk * a.group + s / tl.n;     // query head of this step
     const int bh = b * a.H + h;
@@ -204,7 +222,7 @@ bwd_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, c
       for (int ii = 0; ii < kSub; ++ii) {
         const int i = i0 + ii;
         if (a.mask.causal && j > i) continue;
-        if (a.mask.window > 0 && i >= j + a.mask.window) continue;
+        if (a.mask.window > 0 && j >= a.mask.sinks && i >= j + a.mask.window) continue;
         float sdot = 0.f, ddot = 0.f;
 #pragma unroll
         for (int c = 0; c < kD; ++c) {
@@ -225,7 +243,14 @@ bwd_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, c
       }
     }
   }
-  if (j < a.N) {
+  if (part) {
+    float* dst = a.part + ((((size_t)bk * a.sink_tiles + jt) * a.sink_chunks + chunk) * kTile + r) * 2 * kD;
+#pragma unroll
+    for (int c = 0; c < kD; ++c) {
+      dst[c] = gk[c];
+      dst[kD + c] = gv[c];
+    }
+  } else if (j < a.N) {
 #pragma unroll
     for (int c = 0; c < kD; ++c) {
       dk[kbase + (size_t)j * kst.n + c] = gk[c] * a.scale;
@@ -285,7 +310,7 @@ bwd_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, con
           keep |= dropout_keep8((uint32_t)((j0 >> 3) + gg), row_g, a.drop) << (8 * gg);
       }
       for (int jj = 0; jj < kSub; ++jj) {
-        if (j0 + jj > jmax || j0 + jj < jmin) continue;
+        if (j0 + jj > jmax || (j0 + jj < jmin && j0 + jj >= a.mask.sinks)) continue;
         float sdot = 0.f, ddot = 0.f;
 #pragma unroll
         for (int c = 0; c < kD; ++c) {
@@ -317,7 +342,8 @@ cudaError_t launch_fwd_simt(const float* q, const float* k, const float* v, floa
 
 cudaError_t launch_bwd_simt(const float* q, const float* k, const float* v, const float* dout, float* dq,
                             float* dk, float* dv, Strides st, Strides kst, const BwdArgs& a, cudaStream_t s) {
-  dim3 grid(a.nq, a.B * a.H), kgrid(a.nq, a.B * a.H_kv);
+  const int cut = a.sink_tiles > 0 && a.sink_chunks > 1 ? a.sink_tiles * a.sink_chunks : 0;
+  dim3 grid(a.nq, a.B * a.H), kgrid(a.nq + cut, a.B * a.H_kv);
   constexpr int dyn = 2 * kRows * (kD + 1) * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(bwd_dkdv_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e == cudaSuccess)

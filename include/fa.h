@@ -173,6 +173,25 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
                  void *stream);
 
 /* ---------------------------------------------------------------------------
+ * fa_fwd_sinks / fa_bwd_sinks -- fa_fwd and fa_bwd with a sliding window whose first
+ * `sinks` keys stay visible (ABI 1.5): with p->window = w > 0 (and causal),
+ * key j is visible to query i iff j <= i and (i - w < j or j < sinks), AND
+ * padding AND block mask.  Arguments, dtypes, head dimensions, grouped heads,
+ * dropout and workspaces are those of fa_fwd and fa_bwd; sinks = 0 is the same
+ * call, and without a window sinks change nothing.  Whole K/V tiles between the
+ * first keys and the window are skipped, in both directions.
+ * Every query tile sees the first key tiles.  The backward pass cuts their
+ * items along the queries; the pieces' dK and dV lie in float32 in the workspace
+ * (fa_bwd_sinks_workspace_size bytes) and are summed in a fixed order.
+ * ------------------------------------------------------------------------- */
+fa_status fa_fwd_sinks(const fa_params *p, int32_t sinks, const void *q, const void *k, const void *v, void *o,
+                       float *lse, void *ws, size_t ws_bytes, void *stream);
+size_t fa_bwd_sinks_workspace_size(const fa_params *p, int32_t sinks);
+fa_status fa_bwd_sinks(const fa_params *p, int32_t sinks, const void *q, const void *k, const void *v, const void *o,
+                       const void *dout, const float *lse, void *dq, void *dk, void *dv, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/* ---------------------------------------------------------------------------
  * fa_bwd_noalloc -- fa_bwd for callers that cannot allocate device memory.
  * The FlashAttention pages have no counterpart; this is an interface
  * convenience around the same backward kernels.
@@ -619,8 +638,8 @@ const char *fa_status_string(fa_status s);
 /* Library ABI version (major * 100 + minor): 101 adds H_kv, kv_stride_*
  * and window to fa_params; 102 adds the FP8 forward; 103 adds fwd_kernel,
  * fa_noalloc_check_status and fa_noalloc_scratch; 104 adds fa_rope,
- * fa_diff_* and fa_prefix_*; 105 adds fa_norm_rope* and
- * fa_cache8_*. */
+ * fa_diff_* and fa_prefix_*; 105 adds fa_norm_rope*,
+ * fa_cache8_*, fa_fwd_sinks and fa_bwd_sinks. */
 int32_t fa_version(void);
 
 #ifdef __cplusplus
