@@ -445,6 +445,9 @@ fa_status check_cache8(const fa_cache8_params* in, fa_cache8_params& p, Cache8St
   if ((double)p.B * p.H * p.T >= (double)(1 << 26) || (long long)p.width * p.page > (1 << 28) ||
       (long long)p.pages * p.H_kv >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;
+  // 32-bit units of one sequence: 32 keys of one K/V head and 64 query rows
+  if (!rows && (double)(p.width * p.page / 32 + 1) * p.H_kv * ((p.H / p.H_kv * (long long)p.T + 15) / 16) >= 2147483648.0)
+    return FA_ERR_UNSUPPORTED;
   s.kc = {p.kc_stride_p, p.kc_stride_h, p.kc_stride_n};
   s.vc = {p.vc_stride_p, p.vc_stride_h, p.vc_stride_n};
   fa_status e;

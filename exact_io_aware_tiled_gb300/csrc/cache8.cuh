@@ -21,7 +21,7 @@ struct Cache8Rows {
 
 struct Cache8Args {
   int B, H, Hkv, T, G;         // G = H / Hkv
-  int r, tile, tiles;          // rows of a K/V head (G T), rows of a tile (16, 32 or 64), tiles
+  int r, tile, tiles;          // rows of a K/V head (G T), rows of a tile (8, 16, 32 or 64), tiles
   int page, lg, pages, width, cap;   // cap = width * page
   int window, sinks;
   const void* q;
@@ -35,7 +35,7 @@ struct Cache8Args {
   const float* vs;             // [pages][Hkv]
   float scale_log2;            // tau * log2(e)
   int* status;
-  int* count;                  // [kCMax]: pieces of the rows that start in a CTA and end in another, cleared
+  int* count;                  // [3 kCMax], cleared: pieces left of a group, and groups joined, of rows that were cut
   float2* stat;                // [2 kCMax][tile]: maximum (log2), sum
   float* part;                 // [2 kCMax][tile][D] unnormalised O
   int* pre;                    // [B + 1] units before each sequence, where the kernel does not sum them itself

@@ -46,6 +46,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(nthreads) : "memory");
 }
 
+// Arrives at named barrier `id` without waiting (its memory accesses before are visible to those that wait).
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(nthreads) : "memory");
+}
+
 // Per-warpgroup register budgets (setmaxnreg): every warp of a warpgroup must
 // execute the same call; the launch budget must cover the sum.
 template <uint32_t N> __device__ __forceinline__ void regs_inc() {

@@ -112,7 +112,7 @@ def test_strides_pointers_and_workspace():
     size = _ops._fn("fa_cache8_workspace_size", ctypes.c_void_p, restype=ctypes.c_size_t)
     p = _params()
     need = size(ctypes.addressof(p))
-    assert size(None) == 256 and need >= 256 + 2 * 456 * 16 * (64 * 4 + 8)
+    assert size(None) == 256 and need >= 256 + 2 * 456 * 8 * (64 * 4 + 8)
     assert _fwd(p, ws=need - 1) == 4 and _fwd(p, ws_ptr=None) == 4 and _fwd(p, ws_ptr=(1 << 21) + 8) == 4
     big = _params(B=1000)
     assert size(ctypes.addressof(big)) >= need + 4004
@@ -155,25 +155,31 @@ def test_units_cover_the_visible_keys_once(KS):
 
 
 def test_pieces_of_the_line():
-    # every unit has one owner; a row's pieces are neighbours; a CTA begins one cut row at most
+    # the kernel's cut of the line (kItemUnits in front of every row set): each unit has one owner, a row set's pieces
+    # are neighbours, and a CTA begins one cut row set at most
+    cost = 12
     rng = random.Random(2)
     for _ in range(300):
         segs = [rng.choice([1, 2, rng.randint(1, 300)]) for _ in range(rng.randint(1, 20))]
-        X = sum(segs)
+        X = sum(n + cost for n in segs)
         C = rng.randint(1, min(456, X))
-        begin = [X * c // C for c in range(C + 1)]
-        owner = lambda x: ((x + 1) * C - 1) // X  # noqa: E731
+        each, more = divmod(X, C)
+        begin = [each * c + min(c, more) for c in range(C + 1)]
+        wide = (each + 1) * more
+        owner = lambda x: x // (each + 1) if x < wide else more + (x - wide) // each  # noqa: E731
+        assert begin[C] == X
         for x in range(X):
             assert begin[owner(x)] <= x < begin[owner(x) + 1]
-        assert all(a < b for a, b in zip(begin, begin[1:]))
-        at, cut, slots = 0, [], []
+        at, cut, slots = cost, [], []
         for n in segs:
             c0, c1 = owner(at), owner(at + n - 1)
             if c1 > c0:
                 cut.append(c0)
                 slots += [2 * c + (1 if at >= begin[c] else 0) for c in range(c0, c1 + 1)]
                 assert [2 * c + (1 if c == c0 else 0) for c in range(c0, c1 + 1)] == slots[-(c1 - c0 + 1):]
-            at += n
+            # whole, as the one CTA that has the first unit sees it
+            assert (c1 == c0) == (at >= begin[c0] and at + n <= begin[c0 + 1])
+            at += n + cost
         assert len(set(cut)) == len(cut) and len(set(slots)) == len(slots)
 
 
