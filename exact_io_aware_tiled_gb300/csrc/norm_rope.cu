@@ -29,8 +29,18 @@ constexpr int kNThreads = 128;
 // Where the pairs of a thread's columns lie.
 enum Pairs {
   kHalves = 0,   // (i, i + rot/2), rot/2 a multiple of 8: a thread owns 8 columns of each half, or 8 that do not turn
-  kAdjacent,     // (2i, 2i + 1): 8 columns
+  kAdjacent,     // (2i, 2i + 1): 16 columns
   kShared        // (i, i + rot/2), any rot: 8 columns, the partners through shared memory
+};
+
+// The backward kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.
+__host__ __device__ constexpr int bwd_ctas_of(int pairs) { return pairs == kShared ? 4 : 3; }
+template <typename T, int kPairs> struct BwdCfg {
+  static constexpr int kPer = 16 / (int)sizeof(T);                       // elements of a 16-byte piece
+  static constexpr int kPieces = 2 * (kPairs == kShared ? 8 : 16) / kPer; // of a row of x and dy in a thread
+  static constexpr int kStages = kPieces == 8 ? 3 : kPieces == 4 ? 6 : 8;
+  static constexpr int kBytes = kStages * kPieces * kNThreads * 16;
+  static_assert(kBytes >= kNThreads * 16 * (int)sizeof(float), "room for the sums at the end");
 };
 
 struct NormArgs {
@@ -41,14 +51,14 @@ struct NormArgs {
   Strides xs[2], ds[2], ys[2];
   int heads[2];
   int N, d, rot, units, lg;   // units: threads that own columns of a row; 2^lg lanes a row
-  int hp;                  // heads per blockIdx.y (forward), per work item (backward)
+  int hp;                  // heads per blockIdx.y (forward)
   uint32_t tokens;         // B * N
   const void* pos;
   int pos64;
   int64_t pos_b, pos_n, start;
   const double* inv_freq;
   float mscale, eps, inv_d;
-  // backward: CTAs of q, then of k; each walks over items of (tokens, heads) and leaves one row of sums
+  // backward: CTAs of q, then of k; each leaves one row of sums
   int ctas[2];
   float* part;             // [ctas[0] + ctas[1]][d]
   float* dw[2];            // [d] or nullptr
@@ -62,6 +72,10 @@ template <> struct V8<float> {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
+  __device__ __forceinline__ void pieces(const uint8_t* p, int step) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + step);
+  }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
@@ -73,6 +87,7 @@ template <> struct V8<float> {
 template <typename T> struct V8 {
   uint4 a;
   __device__ __forceinline__ void load(const T* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void pieces(const uint8_t* p, int) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float* f) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -88,34 +103,38 @@ template <typename T> struct V8 {
 };
 
 // The sines, cosines and weights of one thread's columns.  Columns of the
-// thread: c0 .. c0 + 7 and, in kHalves where they turn, c1 .. c1 + 7.
+// thread: c0 .. c0 + 7 and, in kHalves where they turn and in kAdjacent where the row
+// has them, c1 .. c1 + 7 half a row further (the lanes of a load lie side by side).
 template <int kPairs> struct Turn {
-  static constexpr int NC = kPairs == kHalves ? 16 : 8;
-  static constexpr int NP = kPairs == kAdjacent ? 4 : 8;
+  static constexpr int NC = kPairs == kShared ? 8 : 16;
+  static constexpr int NP = 8;
   bool live, rotates, two;         // owns columns; some of them turn; owns the second eight
   int c0, c1, half;
   float cs[NP], sn[NP], w[NC];
 
-  __device__ __forceinline__ void place(int u, int rot, int units) {
+  __device__ __forceinline__ void place(int u, int rot, int units, int d) {
     half = rot >> 1;
     live = u < units;
     if constexpr (kPairs == kHalves) {
       const int nrot = half >> 3;
       two = rotates = u < nrot;
       c0 = rotates ? u * 8 : rot + (u - nrot) * 8;
+      c1 = two ? c0 + half : c0;
     } else {
-      two = false;
       c0 = u * 8;
+      c1 = (units + u) * 8;
+      two = NC > 8 && c1 < d;
+      if (!two) c1 = c0;
       rotates = c0 < rot;
     }
-    c1 = two ? c0 + half : c0;
     if (!live) rotates = two = false;
   }
+  __device__ __forceinline__ int pair_of(int e) const { return e < 4 ? (c0 >> 1) + e : two ? (c1 >> 1) + e - 4 : half; }   // kAdjacent
   __device__ __forceinline__ void angles(long long p, const unsigned long long* sF, const float* sM, float sgn) {
     if (!rotates) return;
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
-      int i = kPairs == kAdjacent ? (c0 >> 1) + e : c0 + e;
+      int i = kPairs == kAdjacent ? pair_of(e) : c0 + e;
       if (kPairs == kShared && i >= half) i -= half;
       cs[e] = 1.f;
       sn[e] = 0.f;
@@ -150,7 +169,7 @@ template <int kPairs> struct Turn {
 #pragma unroll
       for (int e = 0; e < NP; ++e) {
         const int a = kPairs == kHalves ? e : 2 * e, b = kPairs == kHalves ? 8 + e : 2 * e + 1;
-        if (kPairs == kAdjacent && (c0 >> 1) + e >= half) continue;
+        if (kPairs == kAdjacent && pair_of(e) >= half) continue;
         const float x0 = v[a], x1 = v[b];
         v[a] = x0 * cs[e] - x1 * sn[e];
         v[b] = x1 * cs[e] + x0 * sn[e];
@@ -158,6 +177,14 @@ template <int kPairs> struct Turn {
     }
   }
 };
+
+// kL1: through L1, where a thread's two pieces share a 32-byte sector
+template <bool kL1> __device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
+  if constexpr (kL1) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(smem), "l"(g) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem), "l"(g) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // sum over the 2^lg lanes of a row (every lane of the warp takes part)
 __device__ __forceinline__ float row_sum(float s, int lg) {
@@ -192,7 +219,7 @@ __global__ void __launch_bounds__(kNThreads) norm_rope_kernel(const NormArgs a) 
   const uint32_t t = blockIdx.x * kNThreads + threadIdx.x;
   const uint32_t token = t >> a.lg;
   R r;
-  r.place((int)(t & ((1u << a.lg) - 1)), a.rot, a.units);
+  r.place((int)(t & ((1u << a.lg) - 1)), a.rot, a.units, a.d);
   if (token >= a.tokens) r.live = r.rotates = r.two = false;
   const uint32_t tk = min(token, a.tokens - 1);
   const uint32_t b = tk / (uint32_t)a.N, n = tk - b * (uint32_t)a.N;
@@ -236,93 +263,146 @@ __global__ void __launch_bounds__(kNThreads) norm_rope_kernel(const NormArgs a) 
   }
 }
 
-// Backward.  CTA c of q (of k) takes work items c, c + ctas, ...: kNThreads >> lg
-// tokens and hp heads each.
+// Backward.  The rows of q (of k), tile by tile of kNThreads >> lg tokens and in a
+// tile head by head, are shared out evenly over its CTAs.  A thread copies its rows
+// ahead into shared memory that it has to itself (no barriers), so that what is in
+// flight takes no registers: 155 us with two rows in registers for GPT-2-medium q and
+// k, 135 so.
 template <typename T, int kPairs>
-__global__ void __launch_bounds__(kNThreads) norm_rope_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNThreads, bwd_ctas_of(kPairs)) norm_rope_bwd_kernel(const NormArgs a) {
   using R = Turn<kPairs>;
-  constexpr int HB = sizeof(T) == 4 ? 1 : 2;
+  using C = BwdCfg<T, kPairs>;
   __shared__ unsigned long long sF[128];
   __shared__ float sM[128];
   __shared__ float rows[kPairs == kShared ? kNThreads * 8 : 8];
-  __shared__ float sums[kNThreads * R::NC];
+  extern __shared__ __align__(16) uint8_t ahead[];   // [kStages][kPieces][kNThreads] 16-byte pieces
   load_turns(a, sF, sM);
   const int v = (int)blockIdx.x < a.ctas[0] ? 0 : 1;
   const int c = (int)blockIdx.x - (v ? a.ctas[0] : 0);
-  const int per = kNThreads >> a.lg;                 // tokens of an item
-  const uint32_t tiles = (a.tokens + per - 1) / per;
-  const int splits = (a.heads[v] + a.hp - 1) / a.hp;
+  const int per = kNThreads >> a.lg, heads = a.heads[v];      // tokens of a tile
+  const unsigned long long total = (unsigned long long)((a.tokens + per - 1) / per) * heads;
+  const unsigned long long from = total * c / a.ctas[v];
+  const int count = (int)(total * (c + 1) / a.ctas[v] - from);   // rows of this CTA's groups
+  const uint32_t tile0 = (uint32_t)(from / heads);
+  const int head0 = (int)(from - (unsigned long long)tile0 * heads);
   R r;
-  r.place((int)threadIdx.x & ((1 << a.lg) - 1), a.rot, a.units);
+  r.place((int)threadIdx.x & ((1 << a.lg) - 1), a.rot, a.units, a.d);
   r.weights(a.w[v]);
   const R all = r;
   float* row = rows + (kPairs == kShared ? (threadIdx.x >> a.lg << a.lg) * 8 : 0);
   const Strides xs = a.xs[v], ds = a.ds[v], ys = a.ys[v];
+  struct Token { uint32_t b, n; bool there; };
+  auto token_of = [&](uint32_t tile) -> Token {
+    const uint32_t token = tile * per + (threadIdx.x >> a.lg), tk = min(token, a.tokens - 1);
+    Token t;
+    t.b = tk / (uint32_t)a.N;
+    t.n = tk - t.b * (uint32_t)a.N;
+    t.there = token < a.tokens;
+    return t;
+  };
+  // ---- the copies' place in the sequence
+  const uint32_t slot0 = smem_u32(ahead) + threadIdx.x * 16;
+  uint32_t ltile = tile0;
+  int lh = head0, ls = 0, left = count;
+  bool lt = false;
+  const T *lx = nullptr, *lg = nullptr;
+  auto enter = [&]() {
+    const Token t = token_of(ltile);
+    lt = t.there;
+    lx = static_cast<const T*>(a.x[v]) + (int64_t)t.b * xs.b + (int64_t)lh * xs.h + (int64_t)t.n * xs.n;
+    lg = static_cast<const T*>(a.dy[v]) + (int64_t)t.b * ds.b + (int64_t)lh * ds.h + (int64_t)t.n * ds.n;
+  };
+  auto copy = [&]() {                                // the next row, into stage ls
+    if (left > 0) {
+      if (lt) {
+        const uint32_t at = slot0 + ls * (C::kPieces * kNThreads * 16);
+#pragma unroll
+        for (int i = 0; i < C::kPieces / 2; ++i) {
+          // pieces of x, then of dy: of the first eight columns, then of the second
+          const int e = i * C::kPer, col = (e < 8 ? all.c0 + e : all.c1 + e - 8);
+          if (e < 8 ? all.live : all.two) {
+            cp_async16<sizeof(T) == 4>(at + i * (kNThreads * 16), lx + col);
+            cp_async16<sizeof(T) == 4>(at + (C::kPieces / 2 + i) * (kNThreads * 16), lg + col);
+          }
+        }
+      }
+      lx += xs.h;
+      lg += ds.h;
+      if (++lh == heads) {
+        lh = 0;
+        ++ltile;
+        enter();
+      }
+      --left;
+    }
+    cp_async_commit();
+    ls = ls + 1 == C::kStages ? 0 : ls + 1;
+  };
+  enter();
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) copy();
+  int st = 0;
   float acc[R::NC] = {};
-  for (unsigned long long u = c; u < (unsigned long long)tiles * splits; u += a.ctas[v]) {
-    const uint32_t tile = (uint32_t)(u % tiles);
-    const int h0 = (int)(u / tiles) * a.hp, h1 = min(h0 + a.hp, a.heads[v]);
-    const uint32_t token = tile * per + (threadIdx.x >> a.lg);
-    r.live = all.live && token < a.tokens;
-    r.two = all.two && token < a.tokens;
-    r.rotates = all.rotates && token < a.tokens;
-    const uint32_t tk = min(token, a.tokens - 1);
-    const uint32_t b = tk / (uint32_t)a.N, n = tk - b * (uint32_t)a.N;
-    r.angles(position(a, b, n), sF, sM, -1.f);       // the transposed rotation
-    const T* src = static_cast<const T*>(a.x[v]) + (int64_t)b * xs.b + (int64_t)h0 * xs.h + (int64_t)n * xs.n;
-    const T* grd = static_cast<const T*>(a.dy[v]) + (int64_t)b * ds.b + (int64_t)h0 * ds.h + (int64_t)n * ds.n;
-    T* dst = static_cast<T*>(a.y[v]) + (int64_t)b * ys.b + (int64_t)h0 * ys.h + (int64_t)n * ys.n;
-    for (int h = h0; h < h1; h += HB, src += HB * xs.h, grd += HB * ds.h, dst += HB * ys.h) {
-      V8<T> x0[HB], x1[HB], g0[HB], g1[HB];
+  uint32_t tile = tile0;
+  for (int done = 0, h0 = head0; done < count; ++tile, h0 = 0) {
+    const Token it = token_of(tile);
+    const int h1 = min(heads, h0 + count - done);
+    done += h1 - h0;
+    r.live = all.live && it.there;
+    r.two = all.two && it.there;
+    r.rotates = all.rotates && it.there;
+    r.angles(position(a, it.b, it.n), sF, sM, -1.f);       // the transposed rotation
+    T* dst = static_cast<T*>(a.y[v]) + (int64_t)it.b * ys.b + (int64_t)h0 * ys.h + (int64_t)it.n * ys.n;
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, dst += ys.h) {
+      copy();                                        // over the stage of the row before this one
+      cp_async_wait<C::kStages - 1>();
+      float x[R::NC] = {}, g[R::NC] = {};
+      const uint8_t* at = ahead + (st * C::kPieces * kNThreads + threadIdx.x) * 16;
+      st = st + 1 == C::kStages ? 0 : st + 1;
 #pragma unroll
-      for (int j = 0; j < HB; ++j) {
-        if (h + j >= h1) break;
-        if (r.live) {
-          x0[j].load(src + j * xs.h + r.c0);
-          g0[j].load(grd + j * ds.h + r.c0);
-        }
-        if (r.two) {
-          x1[j].load(src + j * xs.h + r.c1);
-          g1[j].load(grd + j * ds.h + r.c1);
-        }
+      for (int e = 0; e < R::NC; e += 8) {
+        if (!(e < 8 ? r.live : r.two)) continue;
+        V8<T> p;
+        p.pieces(at + (e / C::kPer) * (kNThreads * 16), kNThreads * 16);
+        p.get(x + e);
+        p.pieces(at + (C::kPieces / 2 + e / C::kPer) * (kNThreads * 16), kNThreads * 16);
+        p.get(g + e);
       }
+      r.apply(g, row);                               // dz
+      float sx = 0.f, sg = 0.f, sx1 = 0.f, sg1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < HB; ++j) {
-        if (h + j >= h1) break;
-        float x[R::NC] = {}, g[R::NC] = {};
-        if (r.live) {
-          x0[j].get(x);
-          g0[j].get(g);
-        }
-        if (R::NC > 8 && r.two) {
-          x1[j].get(x + (R::NC - 8));
-          g1[j].get(g + (R::NC - 8));
-        }
-        r.apply(g, row);                             // dz
-        float sx = 0.f, sg = 0.f;
-#pragma unroll
-        for (int e = 0; e < R::NC; ++e) {
-          sx += x[e] * x[e];
-          sg += g[e] * r.w[e] * x[e];
-        }
-        for (int o = 1 << a.lg >> 1; o > 0; o >>= 1) {
-          sx += __shfl_xor_sync(0xffffffffu, sx, o);
-          sg += __shfl_xor_sync(0xffffffffu, sg, o);
-        }
-        const float rs = rsqrtf(sx * a.inv_d + a.eps);
-        const float k = rs * rs * sg * a.inv_d;      // dx = rs (w dz - x rs^2 (g . x) / d)
-#pragma unroll
-        for (int e = 0; e < R::NC; ++e) {
-          acc[e] += g[e] * (x[e] * rs);
-          x[e] = rs * (g[e] * r.w[e] - x[e] * k);
-        }
-        if (r.live) V8<T>::store(dst + j * ys.h + r.c0, x);
-        if (R::NC > 8 && r.two) V8<T>::store(dst + j * ys.h + r.c1, x + (R::NC - 8));
+      for (int e = 0; e < R::NC; e += 2) {
+        float y0, y1;                                // w dz
+        mul2(y0, y1, g[e], g[e + 1], r.w[e], r.w[e + 1]);
+        fma2(sg, sg1, y0, y1, x[e], x[e + 1], sg, sg1);
+        fma2(sx, sx1, x[e], x[e + 1], x[e], x[e + 1], sx, sx1);
       }
+      sx += sx1;
+      sg += sg1;
+      for (int o = 1 << a.lg >> 1; o > 0; o >>= 1) {
+        sx += __shfl_xor_sync(0xffffffffu, sx, o);
+        sg += __shfl_xor_sync(0xffffffffu, sg, o);
+      }
+      const float rs = rsqrtf(sx * a.inv_d + a.eps);
+      const float k = -rs * (rs * rs * (sg * a.inv_d));   // dx = rs w dz - x rs^3 (g . x) / d
+#pragma unroll
+      for (int e = 0; e < R::NC; e += 2) {
+        float y0, y1;
+        mul2(y0, y1, g[e], g[e + 1], rs, rs);
+        fma2(acc[e], acc[e + 1], y0, y1, x[e], x[e + 1], acc[e], acc[e + 1]);
+        mul2(y0, y1, y0, y1, r.w[e], r.w[e + 1]);
+        fma2(x[e], x[e + 1], x[e], x[e + 1], k, k, y0, y1);
+      }
+      if (r.live) V8<T>::store(dst + r.c0, x);
+      if (R::NC > 8 && r.two) V8<T>::store(dst + r.c1, x + (R::NC - 8));
     }
   }
   if (a.dw[v] == nullptr) return;
   // the CTA's sums: the groups' partial sums of a column, in the order of the groups
+  cp_async_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ahead);
 #pragma unroll
   for (int e = 0; e < R::NC; ++e) sums[e * kNThreads + threadIdx.x] = acc[e];
   __syncthreads();
@@ -336,28 +416,28 @@ __global__ void __launch_bounds__(kNThreads) norm_rope_bwd_kernel(const NormArgs
   }
 }
 
-// dw of q (block 0) and k (block 1): a column's partial sums, 1024 / d (rounded
-// down) threads a column, joined in their order.
+// dw of q (blockIdx.y = 0) and k: eight columns a block, 128 threads a column, each with
+// every 128th CTA's sums, joined in their order.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int d, int n0, int n1, float* dq,
                                                        float* dk) {
-  __shared__ float sh[1024];
-  float* out = blockIdx.x ? dk : dq;
+  __shared__ float sh[128][9];
+  float* out = blockIdx.y ? dk : dq;
   if (out == nullptr) return;
-  const int n = blockIdx.x ? n1 : n0;
-  part += blockIdx.x ? (size_t)n0 * d : 0;
-  const int g = (int)threadIdx.x / d, c = (int)threadIdx.x - g * d, ng = 1024 / d;
+  const int n = blockIdx.y ? n1 : n0;
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  part += (blockIdx.y ? (size_t)n0 * d : 0) + blockIdx.x * 8 + c;
   float s = 0.f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (g < ng) {
 #pragma unroll 8
-    for (int i = g; i < n; i += ng) s += part[(size_t)i * d + c];
-  }
-  sh[threadIdx.x] = s;
+  for (int i = g; i < n; i += 128) s += part[(size_t)i * d];
+  sh[g][c] = s;
   __syncthreads();
-  if (g != 0) return;
-  s = 0.f;
-  for (int i = 0; i < ng; ++i) s += sh[i * d + c];
-  out[c] = s;
+  if (threadIdx.x >= 256) return;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;      // a warp a column
+  s = (sh[lane][w] + sh[lane + 32][w]) + (sh[lane + 64][w] + sh[lane + 96][w]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) out[blockIdx.x * 8 + w] = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -381,7 +461,8 @@ Pairs pairs_of(const fa_norm_rope_params* p) {
 }
 
 int units_of(const fa_norm_rope_params* p) {
-  return pairs_of(p) == kHalves ? (p->d - p->rot / 2) / 8 : p->d / 8;
+  const Pairs m = pairs_of(p);
+  return m == kHalves ? (p->d - p->rot / 2) / 8 : m == kAdjacent ? (p->d + 8) / 16 : p->d / 8;
 }
 
 int lg_of(int units) {
@@ -412,15 +493,14 @@ fa_status sm_count(int& sms) {
   return FA_OK;
 }
 
-constexpr int kNormCtas = 152 * 5;     // of the backward pass, at most: a workspace's size does not depend on the device
-
-// CTAs of q and of k: by their heads, no more than there are tokens' tiles x heads
+// CTAs of q and of k: by their heads, no more than there are tokens' tiles x heads (152 SMs: a workspace's size does
+// not depend on the device)
 void bwd_ctas(const fa_norm_rope_params* p, int (&n)[2]) {
   const int heads[2] = {p->H, p->H_kv};
   const int per = kNThreads >> lg_of(units_of(p));
   const long long tiles = ((long long)p->B * p->N + per - 1) / per;
   for (int v = 0; v < 2; ++v) {
-    const long long share = std::max<long long>(1, (long long)kNormCtas * heads[v] / (p->H + p->H_kv));
+    const long long share = std::max<long long>(1, 152ll * bwd_ctas_of(pairs_of(p)) * heads[v] / (p->H + p->H_kv));
     n[v] = heads[v] == 0 ? 0 : (int)std::min(share, tiles * heads[v]);
   }
 }
@@ -486,21 +566,16 @@ template <typename T, int kPairs> cudaError_t launch_fwd(NormArgs a, int sms, cu
   return cudaGetLastError();
 }
 
-template <typename T, int kPairs> cudaError_t launch_bwd(NormArgs a, cudaStream_t s) {
-  // heads of an item: all, unless there are fewer tiles of tokens than CTAs
-  const int per = kNThreads >> a.lg;
-  const long long tiles = ((long long)a.tokens + per - 1) / per;
-  a.hp = 1;
-  for (int v = 0; v < 2; ++v)
-    if (a.heads[v] > 0) {
-      const long long splits = std::min<long long>(a.heads[v], (a.ctas[v] + tiles - 1) / tiles);
-      a.hp = std::max(a.hp, (int)((a.heads[v] + splits - 1) / splits));
-    }
-  norm_rope_bwd_kernel<T, kPairs><<<(unsigned)(a.ctas[0] + a.ctas[1]), kNThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+template <typename T, int kPairs> cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s) {
+  auto kern = norm_rope_bwd_kernel<T, kPairs>;
+  constexpr int bytes = BwdCfg<T, kPairs>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(a.ctas[0] + a.ctas[1]), kNThreads, bytes, s>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(2);
+  c.gridDim = dim3((unsigned)(a.d / 8), 2);
   c.blockDim = dim3(1024);
   c.stream = s;
   cudaLaunchAttribute at{};
