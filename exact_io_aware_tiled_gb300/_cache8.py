@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from ._lib import DTYPE_CODE, FA_OK, FAError, int32_lengths
+from ._lib import DTYPE_CODE, FA_OK, FAError, _int32, int32_lengths
 from ._ops import (_check4, _flat_f32, _i32, _i64, _f32, _lens, _need_workspace, _on, _packer, _ptrs, _rows, _size_of,
                    _sized, _vp)
 
@@ -28,24 +28,34 @@ class fa_cache8_params(ctypes.Structure):
 
 _pack = _packer(fa_cache8_params)
 _none3 = (0, 0, 0)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, device):
-    """(pages, H_kv, page, d) of a cache whose tensors fit together."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+def _cache(k_cache, v_cache, k_scale, v_scale, like):
+    """(pages, H_kv, page, d) of a cache whose tensors fit together, on the device of the CUDA tensor `like`."""
+    shape, at = k_cache.shape, like.get_device()
+    if len(shape) == 4 and v_cache.shape == shape and k_cache.dtype in _CODES and v_cache.dtype in _CODES and \
+            k_cache.get_device() == at and v_cache.get_device() == at and k_cache.stride(3) == 1 and \
+            v_cache.stride(3) == 1 and _scales(k_scale, shape, at) and _scales(v_scale, shape, at):
+        return shape
+    device = like.device
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, H_kv, page, d], got %s and %s" %
-                         (tuple(k_cache.shape), tuple(v_cache.shape)))
+                         (tuple(shape), tuple(v_cache.shape)))
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
+        if t.dtype not in _CODES:
             raise ValueError("%s must be float8_e4m3fn (or uint8 codes), got %s" % (n, t.dtype))
         if t.device != device:
             raise ValueError("%s must be on %s, got %s" % (n, device, t.device))
         if t.stride(3) != 1:
             raise ValueError("%s: the last dimension must be contiguous (stride 1), got strides %s" % (n, t.stride()))
-    shape = tuple(k_cache.shape)
-    _flat_f32(k_scale, "k_scale", device, shape[:2])
-    _flat_f32(v_scale, "v_scale", device, shape[:2])
-    return shape
+    _flat_f32(k_scale, "k_scale", device, tuple(shape[:2]))
+    _flat_f32(v_scale, "v_scale", device, tuple(shape[:2]))
+    raise ValueError("the cache's tensors do not fit together")
+
+
+def _scales(t, shape, at):
+    return t.dtype is torch.float32 and t.get_device() == at and t.shape == shape[:2] and t.is_contiguous()
 
 
 def _check_table(table, B):
@@ -58,7 +68,7 @@ def _check_table(table, B):
 def _table(table, device):
     """int32 rows on `device` (converted on the current stream where they are something else; numbers that int32 does
     not hold stay outside the pages)."""
-    if table.dtype is torch.int32 and table.device == device and table.stride(1) == 1 and \
+    if table.dtype is torch.int32 and table.is_cuda and table.get_device() == device.index and table.stride(1) == 1 and \
             (table.shape[0] == 1 or table.stride(0) >= table.shape[1]):
         return table
     return int32_lengths(table, device)
@@ -82,7 +92,7 @@ def cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, table, seqlens, *, s
     B, Hkv, T, d = k.shape
     vs = _rows(v, "v", k, k.shape)
     dev = k.device
-    pages, heads, page, width = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    pages, heads, page, width = _cache(k_cache, v_cache, k_scale, v_scale, k)
     if (heads, width) != (Hkv, d):
         raise ValueError("the cache has %d heads of %d, k %d of %d" % (heads, width, Hkv, d))
     _check_table(table, B)
@@ -106,7 +116,7 @@ def cache8_read(k_cache, v_cache, k_scale, v_scale, table, seqlens, *, dtype=tor
     dev = k_cache.device
     if not k_cache.is_cuda:
         raise ValueError("k_cache must be a CUDA tensor")
-    pages, Hkv, page, d = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    pages, Hkv, page, d = _cache(k_cache, v_cache, k_scale, v_scale, k_cache)
     if table.dim() != 2:
         raise ValueError("table must have shape [B, width]")
     B = table.shape[0]
@@ -153,7 +163,7 @@ def cache8_fwd(q, k_cache, v_cache, k_scale, v_scale, table, seqlens, *, window=
     _check4(q, "q")
     B, H, T, d = q.shape
     dev = q.device
-    pages, Hkv, page, width = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    pages, Hkv, page, width = _cache(k_cache, v_cache, k_scale, v_scale, q)
     if width != d or Hkv < 1 or H % Hkv:
         raise ValueError("the cache has %d heads of %d, q %d of %d" % (Hkv, width, H, d))
     _check_table(table, B)
@@ -167,7 +177,7 @@ def cache8_fwd(q, k_cache, v_cache, k_scale, v_scale, table, seqlens, *, window=
             o, lse = out
             _rows(o, "out o", q, q.shape)
             _flat_f32(lse, "out lse", dev, (B, H, T))
-        p = _pack(B, H, Hkv, T, d, DTYPE_CODE[q.dtype], page, pages, tab.shape[1], int(window), int(sinks),
+        p = _pack(B, H, Hkv, T, d, DTYPE_CODE[q.dtype], page, pages, tab.shape[1], _int32(window), _int32(sinks),
                   0.0 if scale is None else float(scale), lens.data_ptr(), tab.data_ptr(), tab.stride(0),
                   *q.stride()[:3], *o.stride()[:3], *_none3, *_none3, *k_cache.stride()[:3], *v_cache.stride()[:3])
         ws = _need_workspace(workspace, _size_of("fa_cache8_workspace_size")(p), dev)

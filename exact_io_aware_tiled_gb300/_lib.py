@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from pathlib import Path
 from typing import Optional
 
@@ -49,6 +50,40 @@ class fa_params(ctypes.Structure):
         ("window", ctypes.c_int32),
         ("fwd_kernel", ctypes.c_int32),
     ]
+
+
+_pack_code = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_uint64: "Q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+_pack = struct.Struct("@" + "".join(_pack_code[t] for _, t in fa_params._fields_) + "0q").pack
+assert struct.calcsize("@" + "".join(_pack_code[t] for _, t in fa_params._fields_) + "0q") == ctypes.sizeof(fa_params)
+_raw = {}
+
+
+def _fn(name, restype, *argtypes):
+    """The library's function `name` for parameters packed to bytes (its own function object: the one that ``load`` sets
+    up takes the ctypes structure)."""
+    f = _raw.get(name)
+    if f is None:
+        f = _raw[name] = load()[name]
+        f.argtypes, f.restype = list(argtypes), restype
+    return f
+
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _int32(n):
+    """n, or the end of int32 next to it: a window or a number of keys past it hides nothing more."""
+    return max(-2 ** 31, min(int(n), 2 ** 31 - 1))
+
+
+def _packed(q, k, causal, seqlens_k, dropout_p, seed, offset, block_mask, scale, o_f32, prof, window, fwd_kernel):
+    """fa_params of these tensors as bytes (filling the ctypes structure costs three times as long)."""
+    start, stop = (0, 0) if prof is None else (x.value if isinstance(x, ctypes.c_void_p) else x for x in prof)
+    return _pack(*q.shape, DTYPE_CODE[q.dtype], *q.stride()[:3], 0.0 if scale is None else float(scale),
+                 1 if causal else 0, _address(seqlens_k), float(dropout_p), int(seed) & (2 ** 64 - 1),
+                 int(offset) & (2 ** 64 - 1), _address(block_mask), 128, _address(o_f32), start or 0, stop or 0, k.shape[1],
+                 *k.stride()[:3], _int32(window), int(fwd_kernel))
 
 
 class fa_fp8_params(ctypes.Structure):
@@ -121,8 +156,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:       # the current device's current stream, without the Stream object around it
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -260,19 +295,19 @@ def fwd(q, k, v, *, causal=False, seqlens_k=None, dropout_p=0.0, seed=0, offset=
     force the one- / two-query-tile kernel."""
     _check(q)
     (q,), (k, v) = _layouts([q], [k, v])
-    lib = load()
     seqlens_k, block_mask = _aux(seqlens_k, block_mask, q)
     B, H, N, d = q.shape
     if out is not None and not q.is_contiguous():
         raise ValueError("out= takes contiguous outputs, so q must be contiguous too (o shares q's strides)")
     o, lse = _outputs(out, [q, ((B, H, N), torch.float32, q.device)])
     o32 = torch.empty((B, H, N, d), device=q.device, dtype=torch.float32) if return_o_f32 else None
-    p = make_params(q, k=k, causal=causal, seqlens_k=seqlens_k, dropout_p=dropout_p, seed=seed, offset=offset,
-                    block_mask=block_mask, scale=scale, o_f32=o32, prof=prof, window=window, fwd_kernel=fwd_kernel)
-    wsz = lib.fa_fwd_workspace_size(ctypes.byref(p))
+    p = _packed(q, k, causal, seqlens_k, dropout_p, seed, offset, block_mask, scale, o32, prof, window, fwd_kernel)
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    wsz = _fn("fa_fwd_workspace_size", sz, vp)(p)
     ws = _workspace(wsz, workspace, q.device)
-    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(ws), wsz, _stream(stream))
-    st = lib.fa_fwd_sinks(ctypes.byref(p), int(sinks), *args) if sinks else lib.fa_fwd(ctypes.byref(p), *args)
+    st = _fn("fa_fwd_sinks", ctypes.c_int, vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz, vp)(
+        p, _int32(sinks), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), wsz,
+        _stream(stream))
     if st != FA_OK:
         raise FAError(st, "fa_fwd_sinks" if sinks else "fa_fwd")
     fwd.last_workspace = ws
@@ -292,17 +327,15 @@ def bwd(q, k, v, o, do, lse, *, causal=False, seqlens_k=None, dropout_p=0.0, see
         raise ValueError("out= takes contiguous outputs, so q, o, dO, k and v must be contiguous too")
     if not lse.is_contiguous():
         raise ValueError("lse must be the contiguous [B, H, N] float32 tensor fwd returns")
-    lib = load()
     seqlens_k, block_mask = _aux(seqlens_k, block_mask, q)
     dq, dk, dv = _outputs(out, [q, k, v])
-    p = make_params(q, k=k, causal=causal, seqlens_k=seqlens_k, dropout_p=dropout_p, seed=seed, offset=offset,
-                    block_mask=block_mask, scale=scale, prof=prof, window=window)
-    wsz = lib.fa_bwd_sinks_workspace_size(ctypes.byref(p), int(sinks)) if sinks else \
-        lib.fa_bwd_workspace_size(ctypes.byref(p))
+    p = _packed(q, k, causal, seqlens_k, dropout_p, seed, offset, block_mask, scale, None, prof, window, 0)
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    wsz = _fn("fa_bwd_sinks_workspace_size", sz, vp, ctypes.c_int32)(p, _int32(sinks))
     ws = _workspace(wsz, workspace, q.device)
-    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), wsz,
-            _stream(stream))
-    st = lib.fa_bwd_sinks(ctypes.byref(p), int(sinks), *args) if sinks else lib.fa_bwd(ctypes.byref(p), *args)
+    st = _fn("fa_bwd_sinks", ctypes.c_int, vp, ctypes.c_int32, *([vp] * 10), sz, vp)(
+        p, _int32(sinks), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), wsz, _stream(stream))
     if st != FA_OK:
         raise FAError(st, "fa_bwd_sinks" if sinks else "fa_bwd")
     bwd.last_workspace = ws

@@ -45,9 +45,13 @@ __device__ __forceinline__ int exponent_of(float m) {
   return max(-126, (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0));     // 448 = 1.75 2^8
 }
 
+// A thread holds up to kHeld 8-element pieces of the page's new rows: each is read once, all at the same time.
+constexpr int kHeld = 8, kAppendThreads = 256;
+static_assert(kHeld * kAppendThreads * 8 >= 128 * 128, "a page's rows in registers");
+
 template <typename T>
-__global__ void __launch_bounds__(128) cache8_append_kernel(const Cache8Rows a, int touched) {
-  __shared__ float smax[4];
+__global__ void __launch_bounds__(kAppendThreads) cache8_append_kernel(const Cache8Rows a, int touched) {
+  __shared__ float smax[kAppendThreads / 32];
   int u = (int)blockIdx.x;
   const int pi = u % touched;
   u /= touched;
@@ -61,19 +65,22 @@ __global__ void __launch_bounds__(128) cache8_append_kernel(const Cache8Rows a, 
   const int id = a.table[(int64_t)b * a.table_stride + w];
   if ((unsigned)id >= (unsigned)a.pages) return;     // an absent page takes nothing
   const int r0 = max(from - base, 0), r1 = min(L - base, a.page);     // rows of the page that are new
-  const int per = a.d >> 3;                          // 8-element pieces of a row
+  const int per = a.d >> 3, lgp = a.d == 64 ? 3 : 4; // 8-element pieces of a row
   const int n = (r1 - r0) * per;
   const Strides xs = a.xs[y], cs = a.cs[y];
   const T* src = static_cast<const T*>(a.x[y]) + (int64_t)b * xs.b + (int64_t)hk * xs.h + (int64_t)(base + r0 - first) * xs.n;
   uint8_t* page = a.code[y] + (int64_t)id * cs.b + (int64_t)hk * cs.h;
   float* scale = a.scale[y] + (size_t)id * a.Hkv + hk;
   const float was = r0 > 0 ? *scale : 0.f;
-  float m = 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int row = i / per;
-    m = amax8<T>(*reinterpret_cast<const uint4*>(src + (int64_t)row * xs.n + (i - row * per) * 8), m);
+  uint4 held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = threadIdx.x + k * blockDim.x, row = i >> lgp;
+    held[k] = i < n ? *reinterpret_cast<const uint4*>(src + (int64_t)row * xs.n + (i & (per - 1)) * 8) : make_uint4(0u, 0u, 0u, 0u);
   }
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) m = amax8<T>(held[k], m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (blockDim.x > 32) {
@@ -108,21 +115,22 @@ __global__ void __launch_bounds__(128) cache8_append_kernel(const Cache8Rows a, 
   }
   // 1 / now: a power of two too where the cache was written here
   const float f = now > 0.f ? 1.f / now : 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int row = i / per, c = (i - row * per) * 8;
-    const uint4 v = *reinterpret_cast<const uint4*>(src + (int64_t)row * xs.n + c);
-    const uint32_t t[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = threadIdx.x + k * blockDim.x, row = i >> lgp;
+    if (i >= n) break;
+    const uint32_t t[4] = {held[k].x, held[k].y, held[k].z, held[k].w};
     uint32_t o[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      o[k] = e4m3x4(Cvt<T>::lo(t[2 * k]) * f, Cvt<T>::hi(t[2 * k]) * f, Cvt<T>::lo(t[2 * k + 1]) * f,
-                    Cvt<T>::hi(t[2 * k + 1]) * f);
-    *reinterpret_cast<uint2*>(page + (int64_t)(r0 + row) * cs.n + c) = make_uint2(o[0], o[1]);
+    for (int y = 0; y < 2; ++y)
+      o[y] = e4m3x4(Cvt<T>::lo(t[2 * y]) * f, Cvt<T>::hi(t[2 * y]) * f, Cvt<T>::lo(t[2 * y + 1]) * f,
+                    Cvt<T>::hi(t[2 * y + 1]) * f);
+    *reinterpret_cast<uint2*>(page + (int64_t)(r0 + row) * cs.n + (i & (per - 1)) * 8) = make_uint2(o[0], o[1]);
   }
 }
 
-// Rows out: each thread 16 codes to 16 values; zeros behind the last row and for absent pages.
+// Rows out: a thread turns 8 codes into 8 values at a time, so that the lanes' stores lie side by side; zeros behind the
+// last row and for absent pages.
 constexpr int kReadRows = 64;                        // rows of a CTA
 template <typename T>
 __global__ void __launch_bounds__(128) cache8_read_kernel(const Cache8Rows a, int chunks) {
@@ -133,33 +141,41 @@ __global__ void __launch_bounds__(128) cache8_read_kernel(const Cache8Rows a, in
   u >>= 1;
   const int hk = u % a.Hkv, b = u / a.Hkv;
   const int L = max(0, min(a.width * a.page, a.lens[b]));
-  const int per = a.d >> 4;
+  const int per = a.d >> 3, lgp = a.d == 64 ? 3 : 4;
   const Strides xs = a.xs[y], cs = a.cs[y];
   T* dst = static_cast<T*>(a.x[y]) + (int64_t)b * xs.b + (int64_t)hk * xs.h;
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
   const int n = min(kReadRows, a.T - n0) * per;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += 128) {
-    const int row = i / per, at = n0 + row, c = (i - row * per) * 16;
-    uint32_t o[8] = {};
-    if (at < L) {
-      const int id = table[at >> a.lg];
-      if ((unsigned)id < (unsigned)a.pages) {
-        const float s = a.scale[y][(size_t)id * a.Hkv + hk];
-        const uint4 v = *reinterpret_cast<const uint4*>(a.code[y] + (int64_t)id * cs.b + (int64_t)hk * cs.h +
-                                                       (int64_t)(at & (a.page - 1)) * cs.n + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * 128) {
+    int id[4];
+    float sc[4];
+    uint2 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 p = widen2(w[k] & 0xFFFFu), q = widen2(w[k] >> 16);
-          o[2 * k] = Cvt<T>::pack(p.x * s, p.y * s);
-          o[2 * k + 1] = Cvt<T>::pack(q.x * s, q.y * s);
-        }
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * 128, at = n0 + (i >> lgp);
+      id[k] = i < n && at < L ? table[at >> a.lg] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * 128, at = n0 + (i >> lgp);
+      sc[k] = 0.f;
+      v[k] = make_uint2(0u, 0u);
+      if ((unsigned)id[k] < (unsigned)a.pages) {
+        sc[k] = a.scale[y][(size_t)id[k] * a.Hkv + hk];
+        v[k] = *reinterpret_cast<const uint2*>(a.code[y] + (int64_t)id[k] * cs.b + (int64_t)hk * cs.h +
+                                              (int64_t)(at & (a.page - 1)) * cs.n + (i & (per - 1)) * 8);
       }
     }
-    uint4* out = reinterpret_cast<uint4*>(dst + (int64_t)at * xs.n + c);
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * 128;
+      if (i >= n) break;
+      const float2 p0 = widen2(v[k].x & 0xFFFFu), p1 = widen2(v[k].x >> 16), p2 = widen2(v[k].y & 0xFFFFu), p3 = widen2(v[k].y >> 16);
+      const float s = sc[k];
+      *reinterpret_cast<uint4*>(dst + (int64_t)(n0 + (i >> lgp)) * xs.n + (i & (per - 1)) * 8) =
+          make_uint4(Cvt<T>::pack(p0.x * s, p0.y * s), Cvt<T>::pack(p1.x * s, p1.y * s), Cvt<T>::pack(p2.x * s, p2.y * s),
+                     Cvt<T>::pack(p3.x * s, p3.y * s));
+    }
   }
 }
 
@@ -169,8 +185,9 @@ cudaError_t launch_cache8_append(int dtype, const Cache8Rows& a, cudaStream_t s)
   const int touched = (a.T + a.page - 2) / a.page + 1;          // pages that T rows can touch
   const long long grid = 2ll * a.B * a.Hkv * std::min(touched, a.width);
   if (grid >= 1ll << 31) return cudaErrorInvalidValue;
-  // a warp is enough for up to 32 pieces of 8 elements
-  const int threads = (long long)std::min(a.T, a.page) * a.d / 8 <= 32 ? 32 : 128;
+  // as many threads as 8-element pieces of a page's new rows, from a warp up to what kHeld of them a thread need
+  const long long pieces = (long long)std::min(a.T, a.page) * a.d / 8;
+  const int threads = (int)std::clamp<long long>((pieces + 31) / 32 * 32, 32, kAppendThreads);
   const int t = std::min(touched, a.width);
   if (dtype == FA_DT_BF16) cache8_append_kernel<__nv_bfloat16><<<(unsigned)grid, threads, 0, s>>>(a, t);
   else cache8_append_kernel<__half><<<(unsigned)grid, threads, 0, s>>>(a, t);
