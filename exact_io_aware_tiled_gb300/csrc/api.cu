@@ -53,11 +53,19 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
   k.sinks = sinks;
   k.tiles = (sinks + kTile - 1) / kTile;
   const int hkv = p->H_kv == 0 ? p->H : p->H_kv;
-  const long long steps = (long long)((p->N + kTile - 1) / kTile) * (p->H / hkv);
-  // Items of 16 query tiles where there are few first key tiles, and no more than about four for each CTA: their dK and
-  // dV take 64 KB each (d = 128: 128 KB).
-  const long long most = std::max<long long>(1, 4 * 152 / ((long long)p->B * hkv * k.tiles));
-  const long long chunks = std::min((steps + 15) / 16, most);
+  const long long nq = (p->N + kTile - 1) / kTile, g = p->H / hkv, steps = nq * g, heads = (long long)p->B * hkv;
+  // An item of a first key tile may take a CTA's whole share of all steps (query tiles at key tiles), as it starts
+  // among the first: cutting it further costs more, in dK and dV that go through float32, than it balances.  us,
+  // backward, items of 8 / 16 / 32 steps: 64 heads of 64 x 4,096, window 512, 4 first keys 265 / 256 / 243 (one item
+  // each), 8 x 4 K/V heads x 2,047 with 3 query heads and 150 first keys 147 / 141 / 132; float32, whose blocks are one
+  // warpgroup each and four or more on an SM, 32 heads x 2,048 1,398 / 2,010 / 2,010.  At least 16 steps (float32: 2),
+  // and no more than about four items for each CTA: a part takes 64 KB (d = 128: 128 KB).
+  const bool f32 = p->dtype == FA_DT_F32;
+  const long long span = std::min<long long>(nq, (p->window + kTile - 1) / kTile + 1);
+  const long long share = heads * g * (nq * span + k.tiles * nq) / (f32 ? 4 * 152 : 152);
+  const long long least = std::max<long long>(f32 ? 2 : 16, share);
+  const long long most = std::max<long long>(1, 4 * 152 / (heads * k.tiles));
+  const long long chunks = std::min((steps + least - 1) / least, most);
   k.steps = (int)((steps + chunks - 1) / chunks);
   k.chunks = (int)((steps + k.steps - 1) / k.steps);
   return k;

@@ -56,7 +56,7 @@ def test_workspaces():
     p = _params(causal=1, window=300, N=n, stride_h=n * 64, stride_b=3 * n * 64)
     plain = lib.fa_bwd_workspace_size(ctypes.byref(p))
     assert size(p, 0) == plain and size(p, -3) == plain and size(p, n) == plain
-    # 40 query tiles of a first key tile: three items of dK and dV for each of the 6 heads
+    # 40 query tiles of a first key tile: items of 16 of them for each of the 6 heads
     assert size(p, 4) >= plain + 6 * 3 * T * 2 * 64 * 4
     assert _both(p, 4, ws=plain)[1] == 4
     assert size(_params(causal=1, window=0), 4) == lib.fa_bwd_workspace_size(ctypes.byref(_params()))
@@ -86,7 +86,7 @@ def test_schedules_cover_the_visible_pairs_once():
         nq, group = -(-N // T), rng.choice([1, 2, 5])
         tiles = -(-s // T)
         steps = nq * group
-        chunks = min(-(-steps // 16), max(1, 608 // (rng.choice([1, 3, 100]) * tiles)))
+        chunks = min(-(-steps // rng.choice([2, 16, 40])), max(1, 608 // (rng.choice([1, 3, 100]) * tiles)))
         per = -(-steps // chunks)
         chunks = -(-steps // per)
         pairs = {}
@@ -210,9 +210,14 @@ def test_grouped_heads_and_padding(dtype, d, H, Hkv):
 
 @gpu
 @pytest.mark.parametrize("dtype,d", KINDS)
-def test_long_rows_are_cut(dtype, d):
-    # 40 query tiles and more at the first key tile: several items, in float32 parts
-    x = make(1, 4, 2, 5000, d, dtype, 7)
+@pytest.mark.parametrize("B,H,Hkv,N", [(1, 4, 2, 5000), (8, 16, 16, 1100)])
+def test_long_rows_are_cut(dtype, d, B, H, Hkv, N):
+    # 40 query tiles and more at the first key tile: several items, in float32 parts; and many heads, an item each
+    x = make(B, H, Hkv, N, d, dtype, 7)
+    lib = fa.load()
+    p = fa.make_params(x[0], k=x[1], causal=True, window=200)
+    parts = lib.fa_bwd_sinks_workspace_size(ctypes.byref(p), 4) > lib.fa_bwd_workspace_size(ctypes.byref(p))
+    assert parts == (B == 1 or dtype == "f32")
     for w, s in ((200, 4), (513, 140)):
         got = run(x, w, s)
         check(got, plain(*x, w, s), dtype)
