@@ -65,7 +65,7 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
   const long long share = heads * g * (nq * span + k.tiles * nq) / (f32 ? 4 * 152 : 152);
   const long long least = std::max<long long>(f32 ? 2 : 16, share);
   const long long most = std::max<long long>(1, 4 * 152 / (heads * k.tiles));
-  const long long chunks = std::min((steps + least - 1) / least, most);
+  const long long chunks = std::max<long long>(1, std::min((steps + least / 2) / least, most));
   k.steps = (int)((steps + chunks - 1) / chunks);
   k.chunks = (int)((steps + k.steps - 1) / k.steps);
   return k;

@@ -16,6 +16,9 @@
 // serve them all; a row is the columns of a group of 2^n lanes, which shuffles
 // sum.  dw is summed by a thread over its rows in registers, by a CTA through
 // shared memory and over the CTAs by a second kernel, each in a fixed order.
+// Measured: GPT-2-medium q and k, 537 MB forward 87 us (6.1 TB/s, 0.90 of the copy
+// rate), 805 MB backward 137 us (5.9 TB/s); fp16, 32 + 4 heads of 128, interleaved, 581
+// MB backward 119 us (4.9 TB/s: conversions and shuffles of half as many rows).
 #include <algorithm>
 #include <cmath>
 
@@ -33,14 +36,15 @@ enum Pairs {
   kShared        // (i, i + rot/2), any rot: 8 columns, the partners through shared memory
 };
 
-// The backward kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.
-__host__ __device__ constexpr int bwd_ctas_of(int pairs) { return pairs == kShared ? 4 : 3; }
-template <typename T, int kPairs> struct BwdCfg {
+// The kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.
+__host__ __device__ constexpr int ctas_of(int pairs, bool back) { return back ? (pairs == kShared ? 4 : 3) : 3; }
+template <typename T, int kPairs, bool kBack> struct NormCfg {
   static constexpr int kPer = 16 / (int)sizeof(T);                       // elements of a 16-byte piece
-  static constexpr int kPieces = 2 * (kPairs == kShared ? 8 : 16) / kPer; // of a row of x and dy in a thread
+  static constexpr int kRow = (kPairs == kShared ? 8 : 16) / kPer;       // pieces of a row in a thread
+  static constexpr int kPieces = kBack ? 2 * kRow : kRow;
   static constexpr int kStages = kPieces == 8 ? 3 : kPieces == 4 ? 6 : 8;
   static constexpr int kBytes = kStages * kPieces * kNThreads * 16;
-  static_assert(kBytes >= kNThreads * 16 * (int)sizeof(float), "room for the sums at the end");
+  static_assert(!kBack || kBytes >= kNThreads * 16 * (int)sizeof(float), "room for the sums at the end");
 };
 
 struct NormArgs {
@@ -51,15 +55,14 @@ struct NormArgs {
   Strides xs[2], ds[2], ys[2];
   int heads[2];
   int N, d, rot, units, lg;   // units: threads that own columns of a row; 2^lg lanes a row
-  int hp;                  // heads per blockIdx.y (forward)
   uint32_t tokens;         // B * N
   const void* pos;
   int pos64;
   int64_t pos_b, pos_n, start;
   const double* inv_freq;
   float mscale, eps, inv_d;
-  // backward: CTAs of q, then of k; each leaves one row of sums
-  int ctas[2];
+  int ctas[2];             // CTAs of q, then of k
+  // backward: each CTA leaves one row of sums
   float* part;             // [ctas[0] + ctas[1]][d]
   float* dw[2];            // [d] or nullptr
 };
@@ -68,10 +71,6 @@ struct NormArgs {
 template <typename T> struct V8;
 template <> struct V8<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
   __device__ __forceinline__ void pieces(const uint8_t* p, int step) {
     a = *reinterpret_cast<const float4*>(p);
     b = *reinterpret_cast<const float4*>(p + step);
@@ -86,7 +85,6 @@ template <> struct V8<float> {
 };
 template <typename T> struct V8 {
   uint4 a;
-  __device__ __forceinline__ void load(const T* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void pieces(const uint8_t* p, int) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float* f) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -208,74 +206,20 @@ __device__ __forceinline__ long long position(const NormArgs& a, uint32_t b, uin
   return a.pos64 ? static_cast<const long long*>(a.pos)[at] : (long long)static_cast<const int*>(a.pos)[at];
 }
 
-template <typename T, int kPairs>
-__global__ void __launch_bounds__(kNThreads) norm_rope_kernel(const NormArgs a) {
+// Both directions.  The rows of q (of k), tile by tile of kNThreads >> lg tokens and
+// in a tile head by head, are shared out evenly over its CTAs.  A thread copies its
+// rows ahead into shared memory that it has to itself (no barriers), so that what is
+// in flight takes no registers.  GPT-2-medium q and k: backward 155 us with two rows in
+// registers, 137 so; forward 93 with four, 87 so (537 MB, 0.90 of the copy
+// rate).  More CTAs are slower: forward 100 us with four or five on an SM.
+template <typename T, int kPairs, bool kBack>
+__global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_kernel(const NormArgs a) {
   using R = Turn<kPairs>;
-  constexpr int HB = sizeof(T) == 4 ? 2 : 4;         // rows whose loads are in flight together
+  using C = NormCfg<T, kPairs, kBack>;
   __shared__ unsigned long long sF[128];
   __shared__ float sM[128];
   __shared__ float rows[kPairs == kShared ? kNThreads * 8 : 8];
-  load_turns(a, sF, sM);
-  const uint32_t t = blockIdx.x * kNThreads + threadIdx.x;
-  const uint32_t token = t >> a.lg;
-  R r;
-  r.place((int)(t & ((1u << a.lg) - 1)), a.rot, a.units, a.d);
-  if (token >= a.tokens) r.live = r.rotates = r.two = false;
-  const uint32_t tk = min(token, a.tokens - 1);
-  const uint32_t b = tk / (uint32_t)a.N, n = tk - b * (uint32_t)a.N;
-  r.angles(position(a, b, n), sF, sM, 1.f);
-  float* row = rows + (kPairs == kShared ? (threadIdx.x >> a.lg << a.lg) * 8 : 0);
-  const int first = blockIdx.y * a.hp;
-#pragma unroll 1
-  for (int v = 0; v < 2; ++v) {                      // q's heads, then k's
-    const int off = v ? a.heads[0] : 0;
-    const int h0 = max(first - off, 0), h1 = min(first + a.hp - off, a.heads[v]);
-    if (h0 >= h1) continue;
-    r.weights(a.w[v]);
-    const Strides xs = a.xs[v], ys = a.ys[v];
-    const T* src = static_cast<const T*>(a.x[v]) + (int64_t)b * xs.b + (int64_t)h0 * xs.h + (int64_t)n * xs.n;
-    T* dst = static_cast<T*>(a.y[v]) + (int64_t)b * ys.b + (int64_t)h0 * ys.h + (int64_t)n * ys.n;
-    for (int h = h0; h < h1; h += HB, src += HB * xs.h, dst += HB * ys.h) {
-      V8<T> v0[HB], v1[HB];
-#pragma unroll
-      for (int j = 0; j < HB; ++j) {
-        if (h + j >= h1) break;
-        if (r.live) v0[j].load(src + j * xs.h + r.c0);
-        if (r.two) v1[j].load(src + j * xs.h + r.c1);
-      }
-#pragma unroll
-      for (int j = 0; j < HB; ++j) {
-        if (h + j >= h1) break;
-        float x[R::NC] = {};
-        if (r.live) v0[j].get(x);
-        if (R::NC > 8 && r.two) v1[j].get(x + (R::NC - 8));
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < R::NC; ++e) s += x[e] * x[e];
-        s = rsqrtf(row_sum(s, a.lg) * a.inv_d + a.eps);
-#pragma unroll
-        for (int e = 0; e < R::NC; ++e) x[e] = x[e] * s * r.w[e];
-        r.apply(x, row);
-        if (r.live) V8<T>::store(dst + j * ys.h + r.c0, x);
-        if (R::NC > 8 && r.two) V8<T>::store(dst + j * ys.h + r.c1, x + (R::NC - 8));
-      }
-    }
-  }
-}
-
-// Backward.  The rows of q (of k), tile by tile of kNThreads >> lg tokens and in a
-// tile head by head, are shared out evenly over its CTAs.  A thread copies its rows
-// ahead into shared memory that it has to itself (no barriers), so that what is in
-// flight takes no registers: 155 us with two rows in registers for GPT-2-medium q and
-// k, 135 so.
-template <typename T, int kPairs>
-__global__ void __launch_bounds__(kNThreads, bwd_ctas_of(kPairs)) norm_rope_bwd_kernel(const NormArgs a) {
-  using R = Turn<kPairs>;
-  using C = BwdCfg<T, kPairs>;
-  __shared__ unsigned long long sF[128];
-  __shared__ float sM[128];
-  __shared__ float rows[kPairs == kShared ? kNThreads * 8 : 8];
-  extern __shared__ __align__(16) uint8_t ahead[];   // [kStages][kPieces][kNThreads] 16-byte pieces
+  extern __shared__ __align__(16) uint8_t ahead[];   // [kStages][kPieces][kNThreads] 16-byte pieces, of x, then of dy
   load_turns(a, sF, sM);
   const int v = (int)blockIdx.x < a.ctas[0] ? 0 : 1;
   const int c = (int)blockIdx.x - (v ? a.ctas[0] : 0);
@@ -310,24 +254,24 @@ __global__ void __launch_bounds__(kNThreads, bwd_ctas_of(kPairs)) norm_rope_bwd_
     const Token t = token_of(ltile);
     lt = t.there;
     lx = static_cast<const T*>(a.x[v]) + (int64_t)t.b * xs.b + (int64_t)lh * xs.h + (int64_t)t.n * xs.n;
-    lg = static_cast<const T*>(a.dy[v]) + (int64_t)t.b * ds.b + (int64_t)lh * ds.h + (int64_t)t.n * ds.n;
+    if (kBack) lg = static_cast<const T*>(a.dy[v]) + (int64_t)t.b * ds.b + (int64_t)lh * ds.h + (int64_t)t.n * ds.n;
   };
   auto copy = [&]() {                                // the next row, into stage ls
     if (left > 0) {
       if (lt) {
         const uint32_t at = slot0 + ls * (C::kPieces * kNThreads * 16);
 #pragma unroll
-        for (int i = 0; i < C::kPieces / 2; ++i) {
-          // pieces of x, then of dy: of the first eight columns, then of the second
+        for (int i = 0; i < C::kRow; ++i) {
+          // of the first eight columns, then of the second
           const int e = i * C::kPer, col = (e < 8 ? all.c0 + e : all.c1 + e - 8);
           if (e < 8 ? all.live : all.two) {
             cp_async16<sizeof(T) == 4>(at + i * (kNThreads * 16), lx + col);
-            cp_async16<sizeof(T) == 4>(at + (C::kPieces / 2 + i) * (kNThreads * 16), lg + col);
+            if (kBack) cp_async16<sizeof(T) == 4>(at + (C::kRow + i) * (kNThreads * 16), lg + col);
           }
         }
       }
       lx += xs.h;
-      lg += ds.h;
+      if (kBack) lg += ds.h;
       if (++lh == heads) {
         lh = 0;
         ++ltile;
@@ -342,7 +286,7 @@ __global__ void __launch_bounds__(kNThreads, bwd_ctas_of(kPairs)) norm_rope_bwd_
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) copy();
   int st = 0;
-  float acc[R::NC] = {};
+  float acc[kBack ? R::NC : 1] = {};
   uint32_t tile = tile0;
   for (int done = 0, h0 = head0; done < count; ++tile, h0 = 0) {
     const Token it = token_of(tile);
@@ -351,13 +295,13 @@ __global__ void __launch_bounds__(kNThreads, bwd_ctas_of(kPairs)) norm_rope_bwd_
     r.live = all.live && it.there;
     r.two = all.two && it.there;
     r.rotates = all.rotates && it.there;
-    r.angles(position(a, it.b, it.n), sF, sM, -1.f);       // the transposed rotation
+    r.angles(position(a, it.b, it.n), sF, sM, kBack ? -1.f : 1.f);       // the transposed rotation, or the rotation
     T* dst = static_cast<T*>(a.y[v]) + (int64_t)it.b * ys.b + (int64_t)h0 * ys.h + (int64_t)it.n * ys.n;
 #pragma unroll 1
     for (int h = h0; h < h1; ++h, dst += ys.h) {
       copy();                                        // over the stage of the row before this one
       cp_async_wait<C::kStages - 1>();
-      float x[R::NC] = {}, g[R::NC] = {};
+      float x[R::NC] = {}, g[kBack ? R::NC : 1] = {};
       const uint8_t* at = ahead + (st * C::kPieces * kNThreads + threadIdx.x) * 16;
       st = st + 1 == C::kStages ? 0 : st + 1;
 #pragma unroll
@@ -366,45 +310,60 @@ __global__ void __launch_bounds__(kNThreads, bwd_ctas_of(kPairs)) norm_rope_bwd_
         V8<T> p;
         p.pieces(at + (e / C::kPer) * (kNThreads * 16), kNThreads * 16);
         p.get(x + e);
-        p.pieces(at + (C::kPieces / 2 + e / C::kPer) * (kNThreads * 16), kNThreads * 16);
-        p.get(g + e);
+        if constexpr (kBack) {
+          p.pieces(at + (C::kRow + e / C::kPer) * (kNThreads * 16), kNThreads * 16);
+          p.get(g + e);
+        }
       }
-      r.apply(g, row);                               // dz
-      float sx = 0.f, sg = 0.f, sx1 = 0.f, sg1 = 0.f;
+      if constexpr (kBack) {
+        r.apply(g, row);                             // dz
+        float sx = 0.f, sg = 0.f, sx1 = 0.f, sg1 = 0.f;
 #pragma unroll
-      for (int e = 0; e < R::NC; e += 2) {
-        float y0, y1;                                // w dz
-        mul2(y0, y1, g[e], g[e + 1], r.w[e], r.w[e + 1]);
-        fma2(sg, sg1, y0, y1, x[e], x[e + 1], sg, sg1);
-        fma2(sx, sx1, x[e], x[e + 1], x[e], x[e + 1], sx, sx1);
-      }
-      sx += sx1;
-      sg += sg1;
-      for (int o = 1 << a.lg >> 1; o > 0; o >>= 1) {
-        sx += __shfl_xor_sync(0xffffffffu, sx, o);
-        sg += __shfl_xor_sync(0xffffffffu, sg, o);
-      }
-      const float rs = rsqrtf(sx * a.inv_d + a.eps);
-      const float k = -rs * (rs * rs * (sg * a.inv_d));   // dx = rs w dz - x rs^3 (g . x) / d
+        for (int e = 0; e < R::NC; e += 2) {
+          float y0, y1;                              // w dz
+          mul2(y0, y1, g[e], g[e + 1], r.w[e], r.w[e + 1]);
+          fma2(sg, sg1, y0, y1, x[e], x[e + 1], sg, sg1);
+          fma2(sx, sx1, x[e], x[e + 1], x[e], x[e + 1], sx, sx1);
+        }
+        sx += sx1;
+        sg += sg1;
+        for (int o = 1 << a.lg >> 1; o > 0; o >>= 1) {
+          sx += __shfl_xor_sync(0xffffffffu, sx, o);
+          sg += __shfl_xor_sync(0xffffffffu, sg, o);
+        }
+        const float rs = rsqrtf(sx * a.inv_d + a.eps);
+        const float k = -rs * (rs * rs * (sg * a.inv_d));   // dx = rs w dz - x rs^3 (g . x) / d
 #pragma unroll
-      for (int e = 0; e < R::NC; e += 2) {
-        float y0, y1;
-        mul2(y0, y1, g[e], g[e + 1], rs, rs);
-        fma2(acc[e], acc[e + 1], y0, y1, x[e], x[e + 1], acc[e], acc[e + 1]);
-        mul2(y0, y1, y0, y1, r.w[e], r.w[e + 1]);
-        fma2(x[e], x[e + 1], x[e], x[e + 1], k, k, y0, y1);
+        for (int e = 0; e < R::NC; e += 2) {
+          float y0, y1;
+          mul2(y0, y1, g[e], g[e + 1], rs, rs);
+          fma2(acc[e], acc[e + 1], y0, y1, x[e], x[e + 1], acc[e], acc[e + 1]);
+          mul2(y0, y1, y0, y1, r.w[e], r.w[e + 1]);
+          fma2(x[e], x[e + 1], x[e], x[e + 1], k, k, y0, y1);
+        }
+      } else {
+        float sx = 0.f, sx1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < R::NC; e += 2) fma2(sx, sx1, x[e], x[e + 1], x[e], x[e + 1], sx, sx1);
+        const float rs = rsqrtf(row_sum(sx + sx1, a.lg) * a.inv_d + a.eps);
+#pragma unroll
+        for (int e = 0; e < R::NC; e += 2) {
+          mul2(x[e], x[e + 1], x[e], x[e + 1], rs, rs);
+          mul2(x[e], x[e + 1], x[e], x[e + 1], r.w[e], r.w[e + 1]);
+        }
+        r.apply(x, row);
       }
       if (r.live) V8<T>::store(dst + r.c0, x);
       if (R::NC > 8 && r.two) V8<T>::store(dst + r.c1, x + (R::NC - 8));
     }
   }
-  if (a.dw[v] == nullptr) return;
+  if (!kBack || a.dw[v] == nullptr) return;
   // the CTA's sums: the groups' partial sums of a column, in the order of the groups
   cp_async_wait<0>();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(ahead);
 #pragma unroll
-  for (int e = 0; e < R::NC; ++e) sums[e * kNThreads + threadIdx.x] = acc[e];
+  for (int e = 0; e < R::NC; ++e) sums[e * kNThreads + threadIdx.x] = acc[kBack ? e : 0];
   __syncthreads();
   if ((int)threadIdx.x >= 1 << a.lg || !all.live) return;
 #pragma unroll
@@ -485,22 +444,14 @@ fa_status check_norm(const fa_norm_rope_params* p) {
   return FA_OK;
 }
 
-fa_status sm_count(int& sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return FA_OK;
-}
-
 // CTAs of q and of k: by their heads, no more than there are tokens' tiles x heads (152 SMs: a workspace's size does
 // not depend on the device)
-void bwd_ctas(const fa_norm_rope_params* p, int (&n)[2]) {
+void norm_ctas(const fa_norm_rope_params* p, bool back, int (&n)[2]) {
   const int heads[2] = {p->H, p->H_kv};
   const int per = kNThreads >> lg_of(units_of(p));
   const long long tiles = ((long long)p->B * p->N + per - 1) / per;
   for (int v = 0; v < 2; ++v) {
-    const long long share = std::max<long long>(1, 152ll * bwd_ctas_of(pairs_of(p)) * heads[v] / (p->H + p->H_kv));
+    const long long share = std::max<long long>(1, 152ll * ctas_of(pairs_of(p), back) * heads[v] / (p->H + p->H_kv));
     n[v] = heads[v] == 0 ? 0 : (int)std::min(share, tiles * heads[v]);
   }
 }
@@ -551,29 +502,14 @@ fa_status fill(const fa_norm_rope_params* p, const void* const (&x)[2], const vo
   return FA_OK;
 }
 
-template <typename T, int kPairs> cudaError_t launch_fwd(NormArgs a, int sms, cudaStream_t s) {
-  const unsigned long long threads = (unsigned long long)a.tokens << a.lg;
-  const unsigned gx = (unsigned)((threads + kNThreads - 1) / kNThreads);
-  const int heads = a.heads[0] + a.heads[1];
-  // split the heads until the grid fills the GPU about twice at 1,024 threads a SM, as in rope.cu
-  const long long want = 2ll * sms * 1024 / kNThreads;
-  int split = (int)std::min<long long>((want + gx - 1) / gx, heads);
-  split = std::min(split, 65535);
-  a.hp = (heads + split - 1) / split;
-  if (a.hp > 4) a.hp = (a.hp + 3) / 4 * 4;          // whole batches of loads
-  split = (heads + a.hp - 1) / a.hp;
-  norm_rope_kernel<T, kPairs><<<dim3(gx, (unsigned)split), kNThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-template <typename T, int kPairs> cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s) {
-  auto kern = norm_rope_bwd_kernel<T, kPairs>;
-  constexpr int bytes = BwdCfg<T, kPairs>::kBytes;
+template <typename T, int kPairs, bool kBack> cudaError_t launch_n(const NormArgs& a, cudaStream_t s) {
+  auto kern = norm_rope_kernel<T, kPairs, kBack>;
+  constexpr int bytes = NormCfg<T, kPairs, kBack>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)(a.ctas[0] + a.ctas[1]), kNThreads, bytes, s>>>(a);
   e = cudaGetLastError();
-  if (e != cudaSuccess || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
+  if (e != cudaSuccess || !kBack || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)(a.d / 8), 2);
   c.blockDim = dim3(1024);
@@ -586,19 +522,22 @@ template <typename T, int kPairs> cudaError_t launch_bwd(const NormArgs& a, cuda
   return cudaLaunchKernelEx(&c, norm_dw_kernel, (const float*)a.part, a.d, a.ctas[0], a.ctas[1], a.dw[0], a.dw[1]);
 }
 
-template <typename T> cudaError_t launch(const NormArgs& a, Pairs m, bool bwd, int sms, cudaStream_t s) {
+template <typename T, bool kBack> cudaError_t launch_t(const NormArgs& a, Pairs m, cudaStream_t s) {
   switch (m) {
-    case kHalves: return bwd ? launch_bwd<T, kHalves>(a, s) : launch_fwd<T, kHalves>(a, sms, s);
-    case kAdjacent: return bwd ? launch_bwd<T, kAdjacent>(a, s) : launch_fwd<T, kAdjacent>(a, sms, s);
-    default: return bwd ? launch_bwd<T, kShared>(a, s) : launch_fwd<T, kShared>(a, sms, s);
+    case kHalves: return launch_n<T, kHalves, kBack>(a, s);
+    case kAdjacent: return launch_n<T, kAdjacent, kBack>(a, s);
+    default: return launch_n<T, kShared, kBack>(a, s);
   }
 }
 
-cudaError_t launch_dt(const fa_norm_rope_params* p, const NormArgs& a, bool bwd, int sms, cudaStream_t s) {
+template <bool kBack> fa_status launch(const fa_norm_rope_params* p, NormArgs& a, void* stream) {
+  norm_ctas(p, kBack, a.ctas);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Pairs m = pairs_of(p);
-  if (p->dtype == FA_DT_F32) return launch<float>(a, m, bwd, sms, s);
-  if (p->dtype == FA_DT_F16) return launch<__half>(a, m, bwd, sms, s);
-  return launch<__nv_bfloat16>(a, m, bwd, sms, s);
+  const cudaError_t e = p->dtype == FA_DT_F32   ? launch_t<float, kBack>(a, m, s)
+                        : p->dtype == FA_DT_F16 ? launch_t<__half, kBack>(a, m, s)
+                                                : launch_t<__nv_bfloat16, kBack>(a, m, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -611,16 +550,14 @@ extern "C" {
 fa_status fa_norm_rope(const fa_norm_rope_params* p, const void* q, const void* k, const float* q_weight,
                        const float* k_weight, void* q_out, void* k_out, void* stream) {
   NormArgs a{};
-  fa_status s = fill(p, {q, k}, {nullptr, nullptr}, {q_out, k_out}, {q_weight, k_weight}, false, a);
-  int sms = 0;
-  if (s != FA_OK || (s = sm_count(sms)) != FA_OK) return s;
-  return launch_dt(p, a, false, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const fa_status s = fill(p, {q, k}, {nullptr, nullptr}, {q_out, k_out}, {q_weight, k_weight}, false, a);
+  return s == FA_OK ? launch<false>(p, a, stream) : s;
 }
 
 size_t fa_norm_rope_bwd_workspace_size(const fa_norm_rope_params* p) {
   if (check_norm(p) != FA_OK) return 256;
   int n[2];
-  bwd_ctas(p, n);
+  norm_ctas(p, true, n);
   return 256 + (size_t)(n[0] + n[1]) * p->d * sizeof(float);
 }
 
@@ -632,12 +569,10 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params* p, const void* q, const vo
   if (s != FA_OK) return s;
   if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) return FA_ERR_MISALIGNED;
   if (ws == nullptr || ws_bytes < fa_norm_rope_bwd_workspace_size(p) || !n16(ws)) return FA_ERR_WORKSPACE;
-  bwd_ctas(p, a.ctas);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
   a.dw[0] = dq_weight;
   a.dw[1] = p->H_kv > 0 ? dk_weight : nullptr;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launch_dt(p, a, true, 0, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch<true>(p, a, stream);
 }
 
 }  // extern "C"

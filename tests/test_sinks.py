@@ -217,7 +217,7 @@ def test_long_rows_are_cut(dtype, d, B, H, Hkv, N):
     lib = fa.load()
     p = fa.make_params(x[0], k=x[1], causal=True, window=200)
     parts = lib.fa_bwd_sinks_workspace_size(ctypes.byref(p), 4) > lib.fa_bwd_workspace_size(ctypes.byref(p))
-    assert parts == (B == 1 or dtype == "f32")
+    assert parts == (B == 1)
     for w, s in ((200, 4), (513, 140)):
         got = run(x, w, s)
         check(got, plain(*x, w, s), dtype)
