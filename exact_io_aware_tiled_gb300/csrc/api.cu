@@ -450,12 +450,16 @@ fa_status check_cache8(const fa_cache8_params* in, fa_cache8_params& p, Cache8St
   if (p.B > 1 && p.table_stride < p.width) return FA_ERR_INVALID_ARG;
   if (p.seqlens_k == nullptr || p.table == nullptr) return FA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(p.seqlens_k) | reinterpret_cast<uintptr_t>(p.table)) & 3u) return FA_ERR_MISALIGNED;
-  if ((double)p.B * p.H * p.T >= (double)(1 << 26) || (long long)p.width * p.page > (1 << 28) ||
-      (long long)p.pages * p.H_kv >= (1ll << 31))
-    return FA_ERR_UNSUPPORTED;
-  // 32-bit units of one sequence: 32 keys of one K/V head and 64 query rows
-  if (!rows && (double)(p.width * p.page / 32 + 1) * p.H_kv * ((p.H / p.H_kv * (long long)p.T + 15) / 16) >= 2147483648.0)
-    return FA_ERR_UNSUPPORTED;
+  const double most = 2147483648.0;
+  if ((long long)p.width * p.page > (1 << 28) || (double)p.pages * p.H_kv >= most) return FA_ERR_UNSUPPORTED;
+  if (rows) {
+    if ((double)p.B * p.H_kv * (p.T / 16 + 2.0) * 2 >= most) return FA_ERR_UNSUPPORTED;      // CTAs
+  } else {
+    if ((double)p.B * p.H * p.T >= (double)(1 << 26)) return FA_ERR_UNSUPPORTED;
+    // 32-bit units (32 keys and up, 16 more for each sequence): of all sequences, and of one over heads and row tiles
+    const double units = p.width * p.page / 32 + 16.0;
+    if (p.B * units >= most || units * p.H_kv * ((double)(p.H / p.H_kv) * p.T / 8 + 1) >= most) return FA_ERR_UNSUPPORTED;
+  }
   s.kc = {p.kc_stride_p, p.kc_stride_h, p.kc_stride_n};
   s.vc = {p.vc_stride_p, p.vc_stride_h, p.vc_stride_n};
   fa_status e;

@@ -185,8 +185,7 @@ __global__ void __launch_bounds__(128) cache8_read_kernel(const Cache8Rows a, in
 
 cudaError_t launch_cache8_append(int dtype, const Cache8Rows& a, cudaStream_t s) {
   const int touched = (a.T + a.page - 2) / a.page + 1;          // pages that T rows can touch
-  const long long grid = 2ll * a.B * a.Hkv * std::min(touched, a.width);
-  if (grid >= 1ll << 31) return cudaErrorInvalidValue;
+  const long long grid = 2ll * a.B * a.Hkv * std::min(touched, a.width);     // < 2^31, here and below (api.cu)
   // threads that hold kHeld pieces each: 2,047 new rows of 4 sequences and 8 heads of 128 in pages of 64 take 9.8 us with
   // 8 pieces a thread, 15 with 4, in pages of 16 9.7 and 15 (one piece: 46)
   const long long pieces = (long long)std::min(a.T, a.page) * a.d / 8;
@@ -200,7 +199,6 @@ cudaError_t launch_cache8_append(int dtype, const Cache8Rows& a, cudaStream_t s)
 cudaError_t launch_cache8_read(int dtype, const Cache8Rows& a, cudaStream_t s) {
   const int chunks = (a.T + kReadRows - 1) / kReadRows;
   const long long grid = 2ll * a.B * a.Hkv * chunks;
-  if (grid >= 1ll << 31) return cudaErrorInvalidValue;
   if (dtype == FA_DT_BF16) cache8_read_kernel<__nv_bfloat16><<<(unsigned)grid, 128, 0, s>>>(a, chunks);
   else cache8_read_kernel<__half><<<(unsigned)grid, 128, 0, s>>>(a, chunks);
   return cudaGetLastError();

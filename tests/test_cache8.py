@@ -84,7 +84,7 @@ ALL = [
     (dict(pages=0), 1), (dict(width=0), 1), (dict(dtype=5), 1), (dict(dtype=0), 2), (dict(d=96), 2), (dict(page=48), 2),
     (dict(page=8), 2), (dict(page=256), 2), (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(table_stride=5), 1),
     (dict(seqlens_k=0), 1), (dict(table=0), 1), (dict(table=(1 << 22) + 2), 3), (dict(seqlens_k=(1 << 22) + 1), 3),
-    (dict(B=1 << 23), 2), (dict(width=1 << 24, table_stride=1 << 24), 2), (dict(pages=1 << 30), 2),
+    (dict(B=1 << 30), 2), (dict(width=1 << 24, table_stride=1 << 24), 2), (dict(pages=1 << 30), 2),
     (dict(kc_stride_n=48), 1), (dict(kc_stride_n=72), 3), (dict(vc_stride_h=2056), 3), (dict(vc_stride_p=0), 1),
 ]
 
@@ -94,6 +94,15 @@ def test_refusals_before_launch(mut, code):
     assert _fwd(_params(**mut)) == code
     for name in ("fa_cache8_append", "fa_cache8_read"):
         assert _rows(name, _params(**mut)) == code
+
+
+def test_limits_of_the_attention():
+    for mut in (dict(B=1 << 23), dict(T=1 << 23), dict(B=300, width=1 << 23, table_stride=1 << 23),
+                dict(H=1 << 13, H_kv=1 << 13, width=1 << 23, table_stride=1 << 23)):
+        p = dict(mut)
+        for t in "qo":
+            p.update({t + "_stride_h": 64 * mut.get("T", 2), t + "_stride_b": 64 * mut.get("T", 2) * mut.get("H", 4)})
+        assert _fwd(_params(**p)) == 2
 
 
 def test_strides_pointers_and_workspace():
