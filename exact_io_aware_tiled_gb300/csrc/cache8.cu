@@ -42,6 +42,12 @@ constexpr int kCThreads = 160;   // warps 0-3 compute, 4 looks up and loads
 constexpr int kItemUnits = 12;
 constexpr int kGroup = 16;       // pieces that are joined at once
 constexpr float kLn2 = 0.6931471805599453f;
+// The weights' sums, weights over V scales, are held times 2^-28, so that scales down to 2^-126, the smallest that
+// rows are written with, leave them finite; scales up to 2^98 leave them normal.
+constexpr float kSum = 0x1p-28f, kSumLog2 = -28.f;
+// A page of zeros may have the scale 0: it counts as 2^-64, so that it does not set the reference that other pages'
+// weights are rounded against, and its weights still reach the sums.
+constexpr float kZeroPage = 0x1p-64f, kZeroPageLog2 = -64.f;
 
 template <int D, int NX> struct CCfg {
   static constexpr int RW = 8 * NX;              // query rows of a warp
@@ -72,7 +78,7 @@ struct CBars {
 static_assert(sizeof(CBars) <= 288, "barrier block overflows its shared-memory slot");
 
 // What the compute warps need of a stage: per 16 keys the K scale, log2 of the V
-// scale and its inverse, and the first key.  A group whose page is absent has the
+// scale and its inverse (times kSum), and the first key.  A group whose page is absent has the
 // factors 0, -inf and 0: its weights are zero.
 struct __align__(16) CInfo { float kf[4], ve[4], vi[4]; int key0, pad[3]; };
 static_assert(sizeof(CInfo) == 64, "a stage's record");
@@ -418,8 +424,8 @@ template <int D, int NX> struct CRows {
   }
 };
 
-// logsumexp, and the factor of O: a row that saw no key has l = 0, one with a NaN in it l = NaN
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + lg2(l)) * kLn2 : l == 0.f ? -INFINITY : l; }
+// logsumexp, and the factor of kSum O: a row that saw no key has l = 0, one with a NaN in it l = NaN
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? ((m - kSumLog2) + lg2(l)) * kLn2 : l == 0.f ? -INFINITY : l; }
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
 // Units before each sequence, by one CTA, for batches whose prefix sums do not fit the kernel's shared memory.
@@ -624,9 +630,8 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
               const float k = g < C::NG ? ks[g < C::NG ? g : 0] : -1.f, v = g < C::NG ? vs[g < C::NG ? g : 0] : -1.f;
               const bool there = g < C::NG && (unsigned)cur.id[g < C::NG ? g : 0] < (unsigned)a.pages;
               inf.kf[g] = there ? k : 0.f;
-              // a page of zeros may have the scale 0: its codes are zero too
-              inf.ve[g] = there ? (v == 0.f ? 0.f : lg2(v)) : -INFINITY;
-              inf.vi[g] = there ? (v == 0.f ? 1.f : 1.f / v) : 0.f;
+              inf.ve[g] = there ? (v == 0.f ? kZeroPageLog2 : lg2(v)) : -INFINITY;
+              inf.vi[g] = there ? kSum / (v == 0.f ? kZeroPage : v) : 0.f;
             }
             inf.key0 = cur.key0;
             *reinterpret_cast<CInfo*>(smem + C::kInfo + st * 64) = inf;
@@ -749,7 +754,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             for (int y = 0; y < D / 64; ++y) {
               uint32_t u[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) u[i] = Cvt<T>::pack(w.o[z][4 * y + i][x] * inv, w.o[z][4 * y + i][2 + x] * inv);
+              for (int i = 0; i < 4; ++i) u[i] = Cvt<T>::pack(w.o[z][4 * y + i][x] * kSum * inv, w.o[z][4 * y + i][2 + x] * kSum * inv);
               reinterpret_cast<uint4*>(dst)[y] = make_uint4(u[0], u[1], u[2], u[3]);
             }
             if (n == 0) a.lse[((size_t)it.b * a.H + h) * a.T + t] = lse_of(w.m[z][x], w.l[z][x]);
@@ -833,7 +838,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const float inv = inverse(l);
         uint32_t u[E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) u[e] = Cvt<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        for (int e = 0; e < E / 2; ++e) u[e] = Cvt<T>::pack(acc[2 * e] * kSum * inv, acc[2 * e + 1] * kSum * inv);
         T* dst = static_cast<T*>(a.o) + (int64_t)it.b * a.os.b + (int64_t)h * a.os.h + (int64_t)t * a.os.n + lane * E;
         if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = u[0];
         else *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);

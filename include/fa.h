@@ -598,8 +598,9 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params *p, const void *q, const vo
  *     and lse -inf.
  *   - Scores from q rounded to 11 bits (exact for both dtypes) and the codes, float32 sums;
  *     weights times their page's V scale are rounded to 11 bits before the product with
- *     the codes, sums and joins are float32.  Any positive scale serves, 0 for a page of
- *     zeros; the V scales of a sequence's pages have to lie within 2^-100 .. 2^100.
+ *     the codes, sums and joins are float32.  K scales: any positive one.  V scales: 2^-126
+ *     .. 2^98, those of a sequence within 2^96 of one another.  0 serves for a page of
+ *     zeros (as a V scale it counts as 2^-64).
  *   - Results repeat bit for bit for the same batch; how the keys are cut follows from all
  *     lengths, so a sequence's last bit may change with the others' lengths.
  *   - Workspace: fa_cache8_workspace_size bytes, 16-byte aligned, independent of the lengths

@@ -6,7 +6,7 @@ bit for bit against a plain form, attention against a 64-bit one.
 Tolerances of the attention.  delta = 2^-19 (1 + tau sum |q k|) bounds a weight's relative error from its score: float32
 products and sums of d terms, the scale's product and the exponent's rounding.  Weights are rounded to 11 bits (2^-11;
 below 2^-14 of the largest by 2^-25 of it), O once more: |error| <= (2^-11 + 2 delta + 2^-20) sum P |v| + u |O| +
-2^-25 sum |code| / sum exp2(s - t_max), t_max the largest s + log2(V scale).  lse: delta + 2^-20 (1 + |lse|).
+2^-25 sum |code| / sum exp2(s - t_max), t_max the largest s + log2(V scale; 2^-64 for a page of zeros).  lse: delta + 2^-20 (1 + |lse|).
 """
 import ctypes
 import math
@@ -338,7 +338,7 @@ def plain_fwd(q, cache, lens, page, window=0, sinks=0, scale=None):
     w = w / l.masked_fill(none, 1.0)
     o, mag = w @ v, w @ v.abs()
     lse = (m + torch.log(l)).squeeze(-1)
-    lv = torch.where(there[:, None] & (vsc > 0), torch.log(vsc.clamp(min=1e-300)), torch.zeros_like(vsc))[:, :, None]
+    lv = torch.where(there[:, None] & (vsc > 0), torch.log(vsc.clamp(min=1e-300)), torch.full_like(vsc, -64 * math.log(2)))[:, :, None]
     tmax = (s + lv).masked_fill(~see, -math.inf).amax(-1, keepdim=True).masked_fill(none, 0.0)
     ell = torch.exp(s - tmax).sum(-1, keepdim=True).masked_fill(none, 1.0)
     small = 2.0 ** -25 * (see.double() @ code.abs()) / ell
@@ -628,6 +628,29 @@ def test_scales_and_ranges(d):
     check(fa.cache8_fwd(q, *cache, ln), plain_fwd(q, cache, ln, 16), "f16")
     q.zero_()
     check(fa.cache8_fwd(q, *cache, ln), plain_fwd(q, cache, ln, 16), "f16")
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("vs", [2.0 ** -126, 2.0 ** -20, 2.0 ** 90])
+def test_zero_pages_and_the_ends_of_the_value_scales(d, vs):
+    # 40 rows of 300 keys, in one CTA and cut: a page of zeros in V whose keys score highest, the others' values small
+    # enough to overflow a plain sum of weights over scales (2^-126) or large
+    for B, Hkv in ((1, 1), (20, 2)):
+        lens = [300] * B
+        cache = make_cache(B, Hkv, d, 16, lens, 19, seed=11)
+        kc, vc, ks, v_scale, table = cache
+        v_scale.fill_(vs)
+        ks.fill_(2.0 ** -8)
+        if vs < 1:
+            zero = table[:, 7].long()
+            vc[zero] = 0
+            v_scale[zero] = 0.0
+            ks[zero] = 2.0 ** -6
+        q = torch.randn(B, 2 * Hkv, 1, d, generator=torch.Generator(device="cuda").manual_seed(12), device="cuda").bfloat16()
+        ln = torch.tensor(lens, device="cuda")
+        got = fa.cache8_fwd(q, *cache, ln)
+        check(got, plain_fwd(q, cache, ln, 16), "bf16")
 
 
 @gpu
