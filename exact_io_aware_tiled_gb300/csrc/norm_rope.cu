@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
           sg += __shfl_xor_sync(0xffffffffu, sg, o);
         }
         const float rs = rsqrtf(sx * a.inv_d + a.eps);
-        const float k = -rs * (rs * rs * (sg * a.inv_d));   // dx = rs w dz - x rs^3 (g . x) / d
+        const float k = -rs * (rs * (rs * (sg * a.inv_d)));  // dx = rs w dz - x rs^3 (g . x) / d; rs^2 alone may overflow
 #pragma unroll
         for (int e = 0; e < R::NC; e += 2) {
           float y0, y1;

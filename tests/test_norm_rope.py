@@ -375,3 +375,13 @@ def test_refusals_of_the_binding():
     for bad in (dict(eps=0.0), dict(mscale=math.inf), dict(inv_freq=fa.rope_frequencies(66)[0])):
         with pytest.raises(fa.FAError):
             fa.norm_rope(q, k, **bad)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_zeros_and_the_smallest_eps(dtype):
+    # 1 / sqrt(eps) = 2^70, whose square passes float32: a row of zeros has the gradient 2^70 w R^T dy, not NaN
+    x = make(2, 3, 1, 9, 64, dtype, 21)
+    for t in x[:2]:
+        t[:, :, ::2] = 0
+    check_both(x, dtype, freqs(64), eps=2.0 ** -140)
