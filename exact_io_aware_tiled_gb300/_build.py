@@ -19,7 +19,7 @@ LIB = PKG / "libfa_gb300.so"
 SOURCES = ["api.cu", "fwd_tc.cu", "fwd_tc1.cu", "bwd_tc.cu", "bwd_tc128.cu", "simt_f32.cu", "aux_kernels.cu",
            "noalloc.cu", "fwd_fp8.cu", "fp8_quant.cu", "rope.cu",
            "diff_fwd.cu", "diff_bwd.cu", "prefix.cu", "prefix_tc.cu", "norm_rope.cu",
-           "cache8.cu", "cache8_rows.cu"]
+           "cache8.cu", "cache8_rows.cu", "sink_few.cu"]
 HEADERS = ["common.cuh", "bwd_items.cuh", "fa_internal.h", "fwd_plan.cuh", "fp8.cuh", "row_softmax.cuh", "prefix.cuh",
            "register_mma.cuh", "rope.cuh", "cache8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

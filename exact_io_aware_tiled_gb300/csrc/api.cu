@@ -40,6 +40,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct SinkPlan {
   int window = 0, sinks = 0;
   int tiles = 0, chunks = 0, steps = 0;
+  int few = 0, few_chunks = 0;   // backward, 16 bits: see BwdArgs
 };
 
 SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
@@ -51,16 +52,25 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
     return k;
   }
   k.sinks = sinks;
-  k.tiles = (sinks + kTile - 1) / kTile;
   const int hkv = p->H_kv == 0 ? p->H : p->H_kv;
   const long long nq = (p->N + kTile - 1) / kTile, g = p->H / hkv, steps = nq * g, heads = (long long)p->B * hkv;
   // An item of a first key tile may take a CTA's whole share of all steps (query tiles at key tiles), as it starts
   // among the first: cutting it further costs more, in dK and dV that go through float32, than it balances.  us,
-  // backward, items of 8 / 16 / 32 steps: 64 heads of 64 x 4,096, window 512, 4 first keys 265 / 256 / 243 (one item
-  // each), 8 x 4 K/V heads x 2,047 with 3 query heads and 150 first keys 147 / 141 / 132; float32, whose blocks are one
-  // warpgroup each and four or more on an SM, 32 heads x 2,048 1,398 / 2,010 / 2,010.  At least 16 steps (float32: 2),
-  // and no more than about four items for each CTA: a part takes 64 KB (d = 128: 128 KB).
+  // backward, items of 8 / 16 / 32 steps: 64 heads of 64 x 4,096, window 512 265 / 256 / 243 (one item each), 8 x 4 K/V
+  // heads x 2,047 with 3 query heads and 150 first keys 147 / 141 / 132; float32, whose blocks are one warpgroup each
+  // and four or more on an SM, 32 heads x 2,048 1,398 / 2,010 / 2,010.  At least 16 steps (float32: 2), and no more than
+  // about four items for each CTA: a part takes 64 KB (d = 128: 128 KB).  Up to kFewSinks first keys of 16 bits go the
+  // way of sink_few.cu instead, with both sides' times.
   const bool f32 = p->dtype == FA_DT_F32;
+  if (!f32 && sinks <= kFewSinks) {
+    // the CTAs of launch_sink_few, 3 (d = 128: 2) on an SM, in one round where that fills 0.7 of it, else in four
+    const long long all = (long long)p->B * p->H, slots = 152 * (p->d == 128 ? 2 : 3);
+    const long long one = slots / all, cut = 10 * one * all >= 7 * slots ? one : (4 * slots + all - 1) / all;
+    k.few = sinks;
+    k.few_chunks = (int)std::max<long long>(1, std::min({cut, nq * kTile / 64, 256 / g}));
+    return k;
+  }
+  k.tiles = (sinks + kTile - 1) / kTile;
   const long long span = std::min<long long>(nq, (p->window + kTile - 1) / kTile + 1);
   const long long share = heads * g * (nq * span + k.tiles * nq) / (f32 ? 4 * 152 : 152);
   const long long least = std::max<long long>(f32 ? 2 : 16, share);
@@ -72,7 +82,7 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
 }
 
 struct Layout {
-  size_t status = 0, rlist = 0, rcnt = 0, clist = 0, ccnt = 0, lse2 = 0, dvec = 0, dqacc = 0, sched = 0, part = 0,
+  size_t status = 0, rlist = 0, rcnt = 0, clist = 0, ccnt = 0, lse2 = 0, dvec = 0, dqacc = 0, sched = 0, part = 0, few = 0,
          total = 0;
   bool sparse = false;
   int nb = 0, nq = 0, npad = 0;
@@ -103,8 +113,12 @@ Layout layout(const fa_params* p, bool bwd, const SinkPlan& sk = SinkPlan()) {
     L.dvec = take(rows * sizeof(float));
     if (p->dtype != FA_DT_F32) L.dqacc = take((size_t)p->B * p->H * p->N * p->d * sizeof(float));
     L.sched = take(sizeof(int));
-    if (sk.chunks > 1)
-      L.part = take((size_t)p->B * (p->H_kv == 0 ? p->H : p->H_kv) * sk.tiles * sk.chunks * kTile * 2 * p->d * sizeof(float));
+    const size_t heads = (size_t)p->B * (p->H_kv == 0 ? p->H : p->H_kv), row = 2 * p->d * sizeof(float);
+    if (sk.chunks > 1) L.part = take(heads * sk.tiles * sk.chunks * kTile * row);
+    if (sk.few > 0) {
+      L.part = take(heads * kFewSinks * row);
+      L.few = take((size_t)p->B * p->H * sk.few_chunks * kFewSinks * row);
+    }
   }
   L.total = off;
   return L;
@@ -609,6 +623,10 @@ fa_status fa_bwd_sinks(const fa_params* p, int32_t sinks, const void* q, const v
   a.sink_chunks = sk.chunks;
   a.sink_steps = sk.steps;
   a.part = reinterpret_cast<float*>(w + L.part);
+  a.few = sk.few;
+  a.few_chunks = sk.few_chunks;
+  a.few_part = reinterpret_cast<float*>(w + L.few);
+  if (sk.few > 0) a.mask.sinks = 0;
   a.dk = dk;
   a.dv = dv;
   a.kst = skv;
@@ -624,9 +642,11 @@ fa_status fa_bwd_sinks(const fa_params* p, int32_t sinks, const void* q, const v
   // with one packed FMA against -tau D), so their dQ, dK products come out
   // scaled; the fp16 and fp32 kernels read D itself.
   const float dscale = p->dtype == FA_DT_BF16 ? -a.scale : 1.f;
-  cudaError_t e = launch_bwd_prep(p->dtype, o, dout, sd, lse, p->B, p->H, p->N, L.npad, p->d,
-                                  reinterpret_cast<float*>(w + L.lse2), reinterpret_cast<float*>(w + L.dvec), dqacc,
-                                  a.sched, dscale, st);
+  float* const lse2 = reinterpret_cast<float*>(w + L.lse2);
+  float* const dvec = reinterpret_cast<float*>(w + L.dvec);
+  cudaError_t e = a.few > 0 ? launch_sink_few(p->dtype, p->d, q, k, v, o, dout, sd, lse, lse2, dvec, dqacc, dscale, a, st)
+                            : launch_bwd_prep(p->dtype, o, dout, sd, lse, p->B, p->H, p->N, L.npad, p->d, lse2, dvec, dqacc,
+                                              a.sched, dscale, st);
   if (e != cudaSuccess) return FA_ERR_CUDA;
   if (p->dtype == FA_DT_F32) {
     ProfScope prof(p, st);
@@ -652,8 +672,9 @@ fa_status fa_bwd_sinks(const fa_params* p, int32_t sinks, const void* q, const v
                     : launch_bwd_tc(p->dtype, mq, mk, mv, mdo, macc, a, st);
     if (e != cudaSuccess) return FA_ERR_CUDA;
   }
-  // bf16: dK comes out scaled
-  if (launch_sink_sum(p->dtype, p->d, a, p->dtype == FA_DT_BF16 ? 1.f : a.scale, st) != cudaSuccess) return FA_ERR_CUDA;
+  const float kscale = p->dtype == FA_DT_BF16 ? 1.f : a.scale;   // bf16: dK comes out scaled
+  if (a.few > 0) return cuda_status(launch_few_finish(p->dtype, p->d, a, kscale, dqacc, dq, sd, st));
+  if (launch_sink_sum(p->dtype, p->d, a, kscale, st) != cudaSuccess) return FA_ERR_CUDA;
   return cuda_status(launch_dq_convert(p->dtype, dqacc, dq, sd, p->B, p->H, p->N, p->d, st));
 }
 

@@ -9,7 +9,7 @@
 //     (agihunt.info, block-sparse paragraph: only nonzero blocks are visited);
 //   * dropout_mask: the keep-mask of the Philox mapping, for tests;
 //   * sink_sum: dK and dV of the first key tiles under a window with sinks, from
-//     the parts that their items left;
+//     the parts that their items left; few_finish: of a few first keys, with dq_convert;
 //   * wait_selftest: the bounded-wait path of the attention kernels, run on
 //     mbarriers that nothing ever arrives at.
 #include <type_traits>
@@ -88,10 +88,10 @@ __global__ void bwd_prep_kernel(const T* __restrict__ o, const T* __restrict__ d
 }
 
 template <typename T>
-__global__ void dq_convert_kernel(const float* __restrict__ acc, T* __restrict__ dq, Strides st, int H, int N,
-                                  int dh, long long nrows) {
+__device__ __forceinline__ void dq_convert(const float* __restrict__ acc, T* __restrict__ dq, Strides st, int H, int N,
+                                           int dh, long long nrows, long long thread) {
   // 8 consecutive elements per thread; rows of dh (64 or 128) columns
-  const long long e = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const long long e = thread * 8;
   if (e >= nrows * dh) return;
   const long long row = e / dh;
   const int c = (int)(e % dh);
@@ -105,6 +105,12 @@ __global__ void dq_convert_kernel(const float* __restrict__ acc, T* __restrict__
   w.z = Cvt<T>::pack(x1.x, x1.y);
   w.w = Cvt<T>::pack(x1.z, x1.w);
   *reinterpret_cast<uint4*>(dq + (size_t)b * st.b + (size_t)h * st.h + (size_t)i * st.n + c) = w;
+}
+
+template <typename T>
+__global__ void dq_convert_kernel(const float* __restrict__ acc, T* __restrict__ dq, Strides st, int H, int N,
+                                  int dh, long long nrows) {
+  dq_convert(acc, dq, st, H, N, dh, nrows, (long long)blockIdx.x * blockDim.x + threadIdx.x);
 }
 
 // blockIdx.y == 0: row lists (kept kv tiles of q tile blockIdx.x);
@@ -241,6 +247,56 @@ cudaError_t launch_sink_sum(int dtype, int d, const BwdArgs& a, float kscale, cu
   if (dtype == FA_DT_F32) sink_sum_kernel<float><<<grid, 256, 0, s>>>(a, d, kscale);
   else if (dtype == FA_DT_F16) sink_sum_kernel<__half><<<grid, 256, 0, s>>>(a, d, kscale);
   else sink_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, d, kscale);
+  return cudaGetLastError();
+}
+
+// Both last steps of the backward pass under kWindowFew: the first blocks, kFewSinks for each K/V head, sum the
+// float32 rows of the first keys (BwdArgs::few_part in the order of query heads and chunks, part) and round once; the
+// others convert dQ.  A launch of its own for the sums took 8 us.
+template <typename T>
+__global__ void __launch_bounds__(256) few_finish_kernel(const BwdArgs a, int d, float kscale, const float* __restrict__ acc,
+                                                         T* __restrict__ dq, Strides st, long long nrows) {
+  const int sums = a.B * a.H_kv * kFewSinks;
+  if ((int)blockIdx.x >= sums) {
+    dq_convert(acc, dq, st, a.H, a.N, d, nrows, (long long)((int)blockIdx.x - sums) * 256 + threadIdx.x);
+    return;
+  }
+  __shared__ float4 sh[256];
+  const int head = (int)blockIdx.x / kFewSinks, r = (int)blockIdx.x % kFewSinks;
+  const Item it = make_item<kWindowFew>(a, head * a.nq);
+  const int per = d >> 1, c = threadIdx.x % per, slice = threadIdx.x / per, slices = 256 / per;   // dK, then dV
+  const size_t step = (size_t)kFewSinks * 2 * d, at = (size_t)r * 2 * d + 4 * c;
+  const int n = a.group * a.few_chunks;
+  const float* from = a.few_part + (size_t)head * n * step + at;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = slice; i < n; i += slices) {
+    const float4 v = *reinterpret_cast<const float4*>(from + i * step);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  sh[threadIdx.x] = s;
+  __syncthreads();
+  if (slice > 0) return;
+  for (int y = 1; y < slices; ++y) {
+    const float4 v = sh[y * per + c];
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  const int y = 4 * c >= d;                             // dV
+  if (it.n > 0) {
+    const float f = y ? 1.f : kscale;
+    const float4 v = *reinterpret_cast<const float4*>(a.part + head * step + at);
+    s.x += v.x * f; s.y += v.y * f; s.z += v.z * f; s.w += v.w * f;
+  }
+  T* dst = static_cast<T*>(y ? a.dv : a.dk) + (size_t)it.b * a.kst.b + (size_t)it.hk * a.kst.h + (size_t)r * a.kst.n + 4 * c - y * d;
+  if (r < a.N) *reinterpret_cast<uint2*>(dst) = make_uint2(Cvt<T>::pack(s.x, s.y), Cvt<T>::pack(s.z, s.w));
+}
+
+cudaError_t launch_few_finish(int dtype, int d, const BwdArgs& a, float kscale, const float* dqacc, void* dq, Strides st,
+                              cudaStream_t s) {
+  const long long nrows = (long long)a.B * a.H * a.N;
+  const unsigned blocks = (unsigned)(a.B * a.H_kv * kFewSinks + (nrows * d / 8 + 255) / 256);
+  if (dtype == FA_DT_BF16) few_finish_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(a, d, kscale, dqacc, (__nv_bfloat16*)dq, st, nrows);
+  else few_finish_kernel<__half><<<blocks, 256, 0, s>>>(a, d, kscale, dqacc, (__half*)dq, st, nrows);
   return cudaGetLastError();
 }
 

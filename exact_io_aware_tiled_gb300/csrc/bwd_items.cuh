@@ -56,6 +56,7 @@ __device__ __forceinline__ Item make_item(const BwdArgs& a, int u) {
   } else {
     bk = u / a.nq;
     it.jt = u - bk * a.nq;
+    if (kWin == kWindowFew && it.jt == 0) it.part = bk;
   }
   it.b = bk / a.H_kv;
   it.hk = bk - it.b * a.H_kv;

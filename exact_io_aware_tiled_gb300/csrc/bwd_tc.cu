@@ -477,7 +477,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     // the same, unscaled and in float32, to the part of an item of a first key tile
     auto store_part = [&](const Item& it, const uint32_t (&kraw)[16], const uint32_t (&vraw)[16]) {
-      float* dst = a.part + (((size_t)it.part * kTile + r) * 2) * 64 + wg * 16;
+      float* dst = a.part + (((size_t)it.part * (kWin == kWindowFew ? kFewSinks : kTile) + r) * 2) * 64 + wg * 16;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         reinterpret_cast<float4*>(dst)[c] =
@@ -747,6 +747,15 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         tc_fence_before();
         store_part(it, kraw, vraw);
       } else if constexpr (kDrop) {
+        if (kWin == kWindowFew && it.part >= 0 && quarter == 0) {
+          uint32_t kraw[16], vraw[16];
+          tmem_ld16(tl + kColDK + wg * 16, kraw);
+          tmem_ld16(tl + kColDV + wg * 16, vraw);
+          tmem_wait_ld();
+          reg_fence16(kraw);
+          reg_fence16(vraw);
+          if (r < kFewSinks) store_part(it, kraw, vraw);
+        }
         uint32_t raw[32];
         tmem_ld16x256b_x8(kv_taddr, raw);
         tmem_wait_ld();
@@ -762,6 +771,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         reg_fence16(vraw);
         tc_fence_before();
         store_dkv(it, kraw, vraw, true);
+        if (kWin == kWindowFew && it.part >= 0 && r < kFewSinks) store_part(it, kraw, vraw);
       }
     }
     if (ok && t > 0) ok = drain_dq(t - 1);
@@ -795,14 +805,16 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
 template <typename T>
 cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
                      const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
-  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.mask.sinks > 0 ? 4 : 0);
+  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.sink_tiles > 0 ? 4 : a.few > 0 ? 8 : 0);
   switch (sel) {
     case 0: return launch_t<T, false, kAllKeys>(q, k, v, dout, dqacc, a, s);
     case 1: return launch_t<T, true, kAllKeys>(q, k, v, dout, dqacc, a, s);
     case 2: return launch_t<T, false, kWindow>(q, k, v, dout, dqacc, a, s);
     case 3: return launch_t<T, true, kWindow>(q, k, v, dout, dqacc, a, s);
     case 6: return launch_t<T, false, kWindowSinks>(q, k, v, dout, dqacc, a, s);
-    default: return launch_t<T, true, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+    case 7: return launch_t<T, true, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+    case 10: return launch_t<T, false, kWindowFew>(q, k, v, dout, dqacc, a, s);
+    default: return launch_t<T, true, kWindowFew>(q, k, v, dout, dqacc, a, s);
   }
 }
 

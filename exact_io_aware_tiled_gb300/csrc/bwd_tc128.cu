@@ -440,7 +440,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
     // the same, unscaled and in float32, to the part of an item of a first key tile
     auto store_part = [&](const Item& it, int half, const uint32_t (&kraw)[16], const uint32_t (&vraw)[16]) {
-      float* dst = a.part + (((size_t)it.part * kTile + r) * 2) * 128 + wg * 32 + half * 16;
+      float* dst = a.part + (((size_t)it.part * (kWin == kWindowFew ? kFewSinks : kTile) + r) * 2) * 128 + wg * 32 + half * 16;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         reinterpret_cast<float4*>(dst)[c] =
@@ -627,6 +627,7 @@ bwd_tc128_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         reg_fence16(vraw);
         if (kWin == kWindowSinks && it.part >= 0) store_part(it, half, kraw, vraw);
         else store_dkv(it, half, kraw, vraw, true);
+        if (kWin == kWindowFew && it.part >= 0 && r < kFewSinks) store_part(it, half, kraw, vraw);
       }
       tc_fence_before();
     }
@@ -661,14 +662,16 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
 template <typename T>
 cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
                      const CUtensorMap& dqacc, const BwdArgs& a, cudaStream_t s) {
-  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.mask.sinks > 0 ? 4 : 0);
+  const int sel = (a.drop.enabled ? 1 : 0) | (a.mask.window > 0 ? 2 : 0) | (a.sink_tiles > 0 ? 4 : a.few > 0 ? 8 : 0);
   switch (sel) {
     case 0: return launch_t<T, false, kAllKeys>(q, k, v, dout, dqacc, a, s);
     case 1: return launch_t<T, true, kAllKeys>(q, k, v, dout, dqacc, a, s);
     case 2: return launch_t<T, false, kWindow>(q, k, v, dout, dqacc, a, s);
     case 3: return launch_t<T, true, kWindow>(q, k, v, dout, dqacc, a, s);
     case 6: return launch_t<T, false, kWindowSinks>(q, k, v, dout, dqacc, a, s);
-    default: return launch_t<T, true, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+    case 7: return launch_t<T, true, kWindowSinks>(q, k, v, dout, dqacc, a, s);
+    case 10: return launch_t<T, false, kWindowFew>(q, k, v, dout, dqacc, a, s);
+    default: return launch_t<T, true, kWindowFew>(q, k, v, dout, dqacc, a, s);
   }
 }
 

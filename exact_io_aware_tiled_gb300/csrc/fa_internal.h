@@ -15,7 +15,10 @@ constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 constexpr int kTile = 128;       // query rows (and key rows) per tile
 
 // Which keys a query sees of those before it: all, a window's, or a window's and the first ones.
-enum WindowKind { kAllKeys = 0, kWindow = 1, kWindowSinks = 2 };
+// In the backward kernels kWindowFew is a window's pairs alone, whose first kFewSinks keys' dK and dV are also left in
+// float32: launch_sink_few has taken their other pairs.
+enum WindowKind { kAllKeys = 0, kWindow = 1, kWindowSinks = 2, kWindowFew = 3 };
+constexpr int kFewSinks = 8;
 
 struct Strides { int64_t b, h, n; };
 
@@ -102,6 +105,10 @@ struct BwdArgs {
   // launch_sink_sum
   int sink_tiles, sink_chunks, sink_steps;
   float* part;                // [B*H_kv][sink_tiles][sink_chunks][128][2][d]
+  // few > 0 (first keys, at most kFewSinks, and then mask.sinks = sink_tiles = 0): launch_sink_few takes their pairs
+  // behind the window, the backward kernel the window's, and part is [B*H_kv][kFewSinks][2][d]
+  int few, few_chunks;
+  float* few_part;            // [B*H][few_chunks][kFewSinks][2][d]: dK (times tau), dV
 };
 
 // Differential attention: head pair h of H has score maps 2h and 2h + 1.
@@ -165,6 +172,13 @@ cudaError_t launch_bwd_simt(const float* q, const float* k, const float* v, cons
 cudaError_t launch_bwd_prep(int dtype, const void* o, const void* dout, Strides st, const float* lse,
                             int B, int H, int N, int npad, int d, float* lse2, float* dvec, float* dqacc,
                             int* sched, float dscale, cudaStream_t s);
+// launch_bwd_prep and the gradients of a few first keys' pairs behind the window (BwdArgs::few), in one pass.
+cudaError_t launch_sink_few(int dtype, int d, const void* q, const void* k, const void* v, const void* o, const void* dout,
+                            Strides st, const float* lse, float* lse2, float* dvec, float* dqacc, float dscale,
+                            const BwdArgs& a, cudaStream_t s);
+// dQ converted, and dK, dV of a few first keys: the sums of part (dK times kscale) and few_part.
+cudaError_t launch_few_finish(int dtype, int d, const BwdArgs& a, float kscale, const float* dqacc, void* dq, Strides st,
+                              cudaStream_t s);
 // dK, dV of the first key tiles: the sums of their items' parts, in order, dK times kscale.
 cudaError_t launch_sink_sum(int dtype, int d, const BwdArgs& a, float kscale, cudaStream_t s);
 // dq = dqacc (already scaled) cast to dtype with strides.

@@ -181,8 +181,9 @@ fa_status fa_bwd(const fa_params *p, const void *q, const void *k, const void *v
  * call, and without a window sinks change nothing.  Whole K/V tiles between the
  * first keys and the window are skipped, in both directions.
  * Every query tile sees the first key tiles.  The backward pass cuts their
- * items along the queries; the pieces' dK and dV lie in float32 in the workspace
- * (fa_bwd_sinks_workspace_size bytes) and are summed in a fixed order.
+ * items along the queries, or, up to 8 first keys of 16 bits, takes their pairs
+ * behind the window in a pass of its own; the pieces' dK and dV lie in float32 in
+ * the workspace (fa_bwd_sinks_workspace_size bytes) and are summed in a fixed order.
  * ------------------------------------------------------------------------- */
 fa_status fa_fwd_sinks(const fa_params *p, int32_t sinks, const void *q, const void *k, const void *v, void *o,
                        float *lse, void *ws, size_t ws_bytes, void *stream);

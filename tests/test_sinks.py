@@ -56,8 +56,9 @@ def test_workspaces():
     p = _params(causal=1, window=300, N=n, stride_h=n * 64, stride_b=3 * n * 64)
     plain = lib.fa_bwd_workspace_size(ctypes.byref(p))
     assert size(p, 0) == plain and size(p, -3) == plain and size(p, n) == plain
-    # 40 query tiles of a first key tile: items of 16 of them for each of the 6 heads
-    assert size(p, 4) >= plain + 6 * 3 * T * 2 * 64 * 4
+    # 40 query tiles of a first key tile: items of 16 of them for each of the 6 heads; few first keys: their rows
+    assert size(p, 9) >= plain + 6 * 3 * T * 2 * 64 * 4
+    assert plain + 6 * 2 * 8 * 2 * 64 * 4 <= size(p, 4) <= plain + (6 + 456) * 8 * 2 * 64 * 4 + 512
     assert _both(p, 4, ws=plain)[1] == 4
     assert size(_params(causal=1, window=0), 4) == lib.fa_bwd_workspace_size(ctypes.byref(_params()))
     # however many the first keys and heads, the pieces stay within about 1,216
@@ -191,7 +192,7 @@ KINDS = [("bf16", 64), ("f16", 64), ("f32", 64), ("bf16", 128), ("f16", 128)]
 @pytest.mark.parametrize("dtype,d", KINDS)
 @pytest.mark.parametrize("N,w,s", [(2, 1, 1), (100, 10, 3), (128, 64, 4), (129, 128, 1), (300, 1, 1), (300, 64, 4),
                                    (300, 200, 130), (513, 129, 128), (700, 100, 129), (700, 2, 300), (640, 128, 256),
-                                   (1000, 999, 1), (1000, 300, 999), (1500, 17, 1)])
+                                   (1000, 999, 1), (1000, 300, 999), (1500, 17, 1), (1500, 40, 8), (1500, 40, 9), (2050, 129, 2), (135, 130, 4)])
 def test_lengths_windows_and_first_keys(dtype, d, N, w, s):
     x = make(2, 3, 3, N, d, dtype, N + w + s)
     check(run(x, w, s), plain(*x, w, s), dtype)
@@ -216,9 +217,9 @@ def test_long_rows_are_cut(dtype, d, B, H, Hkv, N):
     x = make(B, H, Hkv, N, d, dtype, 7)
     lib = fa.load()
     p = fa.make_params(x[0], k=x[1], causal=True, window=200)
-    parts = lib.fa_bwd_sinks_workspace_size(ctypes.byref(p), 4) > lib.fa_bwd_workspace_size(ctypes.byref(p))
+    parts = lib.fa_bwd_sinks_workspace_size(ctypes.byref(p), 9) > lib.fa_bwd_workspace_size(ctypes.byref(p))
     assert parts == (B == 1)
-    for w, s in ((200, 4), (513, 140)):
+    for w, s in ((200, 4), (513, 140), (300, 8), (300, 9)):
         got = run(x, w, s)
         check(got, plain(*x, w, s), dtype)
         again = run(x, w, s)
