@@ -15,9 +15,9 @@
 // What bounds it: HBM, one byte for each coordinate of a visible key and value,
 // read once for all G T query rows of a K/V head.  Measured: 64 sequences of 1 to
 // 8,191 keys, 16 heads of 64 (537 MB) 97 us, 5.5 TB/s (0.81 of the copy rate); 8 heads
-// of 128, 101 us; 6 sequences of 5 tokens and 12 heads, window 4,096 of up to 23,400
-// keys (32 MB) 15 us, of which 4 are the lengths', pages' and scales' latencies before
-// the first keys and 5 the joins behind the last.
+// of 128, 99 us; 8 query heads a K/V head 101 and 105 us; 6 sequences of 5 tokens and 12
+// heads, window 4,096 of up to 23,400 keys (32 MB) 17 us with the counters' clearing: 4
+// are the lengths', pages' and scales' latencies before the first keys, 5 the joins.
 //
 // Work.  The 64-key (d = 128: 32-key) units that the batch's rows see, sequence by
 // sequence and K/V head by K/V head, form one line; every persistent CTA takes an
@@ -39,8 +39,13 @@ namespace fa {
 namespace {
 
 constexpr int kCThreads = 160;   // warps 0-3 compute, 4 looks up and loads
+// What a CTA spends on a sequence's rows of a K/V head besides their keys, in units.  us with 0 / 6 / 12 / 16: 64
+// sequences of up to 8,191 keys 123 / 97 / 97 / 98, 300 of up to 2,047 193 / 132 / 131 / 137, 8 of 16,384 with 4
+// heads 29 / 27 / 25 / 24, the window above 21 / 17 / 17 / 17.
 constexpr int kItemUnits = 12;
-constexpr int kGroup = 16;       // pieces that are joined at once
+// Pieces that are joined at once; 32 against 16: 102 against 98 us, 8 heads of 128 125 against 101, one head of
+// 131,072 keys 38 against 26.
+constexpr int kGroup = 16;
 constexpr float kLn2 = 0.6931471805599453f;
 // The weights' sums, weights over V scales, are held times 2^-28, so that scales down to 2^-126, the smallest that
 // rows are written with, leave them finite; scales up to 2^98 leave them normal.
@@ -61,7 +66,7 @@ template <int D, int NX> struct CCfg {
   static constexpr int kJoin = 2 * NS * kTile;   // [2][RW][D] O and [2][RW] statistics of two warps
   static constexpr int kInfo = kJoin + 2 * RW * (D * 4 + 8);
   static constexpr int kPre = kInfo + NS * 64;
-  static constexpr int kItem = kPre + (kPreMax + 4) * 4;
+  static constexpr int kItem = kPre + (kPreMax + 4) * 8;
   static constexpr int kBar = kItem + 256;
   static constexpr int kBytes = kBar + 288;
 };
@@ -428,11 +433,11 @@ template <int D, int NX> struct CRows {
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? ((m - kSumLog2) + lg2(l)) * kLn2 : l == 0.f ? -INFINITY : l; }
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
-// Units before each sequence, by one CTA, for batches whose prefix sums do not fit the kernel's shared memory.
+// Units of the line, and sequences with keys, before each sequence, by one CTA, for batches whose prefix sums do not fit the kernel's shared memory.
 template <int KS> __global__ void __launch_bounds__(1024) cache8_plan_kernel(const Cache8Args a) {
-  __shared__ int warps[32];
+  __shared__ int2 warps[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int carry = 0;
+  int2 carry = make_int2(0, 0);
   for (int b0 = 0; b0 < a.B; b0 += 1024) {
     const int b = b0 + threadIdx.x;
     const int n = b < a.B ? units_of<KS>(a, length_of(a, b)).line() : 0;
@@ -442,15 +447,16 @@ template <int KS> __global__ void __launch_bounds__(1024) cache8_plan_kernel(con
       const int up = __shfl_up_sync(0xffffffffu, s, y);
       if (lane >= y) s += up;
     }
-    if (lane == 31) warps[warp] = s;
+    const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+    if (lane == 31) warps[warp] = make_int2(s, __popc(some));
     __syncthreads();
-    int before = carry, all = 0;
+    int2 before = carry;
     for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += warps[w];
-      all += warps[w];
+      if (w < warp) { before.x += warps[w].x; before.y += warps[w].y; }
+      carry.x += warps[w].x;
+      carry.y += warps[w].y;
     }
-    if (b < a.B) a.pre[b] = before + s - n;
-    carry += all;
+    if (b < a.B) a.pre[b] = make_int2(before.x + s - n, before.y + __popc(some & ((1u << lane) - 1u)));
     __syncthreads();
   }
   if (threadIdx.x == 0) a.pre[a.B] = carry;
@@ -468,7 +474,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     return;
   }
   CBars* bars = reinterpret_cast<CBars*>(smem + C::kBar);
-  int* const own = reinterpret_cast<int*>(smem + C::kPre);
+  int2* const own = reinterpret_cast<int2*>(smem + C::kPre);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtl ctl{a.status, &bars->abort, kWaitSleepNs};
   if (threadIdx.x == 0) {
@@ -487,9 +493,9 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
   }
   __syncthreads();
   // ---- units before each sequence: warp 4, whose copies wait for them, sums them; the others meet it behind that
-  const int* pre = a.B <= kPreMax ? own : a.pre;
+  const int2* pre = a.B <= kPreMax ? own : a.pre;
   if (warp == 4 && a.B <= kPreMax) {
-    int carry = 0;
+    int2 carry = make_int2(0, 0);
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int L = b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
       const int n = units_of<KS>(a, L).line();
@@ -499,8 +505,10 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const int up = __shfl_up_sync(0xffffffffu, s, y);
         if (lane >= y) s += up;
       }
-      if (b0 + lane < a.B) own[b0 + lane] = carry + s - n;
-      carry += __shfl_sync(0xffffffffu, s, 31);
+      const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+      if (b0 + lane < a.B) own[b0 + lane] = make_int2(carry.x + s - n, carry.y + __popc(some & ((1u << lane) - 1u)));
+      carry.x += __shfl_sync(0xffffffffu, s, 31);
+      carry.y += __popc(some);
     }
     if (lane == 0) own[a.B] = carry;
     __syncwarp();
@@ -509,21 +517,49 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
   else named_bar_sync(1, kCThreads);
   const int HS = a.Hkv * a.tiles;
   Share sh;
-  const long long X = (long long)pre[a.B] * HS;
+  const long long X = (long long)pre[a.B].x * HS;
   sh.cut(X, (int)max(1ll, min((long long)gridDim.x, X)));
   const int me = blockIdx.x;
   const long long xb = me < sh.C ? sh.begin(me) : sh.X, xe = me < sh.C ? sh.begin(me + 1) : sh.X;
 
   if (warp == 4) {
     // ===================== pages, scales and TMA =====================
-    if (xb >= xe && lane == 0) {
-      reinterpret_cast<CItem*>(smem + C::kItem)->nt = -1;
-      mbar_arrive(&bars->item_full[0]);
-    }
-    if (xb >= xe) return;
     if (lane == 0) {
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
+    }
+    // the keys' units (without the kItemUnits in front of each sequence's rows) before sequence b
+    auto real = [&](int b) -> long long { return (long long)(pre[b].x - kItemUnits * pre[b].y) * HS; };
+    // ... and before unit x of the line; the last sequence that begins at or before it has keys.  The CTA's key units
+    // are rb .. re - 1, of sequences bb .. be.
+    long long rb = real(a.B), re = rb;
+    int bb = 0, be = a.B - 1;
+    if (xb < sh.X) {
+      const long long x = lane & 1 ? xe : xb;        // lanes side by side, for both ends
+      int lo = 0, hi = a.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)pre[mid].x * HS <= x) lo = mid; else hi = mid;
+      }
+      const int line = pre[lo + 1].x - pre[lo].x;
+      const unsigned y = (unsigned)(x - (long long)pre[lo].x * HS), seg = line > 0 ? y / (unsigned)line : 0u;    // < 2^31 (api.cu)
+      const long long r = real(lo) + (line > 0 ? (long long)seg * (line - kItemUnits) +
+                                                     max(0, (int)(y - seg * (unsigned)line) - kItemUnits) : 0);
+      rb = __shfl_sync(0xffffffffu, r, 0);
+      bb = __shfl_sync(0xffffffffu, lo, 0);
+      re = __shfl_sync(0xffffffffu, r, 1);
+      be = __shfl_sync(0xffffffffu, lo, 1);
+      if (xe == sh.X) {
+        re = real(a.B);
+        be = a.B - 1;
+      }
+    }
+    if (rb >= re) {
+      if (lane == 0) {
+        reinterpret_cast<CItem*>(smem + C::kItem)->nt = -1;
+        mbar_arrive(&bars->item_full[0]);
+      }
+      return;
     }
     // one stage a lane
     struct Look {
@@ -531,33 +567,31 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
       bool real, first;      // a stage; the first one of its rows in this CTA
       int key0, id[C::NG];
     };
-    auto look = [&](long long x, Look& k) {
+    auto look = [&](long long x, Look& k) {          // key unit x
       k.key0 = 0;
       k.real = k.first = false;
 #pragma unroll
       for (int g = 0; g < C::NG; ++g) k.id[g] = -1;
-      if (x >= xe) return;
-      int lo = 0, hi = a.B;                  // the sequence of unit x
+      if (x >= re) return;
+      int lo = bb, hi = be + 1;              // the sequence of unit x
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)pre[mid] * HS <= x) lo = mid; else hi = mid;
+        if (real(mid) <= x) lo = mid; else hi = mid;
       }
       const int L = length_of(a, lo);
       const Units un = units_of<KS>(a, L);
-      const long long x0 = (long long)pre[lo] * HS;
-      const unsigned y = (unsigned)(x - x0), seg = y / (unsigned)un.line();                  // < 2^31 (api.cu)
-      const int i = (int)(y - seg * (unsigned)un.line()) - kItemUnits;
-      if (i < 0) return;
-      const long long s0 = x - i;
+      const unsigned y = (unsigned)(x - real(lo)), seg = y / (unsigned)un.n;
+      const int i = (int)(y - seg * (unsigned)un.n);
+      const long long s0 = (long long)pre[lo].x * HS + (long long)seg * un.line() + kItemUnits;
       k.it.b = lo;
       k.it.hk = (int)seg / a.tiles;
       k.it.rt = (int)seg - k.it.hk * a.tiles;
       k.it.L = L;
-      k.it.nt = (int)(min(s0 + un.n, xe) - x);
+      k.it.nt = (int)min((long long)(un.n - i), re - x);
       k.it.n = un.n;
       k.it.s0 = s0;
       k.real = true;
-      k.first = i == 0 || x == xb;
+      k.first = i == 0 || x == rb;
       k.key0 = (i < un.ns ? i : i + un.skip) * KS;
       const int32_t* row = a.table + (int64_t)lo * a.table_stride;
 #pragma unroll
@@ -581,14 +615,14 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     const int rows = min(a.page, KS), boxes = KS / rows;
     const uint32_t box = (uint32_t)rows * D;
     Look cur, nxt;
-    look(xb + lane, cur);
+    look(rb + lane, cur);
     scales(cur);
     int kf = 0;                              // items published
     bool ok = true;
     int g0 = 0;                              // stages loaded
-    for (long long x = xb; x < xe && ok; x += 32) {
+    for (long long x = rb; x < re && ok; x += 32) {
       // the next 32 stages' pages are looked up while these are on their way
-      const int cnt = (int)min(32ll, xe - x);
+      const int cnt = (int)min(32ll, re - x);
       // Four lanes issue their stages side by side: a stage is a chain of some 600 cycles in its lane.  Their items
       // find room in the mailbox, whose eight slots outlast what two batches can publish: the oldest of the eight
       // was published two batches ago, and all stages before it are loaded.
@@ -661,7 +695,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
   // ===================== compute warps =====================
   // sequences without keys
   for (int b = me; b < a.B; b += gridDim.x) {
-    if (pre[b + 1] > pre[b]) continue;
+    if (pre[b + 1].x > pre[b].x) continue;
     for (int i = threadIdx.x; i < a.H * a.T * (D / 8); i += 128) {
       const int row = i / (D / 8), h = row / a.T, t = row - h * a.T;
       T* dst = static_cast<T*>(a.o) + (int64_t)b * a.os.b + (int64_t)h * a.os.h + (int64_t)t * a.os.n + (i % (D / 8)) * 8;
@@ -874,7 +908,7 @@ CLayout clayout(int rows, int d, int B) {
   L.stat = al256(L.count + 3 * kCMax * sizeof(int));
   L.part = L.stat + al256(n * sizeof(float2));
   L.pre = L.part + al256(n * d * sizeof(float));
-  L.total = L.pre + (B > kPreMax ? al256(((size_t)B + 1) * sizeof(int)) : 0);
+  L.total = L.pre + (B > kPreMax ? al256(((size_t)B + 1) * sizeof(int2)) : 0);
   return L;
 }
 
@@ -916,7 +950,7 @@ cudaError_t launch_cache8_fwd(int dtype, int d, const CUtensorMap& mk, const CUt
   a.count = reinterpret_cast<int*>(ws + L.count);
   a.stat = reinterpret_cast<float2*>(ws + L.stat);
   a.part = reinterpret_cast<float*>(ws + L.part);
-  a.pre = reinterpret_cast<int*>(ws + L.pre);
+  a.pre = reinterpret_cast<int2*>(ws + L.pre);
   cudaError_t e = cudaMemsetAsync(ws, 0, L.count + 3 * kCMax * sizeof(int), s);
   if (e != cudaSuccess) return e;
   using B16 = __nv_bfloat16;

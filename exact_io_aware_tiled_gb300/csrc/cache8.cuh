@@ -38,11 +38,14 @@ struct Cache8Args {
   int* count;                  // [3 kCMax], cleared: pieces left of a group, and groups joined, of rows that were cut
   float2* stat;                // [2 kCMax][tile]: maximum (log2), sum
   float* part;                 // [2 kCMax][tile][D] unnormalised O
-  int* pre;                    // [B + 1] units before each sequence, where the kernel does not sum them itself
+  int2* pre;                   // [B + 1] before each sequence: units of the line, sequences with keys, where the
+                               // kernel does not sum them itself
 };
 
 constexpr int kCMax = 152 * 3;   // CTAs at most: a workspace's size does not depend on the device at hand
-constexpr int kPreMax = 384;     // sequences whose units a CTA sums by itself
+// Sequences whose units a CTA sums by itself, as many as its shared memory has room for: 300 sequences of up to 2,047
+// keys took 133.5 us so (where 384 fit) and 135 with the kernel that sums them first.
+constexpr int kPreMax = 192;
 
 size_t cache8_workspace(const fa_cache8_params* p);
 // mk, mv: 4-D byte maps (d, page, Hkv, pages) of the codes, boxes of d x min(page, 64 at d = 64, 32 at d = 128)

@@ -238,11 +238,12 @@ def test_dropout(dtype, d):
     kw = dict(dropout_p=p, seed=11, offset=3)
     for w, s in ((100, 5), (30, 150)):
         check(run(x, w, s, **kw), plain(*x, w, s, keep=keep[None], p_drop=p), dtype, drop=True)
-    # long enough for several items
+    # long enough for several items of the first key tile, and for several CTAs of few first keys
     N = 2500
     x = make(1, 1, 1, N, d, dtype, 10)
     keep = fa.dropout_mask(1, 1, N, 0, 0, 0, N, dropout_p=p, seed=11, offset=3)
-    check(run(x, 100, 5, **kw), plain(*x, 100, 5, keep=keep[None, None], p_drop=p), dtype, drop=True)
+    for s in (5, 20):
+        check(run(x, 100, s, **kw), plain(*x, 100, s, keep=keep[None, None], p_drop=p), dtype, drop=True)
 
 
 @gpu
