@@ -4,7 +4,9 @@ The computation lives in ``libfa_gb300.so`` (C ABI: include/fa.h): a
 tcgen05/TMA/TMEM forward and backward kernel for bf16/fp16, an E4M3 (FP8)
 forward with its quantiser, CUDA-core kernels for float32, rotary positions,
 differential attention (forward and backward), attention over a shared prefix
-with caches, and small HBM-bound helper kernels.  This package is a thin
+with caches, norms of q and k with the rotation and their gradients, a sliding
+window with first keys that stay visible, a paged cache in 8 bits with the
+attention that reads it, and small HBM-bound helper kernels.  This package is a thin
 ctypes binding plus the seeded synthetic workload generators.
 """
 from ._lib import (FAError, bwd, check_status, dropout_mask, fwd, load, make_params,  # noqa: F401

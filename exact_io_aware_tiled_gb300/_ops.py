@@ -1,6 +1,6 @@
 """ctypes binding of the operators around the attention passes (include/fa.h,
-ABI 1.4): rotary positions, differential attention, attention over a shared
-prefix.
+ABI 1.5): rotary positions, norms with the rotation, differential attention,
+attention over a shared prefix.
 
 As in ``_lib``: argument checks, output and workspace allocation with torch,
 raw pointers and the stream; the computation runs in ``libfa_gb300.so``.
