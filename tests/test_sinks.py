@@ -147,6 +147,26 @@ def plain(q, k, v, do, w, s, lens=None, keep=None, p_drop=0.0, blocks=None, scal
             (Pt.transpose(-1, -2) @ dd).sum(2))
 
 
+def test_the_form_against_differences():
+    # central differences of sum O dO with steps of 1e-6: rounding 2^-53 x 100 / 1e-6, the step's square below it
+    g = torch.Generator().manual_seed(1)
+    r = lambda h: torch.randn(2, h, 9, 8, generator=g, dtype=torch.float64)  # noqa: E731
+    q, do = r(4), r(4)
+    k, v = r(2), r(2)
+    lens = torch.tensor([9, 6])
+    keep = torch.rand(2, 4, 9, 9, generator=g) > 0.3
+    for kw in (dict(lens=lens), dict(keep=keep, p_drop=0.3), dict(scale=0.7)):
+        grads = plain(q, k, v, do, 3, 2, **kw)[3:]
+        for n, t in enumerate((q, k, v)):
+            u = torch.randn(t.shape, generator=g, dtype=torch.float64)
+            o = []
+            for e in (1e-6, -1e-6):
+                x = [q, k, v]
+                x[n] = t + e * u
+                o.append((plain(*x, do, 3, 2, **kw)[0] * do).sum())
+            assert abs(float((o[0] - o[1]) / 2e-6 - (grads[n] * u).sum())) < 1e-7
+
+
 def rel(a, b):
     n = float(b.norm())
     return float((a.double() - b).norm()) / n if n else float(a.double().norm())
