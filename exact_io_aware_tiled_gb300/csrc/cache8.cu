@@ -16,7 +16,7 @@
 // read once for all G T query rows of a K/V head.  Measured: 64 sequences of 1 to
 // 8,191 keys, 16 heads of 64 (537 MB) 97 us, 5.5 TB/s (0.81 of the copy rate); 8 heads
 // of 128, 99 us; 8 query heads a K/V head 101 and 105 us; 6 sequences of 5 tokens and 12
-// heads, window 4,096 of up to 23,400 keys (32 MB) 17 us with the counters' clearing: 4
+// heads, window 4,096 of up to 23,400 keys (32 MB) 16 us with the counters' clearing: 4
 // are the lengths', pages' and scales' latencies before the first keys, 5 the joins.
 //
 // Work.  The 64-key (d = 128: 32-key) units that the batch's rows see, sequence by
@@ -25,7 +25,7 @@
 // lie in one CTA leave O and the logsumexp; where they are cut, the CTAs leave
 // partial rows in float32 and the last one to finish joins them in their order.
 // The lengths stay on the device: each CTA sums the units itself (above kPreMax
-// sequences a small kernel does).  In a CTA warp 4 looks up pages and scales a
+// sequences the small kernel that clears the counters does).  In a CTA warp 4 looks up pages and scales a
 // stage a lane, 32 stages ahead, and streams codes with TMA; warps 0-3 take 8 or 16
 // rows each: a tile of 8 or 16 / 32 / 64 rows is split into 1 / 2 / 4 row groups, the
 // stages among 4 / 2 / 1 key groups, which join at the end of their rows.
@@ -433,11 +433,16 @@ template <int D, int NX> struct CRows {
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? ((m - kSumLog2) + lg2(l)) * kLn2 : l == 0.f ? -INFINITY : l; }
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
-// Units of the line, and sequences with keys, before each sequence, by one CTA, for batches whose prefix sums do not fit the kernel's shared memory.
+// Clears the status word and the counters, and, for batches whose prefix sums do not fit the kernel's shared memory,
+// sums the units of the line, and the sequences with keys, before each sequence.  One CTA.
 template <int KS> __global__ void __launch_bounds__(1024) cache8_plan_kernel(const Cache8Args a) {
   __shared__ int2 warps[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int2 carry = make_int2(0, 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) *a.status = 0;
+  for (int i = threadIdx.x; i < 3 * kCMax; i += blockDim.x) a.count[i] = 0;
+  if (a.B <= kPreMax) return;
   for (int b0 = 0; b0 < a.B; b0 += 1024) {
     const int b = b0 + threadIdx.x;
     const int n = b < a.B ? units_of<KS>(a, length_of(a, b)).line() : 0;
@@ -470,6 +475,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
   constexpr int NS = C::NS, KS = C::KS, RW = C::RW;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {       // the swizzled tiles: see diff_fwd.cu
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) atomicExch(a.status, (int)FA_ERR_CUDA);
     return;
   }
@@ -492,6 +498,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     fence_mbar_init();
   }
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- units before each sequence: warp 4, whose copies wait for them, sums them; the others meet it behind that
   const int2* pre = a.B <= kPreMax ? own : a.pre;
   if (warp == 4 && a.B <= kPreMax) {
@@ -921,14 +928,24 @@ cudaError_t launch_n(const CUtensorMap& mk, const CUtensorMap& mv, const Cache8A
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if (a.B > kPreMax) {
-    cache8_plan_kernel<C::KS><<<1, 1024, 0, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
+  // Both launches begin over the end of the kernel before them (griddepcontrol.wait): about 1 us less than a clear and
+  // a plain launch.
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(1);
+  c.blockDim = dim3(a.B > kPreMax ? 1024 : 256);
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&c, cache8_plan_kernel<C::KS>, a)) != cudaSuccess) return e;
   const long long most = (long long)a.B * a.Hkv * a.tiles * ((a.cap + C::KS - 1) / C::KS);
   const unsigned grid = (unsigned)std::min<long long>(std::max<long long>(most, 1), std::min(kCMax, C::kCtas * std::max(sms, 1)));
-  kern<<<grid, kCThreads, C::kBytes, s>>>(mk, mv, a);
-  return cudaGetLastError();
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(kCThreads);
+  c.dynamicSmemBytes = C::kBytes;
+  return cudaLaunchKernelEx(&c, kern, mk, mv, a);
 }
 
 template <typename T, int D>
@@ -951,8 +968,6 @@ cudaError_t launch_cache8_fwd(int dtype, int d, const CUtensorMap& mk, const CUt
   a.stat = reinterpret_cast<float2*>(ws + L.stat);
   a.part = reinterpret_cast<float*>(ws + L.part);
   a.pre = reinterpret_cast<int2*>(ws + L.pre);
-  cudaError_t e = cudaMemsetAsync(ws, 0, L.count + 3 * kCMax * sizeof(int), s);
-  if (e != cudaSuccess) return e;
   using B16 = __nv_bfloat16;
   const bool bf = dtype == FA_DT_BF16;
   if (d == 128) return bf ? launch_c<B16, 128>(mk, mv, a, s) : launch_c<__half, 128>(mk, mv, a, s);

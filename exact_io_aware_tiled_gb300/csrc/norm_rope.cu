@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
   __shared__ float sM[128];
   __shared__ float rows[kPairs == kShared ? kNThreads * 8 : 8];
   extern __shared__ __align__(16) uint8_t ahead[];   // [kStages][kPieces][kNThreads] 16-byte pieces, of x, then of dy
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   load_turns(a, sF, sM);
   const int v = (int)blockIdx.x < a.ctas[0] ? 0 : 1;
   const int c = (int)blockIdx.x - (v ? a.ctas[0] : 0);
@@ -507,18 +508,21 @@ template <typename T, int kPairs, bool kBack> cudaError_t launch_n(const NormArg
   constexpr int bytes = NormCfg<T, kPairs, kBack>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.ctas[0] + a.ctas[1]), kNThreads, bytes, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !kBack || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)(a.d / 8), 2);
-  c.blockDim = dim3(1024);
+  c.gridDim = dim3((unsigned)(a.ctas[0] + a.ctas[1]));
+  c.blockDim = dim3(kNThreads);
+  c.dynamicSmemBytes = bytes;
   c.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
   c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, kern, a);
+  if (e != cudaSuccess || !kBack || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
+  c.gridDim = dim3((unsigned)(a.d / 8), 2);
+  c.blockDim = dim3(1024);
+  c.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&c, norm_dw_kernel, (const float*)a.part, a.d, a.ctas[0], a.ctas[1], a.dw[0], a.dw[1]);
 }
 
