@@ -57,10 +57,10 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
   // An item of a first key tile may take a CTA's whole share of all steps (query tiles at key tiles), as it starts
   // among the first: cutting it further costs more, in dK and dV that go through float32, than it balances.  us,
   // backward, items of 8 / 16 / 32 steps: 64 heads of 64 x 4,096, window 512 265 / 256 / 243 (one item each), 8 x 4 K/V
-  // heads x 2,047 with 3 query heads and 150 first keys 147 / 141 / 132; float32, whose blocks are one warpgroup each
-  // and four or more on an SM, 32 heads x 2,048 1,398 / 2,010 / 2,010.  At least 16 steps (float32: 2), and no more than
-  // about four items for each CTA: a part takes 64 KB (d = 128: 128 KB).  Up to kFewSinks first keys of 16 bits go the
-  // way of sink_few.cu instead, with both sides' times.
+  // heads x 2,047 with 3 query heads and 150 first keys 147 / 141 / 132.  At least 16 steps; float32, whose steps are
+  // longer and whose blocks are two on an SM, 2: with 1 / 2 32 heads x 2,048 take 760 / 715 us, 2 heads x 1,000 119 / 127.
+  // No more than about four items for each CTA: a part takes 64 KB (d = 128: 128 KB).  Up to kFewSinks first keys of 16
+  // bits go the way of sink_few.cu instead, with both sides' times.
   const bool f32 = p->dtype == FA_DT_F32;
   if (!f32 && sinks <= kFewSinks) {
     // the CTAs of launch_sink_few, 3 (d = 128: 2) on an SM, in one round where that fills 0.7 of it, else in four
@@ -72,7 +72,7 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
   }
   k.tiles = (sinks + kTile - 1) / kTile;
   const long long span = std::min<long long>(nq, (p->window + kTile - 1) / kTile + 1);
-  const long long share = heads * g * (nq * span + k.tiles * nq) / (f32 ? 4 * 152 : 152);
+  const long long share = heads * g * (nq * span + k.tiles * nq) / (f32 ? 2 * 152 : 152);
   const long long least = std::max<long long>(f32 ? 2 : 16, share);
   const long long most = std::max<long long>(1, 4 * 152 / (heads * k.tiles));
   const long long chunks = std::max<long long>(1, std::min((steps + least / 2) / least, most));
