@@ -286,9 +286,8 @@ dkdv_rows(const float* __restrict__ q, const float* __restrict__ k, const float*
 
 // dQ: one thread per query row.
 __device__ __forceinline__ void
-dq_rows(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-        const float* __restrict__ dout, float* __restrict__ dq, const Strides& st, const Strides& kst,
-        const BwdArgs& a, int qt, int bh) {
+dq_rows(const float* q, const float* __restrict__ k, const float* __restrict__ v, const float* dout, float* dq,
+        const Strides& st, const Strides& kst, const BwdArgs& a, int qt, int bh) {
   extern __shared__ float dyn_smem[];
   auto QDs = reinterpret_cast<float (*)[kRows][kD + 1]>(dyn_smem);   // [2][kRows][kD + 1]
   __shared__ float Ks[kSub][kD];
@@ -370,12 +369,13 @@ dq_rows(const float* __restrict__ q, const float* __restrict__ k, const float* _
   }
 }
 
-// The first `keys` blocks: dK and dV, then dQ.  In one launch, as neither fills the GPU when there are few heads.
+// Block u = blockIdx.x + u0: the first `keys` dK and dV, then dQ.  In one launch, as neither fills the GPU when there
+// are few heads.
 __global__ void __launch_bounds__(kRows, 2)
-bwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                const float* __restrict__ dout, float* __restrict__ dq, float* __restrict__ dk, float* __restrict__ dv,
-                Strides st, Strides kst, const BwdArgs a, int keys) {
-  const int u = (int)blockIdx.x, per = keys / (a.B * a.H_kv);
+bwd_simt_kernel(const float* q, const float* __restrict__ k, const float* __restrict__ v, const float* dout, float* dq,
+                float* __restrict__ dk, float* __restrict__ dv, Strides st, Strides kst, const BwdArgs a, int keys,
+                int u0) {
+  const int u = (int)blockIdx.x + u0, per = keys / (a.B * a.H_kv);
   if (u < keys) dkdv_rows(q, k, v, dout, dk, dv, st, kst, a, u % per, u / per);
   else dq_rows(q, k, v, dout, dq, st, kst, a, (u - keys) % a.nq, (u - keys) / a.nq);
 }
@@ -397,7 +397,11 @@ cudaError_t launch_bwd_simt(const float* q, const float* k, const float* v, cons
   constexpr int dyn = 2 * kRows * (kD + 1) * (int)sizeof(float);
   const cudaError_t e = cudaFuncSetAttribute(bwd_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
-  bwd_simt_kernel<<<(unsigned)all, kRows, dyn, s>>>(q, k, v, dout, dq, dk, dv, st, kst, a, (int)keys);
+  // dQ in the place of Q or dO: dK and dV have to have read them
+  const unsigned first = dq == q || dq == dout ? (unsigned)keys : (unsigned)all;
+  bwd_simt_kernel<<<first, kRows, dyn, s>>>(q, k, v, dout, dq, dk, dv, st, kst, a, (int)keys, 0);
+  if (first < all)
+    bwd_simt_kernel<<<(unsigned)all - first, kRows, dyn, s>>>(q, k, v, dout, dq, dk, dv, st, kst, a, (int)keys, (int)first);
   return cudaGetLastError();
 }
 

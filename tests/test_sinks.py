@@ -303,6 +303,21 @@ def test_the_same_call_in_other_words(dtype, d):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("place", [0, 3])
+def test_dq_in_the_place_of_q_or_do(dtype, place):
+    x = make(1, 3, 3, 1000, 64, dtype, 15)
+    for s in (0, 3, 20):
+        q, k, v, do = (t.clone() for t in x)
+        kw = dict(causal=True, window=150, sinks=s)
+        o, lse = fa.fwd(q, k, v, **kw)
+        want = fa.bwd(q, k, v, o, do, lse, **kw)
+        got = fa.bwd(q, k, v, o, do, lse, out=((q, do)[place == 3], torch.empty_like(k), torch.empty_like(v)), **kw)
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        assert rel(got[0], want[0].double()) <= (1e-6 if dtype == "f32" else torch.finfo(torch.bfloat16).eps / 2)
+
+
+@gpu
 def test_both_forward_kernels_agree():
     x = make(1, 3, 3, 1300, 64, "bf16", 13)
     for w, s in ((200, 4), (100, 300)):
