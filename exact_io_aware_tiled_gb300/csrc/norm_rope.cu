@@ -36,8 +36,10 @@ enum Pairs {
   kShared        // (i, i + rot/2), any rot: 8 columns, the partners through shared memory
 };
 
-// The kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.
-__host__ __device__ constexpr int ctas_of(int pairs, bool back) { return back ? (pairs == kShared ? 4 : 3) : 3; }
+// The kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.  kShared, whose threads have
+// half the columns, takes more: 46 of 64 columns turned, 268 MB forward 96 / 79 / 69 / 112 us with 3 / 4 / 5 / 6, 403 MB
+// backward 109 / 91 / 138 with 3 / 4 / 5.  The others are slower so: forward 100 us against 87 with 4 or 5.
+__host__ __device__ constexpr int ctas_of(int pairs, bool back) { return pairs != kShared ? 3 : back ? 4 : 5; }
 template <typename T, int kPairs, bool kBack> struct NormCfg {
   static constexpr int kPer = 16 / (int)sizeof(T);                       // elements of a 16-byte piece
   static constexpr int kRow = (kPairs == kShared ? 8 : 16) / kPer;       // pieces of a row in a thread
@@ -137,6 +139,7 @@ template <int kPairs> struct Turn {
       cs[e] = 1.f;
       sn[e] = 0.f;
       if (kPairs == kHalves || i < half) turn(p, sF[i], sM[i], sgn * sM[i], cs[e], sn[e]);
+      if (kPairs == kShared && c0 + e < half) sn[e] = -sn[e];
     }
   }
   __device__ __forceinline__ void weights(const float* g) {
@@ -146,21 +149,21 @@ template <int kPairs> struct Turn {
       w[e] = g != nullptr && live && (e < 8 || two) ? g[c] : 1.f;
     }
   }
-  // v turned (kShared: `row` is the shared memory of this row, which its lanes have to themselves)
-  __device__ __forceinline__ void apply(float (&v)[NC], float* row) const {
+  // v turned (kShared: through `rows`, where column 8 u + e of a row lies at [e][u] behind the row's first lane, so that
+  // neither the lanes' own columns nor their partners, half a rotation away, share a bank)
+  __device__ __forceinline__ void apply(float (&v)[NC], float* rows, int first) const {
     if constexpr (kPairs == kShared) {
       __syncwarp();
       if (live) {
-        reinterpret_cast<float4*>(row + c0)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(row + c0)[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rows[e * kNThreads + threadIdx.x] = v[e];
       }
       __syncwarp();
       if (rotates) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int c = c0 + e;
-          if (c < half) v[e] = v[e] * cs[e] - row[c + half] * sn[e];
-          else if (c < 2 * half) v[e] = v[e] * cs[e] + row[c - half] * sn[e];
+          const int c = c0 + e, pc = c < half ? c + half : c - half;
+          if (c < 2 * half) v[e] = v[e] * cs[e] + rows[(pc & 7) * kNThreads + first + (pc >> 3)] * sn[e];
         }
       }
     } else if (rotates) {
@@ -211,7 +214,7 @@ __device__ __forceinline__ long long position(const NormArgs& a, uint32_t b, uin
 // rows ahead into shared memory that it has to itself (no barriers), so that what is
 // in flight takes no registers.  GPT-2-medium q and k: backward 155 us with two rows in
 // registers, 137 so; forward 93 with four, 87 so (537 MB, 0.90 of the copy
-// rate).  More CTAs are slower: forward 100 us with four or five on an SM.
+// rate).
 template <typename T, int kPairs, bool kBack>
 __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_kernel(const NormArgs a) {
   using R = Turn<kPairs>;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
   r.place((int)threadIdx.x & ((1 << a.lg) - 1), a.rot, a.units, a.d);
   r.weights(a.w[v]);
   const R all = r;
-  float* row = rows + (kPairs == kShared ? (threadIdx.x >> a.lg << a.lg) * 8 : 0);
+  const int first = (int)threadIdx.x >> a.lg << a.lg;      // the row's first lane
   const Strides xs = a.xs[v], ds = a.ds[v], ys = a.ys[v];
   struct Token { uint32_t b, n; bool there; };
   auto token_of = [&](uint32_t tile) -> Token {
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
         }
       }
       if constexpr (kBack) {
-        r.apply(g, row);                             // dz
+        r.apply(g, rows, first);                             // dz
         float sx = 0.f, sg = 0.f, sx1 = 0.f, sg1 = 0.f;
 #pragma unroll
         for (int e = 0; e < R::NC; e += 2) {
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
           mul2(x[e], x[e + 1], x[e], x[e + 1], rs, rs);
           mul2(x[e], x[e + 1], x[e], x[e + 1], r.w[e], r.w[e + 1]);
         }
-        r.apply(x, row);
+        r.apply(x, rows, first);
       }
       if (r.live) V8<T>::store(dst + r.c0, x);
       if (R::NC > 8 && r.two) V8<T>::store(dst + r.c1, x + (R::NC - 8));

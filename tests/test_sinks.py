@@ -212,7 +212,8 @@ KINDS = [("bf16", 64), ("f16", 64), ("f32", 64), ("bf16", 128), ("f16", 128)]
 @pytest.mark.parametrize("dtype,d", KINDS)
 @pytest.mark.parametrize("N,w,s", [(2, 1, 1), (100, 10, 3), (128, 64, 4), (129, 128, 1), (300, 1, 1), (300, 64, 4),
                                    (300, 200, 130), (513, 129, 128), (700, 100, 129), (700, 2, 300), (640, 128, 256),
-                                   (1000, 999, 1), (1000, 300, 999), (1500, 17, 1), (1500, 40, 8), (1500, 40, 9), (2050, 129, 2), (135, 130, 4)])
+                                   (1000, 999, 1), (1000, 300, 999), (1500, 17, 1),
+                                   (1500, 40, 8), (1500, 40, 9), (2050, 129, 2), (135, 130, 4)])
 def test_lengths_windows_and_first_keys(dtype, d, N, w, s):
     x = make(2, 3, 3, N, d, dtype, N + w + s)
     check(run(x, w, s), plain(*x, w, s), dtype)
