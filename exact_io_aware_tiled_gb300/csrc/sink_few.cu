@@ -104,7 +104,7 @@ sink_few_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
           const uint32_t to = mine + ls * C::kStage + (y * NP + p) * kFThreads * 16;
           copy16(to, o + at + 32 * p);
           copy16(to + 2 * NP * kFThreads * 16, dout + at + 32 * p);
-          if (i >= a.mask.window) copy16(to + 4 * NP * kFThreads * 16, q + at + 32 * p);
+          if (few > 0 && i >= a.mask.window) copy16(to + 4 * NP * kFThreads * 16, q + at + 32 * p);
         }
         copy4(minel + ls * C::kStage + y * kFThreads * 4, lse + (size_t)bh * a.N + i);
       }
@@ -171,7 +171,7 @@ sink_few_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
         const float l = *reinterpret_cast<const float*>(atl + y * kFThreads * 4);
         if (l != -INFINITY) l2[y] = l * kLog2e;
       }
-      pairs[y] = there && i >= a.mask.window;
+      pairs[y] = there && few > 0 && i >= a.mask.window;
       if (pairs[y] && a.mask.row_list != nullptr) {
         const int qt = i / kTile;
         pairs[y] = a.mask.row_cnt[qt] > 0 && a.mask.row_list[(size_t)qt * a.mask.nb] == 0;
@@ -190,7 +190,8 @@ sink_few_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
     const bool work = __any_sync(0xffffffffu, pairs[0] || pairs[1]);
     uint32_t da[2] = {0u, 0u};
     if (work) {
-      // rows without pairs are zeros: 0 times a row that is not finite would not be 0
+      // rows without pairs (of a sequence without keys, all of them) are zeros: 0 times a row that is not finite would
+      // not be 0
 #pragma unroll
       for (int y = 0; y < 2; ++y)
 #pragma unroll

@@ -381,3 +381,23 @@ def test_refusals_of_the_binding():
     o, lse = fa.fwd(q, k, v, causal=True, window=10, sinks=1)
     with pytest.raises(fa.FAError):
         fa.bwd(q, k, v, o, do, lse, causal=True, window=10, sinks=-1)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_rows_of_a_sequence_without_keys_may_hold_anything(dtype, d, bad):
+    # padding: nobody sees these rows, whatever they hold, with no, few and many first keys
+    x = make(2, 4, 2, 400, d, dtype, 17)
+    ln = torch.tensor([0, 400], dtype=torch.int32, device="cuda")
+    want = {s: run(x, 64, s, ln) for s in (0, 4, 8, 9)}
+    for t in x:
+        t[0] = bad
+    for s in want:
+        got = run(x, 64, s, ln)
+        o, lse, *grads = got
+        assert bool((o[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+        for g, n in zip(grads, ("dq", "dk", "dv")):
+            assert bool((g[0] == 0).all()), (s, n)
+        for i, (a, b) in enumerate(zip(got, want[s])):
+            assert i == 2 or torch.equal(a[1], b[1])
