@@ -63,8 +63,9 @@ def _fn(name, restype, *argtypes):
     up takes the ctypes structure)."""
     f = _raw.get(name)
     if f is None:
-        f = _raw[name] = load()[name]
+        f = load()[name]
         f.argtypes, f.restype = list(argtypes), restype
+        _raw[name] = f       # last: a function whose types are not set yet would cut pointers to 32 bits
     return f
 
 
