@@ -34,13 +34,15 @@ struct DropoutArgs {
 struct MaskArgs {
   int causal;
   int window;                 // sliding window w (causal only), 0 = none
-  int sinks;                  // first keys that stay visible under a window, < N
   const int32_t* seqlens_k;   // device [B] or nullptr
   const int16_t* row_list;    // [nb][nb]: kept kv tiles of each q tile, ascending
   const int32_t* row_cnt;     // [nb]
   const int16_t* col_list;    // [nb][nb]: q tiles that keep each kv tile, ascending
   const int32_t* col_cnt;     // [nb]
   int nb;                     // tiles per side (0 when dense)
+  // First keys that stay visible under a window, < N.  Last: between window and the pointers it moved the other fields,
+  // and the forward kernel with dropout took 680 us instead of 664 (GPT-2-medium, causal).
+  int sinks;
 };
 
 // FP8 forward: per-tile scales of the quantised operands and the rotation.
