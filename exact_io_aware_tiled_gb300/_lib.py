@@ -84,7 +84,7 @@ def _packed(q, k, causal, seqlens_k, dropout_p, seed, offset, block_mask, scale,
     return _pack(*q.shape, DTYPE_CODE[q.dtype], *q.stride()[:3], 0.0 if scale is None else float(scale),
                  1 if causal else 0, _address(seqlens_k), float(dropout_p), int(seed) & (2 ** 64 - 1),
                  int(offset) & (2 ** 64 - 1), _address(block_mask), 128, _address(o_f32), start or 0, stop or 0, k.shape[1],
-                 *k.stride()[:3], _int32(window), int(fwd_kernel))
+                 *k.stride()[:3], _int32(window), _int32(fwd_kernel))
 
 
 class fa_fp8_params(ctypes.Structure):

@@ -1,7 +1,9 @@
 """What the binding does before a call reaches the library: function objects and packed parameters.  CPU only."""
 import ctypes
+import math
 
 import pytest
+import torch
 
 from exact_io_aware_tiled_gb300 import _lib, _ops
 
@@ -32,3 +34,30 @@ def test_a_function_is_shared_only_when_its_types_are_set(module, known, monkeyp
     else:
         f = module._fn("fa_fwd_workspace_size", ctypes.c_void_p, restype=ctypes.c_size_t)
     assert list(shared.values()) == [f] and f.argtypes == [ctypes.c_void_p] and f.restype is ctypes.c_size_t
+
+
+def _params(**kw):
+    q, k = torch.zeros(1, 2, 3, 64), torch.zeros(1, 1, 3, 64)
+    d = dict(causal=False, seqlens_k=None, dropout_p=0.0, seed=0, offset=0, block_mask=None, scale=None, o_f32=None,
+             prof=None, window=0, fwd_kernel=0)
+    d.update(kw)
+    return _lib.fa_params.from_buffer_copy(_lib._packed(q, k, **d)), _lib.make_params(q, k=k, **d)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(scale=0.3), dict(scale=1e39), dict(scale=-1e39), dict(scale=math.nan),
+                                dict(scale=1e-50), dict(dropout_p=1e39), dict(dropout_p=0.25, seed=-1, offset=2 ** 70),
+                                dict(fwd_kernel=2), dict(window=17, causal=True)])
+def test_packed_parameters_are_the_structure_s(kw):
+    # numbers past float32 are infinite in both: the library then takes its default scale or refuses the call
+    a, b = _params(**kw)
+    for name, _ in _lib.fa_params._fields_:
+        x, y = getattr(a, name), getattr(b, name)
+        assert x == y or (x != x and y != y), name
+
+
+def test_whole_numbers_past_int32_are_its_ends():
+    a, _ = _params(fwd_kernel=7)
+    assert a.fwd_kernel == 7
+    p = _lib.fa_params.from_buffer_copy(_lib._packed(
+        torch.zeros(1, 2, 3, 64), torch.zeros(1, 1, 3, 64), False, None, 0.0, 0, 0, None, None, None, None, 2 ** 40, 2 ** 40))
+    assert (p.window, p.fwd_kernel) == (2 ** 31 - 1, 2 ** 31 - 1)
