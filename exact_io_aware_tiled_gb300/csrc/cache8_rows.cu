@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache8_append_kernel(const 
   const int y = u & 1;                               // K, V
   u >>= 1;
   const int hk = u % a.Hkv, b = u / a.Hkv;
-  const int L = max(0, min(a.width * a.page, a.lens[b]));
-  const int first = L - a.T, from = max(first, 0);   // position of token 0; the first that is written
+  const int tokens = max(0, a.lens[b]), L = min(a.width * a.page, tokens);      // L: those that the table has room for
+  const int first = tokens - a.T, from = max(first, 0);   // position of token 0; the first that is written
+  if (from >= L) return;
   const int w = (from >> a.lg) + pi, base = w << a.lg;
   if (base >= L) return;
   const int id = a.table[(int64_t)b * a.table_stride + w];

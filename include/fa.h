@@ -576,9 +576,10 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params *p, const void *q, const vo
  *     not seen, not written and read as zeros.  Entries behind the last row are not read.
  *     Sequences may share pages that are only read; a page that is written must belong
  *     to one sequence.
- *   - seqlens_k: device int32 [B], rows filled, L_b, taken into [0, width*page]; the T new
- *     tokens are the last T of them (L_b counts them).  Where L_b < T the first T - L_b
- *     tokens do not exist: they are not written and see nothing.
+ *   - seqlens_k: device int32 [B], tokens of a sequence, L_b (a negative one counts as 0); the
+ *     T new tokens are the last T of them (L_b counts them).  Where L_b < T the first T - L_b
+ *     tokens do not exist: they are not written and see nothing.  Tokens from width*page on
+ *     have no place in the table and count as those of an absent page.
  *   - page 16, 32, 64 or 128; d = 64 or 128; dtype float16 or bfloat16 (of q, o, k, v).
  *   - Rows of a page at or past L_b may hold anything; rows below L_b of present pages
  *     should be finite.

@@ -755,3 +755,33 @@ def test_refusals_of_the_binding():
             fa.cache8_fwd(q, *good, **kw)
     with pytest.raises(fa.FAError):
         fa.cache8_fwd(q.float(), *good)
+
+
+@gpu
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("T", [1, 5, 100])
+def test_new_tokens_past_the_table_are_dropped(d, page, T):
+    # as if the table went on with absent pages; the rows that are there keep their places and their codes
+    width, cap = 4, 4 * page
+    lens = [cap + 1, cap + T, cap + 3 * T, cap, 2 ** 31 - 1, cap - 1 + T // 2]
+    B = len(lens)
+    kc, vc, ks, vs, table = make_cache(B, 2, d, page, [cap] * B, width, seed=T)
+    more = torch.cat([table, torch.full((B, -(-3 * T // page) + 1), -1, dtype=torch.int32, device="cuda")], 1)
+    x = torch.randn(B, 2, T, d, device="cuda").bfloat16() * 50
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    keep = [t.clone() for t in (kc, vc, ks, vs)]
+    cv, sv = values(kc).cpu(), ks.double().cpu()
+    for b, n in enumerate(lens):             # what fits, at its own place
+        if cap > n - T:
+            fits = x[b:b + 1, :, :cap - (n - T)] if n > cap else x[b:b + 1]
+            plain_append(fits.cpu(), cv, sv, table[b:b + 1].cpu(), [min(n, cap)], page)
+    for tab in (more, table):
+        a = [t.clone() for t in keep]
+        fa.cache8_append(x, x, *a, tab, ln)
+        assert torch.equal(values(a[0]).cpu().nan_to_num(nan=9999.0), cv.nan_to_num(nan=9999.0))
+        assert torch.equal(a[2].double().cpu().nan_to_num(nan=9999.0), sv.nan_to_num(nan=9999.0))
+    for b in (2, 4):                         # nothing of theirs fits, and nothing is written
+        ids = table[b].long()
+        assert all(torch.equal(m[ids], n[ids]) for m, n in zip(a, keep))
+    k, _ = fa.cache8_read(*a, table, ln, rows=cap + 7)
+    assert bool((k[:, :, cap:] == 0).all()) and bool((k[0, :, :cap] != 0).any())
