@@ -5,7 +5,8 @@ A cache is five tensors that the program owns: ``k_cache`` and ``v_cache``
 ``v_scale`` float32 [pages,H_kv], and ``table`` int32 [B,width], whose row b
 names the pages of sequence b in the order of its tokens (-1, or anything
 outside [0, pages), for a page that is absent).  ``seqlens`` int32 [B] counts the
-filled rows, the new tokens' included.  As in ``_ops``: checks, allocation,
+tokens, the new ones included; tokens from width * page on count as those of an
+absent page.  As in ``_ops``: checks, allocation,
 pointers and the stream; the computation runs in ``libfa_gb300.so``.
 """
 from __future__ import annotations

@@ -995,7 +995,7 @@ fa_status fa_cache8_fwd(const fa_cache8_params* in, const void* q, const void* k
   Cache8Args a{};
   a.B = p.B; a.H = p.H; a.Hkv = p.H_kv; a.T = p.T; a.G = p.H / p.H_kv;
   a.page = p.page; a.lg = rows.lg; a.pages = p.pages; a.width = p.width; a.cap = p.width * p.page;
-  a.window = std::min(p.window, a.cap);          // a window as long as the longest sequence hides nothing
+  a.window = p.window;
   a.sinks = p.sinks;
   a.q = q; a.o = o; a.qs = sd.q; a.os = sd.o;
   a.lse = lse;

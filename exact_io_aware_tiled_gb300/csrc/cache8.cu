@@ -89,32 +89,34 @@ struct __align__(16) CInfo { float kf[4], ve[4], vi[4]; int key0, pad[3]; };
 static_assert(sizeof(CInfo) == 64, "a stage's record");
 
 struct CItem {
-  int b, hk, rt, L;        // rows of tile rt of K/V head hk of sequence b
+  int b, hk, rt, tokens;   // rows of tile rt of K/V head hk of sequence b
   int nt;                  // stages in this CTA; -1: no more
   int n;                   // units of these rows, the first at s0 of the line
   long long s0;
 };
 static_assert(sizeof(CItem) == 32, "a mailbox slot");
 
-// Units of one sequence: [0, ns) and, behind a gap of `skip`, the others.
+// Units of one sequence of n tokens, of which the table has room for L: [0, ns) and, behind a gap of `skip`, the others.
 struct Units {
   int n, ns, skip;
   // On the line each sequence's rows of a K/V head count kItemUnits more, in front: what a CTA spends on them besides
   // their keys (their q, joins and stores).  Without them the CTAs that drew short sequences ended last.
   __device__ __forceinline__ int line() const { return n > 0 ? n + kItemUnits : 0; }
 };
-template <int KS> __device__ __forceinline__ Units units_of(const Cache8Args& a, int L) {
+// The first key that the window leaves to a query at position p, 0 where it leaves all
+__device__ __forceinline__ int first_seen(const Cache8Args& a, int p) { return p + 1 > a.window ? p + 1 - a.window : 0; }
+template <int KS> __device__ __forceinline__ Units units_of(const Cache8Args& a, int n) {
   Units u{0, 0, 0};
-  if (L <= 0) return u;
-  const int hi = (L + KS - 1) / KS;
+  if (n <= 0) return u;
+  const int L = min(n, a.cap), hi = (L + KS - 1) / KS;
   int lo = 0;
-  if (a.window > 0) lo = max(0, L - a.T - a.window + 1) / KS;      // the first query's first key
+  if (a.window > 0) lo = min(hi, first_seen(a, n - a.T) / KS);     // the first query's first key
   u.ns = min((min(a.sinks, L) + KS - 1) / KS, lo);
   u.skip = lo - u.ns;
   u.n = u.ns + hi - lo;
   return u;
 }
-__device__ __forceinline__ int length_of(const Cache8Args& a, int b) { return max(0, min(a.cap, a.lens[b])); }
+__device__ __forceinline__ int tokens_of(const Cache8Args& a, int b) { return max(0, a.lens[b]); }
 
 // The CTAs' shares of the line of X units
 struct Share {
@@ -445,7 +447,7 @@ template <int KS> __global__ void __launch_bounds__(1024) cache8_plan_kernel(con
   if (a.B <= kPreMax) return;
   for (int b0 = 0; b0 < a.B; b0 += 1024) {
     const int b = b0 + threadIdx.x;
-    const int n = b < a.B ? units_of<KS>(a, length_of(a, b)).line() : 0;
+    const int n = b < a.B ? units_of<KS>(a, tokens_of(a, b)).line() : 0;
     int s = n;
 #pragma unroll
     for (int y = 1; y < 32; y <<= 1) {
@@ -504,8 +506,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
   if (warp == 4 && a.B <= kPreMax) {
     int2 carry = make_int2(0, 0);
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int L = b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
-      const int n = units_of<KS>(a, L).line();
+      const int n = b0 + lane < a.B ? units_of<KS>(a, tokens_of(a, b0 + lane)).line() : 0;
       int s = n;
 #pragma unroll
       for (int y = 1; y < 32; y <<= 1) {
@@ -585,15 +586,15 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const int mid = (lo + hi) >> 1;
         if (real(mid) <= x) lo = mid; else hi = mid;
       }
-      const int L = length_of(a, lo);
-      const Units un = units_of<KS>(a, L);
+      const int tokens = tokens_of(a, lo), L = min(tokens, a.cap);
+      const Units un = units_of<KS>(a, tokens);
       const unsigned y = (unsigned)(x - real(lo)), seg = y / (unsigned)un.n;
       const int i = (int)(y - seg * (unsigned)un.n);
       const long long s0 = (long long)pre[lo].x * HS + (long long)seg * un.line() + kItemUnits;
       k.it.b = lo;
       k.it.hk = (int)seg / a.tiles;
       k.it.rt = (int)seg - k.it.hk * a.tiles;
-      k.it.L = L;
+      k.it.tokens = tokens;
       k.it.nt = (int)min((long long)(un.n - i), re - x);
       k.it.n = un.n;
       k.it.s0 = s0;
@@ -654,7 +655,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
           }
           if (ok) {
             // boxes behind the last row are left out: what they would bring is hidden
-            const int nb = min(boxes, (cur.it.L - cur.key0 + rows - 1) / rows);
+            const int nb = min(boxes, (min(cur.it.tokens, a.cap) - cur.key0 + rows - 1) / rows);
             mbar_expect_tx(&bars->full[st], 2 * box * nb);
 #pragma unroll
             for (int y = 0; y < C::NG; ++y) {
@@ -736,6 +737,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     // Stage t of the item is key group t % kgs's: of an item with fewer stages than key groups some have none, of a
     // tile with fewer rows some warps.  They fetch no q and go on to the next item; the joins leave them out.
     const bool busy = lk < it.nt && r0 < a.r;
+    const int L = min(it.tokens, a.cap);                              // rows; the positions go by the tokens
     CRows<D, NX> w;
     w.init();
     int lim[NX][2], low[NX][2];
@@ -751,8 +753,9 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int rx = r0 + 8 * z + 2 * (lane & 3) + x;
-        lim[z][x] = rx < a.r ? it.L - a.T + rx % a.T + 1 : INT_MAX;   // rows that do not exist mask nothing
-        low[z][x] = rx < a.r && a.window > 0 ? lim[z][x] - a.window : 0;
+        const int p = it.tokens - a.T + rx % a.T;
+        lim[z][x] = rx < a.r ? min(L, p + 1) : INT_MAX;               // rows that do not exist mask nothing
+        low[z][x] = rx < a.r && a.window > 0 ? first_seen(a, p) : 0;
       }
     }
     for (int t = 0; t < it.nt; ++t, ++g) {
@@ -760,8 +763,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
       if ((st & (kgs - 1)) != kg) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[st], (uint32_t)(g / NS) & 1u, ctl))) return;
       if (busy)
-        w.step(smem + C::kK + st * C::kTile, smem + C::kV + st * C::kTile, smem + C::kInfo + st * 64, lim, low, a.sinks, it.L,
-               lane);
+        w.step(smem + C::kK + st * C::kTile, smem + C::kV + st * C::kTile, smem + C::kInfo + st * 64, lim, low, a.sinks, L, lane);
       __syncwarp();
       if (lane == 0)
         asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;"

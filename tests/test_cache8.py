@@ -785,3 +785,34 @@ def test_new_tokens_past_the_table_are_dropped(d, page, T):
         assert all(torch.equal(m[ids], n[ids]) for m, n in zip(a, keep))
     k, _ = fa.cache8_read(*a, table, ln, rows=cap + 7)
     assert bool((k[:, :, cap:] == 0).all()) and bool((k[0, :, :cap] != 0).any())
+
+
+@gpu
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("T", [1, 5, 70])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (40, 3), (300, 20), (1, 0), (2 ** 31 - 1, 5)])
+def test_queries_past_the_table_keep_their_positions(d, page, T, window, sinks):
+    # as if the table went on with absent pages
+    width, cap = 4, 4 * page
+    lens = [cap + 1, cap + 39, cap + 40, cap + 300, cap, 30]
+    B = len(lens)
+    *cache, table = make_cache(B, 2, d, page, [cap] * B, width, seed=T)
+    more = torch.cat([table, torch.full((B, -(-300 // page)), -1, dtype=torch.int32, device="cuda")], 1)
+    q = torch.randn(B, 4, T, d, device="cuda").half()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=sinks)
+    want = plain_fwd(q, (*cache, more), ln, page, window, sinks)
+    for tab in (more, table):
+        check(fa.cache8_fwd(q, *cache, tab, ln, **kw), want, "f16")
+        assert fa.check_status(fa.cache8_fwd.last_workspace) == 0
+    # the last length of int32: everything there is without a window, the first keys alone with one
+    ln = torch.full((B,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    here = torch.full((B,), cap, dtype=torch.int32, device="cuda")
+    got = fa.cache8_fwd(q, *cache, table, ln, **kw)
+    if window in (0, 2 ** 31 - 1):
+        check([t[:, :, T - 1:] for t in got], plain_fwd(q[:, :, T - 1:], (*cache, table), here, page), "f16")
+    elif sinks == 0:
+        assert bool((got[0] == 0).all()) and bool((got[1] == -math.inf).all())
+    else:
+        one = torch.full((B,), sinks, dtype=torch.int32, device="cuda")
+        check([t[:, :, :1] for t in got], plain_fwd(q[:, :, :1], (*cache, table), one, page), "f16")
