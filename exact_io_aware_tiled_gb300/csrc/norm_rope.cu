@@ -14,7 +14,7 @@
 // backward reads x and dy and writes dx.  As in rope.cu a thread owns 16 (8)
 // columns of one token and walks over the heads, so that a sine and cosine
 // serve them all; a row is the columns of a group of 2^n lanes, which shuffles
-// sum.  dw is summed by a thread over its rows in registers, by a CTA through
+// sum.  dw is summed by a thread over its rows in registers (kFold), by a CTA through
 // shared memory and over the CTAs by a second kernel, each in a fixed order.
 // Measured: GPT-2-medium q and k, 537 MB forward 87 us (6.1 TB/s, 0.90 of the copy
 // rate), 805 MB backward 137 us (5.9 TB/s); fp16, 32 + 4 heads of 128, interleaved, 581
@@ -28,6 +28,11 @@ namespace fa {
 namespace {
 
 constexpr int kNThreads = 128;
+// Rows whose dw a thread adds up plainly.  A warp's sums of so many go to sums in shared memory that carry what their
+// additions lose (Kahan's summation), so that no chain of additions grows with the number of rows: 3,000 equal terms a
+// thread, the worst case, were off by 2^-14.5 of their sum.  Backward, without and so: GPT-2-medium q and k 148 and 144
+// us, 46 of 64 columns 92 and 94; each thread's sums apart take 16 KB of what float32 rows need as L1, 141 -> 170 us.
+constexpr int kFold = 64;
 
 // Where the pairs of a thread's columns lie.
 enum Pairs {
@@ -40,13 +45,18 @@ enum Pairs {
 // half the columns, takes more: 46 of 64 columns turned, 268 MB forward 96 / 79 / 69 / 112 us with 3 / 4 / 5 / 6, 403 MB
 // backward 109 / 91 / 138 with 3 / 4 / 5.  The others are slower so: forward 100 us against 87 with 4 or 5.
 __host__ __device__ constexpr int ctas_of(int pairs, bool back) { return pairs != kShared ? 3 : back ? 4 : 5; }
+// [warps][sum, lost][d] float32, see kFold
+__host__ __device__ constexpr int sums_bytes(int d) { return kNThreads / 32 * 2 * d * (int)sizeof(float); }
 template <typename T, int kPairs, bool kBack> struct NormCfg {
   static constexpr int kPer = 16 / (int)sizeof(T);                       // elements of a 16-byte piece
   static constexpr int kRow = (kPairs == kShared ? 8 : 16) / kPer;       // pieces of a row in a thread
   static constexpr int kPieces = kBack ? 2 * kRow : kRow;
-  static constexpr int kStages = kPieces == 8 ? 3 : kPieces == 4 ? 6 : 8;
-  static constexpr int kBytes = kStages * kPieces * kNThreads * 16;
-  static_assert(!kBack || kBytes >= kNThreads * 16 * (int)sizeof(float), "room for the sums at the end");
+  // four CTAs of kShared in float32 have room for 5; 16 heads of 46 of 64 columns 87 -> 71 us with 5 instead of 6
+  static constexpr int kStages = kPieces == 8 ? 3 : kPieces == 4 ? (kBack && kPairs == kShared ? 5 : 6) : 8;
+  static constexpr int kAhead = kStages * kPieces * kNThreads * 16;
+  static constexpr int kStatic = 128 * 12 + (kPairs == kShared ? kNThreads * 32 : 32);
+  static constexpr int kMost = kAhead + (kBack ? sums_bytes(256) : 0);
+  static_assert(ctas_of(kPairs, kBack) * (kMost + kStatic + 1024) <= 233472, "the CTAs of one SM exceed its shared memory");
 };
 
 struct NormArgs {
@@ -291,6 +301,31 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
   for (int i = 0; i < C::kStages - 1; ++i) copy();
   int st = 0;
   float acc[kBack ? R::NC : 1] = {};
+  // dw of kFold rows: over the warp's groups, then into its sums
+  float* const sums = reinterpret_cast<float*>(ahead + C::kAhead) + (threadIdx.x >> 5) * 2 * a.d;
+  if constexpr (kBack) {
+    for (int i = threadIdx.x & 31; i < 2 * a.d; i += 32) sums[i] = 0.f;
+    __syncwarp();
+  }
+  auto fold = [&]() {
+    if constexpr (kBack) {
+      for (int o = 16; o >= 1 << a.lg; o >>= 1) {
+#pragma unroll
+        for (int e = 0; e < R::NC; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+      }
+#pragma unroll
+      for (int e = 0; e < R::NC; ++e) {
+        if ((int)(threadIdx.x & 31) < 1 << a.lg && (e < 8 ? all.live : all.two)) {
+          float* const at = sums + (e < 8 ? all.c0 + e : all.c1 + e - 8);
+          const float old = at[0], t = acc[e] - at[a.d], sum = old + t;
+          at[a.d] = (sum - old) - t;
+          at[0] = sum;
+        }
+        acc[e] = 0.f;
+      }
+    }
+  };
+  int since = 0;
   uint32_t tile = tile0;
   for (int done = 0, h0 = head0; done < count; ++tile, h0 = 0) {
     const Token it = token_of(tile);
@@ -345,6 +380,10 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
           mul2(y0, y1, y0, y1, r.w[e], r.w[e + 1]);
           fma2(x[e], x[e + 1], x[e], x[e + 1], k, k, y0, y1);
         }
+        if (++since == kFold) {
+          since = 0;
+          fold();
+        }
       } else {
         float sx = 0.f, sx1 = 0.f;
 #pragma unroll
@@ -362,20 +401,16 @@ __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_k
     }
   }
   if (!kBack || a.dw[v] == nullptr) return;
-  // the CTA's sums: the groups' partial sums of a column, in the order of the groups
+  // the CTA's sums: the warps', in their order
   cp_async_wait<0>();
+  fold();
   __syncthreads();
-  float* sums = reinterpret_cast<float*>(ahead);
-#pragma unroll
-  for (int e = 0; e < R::NC; ++e) sums[e * kNThreads + threadIdx.x] = acc[kBack ? e : 0];
-  __syncthreads();
-  if ((int)threadIdx.x >= 1 << a.lg || !all.live) return;
-#pragma unroll
-  for (int e = 0; e < R::NC; ++e) {
-    if (e >= 8 && !all.two) break;
+  const float* const from0 = reinterpret_cast<const float*>(ahead + C::kAhead);
+  for (int c = threadIdx.x; c < a.d; c += kNThreads) {
     float s = 0.f;
-    for (int g = 0; g < per; ++g) s += sums[e * kNThreads + (g << a.lg) + threadIdx.x];
-    a.part[(size_t)blockIdx.x * a.d + (e < 8 ? all.c0 + e : all.c1 + e - 8)] = s;
+#pragma unroll
+    for (int w = 0; w < kNThreads / 32; ++w) s += from0[w * 2 * a.d + c] - from0[(w * 2 + 1) * a.d + c];
+    a.part[(size_t)blockIdx.x * a.d + c] = s;
   }
 }
 
@@ -508,8 +543,9 @@ fa_status fill(const fa_norm_rope_params* p, const void* const (&x)[2], const vo
 
 template <typename T, int kPairs, bool kBack> cudaError_t launch_n(const NormArgs& a, cudaStream_t s) {
   auto kern = norm_rope_kernel<T, kPairs, kBack>;
-  constexpr int bytes = NormCfg<T, kPairs, kBack>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  using C = NormCfg<T, kPairs, kBack>;
+  const int bytes = C::kAhead + (kBack ? sums_bytes(a.d) : 0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMost);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)(a.ctas[0] + a.ctas[1]));

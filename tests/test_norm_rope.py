@@ -385,3 +385,27 @@ def test_rows_of_zeros_and_the_smallest_eps(dtype):
     for t in x[:2]:
         t[:, :, ::2] = 0
     check_both(x, dtype, freqs(64), eps=2.0 ** -140)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d,rot,inter,rows", [("bf16", 256, 0, False, 3000), ("f16", 128, 64, True, 3000),
+                                                    ("bf16", 64, 46, False, 3000), ("f32", 128, 128, False, 1500),
+                                                    ("bf16", 64, 64, False, 100), ("f16", 8, 8, False, 700)])
+def test_weight_gradients_of_many_rows(dtype, d, rot, inter, rows):
+    # `rows` equal rows a thread, so that all terms of a column have one sign and every addition errs the same way
+    lanes = (d + 8) // 16 if inter else (d - rot // 2) // 8 if rot % 16 == 0 else d // 8
+    per = 128 >> (lanes - 1).bit_length()
+    N = -(-rows * 456 * per // 16)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x, dy = (torch.randn(1, 1, 1, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    pos = torch.full((1,), 77, device="cuda", dtype=torch.int32).expand(N)
+    many = lambda t: t.expand(1, 16, N, d)  # noqa: E731
+    out = torch.empty(1, 16, N, d, device="cuda", dtype=DT[dtype])
+    got = fa.norm_rope_bwd(many(x), None, many(dy), q_weight=w, inv_freq=freqs(rot), positions=pos, interleaved=inter, out=out)
+    p = torch.full((1, 1, 1), 77, device="cuda")
+    dx, dxm, dw, dwm = plain(x, w, dy, 1e-6, p, freqs(rot), 1.0, inter)
+    near(got[0][:, :, ::N - 1], dx, dxm, dtype, -17)
+    M = 16 * N
+    assert bool(((got[2].double() - M * dw).abs() <= 2.0 ** -16 * M * dwm).all()), \
+        float(((got[2].double() - M * dw).abs() / (M * dwm)).max() * 2 ** 16)
