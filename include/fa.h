@@ -531,8 +531,10 @@ fa_status fa_prefix_fwd(const fa_prefix_params *p, const void *q, const void *k_
  *     place (same base, same strides); any other overlap is an error of the caller.
  *   - d, rot, positions, start, inv_freq and mscale as in fa_rope (rot = 0 too); eps > 0.
  *   - Sums and products are float32, rounded once to the dtype: rows whose squares
- *     sum to more than float32 holds become zeros.  A NaN or infinity makes its row
- *     NaN (and, backward, the weights' gradients).
+ *     sum to more than float32 holds become zeros.  A NaN makes its row NaN (and,
+ *     backward, the weights' gradients).  An infinity, whose row has r = 0, becomes NaN
+ *     with the element that it turns with, and the row's others 0; backward its row
+ *     and its column of the weights' gradient are NaN.
  *   - Results repeat bit for bit; the weights' gradients depend on no atomics.
  *   - The forward call is one launch without workspace.  Backward workspace:
  *     fa_norm_rope_bwd_workspace_size bytes, 16-byte aligned; nothing persists in it.

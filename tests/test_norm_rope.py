@@ -409,3 +409,30 @@ def test_weight_gradients_of_many_rows(dtype, d, rot, inter, rows):
     M = 16 * N
     assert bool(((got[2].double() - M * dw).abs() <= 2.0 ** -16 * M * dwm).all()), \
         float(((got[2].double() - M * dw).abs() / (M * dwm)).max() * 2 ** 16)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (46, False), (0, False)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+def test_an_infinity_in_a_row(dtype, rot, inter, bad):
+    # r = 0: the infinity and its partner in the rotation become NaN, the row's others 0; backward the whole row and the
+    # infinity's column of the weights' gradient are NaN; no other row changes
+    q, k, dq, dk, wq, wk = make(1, 3, 1, 9, 64, dtype, 41)
+    kw = dict(q_weight=wq, inv_freq=freqs(rot), interleaved=inter)
+    want, (gwant, _, dwant, _) = fa.norm_rope(q, **kw), fa.norm_rope_bwd(q, None, dq, **kw)
+    for c in (0, 5, 22, 23, 45, 46, 63):
+        x = q.clone()
+        x[0, 1, 4, c] = bad
+        pair = [c]
+        if c < rot:
+            pair.append(c ^ 1 if inter else (c + rot // 2) % rot)
+        y = fa.norm_rope(x, **kw)
+        assert sorted(y[0, 1, 4].isnan().nonzero().flatten().tolist()) == sorted(pair)
+        assert int((y[0, 1, 4] == 0).sum()) == 64 - len(pair)
+        dx, _, dw, _ = fa.norm_rope_bwd(x, None, dq, **kw)
+        assert bool(dx[0, 1, 4].isnan().all())
+        assert dw.isnan().nonzero().flatten().tolist() == [c]
+        for got, ref in ((y, want), (dx, gwant)):
+            got[0, 1, 4] = ref[0, 1, 4]
+            assert torch.equal(got, ref)
