@@ -467,7 +467,7 @@ fa_status check_cache8(const fa_cache8_params* in, fa_cache8_params& p, Cache8St
   const double most = 2147483648.0;
   if ((long long)p.width * p.page > (1 << 28) || (double)p.pages * p.H_kv >= most) return FA_ERR_UNSUPPORTED;
   if (rows) {
-    if ((double)p.B * p.H_kv * (p.T / 16 + 2.0) * 2 >= most) return FA_ERR_UNSUPPORTED;      // CTAs
+    if ((double)p.B * p.H_kv * (p.T / 16 + 2.0) * 2 >= most || p.T > (1 << 30)) return FA_ERR_UNSUPPORTED;   // CTAs, rows
   } else {
     if ((double)p.B * p.H * p.T >= (double)(1 << 26)) return FA_ERR_UNSUPPORTED;
     // 32-bit units (32 keys and up, 16 more for each sequence): of all sequences, and of one over heads and row tiles

@@ -609,8 +609,8 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params *p, const void *q, const vo
  *     lengths, so a sequence's last bit may change with the others' lengths.
  *   - Workspace: fa_cache8_workspace_size bytes, 16-byte aligned, independent of the lengths
  *     and the table's width; nothing persists in it; status word at its start.
- *   - width*page <= 2^28, pages*H_kv < 2^31; fa_cache8_append and _read: B*H_kv*T < 2^33;
- *     fa_cache8_fwd: B*H*T < 2^26, B*(width*page + 512) < 2^36, (width*page + 512)*(H*T/8 +
+ *   - width*page <= 2^28, pages*H_kv < 2^31; fa_cache8_append and _read: T <= 2^30,
+ *     B*H_kv*T < 2^33; fa_cache8_fwd: B*H*T < 2^26, B*(width*page + 512) < 2^36, (width*page + 512)*(H*T/8 +
  *     H_kv) < 2^36.  16-byte rule for bases and strides (a dimension of one element may
  *     have any stride); offsets are 64-bit.
  * ------------------------------------------------------------------------- */

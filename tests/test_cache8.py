@@ -816,3 +816,10 @@ def test_queries_past_the_table_keep_their_positions(d, page, T, window, sinks):
     else:
         one = torch.full((B,), sinks, dtype=torch.int32, device="cuda")
         check([t[:, :, :1] for t in got], plain_fwd(q[:, :, :1], (*cache, table), one, page), "f16")
+
+
+@pytest.mark.parametrize("T", [2 ** 30 + 1, 2 ** 31 - 127, 2 ** 31 - 1])
+def test_rows_near_the_end_of_int32_are_refused(T):
+    # the pages that T rows touch are counted in 32 bits
+    for name in ("fa_cache8_append", "fa_cache8_read"):
+        assert _rows(name, _params(B=1, H=1, H_kv=1, T=T)) == 2
