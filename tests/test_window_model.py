@@ -137,3 +137,44 @@ def test_values_through_the_cache_keep_e4m3s_precision():
         top = want.float().abs().amax()
         err = (got.double() - want.double()).abs()
         assert bool((err <= 2.0 ** -4 * want.double().abs() + 2.0 ** -10 * top.double() / 224).all())
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_a_prompt_in_chunks_reads_back_as_it_was_normed(d, page):
+    # every row of the cache against the normed key and the value that it was written from: a rounding to E4M3 (2^-4
+    # relative, 2^-10 of the page's scale below its normal range), and one more for each later chunk in the row's page
+    B, H, Hkv, width = 3, 4, 2, 512 // page
+    g = torch.Generator(device="cuda").manual_seed(26)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    inv, m = fa.rope_frequencies(d)
+    wk = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    P, table = pages_for(B, width, 27)
+    kc, vc = (torch.full((P, Hkv, page, d), float("nan"), device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.full((P, Hkv), float("nan"), device="cuda") for _ in range(2))
+    cache = (kc, vc, ks, vs, table)
+    chunks = (37, 120, 1, 64)
+    start = torch.tensor([0, 5, 200], dtype=torch.int32, device="cuda")      # the sequences begin apart
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    keys, values, times = [], [], []
+    for i, T in enumerate(chunks):
+        at = lens[:, None] + start[:, None] + torch.arange(T, device="cuda", dtype=torch.int32)
+        first = sum(chunks[:i])
+        lens.add_(T)
+        q, k, v = r(B, H, T, d), r(B, Hkv, T, d) * 2.0 ** i, r(B, Hkv, T, d) * 2.0 ** i      # scales grow
+        kn = fa.norm_rope(q, k, k_weight=wk, inv_freq=inv, positions=at, mscale=m)[1]
+        fa.cache8_append(kn, v, *cache, lens)
+        keys.append(kn)
+        values.append(v)
+        for j in range(first, first + T):
+            end = (j // page + 1) * page
+            times.append(1 + sum(sum(chunks[:c]) < end for c in range(i + 1, len(chunks))))
+    N = sum(chunks)
+    n = torch.tensor(times, device="cuda", dtype=torch.float64)[:, None]
+    got = fa.cache8_read(*cache, lens, rows=N)
+    for x, want, scale in zip(got, (keys, values), (ks, vs)):
+        want = torch.cat(want, 2).double()
+        s = scale[table.long()].transpose(1, 2).repeat_interleave(page, 2)[:, :, :N, None].double()
+        bound = ((1 + 2.0 ** -4) ** n - 1) * want.abs() + n * 2.0 ** -10 * s
+        assert bool(((x.double() - want).abs() <= bound).all())
+        for other in (want.roll(1, 2), want.roll(1, 1), want.roll(1, 0)):      # rows, heads, sequences of others do not pass
+            assert not bool(((x.double() - other).abs() <= bound).all(-1).any())
