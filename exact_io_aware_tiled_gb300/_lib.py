@@ -173,7 +173,7 @@ def make_params(q: torch.Tensor, *, k: Optional[torch.Tensor] = None, causal=Fal
     if k is not None:   # K/V (and dK/dV) layout; fewer heads = grouped-query attention
         p.H_kv = k.shape[1]
         p.kv_stride_b, p.kv_stride_h, p.kv_stride_n = k.stride(0), k.stride(1), k.stride(2)
-    p.window = int(window)
+    p.window = _int32(window)
     p.fwd_kernel = int(fwd_kernel)
     p.scale = 0.0 if scale is None else float(scale)
     p.causal = 1 if causal else 0

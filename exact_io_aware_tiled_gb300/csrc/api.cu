@@ -45,9 +45,9 @@ struct SinkPlan {
 
 SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
   SinkPlan k;
-  k.window = p->window;
-  if (sinks <= 0 || p->window <= 0) return k;
-  if (p->window >= p->N || sinks >= p->N) {
+  k.window = p->window < p->N ? p->window : 0;       // the kernels add a key's index to a window < N
+  if (sinks <= 0 || k.window <= 0) return k;
+  if (sinks >= p->N) {
     k.window = 0;
     return k;
   }

@@ -401,3 +401,23 @@ def test_rows_of_a_sequence_without_keys_may_hold_anything(dtype, d, bad):
             assert bool((g[0] == 0).all()), (s, n)
         for i, (a, b) in enumerate(zip(got, want[s])):
             assert i == 2 or torch.equal(a[1], b[1])
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_a_window_longer_than_the_sequence_hides_nothing(dtype, d):
+    N = 333
+    x = make(2, 4, 2, N, d, dtype, 18)
+    q, k, v, do = x
+    want = run(x, 0, 0)
+    for w in (N, N + 1, 2 ** 30, 2 ** 31 - 130, 2 ** 31 - 1, 2 ** 32 + 5, 2 ** 40):
+        got = run(x, w, 0)
+        for i, (a, b) in enumerate(zip(got, want)):
+            if i == 2:
+                assert rel(a, b.double()) <= (1e-6 if dtype == "f32" else torch.finfo(DT[dtype]).eps / 2), w
+            else:
+                assert torch.equal(a, b), (w, i)
+        kw = dict(causal=True, window=w)
+        assert torch.equal(fa.bwd_noalloc(q, k, v, *got[:1], do, got[1], **kw)[1], want[3]), w
+        if dtype != "f32":
+            assert torch.equal(fa.fwd_fp8(q, k, v, **kw)[0], fa.fwd_fp8(q, k, v, causal=True)[0]), w
