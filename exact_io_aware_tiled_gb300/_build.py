@@ -21,7 +21,7 @@ SOURCES = ["api.cu", "fwd_tc.cu", "fwd_tc1.cu", "bwd_tc.cu", "bwd_tc128.cu", "si
            "diff_fwd.cu", "diff_bwd.cu", "prefix.cu", "prefix_tc.cu", "norm_rope.cu",
            "cache8.cu", "cache8_rows.cu", "sink_few.cu"]
 HEADERS = ["common.cuh", "bwd_items.cuh", "fa_internal.h", "fwd_plan.cuh", "fp8.cuh", "row_softmax.cuh", "prefix.cuh",
-           "register_mma.cuh", "rope.cuh", "cache8.cuh"]
+           "register_mma.cuh", "rope.cuh", "cache8.cuh", "cache8_plan.cuh", "simt_lists.cuh", "sink_plan.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -20,11 +20,11 @@ struct Item {
   int steps;              // n * g; of a first key tile's item, its part of them
   int t0;                 // kWindowSinks: the first step's number among the tile's
   int part;               // where dK and dV go: -1 the tensors, else this place of BwdArgs::part
-  __device__ __forceinline__ int qt(int u) const { return list ? (int)list[u] : i0 + u; }
+  FA_PLAN int qt(int u) const { return list ? (int)list[u] : i0 + u; }
 };
 
 // Work items of the launch.
-template <int kWin> __device__ __forceinline__ int item_count(const BwdArgs& a) {
+template <int kWin> FA_PLAN int item_count(const BwdArgs& a) {
   const int heads = a.B * a.H_kv;
   if constexpr (kWin == kWindowSinks) return heads * (a.sink_tiles * a.sink_chunks + a.nq - a.sink_tiles);
   return a.nq * heads;
@@ -33,7 +33,7 @@ template <int kWin> __device__ __forceinline__ int item_count(const BwdArgs& a) 
 // Under kWindowSinks the items of the first key tiles come first, the longest ones: every query tile sees those, so
 // that one item of them would outlast all others, and each is cut into sink_chunks items of sink_steps steps.
 template <int kWin>
-__device__ __forceinline__ Item make_item(const BwdArgs& a, int u) {
+FA_PLAN Item make_item(const BwdArgs& a, int u) {
   Item it;
   int bk, chunk = 0;
   bool first_keys = false;
@@ -93,11 +93,6 @@ __device__ __forceinline__ Item make_item(const BwdArgs& a, int u) {
     }
   }
   return it;
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  const bool ok = mbar_wait(bar, parity, ctl);
-  return __all_sync(0xffffffffu, ok);
 }
 
 }  // namespace

@@ -33,19 +33,12 @@
 #include <climits>
 #include <cmath>
 
-#include "cache8.cuh"
+#include "cache8_plan.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kCThreads = 160;   // warps 0-3 compute, 4 looks up and loads
-// What a CTA spends on a sequence's rows of a K/V head besides their keys, in units.  us with 0 / 6 / 12 / 16: 64
-// sequences of up to 8,191 keys 123 / 97 / 97 / 98, 300 of up to 2,047 193 / 132 / 131 / 137, 8 of 16,384 with 4
-// heads 29 / 27 / 25 / 24, the window above 21 / 17 / 17 / 17.
-constexpr int kItemUnits = 12;
-// Pieces that are joined at once; 32 against 16: 102 against 98 us, 8 heads of 128 125 against 101, one head of
-// 131,072 keys 38 against 26.
-constexpr int kGroup = 16;
 constexpr float kLn2 = 0.6931471805599453f;
 // The weights' sums, weights over V scales, are held times 2^-28, so that scales down to 2^-126, the smallest that
 // rows are written with, leave them finite; scales up to 2^98 leave them normal.
@@ -96,50 +89,7 @@ struct CItem {
 };
 static_assert(sizeof(CItem) == 32, "a mailbox slot");
 
-// Units of one sequence of n tokens, of which the table has room for L: [0, ns) and, behind a gap of `skip`, the others.
-struct Units {
-  int n, ns, skip;
-  // On the line each sequence's rows of a K/V head count kItemUnits more, in front: what a CTA spends on them besides
-  // their keys (their q, joins and stores).  Without them the CTAs that drew short sequences ended last.
-  __device__ __forceinline__ int line() const { return n > 0 ? n + kItemUnits : 0; }
-};
-// The first key that the window leaves to a query at position p, 0 where it leaves all
-__device__ __forceinline__ int first_seen(const Cache8Args& a, int p) { return p + 1 > a.window ? p + 1 - a.window : 0; }
-template <int KS> __device__ __forceinline__ Units units_of(const Cache8Args& a, int n) {
-  Units u{0, 0, 0};
-  if (n <= 0) return u;
-  const int L = min(n, a.cap), hi = (L + KS - 1) / KS;
-  int lo = 0;
-  if (a.window > 0) lo = min(hi, first_seen(a, n - a.T) / KS);     // the first query's first key
-  u.ns = min((min(a.sinks, L) + KS - 1) / KS, lo);
-  u.skip = lo - u.ns;
-  u.n = u.ns + hi - lo;
-  return u;
-}
 __device__ __forceinline__ int tokens_of(const Cache8Args& a, int b) { return max(0, a.lens[b]); }
-
-// The CTAs' shares of the line of X units
-struct Share {
-  long long X, each;       // every CTA has `each` units, the first `more` CTAs one more
-  int C, more;
-  __device__ __forceinline__ void cut(long long units, int ctas) {
-    X = units;
-    C = ctas;
-    if (X < 1ll << 31) {   // a 64-bit division takes as long as a load from L2
-      each = (unsigned)X / (unsigned)C;
-      more = (int)((unsigned)X - (unsigned)each * (unsigned)C);
-    } else {
-      each = X / C;
-      more = (int)(X - each * C);
-    }
-  }
-  __device__ __forceinline__ long long begin(int c) const { return each * c + min(c, more); }
-  __device__ __forceinline__ int owner(long long x) const {
-    const long long wide = (each + 1) * more;
-    return (int)(x < wide ? x / (each + 1) : more + (x - wide) / each);
-  }
-};
-
 __device__ __forceinline__ void widen(uint32_t four, uint32_t& lo, uint32_t& hi) {   // E4M3 codes -> halves, exact
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
@@ -152,14 +102,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Which of the 8 keys of a product's column tile is column n = 2 m + e: any order
-// serves, as K's and V's agree.  These let the lanes that read K rows together
-// (both e of an m) and those that read V rows together (all m of an e) meet
-// different banks of the swizzled tiles.
-template <int D> __device__ __forceinline__ int key_of(int m, int e) {
-  return D == 64 ? ((m & 2) << 1 | e << 1 | ((m & 1) ^ e)) : (((m >> 1) ^ e) << 2 | (m & 1) << 1 | e);
 }
 
 // Transposes the 8 x 8 matrix of halves whose row l / 4 lane l holds two columns of.
@@ -815,7 +757,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     // ---- rows that were cut: of every kGroup pieces the last CTA to leave its own joins them, of all groups the last
     //      one those; in the CTAs' order, whoever is last
     const int c0 = sh.owner(it.s0), pieces = sh.owner(it.s0 + it.n - 1) - c0 + 1;
-    auto slot_of = [&](int piece) { return 2 * (c0 + piece) + (piece == 0 ? 1 : 0); };   // the first begins in its CTA
+    auto slot_of = [&](int piece) { return piece_slot(c0, piece); };
     auto arrive_last = [&](int* count, int of, bool& ok) -> bool {
       __threadfence();
       if (!(ok = meet())) return false;

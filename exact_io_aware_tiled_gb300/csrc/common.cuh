@@ -73,8 +73,11 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
+// Planning arithmetic is compiled for the host too, where tests run it.
+#define FA_PLAN __host__ __device__ __forceinline__
+
 // Key tiles that hold the first `sinks` keys.
-__device__ __forceinline__ int sink_tiles(int sinks) { return (sinks + kTile - 1) / kTile; }
+FA_PLAN int sink_tiles(int sinks) { return (sinks + kTile - 1) / kTile; }
 
 // ----------------------------------------------------------------------------
 // mbarrier
@@ -148,6 +151,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
       return false;
     }
   }
+}
+
+// mbar_wait by all lanes of a warp: all go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+  const bool ok = mbar_wait(bar, parity, ctl);
+  return __all_sync(0xffffffffu, ok);
 }
 
 // Barrier among a fixed group of threads built on an mbarrier (initialised

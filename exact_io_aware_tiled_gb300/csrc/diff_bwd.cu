@@ -87,11 +87,6 @@ static_assert(sizeof(DBars) <= 320, "barrier block overflows its shared-memory s
 
 constexpr uint32_t kColS1 = 0, kColS2 = 64, kColDP = 128, kColDQ = 192, kColDK = 256, kColDV = 384;
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  const bool ok = mbar_wait(bar, parity, ctl);
-  return __all_sync(0xffffffffu, ok);
-}
-
 // One work item: key tile jt of K/V pair hk of batch b, and its steps: the two
 // 64-row halves of every query tile that sees the key tile, for each of the
 // group's query head pairs.

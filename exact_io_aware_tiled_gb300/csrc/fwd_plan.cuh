@@ -22,7 +22,7 @@ struct Slot {
   const int16_t* list;    // sparse kv list or nullptr
   // kv tile of step s (lo is nonzero only under a sliding window)
   template <int kWin>
-  __device__ __forceinline__ int kv(int s) const {
+  FA_PLAN int kv(int s) const {
     if constexpr (kWin == kWindowSinks) {
       const int t = s < head ? s : s + gap;
       return list ? (int)list[t] : t;
@@ -32,7 +32,7 @@ struct Slot {
 };
 
 template <int kWin>
-__device__ __forceinline__ Slot make_slot(const FwdArgs& a, int qt, int Lk) {
+FA_PLAN Slot make_slot(const FwdArgs& a, int qt, int Lk) {
   Slot sl;
   sl.qt = qt;
   sl.list = nullptr;
@@ -86,13 +86,13 @@ struct StepPlan {
   // Accessors by select rather than by indexing with a run-time value, so
   // the plan stays in registers (an indexed array would live in local memory
   // and cost the single-thread issuers a memory round trip per access).
-  __device__ __forceinline__ int stage(int l) const { return l ? st[1] : st[0]; }
-  __device__ __forceinline__ uint32_t parity(int l) const { return l ? ph[1] : ph[0]; }
-  __device__ __forceinline__ int load_of(int x) const { return x ? use[1] : use[0]; }
+  FA_PLAN int stage(int l) const { return l ? st[1] : st[0]; }
+  FA_PLAN uint32_t parity(int l) const { return l ? ph[1] : ph[0]; }
+  FA_PLAN int load_of(int x) const { return x ? use[1] : use[0]; }
 };
 
 template <int NS, int kWin>
-__device__ __forceinline__ StepPlan plan_step(const Slot (&sl)[2], int s, int& ld) {
+FA_PLAN StepPlan plan_step(const Slot (&sl)[2], int s, int& ld) {
   StepPlan p;
   p.nl = 0;
   p.use[0] = p.use[1] = -1;
@@ -113,9 +113,62 @@ __device__ __forceinline__ StepPlan plan_step(const Slot (&sl)[2], int s, int& l
   return p;
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  const bool ok = mbar_wait(bar, parity, ctl);
-  return __all_sync(0xffffffffu, ok);
+// One query tile per CTA (fwd_tc1.cu): the kv tiles query tile qt visits, in ascending order (causal: j <= qt;
+// padding: j < ceil(Lk / 128); window: from the first tile the window
+// reaches; block-sparse: the tile's row list).
+struct Tile1 {
+  int qt, n, lo;
+  int head, gap;          // kWindowSinks: steps at the first keys' tiles, and what lies between those and the window's
+  const int16_t* list;
+  template <int kWin>
+  FA_PLAN int kv(int s) const {
+    if constexpr (kWin == kWindowSinks) {
+      const int t = s < head ? s : s + gap;
+      return list ? (int)list[t] : t;
+    }
+    return list ? (int)list[s] : (kWin ? lo + s : s);
+  }
+};
+
+template <int kWin>
+FA_PLAN Tile1 make_tile1(const FwdArgs& a, int qt, int Lk) {
+  Tile1 t;
+  t.qt = qt;
+  t.list = nullptr;
+  t.n = 0;
+  t.lo = t.head = t.gap = 0;
+  int lim = (Lk + kTile - 1) / kTile;
+  if (a.mask.causal) lim = min(lim, qt + 1);
+  if (a.mask.window > 0) t.lo = max(0, qt * kTile - a.mask.window + 1) / kTile;
+  if (a.mask.row_list != nullptr) {
+    const int16_t* list = a.mask.row_list + (size_t)qt * a.mask.nb;
+    const int cnt = a.mask.row_cnt[qt];
+    int s0 = 0;
+    if constexpr (kWin == kWindowSinks) {
+      const int tiles = min(sink_tiles(a.mask.sinks), min(t.lo, lim));
+      while (t.head < cnt && list[t.head] < tiles) ++t.head;
+      s0 = t.head;
+    }
+    while (s0 < cnt && list[s0] < t.lo) ++s0;
+    int n = s0;
+    while (n < cnt && list[n] < lim) ++n;
+    if constexpr (kWin == kWindowSinks) {
+      t.list = list;
+      t.gap = s0 - t.head;
+      t.n = t.head + n - s0;
+    } else {
+      t.list = list + s0;
+      t.n = n - s0;
+    }
+  } else {
+    t.n = max(0, lim - t.lo);
+    if constexpr (kWin == kWindowSinks) {
+      t.head = min(sink_tiles(a.mask.sinks), min(t.lo, lim));
+      t.gap = t.lo - t.head;
+      t.n += t.head;
+    }
+  }
+  return t;
 }
 
 }  // namespace

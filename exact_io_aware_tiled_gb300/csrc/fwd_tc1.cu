@@ -31,7 +31,7 @@
 //   * epilogue: O / l -> 16 bit -> shared memory (the dead Q tile, 128-B
 //     swizzle) -> TMA store, which clips rows >= N; logsumexp with plain stores.
 // Tensor memory: S 128 columns | P 64 | O 64 (256 of the SM's 512).
-#include "common.cuh"
+#include "fwd_plan.cuh"
 
 namespace fa {
 namespace {
@@ -61,69 +61,6 @@ struct Bars1 {
   int abort;
 };
 static_assert(sizeof(Bars1) <= 256, "barrier block overflows its shared-memory slot");
-
-// The kv tiles query tile qt visits, in ascending order (causal: j <= qt;
-// padding: j < ceil(Lk / 128); window: from the first tile the window
-// reaches; block-sparse: the tile's row list).
-struct Tile1 {
-  int qt, n, lo;
-  int head, gap;          // kWindowSinks: steps at the first keys' tiles, and what lies between those and the window's
-  const int16_t* list;
-  template <int kWin>
-  __device__ __forceinline__ int kv(int s) const {
-    if constexpr (kWin == kWindowSinks) {
-      const int t = s < head ? s : s + gap;
-      return list ? (int)list[t] : t;
-    }
-    return list ? (int)list[s] : (kWin ? lo + s : s);
-  }
-};
-
-template <int kWin>
-__device__ __forceinline__ Tile1 make_tile1(const FwdArgs& a, int qt, int Lk) {
-  Tile1 t;
-  t.qt = qt;
-  t.list = nullptr;
-  t.n = 0;
-  t.lo = t.head = t.gap = 0;
-  int lim = (Lk + kTile - 1) / kTile;
-  if (a.mask.causal) lim = min(lim, qt + 1);
-  if (a.mask.window > 0) t.lo = max(0, qt * kTile - a.mask.window + 1) / kTile;
-  if (a.mask.row_list != nullptr) {
-    const int16_t* list = a.mask.row_list + (size_t)qt * a.mask.nb;
-    const int cnt = a.mask.row_cnt[qt];
-    int s0 = 0;
-    if constexpr (kWin == kWindowSinks) {
-      const int tiles = min(sink_tiles(a.mask.sinks), min(t.lo, lim));
-      while (t.head < cnt && list[t.head] < tiles) ++t.head;
-      s0 = t.head;
-    }
-    while (s0 < cnt && list[s0] < t.lo) ++s0;
-    int n = s0;
-    while (n < cnt && list[n] < lim) ++n;
-    if constexpr (kWin == kWindowSinks) {
-      t.list = list;
-      t.gap = s0 - t.head;
-      t.n = t.head + n - s0;
-    } else {
-      t.list = list + s0;
-      t.n = n - s0;
-    }
-  } else {
-    t.n = max(0, lim - t.lo);
-    if constexpr (kWin == kWindowSinks) {
-      t.head = min(sink_tiles(a.mask.sinks), min(t.lo, lim));
-      t.gap = t.lo - t.head;
-      t.n += t.head;
-    }
-  }
-  return t;
-}
-
-__device__ __forceinline__ bool warp_wait1(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  const bool ok = mbar_wait(bar, parity, ctl);
-  return __all_sync(0xffffffffu, ok);
-}
 
 template <typename T, bool kDrop, int kWin>
 __global__ void __launch_bounds__(kThreads1, 2)
@@ -308,7 +245,7 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     bool ok = true;
     for (int s = 0; s < n; ++s) {
       const int kv = tile.kv<kWin>(s);
-      if (!(ok = warp_wait1(&bars->s_full, (uint32_t)s & 1u, ctl))) break;
+      if (!(ok = warp_wait(&bars->s_full, (uint32_t)s & 1u, ctl))) break;
       tc_fence_after();
       uint32_t sr[4][32];
 #pragma unroll
@@ -392,7 +329,7 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // Philox words leave no room for that: the wait comes first and P goes
       // out per half of 64 keys.
       if constexpr (kDrop) {
-        if (s > 0 && !(ok = warp_wait1(&bars->pv_done, (uint32_t)(s - 1) & 1u, ctl))) break;
+        if (s > 0 && !(ok = warp_wait(&bars->pv_done, (uint32_t)(s - 1) & 1u, ctl))) break;
         tc_fence_after();
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -405,7 +342,7 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint32_t pk[2][32];
 #pragma unroll
         for (int c2 = 0; c2 < 128; c2 += 2) pk[c2 >> 6][(c2 >> 1) & 31] = p_pair(c2);
-        if (s > 0 && !(ok = warp_wait1(&bars->pv_done, (uint32_t)(s - 1) & 1u, ctl))) break;
+        if (s > 0 && !(ok = warp_wait(&bars->pv_done, (uint32_t)(s - 1) & 1u, ctl))) break;
         tc_fence_after();
         tmem_st32(tP, pk[0]);
         tmem_st32(tP + 32, pk[1]);
@@ -434,7 +371,7 @@ fwd_tc1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     // ---- epilogue: O / l -> 16 bit -> shared (the Q tile, dead once O is
     //      final) -> TMA store; logsumexp
     if (!named_bar_or(1, 128, !ok || bars->abort)) {
-      const bool have = n > 0 && warp_wait1(&bars->pv_done, (uint32_t)(n - 1) & 1u, ctl);
+      const bool have = n > 0 && warp_wait(&bars->pv_done, (uint32_t)(n - 1) & 1u, ctl);
       if (have) tc_fence_after();
       const float inv = l_rnd > 0.f ? 1.f / l_rnd : 0.f;
       const bool row_ok = i < a.N;

@@ -17,11 +17,6 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr uint32_t kStream = 256;           // columns of a stream
 constexpr uint32_t kColP = 64, kColO = 128; // within a stream
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  const bool ok = mbar_wait(bar, parity, ctl);
-  return __all_sync(0xffffffffu, ok);
-}
-
 // Barrier of a fixed group of warps (an mbarrier whose count is the number of
 // warps): bounded like every wait, so that a warp that gave up leaves none behind.
 struct WarpMeet {
