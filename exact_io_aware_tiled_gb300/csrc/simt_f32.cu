@@ -24,6 +24,9 @@ constexpr int kD = 64;
 constexpr int kAtOnce = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// kWin: a WindowKind.  Tests for first keys or a window that are not there cost the unrolled products 5 to 20 %: 32 heads
+// x 2,048 causal 1,225 us with them and 1,065 so, all keys 1,510 and 1,357, window 128 213 and 192.
+template <int kWin>
 __global__ void __launch_bounds__(kRows)
 fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                 float* __restrict__ o, Strides st, Strides kst, const FwdArgs a) {
@@ -54,7 +57,7 @@ fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
     const int kvt = tl.at(s);
     for (int sub = 0; sub < kTile / kSub; ++sub) {
       const int j0 = kvt * kTile + sub * kSub;
-      if (hidden(a.mask, j0, qt * kRows, kRows)) continue;
+      if (kWin != kAllKeys && hidden(a.mask, j0, qt * kRows, kRows)) continue;
       __syncthreads();
       for (int e = r; e < kSub * kD; e += kRows) {
         const int jj = j0 + e / kD, c = e % kD;
@@ -62,7 +65,7 @@ fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
         Vs[e / kD][c] = jj < a.N ? v[kbase + (size_t)jj * kst.n + c] : 0.f;
       }
       __syncthreads();
-      if (hidden(a.mask, j0, i & ~31, 32)) continue;
+      if (kWin != kAllKeys && hidden(a.mask, j0, i & ~31, 32)) continue;
       float sc[kSub];
       float mx = -INFINITY;
 #pragma unroll
@@ -70,7 +73,7 @@ fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
         float d = 0.f;
 #pragma unroll
         for (int c = 0; c < kD; ++c) d = fmaf(qr[c], Ks[jj][c], d);
-        sc[jj] = (j0 + jj <= jmax && (j0 + jj >= jmin || j0 + jj < a.mask.sinks)) ? d * sl2 : -INFINITY;
+        sc[jj] = j0 + jj <= jmax && (kWin == kAllKeys || j0 + jj >= jmin || (kWin == kWindowSinks && j0 + jj < a.mask.sinks)) ? d * sl2 : -INFINITY;
         mx = fmaxf(mx, sc[jj]);
       }
       const float mn = fmaxf(m, mx);
@@ -316,7 +319,9 @@ bwd_simt_kernel(const float* q, const float* __restrict__ k, const float* __rest
 cudaError_t launch_fwd_simt(const float* q, const float* k, const float* v, float* o, Strides st,
                             Strides kst, const FwdArgs& a, cudaStream_t s) {
   dim3 grid(a.nq, a.B * a.H);
-  fwd_simt_kernel<<<grid, kRows, 0, s>>>(q, k, v, o, st, kst, a);
+  if (a.mask.sinks > 0) fwd_simt_kernel<kWindowSinks><<<grid, kRows, 0, s>>>(q, k, v, o, st, kst, a);
+  else if (a.mask.window > 0) fwd_simt_kernel<kWindow><<<grid, kRows, 0, s>>>(q, k, v, o, st, kst, a);
+  else fwd_simt_kernel<kAllKeys><<<grid, kRows, 0, s>>>(q, k, v, o, st, kst, a);
   return cudaGetLastError();
 }
 
