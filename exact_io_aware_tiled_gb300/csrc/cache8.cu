@@ -373,8 +373,15 @@ template <int D, int NX> struct CRows {
   }
 };
 
-// logsumexp, and the factor of kSum O: a row that saw no key has l = 0, one with a NaN in it l = NaN
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? ((m - kSumLog2) + lg2(l)) * kLn2 : l == 0.f ? -INFINITY : l; }
+// logsumexp, and the factor of kSum O: a row that saw no key has l = 0, one with a NaN in it l = NaN.  l = 2^e f with f
+// in [1, 2): lg2 is off by 2^-22 of its result, which would be 28 and more, and m, which the V scales move as they move
+// e, is rounded next to neither 28 nor e.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  if (!(l > 0.f && l < INFINITY)) return l == 0.f ? -INFINITY : l;
+  const uint32_t u = __float_as_uint(l);
+  const float e = (float)((int)(u >> 23) - 127) - kSumLog2, f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
+  return ((m + e) + lg2(f)) * kLn2;
+}
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
 // Clears the status word and the counters, and, for batches whose prefix sums do not fit the kernel's shared memory,

@@ -823,3 +823,19 @@ def test_rows_near_the_end_of_int32_are_refused(T):
     # the pages that T rows touch are counted in 32 bits
     for name in ("fa_cache8_append", "fa_cache8_read"):
         assert _rows(name, _params(B=1, H=1, H_kv=1, T=T)) == 2
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("vs", [1.0, 2.0 ** 30, 2.0 ** 70, 2.0 ** -40])
+def test_logsumexp_near_zero(d, vs):
+    # 100,000 rows of one to three keys with scores near zero: the logsumexp, a sum of numbers of the size of log2(V scale)
+    # that cancel, keeps its absolute precision
+    B, H, T = 200, 64, 8
+    lens = [1 + b % 3 for b in range(B)]
+    cache = make_cache(B, 1, d, 16, lens, 1, seed=51, spread=3.0)
+    cache[2].fill_(2.0 ** -13)
+    cache[3].mul_(vs)
+    q = torch.randn(B, H, T, d, generator=torch.Generator(device="cuda").manual_seed(52), device="cuda").bfloat16()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    check(fa.cache8_fwd(q, *cache, ln), plain_fwd(q, cache, ln, 16), "bf16")
