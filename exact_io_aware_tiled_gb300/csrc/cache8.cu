@@ -47,6 +47,18 @@ constexpr float kSum = 0x1p-28f, kSumLog2 = -28.f;
 // weights are rounded against, and its weights still reach the sums.
 constexpr float kZeroPage = 0x1p-64f, kZeroPageLog2 = -64.f;
 
+// x = 2^e f with f in [1, 2), x > 0 normal.  lg2 is off by up to 2^-22 of its result: for a sum, or a scale, far from 1
+// that is more than the logsumexp may be off by; e + lg2(f) is exact for powers of two.
+struct Power {
+  float e, f;
+  __device__ __forceinline__ explicit Power(float x) {
+    const uint32_t u = __float_as_uint(x);
+    e = (float)((int)(u >> 23) - 127);
+    f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
+  }
+  __device__ __forceinline__ float log2() const { return e + lg2(f); }
+};
+
 template <int D, int NX> struct CCfg {
   static constexpr int RW = 8 * NX;              // query rows of a warp
   static constexpr int KS = D == 64 ? 64 : 32;   // keys of a stage
@@ -373,14 +385,12 @@ template <int D, int NX> struct CRows {
   }
 };
 
-// logsumexp, and the factor of kSum O: a row that saw no key has l = 0, one with a NaN in it l = NaN.  l = 2^e f with f
-// in [1, 2): lg2 is off by 2^-22 of its result, which would be 28 and more, and m, which the V scales move as they move
-// e, is rounded next to neither 28 nor e.
+// logsumexp, and the factor of kSum O: a row that saw no key has l = 0, one with a NaN in it l = NaN
 __device__ __forceinline__ float lse_of(float m, float l) {
   if (!(l > 0.f && l < INFINITY)) return l == 0.f ? -INFINITY : l;
-  const uint32_t u = __float_as_uint(l);
-  const float e = (float)((int)(u >> 23) - 127) - kSumLog2, f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
-  return ((m + e) + lg2(f)) * kLn2;
+  const Power p(l);
+  // m, which the V scales move as they move the power, is rounded next to neither 28 nor the power
+  return ((m + (p.e - kSumLog2)) + lg2(p.f)) * kLn2;
 }
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
@@ -621,7 +631,7 @@ cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
               const float k = g < C::NG ? ks[g < C::NG ? g : 0] : -1.f, v = g < C::NG ? vs[g < C::NG ? g : 0] : -1.f;
               const bool there = g < C::NG && (unsigned)cur.id[g < C::NG ? g : 0] < (unsigned)a.pages;
               inf.kf[g] = there ? k : 0.f;
-              inf.ve[g] = there ? (v == 0.f ? kZeroPageLog2 : lg2(v)) : -INFINITY;
+              inf.ve[g] = there ? (v == 0.f ? kZeroPageLog2 : Power(v).log2()) : -INFINITY;
               inf.vi[g] = there ? kSum / (v == 0.f ? kZeroPage : v) : 0.f;
             }
             inf.key0 = cur.key0;

@@ -827,7 +827,7 @@ def test_rows_near_the_end_of_int32_are_refused(T):
 
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("vs", [1.0, 2.0 ** 30, 2.0 ** 70, 2.0 ** -40])
+@pytest.mark.parametrize("vs", [1.0, 2.0 ** 30, 2.0 ** 70, 2.0 ** -40, 2.0 ** -60])
 def test_logsumexp_near_zero(d, vs):
     # 100,000 rows of one to three keys with scores near zero: the logsumexp, a sum of numbers of the size of log2(V scale)
     # that cancel, keeps its absolute precision
