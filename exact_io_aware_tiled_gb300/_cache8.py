@@ -154,7 +154,8 @@ def cache8_read(k_cache, v_cache, k_scale, v_scale, table, seqlens, *, dtype=tor
 def cache8_fwd(q, k_cache, v_cache, k_scale, v_scale, table, seqlens, *, window=0, sinks=0, scale=None, out=None,
                workspace=None, stream=None):
     """Attention of T new tokens of each of B sequences over their 8-bit caches
-    (fa_cache8_fwd): (o, lse).
+    (fa_cache8_fwd): (o, lse).  T is meant to be a few tokens: a long chunk is
+    taken, but under a short window visits several times the keys it sees.
 
     q [B,H,T,d] (T = 1: one decoding step), H a multiple of the cache's heads;
     seqlens [B] counts the new tokens, whose keys :func:`cache8_append` has

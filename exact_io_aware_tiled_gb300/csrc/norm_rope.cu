@@ -17,8 +17,9 @@
 // sum.  dw is summed by a thread over its rows in registers (kFold), by a CTA through
 // shared memory and over the CTAs by a second kernel, each in a fixed order.
 // Measured: GPT-2-medium q and k, 537 MB forward 87 us (6.1 TB/s, 0.90 of the copy
-// rate), 805 MB backward 137 us (5.9 TB/s); fp16, 32 + 4 heads of 128, interleaved, 581
-// MB backward 119 us (4.9 TB/s: conversions and shuffles of half as many rows).
+// rate), 805 MB backward 131 us (6.2 TB/s); 32 + 4 heads of 128, 581 MB backward 117 us
+// (5.0 TB/s), whichever type, pairs or part of the columns turn: latency, with 12 warps
+// on an SM.
 #include <algorithm>
 #include <cmath>
 
@@ -43,7 +44,7 @@ enum Pairs {
 
 // The kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.  kShared, whose threads have
 // half the columns, takes more: 46 of 64 columns turned, 268 MB forward 96 / 79 / 69 / 112 us with 3 / 4 / 5 / 6, 403 MB
-// backward 109 / 91 / 138 with 3 / 4 / 5.  The others are slower so: forward 100 us against 87 with 4 or 5.
+// backward 109 / 91 / 138 with 3 / 4 / 5 (94 with 4 and dw's sums by warp).  The others are slower so: forward 100 us against 87 with 4 or 5.
 __host__ __device__ constexpr int ctas_of(int pairs, bool back) { return pairs != kShared ? 3 : back ? 4 : 5; }
 // [warps][sum, lost][d] float32, see kFold
 __host__ __device__ constexpr int sums_bytes(int d) { return kNThreads / 32 * 2 * d * (int)sizeof(float); }
@@ -223,8 +224,8 @@ __device__ __forceinline__ long long position(const NormArgs& a, uint32_t b, uin
 // in a tile head by head, are shared out evenly over its CTAs.  A thread copies its
 // rows ahead into shared memory that it has to itself (no barriers), so that what is
 // in flight takes no registers.  GPT-2-medium q and k: backward 155 us with two rows in
-// registers, 137 so; forward 93 with four, 87 so (537 MB, 0.90 of the copy
-// rate).
+// registers, 137 so (131 with dw's sums by warp, kFold); forward 93 with four, 87 so (537
+// MB, 0.90 of the copy rate).
 template <typename T, int kPairs, bool kBack>
 __global__ void __launch_bounds__(kNThreads, ctas_of(kPairs, kBack)) norm_rope_kernel(const NormArgs a) {
   using R = Turn<kPairs>;

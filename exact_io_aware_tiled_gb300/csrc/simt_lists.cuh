@@ -71,8 +71,8 @@ FA_PLAN TileList bwd_list(const MaskArgs& m, int jt, int nq, int Lk) {
 }
 
 // Keys j0 .. j0 + kSub - 1 that none of n queries from i0 on sees under the causal mask, the window and its first
-// keys: a sub-tile that a block leaves out, or (forward) a warp: 32 heads x 2,048, window 128 235 -> 211 us, with 4
-// first keys 330 -> 234.
+// keys: a sub-tile that a block leaves out, or (forward) a warp: 32 heads x 2,048, window 128 235 -> 211 us (192
+// since its kernel knows that there are no first keys), with 4 first keys 330 -> 235.
 FA_PLAN bool hidden(const MaskArgs& m, int j0, int i0, int n) {
   return (m.causal && j0 >= i0 + n) || (m.window > 0 && j0 >= m.sinks && j0 + kSub <= i0 - m.window + 1);
 }

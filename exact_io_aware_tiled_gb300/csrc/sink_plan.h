@@ -29,8 +29,9 @@ SinkPlan sink_plan(const fa_params* p, int32_t sinks) {
   const long long nq = (p->N + kTile - 1) / kTile, g = p->H / hkv, steps = nq * g, heads = (long long)p->B * hkv;
   // An item of a first key tile may take a CTA's whole share of all steps (query tiles at key tiles), as it starts
   // among the first: cutting it further costs more, in dK and dV that go through float32, than it balances.  us,
-  // backward, items of 8 / 16 / 32 steps: 64 heads of 64 x 4,096, window 512 265 / 256 / 243 (one item each), 8 x 4 K/V
-  // heads x 2,047 with 3 query heads and 150 first keys 147 / 141 / 132.  At least 16 steps; float32, whose steps are
+  // backward in one run, items of 8 / 16 / a share's steps: 64 heads of 64 x 4,096, window 512, 9 first keys 264 / 256 /
+  // 243 (32 steps, one item each), 8 padded sequences x 4 K/V heads x 2,047 with 3 query heads and 150 first keys 147 /
+  // 140 / 135.  At least 16 steps; float32, whose steps are
   // longer and whose blocks are two on an SM, 2: with 1 / 2 32 heads x 2,048 take 760 / 715 us, 2 heads x 1,000 119 / 127.
   // No more than about four items for each CTA: a part takes 64 KB (d = 128: 128 KB).  Up to kFewSinks first keys of 16
   // bits go the way of sink_few.cu instead, with both sides' times.

@@ -605,6 +605,9 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params *p, const void *q, const vo
  *     the codes, sums and joins are float32.  K scales: any positive one.  V scales: 2^-126
  *     .. 2^98, those of a sequence within 2^96 of one another.  0 serves for a page of
  *     zeros (as a V scale it counts as 2^-64).
+ *   - T is meant to be a few tokens: each tile of up to 64 query rows visits the keys that any of
+ *     the T tokens sees.  A long chunk under a short window visits several times what its rows
+ *     see (T = 2,047, window 512: 4.3 times).
  *   - Results repeat bit for bit for the same batch; how the keys are cut follows from all
  *     lengths, so a sequence's last bit may change with the others' lengths.
  *   - Workspace: fa_cache8_workspace_size bytes, 16-byte aligned, independent of the lengths
