@@ -256,11 +256,20 @@ def _aux(seqlens_k, block_mask, q):
     return seqlens_k, block_mask
 
 
+def _empty_as(t):
+    """An uninitialised tensor with t's shape and strides.  The library writes an output with the strides of its group;
+    torch.empty_like gives a slice of a larger tensor (a fused projection's q) a compact copy's strides instead, and
+    storage that those writes would leave."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
+
+
 def _outputs(out, likes):
     """Caller-provided output tensors (checked against the shapes, dtypes and
     devices the call would allocate), or fresh ones."""
     if out is None:
-        return [torch.empty_like(t) if isinstance(t, torch.Tensor) else torch.empty(t[0], dtype=t[1], device=t[2])
+        return [_empty_as(t) if isinstance(t, torch.Tensor) else torch.empty(t[0], dtype=t[1], device=t[2])
                 for t in likes]
     if len(out) != len(likes):
         raise ValueError("out must hold %d tensors" % len(likes))
@@ -403,7 +412,7 @@ def bwd_noalloc(q, k, v, o, do, lse, *, causal=False, seqlens_k=None, dropout_p=
     seqlens_k, block_mask = _aux(seqlens_k, block_mask, q)
     if not lse.is_contiguous():
         raise ValueError("lse must be the contiguous [B, H, N] float32 tensor fwd returns")
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dq, dk, dv = _empty_as(q), _empty_as(k), _empty_as(v)
     p = make_params(q, k=k, causal=causal, seqlens_k=seqlens_k, dropout_p=dropout_p, seed=seed, offset=offset,
                     block_mask=block_mask, scale=scale, window=window)
     st = fn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),

@@ -61,3 +61,21 @@ def test_whole_numbers_past_int32_are_its_ends():
     p = _lib.fa_params.from_buffer_copy(_lib._packed(
         torch.zeros(1, 2, 3, 64), torch.zeros(1, 1, 3, 64), False, None, 0.0, 0, 0, None, None, None, None, 2 ** 40, 2 ** 40))
     assert (p.window, p.fwd_kernel) == (2 ** 31 - 1, 2 ** 31 - 1)
+
+
+def _layouts():
+    base = torch.zeros(2, 9, 8, 64, dtype=torch.float16)
+    yield base.transpose(1, 2)                              # dense
+    yield base[:, :, 1:4].transpose(1, 2)                   # q of a fused projection
+    yield torch.zeros(2, 3, 12, 80)[:, :, :9, :64]          # rows and columns of a larger tensor
+    yield torch.zeros(2, 1, 9, 64)[:, :, :1]
+    yield torch.zeros(9, 2, 3, 64).permute(1, 2, 0, 3)
+
+
+@pytest.mark.parametrize("t", list(_layouts()), ids=range(5))
+def test_outputs_have_the_strides_that_the_library_writes_with(t):
+    # q's strides are what O and dQ are written with, k's what dK and dV are: their storage has to reach as far
+    for o in (_lib._outputs(None, [t])[0], _lib._empty_as(t)):
+        assert o.shape == t.shape and o.stride() == t.stride() and o.dtype == t.dtype
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        assert o.untyped_storage().nbytes() >= (o.storage_offset() + last + 1) * o.element_size()

@@ -421,3 +421,32 @@ def test_a_window_longer_than_the_sequence_hides_nothing(dtype, d):
         assert torch.equal(fa.bwd_noalloc(q, k, v, *got[:1], do, got[1], **kw)[1], want[3]), w
         if dtype != "f32":
             assert torch.equal(fa.fwd_fp8(q, k, v, **kw)[0], fa.fwd_fp8(q, k, v, causal=True)[0]), w
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_slices_of_a_fused_projection(dtype, d):
+    # q, k and v as they lie in one projection, and rows and columns of larger tensors: outputs share their strides
+    B, H, Hkv, N = 2, 4, 2, 300
+    x = make(B, H, Hkv, N, d, dtype, 19)
+    fused = torch.full((B, N, 2 * H + 2 * Hkv, d), math.nan, device="cuda", dtype=DT[dtype])
+    at = (0, H, H + Hkv, H + 2 * Hkv)
+    sliced = [fused[:, :, a:a + t.shape[1]].transpose(1, 2) for a, t in zip(at, x)]
+    wide = [torch.full((B, t.shape[1], N + 5, d + 16), math.nan, device="cuda", dtype=DT[dtype])[:, :, :N, :d] for t in x]
+    for w, s in ((0, 0), (70, 5), (70, 40)):
+        want = run(x, w, s)
+        for y in (sliced, wide):
+            for a, b in zip(y, x):
+                a.copy_(b)
+            got = run(y, w, s)
+            assert got[0].stride() == y[0].stride() and got[2].stride() == y[0].stride() and got[3].stride() == y[1].stride()
+            for i, (m, n) in enumerate(zip(got, want)):
+                assert i == 2 or torch.equal(m, n)
+            assert rel(got[2], want[2].double()) <= (1e-6 if dtype == "f32" else torch.finfo(DT[dtype]).eps / 2)
+            if s == 0:
+                q, k, v, do = y
+                assert torch.equal(fa.bwd_noalloc(q, k, v, got[0], do, got[1], causal=True, window=w)[1], want[3])
+                if dtype != "f32":
+                    assert torch.equal(fa.fwd_fp8(q, k, v, causal=True)[0], fa.fwd_fp8(*x[:3], causal=True)[0])
+    keep = fused[:, :, at[-1] + H:]
+    assert keep.numel() == 0 or bool(keep.isnan().all())
