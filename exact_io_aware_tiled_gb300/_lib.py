@@ -200,6 +200,8 @@ def _same_layout(ts):
         if t.shape != ref.shape or t.dtype != ref.dtype:
             raise ValueError("tensors of one group must share shape and dtype: %s %s vs %s %s"
                              % (tuple(t.shape), t.dtype, tuple(ref.shape), ref.dtype))
+        if t.device != ref.device:
+            raise ValueError("tensors must be on one device: %s and %s" % (t.device, ref.device))
         if t.stride() != ref.stride():
             raise ValueError("tensors of one group must share their strides (%s vs %s); make them "
                              "alike, e.g. with .contiguous() on each" % (t.stride(), ref.stride()))
@@ -219,6 +221,8 @@ def _layouts(q_like, kv):
         raise ValueError("the number of query heads must be a multiple of the number of K/V heads")
     if k.dtype != q.dtype:
         raise ValueError("q, k, v must share one dtype")
+    if k.device != q.device:
+        raise ValueError("q, k, v must be on one device: %s and %s" % (q.device, k.device))
     return q_like, kv
 
 
@@ -229,6 +233,13 @@ def _check(q, name="q"):
         raise ValueError("%s must be a CUDA tensor" % name)
     if q.dtype not in DTYPE_CODE:
         raise ValueError("unsupported dtype %s" % q.dtype)
+
+
+def _check_lse(lse, q):
+    if lse.shape != q.shape[:3] or lse.dtype is not torch.float32 or lse.device != q.device or \
+            not lse.is_contiguous():
+        raise ValueError("lse must be the contiguous [B, H, N] float32 tensor fwd returns, got %s %s on %s" %
+                         (tuple(lse.shape), lse.dtype, lse.device))
 
 
 def int32_lengths(t: torch.Tensor, device) -> torch.Tensor:
@@ -286,8 +297,9 @@ def _workspace(lib_size, workspace, device):
     """A caller-provided uint8 workspace of at least lib_size bytes, or a fresh one."""
     if workspace is None:
         return torch.empty(lib_size, device=device, dtype=torch.uint8)
-    if workspace.dtype != torch.uint8 or workspace.numel() < lib_size or workspace.device != device:
-        raise ValueError("workspace must be a uint8 tensor of >= %d bytes on %s" % (lib_size, device))
+    if workspace.dtype != torch.uint8 or workspace.numel() < lib_size or workspace.device != device or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor of >= %d bytes on %s" % (lib_size, device))
     return workspace
 
 
@@ -335,8 +347,7 @@ def bwd(q, k, v, o, do, lse, *, causal=False, seqlens_k=None, dropout_p=0.0, see
     (q, o, do), (k, v) = _layouts([q, o, do], [k, v])
     if out is not None and (not q.is_contiguous() or not k.is_contiguous()):
         raise ValueError("out= takes contiguous outputs, so q, o, dO, k and v must be contiguous too")
-    if not lse.is_contiguous():
-        raise ValueError("lse must be the contiguous [B, H, N] float32 tensor fwd returns")
+    _check_lse(lse, q)
     seqlens_k, block_mask = _aux(seqlens_k, block_mask, q)
     dq, dk, dv = _outputs(out, [q, k, v])
     p = _packed(q, k, causal, seqlens_k, dropout_p, seed, offset, block_mask, scale, None, prof, window, 0)
@@ -410,8 +421,7 @@ def bwd_noalloc(q, k, v, o, do, lse, *, causal=False, seqlens_k=None, dropout_p=
     fn.argtypes = [ctypes.POINTER(fa_params)] + [ctypes.c_void_p] * 10
     fn.restype = ctypes.c_int
     seqlens_k, block_mask = _aux(seqlens_k, block_mask, q)
-    if not lse.is_contiguous():
-        raise ValueError("lse must be the contiguous [B, H, N] float32 tensor fwd returns")
+    _check_lse(lse, q)
     dq, dk, dv = _empty_as(q), _empty_as(k), _empty_as(v)
     p = make_params(q, k=k, causal=causal, seqlens_k=seqlens_k, dropout_p=dropout_p, seed=seed, offset=offset,
                     block_mask=block_mask, scale=scale, window=window)
@@ -494,6 +504,8 @@ def fp8_quantize(q, k, v, *, signs=None, per_tensor=False, stream=None, buf=None
     lay = fp8_layout(p)
     if buf is None:
         buf = torch.empty(lay["total"], device=q.device, dtype=torch.uint8)
+    elif buf.dtype != torch.uint8 or buf.device != q.device or not buf.is_contiguous():
+        raise ValueError("buf must be a contiguous uint8 tensor on %s, got %s on %s" % (q.device, buf.dtype, buf.device))
     st = lib.fa_fp8_quantize(ctypes.byref(p), ctypes.byref(f), _ptr(q), _ptr(k), _ptr(v), _ptr(buf), buf.numel(),
                              _stream(stream))
     if st != FA_OK:

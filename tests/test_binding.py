@@ -79,3 +79,31 @@ def test_outputs_have_the_strides_that_the_library_writes_with(t):
         assert o.shape == t.shape and o.stride() == t.stride() and o.dtype == t.dtype
         last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
         assert o.untyped_storage().nbytes() >= (o.storage_offset() + last + 1) * o.element_size()
+
+
+def test_tensors_on_another_device_are_refused():
+    # their addresses would go to the kernels as they are
+    q, k = torch.zeros(1, 2, 3, 64), torch.zeros(1, 1, 3, 64)
+    with pytest.raises(ValueError, match="one device"):
+        _lib._layouts([q], [k, k.to("meta")])
+    with pytest.raises(ValueError, match="one device"):
+        _lib._layouts([q, q.to("meta"), q], [k, k])
+    with pytest.raises(ValueError, match="one device"):
+        _lib._layouts([q], [k.to("meta"), k.to("meta")])
+    _lib._layouts([q, q], [k, k])
+
+
+def test_lse_and_workspaces_of_another_kind_are_refused():
+    q = torch.zeros(2, 3, 5, 64, dtype=torch.float16)
+    good = torch.zeros(2, 3, 5)
+    _lib._check_lse(good, q)
+    for bad in (good[:, :2], good[..., None], good.double(), good.half(), good.to("meta"), good[:1].expand(2, 3, 5),
+                torch.zeros(2, 5, 3).transpose(1, 2)):
+        with pytest.raises(ValueError, match="lse"):
+            _lib._check_lse(bad, q)
+    cpu = torch.device("cpu")
+    assert _lib._workspace(100, torch.zeros(100, dtype=torch.uint8), cpu).numel() == 100
+    for bad in (torch.zeros(99, dtype=torch.uint8), torch.zeros(100), torch.zeros(1, dtype=torch.uint8).expand(100),
+                torch.zeros(200, dtype=torch.uint8)[::2], torch.zeros(100, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            _lib._workspace(100, bad, cpu)
