@@ -44,7 +44,8 @@ enum Pairs {
 
 // The kernel's CTAs on an SM, of which the whole grid is one round, and its rows in flight.  kShared, whose threads have
 // half the columns, takes more: 46 of 64 columns turned, 268 MB forward 96 / 79 / 69 / 112 us with 3 / 4 / 5 / 6, 403 MB
-// backward 109 / 91 / 138 with 3 / 4 / 5 (94 with 4 and dw's sums by warp).  The others are slower so: forward 100 us against 87 with 4 or 5.
+// backward 109 / 91 / 138 with 3 / 4 / 5 (94 with 4 and dw's sums by warp).  The others are slower so: forward 100 us
+// against 87 with 4 or 5.
 __host__ __device__ constexpr int ctas_of(int pairs, bool back) { return pairs != kShared ? 3 : back ? 4 : 5; }
 // [warps][sum, lost][d] float32, see kFold
 __host__ __device__ constexpr int sums_bytes(int d) { return kNThreads / 32 * 2 * d * (int)sizeof(float); }

@@ -73,7 +73,8 @@ fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const 
         float d = 0.f;
 #pragma unroll
         for (int c = 0; c < kD; ++c) d = fmaf(qr[c], Ks[jj][c], d);
-        sc[jj] = j0 + jj <= jmax && (kWin == kAllKeys || j0 + jj >= jmin || (kWin == kWindowSinks && j0 + jj < a.mask.sinks)) ? d * sl2 : -INFINITY;
+        sc[jj] = j0 + jj <= jmax && (kWin == kAllKeys || j0 + jj >= jmin || (kWin == kWindowSinks && j0 + jj < a.mask.sinks))
+                     ? d * sl2 : -INFINITY;
         mx = fmaxf(mx, sc[jj]);
       }
       const float mn = fmaxf(m, mx);
